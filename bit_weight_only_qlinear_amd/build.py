@@ -32,6 +32,8 @@ SOURCES = {
     "skinny.hip": [],
     "a8w4.hip": [],
     "noalloc.hip": [],
+    "norm.hip": [],
+    "gated.hip": [],
 }
 
 

@@ -10,6 +10,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -620,6 +621,285 @@ qp_status qlinear_forward_a8w4(const qp_desc* d, const void* xq, const float* xs
   return hip_status(qp::launch_a8w4(dd, xq, xs, M, bufs_of(w), bias, y, y_dtype,
                                     (hipStream_t)stream),
                     "qlinear_forward_a8w4 launch");
+}
+
+}  // extern "C"
+
+// ---- the MLP block: norm, checkpoints, gated pair, input gradients
+
+namespace {
+
+// One buffer argument: `need` says whether NULL is an error.
+qp_status check_ptr(const void* p, const char* name, bool need) {
+  if (!p) return need ? fail(QP_EINVAL, "%s is NULL", name) : QP_OK;
+  if (!aligned16(p)) return fail(QP_EALIGN, "%s is not 16-byte aligned", name);
+  return QP_OK;
+}
+
+struct PtrArg {
+  const void* p;
+  const char* name;
+  bool need;
+};
+qp_status check_ptrs(std::initializer_list<PtrArg> args) {
+  for (const PtrArg& a : args) {
+    const qp_status st = check_ptr(a.p, a.name, a.need);
+    if (st != QP_OK) return st;
+  }
+  return QP_OK;
+}
+
+qp_status check_act_dtype(int32_t dt, const char* name) {
+  if (dt != QP_F16 && dt != QP_BF16)
+    return fail(QP_EINVAL, "%s must be QP_F16 or QP_BF16 (got %d)", name, dt);
+  return QP_OK;
+}
+qp_status check_out_dtype(int32_t dt, const char* name) {
+  if (dt != QP_F16 && dt != QP_BF16 && dt != QP_F32)
+    return fail(QP_EINVAL, "%s must be QP_F16, QP_BF16 or QP_F32 (got %d)", name, dt);
+  return QP_OK;
+}
+
+// Row kernels: launches of at most 2^32 threads (one block per row of up to
+// 1024 threads; one thread per 8 columns, or per column where K % 8 != 0).
+qp_status check_rows(int64_t M, int64_t K) {
+  if (M <= 0 || K <= 0)
+    return fail(QP_ESHAPE, "M and K must be positive (M=%lld, K=%lld)", (long long)M, (long long)K);
+  if (M > (int64_t(1) << 21) || K > (int64_t(1) << 24) ||
+      M * K > (int64_t(1) << (K % 8 ? 31 : 34)))
+    return fail(QP_EUNSUPPORTED,
+                "M must be <= 2^21, K <= 2^24 and M * K <= 2^34 (2^31 where K %% 8 != 0; M=%lld, "
+                "K=%lld)",
+                (long long)M, (long long)K);
+  return QP_OK;
+}
+
+// Product kernels' sizes (block counts and 32-bit tile offsets).
+qp_status check_block(const qp::Desc& d, int64_t M) {
+  if (M <= 0) return fail(QP_ESHAPE, "M must be positive (got %lld)", (long long)M);
+  if (M > (int64_t(1) << 20) || d.N > (int64_t(1) << 26) || M * d.N > (int64_t(1) << 36) ||
+      M * d.K > (int64_t(1) << 36))
+    return fail(QP_EUNSUPPORTED,
+                "M must be <= 2^20, N <= 2^26, M * N and M * K <= 2^36 (M=%lld, N=%lld, K=%lld)",
+                (long long)M, (long long)d.N, (long long)d.K);
+  return QP_OK;
+}
+
+qp_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (!need) return QP_OK;
+  if (!ws) return fail(QP_EINVAL, "workspace is NULL, this call needs %zu bytes", need);
+  if (!aligned16(ws)) return fail(QP_EALIGN, "workspace is not 16-byte aligned");
+  if (have < need)
+    return fail(QP_EINVAL, "workspace too small: %zu bytes, this call needs %zu", have, need);
+  return QP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qp_status qnorm_forward(const void* x, const void* residual, int32_t x_dtype, int64_t M, int64_t K,
+                        const void* weight, float eps, void* s, void* y, void* yq, float* ys,
+                        float* rstd, void* stream) {
+  qp_status st = check_act_dtype(x_dtype, "x_dtype");
+  if (st != QP_OK || (st = check_rows(M, K)) != QP_OK) return st;
+  if (!(eps > 0.f && std::isfinite(eps)))
+    return fail(QP_EINVAL, "eps must be positive and finite (got %g)", (double)eps);
+  if (y ? (yq || ys) : (!yq || !ys))
+    return fail(QP_EINVAL, "pass y, or yq and ys, and NULL for the other");
+  if (s && !residual) return fail(QP_EINVAL, "s is written only with a residual (s = x without)");
+  st = check_ptrs({{x, "x", true}, {residual, "residual", false}, {weight, "weight", false},
+                   {s, "s", false}, {y, "y", false}, {yq, "yq", false}, {ys, "ys", false},
+                   {rstd, "rstd", false}});
+  if (st != QP_OK) return st;
+  const void* out = y ? y : yq;
+  if (out == x || out == residual || out == s || out == weight)
+    return fail(QP_EINVAL, "the output must be a buffer of its own");
+  (void)hipGetLastError();
+  return hip_status(qp::launch_norm(x, residual, x_dtype, M, K, weight, eps, s, y, yq, ys, rstd,
+                                    (hipStream_t)stream),
+                    "qnorm_forward launch");
+}
+
+qp_status qnorm_backward_workspace_bytes(int64_t M, int64_t K, size_t* bytes) {
+  if (!bytes) return fail(QP_EINVAL, "bytes is NULL");
+  *bytes = 0;
+  const qp_status st = check_rows(M, K);
+  if (st != QP_OK) return st;
+  *bytes = (size_t)qp::norm_bwd_parts(M) * (size_t)K * 4u;
+  return ok();
+}
+
+qp_status qnorm_backward(const void* dy, const void* s, const void* s_codes, const float* s_scales,
+                         int32_t x_dtype, int64_t M, int64_t K, const void* weight,
+                         const float* rstd, const void* ds_in, void* ds, float* dweight,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  qp_status st = check_act_dtype(x_dtype, "x_dtype");
+  if (st != QP_OK || (st = check_rows(M, K)) != QP_OK) return st;
+  if (s ? (s_codes || s_scales) : (!s_codes || !s_scales))
+    return fail(QP_EINVAL, "pass s, or s_codes and s_scales, and NULL for the other");
+  if (!ds && !dweight) return fail(QP_EINVAL, "ds and dweight are both NULL");
+  st = check_ptrs({{dy, "dy", true}, {s, "s", false}, {s_codes, "s_codes", false},
+                   {s_scales, "s_scales", false}, {weight, "weight", false}, {rstd, "rstd", true},
+                   {ds_in, "ds_in", false}, {ds, "ds", false}, {dweight, "dweight", false}});
+  if (st != QP_OK) return st;
+  if (ds && (ds == s || ds == s_codes || ds == weight))
+    return fail(QP_EINVAL, "ds must not be s, s_codes or weight");
+  if (dweight) {
+    st = check_workspace(workspace, workspace_bytes, (size_t)qp::norm_bwd_parts(M) * (size_t)K * 4u);
+    if (st != QP_OK) return st;
+  }
+  (void)hipGetLastError();
+  return hip_status(qp::launch_norm_bwd(dy, s, s_codes, s_scales, x_dtype, M, K, weight, rstd,
+                                        ds_in, ds, dweight, static_cast<float*>(workspace),
+                                        (hipStream_t)stream),
+                    "qnorm_backward launch");
+}
+
+qp_status qpack_checkpoint(const void* x, int32_t x_dtype, int64_t M, int64_t K, void* codes,
+                           float* scales, void* stream) {
+  qp_status st = check_act_dtype(x_dtype, "x_dtype");
+  if (st != QP_OK || (st = check_rows(M, K)) != QP_OK) return st;
+  st = check_ptrs({{x, "x", true}, {codes, "codes", true}, {scales, "scales", true}});
+  if (st != QP_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(qp::launch_checkpoint(x, x_dtype, M, K, codes, scales, (hipStream_t)stream),
+                    "qpack_checkpoint launch");
+}
+
+qp_status qpack_checkpoint_restore(const void* codes, const float* scales, int64_t M, int64_t K,
+                                   void* x, int32_t x_dtype, void* stream) {
+  qp_status st = check_out_dtype(x_dtype, "x_dtype");
+  if (st != QP_OK || (st = check_rows(M, K)) != QP_OK) return st;
+  st = check_ptrs({{codes, "codes", true}, {scales, "scales", true}, {x, "x", true}});
+  if (st != QP_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(qp::launch_checkpoint_restore(codes, scales, M, K, x, x_dtype,
+                                                  (hipStream_t)stream),
+                    "qpack_checkpoint_restore launch");
+}
+
+qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int32_t x_dtype, int64_t M, int32_t save,
+                                        size_t* bytes) {
+  if (!bytes) return fail(QP_EINVAL, "bytes is NULL");
+  *bytes = 0;
+  qp::Desc dd;
+  qp_status st = check_desc(d, &dd);
+  if (st != QP_OK || (st = check_act_dtype(x_dtype, "x_dtype")) != QP_OK ||
+      (st = check_block(dd, M)) != QP_OK)
+    return st;
+  (void)save;
+  return ok();
+}
+
+qp_status qlinear_gated_forward(const qp_desc* d, const void* x, int32_t x_dtype, int64_t M,
+                                const qp_weights* gate, const qp_weights* up, const void* bias_gate,
+                                const void* bias_up, int32_t act, void* h, int32_t h_dtype,
+                                void* gate_codes, float* gate_scales, void* up_codes,
+                                float* up_scales, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  qp::Desc dd;
+  qp_status st = check_desc(d, &dd);
+  if (st != QP_OK || (st = check_act_dtype(x_dtype, "x_dtype")) != QP_OK ||
+      (st = check_block(dd, M)) != QP_OK || (st = check_weights(dd, gate, false)) != QP_OK ||
+      (st = check_weights(dd, up, false)) != QP_OK ||
+      (st = check_out_dtype(h_dtype, "h_dtype")) != QP_OK)
+    return st;
+  if (act != QP_ACT_SILU && act != QP_ACT_GELU_TANH)
+    return fail(QP_EINVAL, "unknown activation %d", act);
+  const bool save = gate_codes || gate_scales || up_codes || up_scales;
+  st = check_ptrs({{x, "x", true}, {h, "h", true}, {bias_gate, "bias_gate", false},
+                   {bias_up, "bias_up", false}, {gate_codes, "gate_codes", save},
+                   {gate_scales, "gate_scales", save}, {up_codes, "up_codes", save},
+                   {up_scales, "up_scales", save}, {workspace, "workspace", false}});
+  if (st != QP_OK) return st;
+  if (h == x) return fail(QP_EINVAL, "h must be a buffer of its own");
+  (void)workspace_bytes;
+  qp::GatedArgs a{x, x_dtype, h_dtype, act, M, bufs_of(gate), bufs_of(up), bias_gate, bias_up, h,
+                  static_cast<int8_t*>(gate_codes), gate_scales, static_cast<int8_t*>(up_codes),
+                  up_scales};
+  (void)hipGetLastError();
+  return hip_status(qp::launch_gated_any(dd, a, (hipStream_t)stream), "qlinear_gated_forward launch");
+}
+
+qp_status qlinear_backward_workspace_bytes(const qp_desc* d, int64_t M, int32_t gated,
+                                           size_t* bytes) {
+  if (!bytes) return fail(QP_EINVAL, "bytes is NULL");
+  *bytes = 0;
+  qp::Desc dd;
+  qp_status st = check_desc(d, &dd);
+  if (st != QP_OK || (st = check_block(dd, M)) != QP_OK) return st;
+  *bytes = qp::dx_workspace_bytes(dd, M, gated != 0);
+  return ok();
+}
+
+qp_status qlinear_backward(const qp_desc* d, const void* dy, int32_t dy_dtype, int64_t M,
+                           const qp_weights* w, void* dx, int32_t dx_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  qp::Desc dd;
+  qp_status st = check_desc(d, &dd);
+  if (st != QP_OK || (st = check_act_dtype(dy_dtype, "dy_dtype")) != QP_OK ||
+      (st = check_block(dd, M)) != QP_OK || (st = check_weights(dd, w, false)) != QP_OK ||
+      (st = check_out_dtype(dx_dtype, "dx_dtype")) != QP_OK ||
+      (st = check_ptrs({{dy, "dy", true}, {dx, "dx", true}})) != QP_OK ||
+      (st = check_workspace(workspace, workspace_bytes, qp::dx_workspace_bytes(dd, M, false))) != QP_OK)
+    return st;
+  if (dx == dy) return fail(QP_EINVAL, "dx must be a buffer of its own");
+  qp::DxArgs a{};
+  a.dy = dy;
+  a.dydt = dy_dtype;
+  a.dxdt = dx_dtype;
+  a.M = M;
+  a.w = a.w2 = bufs_of(w);
+  a.dx = dx;
+  a.ws = workspace;
+  (void)hipGetLastError();
+  return hip_status(qp::launch_dx(dd, a, (hipStream_t)stream), "qlinear_backward launch");
+}
+
+qp_status qlinear_gated_backward(const qp_desc* d, const void* dh, int32_t dh_dtype, int64_t M,
+                                 const qp_weights* gate, const qp_weights* up, int32_t act,
+                                 const void* gate_codes, const float* gate_scales,
+                                 const void* up_codes, const float* up_scales, void* dgate,
+                                 void* dup, void* dx, int32_t dx_dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  qp::Desc dd;
+  qp_status st = check_desc(d, &dd);
+  if (st != QP_OK || (st = check_act_dtype(dh_dtype, "dh_dtype")) != QP_OK ||
+      (st = check_block(dd, M)) != QP_OK || (st = check_weights(dd, gate, false)) != QP_OK ||
+      (st = check_weights(dd, up, false)) != QP_OK ||
+      (st = check_out_dtype(dx_dtype, "dx_dtype")) != QP_OK)
+    return st;
+  if (act != QP_ACT_SILU && act != QP_ACT_GELU_TANH)
+    return fail(QP_EINVAL, "unknown activation %d", act);
+  st = check_ptrs({{dh, "dh", true}, {gate_codes, "gate_codes", true},
+                   {gate_scales, "gate_scales", true}, {up_codes, "up_codes", true},
+                   {up_scales, "up_scales", true}, {dgate, "dgate", false}, {dup, "dup", false},
+                   {dx, "dx", true}});
+  if (st != QP_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, qp::dx_workspace_bytes(dd, M, true))) != QP_OK)
+    return st;
+  if (dx == dh || dgate == dh || dup == dh || (dgate && dgate == dup) || dgate == dx || dup == dx)
+    return fail(QP_EINVAL, "dx, dgate and dup must be buffers of their own");
+  qp::DxArgs a{};
+  a.dy = dh;
+  a.dydt = dh_dtype;
+  a.dxdt = dx_dtype;
+  a.act = act;
+  a.M = M;
+  a.w = bufs_of(gate);
+  a.w2 = bufs_of(up);
+  a.gated = true;
+  a.gq = static_cast<const int8_t*>(gate_codes);
+  a.gs = gate_scales;
+  a.uq = static_cast<const int8_t*>(up_codes);
+  a.us = up_scales;
+  a.dg = dgate;
+  a.du = dup;
+  a.dx = dx;
+  a.ws = workspace;
+  (void)hipGetLastError();
+  return hip_status(qp::launch_dx(dd, a, (hipStream_t)stream), "qlinear_gated_backward launch");
 }
 
 }  // extern "C"

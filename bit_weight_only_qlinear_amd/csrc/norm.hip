@@ -1,0 +1,635 @@
+// RMS norm with the residual's addition, forward (16-bit rows, or int8 rows
+// with one scale each for the a8w4 path) and backward, and 8-bit activation
+// checkpoints.
+//
+// Mathematics, per row of K values:
+//   s = x + r (rounded once to the activation type, as it is kept);
+//   rstd = (sum s^2 / K + eps)^(-1/2);  y = s w rstd.
+//   int8: ys = fl32(max |y| / 127), yq = rint(y / ys).
+//   backward: xh = s rstd, c = sum(dy w xh) / K,
+//   ds = rstd (dy w - xh c) + ds_in;  dw[k] = sum over rows of dy xh.
+// s w of two 16-bit values is exact in fp32 (at most 22 significant bits), so
+// the int8 row needs only one reduction: sum s^2 and max |s w| together, and
+// max |y| = rstd max |s w|.  The sum and the int8 quotient are held in fp64:
+// a code then differs from the exact value's only within 1e-14 of a tie, and
+// squares of large bf16 do not overflow.  All of it is memory bound (6 to 8
+// bytes per value at two or three fp64 operations), so each row is read once,
+// kept in registers as raw 16-byte chunks, and written once.
+//
+// A checkpoint is one int8 code per value and an fp32 scale per 64 columns
+// of a row: scale = fl32(max |x| / 127), code = rint(x / scale).
+#include "device_common.hpp"
+#include "qp_internal.hpp"
+
+namespace qp {
+namespace {
+
+template <bool BF>
+__device__ __forceinline__ float val16(uint32_t bits) {
+  return BF ? bf16_to_f32(bits) : f16_to_f32(bits);
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t rnd16(float f) {
+  return BF ? f32_to_bf16_rne(f) : f32_to_f16_rne(f);
+}
+template <bool BF>
+__device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = val16<BF>(w[i] & 0xFFFFu);
+    v[2 * i + 1] = val16<BF>(w[i] >> 16);
+  }
+}
+template <bool BF>
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = rnd16<BF>(v[2 * i]) | (rnd16<BF>(v[2 * i + 1]) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void unpack8i(uint2 u, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = (float)(int8_t)(u.x >> (8 * i));
+    v[4 + i] = (float)(int8_t)(u.y >> (8 * i));
+  }
+}
+__device__ __forceinline__ uint32_t pack4i(const int (&q)[8], int o) {
+  return ((uint32_t)q[o] & 255u) | (((uint32_t)q[o + 1] & 255u) << 8) |
+         (((uint32_t)q[o + 2] & 255u) << 16) | ((uint32_t)q[o + 3] << 24);
+}
+
+__device__ __forceinline__ double shfl_xor_d(double v, int off) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)u, off, 64);
+  const uint32_t hi = (uint32_t)__shfl_xor((int)(uint32_t)(u >> 32), off, 64);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Sum and maximum over the TPR threads of a row (a multiple of 64); every
+// thread gets both.  red: one slot per wave of the block.
+template <int TPR>
+__device__ __forceinline__ void row_reduce(double& sum, float& mx, double* red_s, float* red_m) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    sum += shfl_xor_d(sum, off);
+    mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+  }
+  if constexpr (TPR > 64) {
+    const int wave = threadIdx.x >> 6, w0 = wave / (TPR / 64) * (TPR / 64);
+    __syncthreads();   // a row before may still read the slots
+    if ((threadIdx.x & 63) == 0) {
+      red_s[wave] = sum;
+      red_m[wave] = mx;
+    }
+    __syncthreads();
+    sum = 0.;
+    mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) {   // the same order in every thread
+      sum += red_s[w0 + i];
+      mx = fmaxf(mx, red_m[w0 + i]);
+    }
+  }
+}
+
+// The int8 row's scale from max |s w| and rstd, and what s w is multiplied
+// with to give the code before rounding (0 for a row of zeros).
+__device__ __forceinline__ void q8_scale(float mx, double rstd, float& ys, double& mul) {
+  ys = (float)((double)mx * rstd / 127.);
+  mul = ys > 0.f ? rstd / (double)ys : 0.;
+}
+__device__ __forceinline__ int q8_code(float p, double mul) {
+  const int q = (int)rint((double)p * mul);
+  return q > 127 ? 127 : q < -127 ? -127 : q;
+}
+
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* r;
+  const uint16_t* w;
+  uint16_t* s;
+  uint16_t* y;
+  int8_t* yq;
+  float* ys;
+  float* rstd;
+  int64_t M, K;
+  float eps;
+};
+
+// One row per TPR threads, NU chunks of 8 columns per thread (K % 8 == 0,
+// K <= 8 TPR NU).
+template <bool BF, int TPR, int NU>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm(NormArgs a) {
+  constexpr int NT = TPR < 256 ? 256 : TPR;
+  __shared__ double red_s[NT / 64];
+  __shared__ float red_m[NT / 64];
+  const int t = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
+  if (TPR < 256 && row >= a.M) return;   // whole waves (TPR == 64 needs no barrier)
+  const uint32_t nq = (uint32_t)(a.K / 8);
+  const int64_t base = row * a.K;
+  const uint4* xr = reinterpret_cast<const uint4*>(a.x + base);
+  const uint4* rr = reinterpret_cast<const uint4*>(a.r + base);
+  const uint4* wr = reinterpret_cast<const uint4*>(a.w);
+  uint4 u[NU], w[NU];
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const uint32_t c = t + TPR * i;
+    u[i] = c < nq ? xr[c] : make_uint4(0, 0, 0, 0);
+  }
+  if (a.r) {
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const uint32_t c = t + TPR * i;
+      w[i] = c < nq ? rr[c] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      float v[8], b[8];
+      unpack8<BF>(u[i], v);
+      unpack8<BF>(w[i], b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += b[e];   // rounds to 24 bits, then to the type: one rounding
+      u[i] = pack8<BF>(v);
+    }
+    if (a.s) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        const uint32_t c = t + TPR * i;
+        if (c < nq) reinterpret_cast<uint4*>(a.s + base)[c] = u[i];
+      }
+    }
+  }
+  const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const uint32_t c = t + TPR * i;
+    w[i] = a.w && c < nq ? wr[c] : make_uint4(one, one, one, one);
+  }
+  double sum = 0.;
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    float v[8], b[8];
+    unpack8<BF>(u[i], v);
+    unpack8<BF>(w[i], b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double d = v[e];
+      sum = fma(d, d, sum);
+      mx = fmaxf(mx, fabsf(v[e] * b[e]));
+    }
+  }
+  row_reduce<TPR>(sum, mx, red_s, red_m);
+  const double rstd = 1. / sqrt(sum / (double)a.K + (double)a.eps);
+  if (a.rstd && t == 0) a.rstd[row] = (float)rstd;
+  if (a.yq) {
+    float ys;
+    double mul;
+    q8_scale(mx, rstd, ys, mul);
+    if (t == 0) a.ys[row] = ys;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const uint32_t c = t + TPR * i;
+      float v[8], b[8];
+      unpack8<BF>(u[i], v);
+      unpack8<BF>(w[i], b);
+      int q[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = q8_code(v[e] * b[e], mul);
+      if (c < nq)
+        reinterpret_cast<uint2*>(a.yq + base)[c] = make_uint2(pack4i(q, 0), pack4i(q, 4));
+    }
+  } else {
+    const float rs = (float)rstd;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const uint32_t c = t + TPR * i;
+      float v[8], b[8];
+      unpack8<BF>(u[i], v);
+      unpack8<BF>(w[i], b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * b[e] * rs;
+      if (c < nq) reinterpret_cast<uint4*>(a.y + base)[c] = pack8<BF>(v);
+    }
+  }
+}
+
+// Any K: scalar columns, two passes over the row.  s is written in the
+// second pass only, after the thread has read the same element of x and r,
+// so it may be either of them.
+template <bool BF>
+__global__ void __launch_bounds__(256) k_norm_any(NormArgs a) {
+  __shared__ double red_s[4];
+  __shared__ float red_m[4];
+  const int64_t row = blockIdx.x, base = row * a.K;
+  auto stream = [&](int64_t k) {
+    uint32_t b = a.x[base + k];
+    if (a.r) b = rnd16<BF>(val16<BF>(b) + val16<BF>(a.r[base + k]));
+    return b;
+  };
+  auto weight = [&](int64_t k) { return a.w ? val16<BF>(a.w[k]) : 1.f; };
+  double sum = 0.;
+  float mx = 0.f;
+  for (int64_t k = threadIdx.x; k < a.K; k += 256) {
+    const float v = val16<BF>(stream(k));
+    sum = fma((double)v, (double)v, sum);
+    mx = fmaxf(mx, fabsf(v * weight(k)));
+  }
+  row_reduce<256>(sum, mx, red_s, red_m);
+  const double rstd = 1. / sqrt(sum / (double)a.K + (double)a.eps);
+  if (a.rstd && threadIdx.x == 0) a.rstd[row] = (float)rstd;
+  float ys;
+  double mul;
+  q8_scale(mx, rstd, ys, mul);
+  if (a.yq && threadIdx.x == 0) a.ys[row] = ys;
+  const float rs = (float)rstd;
+  for (int64_t k = threadIdx.x; k < a.K; k += 256) {
+    const uint32_t b = stream(k);
+    const float p = val16<BF>(b) * weight(k);
+    if (a.r && a.s) a.s[base + k] = (uint16_t)b;
+    if (a.yq) a.yq[base + k] = (int8_t)q8_code(p, mul);
+    else a.y[base + k] = (uint16_t)rnd16<BF>(p * rs);
+  }
+}
+
+struct NormBwdArgs {
+  const uint16_t* dy;
+  const uint16_t* s;     // the kept stream, or
+  const int8_t* sq;      // its checkpoint: codes and scales
+  const float* ss;
+  const uint16_t* w;
+  const float* rstd;
+  const uint16_t* ds_in;
+  uint16_t* ds;
+  float* part;           // [gridDim.x, K] column sums of the block's rows, or null
+  int64_t M, K;
+};
+
+// Rows blockIdx.x, + gridDim.x, ...: ds of each, and the rows' share of dw
+// in registers (NU * 8 columns per thread).  K % 8 == 0, K <= 8 NT NU.
+template <bool BF, bool CK, int NT, int NU>
+__global__ void __launch_bounds__(NT) k_norm_bwd(NormBwdArgs a) {
+  __shared__ double red_s[NT / 64];
+  __shared__ float red_m[NT / 64];
+  const int t = threadIdx.x;
+  const uint32_t nq = (uint32_t)(a.K / 8);
+  const int64_t ng = (a.K + 63) / 64;
+  const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
+  const uint4 Z = make_uint4(0, 0, 0, 0);
+  uint4 w[NU];
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const uint32_t c = t + NT * i;
+    w[i] = a.w && c < nq ? reinterpret_cast<const uint4*>(a.w)[c] : make_uint4(one, one, one, one);
+  }
+  float dw[NU][8];
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
+    const int64_t base = row * a.K;
+    uint4 d[NU], di[NU];
+    uint4 s[NU];       // raw stream, or codes (x, y) and scale bits (z)
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const uint32_t c = t + NT * i;
+      const bool ok = c < nq;
+      d[i] = ok ? reinterpret_cast<const uint4*>(a.dy + base)[c] : Z;
+      if constexpr (CK) {
+        const uint2 q = ok ? reinterpret_cast<const uint2*>(a.sq + base)[c] : make_uint2(0, 0);
+        const float sc = ok ? a.ss[row * ng + c / 8] : 0.f;
+        s[i] = make_uint4(q.x, q.y, __float_as_uint(sc), 0);
+      } else {
+        s[i] = ok ? reinterpret_cast<const uint4*>(a.s + base)[c] : Z;
+      }
+      di[i] = ok && a.ds_in ? reinterpret_cast<const uint4*>(a.ds_in + base)[c] : Z;
+    }
+    auto stream = [&](int i, float (&v)[8]) {
+      if constexpr (CK) {
+        unpack8i(make_uint2(s[i].x, s[i].y), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= __uint_as_float(s[i].z);
+      } else {
+        unpack8<BF>(s[i], v);
+      }
+    };
+    const float rs = a.rstd[row];
+    double dot = 0.;
+    float none = 0.f;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      float v[8], g[8], b[8];
+      stream(i, v);
+      unpack8<BF>(d[i], g);
+      unpack8<BF>(w[i], b);
+      float part = 0.f;   // 8 products in fp32, then fp64
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float xh = v[e] * rs;
+        part = fmaf(g[e] * b[e], xh, part);
+        dw[i][e] = fmaf(g[e], xh, dw[i][e]);
+      }
+      dot += part;
+    }
+    if (!a.ds) continue;   // uniform
+    row_reduce<NT>(dot, none, red_s, red_m);
+    const float c1 = (float)(dot / (double)a.K);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const uint32_t c = t + NT * i;
+      float v[8], g[8], b[8], z[8];
+      stream(i, v);
+      unpack8<BF>(d[i], g);
+      unpack8<BF>(w[i], b);
+      unpack8<BF>(di[i], z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = fmaf(rs, fmaf(-v[e] * rs, c1, g[e] * b[e]), z[e]);
+      if (c < nq) reinterpret_cast<uint4*>(a.ds + base)[c] = pack8<BF>(z);
+    }
+  }
+  if (a.part) {
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const uint32_t c = t + NT * i;
+      if (c < nq) {
+        float4* p = reinterpret_cast<float4*>(a.part + (int64_t)blockIdx.x * a.K) + 2 * c;
+        p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+        p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+      }
+    }
+  }
+}
+
+template <bool BF, bool CK>
+__device__ __forceinline__ float stream_at(const NormBwdArgs& a, int64_t row, int64_t k) {
+  if constexpr (CK)
+    return (float)a.sq[row * a.K + k] * a.ss[row * ((a.K + 63) / 64) + k / 64];
+  else
+    return val16<BF>(a.s[row * a.K + k]);
+}
+
+// Any K: ds of one row per block, scalar columns.
+template <bool BF, bool CK>
+__global__ void __launch_bounds__(256) k_norm_bwd_any(NormBwdArgs a) {
+  __shared__ double red_s[4];
+  __shared__ float red_m[4];
+  const int64_t row = blockIdx.x, base = row * a.K;
+  const float rs = a.rstd[row];
+  auto weight = [&](int64_t k) { return a.w ? val16<BF>(a.w[k]) : 1.f; };
+  double dot = 0.;
+  float none = 0.f;
+  for (int64_t k = threadIdx.x; k < a.K; k += 256)
+    dot += (double)(val16<BF>(a.dy[base + k]) * weight(k) * (stream_at<BF, CK>(a, row, k) * rs));
+  row_reduce<256>(dot, none, red_s, red_m);
+  const float c1 = (float)(dot / (double)a.K);
+  for (int64_t k = threadIdx.x; k < a.K; k += 256) {
+    const float z = a.ds_in ? val16<BF>(a.ds_in[base + k]) : 0.f;
+    const float g = val16<BF>(a.dy[base + k]) * weight(k);
+    a.ds[base + k] =
+        (uint16_t)rnd16<BF>(fmaf(rs, fmaf(-stream_at<BF, CK>(a, row, k) * rs, c1, g), z));
+  }
+}
+
+// Any K: column sums of dy xh over rows blockIdx.y, + gridDim.y, ...
+template <bool BF, bool CK>
+__global__ void __launch_bounds__(256) k_norm_dw_any(NormBwdArgs a) {
+  const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (k >= a.K) return;
+  float v = 0.f;
+  for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y)
+    v = fmaf(val16<BF>(a.dy[row * a.K + k]), stream_at<BF, CK>(a, row, k) * a.rstd[row], v);
+  a.part[(int64_t)blockIdx.y * a.K + k] = v;
+}
+
+// dw[k] = sum of the P partial rows, in fp64 and a fixed order: 64 columns
+// per block, 16 waves taking every 16th row.
+__global__ void __launch_bounds__(1024) k_col_sum(const float* __restrict__ part, int P, int64_t K,
+                                                  float* __restrict__ out) {
+  __shared__ double red[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t k = (int64_t)blockIdx.x * 64 + lane;
+  double v = 0.;
+  if (k < K) {
+#pragma unroll 8
+    for (int p = wave; p < P; p += 16) v += (double)part[(int64_t)p * K + k];
+  }
+  red[wave][lane] = v;
+  __syncthreads();
+  if (wave == 0 && k < K) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += red[i][lane];
+    out[k] = (float)v;
+  }
+}
+
+// Code of v under a positive scale: the quotient from the reciprocal in fp64
+// with one correction step, exact where v / scale is a tie, so that ties go
+// to even as the definition says.
+__device__ __forceinline__ int ckpt_code(float v, double sc, double inv) {
+  double q = (double)v * inv;
+  q = fma(fma(-q, sc, (double)v), inv, q);
+  const int c = (int)rint(q);
+  return c > 127 ? 127 : c < -127 ? -127 : c;
+}
+
+// 8 lanes per group of 64 columns, 8 columns per lane (K % 8 == 0).  `n`
+// threads in all: rows of ng groups, the last one possibly short.
+template <bool BF>
+__global__ void __launch_bounds__(256) k_ckpt(const uint16_t* __restrict__ x, int8_t* __restrict__ q,
+                                              float* __restrict__ s, uint32_t ng, uint32_t nq,
+                                              uint64_t groups) {
+  const uint64_t grp = (uint64_t)blockIdx.x * 32 + threadIdx.x / 8;
+  const uint32_t l = threadIdx.x & 7;
+  const uint64_t row = grp / ng;
+  const uint32_t gi = (uint32_t)(grp - row * ng), c = gi * 8 + l;
+  const bool ok = grp < groups && c < nq;
+  const uint64_t at = row * nq + c;   // chunk of 8 columns
+  const uint4 u = ok ? reinterpret_cast<const uint4*>(x)[at] : make_uint4(0, 0, 0, 0);
+  float v[8], mx = 0.f;
+  unpack8<BF>(u, v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
+  mx = fmaxf(mx, __shfl_xor(mx, 1, 64));
+  mx = fmaxf(mx, __shfl_xor(mx, 2, 64));
+  mx = fmaxf(mx, __shfl_xor(mx, 4, 64));
+  const float sc = div_rn(mx, 127.f);
+  const double inv = sc > 0.f ? 1. / (double)sc : 0.;
+  int cq[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) cq[e] = ckpt_code(v[e], sc, inv);
+  if (ok) reinterpret_cast<uint2*>(q)[at] = make_uint2(pack4i(cq, 0), pack4i(cq, 4));
+  if (l == 0 && grp < groups) s[grp] = sc;
+}
+
+// Any K: one wave per group, one column per lane.
+template <bool BF>
+__global__ void __launch_bounds__(256) k_ckpt_any(const uint16_t* __restrict__ x,
+                                                  int8_t* __restrict__ q, float* __restrict__ s,
+                                                  uint32_t ng, int64_t K, uint64_t groups) {
+  const uint64_t grp = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (grp >= groups) return;   // whole waves
+  const uint32_t lane = threadIdx.x & 63;
+  const uint64_t row = grp / ng;
+  const int64_t k = (int64_t)(grp - row * ng) * 64 + lane;
+  const float v = k < K ? val16<BF>(x[row * K + k]) : 0.f;
+  const float sc = div_rn(wave_max_all(fabsf(v)), 127.f);
+  const double inv = sc > 0.f ? 1. / (double)sc : 0.;
+  if (k < K) q[row * K + k] = (int8_t)ckpt_code(v, sc, inv);
+  if (lane == 0) s[grp] = sc;
+}
+
+template <int DT>
+__device__ __forceinline__ void put(void* x, uint64_t i, float v) {
+  if constexpr (DT == F32) static_cast<float*>(x)[i] = v;
+  else static_cast<uint16_t*>(x)[i] = (uint16_t)rnd16<DT == BF16>(v);
+}
+
+// Codes back to values; V = 8 columns per thread (K % 8 == 0) or 1.
+template <int DT, int V>
+__global__ void __launch_bounds__(256) k_ckpt_restore(const int8_t* __restrict__ q,
+                                                      const float* __restrict__ s, uint32_t ng,
+                                                      uint32_t nq, uint64_t n,
+                                                      void* __restrict__ x) {
+  const uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= n) return;
+  const uint64_t row = at / nq;
+  const uint32_t c = (uint32_t)(at - row * nq);
+  const float sc = s[row * ng + c / (64 / V)];
+  if constexpr (V == 1) {
+    put<DT>(x, at, (float)q[at] * sc);
+  } else {
+    float v[8];
+    unpack8i(reinterpret_cast<const uint2*>(q)[at], v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= sc;
+    if constexpr (DT == F32) {
+      float4* o = static_cast<float4*>(x) + 2 * at;
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      static_cast<uint4*>(x)[at] = pack8<DT == BF16>(v);
+    }
+  }
+}
+
+typedef void (*NormFn)(NormArgs);
+typedef void (*NormBwdFn)(NormBwdArgs);
+
+template <bool BF>
+NormFn norm_pick(int tpr, int nu) {
+  if (tpr == 64) return nu <= 1 ? k_norm<BF, 64, 1> : nu <= 2 ? k_norm<BF, 64, 2> : k_norm<BF, 64, 4>;
+  if (tpr == 256) return nu <= 1 ? k_norm<BF, 256, 1> : nu <= 2 ? k_norm<BF, 256, 2> : k_norm<BF, 256, 4>;
+  return nu <= 1 ? k_norm<BF, 1024, 1> : nu <= 2 ? k_norm<BF, 1024, 2> : k_norm<BF, 1024, 4>;
+}
+
+template <bool BF, bool CK>
+NormBwdFn norm_bwd_pick(int64_t nq) {
+  if (nq <= 256) return k_norm_bwd<BF, CK, 256, 1>;
+  if (nq <= 512) return k_norm_bwd<BF, CK, 256, 2>;
+  if (nq <= 1024) return k_norm_bwd<BF, CK, 512, 2>;
+  if (nq <= 2048) return k_norm_bwd<BF, CK, 1024, 2>;
+  return k_norm_bwd<BF, CK, 1024, 4>;
+}
+int norm_bwd_threads(int64_t nq) { return nq <= 512 ? 256 : nq <= 1024 ? 512 : 1024; }
+
+}  // namespace
+
+hipError_t launch_norm(const void* x, const void* r, int dt, int64_t M, int64_t K, const void* w,
+                       float eps, void* s, void* y, void* yq, float* ys, float* rstd,
+                       hipStream_t st) {
+  NormArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(r),
+             static_cast<const uint16_t*>(w), static_cast<uint16_t*>(s),
+             static_cast<uint16_t*>(y), static_cast<int8_t*>(yq), ys, rstd, M, K, eps};
+  const int64_t nq = K / 8;
+  if (K % 8 || nq > 4096) {
+    auto fn = dt == BF16 ? k_norm_any<true> : k_norm_any<false>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)M), dim3(256), 0, st, a);
+    return hipGetLastError();
+  }
+  int tpr = nq <= 64 ? 64 : nq <= 1024 ? 256 : 1024;
+  const int nu = (int)((nq + tpr - 1) / tpr);
+  const int rows = tpr == 64 ? 4 : 1;
+  auto fn = dt == BF16 ? norm_pick<true>(tpr, nu) : norm_pick<false>(tpr, nu);
+  hipLaunchKernelGGL(fn, dim3((unsigned)((M + rows - 1) / rows)), dim3(tpr < 256 ? 256 : tpr), 0,
+                     st, a);
+  return hipGetLastError();
+}
+
+int norm_bwd_parts(int64_t M) { return (int)(M < 512 ? M : 512); }
+
+hipError_t launch_norm_bwd(const void* dy, const void* s, const void* sq, const float* ss, int dt,
+                           int64_t M, int64_t K, const void* w, const float* rstd,
+                           const void* ds_in, void* ds, float* dw, float* part, hipStream_t st) {
+  NormBwdArgs a{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(s),
+                static_cast<const int8_t*>(sq), ss, static_cast<const uint16_t*>(w), rstd,
+                static_cast<const uint16_t*>(ds_in), static_cast<uint16_t*>(ds),
+                dw ? part : nullptr, M, K};
+  const bool bf = dt == BF16, ck = sq != nullptr;
+  const int64_t nq = K / 8;
+  const unsigned P = (unsigned)norm_bwd_parts(M);
+  hipError_t e;
+  if (K % 8 || nq > 4096) {
+    if (ds) {
+      auto fn = bf ? (ck ? k_norm_bwd_any<true, true> : k_norm_bwd_any<true, false>)
+                   : (ck ? k_norm_bwd_any<false, true> : k_norm_bwd_any<false, false>);
+      hipLaunchKernelGGL(fn, dim3((unsigned)M), dim3(256), 0, st, a);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (dw) {
+      auto fn = bf ? (ck ? k_norm_dw_any<true, true> : k_norm_dw_any<true, false>)
+                   : (ck ? k_norm_dw_any<false, true> : k_norm_dw_any<false, false>);
+      hipLaunchKernelGGL(fn, dim3((unsigned)((K + 255) / 256), P), dim3(256), 0, st, a);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+  } else {
+    auto fn = bf ? (ck ? norm_bwd_pick<true, true>(nq) : norm_bwd_pick<true, false>(nq))
+                 : (ck ? norm_bwd_pick<false, true>(nq) : norm_bwd_pick<false, false>(nq));
+    hipLaunchKernelGGL(fn, dim3(P), dim3(norm_bwd_threads(nq)), 0, st, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (dw) {
+    hipLaunchKernelGGL(k_col_sum, dim3((unsigned)((K + 63) / 64)), dim3(1024), 0, st, part, (int)P,
+                       K, dw);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_checkpoint(const void* x, int dt, int64_t M, int64_t K, void* q, float* s,
+                             hipStream_t st) {
+  const uint32_t ng = (uint32_t)((K + 63) / 64);
+  const uint64_t groups = (uint64_t)M * ng;
+  if (K % 8) {
+    auto fn = dt == BF16 ? k_ckpt_any<true> : k_ckpt_any<false>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)((groups + 3) / 4)), dim3(256), 0, st,
+                       static_cast<const uint16_t*>(x), static_cast<int8_t*>(q), s, ng, K, groups);
+  } else {
+    auto fn = dt == BF16 ? k_ckpt<true> : k_ckpt<false>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)((groups + 31) / 32)), dim3(256), 0, st,
+                       static_cast<const uint16_t*>(x), static_cast<int8_t*>(q), s, ng,
+                       (uint32_t)(K / 8), groups);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_checkpoint_restore(const void* q, const float* s, int64_t M, int64_t K, void* x,
+                                     int dt, hipStream_t st) {
+  const uint32_t ng = (uint32_t)((K + 63) / 64);
+  const bool v8 = K % 8 == 0;
+  const uint32_t nq = (uint32_t)(v8 ? K / 8 : K);
+  const uint64_t n = (uint64_t)M * nq;
+  auto fn = v8 ? (dt == F32 ? k_ckpt_restore<F32, 8>
+                  : dt == BF16 ? k_ckpt_restore<BF16, 8> : k_ckpt_restore<F16, 8>)
+               : (dt == F32 ? k_ckpt_restore<F32, 1>
+                  : dt == BF16 ? k_ckpt_restore<BF16, 1> : k_ckpt_restore<F16, 1>);
+  hipLaunchKernelGGL(fn, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st,
+                     static_cast<const int8_t*>(q), s, ng, nq, n, x);
+  return hipGetLastError();
+}
+
+}  // namespace qp

@@ -9,6 +9,8 @@ namespace qp {
 
 enum Fmt : int { AFFINE = 0, Q4K = 1, Q6K = 2, SYM4 = 3 };
 enum DType : int { F16 = 0, BF16 = 1, F32 = 2 };
+enum Act : int { ACT_SILU = 0, ACT_GELU_TANH = 1 };
+constexpr int kCkptGroup = 64;   // columns per scale of an 8-bit checkpoint
 
 // Validated, host-side copy of the descriptor.
 struct Desc {
@@ -71,6 +73,60 @@ hipError_t launch_quant_act(const void* x, int xdt, int64_t M, int64_t K, void* 
 // a8w4 forward (SYM4 per output channel, K % 128 == 0, every buffer < 2 GiB).
 hipError_t launch_a8w4(const Desc& d, const void* xq, const float* xs, int64_t M, const Bufs& b,
                        const float* bias, void* y, int ydt, hipStream_t s);
+
+// RMS norm with the residual's addition (norm.hip).  y, or yq and ys.
+hipError_t launch_norm(const void* x, const void* r, int dt, int64_t M, int64_t K, const void* w,
+                       float eps, void* s, void* y, void* yq, float* ys, float* rstd,
+                       hipStream_t st);
+// Its backward; s, or its checkpoint (sq, ss).  part: norm_bwd_parts(M) * K
+// floats where dw is asked for.
+int norm_bwd_parts(int64_t M);
+hipError_t launch_norm_bwd(const void* dy, const void* s, const void* sq, const float* ss, int dt,
+                           int64_t M, int64_t K, const void* w, const float* rstd,
+                           const void* ds_in, void* ds, float* dw, float* part, hipStream_t st);
+// 8-bit checkpoints: int8 codes [M, K], fp32 scales [M, ceil(K / 64)].
+hipError_t launch_checkpoint(const void* x, int dt, int64_t M, int64_t K, void* q, float* s,
+                             hipStream_t st);
+hipError_t launch_checkpoint_restore(const void* q, const float* s, int64_t M, int64_t K, void* x,
+                                     int dt, hipStream_t st);
+
+// Gated pair of projections: h = act(x Wg^T + bg) * (x Wu^T + bu), both
+// layers of descriptor d.  gq .. us: 8-bit checkpoints of the two
+// pre-activations, or all null.
+struct GatedArgs {
+  const void* x;
+  int xdt, hdt, act;
+  int64_t M;
+  Bufs gate, up;
+  const void* bias_g;
+  const void* bias_u;
+  void* h;
+  int8_t* gq;
+  float* gs;
+  int8_t* uq;
+  float* us;
+};
+hipError_t launch_gated_any(const Desc& d, const GatedArgs& a, hipStream_t s);
+
+// Input gradients.  dx [M, K] = dy [M, N] W, or with `gated` the sum of two
+// such products over dg = dh u act'(g) and du = dh act(g).
+struct DxArgs {
+  const void* dy;         // dy, or dh
+  int dydt, dxdt, act;
+  int64_t M;
+  Bufs w, w2;             // the layer; gate and up layers
+  bool gated;
+  const int8_t* gq;       // checkpoints of the pre-activations (gated)
+  const float* gs;
+  const int8_t* uq;
+  const float* us;
+  void* dg;               // [M, N] of dy's type, or null (gated)
+  void* du;
+  void* dx;
+  void* ws;
+};
+size_t dx_workspace_bytes(const Desc& d, int64_t M, bool gated);
+hipError_t launch_dx(const Desc& d, const DxArgs& a, hipStream_t s);
 
 // Static device scratch of the allocation-free forward (noalloc.hip): its
 // size, and its address on the current device (looked up once per device).

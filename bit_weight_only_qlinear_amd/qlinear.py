@@ -6,9 +6,10 @@ The library must be built (``python -m bit_weight_only_qlinear_amd.build``
 or ``__graft_entry__.build()``); importing this module without it raises.
 """
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import Any, NamedTuple, Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqlinear.so")
@@ -16,11 +17,14 @@ LIB_PATH = os.path.join(_HERE, "libqlinear.so")
 QP_OK, QP_EINVAL, QP_ESHAPE, QP_EUNSUPPORTED, QP_EALIGN, QP_EHIP = range(6)
 QP_FMT_AFFINE, QP_FMT_Q4K, QP_FMT_Q6K, QP_FMT_SYM4 = range(4)
 QP_F16, QP_BF16, QP_F32 = range(3)
+QP_ACT_SILU, QP_ACT_GELU_TANH = range(2)
+QP_CHECKPOINT_GROUP = 64
 QP_KERNEL_AUTO, QP_KERNEL_GEMV, QP_KERNEL_GEMM, QP_KERNEL_GEMV_MFMA = range(4)
 
 FMT_IDS = {"affine": QP_FMT_AFFINE, "q4k": QP_FMT_Q4K, "q6k": QP_FMT_Q6K,
            "sym4": QP_FMT_SYM4}
 DTYPE_IDS = {"f16": QP_F16, "bf16": QP_BF16, "f32": QP_F32}
+ACT_IDS = {"silu": QP_ACT_SILU, "gelu_tanh": QP_ACT_GELU_TANH}
 BUFFERS = ("qweight", "qweight_hi", "scales", "zeros", "steps")
 
 
@@ -68,6 +72,18 @@ def _load():
         "qpack_concat_n": (I32, [D, I32, D, W, W, P]),
         "qpack_quantize_activations": (I32, [P, I32, I64, I64, P, P, P]),
         "qlinear_forward_a8w4": (I32, [D, P, P, I64, W, P, P, I32, P]),
+        "qnorm_forward": (I32, [P, P, I32, I64, I64, P, ctypes.c_float, P, P, P, P, P, P]),
+        "qnorm_backward_workspace_bytes": (I32, [I64, I64, ctypes.POINTER(ctypes.c_size_t)]),
+        "qnorm_backward": (I32, [P, P, P, P, I32, I64, I64, P, P, P, P, P, P, ctypes.c_size_t, P]),
+        "qpack_checkpoint": (I32, [P, I32, I64, I64, P, P, P]),
+        "qpack_checkpoint_restore": (I32, [P, P, I64, I64, P, I32, P]),
+        "qlinear_gated_workspace_bytes": (I32, [D, I32, I64, I32, ctypes.POINTER(ctypes.c_size_t)]),
+        "qlinear_gated_forward": (I32, [D, P, I32, I64, W, W, P, P, I32, P, I32, P, P, P, P, P,
+                                        ctypes.c_size_t, P]),
+        "qlinear_backward_workspace_bytes": (I32, [D, I64, I32, ctypes.POINTER(ctypes.c_size_t)]),
+        "qlinear_backward": (I32, [D, P, I32, I64, W, P, I32, P, ctypes.c_size_t, P]),
+        "qlinear_gated_backward": (I32, [D, P, I32, I64, W, W, I32, P, P, P, P, P, P, P, I32, P,
+                                         ctypes.c_size_t, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -84,7 +100,11 @@ EXPORTED = ("qpack_abi_version", "qpack_last_error", "qpack_sizes", "qpack_quant
             "qlinear_forward_ws", "qlinear_forward_static", "qpack_encode_nested",
             "qpack_concat_n",
             "qpack_quantize_activations",
-            "qlinear_forward_a8w4")
+            "qlinear_forward_a8w4",
+            "qnorm_forward", "qnorm_backward_workspace_bytes", "qnorm_backward",
+            "qpack_checkpoint", "qpack_checkpoint_restore",
+            "qlinear_gated_workspace_bytes", "qlinear_gated_forward",
+            "qlinear_backward_workspace_bytes", "qlinear_backward", "qlinear_gated_backward")
 
 
 @dataclass(frozen=True)
@@ -347,3 +367,283 @@ def qlinear_forward_a8w4(desc: QDesc, xq, xs, w, bias=None, y_dtype: str = "bf16
                                     _ptr(bias), _ptr(out), DTYPE_IDS[y_dtype],
                                     _stream(xq.device)))
     return out
+
+
+# ---- the MLP block around the packed layers: RMS norm, 8-bit activation
+# checkpoints, the gated pair of projections, and input gradients.  Every
+# tensor is checked before the call: device, type, shape, contiguous rows.
+
+class QNorm(NamedTuple):
+    """qnorm_forward's outputs; the ones that were not asked for are None."""
+    y: Any        # [M, K] of x's type, or None where quantized
+    s: Any        # the residual stream x + residual (x itself without one)
+    rstd: Any     # fp32 [M]
+    yq: Any       # int8 [M, K] and
+    ys: Any       # fp32 [M]: quantize=True
+
+
+class QGated(NamedTuple):
+    """qlinear_gated_forward's outputs: h, and the checkpoints (codes, scales)
+    of both pre-activations where they were asked for."""
+    h: Any
+    gate: Any
+    up: Any
+
+
+class QGatedGrads(NamedTuple):
+    """qlinear_gated_backward's outputs."""
+    dx: Any
+    dgate: Any
+    dup: Any
+
+
+def _dt_name(t):
+    import torch
+    return {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}.get(t.dtype)
+
+
+def _torch_dt(name):
+    import torch
+    if name not in DTYPE_IDS:
+        raise ValueError(f"dtype must be one of {tuple(DTYPE_IDS)}, got {name!r}")
+    return {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[name]
+
+
+def _arg(t, name, shape, dtype, device):
+    """A device tensor argument of the given shape and type, rows packed."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(t, name, shape, dtype, device):
+    return None if t is None else _arg(t, name, shape, dtype, device)
+
+
+def _rows(t, name):
+    """(M, K, dtype name) of an activation matrix."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix [M, K], got {t.dim()} dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor, got {t.device}")
+    return t.shape[0], t.shape[1], _xdtype(t)
+
+
+@functools.lru_cache(maxsize=None)
+def _expected_sizes(desc):
+    return tuple(qpack_sizes(desc)[n] for n in BUFFERS)
+
+
+def _weights_arg(desc, w, name, device):
+    """The weight struct, its buffers checked against the descriptor."""
+    for n, need in zip(BUFFERS, _expected_sizes(desc)):
+        t = w.get(n)
+        if not need:
+            continue
+        if t is None:
+            raise ValueError(f"{name}[{n!r}] is missing")
+        if t.device != device:
+            raise ValueError(f"{name}[{n!r}] must be on {device}, got {t.device}")
+        if not t.is_contiguous() or t.numel() * t.element_size() < need:
+            raise ValueError(f"{name}[{n!r}] must be contiguous and hold {need} bytes")
+    return _wstruct(w)
+
+
+def _run(device, fn, *args):
+    """Calls a library function on the device's current stream (appended as
+    the last argument), with that device current."""
+    import torch
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream))
+
+
+def _scratch(nbytes, device):
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _groups(n):
+    return (n + QP_CHECKPOINT_GROUP - 1) // QP_CHECKPOINT_GROUP
+
+
+def qnorm_forward(x, weight=None, residual=None, eps: float = 1e-6, quantize: bool = False,
+                  need_rstd: bool = False, s_out=None) -> QNorm:
+    """RMS norm of s = x + residual, times weight: 16-bit rows, or with
+    `quantize` int8 rows with one scale each (qlinear_forward_a8w4's
+    activations).  x, residual [M, K] and weight [K]: fp16 or bf16.  s goes
+    into `s_out` where given (x or residual itself: in place)."""
+    import torch
+    M, K, xd = _rows(x, "x")
+    dev, dt = x.device, x.dtype
+    px = _arg(x, "x", (M, K), dt, dev)
+    pr = _opt(residual, "residual", (M, K), dt, dev)
+    pw = _opt(weight, "weight", (K,), dt, dev)
+    s, ps = x, None
+    if residual is not None:
+        s = torch.empty_like(x) if s_out is None else s_out
+        ps = _arg(s, "s_out", (M, K), dt, dev)
+    elif s_out is not None:
+        raise ValueError("s_out needs a residual (s is x without one)")
+    y = yq = ys = rstd = None
+    if quantize:
+        yq = torch.empty((M, K), dtype=torch.int8, device=dev)
+        ys = torch.empty((M,), dtype=torch.float32, device=dev)
+    else:
+        y = torch.empty_like(x)
+    if need_rstd:
+        rstd = torch.empty((M,), dtype=torch.float32, device=dev)
+    p = [None if t is None else t.data_ptr() for t in (y, yq, ys, rstd)]
+    _run(dev, lib.qnorm_forward, px, pr, DTYPE_IDS[xd], M, K, pw, eps, ps, *p)
+    return QNorm(y, s, rstd, yq, ys)
+
+
+def qnorm_backward(dy, s, rstd, weight=None, saved=None, ds_in=None, need_ds: bool = True,
+                   need_dweight: bool = True):
+    """Gradients of qnorm_forward's 16-bit output: (ds [M, K], dweight fp32
+    [K]), None for one that is not needed.  s: the forward's stream, or None
+    with `saved`, its checkpoint (codes, scales).  ds is the gradient of x
+    and of the residual; ds_in is added to it."""
+    import torch
+    M, K, xd = _rows(dy, "dy")
+    dev, dt = dy.device, dy.dtype
+    if (s is None) == (saved is None):
+        raise ValueError("pass s, or its checkpoint as saved")
+    codes, scales = (None, None) if saved is None else saved
+    ps = _opt(s, "s", (M, K), dt, dev)
+    pc = _opt(codes, "saved codes", (M, K), torch.int8, dev)
+    psc = _opt(scales, "saved scales", (M, _groups(K)), torch.float32, dev)
+    args = (_arg(dy, "dy", (M, K), dt, dev), ps, pc, psc, DTYPE_IDS[xd], M, K,
+            _opt(weight, "weight", (K,), dt, dev), _arg(rstd, "rstd", (M,), torch.float32, dev),
+            _opt(ds_in, "ds_in", (M, K), dt, dev))
+    ds = torch.empty_like(dy) if need_ds else None
+    dw = torch.empty((K,), dtype=torch.float32, device=dev) if need_dweight else None
+    ws, n = None, 0
+    if need_dweight:
+        size = ctypes.c_size_t(0)
+        _check(lib.qnorm_backward_workspace_bytes(M, K, ctypes.byref(size)))
+        n = size.value
+        ws = _scratch(n, dev)
+    _run(dev, lib.qnorm_backward, *args, *[None if t is None else t.data_ptr()
+                                           for t in (ds, dw, ws)], n)
+    return ds, dw
+
+
+def qpack_checkpoint(x):
+    """8-bit checkpoint of activations x [M, K]: (codes int8 [M, K], scales
+    fp32 [M, ceil(K / 64)])."""
+    import torch
+    M, K, xd = _rows(x, "x")
+    px = _arg(x, "x", (M, K), x.dtype, x.device)
+    codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    scales = torch.empty((M, _groups(K)), dtype=torch.float32, device=x.device)
+    _run(x.device, lib.qpack_checkpoint, px, DTYPE_IDS[xd], M, K, codes.data_ptr(),
+         scales.data_ptr())
+    return codes, scales
+
+
+def qpack_checkpoint_restore(saved, dtype: str = "bf16"):
+    """The values a checkpoint (codes, scales) stands for, [M, K] of `dtype`."""
+    import torch
+    codes, scales = saved
+    if codes.dim() != 2:
+        raise ValueError("codes must be a matrix [M, K]")
+    M, K = codes.shape
+    pc = _arg(codes, "codes", (M, K), torch.int8, codes.device)
+    ps = _arg(scales, "scales", (M, _groups(K)), torch.float32, codes.device)
+    x = torch.empty((M, K), dtype=_torch_dt(dtype), device=codes.device)
+    _run(codes.device, lib.qpack_checkpoint_restore, pc, ps, M, K, x.data_ptr(), DTYPE_IDS[dtype])
+    return x
+
+
+def _act_id(act):
+    if act not in ACT_IDS:
+        raise ValueError(f"act must be one of {tuple(ACT_IDS)}, got {act!r}")
+    return ACT_IDS[act]
+
+
+def qlinear_gated_forward(desc: QDesc, x, gate, up, act: str = "silu", bias_gate=None,
+                          bias_up=None, h_dtype: Optional[str] = None,
+                          save: bool = False) -> QGated:
+    """h [M, N] = act(x Wg^T + bias_gate) * (x Wu^T + bias_up) for two packed
+    layers of one descriptor; with `save` also the 8-bit checkpoints of both
+    pre-activations for qlinear_gated_backward."""
+    import torch
+    M, K, xd = _rows(x, "x")
+    dev, N = x.device, desc.N
+    px = _arg(x, "x", (M, desc.K), x.dtype, dev)
+    wg, wu = _weights_arg(desc, gate, "gate", dev), _weights_arg(desc, up, "up", dev)
+    pb = [_opt(b, n, (N,), x.dtype, dev) for b, n in ((bias_gate, "bias_gate"), (bias_up, "bias_up"))]
+    hd = h_dtype or xd
+    a = _act_id(act)
+    h = torch.empty((M, N), dtype=_torch_dt(hd), device=dev)
+    ck = [None] * 4
+    if save:
+        ck = [torch.empty((M, N), dtype=torch.int8, device=dev),
+              torch.empty((M, _groups(N)), dtype=torch.float32, device=dev),
+              torch.empty((M, N), dtype=torch.int8, device=dev),
+              torch.empty((M, _groups(N)), dtype=torch.float32, device=dev)]
+    d, size = desc.c(), ctypes.c_size_t(0)
+    _check(lib.qlinear_gated_workspace_bytes(ctypes.byref(d), DTYPE_IDS[xd], M, int(save),
+                                             ctypes.byref(size)))
+    ws = _scratch(size.value, dev) if size.value else None
+    _run(dev, lib.qlinear_gated_forward, ctypes.byref(d), px, DTYPE_IDS[xd], M, ctypes.byref(wg),
+         ctypes.byref(wu), *pb, a, h.data_ptr(), DTYPE_IDS[hd],
+         *[None if t is None else t.data_ptr() for t in (*ck, ws)], size.value)
+    return QGated(h, tuple(ck[:2]) if save else None, tuple(ck[2:]) if save else None)
+
+
+def _backward_workspace(desc, M, gated, device):
+    size = ctypes.c_size_t(0)
+    _check(lib.qlinear_backward_workspace_bytes(ctypes.byref(desc.c()), M, int(gated),
+                                                ctypes.byref(size)))
+    return _scratch(size.value, device), size.value
+
+
+def qlinear_backward(desc: QDesc, dy, w, dx_dtype: Optional[str] = None):
+    """dx [M, K] = dy [M, N] W: the input gradient of qlinear_forward."""
+    import torch
+    M, _, yd = _rows(dy, "dy")
+    dev = dy.device
+    py = _arg(dy, "dy", (M, desc.N), dy.dtype, dev)
+    ww = _weights_arg(desc, w, "w", dev)
+    xd = dx_dtype or yd
+    dx = torch.empty((M, desc.K), dtype=_torch_dt(xd), device=dev)
+    ws, n = _backward_workspace(desc, M, False, dev)
+    _run(dev, lib.qlinear_backward, ctypes.byref(desc.c()), py, DTYPE_IDS[yd], M,
+         ctypes.byref(ww), dx.data_ptr(), DTYPE_IDS[xd], ws.data_ptr(), n)
+    return dx
+
+
+def qlinear_gated_backward(desc: QDesc, dh, gate, up, gate_saved, up_saved, act: str = "silu",
+                           need_dpre: bool = True, dx_dtype: Optional[str] = None) -> QGatedGrads:
+    """Backward of qlinear_gated_forward from its checkpoints: dx, and with
+    `need_dpre` the gradients of both projections' outputs."""
+    import torch
+    M, _, yd = _rows(dh, "dh")
+    dev, N = dh.device, desc.N
+    ph = _arg(dh, "dh", (M, N), dh.dtype, dev)
+    wg, wu = _weights_arg(desc, gate, "gate", dev), _weights_arg(desc, up, "up", dev)
+    pk = []
+    for (codes, scales), n in ((gate_saved, "gate_saved"), (up_saved, "up_saved")):
+        pk += [_arg(codes, n + " codes", (M, N), torch.int8, dev),
+               _arg(scales, n + " scales", (M, _groups(N)), torch.float32, dev)]
+    a = _act_id(act)
+    xd = dx_dtype or yd
+    dx = torch.empty((M, desc.K), dtype=_torch_dt(xd), device=dev)
+    dg, du = (torch.empty_like(dh), torch.empty_like(dh)) if need_dpre else (None, None)
+    ws, n = _backward_workspace(desc, M, True, dev)
+    _run(dev, lib.qlinear_gated_backward, ctypes.byref(desc.c()), ph, DTYPE_IDS[yd], M,
+         ctypes.byref(wg), ctypes.byref(wu), a, *pk,
+         *[None if t is None else t.data_ptr() for t in (dg, du)], dx.data_ptr(), DTYPE_IDS[xd],
+         ws.data_ptr(), n)
+    return QGatedGrads(dx, dg, du)

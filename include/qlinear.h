@@ -359,6 +359,121 @@ qp_status qlinear_forward_a8w4(const qp_desc* d, const void* xq, const float* xs
                                int64_t M, const qp_weights* w, const float* bias,
                                void* y, int32_t y_dtype, void* stream);
 
+/* ---- The MLP block around the packed layers ------------------------------
+ * Entry points below: row-major contiguous device buffers, 16-byte aligned,
+ * caller-owned; x_dtype (and dy_dtype) QP_F16 or QP_BF16 unless said
+ * otherwise; asynchronous on `stream`; nothing is allocated, so every call
+ * can be captured into a graph; results do not depend on timing (no atomics).
+ * Calls that share a workspace must not overlap.  Limits: M <= 2^20 rows,
+ * N <= 2^26, M * N <= 2^36. */
+
+/* Activation of a gated pair. */
+typedef enum {
+  QP_ACT_SILU = 0,       /* g / (1 + e^-g)                                    */
+  QP_ACT_GELU_TANH = 1   /* g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))     */
+} qp_act;
+
+/* Columns per scale of an 8-bit activation checkpoint. */
+#define QP_CHECKPOINT_GROUP 64
+
+/* RMS norm with the residual's addition, row by row of x [M, K]:
+ *   s = x + residual, rounded once to x_dtype (residual NULL: s = x),
+ *   rstd[m] = (sum_k s^2 / K + eps)^(-1/2),   v = s * weight[k] * rstd
+ * (weight NULL: 1; otherwise [K] of x_dtype), and either
+ *   y [M, K] = v in x_dtype, or, for qlinear_forward_a8w4,
+ *   ys[m] = fl32(max_k |v| / 127), yq[m, k] = rint(v / ys[m]) (int8 [M, K],
+ *   fp32 [M]; a row of zeros gives 0 and 0).
+ * The sum and the int8 quotient are held in fp64, so the codes are those of
+ * the exact values.  Pass y, or yq and ys, and NULL for the other.  s (only
+ * with a residual) and rstd (fp32 [M]) may be NULL to skip them.  s may be
+ * x or residual itself (in place); y and yq are buffers of their own.
+ * Any K >= 1 (rows with K % 8 == 0 and K <= 32768 are read once); eps > 0;
+ * M <= 2^21, and M * K <= 2^34 (2^31 where K % 8 != 0). */
+qp_status qnorm_forward(const void* x, const void* residual, int32_t x_dtype, int64_t M, int64_t K,
+                        const void* weight, float eps, void* s, void* y, void* yq, float* ys,
+                        float* rstd, void* stream);
+
+/* Host only.  Workspace bytes of qnorm_backward with a dweight (0 without). */
+qp_status qnorm_backward_workspace_bytes(int64_t M, int64_t K, size_t* bytes);
+
+/* Gradients of qnorm_forward's 16-bit output: with xh = s * rstd,
+ *   c[m] = sum_k dy * weight * xh / K,
+ *   ds [M, K] (x_dtype) = rstd * (dy * weight - xh * c) + ds_in,
+ *   dweight [K] (fp32) = sum_m dy * xh  (fixed order of additions).
+ * s: the forward's s (x where it had no residual), or NULL with s_codes and
+ * s_scales, its 8-bit checkpoint.  rstd: from the forward.  ds_in: the
+ * gradient that reaches s from elsewhere (the residual stream), or NULL.  ds
+ * is the gradient of x and of the residual alike; it may be ds_in or dy
+ * itself.  ds or dweight may be NULL to skip it; dweight needs the
+ * workspace.  Limits as qnorm_forward. */
+qp_status qnorm_backward(const void* dy, const void* s, const void* s_codes, const float* s_scales,
+                         int32_t x_dtype, int64_t M, int64_t K, const void* weight,
+                         const float* rstd, const void* ds_in, void* ds, float* dweight,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* 8-bit activation checkpoint of x [M, K]: per 64 columns of a row (the last
+ * group may be shorter) scales[m, g] = fl32(max |x| / 127) and codes[m, k] =
+ * rint(x / scale) (exact quotient, ties to even; 0 where the scale is 0).
+ * codes: int8 [M, K]; scales: fp32 [M, ceil(K / 64)].  Any K >= 1; M * K
+ * <= 2^34 (2^31 where K % 8 != 0). */
+qp_status qpack_checkpoint(const void* x, int32_t x_dtype, int64_t M, int64_t K, void* codes,
+                           float* scales, void* stream);
+
+/* The values a checkpoint stands for, codes * scale in fp32 rounded once to
+ * x_dtype (QP_F16, QP_BF16 or QP_F32), into x [M, K]. */
+qp_status qpack_checkpoint_restore(const void* codes, const float* scales, int64_t M, int64_t K,
+                                   void* x, int32_t x_dtype, void* stream);
+
+/* Host only.  Workspace bytes qlinear_gated_forward can use (0: none). */
+qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int32_t x_dtype, int64_t M, int32_t save,
+                                        size_t* bytes);
+
+/* Gated pair of projections in one pass over both layers' codes:
+ *   g = x Wg^T (+ bias_gate),  u = x Wu^T (+ bias_up),  h = act(g) * u
+ * for two layers gate and up of the same descriptor d (N outputs, K inputs);
+ * biases [N] of x_dtype or NULL; h [M, N] in h_dtype (QP_F16, QP_BF16 or
+ * QP_F32), rounded once from fp32.  act: qp_act.
+ * gate_codes, gate_scales, up_codes, up_scales: NULL, or 8-bit checkpoints
+ * of g and u (qpack_checkpoint's layout, from the fp32 values) for
+ * qlinear_gated_backward: all four or none.
+ * Up to 16 rows without checkpoints, K % 128 == 0 and buffers below 2 GiB:
+ * exact codes, as QP_KERNEL_GEMV_MFMA.  Otherwise fp16-rounded weights as
+ * QP_KERNEL_GEMM where K % 64 == 0 (h carries their rounding, a relative
+ * L2 error of about 2e-4, at any K); other K run a slow general form in fp32.
+ * h's contents are undefined until the call completes. */
+qp_status qlinear_gated_forward(const qp_desc* d, const void* x, int32_t x_dtype, int64_t M,
+                                const qp_weights* gate, const qp_weights* up, const void* bias_gate,
+                                const void* bias_up, int32_t act, void* h, int32_t h_dtype,
+                                void* gate_codes, float* gate_scales, void* up_codes,
+                                float* up_scales, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Host only.  Workspace bytes that qlinear_backward (gated = 0) and
+ * qlinear_gated_backward (gated = 1) need. */
+qp_status qlinear_backward_workspace_bytes(const qp_desc* d, int64_t M, int32_t gated,
+                                           size_t* bytes);
+
+/* Input gradient of a packed layer: dx [M, K] (dx_dtype: QP_F16, QP_BF16 or
+ * QP_F32) = dy [M, N] (dy_dtype) * W.  Any N; the weights are frozen and
+ * have no gradient; a bias's gradient is the column sum of dy.  The
+ * workspace (qlinear_backward_workspace_bytes, 16-byte aligned) is required
+ * and busy until the call's kernels finish. */
+qp_status qlinear_backward(const qp_desc* d, const void* dy, int32_t dy_dtype, int64_t M,
+                           const qp_weights* w, void* dx, int32_t dx_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Backward of qlinear_gated_forward from the checkpoints of g and u:
+ *   dg = dh * u * act'(g),  du = dh * act(g),  dx = dg Wg + du Wu.
+ * dh [M, N] of dh_dtype; dgate and dup: [M, N] of dh_dtype (the gradients of
+ * the projections' outputs, for adapters and biases), or NULL; dx [M, K] of
+ * dx_dtype, from the unrounded dg and du.  Workspace as qlinear_backward. */
+qp_status qlinear_gated_backward(const qp_desc* d, const void* dh, int32_t dh_dtype, int64_t M,
+                                 const qp_weights* gate, const qp_weights* up, int32_t act,
+                                 const void* gate_codes, const float* gate_scales,
+                                 const void* up_codes, const float* up_scales, void* dgate,
+                                 void* dup, void* dx, int32_t dx_dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
