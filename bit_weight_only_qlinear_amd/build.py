@@ -34,6 +34,7 @@ SOURCES = {
     "noalloc.hip": [],
     "norm.hip": [],
     "gated.hip": [],
+    "backward.hip": [],
 }
 
 

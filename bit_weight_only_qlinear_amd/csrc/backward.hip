@@ -1,0 +1,730 @@
+// Input gradients through packed weights on fp16 MFMA:
+//   dx[m, k] = sum_n D[m, n] w[n, k],  D = dy, or for the gated pair
+//   D = [dg | du] over the stacked weights [Wg; Wu].
+//
+// The contraction runs over the weight rows n, while codes are packed along
+// k, so a weight tile has to be transposed on its way to the matrix cores.
+//  * Each lane loads 32 columns of one weight row (16 bytes of 4-bit codes);
+//    the four 16-lane groups of a wave hold four consecutive rows of the same
+//    column chunks.  Four v_permlane swaps turn that 4 x 4 (row x word)
+//    arrangement around, so that a lane then has 8 columns of four rows: for
+//    each column the pairs (n, n+1), (n+2, n+3), cut out of two words at once
+//    (v_perm puts the same byte of two rows under the 1024 of an fp16 pair),
+//    one packed subtract and one packed fma, and one 8-byte LDS write of four
+//    consecutive n.  The scales travel the same way: one (S, T) fp16 pair per
+//    lane and step, turned by the same swaps.
+//  * Weights in fp16, each rounded about once.  AFFINE: w = fma(q, scale,
+//    bias), both exact in fp16 (as the qGEMM takes them).  Q6K, SYM4: with v =
+//    u - 32 or u - 8 exact and the scale split into S + s (two fp16 numbers),
+//    w = fma(v, S, v s).  Q4K, scale and offset split: w = fma(q, S, T) +
+//    fma(q, s, t).  Rounding the Q4K scale and offset to one fp16 each left
+//    weight errors of 2e-4 of the largest weight, past the layer's element
+//    bound; a conversion through fp32 would take 2.5 times the instructions.
+//  * The LDS tile holds 256 columns of 64 n (128 bytes): column c's 16-byte
+//    chunk j at line L = c / 2 (256 bytes, all 64 banks), slot
+//    (8 (c & 1) + j) ^ (((L & 7) ^ ((L >> 4) & 7)) + 8 ((L >> 2) & 1)): the 32
+//    lanes of an 8-byte write phase (16 columns, both halves of a chunk) and
+//    the 16 lanes of a 16-byte read phase (16 neighbouring columns) each touch
+//    all 16 slots once.
+//  * D is staged once per call: fp16, each row scaled by a power of two so
+//    that its peak is inside [2^14, 2^15) at most (gradients are small: bf16's
+//    range does not fit fp16), in the B-fragment order of
+//    v_mfma_f32_32x32x16_f16.  For the gated pair both staging passes (row
+//    maxima, then the fragments) compute dg and du from the 8-bit checkpoints;
+//    the second also writes them out in the activation type.  (A bound on the
+//    maxima from dh and the scales alone would spare a read, but rows whose
+//    gates are all far negative would lose their bits to it.)
+//  * Block tile 256 (k) x 256 or 128 (m) x 64 (n), 8 waves as 2 (k) x 4 (m),
+//    fragments of D loaded from L2 straight into registers a step ahead.
+//  * The output is small and the contraction long, so the steps are split
+//    over several blocks where the tiles alone do not fill the 256 CUs; fp32
+//    partial sums meet in a fixed order in a second kernel.
+#include "gemm_kernels.hpp"
+#include "mlp_common.hpp"
+
+namespace qp {
+namespace {
+
+constexpr int kDK = 256, kDN = 64;   // tile columns, contraction rows per step
+constexpr uint32_t kDTile = kDK * kDN * 2u;
+constexpr uint32_t kOff = 0x80000000u;   // past every resource: reads 0
+
+struct DxK {
+  Bufs w[2];
+  int parts;               // 1, or 2 (gated)
+  int64_t N, K, M;
+  int gs;
+  const unsigned char* xf; // staged D: [step][4][MB][64] 16-byte chunks
+  const int* xe;           // row exponents
+  float* part;             // [split, M, K] partial sums, or null
+  void* dx;
+  int dxdt;
+  int T1, T;               // steps per part, in all
+  int MB;                  // 32-row blocks of D
+  int tilesK, tilesM, split;
+};
+
+// One step of one lane: 32 columns of weight row 8 wave + 4 ((lane >> 3) & 1)
+// + (lane >> 4) of the step.
+template <int KIND>
+struct DStage {
+  uint32_t w[KIND == G_AFF2 ? 2 : KIND == G_AFF8 ? 8 : 4];
+  uint32_t h[KIND == G_Q6K ? 2 : 1];
+  uint32_t s0, s1, s2;
+};
+
+// Per-lane offsets inside a step's 64 rows (kOff for columns past K).
+struct DOff {
+  uint32_t w, h, s, z, p;
+};
+
+template <int KIND>
+__device__ __forceinline__ constexpr int64_t row_bytes(int64_t K) {
+  return KIND == G_AFF2 ? K / 4 : KIND == G_AFF8 ? K : K / 2;
+}
+
+template <int KIND>
+__device__ __forceinline__ void dload(const DxK& a, const DOff& o, int t, DStage<KIND>& st) {
+  // uniform: part and rows of the step; steps past the end get empty resources
+  const int second = t >= a.T1 ? 1 : 0;
+  const int64_t n0 = (int64_t)(t - (second ? a.T1 : 0)) * kDN;
+  const int64_t left = t < a.T ? a.N - n0 : 0;
+  const uint32_t rows = (uint32_t)(left < 0 ? 0 : left < kDN ? left : kDN);
+  const Bufs& b = a.w[second];
+  auto res = [&](const void* p, int64_t row) {
+    return rsrc(static_cast<const unsigned char*>(p) + (rows ? n0 * row : 0), rows * (uint32_t)row);
+  };
+  const int64_t K = a.K;
+  const __amdgpu_buffer_rsrc_t rw = res(b.qweight, row_bytes<KIND>(K));
+  if constexpr (KIND == G_AFF2) {
+    const uint2 v = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rw, o.w, 0, 0));
+    st.w[0] = v.x; st.w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < (KIND == G_AFF8 ? 2 : 1); ++i) {
+      const uint4 v = __builtin_bit_cast(
+          uint4, __builtin_amdgcn_raw_buffer_load_b128(rw, o.w + 16u * i, 0, 0));
+      st.w[4 * i] = v.x; st.w[4 * i + 1] = v.y; st.w[4 * i + 2] = v.z; st.w[4 * i + 3] = v.w;
+    }
+  }
+  if constexpr (KIND == G_AFF2 || KIND == G_AFF4 || KIND == G_AFF8) {
+    const int64_t sr = (K / a.gs) * 2;
+    st.s0 = __builtin_amdgcn_raw_buffer_load_b16(res(b.scales, sr), o.s, 0, 0);
+    st.s1 = __builtin_amdgcn_raw_buffer_load_b16(res(b.zeros, sr), o.s, 0, 0);
+  } else if constexpr (KIND == G_Q4K) {
+    st.s0 = __builtin_amdgcn_raw_buffer_load_b8(res(b.scales, K / 32), o.s, 0, 0);
+    st.s1 = __builtin_amdgcn_raw_buffer_load_b8(res(b.zeros, K / 32), o.s, 0, 0);
+    st.s2 = __builtin_amdgcn_raw_buffer_load_b32(res(b.steps, (K / 256) * 4), o.p, 0, 0);
+  } else if constexpr (KIND == G_Q6K) {
+    const uint2 v = __builtin_bit_cast(
+        uint2, __builtin_amdgcn_raw_buffer_load_b64(res(b.qweight_hi, K / 4), o.h, 0, 0));
+    st.h[0] = v.x; st.h[1] = v.y;
+    st.s0 = __builtin_amdgcn_raw_buffer_load_b16(res(b.scales, K / 16), o.s, 0, 0);
+    st.s2 = __builtin_amdgcn_raw_buffer_load_b16(res(b.steps, (K / 256) * 2), o.p, 0, 0);
+  } else {
+    st.s0 = __builtin_amdgcn_raw_buffer_load_b32(res(b.scales, (K / a.gs) * 4), o.s, 0, 0);
+  }
+}
+
+// v_permlane swaps: register t of lane group g <-> register g of lane group t.
+__device__ __forceinline__ void turn4(uint32_t (&w)[4]) {
+  auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+  auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+  auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  w[0] = c[0]; w[1] = c[1]; w[2] = d[0]; w[3] = d[1];
+}
+
+// A stage after the turn: 8 columns of four rows, and the rows' scales and
+// offsets as fp16 pairs (S01, S23, T01, T23).
+template <int KIND>
+struct DTurned {
+  uint32_t w[KIND == G_AFF8 ? 8 : 4];   // rows 0..3 (AFF8: columns 0-3, then 4-7)
+  uint32_t h[KIND == G_Q6K ? 2 : 1];    // high bits of row pairs
+  half2_t S[2], T[2];                   // hi parts (Q6K, SYM4: T is the lo part of S)
+  half2_t s[KIND == G_Q4K ? 2 : 1], t[KIND == G_Q4K ? 2 : 1];   // Q4K: lo parts
+};
+
+// (hi, lo) fp16 parts of a fp32 number, as the halves of a pair.
+__device__ __forceinline__ half2_t split_f16(float v) {
+  half2_t r;
+  r.x = (_Float16)v;
+  r.y = (_Float16)(v - (float)r.x);
+  return r;
+}
+
+template <int KIND, bool MBF16>
+__device__ __forceinline__ void dturn(const DStage<KIND>& st, DTurned<KIND>& d) {
+  if constexpr (KIND == G_AFF8) {
+    uint32_t p[4] = {st.w[0], st.w[2], st.w[4], st.w[6]}, q[4] = {st.w[1], st.w[3], st.w[5], st.w[7]};
+    turn4(p);
+    turn4(q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { d.w[i] = p[i]; d.w[4 + i] = q[i]; }
+  } else if constexpr (KIND == G_AFF2) {
+    uint32_t p[4] = {st.w[0], st.w[0] >> 16, st.w[1], st.w[1] >> 16};
+    turn4(p);   // 16-bit pieces: 8 codes in the low half; join the row pairs
+    d.w[0] = __builtin_amdgcn_perm(p[1], p[0], 0x05040100u);
+    d.w[1] = __builtin_amdgcn_perm(p[3], p[2], 0x05040100u);
+  } else {
+    uint32_t p[4] = {st.w[0], st.w[1], st.w[2], st.w[3]};
+    turn4(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d.w[i] = p[i];
+  }
+  if constexpr (KIND == G_Q6K) {
+    uint32_t p[4] = {st.h[0], st.h[0] >> 16, st.h[1], st.h[1] >> 16};
+    turn4(p);
+    d.h[0] = __builtin_amdgcn_perm(p[1], p[0], 0x05040100u);
+    d.h[1] = __builtin_amdgcn_perm(p[3], p[2], 0x05040100u);
+  }
+  uint32_t m[4];
+  if constexpr (KIND == G_Q6K) {   // two groups of 16 in the chunk's 32 columns
+    const float step = f16_to_f32(st.s2 & 0xFFFFu);
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+      m[2 * g] = m[2 * g + 1] = __builtin_bit_cast(
+          uint32_t, split_f16((float)(int8_t)((st.s0 >> (8 * g)) & 0xFFu) * step));
+  } else if constexpr (KIND == G_SYM4) {
+    m[0] = m[1] = m[2] = m[3] = __builtin_bit_cast(uint32_t, split_f16(__uint_as_float(st.s0)));
+  } else if constexpr (KIND == G_Q4K) {
+    const float S = (float)(st.s0 & 0xFFu) * f16_to_f32(st.s2 & 0xFFFFu);
+    const float T = -S * ((float)(st.s1 & 0xFFu) * f16_to_f32(st.s2 >> 16));
+    const uint32_t hs = __builtin_bit_cast(uint32_t, split_f16(S));
+    const uint32_t ht = __builtin_bit_cast(uint32_t, split_f16(T));
+    m[0] = m[1] = m[2] = m[3] = __builtin_amdgcn_perm(ht, hs, 0x07060302u);   // lo parts
+    turn4(m);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      d.s[i] = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m[2 * i + 1], m[2 * i], 0x05040100u));
+      d.t[i] = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m[2 * i + 1], m[2 * i], 0x07060302u));
+    }
+    m[0] = m[1] = m[2] = m[3] = __builtin_amdgcn_perm(ht, hs, 0x05040100u);   // hi parts
+  } else {
+    half2_t v;
+    v.x = (_Float16)(MBF16 ? bf16_to_f32(st.s0 & 0xFFFFu) : f16_to_f32(st.s0 & 0xFFFFu));
+    v.y = (_Float16)(MBF16 ? bf16_to_f32(st.s1 & 0xFFFFu) : f16_to_f32(st.s1 & 0xFFFFu));
+    m[0] = m[1] = m[2] = m[3] = __builtin_bit_cast(uint32_t, v);
+  }
+  turn4(m);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    d.S[i] = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m[2 * i + 1], m[2 * i], 0x05040100u));
+    d.T[i] = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m[2 * i + 1], m[2 * i], 0x07060302u));
+  }
+}
+
+// Columns 2 b and 2 b + 1 of the lane's 8: four consecutive n each.
+template <int KIND, int b>
+__device__ __forceinline__ void dcols(const DTurned<KIND>& d, uint32_t magic, uint2 (&out)[2]) {
+  constexpr float MG = KIND == G_Q6K ? 1056.f : KIND == G_SYM4 ? 1032.f : 1024.f;
+  const half2_t mag = {(_Float16)MG, (_Float16)MG};
+  uint32_t r[2][2];   // [column][row pair]
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t q[2];
+    if constexpr (KIND == G_AFF2) {
+      q[0] = and_or(d.w[i] >> (4 * b), 0x00030003u, magic);
+      q[1] = and_or(d.w[i] >> (4 * b + 2), 0x00030003u, magic);
+    } else if constexpr (KIND == G_AFF8) {
+      constexpr int o = b < 2 ? 0 : 4, c = (2 * b) & 3;
+      constexpr uint32_t s0 = 0x0C000C00u | ((4u + c) << 16) | c, s1 = s0 + 0x00010001u;
+      q[0] = __builtin_amdgcn_perm(d.w[o + 2 * i + 1], d.w[o + 2 * i], s0) | magic;
+      q[1] = __builtin_amdgcn_perm(d.w[o + 2 * i + 1], d.w[o + 2 * i], s1) | magic;
+    } else {
+      constexpr uint32_t sel = 0x0C000C00u | ((4u + b) << 16) | b;
+      const uint32_t p = __builtin_amdgcn_perm(d.w[2 * i + 1], d.w[2 * i], sel);
+      uint32_t m0 = magic, m1 = magic;
+      if constexpr (KIND == G_Q6K) {   // bits 4 b .. 4 b + 3 of each half: to bits 4, 5
+        constexpr int e0 = 4 * b - 4, e1 = 4 * b - 2;
+        m0 = and_or(e0 < 0 ? d.h[i] << 4 : d.h[i] >> (e0 < 0 ? 0 : e0), 0x00300030u, magic);
+        m1 = and_or(e1 < 0 ? d.h[i] << 2 : d.h[i] >> (e1 < 0 ? 0 : e1), 0x00300030u, magic);
+      }
+      q[0] = and_or(p, 0x000F000Fu, m0);
+      q[1] = and_or(p >> 4, 0x000F000Fu, m1);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const half2_t v = __builtin_bit_cast(half2_t, q[c]) - mag;   // exact
+      half2_t w;
+      if constexpr (KIND == G_Q6K || KIND == G_SYM4)
+        w = __builtin_elementwise_fma(v, d.S[i], v * d.T[i]);
+      else if constexpr (KIND == G_Q4K)
+        w = __builtin_elementwise_fma(v, d.S[i], d.T[i]) + __builtin_elementwise_fma(v, d.s[i], d.t[i]);
+      else
+        w = __builtin_elementwise_fma(v, d.S[i], d.T[i]);
+      r[c][i] = __builtin_bit_cast(uint32_t, w);
+    }
+  }
+  out[0] = make_uint2(r[0][0], r[0][1]);
+  out[1] = make_uint2(r[1][0], r[1][1]);
+}
+
+// J: 32-row blocks of D per wave (tile rows 128 J).
+template <int KIND, bool MBF16, int J>
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
+k_dx(DxK a) {
+  __shared__ __attribute__((aligned(16))) unsigned char smem[2 * kDTile];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wi = wave >> 2, wj = wave & 3;
+
+  // contiguous runs of (split, m, k) tiles per XCD, k fastest: the blocks of
+  // a run read the same rows of D at the same time
+  const int nt = a.tilesK * a.tilesM * a.split, bid = blockIdx.x;
+  const int tile = (nt % 8 == 0) ? (bid % 8) * (nt / 8) + bid / 8 : bid;
+  const int tk = tile % a.tilesK, tms = tile / a.tilesK;
+  const int tm = tms % a.tilesM, sp = tms / a.tilesM;
+  const int t0 = (int)((int64_t)a.T * sp / a.split), t1 = (int)((int64_t)a.T * (sp + 1) / a.split);
+  const int64_t k0 = (int64_t)tk * kDK, K = a.K;
+  const int mb0 = tm * 4 * J + wj * J;   // this wave's first row block
+
+  const int g = lane >> 4, chunk = lane & 7, rsub = (lane >> 3) & 1;
+  DOff o;
+  {
+    const uint32_t row = 8u * wave + 4u * rsub + g;
+    const int64_t kc = k0 + 32 * chunk;
+    const bool ok = kc < K;
+    const uint32_t R = (uint32_t)row_bytes<KIND>(K), kcu = (uint32_t)kc;
+    constexpr uint32_t cb = KIND == G_AFF2 ? 4 : KIND == G_AFF8 ? 1 : 2;   // columns per byte
+    const uint32_t Ku = (uint32_t)K, gs = (uint32_t)a.gs;
+    o.w = ok ? row * R + kcu / cb : kOff;
+    o.h = ok ? row * (Ku / 4u) + kcu / 4u : kOff;
+    o.p = o.z = 0;
+    if constexpr (KIND == G_Q4K) {
+      o.s = row * (Ku / 32u) + kcu / 32u;
+      o.p = ok ? row * (Ku / 256u) * 4u + (kcu / 256u) * 4u : kOff;
+    } else if constexpr (KIND == G_Q6K) {
+      o.s = row * (Ku / 16u) + kcu / 16u;
+      o.p = ok ? row * (Ku / 256u) * 2u + (kcu / 256u) * 2u : kOff;
+    } else if constexpr (KIND == G_SYM4) {
+      o.s = row * (Ku / gs) * 4u + (kcu / gs) * 4u;
+    } else {
+      o.s = row * (Ku / gs) * 2u + (kcu / gs) * 2u;
+    }
+    if (!ok) o.s = kOff;
+  }
+  // LDS byte of column e = 0 (e adds 256 (e >> 1) and turns slot bits)
+  const uint32_t wl = 16u * chunk + 4u * g;
+  // fragment base: slot bits of k-slice 0, subtile 0; entry x is slot ^ x
+  uint32_t fa[8];
+  {
+    const uint32_t L = 64u * wi + ((lane & 31) >> 1);
+    const uint32_t slot = (((lane & 1u) << 3) | (uint32_t)(lane >> 5)) ^
+                          ((((uint32_t)lane >> 1) & 7u) ^ (4u * wi)) ^ ((((uint32_t)lane >> 3) & 1u) << 3);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) fa[x] = L * 256u + (slot ^ (uint32_t)x) * 16u;
+  }
+  auto rd_a = [&](uint32_t buf, int s, int i) {
+    return *reinterpret_cast<const half8_t*>(smem + fa[(2 * s) ^ i] + (buf * kDTile + 4096u * i));
+  };
+  uint32_t xo[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+    xo[j] = mb0 + j < a.MB ? (uint32_t)(mb0 + j) * 1024u + 16u * lane : kOff;
+  const uint32_t xs = (uint32_t)a.MB * 1024u;   // one k-slice of 16
+  auto ld_b = [&](int t, int s, int j) {
+    const __amdgpu_buffer_rsrc_t r = rsrc(a.xf + (int64_t)(t < t1 ? t : t0) * 4 * xs, 4u * xs);
+    return __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                           r, xo[j] == kOff ? kOff : xo[j] + (uint32_t)s * xs, 0, 0));
+  };
+  const uint32_t magic = 0x64006400u;
+  // part b of a step's conversion: columns 2 b, 2 b + 1 of the lane's 8
+  auto put = [&](auto B, uint32_t buf, const DTurned<KIND>& d) {
+    constexpr int b = decltype(B)::value;
+    uint2 v[2];
+    dcols<KIND, b>(d, magic, v);
+    const uint32_t L = wl + b;
+    const uint32_t hs = ((L & 7u) ^ ((L >> 4) & 7u)) | (((L >> 2) & 1u) << 3);
+    const uint32_t at = L * 256u + buf * kDTile + 8u * rsub;
+    *reinterpret_cast<uint2*>(smem + at + (((uint32_t)wave) ^ hs) * 16u) = v[0];
+    *reinterpret_cast<uint2*>(smem + at + ((8u | (uint32_t)wave) ^ hs) * 16u) = v[1];
+  };
+
+  float16_t acc[4][J];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  half8_t Bf[4][J];
+
+  // One step: MFMAs on LDS buffer (t - t0) & 1 and the D fragments in Bf
+  // (reloaded slice by slice for step t + 1); conversion of step t + 1 into
+  // the other buffer; weight loads of step t + 2.  Steps past the end load
+  // nothing that is used (empty resources).
+  auto kstep = [&](int t, DStage<KIND>& fre, DStage<KIND>& nxt) {
+    const uint32_t cur = (uint32_t)((t - t0) & 1);
+    dload<KIND>(a, o, t + 2, fre);
+    DTurned<KIND> d;
+    dturn<KIND, MBF16>(nxt, d);
+    half8_t A[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) A[i] = rd_a(cur, 0, i);
+    static_for<4>([&](auto S) {
+      constexpr int s = decltype(S)::value;
+      static_for<4>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A[i], Bf[s][j], acc[i][j], 0, 0, 0);
+        if constexpr (s < 3) A[i] = rd_a(cur, s + 1, i);
+      });
+#pragma unroll
+      for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t + 1, s, j);
+      put(S, cur ^ 1u, d);
+    });
+    __syncthreads();
+  };
+
+  DStage<KIND> st0, st1;
+  dload<KIND>(a, o, t0, st0);
+  dload<KIND>(a, o, t0 + 1, st1);
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t0, s, j);
+  {
+    DTurned<KIND> d;
+    dturn<KIND, MBF16>(st0, d);
+    static_for<4>([&](auto B) { put(B, 0u, d); });
+  }
+  __syncthreads();
+  for (int t = t0; t < t1; t += 2) {
+    kstep(t, st0, st1);
+    if (t + 1 < t1) kstep(t + 1, st1, st0);
+  }
+
+  // ---- lane: rows k = 8 g + 4 (lane >> 5) + q of column m = lane & 31
+  int el = lane;
+  asm volatile("" : "+v"(el));   // keeps the epilogue's addresses after the loop
+  static_for<J>([&](auto JJ) {
+    constexpr int j = decltype(JJ)::value;
+    const int64_t m = (int64_t)(mb0 + j) * 32 + (el & 31);
+    if (m < a.M) {
+      const int xe = a.xe[m];
+      static_for<4>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        static_for<4>([&](auto G) {
+          constexpr int gg = decltype(G)::value;
+          const int64_t k = k0 + wi * 128 + i * 32 + 8 * gg + 4 * (el >> 5);
+          if (k < K) {   // K is a multiple of 32
+            float v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = acc[i][j][4 * gg + q];
+            const int64_t at = m * K + k;
+            if (a.part) {
+              *reinterpret_cast<float4*>(a.part + (int64_t)sp * a.M * K + at) =
+                  make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) v[q] = ldexpf(v[q], -xe);
+              if (a.dxdt == F32) {
+                *reinterpret_cast<float4*>(static_cast<float*>(a.dx) + at) =
+                    make_float4(v[0], v[1], v[2], v[3]);
+              } else {
+                uint32_t h[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  h[q] = a.dxdt == BF16 ? f32_to_bf16_rne(v[q]) : f32_to_f16_rne(v[q]);
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dx) + at) =
+                    make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+              }
+            }
+          }
+        });
+      });
+    }
+  });
+}
+
+// dx = 2^-e sum of the partial products, in order; 4 columns per thread.
+__global__ void __launch_bounds__(256) k_dx_sum(const float4* __restrict__ part, int split,
+                                                int64_t n4, uint32_t k4, const int* __restrict__ xe,
+                                                void* __restrict__ dx, int dxdt) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  float4 v = part[i];
+  for (int s = 1; s < split; ++s) {
+    const float4 p = part[(int64_t)s * n4 + i];
+    v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+  }
+  const int e = -xe[i / k4];
+  v = make_float4(ldexpf(v.x, e), ldexpf(v.y, e), ldexpf(v.z, e), ldexpf(v.w, e));
+  if (dxdt == F32) {
+    static_cast<float4*>(dx)[i] = v;
+  } else {
+    auto r = [dxdt](float f) { return dxdt == BF16 ? f32_to_bf16_rne(f) : f32_to_f16_rne(f); };
+    static_cast<uint2*>(dx)[i] = make_uint2(r(v.x) | (r(v.y) << 16), r(v.z) | (r(v.w) << 16));
+  }
+}
+
+struct DStageArgs {
+  const uint16_t* dy;
+  const int8_t* gq;
+  const float* gs;
+  const int8_t* uq;
+  const float* us;
+  uint16_t* dg;
+  uint16_t* du;
+  uint4* xf;
+  int* xe;
+  int64_t M, N;
+  int MB, T1;
+};
+
+template <bool BF>
+__device__ __forceinline__ float dval(uint32_t b) {
+  return BF ? bf16_to_f32(b) : f16_to_f32(b);
+}
+
+// dg and du of one value.
+template <int ACT>
+__device__ __forceinline__ void pre_grads(float dh, float g, float u, float& dg, float& du) {
+  float f, d;
+  act_fd<ACT>(g, f, d);
+  dg = dh * u * d;
+  du = dh * f;
+}
+
+// The 8 values n .. n + 7 of a row of dy (and of dg and du where GATED, into
+// x and y); 0 past N and where !rok.  sg, su: the group's scales.
+template <bool BF, bool GATED, bool V8, int ACT>
+__device__ __forceinline__ void load8(const DStageArgs& a, int64_t at, int64_t n, bool rok, float sg,
+                                      float su, float (&x)[8], float (&y)[8]) {
+  float v[8], gv[8], uv[8];
+  if constexpr (V8) {
+    const bool ok = rok && n < a.N;
+    const uint4 u = ok ? *reinterpret_cast<const uint4*>(a.dy + at) : make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = dval<BF>((w[i / 2] >> (16 * (i & 1))) & 0xFFFFu);
+    if constexpr (GATED) {
+      const uint2 q = ok ? *reinterpret_cast<const uint2*>(a.gq + at) : make_uint2(0, 0);
+      const uint2 p = ok ? *reinterpret_cast<const uint2*>(a.uq + at) : make_uint2(0, 0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        gv[i] = (float)(int8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3))) * sg;
+        uv[i] = (float)(int8_t)((i < 4 ? p.x : p.y) >> (8 * (i & 3))) * su;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool ok = rok && n + i < a.N;
+      v[i] = ok ? dval<BF>(a.dy[at + i]) : 0.f;
+      if constexpr (GATED) {
+        gv[i] = ok ? (float)a.gq[at + i] * sg : 0.f;
+        uv[i] = ok ? (float)a.uq[at + i] * su : 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (GATED) pre_grads<ACT>(v[i], gv[i], uv[i], x[i], y[i]);
+    else x[i] = v[i];
+  }
+}
+
+// Exponent of each row of D (rows up to MB * 32; 0 past M): e = 14 -
+// floor(log2 b) with b the row's largest magnitude in D.
+template <bool BF, bool GATED, bool V8, int ACT>
+__global__ void __launch_bounds__(256) k_dx_exp(DStageArgs a) {
+  __shared__ float red[4];
+  const int64_t row = blockIdx.x;
+  float b = 0.f;
+  if (row < a.M) {
+    const int64_t ng = (a.N + kCkptGroup - 1) / kCkptGroup;
+    for (int64_t n = 8 * threadIdx.x; n < a.N; n += 8 * 256) {
+      const int64_t g = row * ng + n / kCkptGroup;
+      float x[8], y[8];
+      load8<BF, GATED, V8, ACT>(a, row * a.N + n, n, true, GATED ? a.gs[g] : 0.f,
+                                GATED ? a.us[g] : 0.f, x, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        b = fmaxf(b, fabsf(x[i]));
+        if constexpr (GATED) b = fmaxf(b, fabsf(y[i]));
+      }
+    }
+  }
+  b = wave_max_all(b);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = b;
+  __syncthreads();
+  b = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  if (threadIdx.x == 0) a.xe[row] = b == 0.f ? 0 : 14 - ilogbf(fminf(b, 3.4e38f));
+}
+
+// One wave per 32 rows x 64 columns (one step): D as fp16 B fragments.
+template <bool BF, bool GATED, bool V8, int ACT>
+__global__ void __launch_bounds__(256) k_dx_stage(DStageArgs a) {
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (id >= (int64_t)a.MB * a.T1) return;   // whole waves
+  const int lane = threadIdx.x & 63;
+  const int t = (int)(id / a.MB), mb = (int)(id - (int64_t)t * a.MB);
+  const int64_t row = (int64_t)mb * 32 + (lane & 31);
+  const bool rok = row < a.M;
+  const int64_t ng = (a.N + kCkptGroup - 1) / kCkptGroup;
+  const int e = a.xe[row];
+  float sg = 0.f, su = 0.f;
+  if (GATED && rok) {
+    sg = a.gs[row * ng + t];
+    su = a.us[row * ng + t];
+  }
+  auto rnd = [](float f) { return BF ? f32_to_bf16_rne(f) : f32_to_f16_rne(f); };
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int64_t n = (int64_t)t * 64 + 16 * s + 8 * (lane >> 5);
+    const int64_t at = row * a.N + n;
+    float dg[8], du[8];
+    load8<BF, GATED, V8, ACT>(a, at, n, rok, sg, su, dg, du);
+    auto frag = [&](const float (&x)[8], int step) {
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = pack_f16(ldexpf(x[2 * i], e), ldexpf(x[2 * i + 1], e));
+      a.xf[(((int64_t)step * 4 + s) * a.MB + mb) * 64 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
+    };
+    frag(dg, t);
+    if constexpr (GATED) {
+      frag(du, t + a.T1);
+      auto out = [&](uint16_t* p, const float (&x)[8]) {
+        if (!p || !rok) return;
+        if constexpr (V8) {
+          if (n < a.N)
+            *reinterpret_cast<uint4*>(p + at) =
+                make_uint4(rnd(x[0]) | (rnd(x[1]) << 16), rnd(x[2]) | (rnd(x[3]) << 16),
+                           rnd(x[4]) | (rnd(x[5]) << 16), rnd(x[6]) | (rnd(x[7]) << 16));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n + i < a.N) p[at + i] = (uint16_t)rnd(x[i]);
+        }
+      };
+      out(a.dg, dg);
+      out(a.du, du);
+    }
+  }
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct DxPlan {
+  int J, split, tilesK, tilesM, MB, T1, T;
+  size_t xf, xe, part;   // workspace bytes of each region (16-byte multiples)
+};
+
+DxPlan dx_plan(const Desc& d, int64_t M, bool gated) {
+  DxPlan p;
+  p.MB = (int)cdiv(M, 32);
+  p.T1 = (int)cdiv(d.N, kDN);
+  p.T = p.T1 * (gated ? 2 : 1);
+  p.tilesK = (int)cdiv(d.K, kDK);
+  p.J = M > 128 ? 2 : 1;
+  p.tilesM = (int)cdiv(M, 128 * p.J);
+  // Waves of blocks over 256 CUs, each block its share of the steps and a
+  // few steps' worth of start and end; more than one split adds the partial
+  // sums' traffic.
+  const double step = p.J == 2 ? 1.4e-6 : 1.0e-6;
+  double best = 0.;
+  p.split = 1;
+  const int64_t tiles = (int64_t)p.tilesK * p.tilesM;
+  for (int s = 1; s <= 32 && s <= p.T; ++s) {
+    if (s > 1 && tiles * s > 1024) break;
+    double t = (double)cdiv(tiles * s, 256) * (double)(cdiv(p.T, s) + 4) * step;
+    if (s > 1) t += 3e-6 + (double)s * (double)M * (double)d.K * 8. / 4e12;
+    if (s == 1 || t < best) {
+      best = t;
+      p.split = s;
+    }
+  }
+  p.xf = (size_t)p.T * 4u * (size_t)p.MB * 1024u;
+  p.xe = (size_t)p.MB * 128u;
+  p.part = p.split > 1 ? (size_t)p.split * (size_t)M * (size_t)d.K * 4u : 0;
+  return p;
+}
+
+typedef void (*DxFn)(DxK);
+template <int KIND, bool MB>
+DxFn dx_pick(int J) {
+  return J == 2 ? k_dx<KIND, MB, 2> : k_dx<KIND, MB, 1>;
+}
+
+typedef void (*DStageFn)(DStageArgs);
+template <bool BF, bool V8>
+void stage_pick(bool gated, int act, DStageFn* ex, DStageFn* st) {
+  if (!gated) {
+    *ex = k_dx_exp<BF, false, V8, 0>;
+    *st = k_dx_stage<BF, false, V8, 0>;
+  } else if (act == ACT_SILU) {
+    *ex = k_dx_exp<BF, true, V8, ACT_SILU>;
+    *st = k_dx_stage<BF, true, V8, ACT_SILU>;
+  } else {
+    *ex = k_dx_exp<BF, true, V8, ACT_GELU_TANH>;
+    *st = k_dx_stage<BF, true, V8, ACT_GELU_TANH>;
+  }
+}
+
+}  // namespace
+
+size_t dx_workspace_bytes(const Desc& d, int64_t M, bool gated) {
+  const DxPlan p = dx_plan(d, M, gated);
+  return p.xf + p.xe + p.part;
+}
+
+hipError_t launch_dx(const Desc& d, const DxArgs& a, hipStream_t s) {
+  const DxPlan p = dx_plan(d, a.M, a.gated);
+  unsigned char* ws = static_cast<unsigned char*>(a.ws);
+  int* xe = reinterpret_cast<int*>(ws + p.xf);
+  DStageArgs sa{static_cast<const uint16_t*>(a.dy), a.gq, a.gs, a.uq, a.us,
+                static_cast<uint16_t*>(a.dg), static_cast<uint16_t*>(a.du),
+                reinterpret_cast<uint4*>(ws), xe, a.M, d.N, p.MB, p.T1};
+  const bool bf = a.dydt == BF16;
+  DStageFn ex, sf;
+  if (d.N % 8 == 0) bf ? stage_pick<true, true>(a.gated, a.act, &ex, &sf)
+                       : stage_pick<false, true>(a.gated, a.act, &ex, &sf);
+  else bf ? stage_pick<true, false>(a.gated, a.act, &ex, &sf)
+          : stage_pick<false, false>(a.gated, a.act, &ex, &sf);
+  hipLaunchKernelGGL(ex, dim3((unsigned)p.MB * 32u), dim3(256), 0, s, sa);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(sf, dim3((unsigned)cdiv((int64_t)p.MB * p.T1, 4)), dim3(256), 0, s, sa);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  DxK k{};
+  k.w[0] = a.w;
+  k.w[1] = a.w2;
+  k.parts = a.gated ? 2 : 1;
+  k.N = d.N;
+  k.K = d.K;
+  k.M = a.M;
+  k.gs = d.gs;
+  k.xf = ws;
+  k.xe = xe;
+  k.part = p.split > 1 ? reinterpret_cast<float*>(ws + p.xf + p.xe) : nullptr;
+  k.dx = a.dx;
+  k.dxdt = a.dxdt;
+  k.T1 = p.T1;
+  k.T = p.T;
+  k.MB = p.MB;
+  k.tilesK = p.tilesK;
+  k.tilesM = p.tilesM;
+  k.split = p.split;
+  const bool mb = d.meta == BF16;
+  DxFn fn = d.fmt == Q4K ? dx_pick<G_Q4K, false>(p.J)
+          : d.fmt == Q6K ? dx_pick<G_Q6K, false>(p.J)
+          : d.fmt == SYM4 ? dx_pick<G_SYM4, false>(p.J)
+          : d.bits == 2 ? (mb ? dx_pick<G_AFF2, true>(p.J) : dx_pick<G_AFF2, false>(p.J))
+          : d.bits == 4 ? (mb ? dx_pick<G_AFF4, true>(p.J) : dx_pick<G_AFF4, false>(p.J))
+                        : (mb ? dx_pick<G_AFF8, true>(p.J) : dx_pick<G_AFF8, false>(p.J));
+  hipLaunchKernelGGL(fn, dim3((unsigned)(p.tilesK * p.tilesM * p.split)), dim3(kThreads), 0, s, k);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (p.split > 1) {
+    const int64_t n4 = a.M * d.K / 4;
+    hipLaunchKernelGGL(k_dx_sum, dim3((unsigned)cdiv(n4, 256)), dim3(256), 0, s,
+                       reinterpret_cast<const float4*>(k.part), p.split, n4, (uint32_t)(d.K / 4), xe,
+                       a.dx, a.dxdt);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+}  // namespace qp

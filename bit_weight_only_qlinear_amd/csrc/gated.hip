@@ -140,68 +140,6 @@ __global__ void __launch_bounds__(1024) k_gated_any(GaArgs ga) {
   }
 }
 
-// ---- input gradients, simple form: fp32 gradients of the products' outputs
-// in the workspace ([M, N], or [M, 2 N] with the gate's first), then one
-// thread per 8 columns and 8 rows over all weight rows.
-struct DxSimple {
-  DxArgs a;
-  Desc d;
-  float* D;
-};
-
-__global__ void __launch_bounds__(256) k_dx_prep(DxSimple p) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, N = p.d.N;
-  if (i >= p.a.M * N) return;
-  const int bf = p.a.dydt == BF16;
-  const float dy = val16(static_cast<const uint16_t*>(p.a.dy)[i], bf);
-  if (!p.a.gated) {
-    p.D[i] = dy;
-    return;
-  }
-  const int64_t m = i / N, n = i - m * N;
-  const int64_t g = m * ((N + kCkptGroup - 1) / kCkptGroup) + n / kCkptGroup;
-  const float gv = (float)p.a.gq[i] * p.a.gs[g], uv = (float)p.a.uq[i] * p.a.us[g];
-  float f, df;
-  if (p.a.act == ACT_SILU) act_fd<ACT_SILU>(gv, f, df);
-  else act_fd<ACT_GELU_TANH>(gv, f, df);
-  const float dg = dy * uv * df, du = dy * f;
-  p.D[m * 2 * N + n] = dg;
-  p.D[m * 2 * N + N + n] = du;
-  auto r16 = [bf](float v) { return (uint16_t)(bf ? f32_to_bf16_rne(v) : f32_to_f16_rne(v)); };
-  if (p.a.dg) static_cast<uint16_t*>(p.a.dg)[i] = r16(dg);
-  if (p.a.du) static_cast<uint16_t*>(p.a.du)[i] = r16(du);
-}
-
-__global__ void __launch_bounds__(256) k_dx_any(DxSimple p) {
-  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, m0 = (int64_t)blockIdx.y * 8;
-  if (k >= p.d.K) return;
-  const int64_t N = p.d.N, NN = p.a.gated ? 2 * N : N;
-  float acc[8][8] = {};
-  for (int64_t n = 0; n < NN; ++n) {
-    float w[8];
-    weights8(p.d, n < N ? p.a.w : p.a.w2, n < N ? n : n - N, k, w);
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int64_t m = m0 + r < p.a.M ? m0 + r : p.a.M - 1;
-      const float v = p.D[m * NN + n];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[r][e] = fmaf(v, w[e], acc[r][e]);
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    if (m0 + r >= p.a.M) break;
-    const int64_t i = (m0 + r) * p.d.K + k;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = acc[r][e];
-      if (p.a.dxdt == F32) static_cast<float*>(p.a.dx)[i + e] = v;
-      else static_cast<uint16_t*>(p.a.dx)[i + e] =
-          (uint16_t)(p.a.dxdt == BF16 ? f32_to_bf16_rne(v) : f32_to_f16_rne(v));
-    }
-  }
-}
-
 }  // namespace
 
 hipError_t launch_gated_any(const Desc& d, const GatedArgs& a, hipStream_t s) {
@@ -210,21 +148,6 @@ hipError_t launch_gated_any(const Desc& d, const GatedArgs& a, hipStream_t s) {
                      dim3((unsigned)((d.N + kGaFeat - 1) / kGaFeat),
                           (unsigned)std::min<int64_t>((a.M + kGaRows - 1) / kGaRows, 4096)),
                      dim3(1024), 0, s, ga);
-  return hipGetLastError();
-}
-
-size_t dx_workspace_bytes(const Desc& d, int64_t M, bool gated) {
-  return (size_t)M * d.N * 4u * (gated ? 2 : 1);
-}
-
-hipError_t launch_dx(const Desc& d, const DxArgs& a, hipStream_t s) {
-  DxSimple p{a, d, static_cast<float*>(a.ws)};
-  hipLaunchKernelGGL(k_dx_prep, dim3((unsigned)((a.M * d.N + 255) / 256)), dim3(256), 0, s, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_dx_any,
-                     dim3((unsigned)((d.K / 8 + 255) / 256), (unsigned)((a.M + 7) / 8)), dim3(256),
-                     0, s, p);
   return hipGetLastError();
 }
 
