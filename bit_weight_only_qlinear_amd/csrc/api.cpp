@@ -818,8 +818,17 @@ qp_status qlinear_gated_forward(const qp_desc* d, const void* x, int32_t x_dtype
   qp::GatedArgs a{x, x_dtype, h_dtype, act, M, bufs_of(gate), bufs_of(up), bias_gate, bias_up, h,
                   static_cast<int8_t*>(gate_codes), gate_scales, static_cast<int8_t*>(up_codes),
                   up_scales};
+  size_t nbytes[5];
+  sizes_of(dd, nbytes);
+  bool small_bufs = (size_t)M * (size_t)dd.K * 2 < (size_t(1) << 31);
+  for (int i = 0; i < 5; ++i) small_bufs = small_bufs && nbytes[i] < (size_t(1) << 31);
+  const hipStream_t s = (hipStream_t)stream;
   (void)hipGetLastError();
-  return hip_status(qp::launch_gated_any(dd, a, (hipStream_t)stream), "qlinear_gated_forward launch");
+  const hipError_t e = !save && M <= 16 && small_bufs && qp::skinny_supported(dd)
+                           ? qp::launch_gated_skinny(dd, a, nbytes, s)
+                       : qp::gated_gemm_supported(dd) ? qp::launch_gated_gemm(dd, a, s)
+                                                      : qp::launch_gated_any(dd, a, s);
+  return hip_status(e, "qlinear_gated_forward launch");
 }
 
 qp_status qlinear_backward_workspace_bytes(const qp_desc* d, int64_t M, int32_t gated,

@@ -106,7 +106,14 @@ struct GatedArgs {
   int8_t* uq;
   float* us;
 };
+// The forms of the gated pair: any K (gated.hip); fp16-rounded weights on
+// MFMA, K % 64 == 0 (gemm.hip); exact codes on MFMA, 16 rows at most and no
+// checkpoints (skinny.hip).
 hipError_t launch_gated_any(const Desc& d, const GatedArgs& a, hipStream_t s);
+bool gated_gemm_supported(const Desc& d);
+hipError_t launch_gated_gemm(const Desc& d, const GatedArgs& a, hipStream_t s);
+hipError_t launch_gated_skinny(const Desc& d, const GatedArgs& a, const size_t bytes[5],
+                               hipStream_t s);
 
 // Input gradients.  dx [M, K] = dy [M, N] W, or with `gated` the sum of two
 // such products over dg = dh u act'(g) and du = dh act(g).

@@ -43,6 +43,7 @@
 #include <utility>
 
 #include "device_common.hpp"
+#include "mlp_common.hpp"
 #include "qp_internal.hpp"
 
 namespace qp {
@@ -76,6 +77,13 @@ struct SxArgs {
   uint32_t meta_bytes[3];   // allocated sizes (16-byte multiples)
   uint32_t meta_row[3];     // bytes per weight row of each metadata array
   uint32_t meta_lds[3];     // LDS offset of each array's slab (LDSM)
+  // the gated pair (GATED): the second layer, its slabs and bias, the activation
+  const void* qw2;
+  const void* qh2;
+  const void* meta2[3];
+  const void* bias2;
+  uint32_t meta_lds2[3];
+  int act;
 };
 
 constexpr uint32_t kSxMetaLds = 64u << 10;   // LDS budget for the metadata slabs
@@ -149,9 +157,11 @@ struct SxStage {
 template <bool LDSM, int BYTES>
 __device__ __forceinline__ void meta_ld(const SxArgs& a, const unsigned char* lds, int q,
                                         __amdgpu_buffer_rsrc_t r, bool ok, uint32_t row_local,
-                                        uint32_t row_global, uint32_t off, uint32_t* dst) {
+                                        uint32_t row_global, uint32_t off, uint32_t* dst,
+                                        bool second = false) {
   if constexpr (LDSM) {
-    const unsigned char* p = lds + a.meta_lds[q] + row_local * a.meta_row[q] + off;
+    const unsigned char* p =
+        lds + (second ? a.meta_lds2[q] : a.meta_lds[q]) + row_local * a.meta_row[q] + off;
     if constexpr (BYTES == 16) {
       const uint4 v = *reinterpret_cast<const uint4*>(p);
       dst[0] = v.x; dst[1] = v.y; dst[2] = v.z; dst[3] = v.w;
@@ -181,7 +191,7 @@ __device__ __forceinline__ void meta_ld(const SxArgs& a, const unsigned char* ld
 
 // PART: 3 = everything; 1 = the global loads only (codes, activations, and
 // metadata when it is not staged); 2 = the staged metadata only (LDS reads).
-template <int KIND, int GS, bool LDSM, int PART = 3>
+template <int KIND, int GS, bool LDSM, int PART = 3, bool GATED = false>
 __device__ __forceinline__ void sx_load(const SxArgs& a, const unsigned char* lds, int kb, int lane,
                                         int64_t n0, int64_t mrow, SxStage<KIND, GS>& s) {
   const uint32_t c0 = (uint32_t)kb * kSxCols;
@@ -199,14 +209,17 @@ __device__ __forceinline__ void sx_load(const SxArgs& a, const unsigned char* ld
                                              rx, xo == kOOB ? kOOB : xo + 64u * t, 0, 0));
   }
   constexpr uint32_t B = code_bits(KIND);
-  const __amdgpu_buffer_rsrc_t rq = rsrc(a.qw, a.qw_bytes);
-  const __amdgpu_buffer_rsrc_t r0 = rsrc(a.meta[0], a.meta_bytes[0]);
-  const __amdgpu_buffer_rsrc_t r1 = rsrc(a.meta[1], a.meta_bytes[1]);
-  const __amdgpu_buffer_rsrc_t r2 = rsrc(a.meta[2], a.meta_bytes[2]);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
+    // GATED: tile 1 is the second layer's rows n0 .. n0 + 15
+    const bool two = GATED && i == 1;
+    const __amdgpu_buffer_rsrc_t rq = rsrc(two ? a.qw2 : a.qw, a.qw_bytes);
+    const __amdgpu_buffer_rsrc_t r0 = rsrc(two ? a.meta2[0] : a.meta[0], a.meta_bytes[0]);
+    const __amdgpu_buffer_rsrc_t r1 = rsrc(two ? a.meta2[1] : a.meta[1], a.meta_bytes[1]);
+    const __amdgpu_buffer_rsrc_t r2 = rsrc(two ? a.meta2[2] : a.meta[2], a.meta_bytes[2]);
     // codes: row n0 + 16 i + r16, columns c0 + 32 g .. + 32
-    const int64_t n = n0 + 16 * i + r16;
+    const int rt = (GATED ? 0 : 16 * i) + r16;
+    const int64_t n = n0 + rt;
     const bool ok = n < a.N;
     const uint32_t off = ok ? (uint32_t)n * (K * B / 8u) + (c0 + 32u * g) * B / 8u : kOOB;
     if constexpr (!GLOB) {
@@ -222,32 +235,32 @@ __device__ __forceinline__ void sx_load(const SxArgs& a, const unsigned char* ld
       }
     }
     if constexpr (KIND == S_Q6K && GLOB) {
-      const __amdgpu_buffer_rsrc_t rh = rsrc(a.qh, a.qh_bytes);
+      const __amdgpu_buffer_rsrc_t rh = rsrc(two ? a.qh2 : a.qh, a.qh_bytes);
       const uint32_t ho = ok ? (uint32_t)n * (K / 4u) + (c0 + 32u * g) / 4u : kOOB;
       const uint2 v = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rh, ho, 0, 2));
       s.h[i][0] = v.x; s.h[i][1] = v.y;
     }
     // metadata of row n for the block's groups (rows past N read 0)
-    const uint32_t rl = (uint32_t)(16 * i + r16), rg = (uint32_t)n;
+    const uint32_t rl = (uint32_t)rt, rg = (uint32_t)n;
     if constexpr (!META) {
     } else if constexpr (KIND == S_AFF2 || KIND == S_AFF4 || KIND == S_AFF8) {
       // 128 / GS groups of 2 bytes: scales into m[0..1], biases into m[2..3]
       constexpr int MB = 256 / GS;
       s.m[i][1] = s.m[i][3] = 0;
-      meta_ld<LDSM, MB>(a, lds, 0, r0, ok, rl, rg, (c0 / GS) * 2u, &s.m[i][0]);
-      meta_ld<LDSM, MB>(a, lds, 1, r1, ok, rl, rg, (c0 / GS) * 2u, &s.m[i][2]);
+      meta_ld<LDSM, MB>(a, lds, 0, r0, ok, rl, rg, (c0 / GS) * 2u, &s.m[i][0], two);
+      meta_ld<LDSM, MB>(a, lds, 1, r1, ok, rl, rg, (c0 / GS) * 2u, &s.m[i][2], two);
     } else if constexpr (KIND == S_Q4K) {
       // 4 uint8 scale codes, 4 uint8 zero codes, the step word
-      meta_ld<LDSM, 4>(a, lds, 0, r0, ok, rl, rg, c0 / 32u, &s.m[i][0]);
-      meta_ld<LDSM, 4>(a, lds, 1, r1, ok, rl, rg, c0 / 32u, &s.m[i][1]);
-      meta_ld<LDSM, 4>(a, lds, 2, r2, ok, rl, rg, (c0 / 256u) * 4u, &s.st[i]);
+      meta_ld<LDSM, 4>(a, lds, 0, r0, ok, rl, rg, c0 / 32u, &s.m[i][0], two);
+      meta_ld<LDSM, 4>(a, lds, 1, r1, ok, rl, rg, c0 / 32u, &s.m[i][1], two);
+      meta_ld<LDSM, 4>(a, lds, 2, r2, ok, rl, rg, (c0 / 256u) * 4u, &s.st[i], two);
     } else if constexpr (KIND == S_Q6K) {
       // 8 int8 scale codes, the fp16 step
-      meta_ld<LDSM, 8>(a, lds, 0, r0, ok, rl, rg, c0 / 16u, &s.m[i][0]);
-      meta_ld<LDSM, 2>(a, lds, 2, r2, ok, rl, rg, (c0 / 256u) * 2u, &s.st[i]);
+      meta_ld<LDSM, 8>(a, lds, 0, r0, ok, rl, rg, c0 / 16u, &s.m[i][0], two);
+      meta_ld<LDSM, 2>(a, lds, 2, r2, ok, rl, rg, (c0 / 256u) * 2u, &s.st[i], two);
     } else if constexpr (GS > 0) {
       // SYM4 per group: 128 / GS fp32 scales
-      meta_ld<LDSM, 512 / GS>(a, lds, 0, r0, ok, rl, rg, (c0 / GS) * 4u, &s.m[i][0]);
+      meta_ld<LDSM, 512 / GS>(a, lds, 0, r0, ok, rl, rg, (c0 / GS) * 4u, &s.m[i][0], two);
     }
   }
 }
@@ -341,7 +354,9 @@ __device__ __forceinline__ void group_st(const SxStage<KIND, GS>& s, int i, int 
 // KIND / GS: format and group size (affine 32, 64, 128; Q4K 32; Q6K 16;
 // SYM4 32, 64, 128, or 0 for one scale per output channel, applied once to
 // the total).
-template <int KIND, int GS, bool XBF16, bool MBF16, bool LDSM>
+// GATED: h = act(g) u of two layers, a block owning 16 features of both (its
+// two 16-row tiles); g and u meet in the final sum.
+template <int KIND, int GS, bool XBF16, bool MBF16, bool LDSM, bool GATED = false>
 __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
   // partial sums [wave][tile][activation row][weight row]
   __shared__ float s_part[kSxWaves][2][16][17];
@@ -353,7 +368,7 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, r16 = lane & 15;
-  const int64_t n0 = (int64_t)blockIdx.x * kSxRows;
+  const int64_t n0 = (int64_t)blockIdx.x * (GATED ? kSxRows / 2 : kSxRows);
   const int64_t mrow = (int64_t)blockIdx.y * 16 + r16;   // this lane's activation row (A row)
   const int KB = (int)(a.K / kSxCols);
 
@@ -469,13 +484,17 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
   if constexpr (LDSM) {
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
-      const uint32_t pieces = (32u * a.meta_row[q] + 1023u) / 1024u;
-      const __amdgpu_buffer_rsrc_t r = rsrc(a.meta[q], a.meta_bytes[q]);
+      const uint32_t pieces = ((GATED ? 16u : 32u) * a.meta_row[q] + 1023u) / 1024u;
       const uint32_t base = (uint32_t)n0 * a.meta_row[q];
-      for (uint32_t pc = (uint32_t)wave; pc < pieces; pc += kSxWaves)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            r, (__attribute__((address_space(3))) void*)(s_meta + a.meta_lds[q] + 1024u * pc), 16,
-            base + 1024u * pc + 16u * (uint32_t)lane, 0, 0, 0);
+#pragma unroll
+      for (int l = 0; l < (GATED ? 2 : 1); ++l) {
+        const __amdgpu_buffer_rsrc_t r = rsrc(l ? a.meta2[q] : a.meta[q], a.meta_bytes[q]);
+        const uint32_t at = l ? a.meta_lds2[q] : a.meta_lds[q];
+        for (uint32_t pc = (uint32_t)wave; pc < pieces; pc += kSxWaves)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              r, (__attribute__((address_space(3))) void*)(s_meta + at + 1024u * pc), 16,
+              base + 1024u * pc + 16u * (uint32_t)lane, 0, 0, 0);
+      }
     }
   }
 
@@ -484,7 +503,7 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
   const int J = wave < KB ? (KB - wave + kSxWaves - 1) / kSxWaves : 0;
   sfor<kSxStages - 1>([&](auto P) {
     constexpr int p = decltype(P)::value;
-    if (p < J) sx_load<KIND, GS, LDSM, 1>(a, s_meta, wave + p * kSxWaves, lane, n0, mrow, st[p]);
+    if (p < J) sx_load<KIND, GS, LDSM, 1, GATED>(a, s_meta, wave + p * kSxWaves, lane, n0, mrow, st[p]);
   });
 
   if constexpr (LDSM) {
@@ -503,7 +522,7 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
   if constexpr (LDSM) {
     sfor<kSxStages - 1>([&](auto P) {
       constexpr int p = decltype(P)::value;
-      if (p < J) sx_load<KIND, GS, LDSM, 2>(a, s_meta, wave + p * kSxWaves, lane, n0, mrow, st[p]);
+      if (p < J) sx_load<KIND, GS, LDSM, 2, GATED>(a, s_meta, wave + p * kSxWaves, lane, n0, mrow, st[p]);
     });
   }
   for (int j0 = 0; j0 < J; j0 += kSxStages) {
@@ -512,7 +531,7 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
       const int j = j0 + q;
       if (j < J) {
         if (j + kSxStages - 1 < J)
-          sx_load<KIND, GS, LDSM>(a, s_meta, wave + (j + kSxStages - 1) * kSxWaves, lane, n0,
+          sx_load<KIND, GS, LDSM, 3, GATED>(a, s_meta, wave + (j + kSxStages - 1) * kSxWaves, lane, n0,
                                   mrow, st[(q + kSxStages - 1) % kSxStages]);
         compute(st[q]);
       }
@@ -537,6 +556,28 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
   const int nl = tid >> 4, m = tid & 15;
   const int64_t n = n0 + nl;
   const int64_t mm = (int64_t)blockIdx.y * 16 + m;
+  if constexpr (GATED) {
+    if (tid < 256 && mm < a.M && n < a.N) {
+      float g = 0.f, u = 0.f;
+#pragma unroll
+      for (int w = 0; w < kSxWaves; ++w) {
+        g += s_part[w][0][m][nl];
+        u += s_part[w][1][m][nl];
+      }
+      if constexpr (PERCH) {
+        g *= static_cast<const float*>(a.meta[0])[n];
+        u *= static_cast<const float*>(a.meta2[0])[n];
+      }
+      if (a.bias) g += meta_f(static_cast<const uint16_t*>(a.bias)[n], XBF16);
+      if (a.bias2) u += meta_f(static_cast<const uint16_t*>(a.bias2)[n], XBF16);
+      const float h = (a.act == ACT_SILU ? act_f<ACT_SILU>(g) : act_f<ACT_GELU_TANH>(g)) * u;
+      const int64_t idx = mm * a.N + n;
+      if (a.ydt == F32) static_cast<float*>(a.y)[idx] = h;
+      else static_cast<uint16_t*>(a.y)[idx] =
+          (uint16_t)(a.ydt == BF16 ? f32_to_bf16_rne(h) : f32_to_f16_rne(h));
+    }
+    return;
+  }
   if (tid < 512 && mm < a.M && n < a.N) {
     float sum = 0.f;
 #pragma unroll
@@ -555,17 +596,55 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
 
 typedef void (*SxFn)(SxArgs);
 
-template <int KIND, int GS, bool MB>
+template <int KIND, int GS, bool MB, bool GATED>
 SxFn sx_pick(bool xb, bool lm) {
-  if (lm) return xb ? k_skinny<KIND, GS, true, MB, true> : k_skinny<KIND, GS, false, MB, true>;
-  return xb ? k_skinny<KIND, GS, true, MB, false> : k_skinny<KIND, GS, false, MB, false>;
+  if (lm) return xb ? k_skinny<KIND, GS, true, MB, true, GATED> : k_skinny<KIND, GS, false, MB, true, GATED>;
+  return xb ? k_skinny<KIND, GS, true, MB, false, GATED> : k_skinny<KIND, GS, false, MB, false, GATED>;
 }
 
-template <int KIND>
+template <int KIND, bool GATED>
 SxFn sx_affine(int gs, bool mb, bool xb, bool lm) {
-  if (gs == 32) return mb ? sx_pick<KIND, 32, true>(xb, lm) : sx_pick<KIND, 32, false>(xb, lm);
-  if (gs == 64) return mb ? sx_pick<KIND, 64, true>(xb, lm) : sx_pick<KIND, 64, false>(xb, lm);
-  return mb ? sx_pick<KIND, 128, true>(xb, lm) : sx_pick<KIND, 128, false>(xb, lm);
+  if (gs == 32) return mb ? sx_pick<KIND, 32, true, GATED>(xb, lm) : sx_pick<KIND, 32, false, GATED>(xb, lm);
+  if (gs == 64) return mb ? sx_pick<KIND, 64, true, GATED>(xb, lm) : sx_pick<KIND, 64, false, GATED>(xb, lm);
+  return mb ? sx_pick<KIND, 128, true, GATED>(xb, lm) : sx_pick<KIND, 128, false, GATED>(xb, lm);
+}
+
+template <bool GATED>
+SxFn sx_kernel(const Desc& d, bool mb, bool xb, bool lm) {
+  if (d.fmt == AFFINE)
+    return d.bits == 2 ? sx_affine<S_AFF2, GATED>(d.gs, mb, xb, lm)
+         : d.bits == 4 ? sx_affine<S_AFF4, GATED>(d.gs, mb, xb, lm)
+                       : sx_affine<S_AFF8, GATED>(d.gs, mb, xb, lm);
+  if (d.fmt == Q4K) return sx_pick<S_Q4K, 32, false, GATED>(xb, lm);
+  if (d.fmt == Q6K) return sx_pick<S_Q6K, 16, false, GATED>(xb, lm);
+  return d.gs == d.K ? sx_pick<S_SYM4, 0, false, GATED>(xb, false)
+       : d.gs == 32  ? sx_pick<S_SYM4, 32, false, GATED>(xb, lm)
+       : d.gs == 64  ? sx_pick<S_SYM4, 64, false, GATED>(xb, lm)
+                     : sx_pick<S_SYM4, 128, false, GATED>(xb, lm);
+}
+
+// The layer's arguments, and the LDS bytes of its metadata slabs (`rows` of
+// each array, whole KiB: the copies' unit) from offset `lds`.
+uint32_t sx_layer(const Desc& d, const Bufs& b, const size_t bytes[5], uint32_t rows, uint32_t lds,
+                  SxArgs* a) {
+  a->qw = b.qweight;
+  a->qh = b.qweight_hi;
+  a->meta[0] = b.scales;
+  a->meta[1] = b.zeros;
+  a->meta[2] = b.steps;
+  a->N = d.N;
+  a->K = d.K;
+  a->qw_bytes = (uint32_t)bytes[0];
+  a->qh_bytes = (uint32_t)bytes[1];
+  for (int q = 0; q < 3; ++q) {
+    a->meta_bytes[q] = (uint32_t)((bytes[2 + q] + 15) & ~size_t(15));
+    // bytes per row: sizes are N * per-row bytes for every metadata array
+    a->meta_row[q] = (uint32_t)(bytes[2 + q] / (size_t)d.N);
+    if (d.fmt == SYM4 && d.gs == d.K && q == 0) a->meta_row[q] = 0;   // scale applied at the end
+    a->meta_lds[q] = lds;
+    lds += (rows * a->meta_row[q] + 1023u) & ~1023u;
+  }
+  return lds;
 }
 
 }  // namespace
@@ -577,49 +656,47 @@ hipError_t launch_skinny(const Desc& d, const void* x, int xdt, int64_t M, const
                          hipStream_t s) {
   if (M < 1 || !skinny_supported(d)) return hipErrorInvalidValue;
   SxArgs a{};
-  a.qw = b.qweight;
-  a.qh = b.qweight_hi;
-  a.meta[0] = b.scales;
-  a.meta[1] = b.zeros;
-  a.meta[2] = b.steps;
+  uint32_t lds = sx_layer(d, b, bytes, 32u, 0u, &a);
   a.x = x;
   a.bias = bias;
   a.y = y;
   a.M = M;
-  a.N = d.N;
-  a.K = d.K;
   a.ydt = ydt;
-  a.qw_bytes = (uint32_t)bytes[0];
-  a.qh_bytes = (uint32_t)bytes[1];
   a.x_bytes = (uint32_t)((uint64_t)M * d.K * 2);
-  uint32_t lds = 0;
-  for (int q = 0; q < 3; ++q) {
-    a.meta_bytes[q] = (uint32_t)((bytes[2 + q] + 15) & ~size_t(15));
-    // bytes per row: sizes are N * per-row bytes for every metadata array
-    a.meta_row[q] = (uint32_t)(bytes[2 + q] / (size_t)d.N);
-    if (d.fmt == SYM4 && d.gs == d.K && q == 0) a.meta_row[q] = 0;   // scale applied at the end
-    a.meta_lds[q] = lds;
-    lds += (32u * a.meta_row[q] + 1023u) & ~1023u;   // whole KiB: the copies' unit
-  }
   const bool lm = lds > 0 && lds <= kSxMetaLds;
   if (!lm) lds = 0;
-  const bool xb = xdt == BF16, mb = d.meta == BF16;
-  SxFn fn = nullptr;
-  if (d.fmt == AFFINE) {
-    fn = d.bits == 2 ? sx_affine<S_AFF2>(d.gs, mb, xb, lm)
-       : d.bits == 4 ? sx_affine<S_AFF4>(d.gs, mb, xb, lm) : sx_affine<S_AFF8>(d.gs, mb, xb, lm);
-  } else if (d.fmt == Q4K) {
-    fn = sx_pick<S_Q4K, 32, false>(xb, lm);
-  } else if (d.fmt == Q6K) {
-    fn = sx_pick<S_Q6K, 16, false>(xb, lm);
-  } else {
-    fn = d.gs == d.K ? sx_pick<S_SYM4, 0, false>(xb, false)
-       : d.gs == 32  ? sx_pick<S_SYM4, 32, false>(xb, lm)
-       : d.gs == 64  ? sx_pick<S_SYM4, 64, false>(xb, lm) : sx_pick<S_SYM4, 128, false>(xb, lm);
-  }
+  SxFn fn = sx_kernel<false>(d, d.meta == BF16, xdt == BF16, lm);
   const unsigned blocks = (unsigned)((d.N + kSxRows - 1) / kSxRows);
   const unsigned mtiles = (unsigned)((M + 15) / 16);
   hipLaunchKernelGGL(fn, dim3(blocks, mtiles), dim3(64 * kSxWaves), lds, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_skinny(const Desc& d, const GatedArgs& g, const size_t bytes[5],
+                               hipStream_t s) {
+  if (g.M < 1 || g.M > 16 || g.gq || !skinny_supported(d)) return hipErrorInvalidValue;
+  SxArgs a{}, b{};
+  uint32_t lds = sx_layer(d, g.gate, bytes, 16u, 0u, &a);
+  lds = sx_layer(d, g.up, bytes, 16u, lds, &b);
+  a.qw2 = b.qw;
+  a.qh2 = b.qh;
+  for (int q = 0; q < 3; ++q) {
+    a.meta2[q] = b.meta[q];
+    a.meta_lds2[q] = b.meta_lds[q];
+  }
+  a.x = g.x;
+  a.bias = g.bias_g;
+  a.bias2 = g.bias_u;
+  a.y = g.h;
+  a.M = g.M;
+  a.ydt = g.hdt;
+  a.act = g.act;
+  a.x_bytes = (uint32_t)((uint64_t)g.M * d.K * 2);
+  const bool lm = lds > 0 && lds <= kSxMetaLds;
+  if (!lm) lds = 0;
+  SxFn fn = sx_kernel<true>(d, d.meta == BF16, g.xdt == BF16, lm);
+  constexpr int rows = kSxRows / 2;
+  hipLaunchKernelGGL(fn, dim3((unsigned)((d.N + rows - 1) / rows)), dim3(64 * kSxWaves), lds, s, a);
   return hipGetLastError();
 }
 

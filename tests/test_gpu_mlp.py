@@ -233,8 +233,11 @@ def test_gated_forward(q, M, N, K, save):
         tol = 1.13 * dg * (np.abs(u) + du) + np.abs(mlp.act(g, kind)[0]) * du + \
             (U[hd] + 2.0 ** -17) * np.abs(h) + TINY[hd]
         within(o.h, h, tol, "h")
-        # first order: g and u are each within 2e-3 of themselves
-        assert oracle.rel_l2(f64(o.h), h) <= rel_limit(h, hd, 6e-3)
+        # first order: g and u are each within 2e-3 of themselves, as L2 over
+        # many outputs (one output alone has no relative bound: |g| may be any
+        # part of the sum |x| |w| of which the weights' rounding takes 2^-11)
+        if h.size >= 256:
+            assert oracle.rel_l2(f64(o.h), h) <= rel_limit(h, hd, 6e-3)
         assert (o.gate is None) == (not save)
         if save:
             for (codes, sc), v, e in ((o.gate, g, dg), (o.up, u, du)):
