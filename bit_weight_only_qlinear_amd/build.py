@@ -35,6 +35,7 @@ SOURCES = {
     "norm.hip": [],
     "gated.hip": [],
     "backward.hip": [],
+    "stage.hip": [],
 }
 
 

@@ -694,6 +694,17 @@ qp_status check_workspace(const void* ws, size_t have, size_t need) {
   return QP_OK;
 }
 
+// Workspace bytes of the gated pair; 0 where the exact-code kernel runs: up
+// to 16 rows (one MFMA tile), nothing to save, every buffer < 2 GiB.
+size_t gated_need(const qp::Desc& d, int64_t M, bool save) {
+  size_t b[5];
+  sizes_of(d, b);
+  bool small_bufs = (size_t)M * (size_t)d.K * 2 < (size_t(1) << 31);
+  for (int i = 0; i < 5; ++i) small_bufs = small_bufs && b[i] < (size_t(1) << 31);
+  return !save && M <= 16 && small_bufs && qp::skinny_supported(d) ? 0
+                                                                   : qp::gated_workspace_bytes(d, M);
+}
+
 }  // namespace
 
 extern "C" {
@@ -779,16 +790,13 @@ qp_status qpack_checkpoint_restore(const void* codes, const float* scales, int64
                     "qpack_checkpoint_restore launch");
 }
 
-qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int32_t x_dtype, int64_t M, int32_t save,
-                                        size_t* bytes) {
+qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int64_t M, int32_t save, size_t* bytes) {
   if (!bytes) return fail(QP_EINVAL, "bytes is NULL");
   *bytes = 0;
   qp::Desc dd;
   qp_status st = check_desc(d, &dd);
-  if (st != QP_OK || (st = check_act_dtype(x_dtype, "x_dtype")) != QP_OK ||
-      (st = check_block(dd, M)) != QP_OK)
-    return st;
-  (void)save;
+  if (st != QP_OK || (st = check_block(dd, M)) != QP_OK) return st;
+  *bytes = gated_need(dd, M, save != 0);
   return ok();
 }
 
@@ -811,23 +819,24 @@ qp_status qlinear_gated_forward(const qp_desc* d, const void* x, int32_t x_dtype
   st = check_ptrs({{x, "x", true}, {h, "h", true}, {bias_gate, "bias_gate", false},
                    {bias_up, "bias_up", false}, {gate_codes, "gate_codes", save},
                    {gate_scales, "gate_scales", save}, {up_codes, "up_codes", save},
-                   {up_scales, "up_scales", save}, {workspace, "workspace", false}});
+                   {up_scales, "up_scales", save}});
   if (st != QP_OK) return st;
   if (h == x) return fail(QP_EINVAL, "h must be a buffer of its own");
-  (void)workspace_bytes;
+  const size_t need = gated_need(dd, M, save);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != QP_OK) return st;
   qp::GatedArgs a{x, x_dtype, h_dtype, act, M, bufs_of(gate), bufs_of(up), bias_gate, bias_up, h,
                   static_cast<int8_t*>(gate_codes), gate_scales, static_cast<int8_t*>(up_codes),
                   up_scales};
-  size_t nbytes[5];
-  sizes_of(dd, nbytes);
-  bool small_bufs = (size_t)M * (size_t)dd.K * 2 < (size_t(1) << 31);
-  for (int i = 0; i < 5; ++i) small_bufs = small_bufs && nbytes[i] < (size_t(1) << 31);
   const hipStream_t s = (hipStream_t)stream;
   (void)hipGetLastError();
-  const hipError_t e = !save && M <= 16 && small_bufs && qp::skinny_supported(dd)
-                           ? qp::launch_gated_skinny(dd, a, nbytes, s)
-                       : qp::gated_gemm_supported(dd) ? qp::launch_gated_gemm(dd, a, s)
-                                                      : qp::launch_gated_any(dd, a, s);
+  hipError_t e;
+  if (need) {
+    e = qp::launch_gated(dd, a, workspace, s);
+  } else {
+    size_t nbytes[5];
+    sizes_of(dd, nbytes);
+    e = qp::launch_gated_skinny(dd, a, nbytes, s);
+  }
   return hip_status(e, "qlinear_gated_forward launch");
 }
 

@@ -1,153 +1,570 @@
-// Gated pair of projections on packed weights, any K:
-//   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) u.
+// Gated pair of projections on packed weights, fp16 MFMA:
+//   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) u,
+// and, for training, 8-bit checkpoints of g and u.
 //
-// A block owns 64 output features (one checkpoint group) and 4 activation
-// rows; each of its 16 waves computes 4 features, its lanes taking every
-// 64th chunk of 8 columns, weights dequantized in fp32.  Bounded by the
-// dequantization arithmetic; a simple form that is right for every shape.
-#include <algorithm>
-
+//  * A block's 256 weight rows are 128 features of both layers: LDS rows 128
+//    wi + 0 .. 63 hold the gate's features 64 wi .. of the tile, rows 128 wi
+//    + 64 .. 127 the up's.  A wave (128 rows x 64 or 32 activation rows) so
+//    ends with g and u of the same outputs in the same lane, and 64
+//    consecutive features of a row, one checkpoint group, in a pair of lanes:
+//    the activation, the product and both checkpoints are register work, and
+//    neither g nor u goes to memory.
+//  * Weights go through LDS dequantized to fp16 as in the qGEMM (same tile
+//    layout and column order); activations are staged once per call (stage.hip)
+//    and their fragments loaded from L2 straight into registers a step ahead.
+//  * Scales and biases come in 16-byte chunks (8 groups, 16 codes or 4 fp32
+//    scales) a chunk ahead where the rows are whole chunks, else per step: a
+//    wave's 32 rows make two loads of 32 cache lines each per step otherwise.
+//  * Bounded by the matrix cores: 4 M N K flop against N K bytes of codes.
+//    Where the last round of 256-row tiles would fill at most half of the 256
+//    CUs it is cut into tiles of 128 activation rows: 2048 x 4096 x 14336 makes
+//    896 tiles, three full rounds and 256 half tiles instead of four rounds.
+#include "gemm_kernels.hpp"
 #include "mlp_common.hpp"
 
 namespace qp {
 namespace {
 
-constexpr int kGaRows = 4, kGaFeat = 64;
+constexpr int kGF = 128;               // features per tile
+constexpr uint32_t kOff = 0x80000000u; // past every resource: reads 0
 
-struct GaArgs {
-  GatedArgs a;
-  Desc d;
+struct GatedK {
+  Bufs gate, up;
+  const unsigned char* xf;   // staged x: [step][4][MB][64] 16-byte chunks
+  const int* xe;             // row exponents
+  const uint16_t* bias_g;
+  const uint16_t* bias_u;
+  void* h;
+  int8_t* gq;                // checkpoints of g and u, or null
+  float* gs;
+  int8_t* uq;
+  float* us;
+  int64_t M, N, K;
+  int lg;                    // log2(group size / 32)
+  int mb, xb, hdt, act;
+  int MB, T;                 // 32-row blocks of x, steps of 64 columns
+  int tilesM, full;          // 256-row tiles; how many of them run whole
+  int small;                 // M <= 128: one 128-row tile per 128 features
 };
 
-__device__ __forceinline__ float val16(uint32_t b, int bf) {
-  return bf ? bf16_to_f32(b) : f16_to_f32(b);
+// One k-step of one thread: half a weight row (32 columns), raw.
+template <int KIND>
+struct GStage {
+  uint32_t w[GT<KIND>::W / 2];
+  uint32_t h[GT<KIND>::H > 0 ? GT<KIND>::H / 2 : 1];
+  uint32_t s0, s1, s2;   // metadata (where it comes per step)
+};
+
+// A chunk of a row's metadata: scales, biases or zero codes, step words.
+struct GChunk {
+  uint4 s, z;
+  uint2 p;
+};
+
+struct GRes {
+  __amdgpu_buffer_rsrc_t w, h, s, z, p;
+  uint32_t wo, ho, so, zo, po;   // the thread's half row; starts of its metadata rows
+  uint32_t half;
+};
+
+__device__ __forceinline__ uint32_t sel4(const uint4& v, int i) {   // uniform i
+  const uint32_t a = i & 1 ? v.y : v.x, b = i & 1 ? v.w : v.z;
+  return i & 2 ? b : a;
 }
 
-// Weights k0 .. k0 + 7 of row n in fp32 (k0 % 8 == 0).
-__device__ __forceinline__ void weights8(const Desc& d, const Bufs& b, int64_t n, int64_t k0,
-                                         float (&w)[8]) {
-  const int64_t K = d.K, e0 = n * K + k0;
-  const uint32_t* qw = static_cast<const uint32_t*>(b.qweight);
-  float S, T;
-  if (d.fmt == AFFINE) {
-    const int64_t g = n * (K / d.gs) + k0 / d.gs;
-    S = meta_to_f32(static_cast<const uint16_t*>(b.scales)[g], d.meta == BF16);
-    T = meta_to_f32(static_cast<const uint16_t*>(b.zeros)[g], d.meta == BF16);
-  } else if (d.fmt == Q4K) {
-    const uint32_t st = static_cast<const uint32_t*>(b.steps)[n * (K / 256) + k0 / 256];
-    const int64_t g = n * (K / 32) + k0 / 32;
-    S = (float)static_cast<const uint8_t*>(b.scales)[g] * f16_to_f32(st & 0xFFFFu);
-    T = -S * ((float)static_cast<const uint8_t*>(b.zeros)[g] * f16_to_f32(st >> 16));
-  } else if (d.fmt == Q6K) {
-    S = (float)static_cast<const int8_t*>(b.scales)[n * (K / 16) + k0 / 16] *
-        f16_to_f32(static_cast<const uint16_t*>(b.steps)[n * (K / 256) + k0 / 256]);
-    T = -32.f * S;
+// Steps per chunk.
+template <int KIND>
+__device__ __forceinline__ int chunk_steps(int lg) {
+  return KIND == G_Q4K ? 8 : KIND == G_Q6K ? 4 : KIND == G_SYM4 ? 2 << lg : 4 << lg;
+}
+
+template <int KIND>
+__device__ __forceinline__ void load_chunk(const GRes& r, int c, GChunk& m) {
+  m.s = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r.s, r.so + 16u * (uint32_t)c, 0, 0));
+  if constexpr (KIND != G_Q6K && KIND != G_SYM4)
+    m.z = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r.z, r.zo + 16u * (uint32_t)c, 0, 0));
+  if constexpr (KIND == G_Q4K)
+    m.p = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r.p, r.po + 8u * (uint32_t)c, 0, 0));
+  if constexpr (KIND == G_Q6K)
+    m.p.x = __builtin_amdgcn_raw_buffer_load_b16(r.p, r.po + 2u * (uint32_t)c, 0, 0);
+}
+
+// The raw metadata of step t (in its chunk) into a stage.
+template <int KIND>
+__device__ __forceinline__ void chunk_meta(const GChunk& m, int t, int lg, uint32_t half,
+                                           GStage<KIND>& st) {
+  const int r = t & (chunk_steps<KIND>(lg) - 1);
+  if constexpr (KIND == G_Q4K) {
+    const uint32_t sh = 16u * (uint32_t)(r & 1) + 8u * half;
+    st.s0 = sel4(m.s, r >> 1) >> sh;
+    st.s1 = sel4(m.z, r >> 1) >> sh;
+    st.s2 = r & 4 ? m.p.y : m.p.x;
+  } else if constexpr (KIND == G_Q6K) {
+    st.s0 = sel4(m.s, r) >> (16u * half);
+    st.s2 = m.p.x;
+  } else if constexpr (KIND == G_SYM4) {
+    const uint32_t a = sel4(m.s, (2 * r) >> lg), b = sel4(m.s, (2 * r + 1) >> lg);
+    st.s0 = half ? b : a;
   } else {
-    S = static_cast<const float*>(b.scales)[n * (K / d.gs) + k0 / d.gs];
-    T = -8.f * S;
+    const uint32_t sh = 16u * (((2u * (uint32_t)r + half) >> lg) & 1u);
+    const int w = ((2 * r) >> lg) >> 1;
+    st.s0 = sel4(m.s, w) >> sh;
+    st.s1 = sel4(m.z, w) >> sh;
   }
-  if (d.fmt == AFFINE && d.bits == 8) {
-    const uint32_t v0 = qw[e0 / 4], v1 = qw[e0 / 4 + 1];
+}
+
+// Steps at or past the row's end read the next row's data or 0 (every offset
+// is range-checked); the staged activations are 0 there.
+template <int KIND, bool CH>
+__device__ __forceinline__ void load_codes(const GRes& r, int t, int lg, GStage<KIND>& st) {
+  constexpr int W = GT<KIND>::W;
+  const uint32_t wk = r.wo + (uint32_t)t * (W * 4);
+  if constexpr (W == 4) {
+    const uint2 v = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r.w, wk, 0, 0));
+    st.w[0] = v.x; st.w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) {
+      const uint4 v = __builtin_bit_cast(
+          uint4, __builtin_amdgcn_raw_buffer_load_b128(r.w, wk + 16u * i, 0, 0));
+      st.w[4 * i] = v.x; st.w[4 * i + 1] = v.y; st.w[4 * i + 2] = v.z; st.w[4 * i + 3] = v.w;
+    }
+  }
+  if constexpr (KIND == G_Q6K) {
+    const uint2 v = __builtin_bit_cast(
+        uint2, __builtin_amdgcn_raw_buffer_load_b64(r.h, r.ho + (uint32_t)t * 16u, 0, 0));
+    st.h[0] = v.x; st.h[1] = v.y;
+  }
+  if constexpr (!CH) {
+    const uint32_t g2 = 2u * (uint32_t)t + r.half;
+    if constexpr (KIND == G_Q4K) {
+      st.s0 = __builtin_amdgcn_raw_buffer_load_b8(r.s, r.so + g2, 0, 0);
+      st.s1 = __builtin_amdgcn_raw_buffer_load_b8(r.z, r.zo + g2, 0, 0);
+      st.s2 = __builtin_amdgcn_raw_buffer_load_b32(r.p, r.po + (uint32_t)(t / 4) * 4u, 0, 0);
+    } else if constexpr (KIND == G_SYM4) {
+      st.s0 = __builtin_amdgcn_raw_buffer_load_b32(r.s, r.so + (g2 >> lg) * 4u, 0, 0);
+    } else if constexpr (KIND == G_AFF2 || KIND == G_AFF4 || KIND == G_AFF8) {
+      st.s0 = __builtin_amdgcn_raw_buffer_load_b16(r.s, r.so + (g2 >> lg) * 2u, 0, 0);
+      st.s1 = __builtin_amdgcn_raw_buffer_load_b16(r.z, r.zo + (g2 >> lg) * 2u, 0, 0);
+    }
+  }
+}
+
+// Scale and offset of the half row (Q6K: of its group grp of 16).
+template <int KIND>
+__device__ __forceinline__ void scale_of(const GStage<KIND>& st, int grp, int mb, float& S, float& T) {
+  if constexpr (KIND == G_Q4K) {
+    S = (float)(st.s0 & 0xFFu) * f16_to_f32(st.s2 & 0xFFFFu);
+    T = -S * ((float)(st.s1 & 0xFFu) * f16_to_f32(st.s2 >> 16));
+  } else if constexpr (KIND == G_Q6K) {
+    S = (float)(int8_t)((st.s0 >> (8 * grp)) & 0xFFu) * f16_to_f32(st.s2 & 0xFFFFu);
+    T = -32.f * S;
+  } else if constexpr (KIND == G_SYM4) {
+    S = __uint_as_float(st.s0);
+    T = -8.f * S;
+  } else if constexpr (KIND == G_SYM4C) {
+    S = 1.f;
+    T = -8.f;
+  } else {
+    S = meta_to_f32(st.s0 & 0xFFFFu, mb);
+    T = meta_to_f32(st.s1 & 0xFFFFu, mb);
+  }
+}
+
+template <int KIND>
+__device__ __forceinline__ uint32_t gfield(const GStage<KIND>& st, int j, int e) {
+  if constexpr (KIND == G_AFF2) return (st.w[j >> 1] >> (2 * (8 * (j & 1) + e))) & 3u;
+  else if constexpr (KIND == G_AFF8) return (st.w[2 * j + (e >> 2)] >> (8 * (e & 3))) & 255u;
+  else if constexpr (KIND == G_Q6K)
+    return ((st.w[j] >> (4 * e)) & 15u) | (((st.h[j >> 1] >> (2 * (8 * (j & 1) + e))) & 3u) << 4);
+  else return (st.w[j] >> (4 * e)) & 15u;
+}
+
+// Chunk j (8 columns) of the half row as fp16 in the order (0,4,1,5,2,6,3,7).
+template <int KIND>
+__device__ __forceinline__ uint4 gchunk(const GStage<KIND>& st, int j, int mb, uint32_t magic) {
+  float S, T;
+  scale_of<KIND>(st, KIND == G_Q6K ? (j >> 1) : 0, mb, S, T);
+  uint32_t p[4];
+  if constexpr (KIND == G_AFF4 || KIND == G_SYM4C) {
+    half2_t s2, t2;
+    s2.x = s2.y = (_Float16)S;
+    t2.x = t2.y = (_Float16)T;
+    const half2_t mag = {(_Float16)1024.f, (_Float16)1024.f};
+    const half2_t mag8 = {(_Float16)1032.f, (_Float16)1032.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = fmaf((float)((v0 >> (8 * i)) & 255u), S, T);
-      w[4 + i] = fmaf((float)((v1 >> (8 * i)) & 255u), S, T);
+      const half2_t q = __builtin_bit_cast(half2_t, and_or(st.w[j] >> (4 * i), 0x000F000Fu, magic));
+      p[i] = __builtin_bit_cast(uint32_t, KIND == G_SYM4C ? q - mag8
+                                                          : __builtin_elementwise_fma(q - mag, s2, t2));
     }
-  } else if (d.fmt == AFFINE && d.bits == 2) {
-    const uint32_t v = qw[e0 / 16] >> (2 * (e0 % 16));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = fmaf((float)((v >> (2 * i)) & 3u), S, T);
   } else {
-    const uint32_t v = qw[e0 / 8];
-    uint32_t h = 0;
-    if (d.fmt == Q6K) h = static_cast<const uint32_t*>(b.qweight_hi)[e0 / 16] >> (2 * (e0 % 16));
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i] = fmaf((float)(((v >> (4 * i)) & 15u) | (((h >> (2 * i)) & 3u) << 4)), S, T);
+    for (int i = 0; i < 4; ++i)
+      p[i] = pack_f16(fmaf((float)gfield<KIND>(st, j, i), S, T),
+                      fmaf((float)gfield<KIND>(st, j, i + 4), S, T));
+  }
+  return make_uint4(p[0], p[1], p[2], p[3]);
+}
+
+__device__ __forceinline__ uint32_t code8(float v, float inv) {
+  return (uint32_t)(int)rintf(fminf(fmaxf(v * inv, -127.f), 127.f)) & 255u;
+}
+
+// g and u of the lane's four consecutive features f .. f + 3 in block (i, j).
+template <int KIND, int J>
+__device__ __forceinline__ void pre_act4(const GatedK& a, const float16_t (&acc)[4][J], int i, int j,
+                                         int g4, int f, int xe, float (&g)[4], float (&u)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    g[q] = ldexpf(acc[i][j][4 * g4 + q], -xe);
+    u[q] = ldexpf(acc[i + 2][j][4 * g4 + q], -xe);
+  }
+  const int last = (int)a.N - 1;
+  if constexpr (KIND == G_SYM4C) {   // channel scales: the contraction ran on the codes
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int fc = min(f + q, last);
+      g[q] *= static_cast<const float*>(a.gate.scales)[fc];
+      u[q] *= static_cast<const float*>(a.up.scales)[fc];
+    }
+  }
+  if (a.bias_g) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t b = a.bias_g[min(f + q, last)];
+      g[q] += a.xb ? bf16_to_f32(b) : f16_to_f32(b);
+    }
+  }
+  if (a.bias_u) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t b = a.bias_u[min(f + q, last)];
+      u[q] += a.xb ? bf16_to_f32(b) : f16_to_f32(b);
+    }
   }
 }
 
-__global__ void __launch_bounds__(1024) k_gated_any(GaArgs ga) {
-  __shared__ float sg[kGaRows][kGaFeat], su[kGaRows][kGaFeat];
-  const GatedArgs& a = ga.a;
-  const Desc& d = ga.d;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t n0 = (int64_t)blockIdx.x * kGaFeat;
-  const int xb = a.xdt == BF16;
-  const uint16_t* x = static_cast<const uint16_t*>(a.x);
-  for (int64_t m0 = (int64_t)blockIdx.y * kGaRows; m0 < a.M; m0 += (int64_t)gridDim.y * kGaRows) {
-  __syncthreads();   // the rows before are stored
-  for (int f = wave; f < kGaFeat; f += 16) {
-    const int64_t n = n0 + f;
-    float g[kGaRows] = {0.f, 0.f, 0.f, 0.f}, u[kGaRows] = {0.f, 0.f, 0.f, 0.f};
-    if (n < d.N) {
-      for (int64_t k = 8 * lane; k < d.K; k += 512) {
-        float wg[8], wu[8];
-        weights8(d, a.gate, n, k, wg);
-        weights8(d, a.up, n, k, wu);
+// Epilogue: lane (el) holds features 8 g + 4 (el >> 5) + q of each 32 of the
+// wave's 64, of row el & 31 of each 32-row block.
+template <int KIND, int J, int ACT>
+__device__ __forceinline__ void finish(const GatedK& a, const float16_t (&acc)[4][J], int el, int mbw,
+                                       int f0) {
+  const int N = (int)a.N;
+  const bool vec = N % 4 == 0;
+  static_for<J>([&](auto JJ) {
+    constexpr int j = decltype(JJ)::value;
+    const int64_t m = (int64_t)(mbw + j) * 32 + (el & 31);
+    const bool mok = m < a.M;
+    const int xe = mok ? a.xe[m] : 0;
+    float inv[2] = {0.f, 0.f};
+    if (a.gq) {   // group scales: 32 values here, 32 in the other half wave
+      float mg = 0.f, mu = 0.f;
+      static_for<8>([&](auto G) {
+        constexpr int i = decltype(G)::value / 4, g4 = decltype(G)::value % 4;
+        const int f = f0 + 32 * i + 8 * g4 + 4 * (el >> 5);
+        float g[4], u[4];
+        pre_act4<KIND, J>(a, acc, i, j, g4, f, xe, g, u);
 #pragma unroll
-        for (int r = 0; r < kGaRows; ++r) {
-          if (m0 + r >= a.M) break;
-          const uint4 v = *reinterpret_cast<const uint4*>(x + (m0 + r) * d.K + k);
-          const uint32_t b[4] = {v.x, v.y, v.z, v.w};
+        for (int q = 0; q < 4; ++q) {
+          mg = fmaxf(mg, f + q < N ? fabsf(g[q]) : 0.f);
+          mu = fmaxf(mu, f + q < N ? fabsf(u[q]) : 0.f);
+        }
+      });
+      mg = div_rn(fmaxf(mg, __shfl_xor(mg, 32, 64)), 127.f);
+      mu = div_rn(fmaxf(mu, __shfl_xor(mu, 32, 64)), 127.f);
+      // the quotient in fp32: the values carry the fp16 weights' rounding anyway
+      inv[0] = mg > 0.f ? 1.f / mg : 0.f;
+      inv[1] = mu > 0.f ? 1.f / mu : 0.f;
+      if (mok && el < 32) {
+        const int64_t at = m * ((a.N + kCkptGroup - 1) / kCkptGroup) + f0 / kCkptGroup;
+        a.gs[at] = mg;
+        a.us[at] = mu;
+      }
+    }
+    if (!mok) return;
+    unsigned char* hrow = static_cast<unsigned char*>(a.h) + m * N * (a.hdt == F32 ? 4 : 2);
+    int8_t* grow = a.gq + m * N;
+    int8_t* urow = a.uq + m * N;
+    static_for<8>([&](auto G) {
+      constexpr int i = decltype(G)::value / 4, g4 = decltype(G)::value % 4;
+      const int f = f0 + 32 * i + 8 * g4 + 4 * (el >> 5);
+      float g[4], u[4];
+      uint32_t b[4];
+      pre_act4<KIND, J>(a, acc, i, j, g4, f, xe, g, u);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float xv = val16((b[e / 2] >> (16 * (e & 1))) & 0xFFFFu, xb);
-            g[r] = fmaf(xv, wg[e], g[r]);
-            u[r] = fmaf(xv, wu[e], u[r]);
+      for (int q = 0; q < 4; ++q) {
+        const float v = act_f<ACT>(g[q]) * u[q];
+        b[q] = a.hdt == F32 ? __float_as_uint(v) : a.hdt == BF16 ? f32_to_bf16_rne(v) : f32_to_f16_rne(v);
+      }
+      if (vec && f < N) {
+        if (a.hdt == F32)
+          *reinterpret_cast<uint4*>(hrow + 4 * f) = make_uint4(b[0], b[1], b[2], b[3]);
+        else
+          *reinterpret_cast<uint2*>(hrow + 2 * f) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+      } else if (!vec) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (f + q >= N) break;
+          if (a.hdt == F32) reinterpret_cast<uint32_t*>(hrow)[f + q] = b[q];
+          else reinterpret_cast<uint16_t*>(hrow)[f + q] = (uint16_t)b[q];
+        }
+      }
+      if (a.gq) {
+        uint32_t c[4], d[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          c[q] = code8(g[q], inv[0]);
+          d[q] = code8(u[q], inv[1]);
+        }
+        if (vec && f < N) {
+          *reinterpret_cast<uint32_t*>(grow + f) = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+          *reinterpret_cast<uint32_t*>(urow + f) = d[0] | d[1] << 8 | d[2] << 16 | d[3] << 24;
+        } else if (!vec) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (f + q >= N) break;
+            grow[f + q] = (int8_t)c[q];
+            urow[f + q] = (int8_t)d[q];
           }
         }
       }
+    });
+  });
+}
+
+// One tile: features n0 .. n0 + 127, 32-row blocks mb0 .. of x (J per wave).
+template <int KIND, bool CH, int J>
+__device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem, int64_t n0, int mb0) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wi = wave >> 2, wj = wave & 3;
+  const int64_t K = a.K;
+  const int mbw = mb0 + wj * J;   // this wave's first row block
+
+  // the wave stages LDS rows 32 wave .. + 31: one layer, 32 features
+  GRes r;
+  {
+    const bool up = (wave >> 1) & 1;
+    const Bufs b = {up ? a.up.qweight : a.gate.qweight, up ? a.up.qweight_hi : a.gate.qweight_hi,
+                    up ? a.up.scales : a.gate.scales, up ? a.up.zeros : a.gate.zeros,
+                    up ? a.up.steps : a.gate.steps};
+    const int64_t nrows = a.N - n0 < kGF ? a.N - n0 : kGF;
+    const uint32_t f = (uint32_t)(wrow_of(tid) - 32 * wave + 64 * wi + 32 * (wave & 1));
+    auto res = [&](const void* p, int64_t row) {
+      return rsrc(static_cast<const unsigned char*>(p) + n0 * row, (uint32_t)(nrows * row));
+    };
+    r.half = (uint32_t)(tid & 1);
+    const int64_t wrow = KIND == G_AFF2 ? K / 4 : KIND == G_AFF8 ? K : K / 2;
+    r.w = res(b.qweight, wrow);
+    r.wo = f * (uint32_t)wrow + r.half * (uint32_t)(GT<KIND>::W * 2);
+    r.h = r.s = r.z = r.p = r.w;
+    r.ho = r.so = r.zo = r.po = 0;
+    const int64_t ng = (K / 32) >> a.lg;
+    if constexpr (KIND == G_Q4K) {
+      r.s = res(b.scales, K / 32);
+      r.z = res(b.zeros, K / 32);
+      r.p = res(b.steps, (K / 256) * 4);
+      r.so = r.zo = f * (uint32_t)(K / 32);
+      r.po = f * (uint32_t)((K / 256) * 4);
+    } else if constexpr (KIND == G_Q6K) {
+      r.h = res(b.qweight_hi, K / 4);
+      r.ho = f * (uint32_t)(K / 4) + r.half * 8u;
+      r.s = res(b.scales, K / 16);
+      r.p = res(b.steps, (K / 256) * 2);
+      r.so = f * (uint32_t)(K / 16);
+      r.po = f * (uint32_t)((K / 256) * 2);
+    } else if constexpr (KIND == G_SYM4) {
+      r.s = res(b.scales, ng * 4);
+      r.so = f * (uint32_t)(ng * 4);
+    } else if constexpr (KIND != G_SYM4C) {
+      r.s = res(b.scales, ng * 2);
+      r.z = res(b.zeros, ng * 2);
+      r.so = r.zo = f * (uint32_t)(ng * 2);
     }
+  }
+
+  float16_t acc[4][J];
 #pragma unroll
-    for (int r = 0; r < kGaRows; ++r) {
-      g[r] = wave_sum_all(g[r]);
-      u[r] = wave_sum_all(u[r]);
-      if (n < d.N) {
-        if (a.bias_g) g[r] += val16(static_cast<const uint16_t*>(a.bias_g)[n], xb);
-        if (a.bias_u) u[r] += val16(static_cast<const uint16_t*>(a.bias_u)[n], xb);
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  // weight fragments, as in the qGEMM: lane row lane & 31, chunk 2 s + (lane >> 5)
+  uint32_t fa[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    fa[s] = (uint32_t)(lane & 31) * 128u + (uint32_t)wi * 128u * 128u +
+            (uint32_t)(((2 * s + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16);
+  auto rd_a = [&](uint32_t buf, int s, int i) {
+    return *reinterpret_cast<const half8_t*>(smem + fa[s] + (buf * kTileBytes + 4096u * i));
+  };
+  uint32_t xo[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+    xo[j] = mbw + j < a.MB ? (uint32_t)(mbw + j) * 1024u + 16u * lane : kOff;
+  const uint32_t xs = (uint32_t)a.MB * 1024u;   // one k-slice of 16
+  auto ld_b = [&](int t, int s, int j) {
+    const __amdgpu_buffer_rsrc_t rx = rsrc(a.xf + (int64_t)(t < a.T ? t : 0) * 4 * xs, 4u * xs);
+    return __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                           rx, xo[j] == kOff ? kOff : xo[j] + (uint32_t)s * xs, 0, 0));
+  };
+  const int wn = wrow_of(tid);
+  const uint32_t magic = 0x64006400u;
+  auto put = [&](uint32_t buf, int p, const GStage<KIND>& st) {
+    const int j = 4 * (tid & 1) + p;
+    *reinterpret_cast<uint4*>(smem + (uint32_t)wn * 128u + (uint32_t)((j ^ ((wn >> 1) & 7)) * 16) +
+                              buf * kTileBytes) = gchunk<KIND>(st, p, a.mb, magic);
+  };
+
+  half8_t Bf[4][J];
+  GChunk cur, nxt;
+  const int MP = chunk_steps<KIND>(a.lg);
+  constexpr bool RING = CH && KIND != G_SYM4C;
+
+  // One step: MFMAs on LDS buffer t & 1 and the fragments of x in Bf (reloaded
+  // slice by slice for step t + 1); conversion of step t + 1 (`nx`) into the
+  // other buffer; code loads of step t + 2 into `fre`.
+  auto kstep = [&](int t, GStage<KIND>& fre, GStage<KIND>& nx) {
+    const uint32_t buf = (uint32_t)(t & 1);
+    load_codes<KIND, CH>(r, t + 2, a.lg, fre);
+    if constexpr (RING) {
+      if (((t + 1) & (MP - 1)) == 0) {   // step t + 1 starts a chunk
+        cur = nxt;
+        load_chunk<KIND>(r, (t + 1) / MP + 1, nxt);
       }
-      if (lane == 0) {
-        sg[r][f] = g[r];
-        su[r][f] = u[r];
-      }
+      chunk_meta<KIND>(cur, t + 1, a.lg, r.half, nx);
     }
+    half8_t A[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) A[i] = rd_a(buf, 0, i);
+    static_for<4>([&](auto S) {
+      constexpr int s = decltype(S)::value;
+      static_for<4>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A[i], Bf[s][j], acc[i][j], 0, 0, 0);
+        if constexpr (s < 3) A[i] = rd_a(buf, s + 1, i);
+      });
+#pragma unroll
+      for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t + 1, s, j);
+      put(buf ^ 1u, s, nx);
+    });
+    __syncthreads();
+  };
+
+  GStage<KIND> st0, st1;
+  load_codes<KIND, CH>(r, 0, a.lg, st0);
+  load_codes<KIND, CH>(r, 1, a.lg, st1);
+  if constexpr (RING) {
+    load_chunk<KIND>(r, 0, cur);
+    load_chunk<KIND>(r, 1, nxt);
+    chunk_meta<KIND>(cur, 0, a.lg, r.half, st0);
   }
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(0, s, j);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) put(0u, p, st0);
   __syncthreads();
-  // wave r: the block's 64 features of row m0 + r
-  const int64_t m = m0 + wave, n = n0 + lane;
-  if (wave >= kGaRows || m >= a.M) continue;   // whole waves
-  const float g = sg[wave][lane], u = su[wave][lane];
-  if (n < d.N) {
-    const float h = (a.act == ACT_SILU ? act_f<ACT_SILU>(g) : act_f<ACT_GELU_TANH>(g)) * u;
-    const int64_t i = m * d.N + n;
-    if (a.hdt == F32) static_cast<float*>(a.h)[i] = h;
-    else static_cast<uint16_t*>(a.h)[i] =
-        (uint16_t)(a.hdt == BF16 ? f32_to_bf16_rne(h) : f32_to_f16_rne(h));
+  for (int t = 0; t < a.T; t += 2) {
+    kstep(t, st0, st1);
+    if (t + 1 < a.T) kstep(t + 1, st1, st0);
   }
-  if (a.gq) {   // features past N hold 0
-    const float sc[2] = {div_rn(wave_max_all(fabsf(g)), 127.f), div_rn(wave_max_all(fabsf(u)), 127.f)};
-    const int64_t ng = (d.N + kCkptGroup - 1) / kCkptGroup;
-    if (n < d.N) {
-      a.gq[m * d.N + n] = (int8_t)(sc[0] > 0.f ? rintf(div_rn(g, sc[0])) : 0.f);
-      a.uq[m * d.N + n] = (int8_t)(sc[1] > 0.f ? rintf(div_rn(u, sc[1])) : 0.f);
-    }
-    if (lane == 0) {
-      a.gs[m * ng + blockIdx.x] = sc[0];
-      a.us[m * ng + blockIdx.x] = sc[1];
-    }
-  }
+
+  int el = lane;
+  asm volatile("" : "+v"(el));   // keeps the epilogue's addresses after the loop
+  const int f0 = (int)n0 + 64 * wi;
+  if (f0 >= a.N) return;
+  if (a.act == ACT_SILU) finish<KIND, J, ACT_SILU>(a, acc, el, mbw, f0);
+  else finish<KIND, J, ACT_GELU_TANH>(a, acc, el, mbw, f0);
+}
+
+template <int KIND, bool CH>
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
+k_gated(GatedK a) {
+  __shared__ __attribute__((aligned(16))) unsigned char smem[2 * kTileBytes];
+  const int bid = blockIdx.x;
+  if (bid < a.full) {   // contiguous runs of tiles per XCD, m fastest
+    const int t = a.full % 8 == 0 ? (bid % 8) * (a.full / 8) + bid / 8 : bid;
+    gated_tile<KIND, CH, 2>(a, smem, (int64_t)(t / a.tilesM) * kGF, (t % a.tilesM) * 8);
+  } else {
+    const int nh = (int)gridDim.x - a.full, i = bid - a.full;
+    const int u = nh % 8 == 0 ? (i % 8) * (nh / 8) + i / 8 : i;
+    const int t = a.full + (a.small ? u : u / 2);
+    gated_tile<KIND, CH, 1>(a, smem, (int64_t)(t / a.tilesM) * kGF,
+                            (t % a.tilesM) * 8 + (a.small ? 0 : 4 * (u & 1)));
   }
 }
 
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t frag_bytes(const Desc& d, int64_t M) {
+  return (size_t)cdiv(d.K, 64) * 4u * (size_t)cdiv(M, 32) * 1024u;
+}
+
+template <int KIND>
+void (*pick(bool ch))(GatedK) { return ch ? k_gated<KIND, true> : k_gated<KIND, false>; }
+
 }  // namespace
 
-hipError_t launch_gated_any(const Desc& d, const GatedArgs& a, hipStream_t s) {
-  GaArgs ga{a, d};
-  hipLaunchKernelGGL(k_gated_any,
-                     dim3((unsigned)((d.N + kGaFeat - 1) / kGaFeat),
-                          (unsigned)std::min<int64_t>((a.M + kGaRows - 1) / kGaRows, 4096)),
-                     dim3(1024), 0, s, ga);
+size_t gated_workspace_bytes(const Desc& d, int64_t M) {
+  return frag_bytes(d, M) + (size_t)cdiv(M, 32) * 128u;
+}
+
+hipError_t launch_gated(const Desc& d, const GatedArgs& g, void* ws, hipStream_t s) {
+  GatedK a{};
+  a.gate = g.gate;
+  a.up = g.up;
+  a.xf = static_cast<const unsigned char*>(ws);
+  int* xe = reinterpret_cast<int*>(static_cast<unsigned char*>(ws) + frag_bytes(d, g.M));
+  a.xe = xe;
+  a.bias_g = static_cast<const uint16_t*>(g.bias_g);
+  a.bias_u = static_cast<const uint16_t*>(g.bias_u);
+  a.h = g.h;
+  a.gq = g.gq;
+  a.gs = g.gs;
+  a.uq = g.uq;
+  a.us = g.us;
+  a.M = g.M;
+  a.N = d.N;
+  a.K = d.K;
+  a.lg = d.gs == 128 ? 2 : d.gs == 64 ? 1 : 0;
+  a.mb = d.meta == BF16;
+  a.xb = g.xdt == BF16;
+  a.hdt = g.hdt;
+  a.act = g.act;
+  a.MB = (int)cdiv(g.M, 32);
+  a.T = (int)cdiv(d.K, 64);
+  a.small = g.M <= 128;
+  a.tilesM = (int)cdiv(g.M, 256);
+  const int64_t tiles = a.tilesM * cdiv(d.N, kGF);
+  int64_t blocks = tiles;
+  if (!a.small) {
+    const int64_t rest = tiles % 256;
+    a.full = (int)(rest && rest <= 128 ? tiles - rest : tiles);
+    blocks = a.full + 2 * (tiles - a.full);
+  }
+  StageArgs sa{};
+  sa.d = static_cast<const uint16_t*>(g.x);
+  sa.xf = ws;
+  sa.xe = xe;
+  sa.M = g.M;
+  sa.N = d.K;
+  const hipError_t e = launch_stage(sa, g.xdt, false, 0, true, s);
+  if (e != hipSuccess) return e;
+  // whole 16-byte metadata chunks per row
+  const bool ch = d.fmt == Q4K ? d.K % 512 == 0 : d.fmt == SYM4 ? d.K % (4 * d.gs) == 0
+                : d.fmt == AFFINE ? d.K % (8 * d.gs) == 0 : true;
+  void (*fn)(GatedK) = d.fmt == Q4K ? pick<G_Q4K>(ch)
+                     : d.fmt == Q6K ? k_gated<G_Q6K, true>
+                     : d.fmt == SYM4 ? (d.gs == d.K ? k_gated<G_SYM4C, true> : pick<G_SYM4>(ch))
+                     : d.bits == 2 ? pick<G_AFF2>(ch)
+                     : d.bits == 4 ? pick<G_AFF4>(ch) : pick<G_AFF8>(ch);
+  hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

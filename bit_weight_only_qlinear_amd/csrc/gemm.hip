@@ -218,7 +218,7 @@ hipError_t launch_gemm(const Desc& d, const void* x, int xdt, int64_t M, const B
                        const void* bias, void* y, int ydt, void* ws, hipStream_t s) {
   const size_t wsb = ws ? gemm_workspace_bytes(d, M) : 0;
   const bool n224 = wsb > 0;
-  GemmArgs a{};
+  GemmArgs a;
   a.qw = b.qweight;
   a.qh = b.qweight_hi;
   a.scales = b.scales;
@@ -271,58 +271,13 @@ hipError_t launch_gemm(const Desc& d, const void* x, int xdt, int64_t M, const B
                        d.K, y, d.N, ydt, BN, a.tilesN);
   }
   const unsigned blocks = (unsigned)a.tilesM * (unsigned)a.tilesN;
-  GemmPick p{};
+  GemmPick p;
   p.n224 = n224;
   p.xb = xdt == BF16;
   p.mb = d.meta == BF16;
   // chunked affine metadata: whole 8-group chunks per row (16-byte aligned)
   p.mch = d.fmt == AFFINE && ((d.gs == 64 && d.K % 512 == 0) || (d.gs == 32 && d.K % 256 == 0) ||
                               (d.gs == 128 && d.K % 1024 == 0));
-  if (d.fmt == AFFINE)
-    return d.bits == 2 ? gemm_launch_aff2(a, p, blocks, s)
-         : d.bits == 4 ? gemm_launch_aff4(a, p, blocks, s) : gemm_launch_aff8(a, p, blocks, s);
-  return gemm_launch_kq(d.fmt, a, p, blocks, s);
-}
-
-bool gated_gemm_supported(const Desc& d) {
-  return d.K % BK == 0 && d.K <= (int64_t(1) << 20);   // 32-bit tile offsets
-}
-
-hipError_t launch_gated_gemm(const Desc& d, const GatedArgs& g, hipStream_t s) {
-  GemmArgs a{};
-  a.qw = g.gate.qweight;
-  a.qh = g.gate.qweight_hi;
-  a.scales = g.gate.scales;
-  a.zeros = g.gate.zeros;
-  a.steps = g.gate.steps;
-  a.w2 = g.up;
-  a.x = g.x;
-  a.bias = g.bias_g;
-  a.bias2 = g.bias_u;
-  a.y = g.h;
-  a.M = g.M;
-  a.N = d.N;
-  a.K = d.K;
-  a.gs = d.gs;
-  a.ydt = g.hdt;
-  a.act = g.act;
-  a.gq = g.gq;
-  a.gsc = g.gs;
-  a.uq = g.uq;
-  a.usc = g.us;
-  a.tilesM = (int)cdiv(g.M, BM);
-  a.tilesN = (int)cdiv(d.N, BN / 2);
-  GemmPick p{};
-  p.gated = true;
-  p.xb = g.xdt == BF16;
-  p.mb = d.meta == BF16;
-  if (p.xb) {
-    hipLaunchKernelGGL(k_xexp, dim3((unsigned)g.M), dim3(256), 0, s,
-                       static_cast<const uint16_t*>(g.x), d.K, g.h, d.N, g.hdt, BN / 2, a.tilesN);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  const unsigned blocks = (unsigned)a.tilesM * (unsigned)a.tilesN;
   if (d.fmt == AFFINE)
     return d.bits == 2 ? gemm_launch_aff2(a, p, blocks, s)
          : d.bits == 4 ? gemm_launch_aff4(a, p, blocks, s) : gemm_launch_aff8(a, p, blocks, s);

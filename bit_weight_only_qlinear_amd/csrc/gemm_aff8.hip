@@ -10,8 +10,7 @@ hipError_t gemm_launch_aff8(const GemmArgs& a, const GemmPick& p, unsigned block
   // (kind, x dtype, metadata dtype, two groups per 64-column step)
 
 #define QP_GEMM_FLAGS(KD, MB, G)                                                       \
-  if (p.gated) fn = p.xb ? k_gemm<KD, true, MB, G, true> : k_gemm<KD, false, MB, G, true>;  \
-  else if (p.n224) fn = p.xb ? k_gemm224<KD, true, MB, G, 0> : k_gemm224<KD, false, MB, G, 0>;  \
+  if (p.n224) fn = p.xb ? k_gemm224<KD, true, MB, G, 0> : k_gemm224<KD, false, MB, G, 0>;  \
   else fn = p.xb ? k_gemm<KD, true, MB, G> : k_gemm<KD, false, MB, G>;
 #define QP_GEMM_FLAGS_CH(KD, MB, G, GSZ)                                               \
   if (p.n224 && p.mch) fn = p.xb ? k_gemm224<KD, true, MB, G, GSZ> : k_gemm224<KD, false, MB, G, GSZ>; \

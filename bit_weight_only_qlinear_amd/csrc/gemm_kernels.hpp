@@ -54,7 +54,6 @@
 #include <utility>
 
 #include "device_common.hpp"
-#include "mlp_common.hpp"
 #include "qp_internal.hpp"
 
 namespace qp {
@@ -72,22 +71,13 @@ struct GemmArgs {
   void* y;
   int64_t M, N, K;
   int gs, ydt, tilesM, tilesN;
-  // the gated pair (k_gemm<..., GATED>): the second layer's weights and bias,
-  // the activation, and the checkpoints of both outputs (or null)
-  Bufs w2;
-  const void* bias2;
-  int act;
-  int8_t* gq;
-  float* gsc;
-  int8_t* uq;
-  float* usc;
 };
 
 // Launches the qGEMM kernel of one format family on `blocks` blocks: n224
 // selects the 224-row tiles over staged activations, mch the chunked
 // affine metadata, xb bf16 activations, mb bf16 metadata.
 struct GemmPick {
-  bool n224, mch, xb, mb, gated;
+  bool n224, mch, xb, mb;
 };
 hipError_t gemm_launch_aff2(const GemmArgs& a, const GemmPick& p, unsigned blocks, hipStream_t s);
 hipError_t gemm_launch_aff4(const GemmArgs& a, const GemmPick& p, unsigned blocks, hipStream_t s);
@@ -365,20 +355,21 @@ __device__ __forceinline__ void convert_part(const Stage<KIND>& st, int p, unsig
   *reinterpret_cast<uint4*>(smem + wb + buf * kTileBytes) = weight_chunk<KIND, MBF16>(st, p, magic);
 }
 
-// Weight-side buffer resources and offsets of rows n0 .. n0 + nrows - 1 of a
-// layer (rows past them read 0); the thread stages half tid & 1 of row n0 + n.
+// Weight-side buffer resources and offsets of a block's rows n0 .. n0 +
+// nrows - 1 (rows past them read 0); thread t stages half row wrow_of(t).
 template <int KIND>
-__device__ __forceinline__ void weight_rsrc(const GemmArgs& a, const Bufs& b, int64_t n0,
-                                            int64_t nrows, int tid, int64_t n, Rsrc& r) {
+__device__ __forceinline__ void weight_rsrc(const GemmArgs& a, int64_t n0, int64_t nrows, int tid,
+                                            Rsrc& r) {
   const int64_t K = a.K;
   const int64_t wrow = (KIND == G_AFF2 ? K / 4 : KIND == G_AFF8 ? K : K / 2);
-  r.w = rsrc(static_cast<const unsigned char*>(b.qweight) + n0 * wrow, (uint32_t)(nrows * wrow));
+  r.w = rsrc(static_cast<const unsigned char*>(a.qw) + n0 * wrow, (uint32_t)(nrows * wrow));
   r.half = (uint32_t)(tid & 1);
+  const int64_t n = wrow_of(tid);
   r.wo = (uint32_t)(n * wrow) + r.half * (uint32_t)(GT<KIND>::W * 2);
   r.h = r.w;
   r.ho = 0;
   if constexpr (KIND == G_Q6K) {
-    r.h = rsrc(static_cast<const unsigned char*>(b.qweight_hi) + n0 * (K / 4), (uint32_t)(nrows * (K / 4)));
+    r.h = rsrc(static_cast<const unsigned char*>(a.qh) + n0 * (K / 4), (uint32_t)(nrows * (K / 4)));
     r.ho = (uint32_t)(n * (K / 4)) + r.half * 8u;
   }
   int64_t srow = 0, zrow = 0, prow = 0;   // bytes per weight row
@@ -386,142 +377,23 @@ __device__ __forceinline__ void weight_rsrc(const GemmArgs& a, const Bufs& b, in
   else if constexpr (KIND == G_Q6K) { srow = K / 16; prow = (K / 256) * 2; }
   else if constexpr (KIND == G_SYM4 || KIND == G_SYM4C) { srow = (K / a.gs) * 4; }
   else { srow = (K / a.gs) * 2; zrow = srow; }
-  r.s = rsrc(static_cast<const unsigned char*>(b.scales) + n0 * srow, (uint32_t)(nrows * srow));
+  r.s = rsrc(static_cast<const unsigned char*>(a.scales) + n0 * srow, (uint32_t)(nrows * srow));
   r.so = (uint32_t)(n * srow);
   r.z = r.s; r.zo = r.so;
   if (zrow) {
-    r.z = rsrc(static_cast<const unsigned char*>(b.zeros) + n0 * zrow, (uint32_t)(nrows * zrow));
+    r.z = rsrc(static_cast<const unsigned char*>(a.zeros) + n0 * zrow, (uint32_t)(nrows * zrow));
     r.zo = (uint32_t)(n * zrow);
   }
   r.p = r.s; r.po = 0;
   if (prow) {
-    r.p = rsrc(static_cast<const unsigned char*>(b.steps) + n0 * prow, (uint32_t)(nrows * prow));
+    r.p = rsrc(static_cast<const unsigned char*>(a.steps) + n0 * prow, (uint32_t)(nrows * prow));
     r.po = (uint32_t)(n * prow);
   }
 }
 
-__device__ __forceinline__ Bufs first_layer(const GemmArgs& a) {
-  return Bufs{a.qw, a.qh, a.scales, a.zeros, a.steps};
-}
-
-// Four consecutive outputs n .. n + 3 of row m into y [., N] of type ydt.
-__device__ __forceinline__ void store_y4(void* y, int ydt, int64_t m, int64_t n, int64_t N,
-                                         const float (&v)[4]) {
-  const int64_t idx = m * N + n;
-  if (N % 4 == 0) {
-    if (n >= N) return;
-    if (ydt == F32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(y) + idx) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-      uint32_t h[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) h[q] = ydt == BF16 ? f32_to_bf16_rne(v[q]) : f32_to_f16_rne(v[q]);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + idx) =
-          make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (n + q >= N) break;
-      if (ydt == F32) static_cast<float*>(y)[idx + q] = v[q];
-      else static_cast<uint16_t*>(y)[idx + q] =
-          (uint16_t)(ydt == BF16 ? f32_to_bf16_rne(v[q]) : f32_to_f16_rne(v[q]));
-    }
-  }
-}
-
-// Epilogue of the gated pair for one activation row m (j of the wave's 32-row
-// blocks): the lane holds, of features f0 .. f0 + 63, 4 consecutive ones per
-// (i, g) at f0 + 32 i + 8 g + 4 (lane >> 5), the gate's in acc[i] and the
-// up's in acc[i + 2]; the other half of the 64 is in lane ^ 32.  f0 is a
-// multiple of 64: one checkpoint group.  The checkpoint's quotient is taken
-// in fp32: the values carry the fp16 weights' rounding anyway.
-template <int KIND, bool XBF16>
-__device__ __forceinline__ void gated_store(const GemmArgs& a, const float16_t (&acc)[4][2], int j,
-                                            int el, int64_t m, int64_t f0, int xe) {
-  const uint16_t* bg = static_cast<const uint16_t*>(a.bias);
-  const uint16_t* bu = static_cast<const uint16_t*>(a.bias2);
-  float gv[2][16], uv[2][16], mg = 0.f, mu = 0.f;
-  static_for<2>([&](auto I) {
-    constexpr int i = decltype(I)::value;
-    static_for<16>([&](auto E) {
-      constexpr int e = decltype(E)::value;
-      const int64_t f = f0 + 32 * i + 8 * (e / 4) + 4 * (el >> 5) + (e & 3);
-      const int64_t fc = f < a.N ? f : a.N - 1;
-      float g = ldexpf(acc[i][j][e], -xe), u = ldexpf(acc[i + 2][j][e], -xe);
-      if constexpr (KIND == G_SYM4C) {   // the channel scales
-        g *= static_cast<const float*>(a.scales)[fc];
-        u *= static_cast<const float*>(a.w2.scales)[fc];
-      }
-      if (bg) g += XBF16 ? bf16_to_f32(bg[fc]) : f16_to_f32(bg[fc]);
-      if (bu) u += XBF16 ? bf16_to_f32(bu[fc]) : f16_to_f32(bu[fc]);
-      gv[i][e] = f < a.N ? g : 0.f;
-      uv[i][e] = f < a.N ? u : 0.f;
-      mg = fmaxf(mg, fabsf(gv[i][e]));
-      mu = fmaxf(mu, fabsf(uv[i][e]));
-    });
-  });
-  if (a.gq) {
-    mg = div_rn(fmaxf(mg, __shfl_xor(mg, 32, 64)), 127.f);
-    mu = div_rn(fmaxf(mu, __shfl_xor(mu, 32, 64)), 127.f);
-    const float ig = mg > 0.f ? 1.f / mg : 0.f, iu = mu > 0.f ? 1.f / mu : 0.f;
-    if (m < a.M && f0 < a.N) {
-      if (el < 32) {
-        const int64_t at = m * ((a.N + kCkptGroup - 1) / kCkptGroup) + f0 / kCkptGroup;
-        a.gsc[at] = mg;
-        a.usc[at] = mu;
-      }
-      auto code = [](float v, float inv) {
-        return (uint32_t)(int)rintf(fminf(fmaxf(v * inv, -127.f), 127.f)) & 255u;
-      };
-      static_for<8>([&](auto G) {
-        constexpr int i = decltype(G)::value / 4, g = decltype(G)::value % 4;
-        const int64_t f = f0 + 32 * i + 8 * g + 4 * (el >> 5), at = m * a.N + f;
-        uint32_t cg[4], cu[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          cg[q] = code(gv[i][4 * g + q], ig);
-          cu[q] = code(uv[i][4 * g + q], iu);
-        }
-        if (a.N % 4 == 0) {
-          if (f < a.N) {
-            *reinterpret_cast<uint32_t*>(a.gq + at) = cg[0] | cg[1] << 8 | cg[2] << 16 | cg[3] << 24;
-            *reinterpret_cast<uint32_t*>(a.uq + at) = cu[0] | cu[1] << 8 | cu[2] << 16 | cu[3] << 24;
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (f + q < a.N) {
-              a.gq[at + q] = (int8_t)cg[q];
-              a.uq[at + q] = (int8_t)cu[q];
-            }
-          }
-        }
-      });
-    }
-  }
-  if (m >= a.M) return;
-  static_for<8>([&](auto G) {
-    constexpr int i = decltype(G)::value / 4, g = decltype(G)::value % 4;
-    float v[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float gg = gv[i][4 * g + q];
-      v[q] = (a.act == ACT_SILU ? act_f<ACT_SILU>(gg) : act_f<ACT_GELU_TANH>(gg)) * uv[i][4 * g + q];
-    }
-    store_y4(a.y, a.ydt, m, f0 + 32 * i + 8 * g + 4 * (el >> 5), a.N, v);
-  });
-}
-
-// GATED: the tile's 256 weight rows are 128 features of both layers, so that
-// a lane ends with the gate's and the up's value of the same output: LDS rows
-// 128 wi + 0 .. 63 are the gate's features 64 wi .. 64 wi + 63 of the tile,
-// rows 128 wi + 64 .. 127 the up's.  A wave stages 32 consecutive LDS rows,
-// so its layer is uniform.
-template <int KIND, bool XBF16, bool MBF16, bool GS32, bool GATED = false>
+template <int KIND, bool XBF16, bool MBF16, bool GS32>
 __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 k_gemm(GemmArgs a) {
-  constexpr int BNF = GATED ? BN / 2 : BN;   // output features per tile
   __shared__ __attribute__((aligned(16))) unsigned char smem[4 * kTileBytes];
   __shared__ int s_xe[BM];   // prescale exponents of the block's activation rows
 
@@ -536,9 +408,9 @@ k_gemm(GemmArgs a) {
   const int bid = blockIdx.x;
   const int tile = (T % 8 == 0) ? (bid % 8) * (T / 8) + bid / 8 : bid;  // a bijection
   const int tm = tile % a.tilesM, tn = tile / a.tilesM;
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BNF;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int64_t mrows = a.M - m0 < BM ? a.M - m0 : BM;
-  const int64_t nrows = a.N - n0 < BNF ? a.N - n0 : BNF;
+  const int64_t nrows = a.N - n0 < BN ? a.N - n0 : BN;
   const int64_t K = a.K;
 
   // ---- buffer resources of this block's rows (rows past M / N read 0)
@@ -548,11 +420,7 @@ k_gemm(GemmArgs a) {
     r.x = rsrc(static_cast<const unsigned char*>(a.x) + m0 * K * 2, (uint32_t)mrows * xrow);
     r.xo = (uint32_t)(tid >> 3) * xrow + (uint32_t)(tid & 7) * 16u;
     r.xstride = 64u * xrow;
-    if constexpr (GATED)
-      weight_rsrc<KIND>(a, (wave >> 1) & 1 ? a.w2 : first_layer(a), n0, nrows, tid,
-                        wrow_of(tid) - 32 * wave + 64 * (wave >> 2) + 32 * (wave & 1), r);
-    else
-      weight_rsrc<KIND>(a, first_layer(a), n0, nrows, tid, wrow_of(tid), r);
+    weight_rsrc<KIND>(a, n0, nrows, tid, r);
   }
 
   float16_t acc[4][2];
@@ -688,14 +556,6 @@ k_gemm(GemmArgs a) {
   // bias loads from being hoisted above the main loop (register pressure)
   int el = lane;
   asm volatile("" : "+v"(el));
-  if constexpr (GATED) {
-    static_for<2>([&](auto J) {
-      constexpr int j = decltype(J)::value;
-      const int r = wj * 64 + j * 32 + (el & 31);
-      gated_store<KIND, XBF16>(a, acc, j, el, m0 + r, n0 + wi * 64, XBF16 ? s_xe[r] : 0);
-    });
-    return;
-  }
   static_for<4>([&](auto I) {
     constexpr int i = decltype(I)::value;
     static_for<4>([&](auto G) {
@@ -799,7 +659,7 @@ k_gemm224(GemmArgs a) {
   const int64_t K = a.K;
 
   Rsrc r;
-  weight_rsrc<KIND>(a, first_layer(a), n0, nrows, tid, wrow_of(tid), r);
+  weight_rsrc<KIND>(a, n0, nrows, tid, r);
   // staged activations of rows m0 .. m0 + 255 (M rounded up to 16 is staged)
   const int64_t srows = (a.M + 15) / 16 * 16 - m0;
   const __amdgpu_buffer_rsrc_t xr = rsrc(static_cast<const unsigned char*>(a.xf) + m0 * K * 2,

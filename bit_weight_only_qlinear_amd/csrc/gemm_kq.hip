@@ -9,8 +9,7 @@ hipError_t gemm_launch_kq(int fmt, const GemmArgs& a, const GemmPick& p, unsigne
   void (*fn)(GemmArgs) = nullptr;
   const bool xb = p.xb, n224 = p.n224;
 #define QP_GEMM_FLAGS(KD, MB, G)                                                 \
-  if (p.gated) fn = p.xb ? k_gemm<KD, true, MB, G, true> : k_gemm<KD, false, MB, G, true>;  \
-  else if (n224) fn = xb ? k_gemm224<KD, true, MB, G, 0> : k_gemm224<KD, false, MB, G, 0>;  \
+  if (n224) fn = xb ? k_gemm224<KD, true, MB, G, 0> : k_gemm224<KD, false, MB, G, 0>;  \
   else fn = xb ? k_gemm<KD, true, MB, G> : k_gemm<KD, false, MB, G>;
   if (fmt == Q4K) {
     if (n224 && a.K % 512 == 0)

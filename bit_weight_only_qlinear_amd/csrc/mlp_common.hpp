@@ -12,17 +12,18 @@ namespace qp {
 // a = sqrt(2 / pi), b = 0.044715 and t = tanh v = 1 - 2 / (1 + e^(2 v)):
 // 1/2 (1 + t) = 1 / (1 + e^(-2 v)) =: s, so act = g s and
 // act' = s + 2 g s (1 - s) a (1 + 3 b g^2) -- the logistic form again, with
-// no cancellation of 1 + t and no overflow: e^(+inf) gives s = 0.
+// no cancellation of 1 + t and no overflow: e^(+inf) gives s = 0.  The
+// reciprocal is the hardware's, within one unit in the last place.
 template <int ACT>
 __device__ __forceinline__ float act_sig(float g, float& slope) {
   if constexpr (ACT == ACT_SILU) {
     slope = 1.f;
-    return 1.f / (1.f + __expf(-g));
+    return __builtin_amdgcn_rcpf(1.f + __expf(-g));
   } else {
     constexpr float a2 = 1.5957691216057308f, b = 0.044715f;
     const float g2 = g * g;
     slope = a2 * fmaf(3.f * b, g2, 1.f);
-    return 1.f / (1.f + __expf(-a2 * g * fmaf(b, g2, 1.f)));
+    return __builtin_amdgcn_rcpf(1.f + __expf(-a2 * g * fmaf(b, g2, 1.f)));
   }
 }
 template <int ACT>

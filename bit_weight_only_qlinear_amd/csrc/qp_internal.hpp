@@ -106,14 +106,30 @@ struct GatedArgs {
   int8_t* uq;
   float* us;
 };
-// The forms of the gated pair: any K (gated.hip); fp16-rounded weights on
-// MFMA, K % 64 == 0 (gemm.hip); exact codes on MFMA, 16 rows at most and no
+// The forms of the gated pair: fp16-rounded weights on MFMA with a workspace
+// (gated.hip); exact codes on MFMA, K % 128 == 0, 16 rows at most and no
 // checkpoints (skinny.hip).
-hipError_t launch_gated_any(const Desc& d, const GatedArgs& a, hipStream_t s);
-bool gated_gemm_supported(const Desc& d);
-hipError_t launch_gated_gemm(const Desc& d, const GatedArgs& a, hipStream_t s);
+size_t gated_workspace_bytes(const Desc& d, int64_t M);
+hipError_t launch_gated(const Desc& d, const GatedArgs& a, void* ws, hipStream_t s);
 hipError_t launch_gated_skinny(const Desc& d, const GatedArgs& a, const size_t bytes[5],
                                hipStream_t s);
+
+// fp16 fragments of a product's 16-bit operand d [M, N] (stage.hip): row
+// exponents into xe [ceil(M / 32) * 32], fragments into xf (ceil(N / 64) *
+// ceil(M / 32) * 4 KiB, twice that for the gated pair's [dg | du]).
+struct StageArgs {
+  const uint16_t* d;
+  const int8_t* gq;   // gated: checkpoints of the pre-activations
+  const float* gs;
+  const int8_t* uq;
+  const float* us;
+  uint16_t* dg;       // gated: the gradients themselves, or null
+  uint16_t* du;
+  void* xf;
+  int* xe;
+  int64_t M, N;
+};
+hipError_t launch_stage(const StageArgs& r, int dt, bool gated, int act, bool perm, hipStream_t s);
 
 // Input gradients.  dx [M, K] = dy [M, N] W, or with `gated` the sum of two
 // such products over dg = dh u act'(g) and du = dh act(g).

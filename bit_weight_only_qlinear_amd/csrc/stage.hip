@@ -1,0 +1,210 @@
+// Staging of a product's 16-bit operand D [M, N] for fp16 MFMA: every row is
+// scaled by a power of two that brings its largest magnitude into [2^14,
+// 2^15) (bf16's range does not fit fp16, and gradients are small), rounded
+// once to fp16, and laid out in the B-fragment order of
+// v_mfma_f32_32x32x16_f16: [step of 64 columns][slice of 16][32-row block]
+// [64 lanes] 16-byte chunks, the lane holding row lane & 31, columns 8
+// (lane >> 5) .. + 7 of the slice, in order or (PERM) as (0,4,1,5,2,6,3,7), the
+// order in which packed weights dequantize.  Rows past M and columns past N
+// are 0, so a product needs no edge cases in its contraction.
+//
+// D is a given matrix, or for the gated pair's backward [dg | du], computed
+// here from dh and the 8-bit checkpoints and also written out in the
+// activation type.  Two passes: row maxima, then the fragments.  (A bound on
+// |dg| and |du| from dh and the scales alone would spare the first pass the
+// codes, but rows whose gates are all far negative would lose their bits.)
+#include "mlp_common.hpp"
+
+namespace qp {
+namespace {
+
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  half2_t h;
+  h.x = (_Float16)lo;
+  h.y = (_Float16)hi;
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+struct StageK {
+  const uint16_t* dy;
+  const int8_t* gq;
+  const float* gs;
+  const int8_t* uq;
+  const float* us;
+  uint16_t* dg;
+  uint16_t* du;
+  uint4* xf;
+  int* xe;
+  int64_t M, N;
+  int MB, T1;
+};
+
+template <bool BF>
+__device__ __forceinline__ float dval(uint32_t b) {
+  return BF ? bf16_to_f32(b) : f16_to_f32(b);
+}
+
+// dg and du of one value.
+template <int ACT>
+__device__ __forceinline__ void pre_grads(float dh, float g, float u, float& dg, float& du) {
+  float f, d;
+  act_fd<ACT>(g, f, d);
+  dg = dh * u * d;
+  du = dh * f;
+}
+
+// The 8 values n .. n + 7 of a row of dy (and of dg and du where GATED, into
+// x and y); 0 past N and where !rok.  sg, su: the group's scales.
+template <bool BF, bool GATED, bool V8, int ACT>
+__device__ __forceinline__ void load8(const StageK& a, int64_t at, int64_t n, bool rok, float sg,
+                                      float su, float (&x)[8], float (&y)[8]) {
+  float v[8], gv[8], uv[8];
+  if constexpr (V8) {
+    const bool ok = rok && n < a.N;
+    const uint4 u = ok ? *reinterpret_cast<const uint4*>(a.dy + at) : make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = dval<BF>((w[i / 2] >> (16 * (i & 1))) & 0xFFFFu);
+    if constexpr (GATED) {
+      const uint2 q = ok ? *reinterpret_cast<const uint2*>(a.gq + at) : make_uint2(0, 0);
+      const uint2 p = ok ? *reinterpret_cast<const uint2*>(a.uq + at) : make_uint2(0, 0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        gv[i] = (float)(int8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3))) * sg;
+        uv[i] = (float)(int8_t)((i < 4 ? p.x : p.y) >> (8 * (i & 3))) * su;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool ok = rok && n + i < a.N;
+      v[i] = ok ? dval<BF>(a.dy[at + i]) : 0.f;
+      if constexpr (GATED) {
+        gv[i] = ok ? (float)a.gq[at + i] * sg : 0.f;
+        uv[i] = ok ? (float)a.uq[at + i] * su : 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (GATED) pre_grads<ACT>(v[i], gv[i], uv[i], x[i], y[i]);
+    else x[i] = v[i];
+  }
+}
+
+// Exponent of each row of D (rows up to MB * 32; 0 past M): e = 14 -
+// floor(log2 b) with b the row's largest magnitude in D.
+template <bool BF, bool GATED, bool V8, int ACT>
+__global__ void __launch_bounds__(256) k_stage_exp(StageK a) {
+  __shared__ float red[4];
+  const int64_t row = blockIdx.x;
+  float b = 0.f;
+  if (row < a.M) {
+    const int64_t ng = (a.N + kCkptGroup - 1) / kCkptGroup;
+    for (int64_t n = 8 * threadIdx.x; n < a.N; n += 8 * 256) {
+      const int64_t g = row * ng + n / kCkptGroup;
+      float x[8], y[8];
+      load8<BF, GATED, V8, ACT>(a, row * a.N + n, n, true, GATED ? a.gs[g] : 0.f,
+                                GATED ? a.us[g] : 0.f, x, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        b = fmaxf(b, fabsf(x[i]));
+        if constexpr (GATED) b = fmaxf(b, fabsf(y[i]));
+      }
+    }
+  }
+  b = wave_max_all(b);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = b;
+  __syncthreads();
+  b = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  if (threadIdx.x == 0) a.xe[row] = b == 0.f ? 0 : 14 - ilogbf(fminf(b, 3.4e38f));
+}
+
+// One wave per 32 rows x 64 columns (one step): D as fp16 B fragments.
+template <bool BF, bool GATED, bool V8, int ACT, bool PERM>
+__global__ void __launch_bounds__(256) k_stage(StageK a) {
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (id >= (int64_t)a.MB * a.T1) return;   // whole waves
+  const int lane = threadIdx.x & 63;
+  const int t = (int)(id / a.MB), mb = (int)(id - (int64_t)t * a.MB);
+  const int64_t row = (int64_t)mb * 32 + (lane & 31);
+  const bool rok = row < a.M;
+  const int64_t ng = (a.N + kCkptGroup - 1) / kCkptGroup;
+  const int e = a.xe[row];
+  float sg = 0.f, su = 0.f;
+  if (GATED && rok) {
+    sg = a.gs[row * ng + t];
+    su = a.us[row * ng + t];
+  }
+  auto rnd = [](float f) { return BF ? f32_to_bf16_rne(f) : f32_to_f16_rne(f); };
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int64_t n = (int64_t)t * 64 + 16 * s + 8 * (lane >> 5);
+    const int64_t at = row * a.N + n;
+    float dg[8], du[8];
+    load8<BF, GATED, V8, ACT>(a, at, n, rok, sg, su, dg, du);
+    auto frag = [&](const float (&x)[8], int step) {
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        h[i] = PERM ? pack2(ldexpf(x[i], e), ldexpf(x[i + 4], e))
+                    : pack2(ldexpf(x[2 * i], e), ldexpf(x[2 * i + 1], e));
+      a.xf[(((int64_t)step * 4 + s) * a.MB + mb) * 64 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
+    };
+    frag(dg, t);
+    if constexpr (GATED) {
+      frag(du, t + a.T1);
+      auto out = [&](uint16_t* p, const float (&x)[8]) {
+        if (!p || !rok) return;
+        if constexpr (V8) {
+          if (n < a.N)
+            *reinterpret_cast<uint4*>(p + at) =
+                make_uint4(rnd(x[0]) | (rnd(x[1]) << 16), rnd(x[2]) | (rnd(x[3]) << 16),
+                           rnd(x[4]) | (rnd(x[5]) << 16), rnd(x[6]) | (rnd(x[7]) << 16));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n + i < a.N) p[at + i] = (uint16_t)rnd(x[i]);
+        }
+      };
+      out(a.dg, dg);
+      out(a.du, du);
+    }
+  }
+}
+
+typedef void (*StageFn)(StageK);
+template <bool BF, bool V8>
+void stage_pick(bool gated, int act, bool perm, StageFn* ex, StageFn* st) {
+  if (!gated) {
+    *ex = k_stage_exp<BF, false, V8, 0>;
+    *st = perm ? k_stage<BF, false, V8, 0, true> : k_stage<BF, false, V8, 0, false>;
+  } else if (act == ACT_SILU) {
+    *ex = k_stage_exp<BF, true, V8, ACT_SILU>;
+    *st = k_stage<BF, true, V8, ACT_SILU, false>;
+  } else {
+    *ex = k_stage_exp<BF, true, V8, ACT_GELU_TANH>;
+    *st = k_stage<BF, true, V8, ACT_GELU_TANH, false>;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_stage(const StageArgs& r, int dt, bool gated, int act, bool perm, hipStream_t s) {
+  StageK a{r.d, r.gq, r.gs, r.uq, r.us, r.dg, r.du, static_cast<uint4*>(r.xf), r.xe, r.M, r.N,
+           (int)((r.M + 31) / 32), (int)((r.N + 63) / 64)};
+  const bool bf = dt == BF16;
+  StageFn ex, sf;
+  if (r.N % 8 == 0) bf ? stage_pick<true, true>(gated, act, perm, &ex, &sf)
+                       : stage_pick<false, true>(gated, act, perm, &ex, &sf);
+  else bf ? stage_pick<true, false>(gated, act, perm, &ex, &sf)
+          : stage_pick<false, false>(gated, act, perm, &ex, &sf);
+  hipLaunchKernelGGL(ex, dim3((unsigned)a.MB * 32u), dim3(256), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(sf, dim3((unsigned)(((int64_t)a.MB * a.T1 + 3) / 4)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace qp

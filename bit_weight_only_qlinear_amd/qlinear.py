@@ -77,7 +77,7 @@ def _load():
         "qnorm_backward": (I32, [P, P, P, P, I32, I64, I64, P, P, P, P, P, P, ctypes.c_size_t, P]),
         "qpack_checkpoint": (I32, [P, I32, I64, I64, P, P, P]),
         "qpack_checkpoint_restore": (I32, [P, P, I64, I64, P, I32, P]),
-        "qlinear_gated_workspace_bytes": (I32, [D, I32, I64, I32, ctypes.POINTER(ctypes.c_size_t)]),
+        "qlinear_gated_workspace_bytes": (I32, [D, I64, I32, ctypes.POINTER(ctypes.c_size_t)]),
         "qlinear_gated_forward": (I32, [D, P, I32, I64, W, W, P, P, I32, P, I32, P, P, P, P, P,
                                         ctypes.c_size_t, P]),
         "qlinear_backward_workspace_bytes": (I32, [D, I64, I32, ctypes.POINTER(ctypes.c_size_t)]),
@@ -593,8 +593,7 @@ def qlinear_gated_forward(desc: QDesc, x, gate, up, act: str = "silu", bias_gate
               torch.empty((M, N), dtype=torch.int8, device=dev),
               torch.empty((M, _groups(N)), dtype=torch.float32, device=dev)]
     d, size = desc.c(), ctypes.c_size_t(0)
-    _check(lib.qlinear_gated_workspace_bytes(ctypes.byref(d), DTYPE_IDS[xd], M, int(save),
-                                             ctypes.byref(size)))
+    _check(lib.qlinear_gated_workspace_bytes(ctypes.byref(d), M, int(save), ctypes.byref(size)))
     ws = _scratch(size.value, dev) if size.value else None
     _run(dev, lib.qlinear_gated_forward, ctypes.byref(d), px, DTYPE_IDS[xd], M, ctypes.byref(wg),
          ctypes.byref(wu), *pb, a, h.data_ptr(), DTYPE_IDS[hd],

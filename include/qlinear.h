@@ -424,9 +424,9 @@ qp_status qpack_checkpoint(const void* x, int32_t x_dtype, int64_t M, int64_t K,
 qp_status qpack_checkpoint_restore(const void* codes, const float* scales, int64_t M, int64_t K,
                                    void* x, int32_t x_dtype, void* stream);
 
-/* Host only.  Workspace bytes qlinear_gated_forward can use (0: none). */
-qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int32_t x_dtype, int64_t M, int32_t save,
-                                        size_t* bytes);
+/* Host only.  Workspace bytes that qlinear_gated_forward needs (0: none); save
+ * != 0: with checkpoints. */
+qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int64_t M, int32_t save, size_t* bytes);
 
 /* Gated pair of projections in one pass over both layers' codes:
  *   g = x Wg^T (+ bias_gate),  u = x Wu^T (+ bias_up),  h = act(g) * u
@@ -437,10 +437,11 @@ qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int32_t x_dtype, int64
  * of g and u (qpack_checkpoint's layout, from the fp32 values) for
  * qlinear_gated_backward: all four or none.
  * Up to 16 rows without checkpoints, K % 128 == 0 and buffers below 2 GiB:
- * exact codes, as QP_KERNEL_GEMV_MFMA.  Otherwise fp16-rounded weights as
- * QP_KERNEL_GEMM where K % 64 == 0 (h carries their rounding, a relative
- * L2 error of about 2e-4, at any K); other K run a slow general form in fp32.
- * h's contents are undefined until the call completes. */
+ * exact codes, as QP_KERNEL_GEMV_MFMA, and no workspace.  Otherwise fp16
+ * MFMA as QP_KERNEL_GEMM, at any K: x staged as fp16 in the workspace (16-byte
+ * aligned, busy until the call's kernels finish), each weight rounded once
+ * to fp16 (per-channel SYM4: exact codes), a relative L2 error of about 3e-4
+ * in g and u. */
 qp_status qlinear_gated_forward(const qp_desc* d, const void* x, int32_t x_dtype, int64_t M,
                                 const qp_weights* gate, const qp_weights* up, const void* bias_gate,
                                 const void* bias_up, int32_t act, void* h, int32_t h_dtype,

@@ -478,15 +478,18 @@ def test_outputs_stay_inside(q):
     size = ctypes.c_size_t(0)
     q._check(q.lib.qlinear_backward_workspace_bytes(ctypes.byref(d.c()), M, 1, ctypes.byref(size)))
     ws, n = guarded(1, (size.value + 15) // 16 * 16, torch.uint8)
+    fsize = ctypes.c_size_t(0)
+    q._check(q.lib.qlinear_gated_workspace_bytes(ctypes.byref(d.c()), M, 1, ctypes.byref(fsize)))
+    fws, fn = guarded(1, (fsize.value + 15) // 16 * 16, torch.uint8)
     wg, wu = q._wstruct(bg), q._wstruct(bu)
     q._check(q.lib.qlinear_gated_forward(ctypes.byref(d.c()), x.data_ptr(), 1, M, ctypes.byref(wg),
                                          ctypes.byref(wu), None, None, 0, p["h"], 1, p["gc"], p["gs"],
-                                         p["uc"], p["us"], None, 0, None))
+                                         p["uc"], p["us"], fws.data_ptr(), fsize.value, None))
     q._check(q.lib.qlinear_gated_backward(ctypes.byref(d.c()), dh.data_ptr(), 1, M, ctypes.byref(wg),
                                           ctypes.byref(wu), 0, p["gc"], p["gs"], p["uc"], p["us"],
                                           p["dg"], p["du"], p["dx"], 1, ws.data_ptr(), size.value, None))
     torch.cuda.synchronize()
-    for k, (t, used) in dict(outs, ws=(ws, n)).items():
+    for k, (t, used) in dict(outs, ws=(ws, n), fws=(fws, fn)).items():
         assert torch.all(t[used:] == 77), k
     assert torch.equal(outs["h"][0][:M * N].view(M, N),
                        q.qlinear_gated_forward(d, x, bg, bu, save=True).h)
