@@ -315,7 +315,7 @@ k_dx(DxK a) {
   uint32_t xo[J];
 #pragma unroll
   for (int j = 0; j < J; ++j)
-    xo[j] = mb0 + j < a.MB ? (uint32_t)(mb0 + j) * 1024u + 16u * lane : kOff;
+    xo[j] = mb0 + j < a.MB ? (uint32_t)(mb0 + j) * 1024u + 16u * (2u * (lane & 31) + (lane >> 5)) : kOff;
   const uint32_t xs = (uint32_t)a.MB * 1024u;   // one k-slice of 16
   auto ld_b = [&](int t, int s, int j) {
     const __amdgpu_buffer_rsrc_t r = rsrc(a.xf + (int64_t)(t < t1 ? t : t0) * 4 * xs, 4u * xs);

@@ -404,7 +404,7 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
   uint32_t xo[J];
 #pragma unroll
   for (int j = 0; j < J; ++j)
-    xo[j] = mbw + j < a.MB ? (uint32_t)(mbw + j) * 1024u + 16u * lane : kOff;
+    xo[j] = mbw + j < a.MB ? (uint32_t)(mbw + j) * 1024u + 16u * (2u * (lane & 31) + (lane >> 5)) : kOff;
   const uint32_t xs = (uint32_t)a.MB * 1024u;   // one k-slice of 16
   auto ld_b = [&](int t, int s, int j) {
     const __amdgpu_buffer_rsrc_t rx = rsrc(a.xf + (int64_t)(t < a.T ? t : 0) * 4 * xs, 4u * xs);

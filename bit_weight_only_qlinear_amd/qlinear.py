@@ -134,6 +134,16 @@ class QDesc:
     def sym4(N, K, group_size=None):
         return QDesc("sym4", 4, K if group_size is None else group_size, N, K, "f32", 0)
 
+    @functools.cached_property
+    def _cref(self):
+        """The C form, built once (read only)."""
+        return ctypes.byref(self.c())
+
+    @functools.cached_property
+    def _buffer_sizes(self):
+        """(name, bytes) of every buffer, from the library."""
+        return tuple(qpack_sizes(self).items())
+
     def c(self):
         return _Desc(FMT_IDS[self.fmt], self.bits, self.group_size, self.super_block,
                      DTYPE_IDS[self.meta], 0, self.N, self.K)
@@ -397,11 +407,6 @@ class QGatedGrads(NamedTuple):
     dup: Any
 
 
-def _dt_name(t):
-    import torch
-    return {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32"}.get(t.dtype)
-
-
 def _torch_dt(name):
     import torch
     if name not in DTYPE_IDS:
@@ -410,16 +415,17 @@ def _torch_dt(name):
 
 
 def _arg(t, name, shape, dtype, device):
-    """A device tensor argument of the given shape and type, rows packed."""
-    if not t.is_cuda or t.device != device:
+    """Address of a device tensor argument of the given shape and type, rows
+    packed."""
+    if t.device == device and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _opt(t, name, shape, dtype, device):
@@ -435,36 +441,29 @@ def _rows(t, name):
     return t.shape[0], t.shape[1], _xdtype(t)
 
 
-@functools.lru_cache(maxsize=None)
-def _expected_sizes(desc):
-    return tuple(qpack_sizes(desc)[n] for n in BUFFERS)
-
-
 def _weights_arg(desc, w, name, device):
     """The weight struct, its buffers checked against the descriptor."""
-    for n, need in zip(BUFFERS, _expected_sizes(desc)):
-        t = w.get(n)
-        if not need:
-            continue
-        if t is None:
-            raise ValueError(f"{name}[{n!r}] is missing")
-        if t.device != device:
-            raise ValueError(f"{name}[{n!r}] must be on {device}, got {t.device}")
-        if not t.is_contiguous() or t.numel() * t.element_size() < need:
-            raise ValueError(f"{name}[{n!r}] must be contiguous and hold {need} bytes")
-    return _wstruct(w)
+    ptrs = []
+    for n, need in desc._buffer_sizes:
+        t = w.get(n) if need else None
+        if need and (t is None or t.device != device or not t.is_contiguous() or t.nbytes < need):
+            raise ValueError(f"{name}[{n!r}] must be a contiguous tensor of {need} bytes on {device}")
+        ptrs.append(t.data_ptr() if need else None)
+    return ctypes.byref(_Weights(*ptrs))
 
 
 def _run(device, fn, *args):
     """Calls a library function on the device's current stream (appended as
     the last argument), with that device current."""
     import torch
-    stream = torch.cuda.current_stream(device).cuda_stream
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() == device.index:
-        _check(fn(*args, stream))
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, stream))
+            status = fn(*args, stream)
+    if status != QP_OK:
+        _check(status)
 
 
 def _scratch(nbytes, device):
@@ -558,6 +557,8 @@ def qpack_checkpoint_restore(saved, dtype: str = "bf16"):
     if codes.dim() != 2:
         raise ValueError("codes must be a matrix [M, K]")
     M, K = codes.shape
+    if not codes.is_cuda:
+        raise ValueError(f"codes must be a GPU tensor, got {codes.device}")
     pc = _arg(codes, "codes", (M, K), torch.int8, codes.device)
     ps = _arg(scales, "scales", (M, _groups(K)), torch.float32, codes.device)
     x = torch.empty((M, K), dtype=_torch_dt(dtype), device=codes.device)
@@ -592,19 +593,18 @@ def qlinear_gated_forward(desc: QDesc, x, gate, up, act: str = "silu", bias_gate
               torch.empty((M, _groups(N)), dtype=torch.float32, device=dev),
               torch.empty((M, N), dtype=torch.int8, device=dev),
               torch.empty((M, _groups(N)), dtype=torch.float32, device=dev)]
-    d, size = desc.c(), ctypes.c_size_t(0)
-    _check(lib.qlinear_gated_workspace_bytes(ctypes.byref(d), M, int(save), ctypes.byref(size)))
+    size = ctypes.c_size_t(0)
+    _check(lib.qlinear_gated_workspace_bytes(desc._cref, M, int(save), ctypes.byref(size)))
     ws = _scratch(size.value, dev) if size.value else None
-    _run(dev, lib.qlinear_gated_forward, ctypes.byref(d), px, DTYPE_IDS[xd], M, ctypes.byref(wg),
-         ctypes.byref(wu), *pb, a, h.data_ptr(), DTYPE_IDS[hd],
+    _run(dev, lib.qlinear_gated_forward, desc._cref, px, DTYPE_IDS[xd], M, wg, wu, *pb, a,
+         h.data_ptr(), DTYPE_IDS[hd],
          *[None if t is None else t.data_ptr() for t in (*ck, ws)], size.value)
     return QGated(h, tuple(ck[:2]) if save else None, tuple(ck[2:]) if save else None)
 
 
 def _backward_workspace(desc, M, gated, device):
     size = ctypes.c_size_t(0)
-    _check(lib.qlinear_backward_workspace_bytes(ctypes.byref(desc.c()), M, int(gated),
-                                                ctypes.byref(size)))
+    _check(lib.qlinear_backward_workspace_bytes(desc._cref, M, int(gated), ctypes.byref(size)))
     return _scratch(size.value, device), size.value
 
 
@@ -618,8 +618,7 @@ def qlinear_backward(desc: QDesc, dy, w, dx_dtype: Optional[str] = None):
     xd = dx_dtype or yd
     dx = torch.empty((M, desc.K), dtype=_torch_dt(xd), device=dev)
     ws, n = _backward_workspace(desc, M, False, dev)
-    _run(dev, lib.qlinear_backward, ctypes.byref(desc.c()), py, DTYPE_IDS[yd], M,
-         ctypes.byref(ww), dx.data_ptr(), DTYPE_IDS[xd], ws.data_ptr(), n)
+    _run(dev, lib.qlinear_backward, desc._cref, py, DTYPE_IDS[yd], M, ww, dx.data_ptr(), DTYPE_IDS[xd], ws.data_ptr(), n)
     return dx
 
 
@@ -641,8 +640,7 @@ def qlinear_gated_backward(desc: QDesc, dh, gate, up, gate_saved, up_saved, act:
     dx = torch.empty((M, desc.K), dtype=_torch_dt(xd), device=dev)
     dg, du = (torch.empty_like(dh), torch.empty_like(dh)) if need_dpre else (None, None)
     ws, n = _backward_workspace(desc, M, True, dev)
-    _run(dev, lib.qlinear_gated_backward, ctypes.byref(desc.c()), ph, DTYPE_IDS[yd], M,
-         ctypes.byref(wg), ctypes.byref(wu), a, *pk,
+    _run(dev, lib.qlinear_gated_backward, desc._cref, ph, DTYPE_IDS[yd], M, wg, wu, a, *pk,
          *[None if t is None else t.data_ptr() for t in (dg, du)], dx.data_ptr(), DTYPE_IDS[xd],
          ws.data_ptr(), n)
     return QGatedGrads(dx, dg, du)
