@@ -9,8 +9,9 @@
 //    column chunks.  Four v_permlane swaps turn that 4 x 4 (row x word)
 //    arrangement around, so that a lane then has 8 columns of four rows: for
 //    each column the pairs (n, n+1), (n+2, n+3), cut out of two words at once
-//    (v_perm puts the same byte of two rows under the 1024 of an fp16 pair),
-//    one packed subtract and one packed fma, and one 8-byte LDS write of four
+//    (v_perm puts the same byte of two rows into the halves of a pair; its low
+//    nibbles make 1024 + q, its high ones 64 + q, with no shift), one packed
+//    subtract and one packed fma, and one 8-byte LDS write of four
 //    consecutive n.  The scales travel the same way: one (S, T) fp16 pair per
 //    lane and step, turned by the same swaps.
 //  * Weights in fp16, each rounded about once.  AFFINE: w = fma(q, scale,
@@ -210,9 +211,13 @@ __device__ __forceinline__ void dturn(const DStage<KIND>& st, DTurned<KIND>& d) 
 
 // Columns 2 b and 2 b + 1 of the lane's 8: four consecutive n each.
 template <int KIND, int b>
-__device__ __forceinline__ void dcols(const DTurned<KIND>& d, uint32_t magic, uint2 (&out)[2]) {
-  constexpr float MG = KIND == G_Q6K ? 1056.f : KIND == G_SYM4 ? 1032.f : 1024.f;
-  const half2_t mag = {(_Float16)MG, (_Float16)MG};
+__device__ __forceinline__ void dcols(const DTurned<KIND>& d, uint32_t magic, uint32_t magic64, uint2 (&out)[2]) {
+  // column 2 b: 1024 + u; column 2 b + 1: for nibbles, left where they are in
+  // the byte (mantissa bits 4 and up of 64, whose unit they are: 64 + u)
+  constexpr bool NIB = KIND != G_AFF2 && KIND != G_AFF8;
+  constexpr float OFF = KIND == G_Q6K ? 32.f : KIND == G_SYM4 ? 8.f : 0.f;
+  constexpr float M0 = 1024.f + OFF, M1 = (NIB ? 64.f : 1024.f) + OFF;
+  const half2_t mag[2] = {{(_Float16)M0, (_Float16)M0}, {(_Float16)M1, (_Float16)M1}};
   uint32_t r[2][2];   // [column][row pair]
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -228,18 +233,19 @@ __device__ __forceinline__ void dcols(const DTurned<KIND>& d, uint32_t magic, ui
     } else {
       constexpr uint32_t sel = 0x0C000C00u | ((4u + b) << 16) | b;
       const uint32_t p = __builtin_amdgcn_perm(d.w[2 * i + 1], d.w[2 * i], sel);
-      uint32_t m0 = magic, m1 = magic;
-      if constexpr (KIND == G_Q6K) {   // bits 4 b .. 4 b + 3 of each half: to bits 4, 5
-        constexpr int e0 = 4 * b - 4, e1 = 4 * b - 2;
+      uint32_t m0 = magic, m1 = magic64;
+      if constexpr (KIND == G_Q6K) {   // bits 4 b .. 4 b + 3 of each half: to 4, 5 and 8, 9
+        constexpr int e0 = 4 * b - 4, e1 = 4 * b + 2 - 8;
         m0 = and_or(e0 < 0 ? d.h[i] << 4 : d.h[i] >> (e0 < 0 ? 0 : e0), 0x00300030u, magic);
-        m1 = and_or(e1 < 0 ? d.h[i] << 2 : d.h[i] >> (e1 < 0 ? 0 : e1), 0x00300030u, magic);
+        m1 = and_or(e1 < 0 ? d.h[i] << (e1 < 0 ? -e1 : 0) : d.h[i] >> (e1 < 0 ? 0 : e1), 0x03000300u,
+                    magic64);
       }
       q[0] = and_or(p, 0x000F000Fu, m0);
-      q[1] = and_or(p >> 4, 0x000F000Fu, m1);
+      q[1] = and_or(p, 0x00F000F0u, m1);
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const half2_t v = __builtin_bit_cast(half2_t, q[c]) - mag;   // exact
+      const half2_t v = __builtin_bit_cast(half2_t, q[c]) - mag[c];   // exact
       half2_t w;
       if constexpr (KIND == G_Q6K || KIND == G_SYM4)
         w = __builtin_elementwise_fma(v, d.S[i], v * d.T[i]);
@@ -319,20 +325,26 @@ k_dx(DxK a) {
   const uint32_t xs = (uint32_t)a.MB * 1024u;   // one k-slice of 16
   auto ld_b = [&](int t, int s, int j) {
     const __amdgpu_buffer_rsrc_t r = rsrc(a.xf + (int64_t)(t < t1 ? t : t0) * 4 * xs, 4u * xs);
-    return __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                           r, xo[j] == kOff ? kOff : xo[j] + (uint32_t)s * xs, 0, 0));
+    // the slice as the scalar offset: the range check is on xo[j] alone, and
+    // a row block inside a slice is inside all four
+    return __builtin_bit_cast(half8_t,
+                              __builtin_amdgcn_raw_buffer_load_b128(r, xo[j], (uint32_t)s * xs, 0));
   };
-  const uint32_t magic = 0x64006400u;
-  // part b of a step's conversion: columns 2 b, 2 b + 1 of the lane's 8
+  const uint32_t magic = 0x64006400u, magic64 = 0x54005400u;   // 1024, 64
+  // part b of a step's conversion: columns 2 b, 2 b + 1 of the lane's 8, at
+  // line wl + b; wl is a multiple of 4, so b only turns slot bits
+  uint32_t pa[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint32_t L = wl + b, hs = ((L & 7u) ^ ((L >> 4) & 7u)) | (((L >> 2) & 1u) << 3);
+    pa[b] = L * 256u + 8u * rsub + (((uint32_t)wave) ^ hs) * 16u;
+  }
   auto put = [&](auto B, uint32_t buf, const DTurned<KIND>& d) {
     constexpr int b = decltype(B)::value;
     uint2 v[2];
-    dcols<KIND, b>(d, magic, v);
-    const uint32_t L = wl + b;
-    const uint32_t hs = ((L & 7u) ^ ((L >> 4) & 7u)) | (((L >> 2) & 1u) << 3);
-    const uint32_t at = L * 256u + buf * kDTile + 8u * rsub;
-    *reinterpret_cast<uint2*>(smem + at + (((uint32_t)wave) ^ hs) * 16u) = v[0];
-    *reinterpret_cast<uint2*>(smem + at + ((8u | (uint32_t)wave) ^ hs) * 16u) = v[1];
+    dcols<KIND, b>(d, magic, magic64, v);
+    *reinterpret_cast<uint2*>(smem + pa[b] + buf * kDTile) = v[0];
+    *reinterpret_cast<uint2*>(smem + (pa[b] ^ 128u) + buf * kDTile) = v[1];   // slot ^ 8
   };
 
   float16_t acc[4][J];
@@ -344,15 +356,14 @@ k_dx(DxK a) {
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
   half8_t Bf[4][J];
 
-  // One step: MFMAs on LDS buffer (t - t0) & 1 and the D fragments in Bf
+  // One step: MFMAs on LDS buffer cur = (t - t0) & 1 and the D fragments in Bf
   // (reloaded slice by slice for step t + 1); conversion of step t + 1 into
   // the other buffer; weight loads of step t + 2.  Steps past the end load
   // nothing that is used (empty resources).
-  auto kstep = [&](int t, DStage<KIND>& fre, DStage<KIND>& nxt) {
-    const uint32_t cur = (uint32_t)((t - t0) & 1);
+  auto kstep = [&](auto CUR, int t, DStage<KIND>& fre, DStage<KIND>& nxt) {
+    constexpr uint32_t cur = decltype(CUR)::value;
     dload<KIND>(a, o, t + 2, fre);
     DTurned<KIND> d;
-    dturn<KIND, MBF16>(nxt, d);
     half8_t A[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) A[i] = rd_a(cur, 0, i);
@@ -367,7 +378,12 @@ k_dx(DxK a) {
       });
 #pragma unroll
       for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t + 1, s, j);
-      put(S, cur ^ 1u, d);
+      // the conversion among the MFMAs of the first three slices
+      if constexpr (s == 0) dturn<KIND, MBF16>(nxt, d);
+      if constexpr (s == 1 || s == 2) {
+        put(std::integral_constant<int, 2 * s - 2>{}, cur ^ 1u, d);
+        put(std::integral_constant<int, 2 * s - 1>{}, cur ^ 1u, d);
+      }
     });
     __syncthreads();
   };
@@ -386,8 +402,8 @@ k_dx(DxK a) {
   }
   __syncthreads();
   for (int t = t0; t < t1; t += 2) {
-    kstep(t, st0, st1);
-    if (t + 1 < t1) kstep(t + 1, st1, st0);
+    kstep(std::integral_constant<uint32_t, 0>{}, t, st0, st1);
+    if (t + 1 < t1) kstep(std::integral_constant<uint32_t, 1>{}, t + 1, st1, st0);
   }
 
   // ---- lane: rows k = 8 g + 4 (lane >> 5) + q of column m = lane & 31

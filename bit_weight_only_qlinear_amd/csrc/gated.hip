@@ -182,7 +182,8 @@ __device__ __forceinline__ uint32_t gfield(const GStage<KIND>& st, int j, int e)
 
 // Chunk j (8 columns) of the half row as fp16 in the order (0,4,1,5,2,6,3,7).
 template <int KIND>
-__device__ __forceinline__ uint4 gchunk(const GStage<KIND>& st, int j, int mb, uint32_t magic) {
+__device__ __forceinline__ uint4 gchunk(const GStage<KIND>& st, int j, int mb, uint32_t magic,
+                                        uint32_t magic64) {
   float S, T;
   scale_of<KIND>(st, KIND == G_Q6K ? (j >> 1) : 0, mb, S, T);
   uint32_t p[4];
@@ -190,13 +191,17 @@ __device__ __forceinline__ uint4 gchunk(const GStage<KIND>& st, int j, int mb, u
     half2_t s2, t2;
     s2.x = s2.y = (_Float16)S;
     t2.x = t2.y = (_Float16)T;
-    const half2_t mag = {(_Float16)1024.f, (_Float16)1024.f};
-    const half2_t mag8 = {(_Float16)1032.f, (_Float16)1032.f};
+    // pairs 0 and 2 as 1024 + q; pairs 1 and 3 left at mantissa bits 4 .. 7 of
+    // 64, whose unit they are: 64 + q, without a shift
+    constexpr float OFF = KIND == G_SYM4C ? 8.f : 0.f;
+    const half2_t mag = {(_Float16)(1024.f + OFF), (_Float16)(1024.f + OFF)};
+    const half2_t mag64 = {(_Float16)(64.f + OFF), (_Float16)(64.f + OFF)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const half2_t q = __builtin_bit_cast(half2_t, and_or(st.w[j] >> (4 * i), 0x000F000Fu, magic));
-      p[i] = __builtin_bit_cast(uint32_t, KIND == G_SYM4C ? q - mag8
-                                                          : __builtin_elementwise_fma(q - mag, s2, t2));
+      const uint32_t w = i < 2 ? st.w[j] : st.w[j] >> 8;
+      const half2_t q = i & 1 ? __builtin_bit_cast(half2_t, and_or(w, 0x00F000F0u, magic64)) - mag64
+                              : __builtin_bit_cast(half2_t, and_or(w, 0x000F000Fu, magic)) - mag;
+      p[i] = __builtin_bit_cast(uint32_t, KIND == G_SYM4C ? q : __builtin_elementwise_fma(q, s2, t2));
     }
   } else {
 #pragma unroll
@@ -408,15 +413,17 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
   const uint32_t xs = (uint32_t)a.MB * 1024u;   // one k-slice of 16
   auto ld_b = [&](int t, int s, int j) {
     const __amdgpu_buffer_rsrc_t rx = rsrc(a.xf + (int64_t)(t < a.T ? t : 0) * 4 * xs, 4u * xs);
-    return __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                           rx, xo[j] == kOff ? kOff : xo[j] + (uint32_t)s * xs, 0, 0));
+    // the slice as the scalar offset: the range check is on xo[j] alone, and
+    // a row block inside a slice is inside all four
+    return __builtin_bit_cast(half8_t,
+                              __builtin_amdgcn_raw_buffer_load_b128(rx, xo[j], (uint32_t)s * xs, 0));
   };
   const int wn = wrow_of(tid);
-  const uint32_t magic = 0x64006400u;
+  const uint32_t magic = 0x64006400u, magic64 = 0x54005400u;   // 1024, 64
   auto put = [&](uint32_t buf, int p, const GStage<KIND>& st) {
     const int j = 4 * (tid & 1) + p;
     *reinterpret_cast<uint4*>(smem + (uint32_t)wn * 128u + (uint32_t)((j ^ ((wn >> 1) & 7)) * 16) +
-                              buf * kTileBytes) = gchunk<KIND>(st, p, a.mb, magic);
+                              buf * kTileBytes) = gchunk<KIND>(st, p, a.mb, magic, magic64);
   };
 
   half8_t Bf[4][J];
@@ -424,11 +431,11 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
   const int MP = chunk_steps<KIND>(a.lg);
   constexpr bool RING = CH && KIND != G_SYM4C;
 
-  // One step: MFMAs on LDS buffer t & 1 and the fragments of x in Bf (reloaded
+  // One step: MFMAs on LDS buffer buf = t & 1 and the fragments of x in Bf (reloaded
   // slice by slice for step t + 1); conversion of step t + 1 (`nx`) into the
   // other buffer; code loads of step t + 2 into `fre`.
-  auto kstep = [&](int t, GStage<KIND>& fre, GStage<KIND>& nx) {
-    const uint32_t buf = (uint32_t)(t & 1);
+  auto kstep = [&](auto BUF, int t, GStage<KIND>& fre, GStage<KIND>& nx) {
+    constexpr uint32_t buf = decltype(BUF)::value;
     load_codes<KIND, CH>(r, t + 2, a.lg, fre);
     if constexpr (RING) {
       if (((t + 1) & (MP - 1)) == 0) {   // step t + 1 starts a chunk
@@ -472,8 +479,8 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
   for (int p = 0; p < 4; ++p) put(0u, p, st0);
   __syncthreads();
   for (int t = 0; t < a.T; t += 2) {
-    kstep(t, st0, st1);
-    if (t + 1 < a.T) kstep(t + 1, st1, st0);
+    kstep(std::integral_constant<uint32_t, 0>{}, t, st0, st1);
+    if (t + 1 < a.T) kstep(std::integral_constant<uint32_t, 1>{}, t + 1, st1, st0);
   }
 
   int el = lane;
