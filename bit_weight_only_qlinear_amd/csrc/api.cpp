@@ -694,15 +694,19 @@ qp_status check_workspace(const void* ws, size_t have, size_t need) {
   return QP_OK;
 }
 
-// Workspace bytes of the gated pair; 0 where the exact-code kernel runs: up
-// to 16 rows (one MFMA tile), nothing to save, every buffer < 2 GiB.
-size_t gated_need(const qp::Desc& d, int64_t M, bool save) {
+// Which form of the gated pair a call takes.  With checkpoints, or above 16
+// rows (one MFMA tile), or with a buffer of 2 GiB, the staged product; one row
+// streams the codes (int4 affine, 4096 -> 2 x 14336: @G1@ us, @S1@ as an MFMA
+// tile), 2 .. 16 rows the MFMA tile on exact codes.
+enum GatedForm { GATED_GEMV, GATED_SKINNY, GATED_STAGED };
+GatedForm gated_form(const qp::Desc& d, int64_t M, bool save) {
   size_t b[5];
   sizes_of(d, b);
   bool small_bufs = (size_t)M * (size_t)d.K * 2 < (size_t(1) << 31);
   for (int i = 0; i < 5; ++i) small_bufs = small_bufs && b[i] < (size_t(1) << 31);
-  return !save && M <= 16 && small_bufs && qp::skinny_supported(d) ? 0
-                                                                   : qp::gated_workspace_bytes(d, M);
+  if (save || !small_bufs || M > 16) return GATED_STAGED;
+  if (M == 1 && qp::gated_gemv_supported(d)) return GATED_GEMV;
+  return qp::skinny_supported(d) ? GATED_SKINNY : GATED_STAGED;
 }
 
 }  // namespace
@@ -796,7 +800,7 @@ qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int64_t M, int32_t sav
   qp::Desc dd;
   qp_status st = check_desc(d, &dd);
   if (st != QP_OK || (st = check_block(dd, M)) != QP_OK) return st;
-  *bytes = gated_need(dd, M, save != 0);
+  if (gated_form(dd, M, save != 0) == GATED_STAGED) *bytes = qp::gated_workspace_bytes(dd, M);
   return ok();
 }
 
@@ -822,21 +826,21 @@ qp_status qlinear_gated_forward(const qp_desc* d, const void* x, int32_t x_dtype
                    {up_scales, "up_scales", save}});
   if (st != QP_OK) return st;
   if (h == x) return fail(QP_EINVAL, "h must be a buffer of its own");
-  const size_t need = gated_need(dd, M, save);
-  if ((st = check_workspace(workspace, workspace_bytes, need)) != QP_OK) return st;
+  const GatedForm form = gated_form(dd, M, save);
+  if (form == GATED_STAGED) {
+    st = check_workspace(workspace, workspace_bytes, qp::gated_workspace_bytes(dd, M));
+    if (st != QP_OK) return st;
+  }
   qp::GatedArgs a{x, x_dtype, h_dtype, act, M, bufs_of(gate), bufs_of(up), bias_gate, bias_up, h,
                   static_cast<int8_t*>(gate_codes), gate_scales, static_cast<int8_t*>(up_codes),
                   up_scales};
   const hipStream_t s = (hipStream_t)stream;
   (void)hipGetLastError();
-  hipError_t e;
-  if (need) {
-    e = qp::launch_gated(dd, a, workspace, s);
-  } else {
-    size_t nbytes[5];
-    sizes_of(dd, nbytes);
-    e = qp::launch_gated_skinny(dd, a, nbytes, s);
-  }
+  size_t nbytes[5];
+  sizes_of(dd, nbytes);
+  const hipError_t e = form == GATED_STAGED ? qp::launch_gated(dd, a, workspace, s)
+                     : form == GATED_GEMV   ? qp::launch_gated_gemv(dd, a, nbytes, s)
+                                            : qp::launch_gated_skinny(dd, a, nbytes, s);
   return hip_status(e, "qlinear_gated_forward launch");
 }
 

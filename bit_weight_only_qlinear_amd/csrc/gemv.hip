@@ -46,6 +46,7 @@
 // int8 scale codes are read once per 16-byte code load); ExecuTorch PR
 // #16577 (symmetric int4, qmin=-7..7).
 #include "device_common.hpp"
+#include "mlp_common.hpp"
 #include "qp_internal.hpp"
 
 namespace qp {
@@ -109,6 +110,14 @@ struct GemvArgs {
   uint32_t meta_lds[kMeta];
   uint32_t x_lds;         // LDS byte offset of the staged activation row (MT == 1)
   uint32_t x_prep;        // LDS byte offset of its pairs [C][XW] u32 and sums [C][GP] f32
+  // the gated pair (GATED): the second layer (same sizes), its slices, the
+  // activation
+  const uint32_t* qw2;
+  const uint32_t* qh2;
+  const void* meta2[kMeta];
+  uint32_t meta_lds2[kMeta];
+  uint32_t bias_row[2];   // 2 where the layer has a bias
+  int act;
 };
 
 // Raw buffer loads (gfx9 buffer resource, stride 0).  An offset at or beyond
@@ -213,6 +222,12 @@ __host__ __device__ constexpr int row_batch(int kind, int mt, int cpl, int nb) {
   return mt >= 2 ? (capped > 2 ? 2 : capped) : capped;
 }
 
+// GATED batches hold PB features: the first layer's rows, then the second's.
+__host__ __device__ constexpr int gated_feats(int kind, int cpl) {
+  const int n = (single_loads(kind) + 2) / (2 * cpl);
+  return n > 4 ? 4 : n > 0 ? n : 1;
+}
+
 // Raw code words of one batch of RB rows.
 template <int KIND, int RB, int CPL>
 struct Batch {
@@ -220,11 +235,32 @@ struct Batch {
   uint2 hw[RB][CPL];          // Q6K high plane
 };
 
-template <int KIND, int RB, int CPL, int RLO = 0, int RHI = RB>
+template <int KIND, int RB, int CPL, int RLO = 0, int RHI = RB, bool GATED = false>
 __device__ __forceinline__ void load_batch(const GemvArgs& a, __amdgpu_buffer_rsrc_t rqw,
                                            __amdgpu_buffer_rsrc_t rqh, const uint32_t (&lane_cw)[CPL],
                                            Batch<KIND, RB, CPL>& B, int r, int rowEnd) {
   const uint32_t C = (uint32_t)a.C;
+  if constexpr (GATED) {
+    // row rb: feature r + rb % PB of layer rb / PB
+    constexpr int PB = RB / 2;
+    const __amdgpu_buffer_rsrc_t rqw2 = rsrc(a.qw2, a.qw_bytes), rqh2 = rsrc(a.qh2, a.qh_bytes);
+#pragma unroll
+    for (int rb = RLO; rb < RHI; ++rb) {
+      const uint32_t n = (uint32_t)max(min(r + rb % PB, rowEnd - 1), 0);
+#pragma unroll
+      for (int j = 0; j < CPL; ++j) {
+        B.cw[rb][j] = __builtin_bit_cast(
+            uint4, __builtin_amdgcn_raw_buffer_load_b128(rb < PB ? rqw : rqw2, lane_cw[j], n * C * 16u, kNT));
+        if constexpr (base_kind(KIND) == K_Q6K)
+          B.hw[rb][j] = __builtin_bit_cast(
+              uint2, __builtin_amdgcn_raw_buffer_load_b64(
+                         rb < PB ? rqh : rqh2, lane_cw[j] == kOOB ? kOOB : lane_cw[j] / 2u,
+                         n * (uint32_t)(a.K / 4), kNT));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    return;
+  }
 #pragma unroll
   for (int rb = RLO; rb < RHI; ++rb) {
     // rows past the end of a partial batch re-read the last valid row
@@ -374,12 +410,13 @@ __device__ __forceinline__ void chunk_dots(const uint4 cw, const uint2 hw,
   }
 }
 
-template <int KIND, bool XBF16, int MT, int CPL, int RB, int XW, int GP>
+template <int KIND, bool XBF16, int MT, int CPL, int RB, int XW, int GP, bool GATED = false>
 __device__ __forceinline__ void compute_batch(const GemvArgs& a, const uint8_t* smem,
                                               const Batch<KIND, RB, CPL>& B,
                                               const uint32_t (&lane_meta)[CPL][GP],
                                               const uint32_t (&lane_step)[CPL],
-                                              const uint32_t (&row_base)[kMeta], int lrow0,
+                                              const uint32_t (&row_base)[kMeta],
+                                              const uint32_t (&row_base2)[kMeta], int lrow0,
                                               int lrmax,
                                               const uint32_t (&xq)[CPL][MT][XW],
                                               const float (&xs)[CPL][MT][GP],
@@ -392,10 +429,11 @@ __device__ __forceinline__ void compute_batch(const GemvArgs& a, const uint8_t* 
   for (int rb = 0; rb < RB; ++rb) {
     // LDS byte offsets of this row's metadata (wave-uniform); rows past the
     // end of a partial batch use the last valid row, like their code loads
-    const uint32_t lr = (uint32_t)min(lrow0 + rb, lrmax);
-    const uint32_t m0 = row_base[0] + lr * a.meta_row[0];
-    const uint32_t m1 = row_base[1] + lr * a.meta_row[1];
-    const uint32_t m2 = row_base[2] + lr * a.meta_row[2];
+    const uint32_t lr = (uint32_t)min(lrow0 + (GATED ? rb % (RB / 2) : rb), lrmax);
+    const bool two = GATED && rb >= RB / 2;
+    const uint32_t m0 = (two ? row_base2 : row_base)[0] + lr * a.meta_row[0];
+    const uint32_t m1 = (two ? row_base2 : row_base)[1] + lr * a.meta_row[1];
+    const uint32_t m2 = (two ? row_base2 : row_base)[2] + lr * a.meta_row[2];
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
       float S[GP], Tt[GP];
@@ -468,12 +506,15 @@ __device__ __forceinline__ uint32_t stage_meta(uint8_t* smem, __amdgpu_buffer_rs
   return src0 - a0;
 }
 
-template <int KIND, bool XBF16, int MT, int CPL, int NB>
+// GATED (one activation row, single batches): h = act(g) u of two layers; a
+// wave owns features, i.e. pairs of rows, whose two sums meet in its lanes.
+template <int KIND, bool XBF16, int MT, int CPL, int NB, bool GATED = false>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(QP_GEMV_MIN_WAVES_PER_EU)))
 k_gemv(GemvArgs a) {
+  static_assert(!GATED || (MT == 1 && NB == 1), "the gated pair: one activation row");
   using T = KT<KIND>;
   constexpr int CC = T::CC, XW = T::XW, GP = T::GP;
-  constexpr int RB = row_batch(KIND, MT, CPL, NB);
+  constexpr int RB = GATED ? 2 * gated_feats(KIND, CPL) : row_batch(KIND, MT, CPL, NB);
   constexpr int NV = CC / 8;   // 16-byte loads of x per chunk
 
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -501,13 +542,22 @@ k_gemv(GemvArgs a) {
   // -> LDS with direct loads; the code stream is released only once this
   // small prologue has landed, so that it does not queue behind the codes
   // of the whole grid
-  uint32_t row_base[kMeta];
+  uint32_t row_base[kMeta], row_base2[kMeta];
 #pragma unroll
   for (int i = 0; i < kMeta; ++i) {
+    const uint32_t mr = GATED && i == 3 ? a.bias_row[0] : a.meta_row[i];
     row_base[i] = a.meta_lds[i];
-    if (a.meta_row[i])
-      row_base[i] += stage_meta(smem, rsrc(a.meta[i], a.meta_bytes[i]), a.meta_row[i],
+    if (mr)
+      row_base[i] += stage_meta(smem, rsrc(a.meta[i], a.meta_bytes[i]), mr,
                                 (uint32_t)brow0, (uint32_t)brows, a.meta_lds[i], wave, lane);
+    row_base2[i] = 0;
+    if constexpr (GATED) {
+      const uint32_t mr2 = i == 3 ? a.bias_row[1] : a.meta_row[i];
+      row_base2[i] = a.meta_lds2[i];
+      if (mr2)
+        row_base2[i] += stage_meta(smem, rsrc(a.meta2[i], a.meta_bytes[i]), mr2, (uint32_t)brow0,
+                                   (uint32_t)brows, a.meta_lds2[i], wave, lane);
+    }
   }
   const __amdgpu_buffer_rsrc_t rx = rsrc(a.x, a.x_bytes);
   if constexpr (MT == 1)
@@ -542,7 +592,7 @@ k_gemv(GemvArgs a) {
   constexpr int EARLY = early_rows(KIND) < RB ? early_rows(KIND) : RB;
   Batch<KIND, RB, CPL> B0;
   if constexpr (EARLY > 0) {
-    load_batch<KIND, RB, CPL, 0, EARLY>(a, rqw, rqh, lane_cw, B0, row0, rowEnd);
+    load_batch<KIND, RB, CPL, 0, EARLY, GATED>(a, rqw, rqh, lane_cw, B0, row0, rowEnd);
     constexpr int n = EARLY * CPL * (base_kind(KIND) == K_Q6K ? 2 : 1);
     constexpr int nn = n > 63 ? 63 : n;
     __builtin_amdgcn_s_waitcnt((nn & 0xF) | (0x7 << 4) | (0xF << 8) | ((nn >> 4) << 14));
@@ -607,7 +657,7 @@ k_gemv(GemvArgs a) {
       lane_meta[j][0] = 4u * ((cu * CC) / (uint32_t)a.gs);
     }
   }
-  if constexpr (EARLY < RB) load_batch<KIND, RB, CPL, EARLY, RB>(a, rqw, rqh, lane_cw, B0, row0, rowEnd);
+  if constexpr (EARLY < RB) load_batch<KIND, RB, CPL, EARLY, RB, GATED>(a, rqw, rqh, lane_cw, B0, row0, rowEnd);
 
   // ---- 3. activations as pairs matching the code pairs, and their sums
   uint32_t xq[CPL][MT][XW];
@@ -641,6 +691,47 @@ k_gemv(GemvArgs a) {
       }
     }
   }
+
+  // the gated pair's last step for one feature
+  auto gate_store = [&](int n, float g, float u) {
+    if (a.bias_row[0]) g += xval<XBF16>(lds_read<uint16_t>(smem, row_base[3] + 2u * (uint32_t)(n - brow0)));
+    if (a.bias_row[1]) u += xval<XBF16>(lds_read<uint16_t>(smem, row_base2[3] + 2u * (uint32_t)(n - brow0)));
+    store_y(a.y, n, (a.act == ACT_SILU ? act_f<ACT_SILU>(g) : act_f<ACT_GELU_TANH>(g)) * u, a.ydt);
+  };
+  auto finish_gated = [&](float (&yacc)[RB][MT], int r) {
+    constexpr int PB = RB / 2;
+    if (KW == 1) {
+      // gates as values 0 .. 3, ups as 4 .. 7 of the transposed reduction: a
+      // feature's two sums end 8 lanes apart
+      float v[8];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        v[p] = p < PB ? yacc[p < PB ? p : 0][0] : 0.f;
+        v[4 + p] = p < PB ? yacc[PB + (p < PB ? p : 0)][0] : 0.f;
+      }
+      const float t = wave_sums8<8>(v, lane);
+      const float u = dpp_f<QP_DPP_ROW_ROR8>(0.f, t);
+      const int R = lane >> 4, p = ((R & 1) << 1) | (R >> 1), n = r + p;
+      if ((lane & 15) == 0 && p < PB && n < rowEnd) gate_store(n, t, u);
+    } else {
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) yacc[rb][0] = wave_sum_lane63(yacc[rb][0]);
+      if (lane == 63) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) red[wave][rb][0] = yacc[rb][0];
+      }
+      __syncthreads();
+      if (kw == 0 && lane < PB) {
+        float g = 0.f, u = 0.f;
+        for (int q = 0; q < KW; ++q) {
+          g += red[wave + q][lane][0];
+          u += red[wave + q][PB + lane][0];
+        }
+        if (r + lane < rowEnd) gate_store(r + lane, g, u);
+      }
+      __syncthreads();
+    }
+  };
 
   auto finish = [&](float (&yacc)[RB][MT], int r) {
     if constexpr (MT == 1 && multi_sum(KIND)) {
@@ -707,13 +798,26 @@ k_gemv(GemvArgs a) {
   };
 
   float yacc[RB][MT];
+  if constexpr (GATED) {
+    constexpr int PB = RB / 2;
+    for (int r = row0; r < rowStop; r += PB) {
+      if (KW == 1 && r >= rowEnd) break;
+      if (r != row0 && r < rowEnd)
+        load_batch<KIND, RB, CPL, 0, RB, true>(a, rqw, rqh, lane_cw, B0, r, rowEnd);
+      compute_batch<KIND, XBF16, MT, CPL, RB, XW, GP, true>(a, smem, B0, lane_meta, lane_step, row_base,
+                                                            row_base2, r - brow0, rowEnd - 1 - brow0,
+                                                            xq, xs, yacc);
+      finish_gated(yacc, r);
+    }
+    return;
+  }
   if constexpr (NB == 1) {
     // ---- one batch in flight at a time (normally a wave owns one batch)
     for (int r = row0; r < rowStop; r += RB) {
       if (KW == 1 && r >= rowEnd) break;
       if (r != row0 && r < rowEnd) load_batch<KIND, RB, CPL>(a, rqw, rqh, lane_cw, B0, r, rowEnd);
       compute_batch<KIND, XBF16, MT, CPL, RB, XW, GP>(a, smem, B0, lane_meta, lane_step, row_base,
-                                                      r - brow0, rowEnd - 1 - brow0, xq, xs, yacc);
+                                                      row_base2, r - brow0, rowEnd - 1 - brow0, xq, xs, yacc);
       finish(yacc, r);
     }
     return;
@@ -725,12 +829,12 @@ k_gemv(GemvArgs a) {
     if (KW == 1 && r >= rowEnd) break;
     if (r + RB < rowEnd) load_batch<KIND, RB, CPL>(a, rqw, rqh, lane_cw, B1, r + RB, rowEnd);
     compute_batch<KIND, XBF16, MT, CPL, RB, XW, GP>(a, smem, B0, lane_meta, lane_step, row_base,
-                                                    r - brow0, rowEnd - 1 - brow0, xq, xs, yacc);
+                                                    row_base2, r - brow0, rowEnd - 1 - brow0, xq, xs, yacc);
     finish(yacc, r);
     if (r + RB >= rowStop || (KW == 1 && r + RB >= rowEnd)) break;
     if (r + 2 * RB < rowEnd) load_batch<KIND, RB, CPL>(a, rqw, rqh, lane_cw, B0, r + 2 * RB, rowEnd);
     compute_batch<KIND, XBF16, MT, CPL, RB, XW, GP>(a, smem, B1, lane_meta, lane_step, row_base,
-                                                    r + RB - brow0, rowEnd - 1 - brow0, xq, xs, yacc);
+                                                    row_base2, r + RB - brow0, rowEnd - 1 - brow0, xq, xs, yacc);
     finish(yacc, r + RB);
   }
 }
@@ -776,6 +880,31 @@ GemvFn pick(int kind, bool xb, int mt, int cpl, int nb) {
     case K_AFF2H: return pick_x<K_AFF2H>(xb, mt, cpl, nb);
     case K_AFF4H: return pick_x<K_AFF4H>(xb, mt, cpl, nb);
     case K_AFF8H: return pick_x<K_AFF8H>(xb, mt, cpl, nb);
+  }
+  return nullptr;
+}
+
+template <int KIND, bool XB>
+GemvFn pick_gated(int cpl) {
+  switch (cpl) {
+    case 1: return k_gemv<KIND, XB, 1, 1, 1, true>;
+    case 2: return k_gemv<KIND, XB, 1, 2, 1, true>;
+    case 3: return k_gemv<KIND, XB, 1, 3, 1, true>;
+    case 4: return k_gemv<KIND, XB, 1, 4, 1, true>;
+  }
+  return nullptr;
+}
+GemvFn pick_gated(int kind, bool xb, int cpl) {
+  switch (kind) {
+    case K_AFF2: return xb ? pick_gated<K_AFF2, true>(cpl) : pick_gated<K_AFF2, false>(cpl);
+    case K_AFF4: return xb ? pick_gated<K_AFF4, true>(cpl) : pick_gated<K_AFF4, false>(cpl);
+    case K_AFF8: return xb ? pick_gated<K_AFF8, true>(cpl) : pick_gated<K_AFF8, false>(cpl);
+    case K_Q4K: return xb ? pick_gated<K_Q4K, true>(cpl) : pick_gated<K_Q4K, false>(cpl);
+    case K_Q6K: return xb ? pick_gated<K_Q6K, true>(cpl) : pick_gated<K_Q6K, false>(cpl);
+    case K_SYM4: return xb ? pick_gated<K_SYM4, true>(cpl) : pick_gated<K_SYM4, false>(cpl);
+    case K_AFF2H: return xb ? pick_gated<K_AFF2H, true>(cpl) : pick_gated<K_AFF2H, false>(cpl);
+    case K_AFF4H: return xb ? pick_gated<K_AFF4H, true>(cpl) : pick_gated<K_AFF4H, false>(cpl);
+    case K_AFF8H: return xb ? pick_gated<K_AFF8H, true>(cpl) : pick_gated<K_AFF8H, false>(cpl);
   }
   return nullptr;
 }
@@ -935,6 +1064,84 @@ hipError_t launch_gemv(const Desc& d, const void* x, int xdt, int64_t M, const B
   if (x_prep_in_lds(kind, mt)) lds += ((uint32_t)C * (16 + 1) * 4u + 15u) & ~15u;
   const unsigned mtiles = (unsigned)((M + mt - 1) / mt);
   hipLaunchKernelGGL(fn, dim3((unsigned)blocks, mtiles), dim3(256), lds, s, a);
+  return hipGetLastError();
+}
+
+bool gated_gemv_supported(const Desc& d) {
+  const int kind = gemv_kind(d);
+  int mt = 1, kw = 0, cpl = 0;
+  if (!gemv_plan(kind, gemv_chunks(d, kind), &mt, &kw, &cpl)) return false;
+  // both layers' metadata of one feature per wave and the activation row in LDS
+  uint32_t row[kMeta], off[kMeta];
+  meta_rows(d, true, row);
+  return 2 * meta_lds_bytes(row, 4 / kw, off) + 4 * d.K + 2048 + 34 * gemv_chunks(d, kind) * 4 <=
+         kMaxMetaLds + 64 * 1024;
+}
+
+hipError_t launch_gated_gemv(const Desc& d, const GatedArgs& g, const size_t bytes[5],
+                             hipStream_t s) {
+  const int kind = gemv_kind(d);
+  const int C = gemv_chunks(d, kind);
+  int mt = 1, KW = 1, cpl = 0;
+  if (g.M != 1 || g.gq || !gemv_plan(kind, C, &mt, &KW, &cpl)) return hipErrorInvalidValue;
+  GemvFn fn = pick_gated(kind, g.xdt == BF16, cpl);
+  if (!fn) return hipErrorInvalidValue;
+  const int RW = 4 / KW;
+  uint32_t row[kMeta];
+  meta_rows(d, true, row);
+  uint32_t rowMeta = 0;
+  for (int i = 0; i < kMeta; ++i) rowMeta += row[i];
+  // one batch of features per team while that keeps every CU at 16 waves or
+  // fewer, several in turn beyond; fewer where the staged metadata of both
+  // layers would not fit
+  const int pb = gated_feats(kind, cpl);
+  const int64_t teamsMax = (int64_t)kNumCU * QP_GEMV_MAX_WAVES_PER_CU / KW;
+  int64_t rpt = (d.N + teamsMax - 1) / teamsMax;
+  rpt = (rpt + pb - 1) / pb * pb;
+  const int64_t rptMeta = (int64_t)((kMaxMetaLds / 4) / ((uint64_t)RW * (rowMeta + 1)));
+  if (rpt > rptMeta) rpt = rptMeta > 0 ? rptMeta : 1;
+  auto pad16 = [](uint64_t n) { return (uint32_t)((n + 15) & ~uint64_t(15)); };
+  GemvArgs a{};
+  a.qw = static_cast<const uint32_t*>(g.gate.qweight);
+  a.qh = static_cast<const uint32_t*>(g.gate.qweight_hi);
+  a.meta[0] = g.gate.scales;
+  a.meta[1] = g.gate.zeros;
+  a.meta[2] = g.gate.steps;
+  a.meta[3] = g.bias_g;
+  a.qw2 = static_cast<const uint32_t*>(g.up.qweight);
+  a.qh2 = static_cast<const uint32_t*>(g.up.qweight_hi);
+  a.meta2[0] = g.up.scales;
+  a.meta2[1] = g.up.zeros;
+  a.meta2[2] = g.up.steps;
+  a.meta2[3] = g.bias_u;
+  a.bias_row[0] = g.bias_g ? 2 : 0;
+  a.bias_row[1] = g.bias_u ? 2 : 0;
+  a.act = g.act;
+  a.x = static_cast<const uint16_t*>(g.x);
+  a.y = g.h;
+  a.N = d.N;
+  a.K = d.K;
+  a.M = 1;
+  a.C = C;
+  a.gs = d.gs;
+  a.ydt = g.hdt;
+  a.KW = KW;
+  a.RPT = (int)rpt;
+  a.qw_bytes = (uint32_t)bytes[0];
+  a.qh_bytes = (uint32_t)bytes[1];
+  a.x_bytes = (uint32_t)(d.K * 2);
+  for (int i = 0; i < 3; ++i) a.meta_bytes[i] = pad16(bytes[2 + i]);
+  a.meta_bytes[3] = pad16((uint64_t)d.N * 2);
+  for (int i = 0; i < kMeta; ++i) a.meta_row[i] = row[i];
+  uint32_t lds = meta_lds_bytes(row, (int64_t)RW * rpt, a.meta_lds);
+  for (int i = 0; i < kMeta; ++i) a.meta_lds2[i] = a.meta_lds[i] + lds;
+  lds *= 2;
+  a.x_lds = lds;
+  lds += (uint32_t)(((15 + 2 * d.K) + 1023) / 1024 * 1024);
+  a.x_prep = lds;
+  if (x_prep_in_lds(kind, 1)) lds += ((uint32_t)C * (16 + 1) * 4u + 15u) & ~15u;
+  const int64_t teams = (d.N + rpt - 1) / rpt;
+  hipLaunchKernelGGL(fn, dim3((unsigned)((teams + RW - 1) / RW)), dim3(256), lds, s, a);
   return hipGetLastError();
 }
 

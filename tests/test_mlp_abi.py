@@ -100,6 +100,7 @@ def test_gated_refusals(q):
         (dict(ck=(FAKE, FAKE, FAKE + 4, FAKE)), 4, "up_codes"), (dict(M=17, ws=FAKE + 4, n=1 << 30), 4, "workspace"),
         (dict(M=17), 1, "workspace is NULL"), (dict(M=17, ws=FAKE, n=16), 1, "too small"),
         (dict(ck=(FAKE,) * 4), 1, "workspace is NULL"), (dict(d=D.affine(64, 96, 4, 32)), 1, "workspace is NULL"),
+        (dict(M=1, ck=(FAKE,) * 4), 1, "workspace is NULL"),
         (dict(g=q._Weights(FAKE, None, None, FAKE, None)), 1, "scales"),
         (dict(u=q._Weights(FAKE + 4, None, FAKE, FAKE, None)), 4, "qweight"),
     ]:
