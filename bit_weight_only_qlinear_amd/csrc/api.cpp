@@ -696,8 +696,8 @@ qp_status check_workspace(const void* ws, size_t have, size_t need) {
 
 // Which form of the gated pair a call takes.  With checkpoints, or above 16
 // rows (one MFMA tile), or with a buffer of 2 GiB, the staged product; one row
-// streams the codes (int4 affine, 4096 -> 2 x 14336: @G1@ us, @S1@ as an MFMA
-// tile), 2 .. 16 rows the MFMA tile on exact codes.
+// (two in some formats) streams the codes (int4 affine, 4096 -> 2 x 14336:
+// 14.9 us, 21.9 as an MFMA tile), up to 16 rows the MFMA tile on exact codes.
 enum GatedForm { GATED_GEMV, GATED_SKINNY, GATED_STAGED };
 GatedForm gated_form(const qp::Desc& d, int64_t M, bool save) {
   size_t b[5];
@@ -705,7 +705,7 @@ GatedForm gated_form(const qp::Desc& d, int64_t M, bool save) {
   bool small_bufs = (size_t)M * (size_t)d.K * 2 < (size_t(1) << 31);
   for (int i = 0; i < 5; ++i) small_bufs = small_bufs && b[i] < (size_t(1) << 31);
   if (save || !small_bufs || M > 16) return GATED_STAGED;
-  if (M == 1 && qp::gated_gemv_supported(d)) return GATED_GEMV;
+  if (qp::gated_gemv_supported(d, M)) return GATED_GEMV;
   return qp::skinny_supported(d) ? GATED_SKINNY : GATED_STAGED;
 }
 

@@ -223,9 +223,9 @@ __host__ __device__ constexpr int row_batch(int kind, int mt, int cpl, int nb) {
 }
 
 // GATED batches hold PB features: the first layer's rows, then the second's.
-__host__ __device__ constexpr int gated_feats(int kind, int cpl) {
-  const int n = (single_loads(kind) + 2) / (2 * cpl);
-  return n > 4 ? 4 : n > 0 ? n : 1;
+__host__ __device__ constexpr int gated_feats(int kind, int mt, int cpl) {
+  const int n = (single_loads(kind) + 2) / (2 * cpl), most = mt == 1 ? 4 : 2;
+  return n > most ? most : n > 0 ? n : 1;
 }
 
 // Raw code words of one batch of RB rows.
@@ -506,15 +506,15 @@ __device__ __forceinline__ uint32_t stage_meta(uint8_t* smem, __amdgpu_buffer_rs
   return src0 - a0;
 }
 
-// GATED (one activation row, single batches): h = act(g) u of two layers; a
+// GATED (one or two activation rows, single batches): h = act(g) u of two layers; a
 // wave owns features, i.e. pairs of rows, whose two sums meet in its lanes.
 template <int KIND, bool XBF16, int MT, int CPL, int NB, bool GATED = false>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(QP_GEMV_MIN_WAVES_PER_EU)))
 k_gemv(GemvArgs a) {
-  static_assert(!GATED || (MT == 1 && NB == 1), "the gated pair: one activation row");
+  static_assert(!GATED || (MT <= 2 && NB == 1), "the gated pair: one or two activation rows");
   using T = KT<KIND>;
   constexpr int CC = T::CC, XW = T::XW, GP = T::GP;
-  constexpr int RB = GATED ? 2 * gated_feats(KIND, CPL) : row_batch(KIND, MT, CPL, NB);
+  constexpr int RB = GATED ? 2 * gated_feats(KIND, MT, CPL) : row_batch(KIND, MT, CPL, NB);
   constexpr int NV = CC / 8;   // 16-byte loads of x per chunk
 
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -692,42 +692,50 @@ k_gemv(GemvArgs a) {
     }
   }
 
-  // the gated pair's last step for one feature
-  auto gate_store = [&](int n, float g, float u) {
+  // the gated pair's last step for one feature of activation row m
+  auto gate_store = [&](int n, int m, float g, float u) {
     if (a.bias_row[0]) g += xval<XBF16>(lds_read<uint16_t>(smem, row_base[3] + 2u * (uint32_t)(n - brow0)));
     if (a.bias_row[1]) u += xval<XBF16>(lds_read<uint16_t>(smem, row_base2[3] + 2u * (uint32_t)(n - brow0)));
-    store_y(a.y, n, (a.act == ACT_SILU ? act_f<ACT_SILU>(g) : act_f<ACT_GELU_TANH>(g)) * u, a.ydt);
+    store_y(a.y, (int64_t)m * a.N + n,
+            (a.act == ACT_SILU ? act_f<ACT_SILU>(g) : act_f<ACT_GELU_TANH>(g)) * u, a.ydt);
   };
   auto finish_gated = [&](float (&yacc)[RB][MT], int r) {
     constexpr int PB = RB / 2;
+    static_assert(!GATED || PB * MT <= 4, "eight values of the transposed reduction");
     if (KW == 1) {
       // gates as values 0 .. 3, ups as 4 .. 7 of the transposed reduction: a
       // feature's two sums end 8 lanes apart
       float v[8];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        v[p] = p < PB ? yacc[p < PB ? p : 0][0] : 0.f;
-        v[4 + p] = p < PB ? yacc[PB + (p < PB ? p : 0)][0] : 0.f;
+        const bool on = p < PB * MT;
+        v[p] = on ? yacc[on ? p / MT : 0][p % MT] : 0.f;
+        v[4 + p] = on ? yacc[PB + (on ? p / MT : 0)][p % MT] : 0.f;
       }
       const float t = wave_sums8<8>(v, lane);
       const float u = dpp_f<QP_DPP_ROW_ROR8>(0.f, t);
-      const int R = lane >> 4, p = ((R & 1) << 1) | (R >> 1), n = r + p;
-      if ((lane & 15) == 0 && p < PB && n < rowEnd) gate_store(n, t, u);
+      const int R = lane >> 4, p = ((R & 1) << 1) | (R >> 1), n = r + p / MT;
+      if ((lane & 15) == 0 && p < PB * MT && n < rowEnd && p % MT < a.M) gate_store(n, p % MT, t, u);
     } else {
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) yacc[rb][0] = wave_sum_lane63(yacc[rb][0]);
+      for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) yacc[rb][m] = wave_sum_lane63(yacc[rb][m]);
       if (lane == 63) {
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) red[wave][rb][0] = yacc[rb][0];
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) red[wave][rb][m] = yacc[rb][m];
       }
       __syncthreads();
-      if (kw == 0 && lane < PB) {
+      if (kw == 0 && lane < PB * MT) {
+        const int p = lane / MT, m = lane % MT;
         float g = 0.f, u = 0.f;
         for (int q = 0; q < KW; ++q) {
-          g += red[wave + q][lane][0];
-          u += red[wave + q][PB + lane][0];
+          g += red[wave + q][p][m];
+          u += red[wave + q][PB + p][m];
         }
-        if (r + lane < rowEnd) gate_store(r + lane, g, u);
+        if (r + p < rowEnd && m < a.M) gate_store(r + p, m, g, u);
       }
       __syncthreads();
     }
@@ -885,26 +893,31 @@ GemvFn pick(int kind, bool xb, int mt, int cpl, int nb) {
 }
 
 template <int KIND, bool XB>
-GemvFn pick_gated(int cpl) {
-  switch (cpl) {
-    case 1: return k_gemv<KIND, XB, 1, 1, 1, true>;
-    case 2: return k_gemv<KIND, XB, 1, 2, 1, true>;
-    case 3: return k_gemv<KIND, XB, 1, 3, 1, true>;
-    case 4: return k_gemv<KIND, XB, 1, 4, 1, true>;
-  }
-  return nullptr;
+GemvFn pick_gated(int mt, int cpl) {
+  if (mt == 2)   // the formats that take it: see gated_gemv_supported
+    return base_kind(KIND) != K_AFF8 && base_kind(KIND) != K_Q4K && base_kind(KIND) != K_Q6K ? nullptr
+         : cpl == 1 ? k_gemv<KIND, XB, 2, 1, 1, true>
+         : cpl == 2 ? k_gemv<KIND, XB, 2, 2, 1, true>
+         : cpl == 3 ? k_gemv<KIND, XB, 2, 3, 1, true> : k_gemv<KIND, XB, 2, 4, 1, true>;
+  return cpl == 1 ? k_gemv<KIND, XB, 1, 1, 1, true>
+       : cpl == 2 ? k_gemv<KIND, XB, 1, 2, 1, true>
+       : cpl == 3 ? k_gemv<KIND, XB, 1, 3, 1, true> : k_gemv<KIND, XB, 1, 4, 1, true>;
 }
-GemvFn pick_gated(int kind, bool xb, int cpl) {
+template <int KIND>
+GemvFn pick_gated(bool xb, int mt, int cpl) {
+  return xb ? pick_gated<KIND, true>(mt, cpl) : pick_gated<KIND, false>(mt, cpl);
+}
+GemvFn pick_gated(int kind, bool xb, int mt, int cpl) {
   switch (kind) {
-    case K_AFF2: return xb ? pick_gated<K_AFF2, true>(cpl) : pick_gated<K_AFF2, false>(cpl);
-    case K_AFF4: return xb ? pick_gated<K_AFF4, true>(cpl) : pick_gated<K_AFF4, false>(cpl);
-    case K_AFF8: return xb ? pick_gated<K_AFF8, true>(cpl) : pick_gated<K_AFF8, false>(cpl);
-    case K_Q4K: return xb ? pick_gated<K_Q4K, true>(cpl) : pick_gated<K_Q4K, false>(cpl);
-    case K_Q6K: return xb ? pick_gated<K_Q6K, true>(cpl) : pick_gated<K_Q6K, false>(cpl);
-    case K_SYM4: return xb ? pick_gated<K_SYM4, true>(cpl) : pick_gated<K_SYM4, false>(cpl);
-    case K_AFF2H: return xb ? pick_gated<K_AFF2H, true>(cpl) : pick_gated<K_AFF2H, false>(cpl);
-    case K_AFF4H: return xb ? pick_gated<K_AFF4H, true>(cpl) : pick_gated<K_AFF4H, false>(cpl);
-    case K_AFF8H: return xb ? pick_gated<K_AFF8H, true>(cpl) : pick_gated<K_AFF8H, false>(cpl);
+    case K_AFF2: return pick_gated<K_AFF2>(xb, mt, cpl);
+    case K_AFF4: return pick_gated<K_AFF4>(xb, mt, cpl);
+    case K_AFF8: return pick_gated<K_AFF8>(xb, mt, cpl);
+    case K_Q4K: return pick_gated<K_Q4K>(xb, mt, cpl);
+    case K_Q6K: return pick_gated<K_Q6K>(xb, mt, cpl);
+    case K_SYM4: return pick_gated<K_SYM4>(xb, mt, cpl);
+    case K_AFF2H: return pick_gated<K_AFF2H>(xb, mt, cpl);
+    case K_AFF4H: return pick_gated<K_AFF4H>(xb, mt, cpl);
+    case K_AFF8H: return pick_gated<K_AFF8H>(xb, mt, cpl);
   }
   return nullptr;
 }
@@ -1067,10 +1080,15 @@ hipError_t launch_gemv(const Desc& d, const void* x, int xdt, int64_t M, const B
   return hipGetLastError();
 }
 
-bool gated_gemv_supported(const Desc& d) {
-  const int kind = gemv_kind(d);
-  int mt = 1, kw = 0, cpl = 0;
-  if (!gemv_plan(kind, gemv_chunks(d, kind), &mt, &kw, &cpl)) return false;
+// One activation row: every format.  Two: the formats whose streaming kernel
+// still beats an MFMA tile there (us a pair, in a
+// HIP graph: int8 affine 4096 -> 14336 27.0 against 35.5, Q4K 5120 -> 25600
+// 44.3 against 59.3, Q6K 8192 -> 8192 28.8 against 39.6).
+bool gated_gemv_supported(const Desc& d, int64_t M) {
+  const int kind = gemv_kind(d), bk = base_kind(kind);
+  if (M != 1 && !(M == 2 && (bk == K_AFF8 || bk == K_Q4K || bk == K_Q6K))) return false;
+  int mt = (int)M, kw = 0, cpl = 0;
+  if (!gemv_plan(kind, gemv_chunks(d, kind), &mt, &kw, &cpl) || mt != M) return false;
   // both layers' metadata of one feature per wave and the activation row in LDS
   uint32_t row[kMeta], off[kMeta];
   meta_rows(d, true, row);
@@ -1082,9 +1100,10 @@ hipError_t launch_gated_gemv(const Desc& d, const GatedArgs& g, const size_t byt
                              hipStream_t s) {
   const int kind = gemv_kind(d);
   const int C = gemv_chunks(d, kind);
-  int mt = 1, KW = 1, cpl = 0;
-  if (g.M != 1 || g.gq || !gemv_plan(kind, C, &mt, &KW, &cpl)) return hipErrorInvalidValue;
-  GemvFn fn = pick_gated(kind, g.xdt == BF16, cpl);
+  int mt = (int)g.M, KW = 1, cpl = 0;
+  if (g.gq || !gated_gemv_supported(d, g.M) || !gemv_plan(kind, C, &mt, &KW, &cpl))
+    return hipErrorInvalidValue;
+  GemvFn fn = pick_gated(kind, g.xdt == BF16, mt, cpl);
   if (!fn) return hipErrorInvalidValue;
   const int RW = 4 / KW;
   uint32_t row[kMeta];
@@ -1094,7 +1113,7 @@ hipError_t launch_gated_gemv(const Desc& d, const GatedArgs& g, const size_t byt
   // one batch of features per team while that keeps every CU at 16 waves or
   // fewer, several in turn beyond; fewer where the staged metadata of both
   // layers would not fit
-  const int pb = gated_feats(kind, cpl);
+  const int pb = gated_feats(kind, mt, cpl);
   const int64_t teamsMax = (int64_t)kNumCU * QP_GEMV_MAX_WAVES_PER_CU / KW;
   int64_t rpt = (d.N + teamsMax - 1) / teamsMax;
   rpt = (rpt + pb - 1) / pb * pb;
@@ -1121,7 +1140,7 @@ hipError_t launch_gated_gemv(const Desc& d, const GatedArgs& g, const size_t byt
   a.y = g.h;
   a.N = d.N;
   a.K = d.K;
-  a.M = 1;
+  a.M = g.M;
   a.C = C;
   a.gs = d.gs;
   a.ydt = g.hdt;
@@ -1129,7 +1148,7 @@ hipError_t launch_gated_gemv(const Desc& d, const GatedArgs& g, const size_t byt
   a.RPT = (int)rpt;
   a.qw_bytes = (uint32_t)bytes[0];
   a.qh_bytes = (uint32_t)bytes[1];
-  a.x_bytes = (uint32_t)(d.K * 2);
+  a.x_bytes = (uint32_t)(g.M * d.K * 2);
   for (int i = 0; i < 3; ++i) a.meta_bytes[i] = pad16(bytes[2 + i]);
   a.meta_bytes[3] = pad16((uint64_t)d.N * 2);
   for (int i = 0; i < kMeta; ++i) a.meta_row[i] = row[i];
@@ -1137,9 +1156,9 @@ hipError_t launch_gated_gemv(const Desc& d, const GatedArgs& g, const size_t byt
   for (int i = 0; i < kMeta; ++i) a.meta_lds2[i] = a.meta_lds[i] + lds;
   lds *= 2;
   a.x_lds = lds;
-  lds += (uint32_t)(((15 + 2 * d.K) + 1023) / 1024 * 1024);
+  if (mt == 1) lds += (uint32_t)(((15 + 2 * d.K) + 1023) / 1024 * 1024);
   a.x_prep = lds;
-  if (x_prep_in_lds(kind, 1)) lds += ((uint32_t)C * (16 + 1) * 4u + 15u) & ~15u;
+  if (x_prep_in_lds(kind, mt)) lds += ((uint32_t)C * (16 + 1) * 4u + 15u) & ~15u;
   const int64_t teams = (d.N + rpt - 1) / rpt;
   hipLaunchKernelGGL(fn, dim3((unsigned)((teams + RW - 1) / RW)), dim3(256), lds, s, a);
   return hipGetLastError();

@@ -60,28 +60,63 @@ __device__ __forceinline__ uint32_t pack4i(const int (&q)[8], int o) {
          (((uint32_t)q[o + 2] & 255u) << 16) | ((uint32_t)q[o + 3] << 24);
 }
 
-__device__ __forceinline__ double shfl_xor_d(double v, int off) {
+// p[c] where ok, else 0: the load itself is unconditional (p[0] is always
+// there), so that a thread's loads go out together, without branches.
+__device__ __forceinline__ uint4 ldz(const uint4* p, uint32_t c, bool ok) {
+  const uint4 v = p[ok ? c : 0u];
+  return make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
+}
+__device__ __forceinline__ uint2 ldz(const uint2* p, uint32_t c, bool ok) {
+  const uint2 v = p[ok ? c : 0u];
+  return make_uint2(ok ? v.x : 0u, ok ? v.y : 0u);
+}
+
+// v plus its neighbour by a DPP control; lanes without one add 0.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_add(double v) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)u, off, 64);
-  const uint32_t hi = (uint32_t)__shfl_xor((int)(uint32_t)(u >> 32), off, 64);
-  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROW_MASK, 0xF, false);
+  const uint32_t hi =
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROW_MASK, 0xF, false);
+  return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// Sum over the wave, in lane 63.
+__device__ __forceinline__ double wave_sum_d63(double v) {
+  v = dpp_add<QP_DPP_QUAD_1032, 0xF>(v);
+  v = dpp_add<QP_DPP_QUAD_2301, 0xF>(v);
+  v = dpp_add<QP_DPP_ROW_ROR4, 0xF>(v);
+  v = dpp_add<QP_DPP_ROW_ROR8, 0xF>(v);
+  v = dpp_add<QP_DPP_ROW_BCAST15, 0xA>(v);
+  return dpp_add<QP_DPP_ROW_BCAST31, 0xC>(v);
+}
+// Maximum of values >= 0 over the wave, in lane 63.
+__device__ __forceinline__ float wave_max63(float v) {
+  v = fmaxf(v, dpp_f<QP_DPP_QUAD_1032>(0.f, v));
+  v = fmaxf(v, dpp_f<QP_DPP_QUAD_2301>(0.f, v));
+  v = fmaxf(v, dpp_f<QP_DPP_ROW_ROR4>(0.f, v));
+  v = fmaxf(v, dpp_f<QP_DPP_ROW_ROR8>(0.f, v));
+  v = fmaxf(v, dpp_f<QP_DPP_ROW_BCAST15, 0xA>(0.f, v));
+  return fmaxf(v, dpp_f<QP_DPP_ROW_BCAST31, 0xC>(0.f, v));
 }
 
 // Sum and maximum over the TPR threads of a row (a multiple of 64); every
 // thread gets both.  red: one slot per wave of the block.
-template <int TPR>
+template <int TPR, bool MAX = true>
 __device__ __forceinline__ void row_reduce(double& sum, float& mx, double* red_s, float* red_m) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    sum += shfl_xor_d(sum, off);
-    mx = fmaxf(mx, __shfl_xor(mx, off, 64));
-  }
-  if constexpr (TPR > 64) {
+  sum = wave_sum_d63(sum);
+  if constexpr (MAX) mx = wave_max63(mx);
+  if constexpr (TPR == 64) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, sum);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    sum = __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+    mx = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mx), 63));
+  } else {
     const int wave = threadIdx.x >> 6, w0 = wave / (TPR / 64) * (TPR / 64);
     __syncthreads();   // a row before may still read the slots
-    if ((threadIdx.x & 63) == 0) {
+    if ((threadIdx.x & 63) == 63) {
       red_s[wave] = sum;
-      red_m[wave] = mx;
+      if constexpr (MAX) red_m[wave] = mx;
     }
     __syncthreads();
     sum = 0.;
@@ -89,7 +124,7 @@ __device__ __forceinline__ void row_reduce(double& sum, float& mx, double* red_s
 #pragma unroll
     for (int i = 0; i < TPR / 64; ++i) {   // the same order in every thread
       sum += red_s[w0 + i];
-      mx = fmaxf(mx, red_m[w0 + i]);
+      if constexpr (MAX) mx = fmaxf(mx, red_m[w0 + i]);
     }
   }
 }
@@ -220,10 +255,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm(NormArgs a) {
 // Any K: scalar columns, two passes over the row.  s is written in the
 // second pass only, after the thread has read the same element of x and r,
 // so it may be either of them.
+constexpr int kAny = 1024;   // threads of the general forms: a few columns each, for latency
+
 template <bool BF>
-__global__ void __launch_bounds__(256) k_norm_any(NormArgs a) {
-  __shared__ double red_s[4];
-  __shared__ float red_m[4];
+__global__ void __launch_bounds__(kAny) k_norm_any(NormArgs a) {
+  __shared__ double red_s[kAny / 64];
+  __shared__ float red_m[kAny / 64];
   const int64_t row = blockIdx.x, base = row * a.K;
   auto stream = [&](int64_t k) {
     uint32_t b = a.x[base + k];
@@ -233,12 +270,13 @@ __global__ void __launch_bounds__(256) k_norm_any(NormArgs a) {
   auto weight = [&](int64_t k) { return a.w ? val16<BF>(a.w[k]) : 1.f; };
   double sum = 0.;
   float mx = 0.f;
-  for (int64_t k = threadIdx.x; k < a.K; k += 256) {
+#pragma unroll 4
+  for (int64_t k = threadIdx.x; k < a.K; k += kAny) {
     const float v = val16<BF>(stream(k));
     sum = fma((double)v, (double)v, sum);
     mx = fmaxf(mx, fabsf(v * weight(k)));
   }
-  row_reduce<256>(sum, mx, red_s, red_m);
+  row_reduce<kAny>(sum, mx, red_s, red_m);
   const double rstd = 1. / sqrt(sum / (double)a.K + (double)a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = (float)rstd;
   float ys;
@@ -246,7 +284,8 @@ __global__ void __launch_bounds__(256) k_norm_any(NormArgs a) {
   q8_scale(mx, rstd, ys, mul);
   if (a.yq && threadIdx.x == 0) a.ys[row] = ys;
   const float rs = (float)rstd;
-  for (int64_t k = threadIdx.x; k < a.K; k += 256) {
+#pragma unroll 4
+  for (int64_t k = threadIdx.x; k < a.K; k += kAny) {
     const uint32_t b = stream(k);
     const float p = val16<BF>(b) * weight(k);
     if (a.r && a.s) a.s[base + k] = (uint16_t)b;
@@ -268,93 +307,116 @@ struct NormBwdArgs {
   int64_t M, K;
 };
 
+// One thread's share of a row: dy, the stream (raw, or codes in x, y and the
+// scale's bits in z) and ds_in.
+template <int NU>
+struct BwdRow {
+  uint4 d[NU], s[NU], di[NU];
+  float rs;
+};
+
+template <bool CK, int NT, int NU>
+__device__ __forceinline__ void load_row(const NormBwdArgs& a, int64_t row, uint32_t nq, int64_t ng,
+                                         BwdRow<NU>& r) {
+  const int64_t base = row * a.K;
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const uint32_t c = threadIdx.x + NT * i;
+    const bool ok = c < nq;
+    r.d[i] = ldz(reinterpret_cast<const uint4*>(a.dy + base), c, ok);
+    if constexpr (CK) {
+      const uint2 q = ldz(reinterpret_cast<const uint2*>(a.sq + base), c, ok);
+      const float sc = a.ss[row * ng + (ok ? c / 8 : 0u)];
+      r.s[i] = make_uint4(q.x, q.y, __float_as_uint(sc), 0);
+    } else {
+      r.s[i] = ldz(reinterpret_cast<const uint4*>(a.s + base), c, ok);
+    }
+    r.di[i] = make_uint4(0, 0, 0, 0);
+    if (a.ds_in) r.di[i] = ldz(reinterpret_cast<const uint4*>(a.ds_in + base), c, ok);
+  }
+  r.rs = a.rstd[row];
+}
+
 // Rows blockIdx.x, + gridDim.x, ...: ds of each, and the rows' share of dw
-// in registers (NU * 8 columns per thread).  K % 8 == 0, K <= 8 NT NU.
+// in registers (NU * 8 columns per thread).  The next row is on its way
+// while one is reduced and written (up to 512 threads: both fit the
+// registers).  K % 8 == 0, K <= 8 NT NU.  ds may be ds_in or dy: a row's elements are read
+// by the thread that writes them, before it does.
 template <bool BF, bool CK, int NT, int NU>
 __global__ void __launch_bounds__(NT) k_norm_bwd(NormBwdArgs a) {
   __shared__ double red_s[NT / 64];
-  __shared__ float red_m[NT / 64];
-  const int t = threadIdx.x;
   const uint32_t nq = (uint32_t)(a.K / 8);
   const int64_t ng = (a.K + 63) / 64;
   const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
-  const uint4 Z = make_uint4(0, 0, 0, 0);
   uint4 w[NU];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const uint32_t c = t + NT * i;
-    w[i] = a.w && c < nq ? reinterpret_cast<const uint4*>(a.w)[c] : make_uint4(one, one, one, one);
+    const uint32_t c = threadIdx.x + NT * i;
+    w[i] = make_uint4(one, one, one, one);
+    if (a.w) w[i] = ldz(reinterpret_cast<const uint4*>(a.w), c, c < nq);
   }
   float dw[NU][8];
 #pragma unroll
   for (int i = 0; i < NU; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+  constexpr bool AHEAD = NT <= 512;
+  BwdRow<NU> r, nx;
+  if (AHEAD) load_row<CK, NT, NU>(a, blockIdx.x, nq, ng, nx);
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
-    const int64_t base = row * a.K;
-    uint4 d[NU], di[NU];
-    uint4 s[NU];       // raw stream, or codes (x, y) and scale bits (z)
-#pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      const uint32_t c = t + NT * i;
-      const bool ok = c < nq;
-      d[i] = ok ? reinterpret_cast<const uint4*>(a.dy + base)[c] : Z;
-      if constexpr (CK) {
-        const uint2 q = ok ? reinterpret_cast<const uint2*>(a.sq + base)[c] : make_uint2(0, 0);
-        const float sc = ok ? a.ss[row * ng + c / 8] : 0.f;
-        s[i] = make_uint4(q.x, q.y, __float_as_uint(sc), 0);
-      } else {
-        s[i] = ok ? reinterpret_cast<const uint4*>(a.s + base)[c] : Z;
-      }
-      di[i] = ok && a.ds_in ? reinterpret_cast<const uint4*>(a.ds_in + base)[c] : Z;
+    if constexpr (AHEAD) {
+      r = nx;
+      if (row + gridDim.x < a.M) load_row<CK, NT, NU>(a, row + gridDim.x, nq, ng, nx);
+    } else {
+      load_row<CK, NT, NU>(a, row, nq, ng, r);
     }
-    auto stream = [&](int i, float (&v)[8]) {
+    auto stream = [&](int i, float (&v)[8]) __attribute__((always_inline)) {   // xh
       if constexpr (CK) {
-        unpack8i(make_uint2(s[i].x, s[i].y), v);
+        unpack8i(make_uint2(r.s[i].x, r.s[i].y), v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= __uint_as_float(s[i].z);
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * __uint_as_float(r.s[i].z) * r.rs;
       } else {
-        unpack8<BF>(s[i], v);
+        unpack8<BF>(r.s[i], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= r.rs;
       }
     };
-    const float rs = a.rstd[row];
     double dot = 0.;
     float none = 0.f;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       float v[8], g[8], b[8];
       stream(i, v);
-      unpack8<BF>(d[i], g);
+      unpack8<BF>(r.d[i], g);
       unpack8<BF>(w[i], b);
       float part = 0.f;   // 8 products in fp32, then fp64
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float xh = v[e] * rs;
-        part = fmaf(g[e] * b[e], xh, part);
-        dw[i][e] = fmaf(g[e], xh, dw[i][e]);
+        part = fmaf(g[e] * b[e], v[e], part);
+        dw[i][e] = fmaf(g[e], v[e], dw[i][e]);
       }
       dot += part;
     }
     if (!a.ds) continue;   // uniform
-    row_reduce<NT>(dot, none, red_s, red_m);
+    row_reduce<NT, false>(dot, none, red_s, nullptr);
     const float c1 = (float)(dot / (double)a.K);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const uint32_t c = t + NT * i;
+      const uint32_t c = threadIdx.x + NT * i;
       float v[8], g[8], b[8], z[8];
       stream(i, v);
-      unpack8<BF>(d[i], g);
+      unpack8<BF>(r.d[i], g);
       unpack8<BF>(w[i], b);
-      unpack8<BF>(di[i], z);
+      unpack8<BF>(r.di[i], z);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = fmaf(rs, fmaf(-v[e] * rs, c1, g[e] * b[e]), z[e]);
-      if (c < nq) reinterpret_cast<uint4*>(a.ds + base)[c] = pack8<BF>(z);
+      for (int e = 0; e < 8; ++e) z[e] = fmaf(r.rs, fmaf(-v[e], c1, g[e] * b[e]), z[e]);
+      if (c < nq) reinterpret_cast<uint4*>(a.ds + row * a.K)[c] = pack8<BF>(z);
     }
   }
   if (a.part) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const uint32_t c = t + NT * i;
+      const uint32_t c = threadIdx.x + NT * i;
       if (c < nq) {
         float4* p = reinterpret_cast<float4*>(a.part + (int64_t)blockIdx.x * a.K) + 2 * c;
         p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
@@ -374,19 +436,20 @@ __device__ __forceinline__ float stream_at(const NormBwdArgs& a, int64_t row, in
 
 // Any K: ds of one row per block, scalar columns.
 template <bool BF, bool CK>
-__global__ void __launch_bounds__(256) k_norm_bwd_any(NormBwdArgs a) {
-  __shared__ double red_s[4];
-  __shared__ float red_m[4];
+__global__ void __launch_bounds__(kAny) k_norm_bwd_any(NormBwdArgs a) {
+  __shared__ double red_s[kAny / 64];
   const int64_t row = blockIdx.x, base = row * a.K;
   const float rs = a.rstd[row];
   auto weight = [&](int64_t k) { return a.w ? val16<BF>(a.w[k]) : 1.f; };
   double dot = 0.;
   float none = 0.f;
-  for (int64_t k = threadIdx.x; k < a.K; k += 256)
+#pragma unroll 4
+  for (int64_t k = threadIdx.x; k < a.K; k += kAny)
     dot += (double)(val16<BF>(a.dy[base + k]) * weight(k) * (stream_at<BF, CK>(a, row, k) * rs));
-  row_reduce<256>(dot, none, red_s, red_m);
+  row_reduce<kAny, false>(dot, none, red_s, nullptr);
   const float c1 = (float)(dot / (double)a.K);
-  for (int64_t k = threadIdx.x; k < a.K; k += 256) {
+#pragma unroll 4
+  for (int64_t k = threadIdx.x; k < a.K; k += kAny) {
     const float z = a.ds_in ? val16<BF>(a.ds_in[base + k]) : 0.f;
     const float g = val16<BF>(a.dy[base + k]) * weight(k);
     a.ds[base + k] =
@@ -405,80 +468,127 @@ __global__ void __launch_bounds__(256) k_norm_dw_any(NormBwdArgs a) {
   a.part[(int64_t)blockIdx.y * a.K + k] = v;
 }
 
-// dw[k] = sum of the P partial rows, in fp64 and a fixed order: 64 columns
-// per block, 16 waves taking every 16th row.
+// dw[k] = sum of the P partial rows, in fp64 and a fixed order: 32 columns
+// per block, 32 half waves taking every 32nd row.
 __global__ void __launch_bounds__(1024) k_col_sum(const float* __restrict__ part, int P, int64_t K,
                                                   float* __restrict__ out) {
-  __shared__ double red[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t k = (int64_t)blockIdx.x * 64 + lane;
+  __shared__ double red[32][33];
+  const int c = threadIdx.x & 31, h = threadIdx.x >> 5;
+  const int64_t k = (int64_t)blockIdx.x * 32 + c;
   double v = 0.;
   if (k < K) {
 #pragma unroll 8
-    for (int p = wave; p < P; p += 16) v += (double)part[(int64_t)p * K + k];
+    for (int p = h; p < P; p += 32) v += (double)part[(int64_t)p * K + k];
   }
-  red[wave][lane] = v;
+  red[h][c] = v;
   __syncthreads();
-  if (wave == 0 && k < K) {
+  if (h == 0 && k < K) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) v += red[i][lane];
+    for (int i = 1; i < 32; ++i) v += red[i][c];
     out[k] = (float)v;
   }
 }
 
-// Code of v under a positive scale: the quotient from the reciprocal in fp64
-// with one correction step, exact where v / scale is a tie, so that ties go
-// to even as the definition says.
-__device__ __forceinline__ int ckpt_code(float v, double sc, double inv) {
-  double q = (double)v * inv;
-  q = fma(fma(-q, sc, (double)v), inv, q);
-  const int c = (int)rint(q);
-  return c > 127 ? 127 : c < -127 ? -127 : c;
+// fl32(m / 127): the product with the reciprocal and one correction step,
+// correctly rounded away from the subnormals.
+__device__ __forceinline__ float scale127(float m) {
+  if (m < 1e-30f) return m / 127.f;
+  constexpr float r = 1.f / 127.f;
+  const float q = m * r;
+  return fmaf(fmaf(-q, 127.f, m), r, q);
 }
 
-// 8 lanes per group of 64 columns, 8 columns per lane (K % 8 == 0).  `n`
-// threads in all: rows of ng groups, the last one possibly short.
-template <bool BF>
+// Codes of a lane's values under a scale, as bytes: rint of the exact
+// quotient.  fma(v, 1 / scale, 1.5 2^23) rounds the product to an integer in
+// its low bits; the product is within 4e-5 of the quotient (127 steps, 2^-23
+// from the reciprocal and 2^-24 more), so only a value whose product is that
+// near to a tie needs the fp64 quotient (about one wave in ten has one): with
+// one correction step that is exact at a tie, which then goes to even.
+template <int N>
+__device__ __forceinline__ void ckpt_codes(const float (&v)[N], float sc, uint32_t (&c)[N]) {
+  constexpr float magic = 12582912.f;
+  const float inv = sc > 0.f ? __builtin_amdgcn_rcpf(sc) : 0.f;
+  float off = inv > 1e38f ? 1.f : 0.f;   // an infinite or subnormal reciprocal: fp64 too
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float t = fmaf(v[e], inv, magic);
+    off = fmaxf(off, fabsf(fmaf(v[e], inv, magic - t)));
+    c[e] = __float_as_uint(t);
+  }
+  if (off > 0.4999f) {
+    const double ds = sc, di = 1. / ds;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      double q = (double)v[e] * di;
+      q = fma(fma(-q, ds, (double)v[e]), di, q);
+      c[e] = (uint32_t)(int)fmin(fmax(rint(q), -127.), 127.);
+    }
+  }
+}
+// Low bytes of four words.
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0C0C0400u),
+                               __builtin_amdgcn_perm(b, a, 0x0C0C0400u), 0x05040100u);
+}
+
+// 8 lanes per group of 64 columns, 8 columns per lane (K % 8 == 0), NI groups
+// per lane, 32 apart, all loads first; rows of ng groups, the last one
+// possibly short.
+template <bool BF, int NI>
 __global__ void __launch_bounds__(256) k_ckpt(const uint16_t* __restrict__ x, int8_t* __restrict__ q,
                                               float* __restrict__ s, uint32_t ng, uint32_t nq,
-                                              uint64_t groups) {
-  const uint64_t grp = (uint64_t)blockIdx.x * 32 + threadIdx.x / 8;
-  const uint32_t l = threadIdx.x & 7;
-  const uint64_t row = grp / ng;
-  const uint32_t gi = (uint32_t)(grp - row * ng), c = gi * 8 + l;
-  const bool ok = grp < groups && c < nq;
-  const uint64_t at = row * nq + c;   // chunk of 8 columns
-  const uint4 u = ok ? reinterpret_cast<const uint4*>(x)[at] : make_uint4(0, 0, 0, 0);
-  float v[8], mx = 0.f;
-  unpack8<BF>(u, v);
+                                              uint32_t groups) {
+  const uint32_t g0 = blockIdx.x * (32u * NI) + threadIdx.x / 8u, l = threadIdx.x & 7u;
+  uint4 u[NI];
+  uint64_t at[NI];   // chunk of 8 columns
+  bool ok[NI];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
-  mx = fmaxf(mx, __shfl_xor(mx, 1, 64));
-  mx = fmaxf(mx, __shfl_xor(mx, 2, 64));
-  mx = fmaxf(mx, __shfl_xor(mx, 4, 64));
-  const float sc = div_rn(mx, 127.f);
-  const double inv = sc > 0.f ? 1. / (double)sc : 0.;
-  int cq[8];
+  for (int i = 0; i < NI; ++i) {
+    const uint32_t grp = g0 + 32u * i;
+    at[i] = (uint64_t)grp * 8u + l;
+    ok[i] = grp < groups;
+    if (nq != 8u * ng) {   // rows of whole groups need no division
+      const uint32_t row = grp / ng, c = (grp - row * ng) * 8u + l;
+      at[i] = (uint64_t)row * nq + c;
+      ok[i] = ok[i] && c < nq;
+    }
+    const uint4 v = reinterpret_cast<const uint4*>(x)[ok[i] ? at[i] : 0u];   // unconditional
+    u[i] = make_uint4(ok[i] ? v.x : 0u, ok[i] ? v.y : 0u, ok[i] ? v.z : 0u, ok[i] ? v.w : 0u);
+  }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) cq[e] = ckpt_code(v[e], sc, inv);
-  if (ok) reinterpret_cast<uint2*>(q)[at] = make_uint2(pack4i(cq, 0), pack4i(cq, 4));
-  if (l == 0 && grp < groups) s[grp] = sc;
+  for (int i = 0; i < NI; ++i) {
+    float v[8], mx = 0.f;
+    unpack8<BF>(u[i], v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
+    mx = fmaxf(mx, dpp_f<QP_DPP_QUAD_1032>(0.f, mx));
+    mx = fmaxf(mx, dpp_f<QP_DPP_QUAD_2301>(0.f, mx));
+    mx = fmaxf(mx, dpp_f<QP_DPP_ROW_HALF_MIRROR>(0.f, mx));   // 8 lanes: the other four
+    const float sc = scale127(mx);
+    uint32_t cq[8];
+    ckpt_codes<8>(v, sc, cq);
+    if (ok[i])
+      reinterpret_cast<uint2*>(q)[at[i]] =
+          make_uint2(bytes4(cq[0], cq[1], cq[2], cq[3]), bytes4(cq[4], cq[5], cq[6], cq[7]));
+    if (l == 0 && g0 + 32u * i < groups) s[g0 + 32u * i] = sc;
+  }
 }
 
 // Any K: one wave per group, one column per lane.
 template <bool BF>
 __global__ void __launch_bounds__(256) k_ckpt_any(const uint16_t* __restrict__ x,
                                                   int8_t* __restrict__ q, float* __restrict__ s,
-                                                  uint32_t ng, int64_t K, uint64_t groups) {
-  const uint64_t grp = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+                                                  uint32_t ng, int64_t K, uint32_t groups) {
+  const uint32_t grp = blockIdx.x * 4u + (threadIdx.x >> 6);
   if (grp >= groups) return;   // whole waves
   const uint32_t lane = threadIdx.x & 63;
-  const uint64_t row = grp / ng;
-  const int64_t k = (int64_t)(grp - row * ng) * 64 + lane;
-  const float v = k < K ? val16<BF>(x[row * K + k]) : 0.f;
-  const float sc = div_rn(wave_max_all(fabsf(v)), 127.f);
-  const double inv = sc > 0.f ? 1. / (double)sc : 0.;
-  if (k < K) q[row * K + k] = (int8_t)ckpt_code(v, sc, inv);
+  const int64_t row = grp / ng;
+  const int64_t k = (int64_t)(grp - (uint32_t)row * ng) * 64 + lane;
+  const float v[1] = {k < K ? val16<BF>(x[row * K + k]) : 0.f};
+  const float sc = scale127(wave_max_all(fabsf(v[0])));
+  uint32_t c[1];
+  ckpt_codes<1>(v, sc, c);
+  if (k < K) q[row * K + k] = (int8_t)c[0];
   if (lane == 0) s[grp] = sc;
 }
 
@@ -492,13 +602,16 @@ __device__ __forceinline__ void put(void* x, uint64_t i, float v) {
 template <int DT, int V>
 __global__ void __launch_bounds__(256) k_ckpt_restore(const int8_t* __restrict__ q,
                                                       const float* __restrict__ s, uint32_t ng,
-                                                      uint32_t nq, uint64_t n,
+                                                      uint32_t nq, uint32_t n,
                                                       void* __restrict__ x) {
-  const uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  const uint32_t at = blockIdx.x * 256u + threadIdx.x;
   if (at >= n) return;
-  const uint64_t row = at / nq;
-  const uint32_t c = (uint32_t)(at - row * nq);
-  const float sc = s[row * ng + c / (64 / V)];
+  uint32_t gi = at / (64u / V);   // rows of whole groups need no division
+  if (nq != (64u / V) * ng) {
+    const uint32_t row = at / nq;
+    gi = row * ng + (at - row * nq) / (64u / V);
+  }
+  const float sc = s[gi];
   if constexpr (V == 1) {
     put<DT>(x, at, (float)q[at] * sc);
   } else {
@@ -531,8 +644,7 @@ NormBwdFn norm_bwd_pick(int64_t nq) {
   if (nq <= 256) return k_norm_bwd<BF, CK, 256, 1>;
   if (nq <= 512) return k_norm_bwd<BF, CK, 256, 2>;
   if (nq <= 1024) return k_norm_bwd<BF, CK, 512, 2>;
-  if (nq <= 2048) return k_norm_bwd<BF, CK, 1024, 2>;
-  return k_norm_bwd<BF, CK, 1024, 4>;
+  return k_norm_bwd<BF, CK, 1024, 2>;
 }
 int norm_bwd_threads(int64_t nq) { return nq <= 512 ? 256 : nq <= 1024 ? 512 : 1024; }
 
@@ -547,7 +659,7 @@ hipError_t launch_norm(const void* x, const void* r, int dt, int64_t M, int64_t 
   const int64_t nq = K / 8;
   if (K % 8 || nq > 4096) {
     auto fn = dt == BF16 ? k_norm_any<true> : k_norm_any<false>;
-    hipLaunchKernelGGL(fn, dim3((unsigned)M), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(fn, dim3((unsigned)M), dim3(kAny), 0, st, a);
     return hipGetLastError();
   }
   int tpr = nq <= 64 ? 64 : nq <= 1024 ? 256 : 1024;
@@ -572,11 +684,11 @@ hipError_t launch_norm_bwd(const void* dy, const void* s, const void* sq, const 
   const int64_t nq = K / 8;
   const unsigned P = (unsigned)norm_bwd_parts(M);
   hipError_t e;
-  if (K % 8 || nq > 4096) {
+  if (K % 8 || nq > 2048) {
     if (ds) {
       auto fn = bf ? (ck ? k_norm_bwd_any<true, true> : k_norm_bwd_any<true, false>)
                    : (ck ? k_norm_bwd_any<false, true> : k_norm_bwd_any<false, false>);
-      hipLaunchKernelGGL(fn, dim3((unsigned)M), dim3(256), 0, st, a);
+      hipLaunchKernelGGL(fn, dim3((unsigned)M), dim3(kAny), 0, st, a);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (dw) {
@@ -592,7 +704,7 @@ hipError_t launch_norm_bwd(const void* dy, const void* s, const void* sq, const 
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (dw) {
-    hipLaunchKernelGGL(k_col_sum, dim3((unsigned)((K + 63) / 64)), dim3(1024), 0, st, part, (int)P,
+    hipLaunchKernelGGL(k_col_sum, dim3((unsigned)((K + 31) / 32)), dim3(1024), 0, st, part, (int)P,
                        K, dw);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -603,14 +715,18 @@ hipError_t launch_norm_bwd(const void* dy, const void* s, const void* sq, const 
 hipError_t launch_checkpoint(const void* x, int dt, int64_t M, int64_t K, void* q, float* s,
                              hipStream_t st) {
   const uint32_t ng = (uint32_t)((K + 63) / 64);
-  const uint64_t groups = (uint64_t)M * ng;
+  const uint32_t groups = (uint32_t)((uint64_t)M * ng);   // < 2^31 (host check)
   if (K % 8) {
     auto fn = dt == BF16 ? k_ckpt_any<true> : k_ckpt_any<false>;
-    hipLaunchKernelGGL(fn, dim3((unsigned)((groups + 3) / 4)), dim3(256), 0, st,
+    hipLaunchKernelGGL(fn, dim3((groups + 3u) / 4u), dim3(256), 0, st,
                        static_cast<const uint16_t*>(x), static_cast<int8_t*>(q), s, ng, K, groups);
   } else {
-    auto fn = dt == BF16 ? k_ckpt<true> : k_ckpt<false>;
-    hipLaunchKernelGGL(fn, dim3((unsigned)((groups + 31) / 32)), dim3(256), 0, st,
+    // four groups per lane where that leaves every CU several blocks
+    const bool many = groups >= 32u * 4u * 1024u;
+    const uint32_t per = many ? 128u : 32u;
+    auto fn = dt == BF16 ? (many ? k_ckpt<true, 4> : k_ckpt<true, 1>)
+                         : (many ? k_ckpt<false, 4> : k_ckpt<false, 1>);
+    hipLaunchKernelGGL(fn, dim3((groups + per - 1u) / per), dim3(256), 0, st,
                        static_cast<const uint16_t*>(x), static_cast<int8_t*>(q), s, ng,
                        (uint32_t)(K / 8), groups);
   }
@@ -622,12 +738,12 @@ hipError_t launch_checkpoint_restore(const void* q, const float* s, int64_t M, i
   const uint32_t ng = (uint32_t)((K + 63) / 64);
   const bool v8 = K % 8 == 0;
   const uint32_t nq = (uint32_t)(v8 ? K / 8 : K);
-  const uint64_t n = (uint64_t)M * nq;
+  const uint32_t n = (uint32_t)((uint64_t)M * nq);   // <= 2^31 (host check)
   auto fn = v8 ? (dt == F32 ? k_ckpt_restore<F32, 8>
                   : dt == BF16 ? k_ckpt_restore<BF16, 8> : k_ckpt_restore<F16, 8>)
                : (dt == F32 ? k_ckpt_restore<F32, 1>
                   : dt == BF16 ? k_ckpt_restore<BF16, 1> : k_ckpt_restore<F16, 1>);
-  hipLaunchKernelGGL(fn, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st,
+  hipLaunchKernelGGL(fn, dim3((n + 255u) / 256u), dim3(256), 0, st,
                      static_cast<const int8_t*>(q), s, ng, nq, n, x);
   return hipGetLastError();
 }

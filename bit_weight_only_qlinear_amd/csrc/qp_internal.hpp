@@ -111,8 +111,9 @@ struct GatedArgs {
 // checkpoints (skinny.hip).
 size_t gated_workspace_bytes(const Desc& d, int64_t M);
 hipError_t launch_gated(const Desc& d, const GatedArgs& a, void* ws, hipStream_t s);
-// Exact codes, one activation row, no checkpoints (gemv.hip).
-bool gated_gemv_supported(const Desc& d);
+// Exact codes, streamed: one activation row, or two in some formats, and no
+// checkpoints (gemv.hip).
+bool gated_gemv_supported(const Desc& d, int64_t M);
 hipError_t launch_gated_gemv(const Desc& d, const GatedArgs& a, const size_t bytes[5],
                              hipStream_t s);
 hipError_t launch_gated_skinny(const Desc& d, const GatedArgs& a, const size_t bytes[5],

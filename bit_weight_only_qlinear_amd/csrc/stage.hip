@@ -201,17 +201,22 @@ __global__ void __launch_bounds__(NT) k_stage_row(StageK a) {
   uint4 d[NC];
   uint2 gq[GATED ? NC : 1], uq[GATED ? NC : 1];
   float sg[GATED ? NC : 1], su[GATED ? NC : 1];
-  const int64_t base = row * a.N, gbase = row * a.T1;   // 64 columns per scale and step
+  const int64_t rrow = rok ? row : a.M - 1;   // rows past M: any that is there
+  const int64_t base = rrow * a.N, gbase = rrow * a.T1;   // 64 columns per scale and step
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const uint32_t c = threadIdx.x + NT * i;
     const bool ok = c < nq;
-    d[i] = ok ? reinterpret_cast<const uint4*>(a.dy + base)[c] : make_uint4(0, 0, 0, 0);
+    // unconditional loads (of the row's first chunk past its end; a zero dy
+    // makes everything zero): all of them go out together
+    const uint32_t cc = ok ? c : 0u;
+    const uint4 v = reinterpret_cast<const uint4*>(a.dy + base)[cc];
+    d[i] = make_uint4(ok ? v.x : 0u, ok ? v.y : 0u, ok ? v.z : 0u, ok ? v.w : 0u);
     if constexpr (GATED) {
-      gq[i] = ok ? reinterpret_cast<const uint2*>(a.gq + base)[c] : make_uint2(0, 0);
-      uq[i] = ok ? reinterpret_cast<const uint2*>(a.uq + base)[c] : make_uint2(0, 0);
-      sg[i] = ok ? a.gs[gbase + c / 8] : 0.f;
-      su[i] = ok ? a.us[gbase + c / 8] : 0.f;
+      gq[i] = reinterpret_cast<const uint2*>(a.gq + base)[cc];
+      uq[i] = reinterpret_cast<const uint2*>(a.uq + base)[cc];
+      sg[i] = a.gs[gbase + cc / 8];
+      su[i] = a.us[gbase + cc / 8];
     }
   }
   float x[NC][8], y[GATED ? NC : 1][8], b = 0.f;

@@ -387,7 +387,7 @@ typedef enum {
  * the exact values.  Pass y, or yq and ys, and NULL for the other.  s (only
  * with a residual) and rstd (fp32 [M]) may be NULL to skip them.  s may be
  * x or residual itself (in place); y and yq are buffers of their own.
- * Any K >= 1 (rows with K % 8 == 0 and K <= 32768 are read once); eps > 0;
+ * Any K >= 1 (rows with K % 8 == 0 are read once, up to K = 32768); eps > 0;
  * M <= 2^21, and M * K <= 2^34 (2^31 where K % 8 != 0). */
 qp_status qnorm_forward(const void* x, const void* residual, int32_t x_dtype, int64_t M, int64_t K,
                         const void* weight, float eps, void* s, void* y, void* yq, float* ys,

@@ -165,6 +165,21 @@ def test_checkpoint(q, M, K, dt):
         assert torch.equal(got.cpu(), ref), od
 
 
+def test_checkpoint_scales_over_the_range(q):
+    """Groups of very small and very large values, subnormal scales and
+    quotients among them."""
+    rng = np.random.default_rng(9)
+    v = rng.normal(size=(130, 64)) * 10.0 ** rng.uniform(-39, 38, size=(130, 1))
+    v[0] = 0
+    v[1, 1:] = 0
+    for K in (64, 60):
+        x, x64 = dev(np.clip(v[:, :K], -3e38, 3e38), "bf16")
+        codes, scales = q.qpack_checkpoint(x)
+        rq, rs = mlp.checkpoint(x64)
+        assert np.array_equal(scales.cpu().numpy(), rs)
+        assert np.array_equal(codes.cpu().numpy(), rq)
+
+
 def test_checkpoint_ties_go_to_even(q):
     """Scales 3 and 2 with values half way between codes."""
     x = torch.zeros((2, 64), dtype=torch.float16)
@@ -226,7 +241,8 @@ def product_tolerance(D, w):
 
 GATED_SIZES = [(1, 48, 512), (1, 1, 256), (3, 100, 256), (8, 64, 768), (16, 257, 512), (17, 130, 512),
                (70, 64, 256), (300, 200, 512), (5, 96, 96), (40, 33, 160), (2, 65, 320), (33, 448, 320),
-               (1, 300, 4096), (1, 33, 5120), (1, 70, 8192), (1, 37, 16384), (1, 90, 1056), (6, 35, 4096)]
+               (1, 300, 4096), (1, 33, 5120), (1, 70, 8192), (1, 37, 16384), (1, 90, 1056), (6, 35, 4096),
+               (2, 33, 4096), (2, 50, 8192), (2, 40, 512)]
 
 
 @pytest.mark.parametrize("M,N,K", GATED_SIZES)
