@@ -150,64 +150,91 @@ __device__ __forceinline__ void load_codes(const GRes& r, int t, int lg, GStage<
   }
 }
 
-// Scale and offset of the half row (Q6K: of its group grp of 16).
+// A step's scales and offsets of the half row, for gchunk.
 template <int KIND>
-__device__ __forceinline__ void scale_of(const GStage<KIND>& st, int grp, int mb, float& S, float& T) {
+struct GScale {
+  half2_t S[2], T[2];   // broadcast; Q6K, SYM4: hi and lo parts of the scale (Q6K: per group)
+  half2_t s, t;         // Q4K: lo parts
+  float Sf, Tf;         // AFF8
+};
+
+__device__ __forceinline__ void split2(float v, half2_t& hi, half2_t& lo) {
+  hi.x = hi.y = (_Float16)v;
+  lo.x = lo.y = (_Float16)(v - (float)hi.x);
+}
+
+template <int KIND>
+__device__ __forceinline__ void scales_of(const GStage<KIND>& st, int mb, GScale<KIND>& c) {
   if constexpr (KIND == G_Q4K) {
-    S = (float)(st.s0 & 0xFFu) * f16_to_f32(st.s2 & 0xFFFFu);
-    T = -S * ((float)(st.s1 & 0xFFu) * f16_to_f32(st.s2 >> 16));
+    const float S = (float)(st.s0 & 0xFFu) * f16_to_f32(st.s2 & 0xFFFFu);
+    split2(S, c.S[0], c.s);
+    split2(-S * ((float)(st.s1 & 0xFFu) * f16_to_f32(st.s2 >> 16)), c.T[0], c.t);
   } else if constexpr (KIND == G_Q6K) {
-    S = (float)(int8_t)((st.s0 >> (8 * grp)) & 0xFFu) * f16_to_f32(st.s2 & 0xFFFFu);
-    T = -32.f * S;
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+      split2((float)(int8_t)((st.s0 >> (8 * g)) & 0xFFu) * f16_to_f32(st.s2 & 0xFFFFu), c.S[g], c.T[g]);
   } else if constexpr (KIND == G_SYM4) {
-    S = __uint_as_float(st.s0);
-    T = -8.f * S;
-  } else if constexpr (KIND == G_SYM4C) {
-    S = 1.f;
-    T = -8.f;
-  } else {
-    S = meta_to_f32(st.s0 & 0xFFFFu, mb);
-    T = meta_to_f32(st.s1 & 0xFFFFu, mb);
+    split2(__uint_as_float(st.s0), c.S[0], c.T[0]);
+  } else if constexpr (KIND != G_SYM4C) {
+    c.Sf = meta_to_f32(st.s0 & 0xFFFFu, mb);
+    c.Tf = meta_to_f32(st.s1 & 0xFFFFu, mb);
+    c.S[0].x = c.S[0].y = (_Float16)c.Sf;
+    c.T[0].x = c.T[0].y = (_Float16)c.Tf;
   }
 }
 
-template <int KIND>
-__device__ __forceinline__ uint32_t gfield(const GStage<KIND>& st, int j, int e) {
-  if constexpr (KIND == G_AFF2) return (st.w[j >> 1] >> (2 * (8 * (j & 1) + e))) & 3u;
-  else if constexpr (KIND == G_AFF8) return (st.w[2 * j + (e >> 2)] >> (8 * (e & 3))) & 255u;
-  else if constexpr (KIND == G_Q6K)
-    return ((st.w[j] >> (4 * e)) & 15u) | (((st.h[j >> 1] >> (2 * (8 * (j & 1) + e))) & 3u) << 4);
-  else return (st.w[j] >> (4 * e)) & 15u;
-}
-
 // Chunk j (8 columns) of the half row as fp16 in the order (0,4,1,5,2,6,3,7).
+// Pairs 0 and 2 as 1024 + u; pairs 1 and 3 of nibbles left at mantissa bits 4
+// and up of 64, whose unit they are: 64 + u, without a shift.  Then the exact
+// u (less the format's zero) and one rounding or two of about 2^-12 each:
+// AFF2, AFF4 fma(u, S, T); SYM4, Q6K fma(v, S, v s); Q4K fma(u, S, T) +
+// fma(u, s, t), S + s and T + t being the scale and the offset.  8-bit codes
+// go through fp32: their scales are the smallest, next to fp16's subnormals.
 template <int KIND>
-__device__ __forceinline__ uint4 gchunk(const GStage<KIND>& st, int j, int mb, uint32_t magic,
-                                        uint32_t magic64) {
-  float S, T;
-  scale_of<KIND>(st, KIND == G_Q6K ? (j >> 1) : 0, mb, S, T);
+__device__ __forceinline__ uint4 gchunk(const GStage<KIND>& st, int j, const GScale<KIND>& c,
+                                        uint32_t magic, uint32_t magic64) {
   uint32_t p[4];
-  if constexpr (KIND == G_AFF4 || KIND == G_SYM4C) {
-    half2_t s2, t2;
-    s2.x = s2.y = (_Float16)S;
-    t2.x = t2.y = (_Float16)T;
-    // pairs 0 and 2 as 1024 + q; pairs 1 and 3 left at mantissa bits 4 .. 7 of
-    // 64, whose unit they are: 64 + q, without a shift
-    constexpr float OFF = KIND == G_SYM4C ? 8.f : 0.f;
-    const half2_t mag = {(_Float16)(1024.f + OFF), (_Float16)(1024.f + OFF)};
-    const half2_t mag64 = {(_Float16)(64.f + OFF), (_Float16)(64.f + OFF)};
+  if constexpr (KIND == G_AFF8) {
+    auto f = [&](int e) { return (float)((st.w[2 * j + (e >> 2)] >> (8 * (e & 3))) & 255u); };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = i < 2 ? st.w[j] : st.w[j] >> 8;
-      const half2_t q = i & 1 ? __builtin_bit_cast(half2_t, and_or(w, 0x00F000F0u, magic64)) - mag64
-                              : __builtin_bit_cast(half2_t, and_or(w, 0x000F000Fu, magic)) - mag;
-      p[i] = __builtin_bit_cast(uint32_t, KIND == G_SYM4C ? q : __builtin_elementwise_fma(q, s2, t2));
+    for (int i = 0; i < 4; ++i) p[i] = pack_f16(fmaf(f(i), c.Sf, c.Tf), fmaf(f(i + 4), c.Sf, c.Tf));
+    return make_uint4(p[0], p[1], p[2], p[3]);
+  }
+  constexpr bool NIB = KIND != G_AFF2 && KIND != G_AFF8;
+  constexpr float OFF = KIND == G_Q6K ? 32.f : (KIND == G_SYM4 || KIND == G_SYM4C) ? 8.f : 0.f;
+  constexpr float M0 = 1024.f + OFF, M1 = (NIB ? 64.f : 1024.f) + OFF;
+  const half2_t mag[2] = {{(_Float16)M0, (_Float16)M0}, {(_Float16)M1, (_Float16)M1}};
+  uint32_t h = 0;   // Q6K: high bits of columns 0-3 and 4-7 in the halves; AFF2: the codes
+  if constexpr (KIND == G_Q6K || KIND == G_AFF2) {
+    const uint32_t v = KIND == G_Q6K ? st.h[(j >> 1) % (GT<KIND>::H > 0 ? GT<KIND>::H / 2 : 1)]
+                                     : st.w[j >> 1];
+    h = __builtin_amdgcn_perm(0u, v, j & 1 ? 0x0C030C02u : 0x0C010C00u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t q;
+    if constexpr (KIND == G_AFF2) {
+      q = and_or(h >> (2 * i), 0x00030003u, magic);
+    } else {
+      uint32_t m = i & 1 ? magic64 : magic;
+      if constexpr (KIND == G_Q6K) {   // bits 2 i, 2 i + 1 to 4, 5 or (odd i) 8, 9
+        const int up = (i & 1 ? 8 : 4) - 2 * i;
+        m = and_or(up >= 0 ? h << (up >= 0 ? up : 0) : h >> (up >= 0 ? 0 : -up),
+                   i & 1 ? 0x03000300u : 0x00300030u, m);
+      }
+      q = and_or(i < 2 ? st.w[j] : st.w[j] >> 8, i & 1 ? 0x00F000F0u : 0x000F000Fu, m);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      p[i] = pack_f16(fmaf((float)gfield<KIND>(st, j, i), S, T),
-                      fmaf((float)gfield<KIND>(st, j, i + 4), S, T));
+    const half2_t v = __builtin_bit_cast(half2_t, q) - mag[i & 1];   // exact
+    half2_t w = v;
+    if constexpr (KIND == G_Q4K)
+      w = __builtin_elementwise_fma(v, c.S[0], c.T[0]) + __builtin_elementwise_fma(v, c.s, c.t);
+    else if constexpr (KIND == G_Q6K)
+      w = __builtin_elementwise_fma(v, c.S[j >> 1], v * c.T[j >> 1]);
+    else if constexpr (KIND == G_SYM4)
+      w = __builtin_elementwise_fma(v, c.S[0], v * c.T[0]);
+    else if constexpr (KIND != G_SYM4C)
+      w = __builtin_elementwise_fma(v, c.S[0], c.T[0]);
+    p[i] = __builtin_bit_cast(uint32_t, w);
   }
   return make_uint4(p[0], p[1], p[2], p[3]);
 }
@@ -420,10 +447,10 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
   };
   const int wn = wrow_of(tid);
   const uint32_t magic = 0x64006400u, magic64 = 0x54005400u;   // 1024, 64
-  auto put = [&](uint32_t buf, int p, const GStage<KIND>& st) {
+  auto put = [&](uint32_t buf, int p, const GStage<KIND>& st, const GScale<KIND>& sc) {
     const int j = 4 * (tid & 1) + p;
     *reinterpret_cast<uint4*>(smem + (uint32_t)wn * 128u + (uint32_t)((j ^ ((wn >> 1) & 7)) * 16) +
-                              buf * kTileBytes) = gchunk<KIND>(st, p, a.mb, magic, magic64);
+                              buf * kTileBytes) = gchunk<KIND>(st, p, sc, magic, magic64);
   };
 
   half8_t Bf[4][J];
@@ -444,6 +471,8 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
       }
       chunk_meta<KIND>(cur, t + 1, a.lg, r.half, nx);
     }
+    GScale<KIND> sc;
+    scales_of<KIND>(nx, a.mb, sc);
     half8_t A[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) A[i] = rd_a(buf, 0, i);
@@ -458,7 +487,7 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
       });
 #pragma unroll
       for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t + 1, s, j);
-      put(buf ^ 1u, s, nx);
+      put(buf ^ 1u, s, nx, sc);
     });
     __syncthreads();
   };
@@ -475,8 +504,12 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
   for (int s = 0; s < 4; ++s)
 #pragma unroll
     for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(0, s, j);
+  {
+    GScale<KIND> sc;
+    scales_of<KIND>(st0, a.mb, sc);
 #pragma unroll
-  for (int p = 0; p < 4; ++p) put(0u, p, st0);
+    for (int p = 0; p < 4; ++p) put(0u, p, st0, sc);
+  }
   __syncthreads();
   for (int t = 0; t < a.T; t += 2) {
     kstep(std::integral_constant<uint32_t, 0>{}, t, st0, st1);
