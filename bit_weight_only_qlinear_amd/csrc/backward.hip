@@ -356,6 +356,20 @@ k_dx(DxK a) {
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
   half8_t Bf[4][J];
 
+  // Fragments of the step; A[2] and A[3] of its last slice, with Bf[3], are
+  // kept for the products that run after the next barrier.
+  half8_t A[4];
+  A[2] = A[3] = half8_t{};
+#pragma unroll
+  for (int j = 0; j < J; ++j) Bf[3][j] = half8_t{};
+  auto deferred = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 2; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A[i], Bf[3][j], acc[i][j], 0, 0, 0);
+  };
+
   // One step: MFMAs on LDS buffer cur = (t - t0) & 1 and the D fragments in Bf
   // (reloaded slice by slice for step t + 1); conversion of step t + 1 into
   // the other buffer; weight loads of step t + 2.  Steps past the end load
@@ -364,20 +378,29 @@ k_dx(DxK a) {
     constexpr uint32_t cur = decltype(CUR)::value;
     dload<KIND>(a, o, t + 2, fre);
     DTurned<KIND> d;
-    half8_t A[4];
+    // the matrix cores start on the last step's deferred products while this
+    // step's first fragments come from LDS
+    A[0] = rd_a(cur, 0, 0);
+    A[1] = rd_a(cur, 0, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    deferred();
+    A[2] = rd_a(cur, 0, 2);
+    A[3] = rd_a(cur, 0, 3);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) A[i] = rd_a(cur, 0, i);
+    for (int j = 0; j < J; ++j) Bf[3][j] = ld_b(t, 3, j);
     static_for<4>([&](auto S) {
       constexpr int s = decltype(S)::value;
-      static_for<4>([&](auto I) {
+      static_for<(s < 3 ? 4 : 2)>([&](auto I) {
         constexpr int i = decltype(I)::value;
 #pragma unroll
         for (int j = 0; j < J; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A[i], Bf[s][j], acc[i][j], 0, 0, 0);
         if constexpr (s < 3) A[i] = rd_a(cur, s + 1, i);
       });
+      if constexpr (s < 3) {
 #pragma unroll
-      for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t + 1, s, j);
+        for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t + 1, s, j);
+      }
       // the conversion among the MFMAs of the first three slices
       if constexpr (s == 0) dturn<KIND, MBF16>(nxt, d);
       if constexpr (s == 1 || s == 2) {
@@ -392,7 +415,7 @@ k_dx(DxK a) {
   dload<KIND>(a, o, t0, st0);
   dload<KIND>(a, o, t0 + 1, st1);
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
+  for (int s = 0; s < 3; ++s)
 #pragma unroll
     for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t0, s, j);
   {
@@ -405,6 +428,7 @@ k_dx(DxK a) {
     kstep(std::integral_constant<uint32_t, 0>{}, t, st0, st1);
     if (t + 1 < t1) kstep(std::integral_constant<uint32_t, 1>{}, t + 1, st1, st0);
   }
+  deferred();
 
   // ---- lane: rows k = 8 g + 4 (lane >> 5) + q of column m = lane & 31
   int el = lane;

@@ -458,6 +458,20 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
   const int MP = chunk_steps<KIND>(a.lg);
   constexpr bool RING = CH && KIND != G_SYM4C;
 
+  // Fragments of the step; A[2] and A[3] of its last slice, with Bf[3], are
+  // kept for the products that run after the next barrier.
+  half8_t A[4];
+  A[2] = A[3] = half8_t{};
+#pragma unroll
+  for (int j = 0; j < J; ++j) Bf[3][j] = half8_t{};
+  auto deferred = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 2; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A[i], Bf[3][j], acc[i][j], 0, 0, 0);
+  };
+
   // One step: MFMAs on LDS buffer buf = t & 1 and the fragments of x in Bf (reloaded
   // slice by slice for step t + 1); conversion of step t + 1 (`nx`) into the
   // other buffer; code loads of step t + 2 into `fre`.
@@ -473,20 +487,29 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
     }
     GScale<KIND> sc;
     scales_of<KIND>(nx, a.mb, sc);
-    half8_t A[4];
+    // the matrix cores start on the last step's deferred products while this
+    // step's first fragments come from LDS
+    A[0] = rd_a(buf, 0, 0);
+    A[1] = rd_a(buf, 0, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    deferred();
+    A[2] = rd_a(buf, 0, 2);
+    A[3] = rd_a(buf, 0, 3);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) A[i] = rd_a(buf, 0, i);
+    for (int j = 0; j < J; ++j) Bf[3][j] = ld_b(t, 3, j);
     static_for<4>([&](auto S) {
       constexpr int s = decltype(S)::value;
-      static_for<4>([&](auto I) {
+      static_for<(s < 3 ? 4 : 2)>([&](auto I) {
         constexpr int i = decltype(I)::value;
 #pragma unroll
         for (int j = 0; j < J; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A[i], Bf[s][j], acc[i][j], 0, 0, 0);
         if constexpr (s < 3) A[i] = rd_a(buf, s + 1, i);
       });
+      if constexpr (s < 3) {
 #pragma unroll
-      for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t + 1, s, j);
+        for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t + 1, s, j);
+      }
       put(buf ^ 1u, s, nx, sc);
     });
     __syncthreads();
@@ -501,7 +524,7 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
     chunk_meta<KIND>(cur, 0, a.lg, r.half, st0);
   }
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
+  for (int s = 0; s < 3; ++s)
 #pragma unroll
     for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(0, s, j);
   {
@@ -515,6 +538,7 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
     kstep(std::integral_constant<uint32_t, 0>{}, t, st0, st1);
     if (t + 1 < a.T) kstep(std::integral_constant<uint32_t, 1>{}, t + 1, st1, st0);
   }
+  deferred();
 
   int el = lane;
   asm volatile("" : "+v"(el));   // keeps the epilogue's addresses after the loop
