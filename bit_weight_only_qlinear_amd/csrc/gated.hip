@@ -253,6 +253,7 @@ __device__ __forceinline__ void pre_act4(const GatedK& a, const float16_t (&acc)
     u[q] = ldexpf(acc[i + 2][j][4 * g4 + q], -xe);
   }
   const int last = (int)a.N - 1;
+  asm volatile("" : "+v"(f));   // keeps the loads below from gathering ahead of all their uses
   if constexpr (KIND == G_SYM4C) {   // channel scales: the contraction ran on the codes
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -277,32 +278,50 @@ __device__ __forceinline__ void pre_act4(const GatedK& a, const float16_t (&acc)
   }
 }
 
+// The wave's 64 features of 32 rows as 16-bit words or bytes in its 8 KiB of
+// LDS: h rows of 128 bytes, code rows of 64 behind them, in 16-byte chunks at
+// chunk ^ row bits (64 banks: 2 h rows or 4 code rows share a bank line).
+__device__ __forceinline__ uint32_t h_at(int r, int chunk) {
+  return (uint32_t)(r * 128 + ((chunk ^ (r >> 1)) & 7) * 16);
+}
+__device__ __forceinline__ uint32_t q_at(int r, int chunk) {
+  return (uint32_t)(r * 64 + ((chunk ^ (r >> 2)) & 3) * 16);
+}
+
 // Epilogue: lane (el) holds features 8 g + 4 (el >> 5) + q of each 32 of the
-// wave's 64, of row el & 31 of each 32-row block.
+// wave's 64, of row el & 31 of each 32-row block.  16-bit outputs whose rows
+// keep 16-byte chunks (N % 16 == 0) go through the wave's part of LDS (the
+// weight tiles are done with) and leave as whole lines: stored straight from
+// the accumulators' layout, 8 bytes of h and 4 of each code row per lane, the
+// 2048 x 4096 x 14336 layer with checkpoints took 18 us longer on the L2's
+// request rate.
 template <int KIND, int J, int ACT>
-__device__ __forceinline__ void finish(const GatedK& a, const float16_t (&acc)[4][J], int el, int mbw,
-                                       int f0) {
+__device__ __forceinline__ void finish(const GatedK& a, float16_t (&acc)[4][J], int el, int mbw,
+                                       int f0, unsigned char* lds) {
   const int N = (int)a.N;
-  const bool vec = N % 4 == 0;
+  const bool lines = N % 16 == 0 && a.hdt != F32, vec = N % 4 == 0;
+  const int hh = el >> 5;
   static_for<J>([&](auto JJ) {
     constexpr int j = decltype(JJ)::value;
-    const int64_t m = (int64_t)(mbw + j) * 32 + (el & 31);
+    const int64_t mb = (int64_t)(mbw + j) * 32, m = mb + (el & 31);
     const bool mok = m < a.M;
     const int xe = mok ? a.xe[m] : 0;
+    float mg = 0.f, mu = 0.f;
+    static_for<8>([&](auto G) {   // g and u in place of the accumulators
+      constexpr int i = decltype(G)::value / 4, g4 = decltype(G)::value % 4;
+      const int f = f0 + 32 * i + 8 * g4 + 4 * hh;
+      float g[4], u[4];
+      pre_act4<KIND, J>(a, acc, i, j, g4, f, xe, g, u);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        acc[i][j][4 * g4 + q] = g[q];
+        acc[i + 2][j][4 * g4 + q] = u[q];
+        mg = fmaxf(mg, f + q < N ? fabsf(g[q]) : 0.f);
+        mu = fmaxf(mu, f + q < N ? fabsf(u[q]) : 0.f);
+      }
+    });
     float inv[2] = {0.f, 0.f};
     if (a.gq) {   // group scales: 32 values here, 32 in the other half wave
-      float mg = 0.f, mu = 0.f;
-      static_for<8>([&](auto G) {
-        constexpr int i = decltype(G)::value / 4, g4 = decltype(G)::value % 4;
-        const int f = f0 + 32 * i + 8 * g4 + 4 * (el >> 5);
-        float g[4], u[4];
-        pre_act4<KIND, J>(a, acc, i, j, g4, f, xe, g, u);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          mg = fmaxf(mg, f + q < N ? fabsf(g[q]) : 0.f);
-          mu = fmaxf(mu, f + q < N ? fabsf(u[q]) : 0.f);
-        }
-      });
       mg = div_rn(fmaxf(mg, __shfl_xor(mg, 32, 64)), 127.f);
       mu = div_rn(fmaxf(mu, __shfl_xor(mu, 32, 64)), 127.f);
       // the quotient in fp32: the values carry the fp16 weights' rounding anyway
@@ -314,54 +333,79 @@ __device__ __forceinline__ void finish(const GatedK& a, const float16_t (&acc)[4
         a.us[at] = mu;
       }
     }
-    if (!mok) return;
     unsigned char* hrow = static_cast<unsigned char*>(a.h) + m * N * (a.hdt == F32 ? 4 : 2);
     int8_t* grow = a.gq + m * N;
     int8_t* urow = a.uq + m * N;
     static_for<8>([&](auto G) {
       constexpr int i = decltype(G)::value / 4, g4 = decltype(G)::value % 4;
-      const int f = f0 + 32 * i + 8 * g4 + 4 * (el >> 5);
-      float g[4], u[4];
-      uint32_t b[4];
-      pre_act4<KIND, J>(a, acc, i, j, g4, f, xe, g, u);
+      const int f = f0 + 32 * i + 8 * g4 + 4 * hh;
+      uint32_t b[4], c[4] = {0, 0, 0, 0}, d[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float v = act_f<ACT>(g[q]) * u[q];
+        const float g = acc[i][j][4 * g4 + q], u = acc[i + 2][j][4 * g4 + q];
+        const float v = act_f<ACT>(g) * u;
         b[q] = a.hdt == F32 ? __float_as_uint(v) : a.hdt == BF16 ? f32_to_bf16_rne(v) : f32_to_f16_rne(v);
       }
-      if (vec && f < N) {
+      if (a.gq) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          c[q] = code8(acc[i][j][4 * g4 + q], inv[0]);
+          d[q] = code8(acc[i + 2][j][4 * g4 + q], inv[1]);
+        }
+      }
+      const uint32_t cw = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+      const uint32_t dw = d[0] | d[1] << 8 | d[2] << 16 | d[3] << 24;
+      if (lines) {
+        *reinterpret_cast<uint2*>(lds + h_at(el & 31, 4 * i + g4) + 8 * hh) =
+            make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+        if (a.gq) {
+          const uint32_t at = 4096u + q_at(el & 31, 2 * i + g4 / 2) + 8 * (g4 & 1) + 4 * hh;
+          *reinterpret_cast<uint32_t*>(lds + at) = cw;
+          *reinterpret_cast<uint32_t*>(lds + at + 2048u) = dw;
+        }
+      } else if (mok && vec && f < N) {
         if (a.hdt == F32)
           *reinterpret_cast<uint4*>(hrow + 4 * f) = make_uint4(b[0], b[1], b[2], b[3]);
         else
           *reinterpret_cast<uint2*>(hrow + 2 * f) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
-      } else if (!vec) {
+        if (a.gq) {
+          *reinterpret_cast<uint32_t*>(grow + f) = cw;
+          *reinterpret_cast<uint32_t*>(urow + f) = dw;
+        }
+      } else if (mok && !vec) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (f + q >= N) break;
           if (a.hdt == F32) reinterpret_cast<uint32_t*>(hrow)[f + q] = b[q];
           else reinterpret_cast<uint16_t*>(hrow)[f + q] = (uint16_t)b[q];
-        }
-      }
-      if (a.gq) {
-        uint32_t c[4], d[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          c[q] = code8(g[q], inv[0]);
-          d[q] = code8(u[q], inv[1]);
-        }
-        if (vec && f < N) {
-          *reinterpret_cast<uint32_t*>(grow + f) = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
-          *reinterpret_cast<uint32_t*>(urow + f) = d[0] | d[1] << 8 | d[2] << 16 | d[3] << 24;
-        } else if (!vec) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (f + q >= N) break;
+          if (a.gq) {
             grow[f + q] = (int8_t)c[q];
             urow[f + q] = (int8_t)d[q];
           }
         }
       }
     });
+    if (lines) {   // same wave: LDS operations stay in order
+      unsigned char* h = static_cast<unsigned char*>(a.h);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = 8 * k + (el >> 3), ch = el & 7, f = f0 + 8 * ch;
+        const uint4 v = *reinterpret_cast<const uint4*>(lds + h_at(r, ch));
+        if (mb + r < a.M && f < N) *reinterpret_cast<uint4*>(h + ((mb + r) * N + f) * 2) = v;
+      }
+      if (a.gq) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = 16 * k + (el >> 2), ch = el & 3, f = f0 + 16 * ch;
+          const uint4 v = *reinterpret_cast<const uint4*>(lds + 4096 + q_at(r, ch));
+          const uint4 w = *reinterpret_cast<const uint4*>(lds + 6144 + q_at(r, ch));
+          if (mb + r < a.M && f < N) {
+            *reinterpret_cast<uint4*>(a.gq + (mb + r) * N + f) = v;
+            *reinterpret_cast<uint4*>(a.uq + (mb + r) * N + f) = w;
+          }
+        }
+      }
+    }
   });
 }
 
@@ -544,8 +588,9 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
   asm volatile("" : "+v"(el));   // keeps the epilogue's addresses after the loop
   const int f0 = (int)n0 + 64 * wi;
   if (f0 >= a.N) return;
-  if (a.act == ACT_SILU) finish<KIND, J, ACT_SILU>(a, acc, el, mbw, f0);
-  else finish<KIND, J, ACT_GELU_TANH>(a, acc, el, mbw, f0);
+  unsigned char* lds = smem + 8192 * wave;
+  if (a.act == ACT_SILU) finish<KIND, J, ACT_SILU>(a, acc, el, mbw, f0, lds);
+  else finish<KIND, J, ACT_GELU_TANH>(a, acc, el, mbw, f0, lds);
 }
 
 template <int KIND, bool CH>
