@@ -430,45 +430,62 @@ k_dx(DxK a) {
   }
   deferred();
 
-  // ---- lane: rows k = 8 g + 4 (lane >> 5) + q of column m = lane & 31
+  // ---- lane: rows k = 8 g + 4 (lane >> 5) + q of column m = lane & 31.
+  // Through the wave's 8 KiB of LDS (the weight tiles are done with), so that
+  // the stores are 256-byte pieces of rows of dx: 32 rows of 128 16-bit
+  // columns, or of 64 fp32 ones in two passes; 16-byte chunk c of row r at
+  // c ^ (r & 15).
   int el = lane;
   asm volatile("" : "+v"(el));   // keeps the epilogue's addresses after the loop
+  unsigned char* lds = smem + 8192 * wave;
+  const int r0 = el & 31, hh = el >> 5;
+  const int64_t kw = k0 + wi * 128;
   static_for<J>([&](auto JJ) {
     constexpr int j = decltype(JJ)::value;
-    const int64_t m = (int64_t)(mb0 + j) * 32 + (el & 31);
-    if (m < a.M) {
-      const int xe = a.xe[m];
-      static_for<4>([&](auto I) {
-        constexpr int i = decltype(I)::value;
-        static_for<4>([&](auto G) {
-          constexpr int gg = decltype(G)::value;
-          const int64_t k = k0 + wi * 128 + i * 32 + 8 * gg + 4 * (el >> 5);
-          if (k < K) {   // K is a multiple of 32
-            float v[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = acc[i][j][4 * gg + q];
-            const int64_t at = m * K + k;
-            if (a.part) {
-              *reinterpret_cast<float4*>(a.part + (int64_t)sp * a.M * K + at) =
-                  make_float4(v[0], v[1], v[2], v[3]);
-            } else {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) v[q] = ldexpf(v[q], -xe);
-              if (a.dxdt == F32) {
-                *reinterpret_cast<float4*>(static_cast<float*>(a.dx) + at) =
-                    make_float4(v[0], v[1], v[2], v[3]);
-              } else {
-                uint32_t h[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  h[q] = a.dxdt == BF16 ? f32_to_bf16_rne(v[q]) : f32_to_f16_rne(v[q]);
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dx) + at) =
-                    make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-              }
-            }
-          }
+    const int64_t mb = (int64_t)(mb0 + j) * 32;
+    if (a.part || a.dxdt == F32) {
+      const int xe = !a.part && mb + r0 < a.M ? a.xe[mb + r0] : 0;   // shares stay scaled
+      float* out = a.part ? a.part + (int64_t)sp * a.M * K : static_cast<float*>(a.dx);
+      static_for<2>([&](auto H) {
+        constexpr int h = decltype(H)::value;
+        static_for<8>([&](auto G) {
+          constexpr int i = 2 * h + decltype(G)::value / 4, gg = decltype(G)::value % 4;
+          float4 v;
+          v.x = ldexpf(acc[i][j][4 * gg], -xe);
+          v.y = ldexpf(acc[i][j][4 * gg + 1], -xe);
+          v.z = ldexpf(acc[i][j][4 * gg + 2], -xe);
+          v.w = ldexpf(acc[i][j][4 * gg + 3], -xe);
+          *reinterpret_cast<float4*>(lds + r0 * 256 + ((8 * (i & 1) + 2 * gg + hh) ^ (r0 & 15)) * 16) = v;
         });
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {   // same wave: LDS operations stay in order
+          const int r = 4 * t + (el >> 4), c = el & 15;
+          const float4 v = *reinterpret_cast<const float4*>(lds + r * 256 + (c ^ (r & 15)) * 16);
+          const int64_t k = kw + 64 * h + 4 * c;
+          if (mb + r < a.M && k < K) *reinterpret_cast<float4*>(out + (mb + r) * K + k) = v;
+        }
       });
+    } else {
+      const int xe = mb + r0 < a.M ? a.xe[mb + r0] : 0;
+      static_for<16>([&](auto G) {
+        constexpr int i = decltype(G)::value / 4, gg = decltype(G)::value % 4;
+        uint32_t h[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float v = ldexpf(acc[i][j][4 * gg + q], -xe);
+          h[q] = a.dxdt == BF16 ? f32_to_bf16_rne(v) : f32_to_f16_rne(v);
+        }
+        *reinterpret_cast<uint2*>(lds + r0 * 256 + ((4 * i + gg) ^ (r0 & 15)) * 16 + 8 * hh) =
+            make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+      });
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const int r = 4 * t + (el >> 4), c = el & 15;
+        const uint4 v = *reinterpret_cast<const uint4*>(lds + r * 256 + (c ^ (r & 15)) * 16);
+        const int64_t k = kw + 8 * c;
+        if (mb + r < a.M && k < K)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dx) + (mb + r) * K + k) = v;
+      }
     }
   });
 }
@@ -507,24 +524,24 @@ DxPlan dx_plan(const Desc& d, int64_t M, bool gated) {
   p.T1 = (int)cdiv(d.N, kDN);
   p.T = p.T1 * (gated ? 2 : 1);
   p.tilesK = (int)cdiv(d.K, kDK);
-  p.J = M > 128 ? 2 : 1;
-  p.tilesM = (int)cdiv(M, 128 * p.J);
-  // Waves of blocks over 256 CUs, each block its share of the steps and a
-  // few steps' worth of start and end; more than one split adds the partial
-  // sums' traffic.
-  const double step = p.J == 2 ? 1.4e-6 : 1.0e-6;
+  // Rounds of blocks over 256 CUs, each block its share of the steps (1.6 us
+  // with 256 rows of D, 1.1 with 128) and a few steps' worth of start and end;
+  // more than one share adds the partial sums' traffic and a second kernel.
   double best = 0.;
-  p.split = 1;
-  const int64_t tiles = (int64_t)p.tilesK * p.tilesM;
-  for (int s = 1; s <= 32 && s <= p.T; ++s) {
-    if (s > 1 && tiles * s > 1024) break;
-    double t = (double)cdiv(tiles * s, 256) * (double)(cdiv(p.T, s) + 4) * step;
-    if (s > 1) t += 3e-6 + (double)s * (double)M * (double)d.K * 8. / 4e12;
-    if (s == 1 || t < best) {
-      best = t;
-      p.split = s;
+  for (int J = M > 128 ? 2 : 1; J >= 1; --J) {
+    const int64_t tiles = p.tilesK * cdiv(M, 128 * J);
+    for (int s = 1; s <= 32 && s <= p.T; ++s) {
+      if (s > 1 && tiles * s > 1024) break;
+      double t = (double)cdiv(tiles * s, 256) * (double)(cdiv(p.T, s) + 4) * (J == 2 ? 1.6e-6 : 1.1e-6);
+      if (s > 1) t += 3e-6 + (double)s * (double)M * (double)d.K * 8. / 4e12;
+      if (best == 0. || t < best) {
+        best = t;
+        p.J = J;
+        p.split = s;
+      }
     }
   }
+  p.tilesM = (int)cdiv(M, 128 * p.J);
   p.xf = (size_t)p.T * 4u * (size_t)p.MB * 1024u;
   p.xe = (size_t)p.MB * 128u;
   p.part = p.split > 1 ? (size_t)p.split * (size_t)M * (size_t)d.K * 4u : 0;

@@ -19,6 +19,8 @@
 //    Where the last round of 256-row tiles would fill at most half of the 256
 //    CUs it is cut into tiles of 128 activation rows: 2048 x 4096 x 14336 makes
 //    896 tiles, three full rounds and 256 half tiles instead of four rounds.
+//    Few tiles are cut along K instead: the blocks' fp32 shares of g and u meet
+//    in a fixed order in a second kernel, which then has the activation.
 #include "gemm_kernels.hpp"
 #include "mlp_common.hpp"
 
@@ -44,7 +46,10 @@ struct GatedK {
   int mb, xb, hdt, act;
   int MB, T;                 // 32-row blocks of x, steps of 64 columns
   int tilesM, full;          // 256-row tiles; how many of them run whole
-  int small;                 // M <= 128: one 128-row tile per 128 features
+  int small, tilesM1;        // all tiles of 128 rows; their number along M
+  int split;                 // blocks along K; > 1: sums into part, all tiles alike
+  float* part;               // [split, M, 2, Np]
+  int64_t Np;                // N rounded up to 4
 };
 
 // One k-step of one thread: half a weight row (32 columns), raw.
@@ -244,7 +249,7 @@ __device__ __forceinline__ uint32_t code8(float v, float inv) {
 }
 
 // g and u of the lane's four consecutive features f .. f + 3 in block (i, j).
-template <int KIND, int J>
+template <int KIND, int J, bool BIAS = true>
 __device__ __forceinline__ void pre_act4(const GatedK& a, const float16_t (&acc)[4][J], int i, int j,
                                          int g4, int f, int xe, float (&g)[4], float (&u)[4]) {
 #pragma unroll
@@ -262,6 +267,7 @@ __device__ __forceinline__ void pre_act4(const GatedK& a, const float16_t (&acc)
       u[q] *= static_cast<const float*>(a.up.scales)[fc];
     }
   }
+  if constexpr (!BIAS) return;
   if (a.bias_g) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -409,9 +415,75 @@ __device__ __forceinline__ void finish(const GatedK& a, float16_t (&acc)[4][J], 
   });
 }
 
-// One tile: features n0 .. n0 + 127, 32-row blocks mb0 .. of x (J per wave).
+// The same for one of several blocks along K: its share of g and u.
+template <int KIND, int J>
+__device__ __forceinline__ void finish_part(const GatedK& a, float16_t (&acc)[4][J], int el, int mbw,
+                                            int f0, int sp) {
+  static_for<J>([&](auto JJ) {
+    constexpr int j = decltype(JJ)::value;
+    const int64_t m = (int64_t)(mbw + j) * 32 + (el & 31);
+    if (m < a.M) {
+      const int xe = a.xe[m];
+      float* row = a.part + ((int64_t)sp * a.M + m) * 2 * a.Np;
+      static_for<8>([&](auto G) {
+        constexpr int i = decltype(G)::value / 4, g4 = decltype(G)::value % 4;
+        const int f = f0 + 32 * i + 8 * g4 + 4 * (el >> 5);
+        float g[4], u[4];
+        pre_act4<KIND, J, false>(a, acc, i, j, g4, f, xe, g, u);
+        if (f < a.Np) {
+          *reinterpret_cast<float4*>(row + f) = make_float4(g[0], g[1], g[2], g[3]);
+          *reinterpret_cast<float4*>(row + a.Np + f) = make_float4(u[0], u[1], u[2], u[3]);
+        }
+      });
+    }
+  });
+}
+
+// Joins the shares of one row's group of 64 features (one wave each), in
+// order: bias, activation, product, checkpoints.
+template <int ACT>
+__global__ void __launch_bounds__(256) k_gated_join(GatedK a) {
+  const uint32_t ng = (uint32_t)((a.N + kCkptGroup - 1) / kCkptGroup);
+  const uint32_t id = blockIdx.x * 4u + (threadIdx.x >> 6);
+  if (id >= (uint64_t)a.M * ng) return;   // whole waves
+  const int64_t m = id / ng, grp = id - (uint32_t)m * ng, f = grp * 64 + (threadIdx.x & 63);
+  const bool ok = f < a.N;
+  const float* p = a.part + m * 2 * a.Np + (ok ? f : 0);
+  const int64_t step = a.M * 2 * a.Np;
+  float g = 0.f, u = 0.f;
+  for (int s = 0; s < a.split; ++s) {
+    g += p[s * step];
+    u += p[s * step + a.Np];
+  }
+  if (ok && a.bias_g) g += a.xb ? bf16_to_f32(a.bias_g[f]) : f16_to_f32(a.bias_g[f]);
+  if (ok && a.bias_u) u += a.xb ? bf16_to_f32(a.bias_u[f]) : f16_to_f32(a.bias_u[f]);
+  const int64_t at = m * a.N + f;
+  if (ok) {
+    const float h = act_f<ACT>(g) * u;
+    if (a.hdt == F32) static_cast<float*>(a.h)[at] = h;
+    else static_cast<uint16_t*>(a.h)[at] =
+        (uint16_t)(a.hdt == BF16 ? f32_to_bf16_rne(h) : f32_to_f16_rne(h));
+  }
+  if (a.gq) {
+    const float mg = div_rn(wave_max_all(ok ? fabsf(g) : 0.f), 127.f);
+    const float mu = div_rn(wave_max_all(ok ? fabsf(u) : 0.f), 127.f);
+    if (ok) {
+      a.gq[at] = (int8_t)code8(g, mg > 0.f ? 1.f / mg : 0.f);
+      a.uq[at] = (int8_t)code8(u, mu > 0.f ? 1.f / mu : 0.f);
+    }
+    if ((threadIdx.x & 63) == 0) {
+      a.gs[m * ng + grp] = mg;
+      a.us[m * ng + grp] = mu;
+    }
+  }
+}
+
+// One tile: features n0 .. n0 + 127, 32-row blocks mb0 .. of x (J per wave),
+// share sp of the steps along K.
 template <int KIND, bool CH, int J>
-__device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem, int64_t n0, int mb0) {
+__device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem, int64_t n0, int mb0,
+                                           int sp) {
+  const int t0 = (int)((int64_t)a.T * sp / a.split), t1 = (int)((int64_t)a.T * (sp + 1) / a.split);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wi = wave >> 2, wj = wave & 3;
@@ -483,7 +555,7 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
     xo[j] = mbw + j < a.MB ? (uint32_t)(mbw + j) * 1024u + 16u * (2u * (lane & 31) + (lane >> 5)) : kOff;
   const uint32_t xs = (uint32_t)a.MB * 1024u;   // one k-slice of 16
   auto ld_b = [&](int t, int s, int j) {
-    const __amdgpu_buffer_rsrc_t rx = rsrc(a.xf + (int64_t)(t < a.T ? t : 0) * 4 * xs, 4u * xs);
+    const __amdgpu_buffer_rsrc_t rx = rsrc(a.xf + (int64_t)(t < t1 ? t : t0) * 4 * xs, 4u * xs);
     // the slice as the scalar offset: the range check is on xo[j] alone, and
     // a row block inside a slice is inside all four
     return __builtin_bit_cast(half8_t,
@@ -516,7 +588,7 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(A[i], Bf[3][j], acc[i][j], 0, 0, 0);
   };
 
-  // One step: MFMAs on LDS buffer buf = t & 1 and the fragments of x in Bf (reloaded
+  // One step: MFMAs on LDS buffer buf = (t - t0) & 1 and the fragments of x in Bf (reloaded
   // slice by slice for step t + 1); conversion of step t + 1 (`nx`) into the
   // other buffer; code loads of step t + 2 into `fre`.
   auto kstep = [&](auto BUF, int t, GStage<KIND>& fre, GStage<KIND>& nx) {
@@ -560,17 +632,17 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
   };
 
   GStage<KIND> st0, st1;
-  load_codes<KIND, CH>(r, 0, a.lg, st0);
-  load_codes<KIND, CH>(r, 1, a.lg, st1);
+  load_codes<KIND, CH>(r, t0, a.lg, st0);
+  load_codes<KIND, CH>(r, t0 + 1, a.lg, st1);
   if constexpr (RING) {
-    load_chunk<KIND>(r, 0, cur);
-    load_chunk<KIND>(r, 1, nxt);
-    chunk_meta<KIND>(cur, 0, a.lg, r.half, st0);
+    load_chunk<KIND>(r, t0 / MP, cur);
+    load_chunk<KIND>(r, t0 / MP + 1, nxt);
+    chunk_meta<KIND>(cur, t0, a.lg, r.half, st0);
   }
 #pragma unroll
   for (int s = 0; s < 3; ++s)
 #pragma unroll
-    for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(0, s, j);
+    for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t0, s, j);
   {
     GScale<KIND> sc;
     scales_of<KIND>(st0, a.mb, sc);
@@ -578,9 +650,9 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
     for (int p = 0; p < 4; ++p) put(0u, p, st0, sc);
   }
   __syncthreads();
-  for (int t = 0; t < a.T; t += 2) {
+  for (int t = t0; t < t1; t += 2) {
     kstep(std::integral_constant<uint32_t, 0>{}, t, st0, st1);
-    if (t + 1 < a.T) kstep(std::integral_constant<uint32_t, 1>{}, t + 1, st1, st0);
+    if (t + 1 < t1) kstep(std::integral_constant<uint32_t, 1>{}, t + 1, st1, st0);
   }
   deferred();
 
@@ -588,6 +660,10 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
   asm volatile("" : "+v"(el));   // keeps the epilogue's addresses after the loop
   const int f0 = (int)n0 + 64 * wi;
   if (f0 >= a.N) return;
+  if (a.part) {
+    finish_part<KIND, J>(a, acc, el, mbw, f0, sp);
+    return;
+  }
   unsigned char* lds = smem + 8192 * wave;
   if (a.act == ACT_SILU) finish<KIND, J, ACT_SILU>(a, acc, el, mbw, f0, lds);
   else finish<KIND, J, ACT_GELU_TANH>(a, acc, el, mbw, f0, lds);
@@ -597,16 +673,21 @@ template <int KIND, bool CH>
 __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 k_gated(GatedK a) {
   __shared__ __attribute__((aligned(16))) unsigned char smem[2 * kTileBytes];
+  // contiguous runs of tiles per XCD, m fastest
   const int bid = blockIdx.x;
-  if (bid < a.full) {   // contiguous runs of tiles per XCD, m fastest
-    const int t = a.full % 8 == 0 ? (bid % 8) * (a.full / 8) + bid / 8 : bid;
-    gated_tile<KIND, CH, 2>(a, smem, (int64_t)(t / a.tilesM) * kGF, (t % a.tilesM) * 8);
+  auto run = [](int i, int n) { return n % 8 == 0 ? (i % 8) * (n / 8) + i / 8 : i; };
+  if (bid < a.full) {
+    const int t = run(bid, a.full), sp = t / (a.full / a.split), u = t - sp * (a.full / a.split);
+    gated_tile<KIND, CH, 2>(a, smem, (int64_t)(u / a.tilesM) * kGF, (u % a.tilesM) * 8, sp);
   } else {
-    const int nh = (int)gridDim.x - a.full, i = bid - a.full;
-    const int u = nh % 8 == 0 ? (i % 8) * (nh / 8) + i / 8 : i;
-    const int t = a.full + (a.small ? u : u / 2);
-    gated_tile<KIND, CH, 1>(a, smem, (int64_t)(t / a.tilesM) * kGF,
-                            (t % a.tilesM) * 8 + (a.small ? 0 : 4 * (u & 1)));
+    const int nh = (int)gridDim.x - a.full, t = run(bid - a.full, nh);
+    if (a.small) {
+      const int sp = t / (nh / a.split), u = t - sp * (nh / a.split);
+      gated_tile<KIND, CH, 1>(a, smem, (int64_t)(u / a.tilesM1) * kGF, (u % a.tilesM1) * 4, sp);
+    } else {   // halves of the last round's tiles
+      const int u = a.full + t / 2;
+      gated_tile<KIND, CH, 1>(a, smem, (int64_t)(u / a.tilesM) * kGF, (u % a.tilesM) * 8 + 4 * (t & 1), 0);
+    }
   }
 }
 
@@ -615,13 +696,55 @@ size_t frag_bytes(const Desc& d, int64_t M) {
   return (size_t)cdiv(d.K, 64) * 4u * (size_t)cdiv(M, 32) * 1024u;
 }
 
+// Tiles and blocks along K.  Time in steps of a 256-row tile (1.85 us on the
+// 2048 x 4096 x 14336 layer; 128 rows: 0.7 of that, the weights' share does
+// not halve), rounds of 256 blocks, 8 steps of start and end per round, and
+// for more than one block along K the shares' traffic and a second kernel.
+struct GatedPlan {
+  int small, split, full, blocks;
+  size_t part;
+};
+GatedPlan gated_plan(const Desc& d, int64_t M) {
+  const int64_t T = cdiv(d.K, 64), nf = cdiv(d.N, kGF), Np = cdiv(d.N, 4) * 4;
+  const int64_t t2 = cdiv(M, 256) * nf, t1 = cdiv(M, 128) * nf;
+  GatedPlan best{};
+  double bt = 0.;
+  for (int small = M <= 128 ? 1 : 0; small < 2; ++small) {
+    const int64_t tiles = small ? t1 : t2;
+    const double c = small ? 0.7 : 1.;
+    for (int s = 1; s <= 16 && s * 4 <= T + 3; ++s) {
+      if (s > 1 && (tiles * s > 768 || (double)s * M * Np * 8. > 512e6)) break;
+      GatedPlan p{small, s, 0, (int)(tiles * s), 0};
+      double t;
+      if (!small && s == 1) {   // the last round in halves where they fit one
+        const int64_t rest = tiles % 256;
+        p.full = (int)(rest && rest <= 128 ? tiles - rest : tiles);
+        p.blocks = (int)(p.full + 2 * (tiles - p.full));
+        t = (double)(T + 8) * ((double)cdiv(p.full, 256) + (p.full < tiles ? 0.7 : 0.));
+      } else {
+        p.full = small ? 0 : p.blocks;
+        t = (double)cdiv(tiles * s, 256) * (double)(cdiv(T, s) + 8) * c;
+      }
+      if (s > 1) {
+        t += 2.2 + (double)s * M * Np * 16. / 4e12 / 1.85e-6;
+        p.part = (size_t)s * (size_t)M * 2u * (size_t)Np * 4u;
+      }
+      if (bt == 0. || t < bt) {
+        bt = t;
+        best = p;
+      }
+    }
+  }
+  return best;
+}
+
 template <int KIND>
 void (*pick(bool ch))(GatedK) { return ch ? k_gated<KIND, true> : k_gated<KIND, false>; }
 
 }  // namespace
 
 size_t gated_workspace_bytes(const Desc& d, int64_t M) {
-  return frag_bytes(d, M) + (size_t)cdiv(M, 32) * 128u;
+  return frag_bytes(d, M) + (size_t)cdiv(M, 32) * 128u + gated_plan(d, M).part;
 }
 
 hipError_t launch_gated(const Desc& d, const GatedArgs& g, void* ws, hipStream_t s) {
@@ -648,22 +771,23 @@ hipError_t launch_gated(const Desc& d, const GatedArgs& g, void* ws, hipStream_t
   a.act = g.act;
   a.MB = (int)cdiv(g.M, 32);
   a.T = (int)cdiv(d.K, 64);
-  a.small = g.M <= 128;
+  const GatedPlan p = gated_plan(d, g.M);
+  a.small = p.small;
+  a.split = p.split;
+  a.full = p.full;
   a.tilesM = (int)cdiv(g.M, 256);
-  const int64_t tiles = a.tilesM * cdiv(d.N, kGF);
-  int64_t blocks = tiles;
-  if (!a.small) {
-    const int64_t rest = tiles % 256;
-    a.full = (int)(rest && rest <= 128 ? tiles - rest : tiles);
-    blocks = a.full + 2 * (tiles - a.full);
-  }
+  a.tilesM1 = (int)cdiv(g.M, 128);
+  a.Np = cdiv(d.N, 4) * 4;
+  if (p.split > 1)
+    a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + frag_bytes(d, g.M) +
+                                      (size_t)a.MB * 128u);
   StageArgs sa{};
   sa.d = static_cast<const uint16_t*>(g.x);
   sa.xf = ws;
   sa.xe = xe;
   sa.M = g.M;
   sa.N = d.K;
-  const hipError_t e = launch_stage(sa, g.xdt, false, 0, true, s);
+  hipError_t e = launch_stage(sa, g.xdt, false, 0, true, s);
   if (e != hipSuccess) return e;
   // whole 16-byte metadata chunks per row
   const bool ch = d.fmt == Q4K ? d.K % 512 == 0 : d.fmt == SYM4 ? d.K % (4 * d.gs) == 0
@@ -673,7 +797,10 @@ hipError_t launch_gated(const Desc& d, const GatedArgs& g, void* ws, hipStream_t
                      : d.fmt == SYM4 ? (d.gs == d.K ? k_gated<G_SYM4C, true> : pick<G_SYM4>(ch))
                      : d.bits == 2 ? pick<G_AFF2>(ch)
                      : d.bits == 4 ? pick<G_AFF4>(ch) : pick<G_AFF8>(ch);
-  hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL(fn, dim3((unsigned)p.blocks), dim3(kThreads), 0, s, a);
+  if ((e = hipGetLastError()) != hipSuccess || p.split == 1) return e;
+  auto join = g.act == ACT_SILU ? k_gated_join<ACT_SILU> : k_gated_join<ACT_GELU_TANH>;
+  hipLaunchKernelGGL(join, dim3((unsigned)cdiv(g.M * cdiv(d.N, kCkptGroup), 4)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

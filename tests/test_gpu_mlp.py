@@ -245,11 +245,17 @@ GATED_SIZES = [(1, 48, 512), (1, 1, 256), (3, 100, 256), (8, 64, 768), (16, 257,
                (2, 33, 4096), (2, 50, 8192), (2, 40, 512)]
 
 
-@pytest.mark.parametrize("M,N,K", GATED_SIZES)
+# enough tiles for whole rounds, a last round in halves, and halves alone
+LARGE = [(1000, 6000, 256), (1500, 8000, 256), (700, 5000, 256), (700, 5006, 256)]
+
+
+@pytest.mark.parametrize("M,N,K", GATED_SIZES + LARGE)
 @pytest.mark.parametrize("save", [False, True])
 def test_gated_forward(q, M, N, K, save):
     rng = np.random.default_rng(M + N)
     for i, d in enumerate(formats(q, N, K)):
+        if (M, N, K) in LARGE and (d.fmt, d.group_size) not in (("affine", 64), ("sym4", K), ("q6k", 16)):
+            continue
         dt, kind = ("bf16", "f16")[i % 2], ("silu", "gelu_tanh")[(i // 2) % 2]
         hd = (dt, "f32")[i % 3 == 2]
         print("gated", M, N, K, d.fmt, d.bits, d.group_size, dt, hd, kind, save, flush=True)
