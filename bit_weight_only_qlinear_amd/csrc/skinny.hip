@@ -273,12 +273,20 @@ __device__ __forceinline__ uint32_t spread2(uint32_t p) { return (p & 0xFFu) | (
 // (0, 4, 1, 5, 2, 6, 3, 7), each MAG + u exactly.
 template <int KIND, bool XBF16>
 __device__ __forceinline__ uint4 code_frag(uint32_t w, uint32_t w2, uint32_t hq) {
-  const uint32_t magic = XBF16 ? 0x43004300u : 0x64006400u;
+  // The constants in registers the compiler cannot see through: as literals
+  // they would need an and and an or each; so the pair is one v_and_or_b32,
+  // emitted by the compiler (which knows what an MFMA operand has to wait for).
+  // (Nibbles and 2-bit codes 2 to 5% faster; Q6K's longer expression 1% slower.)
+  const uint32_t mlit = XBF16 ? 0x43004300u : 0x64006400u;
+  uint32_t magic = mlit, m4 = 0x000F000Fu, m2 = 0x00030003u;
+  asm("" : "+v"(magic));
+  asm("" : "+s"(m4));
+  asm("" : "+s"(m2));
   uint32_t p[4];
   if constexpr (KIND == S_AFF2) {
     const uint32_t q = spread2(w);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = ((q >> (2 * e)) & 0x00030003u) | magic;
+    for (int e = 0; e < 4; ++e) p[e] = ((q >> (2 * e)) & m2) | magic;
   } else if constexpr (KIND == S_AFF8) {
     // w: codes 0-3 (bytes), w2: codes 4-7
     if constexpr (XBF16) {
@@ -297,10 +305,10 @@ __device__ __forceinline__ uint4 code_frag(uint32_t w, uint32_t w2, uint32_t hq)
     const uint32_t q = spread2(hq);   // high 2 bits of the 8 codes
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      p[e] = ((w >> (4 * e)) & 0x000F000Fu) | (((q >> (2 * e)) & 0x00030003u) << 4) | magic;
+      p[e] = ((w >> (4 * e)) & 0x000F000Fu) | (((q >> (2 * e)) & 0x00030003u) << 4) | mlit;
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = ((w >> (4 * e)) & 0x000F000Fu) | magic;
+    for (int e = 0; e < 4; ++e) p[e] = ((w >> (4 * e)) & m4) | magic;
   }
   return make_uint4(p[0], p[1], p[2], p[3]);
 }
