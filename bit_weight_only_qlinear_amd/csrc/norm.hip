@@ -685,16 +685,17 @@ hipError_t launch_norm_bwd(const void* dy, const void* s, const void* sq, const 
   const unsigned P = (unsigned)norm_bwd_parts(M);
   hipError_t e;
   if (K % 8 || nq > 2048) {
-    if (ds) {
-      auto fn = bf ? (ck ? k_norm_bwd_any<true, true> : k_norm_bwd_any<true, false>)
-                   : (ck ? k_norm_bwd_any<false, true> : k_norm_bwd_any<false, false>);
-      hipLaunchKernelGGL(fn, dim3((unsigned)M), dim3(kAny), 0, st, a);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
+    // dw first: ds may be dy itself
     if (dw) {
       auto fn = bf ? (ck ? k_norm_dw_any<true, true> : k_norm_dw_any<true, false>)
                    : (ck ? k_norm_dw_any<false, true> : k_norm_dw_any<false, false>);
       hipLaunchKernelGGL(fn, dim3((unsigned)((K + 255) / 256), P), dim3(256), 0, st, a);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (ds) {
+      auto fn = bf ? (ck ? k_norm_bwd_any<true, true> : k_norm_bwd_any<true, false>)
+                   : (ck ? k_norm_bwd_any<false, true> : k_norm_bwd_any<false, false>);
+      hipLaunchKernelGGL(fn, dim3((unsigned)M), dim3(kAny), 0, st, a);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   } else {

@@ -146,6 +146,24 @@ def test_norm_backward(q, M, K, dt, saved):
     assert torch.equal(a, only) and torch.equal(b, dw2)
 
 
+@pytest.mark.parametrize("K", [512, 515, 40960])
+@pytest.mark.parametrize("alias", ["dy", "ds_in"])
+def test_norm_backward_in_place(q, K, alias):
+    """ds written over dy or ds_in (the C call takes the output's address)."""
+    rng = np.random.default_rng(K)
+    M = 9
+    s, dy, di = (dev(rng.normal(size=(M, K)), "bf16")[0] for _ in range(3))
+    w, r = dev(rng.normal(size=K), "bf16")[0], torch.rand(M, device="cuda") + 0.5
+    ds, dw = q.qnorm_backward(dy, s, r, w, ds_in=di)
+    out = dy if alias == "dy" else di
+    dw2 = torch.empty_like(dw)
+    ws = torch.empty(M * K * 4, dtype=torch.uint8, device="cuda")
+    q._check(q.lib.qnorm_backward(dy.data_ptr(), s.data_ptr(), None, None, 1, M, K, w.data_ptr(),
+                                  r.data_ptr(), di.data_ptr(), out.data_ptr(), dw2.data_ptr(),
+                                  ws.data_ptr(), ws.numel(), q._stream()))
+    assert torch.equal(out, ds) and torch.equal(dw2, dw)
+
+
 # ---------------------------------------------------------------- checkpoints
 @pytest.mark.parametrize("M,K", [(1, 1), (2, 63), (3, 64), (5, 65), (1, 72), (4, 128), (19, 1000),
                                  (33, 4099), (7, 14336)])
