@@ -706,7 +706,13 @@ GatedForm gated_form(const qp::Desc& d, int64_t M, bool save) {
   for (int i = 0; i < 5; ++i) small_bufs = small_bufs && b[i] < (size_t(1) << 31);
   if (save || !small_bufs || M > 16) return GATED_STAGED;
   if (qp::gated_gemv_supported(d, M)) return GATED_GEMV;
-  return qp::skinny_supported(d) ? GATED_SKINNY : GATED_STAGED;
+  // Per-channel SYM4 sums (1024 + u) x (fp16) over the whole row before the
+  // offset is taken away: about 2^-24 1024 K / 45 scales of rounding, against
+  // an element bound of 0.07 scales for rows of unit activations -- a
+  // fifteenth of it at K = 8192, more than all of it at 65536.  The staged
+  // form sums q x.
+  const bool long_row = d.fmt == qp::SYM4 && d.gs == d.K && d.K > 8192;
+  return qp::skinny_supported(d) && !long_row ? GATED_SKINNY : GATED_STAGED;
 }
 
 }  // namespace
@@ -825,7 +831,8 @@ qp_status qlinear_gated_forward(const qp_desc* d, const void* x, int32_t x_dtype
                    {gate_scales, "gate_scales", save}, {up_codes, "up_codes", save},
                    {up_scales, "up_scales", save}});
   if (st != QP_OK) return st;
-  if (h == x) return fail(QP_EINVAL, "h must be a buffer of its own");
+  if (h == x || (save && (gate_codes == up_codes || gate_scales == up_scales)))
+    return fail(QP_EINVAL, "h and the checkpoints must be buffers of their own");
   const GatedForm form = gated_form(dd, M, save);
   if (form == GATED_STAGED) {
     st = check_workspace(workspace, workspace_bytes, qp::gated_workspace_bytes(dd, M));

@@ -45,8 +45,7 @@ constexpr uint32_t kDTile = kDK * kDN * 2u;
 constexpr uint32_t kOff = 0x80000000u;   // past every resource: reads 0
 
 struct DxK {
-  Bufs w[2];
-  int parts;               // 1, or 2 (gated)
+  Bufs w[2];               // the layer; gate and up
   int64_t N, K, M;
   int gs;
   const unsigned char* xf; // staged D: [step][4][MB][64] 16-byte chunks
@@ -70,7 +69,7 @@ struct DStage {
 
 // Per-lane offsets inside a step's 64 rows (kOff for columns past K).
 struct DOff {
-  uint32_t w, h, s, z, p;
+  uint32_t w, h, s, p;   // s: scales, and zeros alike
 };
 
 template <int KIND>
@@ -290,7 +289,7 @@ k_dx(DxK a) {
     const uint32_t Ku = (uint32_t)K, gs = (uint32_t)a.gs;
     o.w = ok ? row * R + kcu / cb : kOff;
     o.h = ok ? row * (Ku / 4u) + kcu / 4u : kOff;
-    o.p = o.z = 0;
+    o.p = 0;
     if constexpr (KIND == G_Q4K) {
       o.s = row * (Ku / 32u) + kcu / 32u;
       o.p = ok ? row * (Ku / 256u) * 4u + (kcu / 256u) * 4u : kOff;
@@ -572,7 +571,6 @@ hipError_t launch_dx(const Desc& d, const DxArgs& a, hipStream_t s) {
   DxK k{};
   k.w[0] = a.w;
   k.w[1] = a.w2;
-  k.parts = a.gated ? 2 : 1;
   k.N = d.N;
   k.K = d.K;
   k.M = a.M;

@@ -144,6 +144,9 @@ class QDesc:
         """(name, bytes) of every buffer, from the library."""
         return tuple(qpack_sizes(self).items())
 
+    def __getstate__(self):   # the cached C form stays with the process
+        return {k: v for k, v in self.__dict__.items() if not k.startswith("_")}
+
     def c(self):
         return _Desc(FMT_IDS[self.fmt], self.bits, self.group_size, self.super_block,
                      DTYPE_IDS[self.meta], 0, self.N, self.K)
@@ -456,7 +459,8 @@ def _run(device, fn, *args):
     """Calls a library function on the device's current stream (appended as
     the last argument), with that device current."""
     import torch
-    stream = torch._C._cuda_getCurrentRawStream(device.index)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without a Stream object
+    stream = raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
     if torch.cuda.current_device() == device.index:
         status = fn(*args, stream)
     else:

@@ -260,7 +260,7 @@ def product_tolerance(D, w):
 GATED_SIZES = [(1, 48, 512), (1, 1, 256), (3, 100, 256), (8, 64, 768), (16, 257, 512), (17, 130, 512),
                (70, 64, 256), (300, 200, 512), (5, 96, 96), (40, 33, 160), (2, 65, 320), (33, 448, 320),
                (1, 300, 4096), (1, 33, 5120), (1, 70, 8192), (1, 37, 16384), (1, 90, 1056), (6, 35, 4096),
-               (2, 33, 4096), (2, 50, 8192), (2, 40, 512)]
+               (2, 33, 4096), (2, 50, 8192), (2, 40, 512), (1, 20, 65536), (4, 20, 65536)]
 
 
 # enough tiles for whole rounds, a last round in halves, and halves alone
@@ -540,6 +540,44 @@ def test_outputs_stay_inside(q):
         assert torch.all(t[used:] == 77), k
     assert torch.equal(outs["h"][0][:M * N].view(M, N),
                        q.qlinear_gated_forward(d, x, bg, bu, save=True).h)
+
+
+def test_offsets_past_32_bits(q):
+    """Matrices of more than 2^32 elements or bytes: their last rows against
+    the same rows alone."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    M, K = 66000, 65536
+    x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    x[:] = torch.randn((1, K), device="cuda", generator=g)
+    x[-8:] = torch.randn((8, K), device="cuda", generator=g)
+    codes, scales = q.qpack_checkpoint(x)
+    c8, s8 = q.qpack_checkpoint(x[-8:].contiguous())
+    assert torch.equal(codes[-8:], c8) and torch.equal(scales[-8:], s8)
+    y = q.qpack_checkpoint_restore((codes, scales))
+    assert torch.equal(y[-8:], q.qpack_checkpoint_restore((c8, s8)))
+    assert torch.equal(codes[0], codes[M // 2]) and torch.equal(y[1], y[M // 2])
+    del codes, scales, y
+    o, t = q.qnorm_forward(x, need_rstd=True), q.qnorm_forward(x[-8:].contiguous(), need_rstd=True)
+    assert torch.equal(o.y[-8:], t.y) and torch.equal(o.rstd[-8:], t.rstd)
+    ds, _ = q.qnorm_backward(o.y, x, o.rstd, need_dweight=False)
+    d8, _ = q.qnorm_backward(t.y, x[-8:].contiguous(), t.rstd, need_dweight=False)
+    assert torch.equal(ds[-8:], d8)
+    del o, ds, x
+    M, N, K = 140000, 16384, 128
+    d = q.QDesc.affine(N, K, 4, 64, "bf16")
+    w = [q.qpack_quantize(d, torch.randn((N, K), device="cuda", generator=g) * 0.1) for _ in range(2)]
+    x = torch.randn((M, K), device="cuda", generator=g).bfloat16()
+    f = q.qlinear_gated_forward(d, x, *w, save=True)
+    e = q.qlinear_gated_forward(d, x[-300:].contiguous(), *w, save=True)
+    # other tiles, another order of the fp32 sums: a bf16 step at most
+    assert oracle.rel_l2(f64(f.h[-300:]), f64(e.h)) <= 2.0 ** -8
+    assert oracle.rel_l2(f64(f.up[0][-300:]), f64(e.up[0])) <= 2.0 ** -8
+    b = q.qlinear_gated_backward(d, f.h, *w, f.gate, f.up)
+    tail = [tuple(v[-300:].contiguous() for v in ck) for ck in (f.gate, f.up)]
+    c = q.qlinear_gated_backward(d, f.h[-300:].contiguous(), *w, *tail)
+    assert torch.equal(b.dgate[-300:], c.dgate) and torch.equal(b.dup[-300:], c.dup)
+    assert oracle.rel_l2(f64(b.dx[-300:]), f64(c.dx)) <= 2.0 ** -8
 
 
 def test_binding_refuses_wrong_tensors(q):

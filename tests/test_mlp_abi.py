@@ -99,8 +99,9 @@ def test_gated_refusals(q):
         (dict(ck=(FAKE, FAKE, FAKE, None)), 1, "up_scales"),
         (dict(ck=(FAKE, FAKE, FAKE + 4, FAKE)), 4, "up_codes"), (dict(M=17, ws=FAKE + 4, n=1 << 30), 4, "workspace"),
         (dict(M=17), 1, "workspace is NULL"), (dict(M=17, ws=FAKE, n=16), 1, "too small"),
-        (dict(ck=(FAKE,) * 4), 1, "workspace is NULL"), (dict(d=D.affine(64, 96, 4, 32)), 1, "workspace is NULL"),
-        (dict(M=1, ck=(FAKE,) * 4), 1, "workspace is NULL"),
+        (dict(ck=(FAKE, FAKE, FAKE, OTHER)), 1, "own"), (dict(ck=(FAKE, FAKE, OTHER, FAKE)), 1, "own"),
+        (dict(ck=(FAKE, FAKE, OTHER, OTHER)), 1, "workspace is NULL"), (dict(d=D.affine(64, 96, 4, 32)), 1, "workspace is NULL"),
+        (dict(M=1, ck=(FAKE, FAKE, OTHER, OTHER)), 1, "workspace is NULL"),
         (dict(g=q._Weights(FAKE, None, None, FAKE, None)), 1, "scales"),
         (dict(u=q._Weights(FAKE + 4, None, FAKE, FAKE, None)), 4, "qweight"),
     ]:
@@ -163,3 +164,12 @@ def test_binding_refuses_host_tensors_and_shapes(q):
         q._torch_dt("f64")
     with pytest.raises(ValueError):
         q._act_id("relu")
+
+
+def test_descriptor_is_copied_and_pickled_after_use(q):
+    import copy
+    import pickle
+    d = q.QDesc.affine(64, 512)
+    d._cref, d._buffer_sizes
+    for e in (pickle.loads(pickle.dumps(d)), copy.deepcopy(d), copy.copy(d)):
+        assert e == d and hash(e) == hash(d) and e._buffer_sizes == d._buffer_sizes
