@@ -898,7 +898,7 @@ GemvFn pick_gated(int mt, int cpl) {
     return base_kind(KIND) != K_AFF8 && base_kind(KIND) != K_Q4K && base_kind(KIND) != K_Q6K ? nullptr
          : cpl == 1 ? k_gemv<KIND, XB, 2, 1, 1, true>
          : cpl == 2 ? k_gemv<KIND, XB, 2, 2, 1, true>
-         : cpl == 3 ? k_gemv<KIND, XB, 2, 3, 1, true> : k_gemv<KIND, XB, 2, 4, 1, true>;
+                    : k_gemv<KIND, XB, 2, KIND == K_Q4K ? 3 : 2, 1, true>;
   return cpl == 1 ? k_gemv<KIND, XB, 1, 1, 1, true>
        : cpl == 2 ? k_gemv<KIND, XB, 1, 2, 1, true>
        : cpl == 3 ? k_gemv<KIND, XB, 1, 3, 1, true> : k_gemv<KIND, XB, 1, 4, 1, true>;
@@ -941,6 +941,18 @@ bool gemv_plan(int k, int C, int* mt, int* KW, int* cpl) {
       }
     }
   }
+  return false;
+}
+
+// The gated pair's: two rows take two chunks per lane at most (Q4K three: 5120
+// -> 25600 43.2 us a pair, 48.0 with two and the row over two waves).  Where
+// int8 codes would take four, both layers' codes in flight spill (4096 -> 14336
+// 27.2 us, 26.0 with two).
+bool gated_gemv_plan(int kind, int C, int64_t M, int* KW, int* cpl) {
+  int mt = (int)M;
+  if (M == 1) return gemv_plan(kind, C, &mt, KW, cpl);
+  for (*KW = 1; *KW <= 4; *KW *= 2)
+    if ((*cpl = (C + 64 * *KW - 1) / (64 * *KW)) <= (kind == K_Q4K ? 3 : 2)) return true;
   return false;
 }
 
@@ -1082,13 +1094,13 @@ hipError_t launch_gemv(const Desc& d, const void* x, int xdt, int64_t M, const B
 
 // One activation row: every format.  Two: the formats whose streaming kernel
 // still beats an MFMA tile there (us a pair, in a
-// HIP graph: int8 affine 4096 -> 14336 27.0 against 35.5, Q4K 5120 -> 25600
+// HIP graph: int8 affine 4096 -> 14336 26.0 against 35.5, Q4K 5120 -> 25600
 // 44.3 against 59.3, Q6K 8192 -> 8192 28.8 against 39.6).
 bool gated_gemv_supported(const Desc& d, int64_t M) {
   const int kind = gemv_kind(d), bk = base_kind(kind);
   if (M != 1 && !(M == 2 && (bk == K_AFF8 || bk == K_Q4K || bk == K_Q6K))) return false;
-  int mt = (int)M, kw = 0, cpl = 0;
-  if (!gemv_plan(kind, gemv_chunks(d, kind), &mt, &kw, &cpl) || mt != M) return false;
+  int kw = 0, cpl = 0;
+  if (!gated_gemv_plan(kind, gemv_chunks(d, kind), M, &kw, &cpl)) return false;
   // both layers' metadata of one feature per wave and the activation row in LDS
   uint32_t row[kMeta], off[kMeta];
   meta_rows(d, true, row);
@@ -1100,8 +1112,9 @@ hipError_t launch_gated_gemv(const Desc& d, const GatedArgs& g, const size_t byt
                              hipStream_t s) {
   const int kind = gemv_kind(d);
   const int C = gemv_chunks(d, kind);
-  int mt = (int)g.M, KW = 1, cpl = 0;
-  if (g.gq || !gated_gemv_supported(d, g.M) || !gemv_plan(kind, C, &mt, &KW, &cpl))
+  const int mt = (int)g.M;
+  int KW = 1, cpl = 0;
+  if (g.gq || !gated_gemv_supported(d, g.M) || !gated_gemv_plan(kind, C, g.M, &KW, &cpl))
     return hipErrorInvalidValue;
   GemvFn fn = pick_gated(kind, g.xdt == BF16, mt, cpl);
   if (!fn) return hipErrorInvalidValue;

@@ -260,7 +260,8 @@ def product_tolerance(D, w):
 GATED_SIZES = [(1, 48, 512), (1, 1, 256), (3, 100, 256), (8, 64, 768), (16, 257, 512), (17, 130, 512),
                (70, 64, 256), (300, 200, 512), (5, 96, 96), (40, 33, 160), (2, 65, 320), (33, 448, 320),
                (1, 300, 4096), (1, 33, 5120), (1, 70, 8192), (1, 37, 16384), (1, 90, 1056), (6, 35, 4096),
-               (2, 33, 4096), (2, 50, 8192), (2, 40, 512), (1, 20, 65536), (4, 20, 65536)]
+               (2, 33, 4096), (2, 50, 8192), (2, 40, 512), (1, 20, 65536), (4, 20, 65536), (2, 31, 2560),
+               (2, 37, 5120), (16, 41, 2176)]
 
 
 # enough tiles for whole rounds, a last round in halves, and halves alone
