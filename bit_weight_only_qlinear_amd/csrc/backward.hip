@@ -456,13 +456,15 @@ k_dx(DxK a) {
           v.w = ldexpf(acc[i][j][4 * gg + 3], -xe);
           *reinterpret_cast<float4*>(lds + r0 * 256 + ((8 * (i & 1) + 2 * gg + hh) ^ (r0 & 15)) * 16) = v;
         });
+        lds_turn();
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {   // same wave: LDS operations stay in order
+        for (int t = 0; t < 8; ++t) {
           const int r = 4 * t + (el >> 4), c = el & 15;
           const float4 v = *reinterpret_cast<const float4*>(lds + r * 256 + (c ^ (r & 15)) * 16);
           const int64_t k = kw + 64 * h + 4 * c;
           if (mb + r < a.M && k < K) *reinterpret_cast<float4*>(out + (mb + r) * K + k) = v;
         }
+        lds_turn();
       });
     } else {
       const int xe = mb + r0 < a.M ? a.xe[mb + r0] : 0;
@@ -477,6 +479,7 @@ k_dx(DxK a) {
         *reinterpret_cast<uint2*>(lds + r0 * 256 + ((4 * i + gg) ^ (r0 & 15)) * 16 + 8 * hh) =
             make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
       });
+      lds_turn();
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         const int r = 4 * t + (el >> 4), c = el & 15;
@@ -485,6 +488,7 @@ k_dx(DxK a) {
         if (mb + r < a.M && k < K)
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dx) + (mb + r) * K + k) = v;
       }
+      lds_turn();
     }
   });
 }

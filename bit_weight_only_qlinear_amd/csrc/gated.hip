@@ -391,7 +391,8 @@ __device__ __forceinline__ void finish(const GatedK& a, float16_t (&acc)[4][J], 
         }
       }
     });
-    if (lines) {   // same wave: LDS operations stay in order
+    if (lines) {
+      lds_turn();
       unsigned char* h = static_cast<unsigned char*>(a.h);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -411,6 +412,7 @@ __device__ __forceinline__ void finish(const GatedK& a, float16_t (&acc)[4][J], 
           }
         }
       }
+      lds_turn();
     }
   });
 }

@@ -42,4 +42,11 @@ __device__ __forceinline__ void act_fd(float g, float& f, float& d) {
   d = s + (m > 0.f ? g * sl * m : 0.f);
 }
 
+// Between a wave's LDS writes and its other lanes' reads of them: the LDS
+// takes one wave's operations in order, so only the compiler has to keep it.
+__device__ __forceinline__ void lds_turn() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 }  // namespace qp
