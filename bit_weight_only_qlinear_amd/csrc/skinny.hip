@@ -36,6 +36,14 @@
 // per-lane loads straight from HBM, 16 rows per instruction, cost more than
 // the codes themselves; they remain only for rows too long for LDS.
 //
+// Registers: at most 128, so that two blocks share a CU and one's start and
+// end run beside the other's loop.  So a step's activations, read from L2, are
+// replaced by the next block's as they are used (two stages of them would be
+// 16 registers more), and a block's sums are held to its own iteration.  With
+// 8 rows, a gated pair of Q4K 5120 -> 25600: 63 us with one block per CU, 52
+// with two; int8 4096 -> 14336 gs64 37.8 and 32.8; Q6K 8192 -> 8192 41.5 and
+// 38.4.  Four or six waves per block, and two stages ahead, gained nothing.
+//
 // Sources: HF Transformers "Metal" page (uint32 codes, per-group scale and
 // bias, bits 2/4/8); ExecuTorch PR #20571 "Quant schema update" (Q4_K/Q6_K-
 // style nested metadata); ExecuTorch PR #16577 (symmetric int4, stored as
@@ -147,7 +155,6 @@ struct SxStage {
   // int2 2 words, int4 4, int8 8; Q6K 4 low-nibble words + 2 high-bit words
   uint32_t w[2][code_bits(KIND)];
   uint32_t h[2][KIND == S_Q6K ? 2 : 1];
-  uint4 x[4];            // activations, 8 columns per MFMA step
   uint32_t m[2][meta_words<KIND, GS>()];
   uint32_t st[2];        // Q4K step word / Q6K fp16 step (per 256 columns)
 };
@@ -189,25 +196,16 @@ __device__ __forceinline__ void meta_ld(const SxArgs& a, const unsigned char* ld
   }
 }
 
-// PART: 3 = everything; 1 = the global loads only (codes, activations, and
-// metadata when it is not staged); 2 = the staged metadata only (LDS reads).
+// PART: 3 = everything; 1 = the global loads only (codes, and metadata when
+// it is not staged); 2 = the staged metadata only (LDS reads).
 template <int KIND, int GS, bool LDSM, int PART = 3, bool GATED = false>
 __device__ __forceinline__ void sx_load(const SxArgs& a, const unsigned char* lds, int kb, int lane,
-                                        int64_t n0, int64_t mrow, SxStage<KIND, GS>& s) {
+                                        int64_t n0, SxStage<KIND, GS>& s) {
   const uint32_t c0 = (uint32_t)kb * kSxCols;
   const int g = lane >> 4, r16 = lane & 15;
   constexpr bool GLOB = (PART & 1) != 0;
   constexpr bool META = LDSM ? (PART & 2) != 0 : GLOB;
   const uint32_t K = (uint32_t)a.K;
-  // activations of row mrow: step t takes columns c0 + 32 t + 8 g .. + 8
-  const __amdgpu_buffer_rsrc_t rx = rsrc(a.x, a.x_bytes);
-  const uint32_t xo = mrow < a.M ? (uint32_t)mrow * K * 2u + 2u * (c0 + 8u * g) : kOOB;
-  if constexpr (GLOB) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      s.x[t] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             rx, xo == kOOB ? kOOB : xo + 64u * t, 0, 0));
-  }
   constexpr uint32_t B = code_bits(KIND);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -402,19 +400,29 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
                               coff | (coff << 16));
 
   // group gg of the block is complete in Dd, DXd: apply its (S, T)
-  auto epilogue = [&](const SxStage<KIND, GS>& s, int gg, const float4_t (&Dd)[2],
-                      const float4_t& DXd) __attribute__((always_inline)) {
+  auto apply = [&](const SxStage<KIND, GS>& s, int i, int gg, const float4_t& Dd,
+                   const float4_t& DXd) __attribute__((always_inline)) {
+    float S, T;
+    group_st<KIND, GS, MBF16>(s, i, gg, MAG, S, T);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float S, T;
-      group_st<KIND, GS, MBF16>(s, i, gg, MAG, S, T);
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        acc[i][v] = COFF ? fmaf(S, Dd[i][v], acc[i][v]) : fmaf(T, DXd[v], fmaf(S, Dd[i][v], acc[i][v]));
-    }
+    for (int v = 0; v < 4; ++v)
+      acc[i][v] = COFF ? fmaf(S, Dd[v], acc[i][v]) : fmaf(T, DXd[v], fmaf(S, Dd[v], acc[i][v]));
   };
 
-  auto compute = [&](const SxStage<KIND, GS>& s) __attribute__((always_inline)) {
+  // Activations of row mrow: step t of column block kb takes columns 128 kb +
+  // 32 t + 8 g .. + 8.  One block's worth: a step's are replaced by the next
+  // block's as soon as they are used.
+  uint4 X[4];
+  const uint32_t xv = mrow < a.M ? (uint32_t)mrow * (uint32_t)a.K * 2u + 16u * g : kOOB;
+  auto ld_x = [&](int kb, int t) __attribute__((always_inline)) {
+    // past the last block: an empty resource
+    const __amdgpu_buffer_rsrc_t r = rsrc(a.x, kb < KB ? a.x_bytes : 0u);
+    X[t] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                                         r, xv, (uint32_t)kb * (2u * kSxCols) + 64u * t, 0));
+  };
+
+  // a block's stage, and the block whose activations are loaded next
+  auto compute = [&](const SxStage<KIND, GS>& s, int kbn) __attribute__((always_inline)) {
     // code words of both tiles, transposed so that step t is columns
     // 32 t .. 32 t + 31 of the block (2-bit fields: 16 bits per 8 columns;
     // every index is a compile-time constant, so all stays in registers)
@@ -450,22 +458,23 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
       constexpr int t = decltype(TT)::value;
       if constexpr (KIND == S_Q6K) {
         // two groups per step: lane groups 0-1 (group 2 t), 2-3 (2 t + 1)
-        const uint4 Al = act_frag_sel(s.x[t], selL0, selL1);
-        const uint4 Ah = act_frag_sel(s.x[t], selH0, selH1);
-        float4_t Dh[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        const uint4 Al = act_frag_sel(X[t], selL0, selL1);
+        const uint4 Ah = act_frag_sel(X[t], selH0, selH1);
+        ld_x(kbn, t);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2; ++i) {   // a tile at a time: 8 sums live
           const uint4 Bq = code_frag<KIND, XBF16>(W[i][t], 0u, H[i][t]);
-          D[i] = mfma<XBF16>(Al, Bq, D[i]);
-          D[i] = mfma<XBF16>(Al, BC, D[i]);
-          Dh[i] = mfma<XBF16>(Ah, Bq, Dh[i]);
-          Dh[i] = mfma<XBF16>(Ah, BC, Dh[i]);
+          float4_t Dl = {0.f, 0.f, 0.f, 0.f}, Dh = {0.f, 0.f, 0.f, 0.f};
+          Dl = mfma<XBF16>(Al, Bq, Dl);
+          Dl = mfma<XBF16>(Al, BC, Dl);
+          Dh = mfma<XBF16>(Ah, Bq, Dh);
+          Dh = mfma<XBF16>(Ah, BC, Dh);
+          apply(s, i, 2 * t, Dl, DX);
+          apply(s, i, 2 * t + 1, Dh, DX);
         }
-        epilogue(s, 2 * t, D, DX);
-        epilogue(s, 2 * t + 1, Dh, DX);
-        D[0] = D[1] = float4_t{0.f, 0.f, 0.f, 0.f};
       } else {
-        const uint4 A = act_frag(s.x[t]);
+        const uint4 A = act_frag(X[t]);
+        ld_x(kbn, t);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           D[i] = mfma<XBF16>(A, code_frag<KIND, XBF16>(W[i][t], KIND == S_AFF8 ? W2[i][t] : 0u, 0u),
@@ -477,12 +486,19 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
           // a group ends every GS / 32 steps
           constexpr int spg = (GS > 0 ? GS : 128) / 32;
           if constexpr ((t + 1) % spg == 0) {
-            epilogue(s, t / spg, D, DX);
+            apply(s, 0, t / spg, D[0], DX);
+            apply(s, 1, t / spg, D[1], DX);
             D[0] = D[1] = DX = float4_t{0.f, 0.f, 0.f, 0.f};
           }
         }
       }
     });
+    // the sums of this block are taken here: moved past the loop's branch they
+    // would keep all its MFMA results live
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) asm volatile("" : "+v"(acc[i][v]));
   };
 
   // The block's metadata slabs (rows n0 .. n0 + 31, contiguous in each
@@ -509,16 +525,18 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
   // the wave's column blocks: wave, wave + 8, ...; kSxStages - 1 ahead
   SxStage<KIND, GS> st[kSxStages];
   const int J = wave < KB ? (KB - wave + kSxWaves - 1) / kSxWaves : 0;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) ld_x(wave, t);
   sfor<kSxStages - 1>([&](auto P) {
     constexpr int p = decltype(P)::value;
-    if (p < J) sx_load<KIND, GS, LDSM, 1, GATED>(a, s_meta, wave + p * kSxWaves, lane, n0, mrow, st[p]);
+    if (p < J) sx_load<KIND, GS, LDSM, 1, GATED>(a, s_meta, wave + p * kSxWaves, lane, n0, st[p]);
   });
 
   if constexpr (LDSM) {
     // the slab copies are older than the code loads: wait for them only
     // (all loads where this wave has fewer blocks than stages ahead)
     constexpr int B = code_bits(KIND);
-    constexpr int n = (kSxStages - 1) * (4 + 2 * (B == 2 ? 1 : B / 4) + (KIND == S_Q6K ? 2 : 0));
+    constexpr int n = 4 + (kSxStages - 1) * (2 * (B == 2 ? 1 : B / 4) + (KIND == S_Q6K ? 2 : 0));
     static_assert(n < 64, "vmcnt range");
     if (J >= kSxStages - 1)
       __builtin_amdgcn_s_waitcnt((n & 0xF) | (0x7 << 4) | (0xF << 8) | ((n >> 4) << 14));
@@ -530,7 +548,7 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
   if constexpr (LDSM) {
     sfor<kSxStages - 1>([&](auto P) {
       constexpr int p = decltype(P)::value;
-      if (p < J) sx_load<KIND, GS, LDSM, 2, GATED>(a, s_meta, wave + p * kSxWaves, lane, n0, mrow, st[p]);
+      if (p < J) sx_load<KIND, GS, LDSM, 2, GATED>(a, s_meta, wave + p * kSxWaves, lane, n0, st[p]);
     });
   }
   for (int j0 = 0; j0 < J; j0 += kSxStages) {
@@ -540,8 +558,8 @@ __global__ void __launch_bounds__(64 * kSxWaves) k_skinny(SxArgs a) {
       if (j < J) {
         if (j + kSxStages - 1 < J)
           sx_load<KIND, GS, LDSM, 3, GATED>(a, s_meta, wave + (j + kSxStages - 1) * kSxWaves, lane, n0,
-                                  mrow, st[(q + kSxStages - 1) % kSxStages]);
-        compute(st[q]);
+                                            st[(q + kSxStages - 1) % kSxStages]);
+        compute(st[q], wave + (j + 1) * kSxWaves);
       }
     });
   }
