@@ -436,13 +436,13 @@ qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int64_t M, int32_t sav
  * gate_codes, gate_scales, up_codes, up_scales: NULL, or 8-bit checkpoints
  * of g and u (qpack_checkpoint's layout, from the fp32 values) for
  * qlinear_gated_backward: all four or none.
- * One row, or up to 16 rows with K % 128 == 0 (and K <= 8192 for per-channel
- * SYM4), without checkpoints and with buffers below 2 GiB: exact codes, as QP_KERNEL_GEMV and
- * QP_KERNEL_GEMV_MFMA, and no workspace.  Otherwise fp16
- * MFMA as QP_KERNEL_GEMM, at any K: x staged as fp16 in the workspace (16-byte
- * aligned, busy until the call's kernels finish), each weight rounded once
- * to fp16 (per-channel SYM4: exact codes), a relative L2 error of about 3e-4
- * in g and u. */
+ * One row of K <= 8192, or up to 16 rows with K % 128 == 0 (and K <= 8192 for
+ * per-channel SYM4), without checkpoints and with buffers below 2 GiB: exact
+ * codes, as QP_KERNEL_GEMV and QP_KERNEL_GEMV_MFMA, and no workspace.
+ * Otherwise (but for some longer single rows) fp16 MFMA as QP_KERNEL_GEMM, at
+ * any K: x staged as fp16 in the workspace (16-byte aligned, busy until the
+ * call's kernels finish), each weight rounded once to fp16 (per-channel SYM4:
+ * exact codes), a relative L2 error of about 3e-4 in g and u. */
 qp_status qlinear_gated_forward(const qp_desc* d, const void* x, int32_t x_dtype, int64_t M,
                                 const qp_weights* gate, const qp_weights* up, const void* bias_gate,
                                 const void* bias_up, int32_t act, void* h, int32_t h_dtype,
