@@ -1093,9 +1093,9 @@ hipError_t launch_gemv(const Desc& d, const void* x, int xdt, int64_t M, const B
 }
 
 // One activation row: every format.  Two: the formats whose streaming kernel
-// still beats an MFMA tile there (us a pair, in a
-// HIP graph: int8 affine 4096 -> 14336 26.0 against 35.5, Q4K 5120 -> 25600
-// 44.3 against 59.3, Q6K 8192 -> 8192 28.8 against 39.6).
+// still beats an MFMA tile there (us a pair in a HIP graph, against the tile's
+// with three rows: int8 affine 4096 -> 14336 26.0 and 31.0, Q4K 5120 -> 25600
+// 43.2 and 46.2, Q6K 8192 -> 8192 27.6 and 36.8).
 bool gated_gemv_supported(const Desc& d, int64_t M) {
   const int kind = gemv_kind(d), bk = base_kind(kind);
   if (M != 1 && !(M == 2 && (bk == K_AFF8 || bk == K_Q4K || bk == K_Q6K))) return false;
