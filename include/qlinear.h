@@ -434,8 +434,9 @@ qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int64_t M, int32_t sav
  * biases [N] of x_dtype or NULL; h [M, N] in h_dtype (QP_F16, QP_BF16 or
  * QP_F32), rounded once from fp32.  act: qp_act.
  * gate_codes, gate_scales, up_codes, up_scales: NULL, or 8-bit checkpoints
- * of g and u (qpack_checkpoint's layout, from the fp32 values) for
- * qlinear_gated_backward: all four or none.
+ * of g and u (qpack_checkpoint's layout, from the fp32 values with the errors
+ * below: about 1 code in 100 is its neighbour) for qlinear_gated_backward: all
+ * four or none.
  * One row of K <= 8192, or up to 16 rows with K % 128 == 0 (and K <= 8192 for
  * per-channel SYM4), without checkpoints and with buffers below 2 GiB: exact
  * codes, as QP_KERNEL_GEMV and QP_KERNEL_GEMV_MFMA, and no workspace.
