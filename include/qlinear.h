@@ -435,7 +435,7 @@ qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int64_t M, int32_t sav
  * QP_F32), rounded once from fp32.  act: qp_act.
  * gate_codes, gate_scales, up_codes, up_scales: NULL, or 8-bit checkpoints
  * of g and u (qpack_checkpoint's layout, from the fp32 values with the errors
- * below: about 1 code in 100 is its neighbour) for qlinear_gated_backward: all
+ * below: up to 1 code in 100 is its neighbour) for qlinear_gated_backward: all
  * four or none.
  * One row of K <= 8192, or up to 16 rows with K % 128 == 0 (and K <= 8192 for
  * per-channel SYM4), without checkpoints and with buffers below 2 GiB: exact
