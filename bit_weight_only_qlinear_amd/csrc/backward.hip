@@ -14,8 +14,13 @@
 //    subtract and one packed fma, and one 8-byte LDS write of four
 //    consecutive n.  The scales travel the same way: one (S, T) fp16 pair per
 //    lane and step, turned by the same swaps.
-//  * Weights in fp16, each rounded about once.  AFFINE: w = fma(q, scale,
-//    bias), both exact in fp16 (as the qGEMM takes them).  Q6K, SYM4: with v =
+//  * Weights in fp16, each rounded about once.  AFFINE of 2 and 4 bits: w =
+//    fma(q, scale, bias) on fp16 scales and biases, as the qGEMM takes them
+//    (bf16 metadata is exact there from 2^-17 up, where the weights themselves
+//    reach fp16's subnormals).  8 bits: the fp32 fma, rounded once; their
+//    scales are 255ths of a group's range, so ordinary weights (std 3e-4) have
+//    bf16 scales that fp16 cannot hold, and 255 codes carry the error (relative
+//    L2 of dx 1e-2 there, 2e-4 in fp32).  Q6K, SYM4: with v =
 //    u - 32 or u - 8 exact and the scale split into S + s (two fp16 numbers),
 //    w = fma(v, S, v s).  Q4K, scale and offset split: w = fma(q, S, T) +
 //    fma(q, s, t).  Rounding the Q4K scale and offset to one fp16 each left
@@ -136,6 +141,7 @@ struct DTurned {
   uint32_t w[KIND == G_AFF8 ? 8 : 4];   // rows 0..3 (AFF8: columns 0-3, then 4-7)
   uint32_t h[KIND == G_Q6K ? 2 : 1];    // high bits of row pairs
   half2_t S[2], T[2];                   // hi parts (Q6K, SYM4: T is the lo part of S)
+  float Sf[KIND == G_AFF8 ? 4 : 1], Tf[KIND == G_AFF8 ? 4 : 1];   // AFF8, instead
   half2_t s[KIND == G_Q4K ? 2 : 1], t[KIND == G_Q4K ? 2 : 1];   // Q4K: lo parts
 };
 
@@ -194,6 +200,15 @@ __device__ __forceinline__ void dturn(const DStage<KIND>& st, DTurned<KIND>& d) 
       d.t[i] = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m[2 * i + 1], m[2 * i], 0x07060302u));
     }
     m[0] = m[1] = m[2] = m[3] = __builtin_amdgcn_perm(ht, hs, 0x05040100u);   // hi parts
+  } else if constexpr (KIND == G_AFF8) {
+    m[0] = m[1] = m[2] = m[3] = __builtin_amdgcn_perm(st.s1, st.s0, 0x05040100u);   // as stored
+    turn4(m);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      d.Sf[i] = meta_to_f32(m[i] & 0xFFFFu, MBF16);
+      d.Tf[i] = meta_to_f32(m[i] >> 16, MBF16);
+    }
+    return;
   } else {
     half2_t v;
     v.x = (_Float16)(MBF16 ? bf16_to_f32(st.s0 & 0xFFFFu) : f16_to_f32(st.s0 & 0xFFFFu));
@@ -211,9 +226,21 @@ __device__ __forceinline__ void dturn(const DStage<KIND>& st, DTurned<KIND>& d) 
 // Columns 2 b and 2 b + 1 of the lane's 8: four consecutive n each.
 template <int KIND, int b>
 __device__ __forceinline__ void dcols(const DTurned<KIND>& d, uint32_t magic, uint32_t magic64, uint2 (&out)[2]) {
+  if constexpr (KIND == G_AFF8) {
+    constexpr int o = b < 2 ? 0 : 4, c = (2 * b) & 3;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = fmaf((float)((d.w[o + i] >> (8 * (c + e))) & 255u), d.Sf[i], d.Tf[i]);
+      out[e] = make_uint2(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]));
+    }
+    return;
+  }
   // column 2 b: 1024 + u; column 2 b + 1: for nibbles, left where they are in
   // the byte (mantissa bits 4 and up of 64, whose unit they are: 64 + u)
-  constexpr bool NIB = KIND != G_AFF2 && KIND != G_AFF8;
+  constexpr bool NIB = KIND != G_AFF2;
   constexpr float OFF = KIND == G_Q6K ? 32.f : KIND == G_SYM4 ? 8.f : 0.f;
   constexpr float M0 = 1024.f + OFF, M1 = (NIB ? 64.f : 1024.f) + OFF;
   const half2_t mag[2] = {{(_Float16)M0, (_Float16)M0}, {(_Float16)M1, (_Float16)M1}};
@@ -224,11 +251,6 @@ __device__ __forceinline__ void dcols(const DTurned<KIND>& d, uint32_t magic, ui
     if constexpr (KIND == G_AFF2) {
       q[0] = and_or(d.w[i] >> (4 * b), 0x00030003u, magic);
       q[1] = and_or(d.w[i] >> (4 * b + 2), 0x00030003u, magic);
-    } else if constexpr (KIND == G_AFF8) {
-      constexpr int o = b < 2 ? 0 : 4, c = (2 * b) & 3;
-      constexpr uint32_t s0 = 0x0C000C00u | ((4u + c) << 16) | c, s1 = s0 + 0x00010001u;
-      q[0] = __builtin_amdgcn_perm(d.w[o + 2 * i + 1], d.w[o + 2 * i], s0) | magic;
-      q[1] = __builtin_amdgcn_perm(d.w[o + 2 * i + 1], d.w[o + 2 * i], s1) | magic;
     } else {
       constexpr uint32_t sel = 0x0C000C00u | ((4u + b) << 16) | b;
       const uint32_t p = __builtin_amdgcn_perm(d.w[2 * i + 1], d.w[2 * i], sel);

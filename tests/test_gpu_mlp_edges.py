@@ -1,0 +1,41 @@
+"""GPU tests of the MLP-block operators at the ends of their ranges.
+
+Tolerances as in test_gpu_mlp.py, whose helpers are used here.
+"""
+import numpy as np
+import pytest
+
+import oracle
+from oracle import mlp
+from test_gpu_mlp import dev, f64, packed, q  # noqa: F401  (q: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+# ---------------------------------------------------------------- small weights
+# fp16 keeps weights down to 2^-14 = 6.1e-5 in full and then steps of 2^-24:
+# rounding to the nearest costs at most 2^-25 each, 2^-25 / sqrt(3) in the rms,
+# so weights of std 1e-4 lose 1.7e-4 of themselves that way, under a tenth of
+# the 2e-3; the scales (down to 1e-6) may lose no more than their own rounding.
+@pytest.mark.parametrize("std", [6e-4, 3e-4, 2e-4, 1e-4])
+@pytest.mark.parametrize("meta", ["bf16", "f16"])
+def test_backward_of_small_int8_weights(q, std, meta):
+    rng = np.random.default_rng(int(std * 1e6))
+    M, N, K = 40, 320, 256
+    for gs in (32, 64, 128):
+        print("small int8", std, meta, gs, flush=True)
+        d = q.QDesc.affine(N, K, 8, gs, meta)
+        (bg, wg), (bu, wu) = packed(q, d, rng, std), packed(q, d, rng, std)
+        dy, dy64 = dev(rng.normal(size=(M, N)), "bf16")
+        ref = dy64 @ wg
+        assert oracle.rel_l2(f64(q.qlinear_backward(d, dy, bg, dx_dtype="f32")), ref) <= 2e-3
+        ck = []
+        for _ in range(2):
+            c, s = mlp.checkpoint(rng.normal(size=(M, N)) * 2)
+            ck.append((c, s, torch.from_numpy(c).cuda(), torch.from_numpy(s).cuda()))
+        g, u = (mlp.restore(c[0], c[1]) for c in ck)
+        o = q.qlinear_gated_backward(d, dy, bg, bu, ck[0][2:], ck[1][2:], dx_dtype="f32")
+        dx, _, _ = mlp.gated_backward(dy64, g, u, wg, wu, "silu")
+        assert oracle.rel_l2(f64(o.dx), dx) <= 2e-3
