@@ -125,4 +125,13 @@ __device__ __forceinline__ float wave_max_all(float v) {
   return v;
 }
 
+// Maximum of magnitudes that keeps a NaN (fmaxf drops it): a checkpoint's
+// group with a value that is not finite gets such a scale and codes of 0, and
+// so restores as NaN.
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+__device__ __forceinline__ float wave_max_nan(float v) {
+  for (int off = 32; off > 0; off >>= 1) v = max_nan(v, __shfl_xor(v, off, 64));
+  return v;
+}
+
 }  // namespace qp

@@ -490,9 +490,9 @@ __global__ void __launch_bounds__(1024) k_col_sum(const float* __restrict__ part
 }
 
 // fl32(m / 127): the product with the reciprocal and one correction step,
-// correctly rounded away from the subnormals.
+// correctly rounded away from the subnormals and the infinity.
 __device__ __forceinline__ float scale127(float m) {
-  if (m < 1e-30f) return m / 127.f;
+  if (!(m >= 1e-30f && m < __builtin_inff())) return m / 127.f;
   constexpr float r = 1.f / 127.f;
   const float q = m * r;
   return fmaf(fmaf(-q, 127.f, m), r, q);
@@ -503,7 +503,8 @@ __device__ __forceinline__ float scale127(float m) {
 // its low bits; the product is within 4e-5 of the quotient (127 steps, 2^-23
 // from the reciprocal and 2^-24 more), so only a value whose product is that
 // near to a tie needs the fp64 quotient (about one wave in ten has one): with
-// one correction step that is exact at a tie, which then goes to even.
+// one correction step that is exact at a tie, which then goes to even.  Scales
+// that are not finite have 0 for the reciprocal; a NaN's low byte is 0 too.
 template <int N>
 __device__ __forceinline__ void ckpt_codes(const float (&v)[N], float sc, uint32_t (&c)[N]) {
   constexpr float magic = 12582912.f;
@@ -560,10 +561,10 @@ __global__ void __launch_bounds__(256) k_ckpt(const uint16_t* __restrict__ x, in
     float v[8], mx = 0.f;
     unpack8<BF>(u[i], v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
-    mx = fmaxf(mx, dpp_f<QP_DPP_QUAD_1032>(0.f, mx));
-    mx = fmaxf(mx, dpp_f<QP_DPP_QUAD_2301>(0.f, mx));
-    mx = fmaxf(mx, dpp_f<QP_DPP_ROW_HALF_MIRROR>(0.f, mx));   // 8 lanes: the other four
+    for (int e = 0; e < 8; ++e) mx = max_nan(mx, fabsf(v[e]));
+    mx = max_nan(mx, dpp_f<QP_DPP_QUAD_1032>(0.f, mx));
+    mx = max_nan(mx, dpp_f<QP_DPP_QUAD_2301>(0.f, mx));
+    mx = max_nan(mx, dpp_f<QP_DPP_ROW_HALF_MIRROR>(0.f, mx));   // 8 lanes: the other four
     const float sc = scale127(mx);
     uint32_t cq[8];
     ckpt_codes<8>(v, sc, cq);
@@ -585,7 +586,7 @@ __global__ void __launch_bounds__(256) k_ckpt_any(const uint16_t* __restrict__ x
   const int64_t row = grp / ng;
   const int64_t k = (int64_t)(grp - (uint32_t)row * ng) * 64 + lane;
   const float v[1] = {k < K ? val16<BF>(x[row * K + k]) : 0.f};
-  const float sc = scale127(wave_max_all(fabsf(v[0])));
+  const float sc = scale127(wave_max_nan(fabsf(v[0])));
   uint32_t c[1];
   ckpt_codes<1>(v, sc, c);
   if (k < K) q[row * K + k] = (int8_t)c[0];

@@ -78,7 +78,7 @@
  *     nested formats), supported (fmt, bits, group_size, dtype) combinations,
  *     alignment, N, K, M > 0.
  *   * Inputs must be finite; non-finite weights or activations give
- *     unspecified results.
+ *     unspecified results (8-bit checkpoints keep them, see there).
  */
 #ifndef QLINEAR_H
 #define QLINEAR_H
@@ -413,7 +413,9 @@ qp_status qnorm_backward(const void* dy, const void* s, const void* s_codes, con
 
 /* 8-bit activation checkpoint of x [M, K]: per 64 columns of a row (the last
  * group may be shorter) scales[m, g] = fl32(max |x| / 127) and codes[m, k] =
- * rint(x / scale) (exact quotient, ties to even; 0 where the scale is 0).
+ * rint(x / scale) (exact quotient, ties to even; 0 where the scale is 0).  A
+ * NaN or an infinity makes its group's scale one of these too, with codes of
+ * 0, so that the whole group restores as NaN.
  * codes: int8 [M, K]; scales: fp32 [M, ceil(K / 64)].  Any K >= 1; M * K
  * <= 2^34 (2^31 where K % 8 != 0). */
 qp_status qpack_checkpoint(const void* x, int32_t x_dtype, int64_t M, int64_t K, void* codes,

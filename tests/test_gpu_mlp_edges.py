@@ -7,7 +7,7 @@ import pytest
 
 import oracle
 from oracle import mlp
-from test_gpu_mlp import dev, f64, packed, q  # noqa: F401  (q: the fixture)
+from test_gpu_mlp import DT, dev, f64, packed, q  # noqa: F401  (q: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,29 @@ def test_backward_of_small_int8_weights(q, std, meta):
         o = q.qlinear_gated_backward(d, dy, bg, bu, ck[0][2:], ck[1][2:], dx_dtype="f32")
         dx, _, _ = mlp.gated_backward(dy64, g, u, wg, wu, "silu")
         assert oracle.rel_l2(f64(o.dx), dx) <= 2e-3
+
+
+# ---------------------------------------------------------------- not finite
+BAD = (float("nan"), float("inf"), float("-inf"))
+
+
+def restored(q, ck):
+    return f64(q.qpack_checkpoint_restore(ck, "f32"))
+
+
+@pytest.mark.parametrize("K", [8, 64, 200, 1024, 65, 333])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_checkpoint_keeps_what_is_not_finite(q, K, dt):
+    """A NaN or an infinity makes its group of 64 columns NaN, and no other."""
+    rng = np.random.default_rng(K)
+    M = 70
+    x = torch.from_numpy(rng.normal(size=(M, K))).to(DT[dt])
+    y, bad = x.clone(), np.zeros((M, K), bool)
+    for m in range(0, M, 3):
+        k = int(rng.integers(0, K))
+        y[m, k] = BAD[(m // 3) % 3]
+        bad[m, k // 64 * 64:k // 64 * 64 + 64] = True
+    ck = q.qpack_checkpoint(y.cuda())
+    clean, got = restored(q, q.qpack_checkpoint(x.cuda())), restored(q, ck)
+    assert np.all(np.isnan(got[bad])) and np.array_equal(got[~bad], clean[~bad])
+    assert not ck[0].cpu().numpy()[bad].any()
