@@ -244,9 +244,12 @@ __device__ __forceinline__ uint4 gchunk(const GStage<KIND>& st, int j, const GSc
   return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-__device__ __forceinline__ uint32_t code8(float v, float inv) {
-  return (uint32_t)(int)rintf(fminf(fmaxf(v * inv, -127.f), 127.f)) & 255u;
+// A value's checkpoint code, as a byte; keep: 0 where the group's scale is not
+// finite (its codes are 0), else 255.
+__device__ __forceinline__ uint32_t code8(float v, float inv, uint32_t keep) {
+  return (uint32_t)(int)rintf(fminf(fmaxf(v * inv, -127.f), 127.f)) & keep;
 }
+__device__ __forceinline__ uint32_t code_mask(float scale) { return scale < __builtin_inff() ? 255u : 0u; }
 
 // g and u of the lane's four consecutive features f .. f + 3 in block (i, j).
 template <int KIND, int J, bool BIAS = true>
@@ -322,14 +325,17 @@ __device__ __forceinline__ void finish(const GatedK& a, float16_t (&acc)[4][J], 
       for (int q = 0; q < 4; ++q) {
         acc[i][j][4 * g4 + q] = g[q];
         acc[i + 2][j][4 * g4 + q] = u[q];
-        mg = fmaxf(mg, f + q < N ? fabsf(g[q]) : 0.f);
-        mu = fmaxf(mu, f + q < N ? fabsf(u[q]) : 0.f);
+        mg = max_nan(mg, f + q < N ? fabsf(g[q]) : 0.f);
+        mu = max_nan(mu, f + q < N ? fabsf(u[q]) : 0.f);
       }
     });
     float inv[2] = {0.f, 0.f};
+    uint32_t keep[2] = {0u, 0u};
     if (a.gq) {   // group scales: 32 values here, 32 in the other half wave
-      mg = div_rn(fmaxf(mg, __shfl_xor(mg, 32, 64)), 127.f);
-      mu = div_rn(fmaxf(mu, __shfl_xor(mu, 32, 64)), 127.f);
+      mg = div_rn(max_nan(mg, __shfl_xor(mg, 32, 64)), 127.f);
+      mu = div_rn(max_nan(mu, __shfl_xor(mu, 32, 64)), 127.f);
+      keep[0] = code_mask(mg);
+      keep[1] = code_mask(mu);
       // the quotient in fp32: the values carry the fp16 weights' rounding anyway
       inv[0] = mg > 0.f ? 1.f / mg : 0.f;
       inv[1] = mu > 0.f ? 1.f / mu : 0.f;
@@ -355,8 +361,8 @@ __device__ __forceinline__ void finish(const GatedK& a, float16_t (&acc)[4][J], 
       if (a.gq) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          c[q] = code8(acc[i][j][4 * g4 + q], inv[0]);
-          d[q] = code8(acc[i + 2][j][4 * g4 + q], inv[1]);
+          c[q] = code8(acc[i][j][4 * g4 + q], inv[0], keep[0]);
+          d[q] = code8(acc[i + 2][j][4 * g4 + q], inv[1], keep[1]);
         }
       }
       const uint32_t cw = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
@@ -467,11 +473,11 @@ __global__ void __launch_bounds__(256) k_gated_join(GatedK a) {
         (uint16_t)(a.hdt == BF16 ? f32_to_bf16_rne(h) : f32_to_f16_rne(h));
   }
   if (a.gq) {
-    const float mg = div_rn(wave_max_all(ok ? fabsf(g) : 0.f), 127.f);
-    const float mu = div_rn(wave_max_all(ok ? fabsf(u) : 0.f), 127.f);
+    const float mg = div_rn(wave_max_nan(ok ? fabsf(g) : 0.f), 127.f);
+    const float mu = div_rn(wave_max_nan(ok ? fabsf(u) : 0.f), 127.f);
     if (ok) {
-      a.gq[at] = (int8_t)code8(g, mg > 0.f ? 1.f / mg : 0.f);
-      a.uq[at] = (int8_t)code8(u, mu > 0.f ? 1.f / mu : 0.f);
+      a.gq[at] = (int8_t)code8(g, mg > 0.f ? 1.f / mg : 0.f, code_mask(mg));
+      a.uq[at] = (int8_t)code8(u, mu > 0.f ? 1.f / mu : 0.f, code_mask(mu));
     }
     if ((threadIdx.x & 63) == 0) {
       a.gs[m * ng + grp] = mg;

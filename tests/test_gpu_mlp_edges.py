@@ -65,3 +65,40 @@ def test_checkpoint_keeps_what_is_not_finite(q, K, dt):
     clean, got = restored(q, q.qpack_checkpoint(x.cuda())), restored(q, ck)
     assert np.all(np.isnan(got[bad])) and np.array_equal(got[~bad], clean[~bad])
     assert not ck[0].cpu().numpy()[bad].any()
+
+
+# stored as lines, as 4-column pieces and value by value; shares along K joined
+@pytest.mark.parametrize("M,N,K", [(300, 208, 256), (300, 196, 256), (300, 201, 256), (20, 200, 2048)])
+def test_gated_checkpoints_keep_what_is_not_finite(q, M, N, K):
+    """A bias that is not finite: the outputs of its feature, and its group of
+    64 in that layer's checkpoint; a row of x that is not: the whole row."""
+    rng = np.random.default_rng(N)
+    d = q.QDesc.affine(N, K, 4, 64, "bf16")
+    (bg, _), (bu, _) = packed(q, d, rng), packed(q, d, rng)
+    x = torch.from_numpy(rng.normal(size=(M, K))).bfloat16().cuda()
+    c = torch.from_numpy(rng.normal(size=(2, N))).bfloat16()
+    ref = q.qlinear_gated_forward(d, x, bg, bu, bias_gate=c[0].cuda(), bias_up=c[1].cuda(), save=True)
+    for v in BAD:
+        print("not finite", M, N, K, v, flush=True)
+        b, xx = c.clone(), x.clone()
+        b[0, 3], b[1, 77] = v, v
+        xx[5, 9] = v
+        o = q.qlinear_gated_forward(d, xx, bg, bu, bias_gate=b[0].cuda(), bias_up=b[1].cuda(), save=True)
+        for ck, base, f in ((o.gate, ref.gate, 3), (o.up, ref.up, 77)):
+            bad = np.zeros((M, N), bool)
+            bad[5] = True
+            bad[:, f // 64 * 64:f // 64 * 64 + 64] = True
+            got = restored(q, ck)
+            assert np.all(np.isnan(got[bad])) and np.array_equal(got[~bad], restored(q, base)[~bad])
+        keep = np.ones((M, N), bool)
+        keep[5] = False
+        keep[:, [3, 77]] = False
+        assert np.array_equal(f64(o.h)[keep], f64(ref.h)[keep])
+        # into the gradients: the row, and nothing but the groups elsewhere
+        g = q.qlinear_gated_backward(d, ref.h, bg, bu, o.gate, o.up)
+        assert torch.isnan(g.dx).all()          # every row has such a group
+        e = q.qlinear_gated_backward(d, ref.h, bg, bu, ref.gate, ref.up)
+        far = np.ones((M, N), bool)
+        far[5] = False
+        far[:, :128] = False
+        assert np.array_equal(f64(g.dgate)[far], f64(e.dgate)[far])
