@@ -244,12 +244,21 @@ __device__ __forceinline__ uint4 gchunk(const GStage<KIND>& st, int j, const GSc
   return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
-// A value's checkpoint code, as a byte; keep: 0 where the group's scale is not
-// finite (its codes are 0), else 255.
-__device__ __forceinline__ uint32_t code8(float v, float inv, uint32_t keep) {
-  return (uint32_t)(int)rintf(fminf(fmaxf(v * inv, -127.f), 127.f)) & keep;
+// What makes checkpoint codes of a group with the given scale: rint(v up inv)
+// & keep.  The quotient is taken in fp32 (the values carry the fp16 weights'
+// rounding anyway); up, a power of two, keeps the reciprocal of a subnormal
+// scale finite; keep is 0 where the scale is not finite, whose codes are 0.
+struct CodeOf {
+  float up, inv;
+  uint32_t keep;
+};
+__device__ __forceinline__ CodeOf code_of(float scale) {
+  const float up = scale < 0x1p-100f ? 0x1p64f : 1.f;
+  return {up, scale > 0.f ? 1.f / (scale * up) : 0.f, scale < __builtin_inff() ? 255u : 0u};
 }
-__device__ __forceinline__ uint32_t code_mask(float scale) { return scale < __builtin_inff() ? 255u : 0u; }
+__device__ __forceinline__ uint32_t code8(float v, const CodeOf& c) {
+  return (uint32_t)(int)rintf(fminf(fmaxf(v * c.up * c.inv, -127.f), 127.f)) & c.keep;
+}
 
 // g and u of the lane's four consecutive features f .. f + 3 in block (i, j).
 template <int KIND, int J, bool BIAS = true>
@@ -329,16 +338,12 @@ __device__ __forceinline__ void finish(const GatedK& a, float16_t (&acc)[4][J], 
         mu = max_nan(mu, f + q < N ? fabsf(u[q]) : 0.f);
       }
     });
-    float inv[2] = {0.f, 0.f};
-    uint32_t keep[2] = {0u, 0u};
+    CodeOf cg{}, cu{};
     if (a.gq) {   // group scales: 32 values here, 32 in the other half wave
       mg = div_rn(max_nan(mg, __shfl_xor(mg, 32, 64)), 127.f);
       mu = div_rn(max_nan(mu, __shfl_xor(mu, 32, 64)), 127.f);
-      keep[0] = code_mask(mg);
-      keep[1] = code_mask(mu);
-      // the quotient in fp32: the values carry the fp16 weights' rounding anyway
-      inv[0] = mg > 0.f ? 1.f / mg : 0.f;
-      inv[1] = mu > 0.f ? 1.f / mu : 0.f;
+      cg = code_of(mg);
+      cu = code_of(mu);
       if (mok && el < 32) {
         const int64_t at = m * ((a.N + kCkptGroup - 1) / kCkptGroup) + f0 / kCkptGroup;
         a.gs[at] = mg;
@@ -361,8 +366,8 @@ __device__ __forceinline__ void finish(const GatedK& a, float16_t (&acc)[4][J], 
       if (a.gq) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          c[q] = code8(acc[i][j][4 * g4 + q], inv[0], keep[0]);
-          d[q] = code8(acc[i + 2][j][4 * g4 + q], inv[1], keep[1]);
+          c[q] = code8(acc[i][j][4 * g4 + q], cg);
+          d[q] = code8(acc[i + 2][j][4 * g4 + q], cu);
         }
       }
       const uint32_t cw = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
@@ -476,8 +481,8 @@ __global__ void __launch_bounds__(256) k_gated_join(GatedK a) {
     const float mg = div_rn(wave_max_nan(ok ? fabsf(g) : 0.f), 127.f);
     const float mu = div_rn(wave_max_nan(ok ? fabsf(u) : 0.f), 127.f);
     if (ok) {
-      a.gq[at] = (int8_t)code8(g, mg > 0.f ? 1.f / mg : 0.f, code_mask(mg));
-      a.uq[at] = (int8_t)code8(u, mu > 0.f ? 1.f / mu : 0.f, code_mask(mu));
+      a.gq[at] = (int8_t)code8(g, code_of(mg));
+      a.uq[at] = (int8_t)code8(u, code_of(mu));
     }
     if ((threadIdx.x & 63) == 0) {
       a.gs[m * ng + grp] = mg;

@@ -102,3 +102,28 @@ def test_gated_checkpoints_keep_what_is_not_finite(q, M, N, K):
         far[5] = False
         far[:, :128] = False
         assert np.array_equal(f64(g.dgate)[far], f64(e.dgate)[far])
+
+
+# ---------------------------------------------------------------- subnormal scales
+@pytest.mark.parametrize("N,K", [(208, 256), (196, 256), (201, 256), (200, 2048)])
+def test_gated_checkpoints_of_tiny_groups(q, N, K):
+    """Rows of zeros leave g and u equal to the biases: groups whose scale is
+    subnormal keep their codes, and their zeros."""
+    rng = np.random.default_rng(N + 1)
+    d = q.QDesc.affine(N, K, 4, 64, "bf16")
+    (bg, _), (bu, _) = packed(q, d, rng), packed(q, d, rng)
+    M = 20 if K > 256 else 150
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    for top in (1e-30, 3e-37, 1e-37, 3e-39, 1e-40):
+        print("tiny", N, K, top, flush=True)
+        c = rng.uniform(-1, 1, size=(2, N)) * top
+        c[:, ::5] = 0
+        b, b64 = dev(c, "bf16")
+        o = q.qlinear_gated_forward(d, x, bg, bu, bias_gate=b[0].clone(), bias_up=b[1].clone(), save=True)
+        for (codes, sc), v in ((o.gate, b64[:1]), (o.up, b64[1:])):
+            rq, rs = mlp.checkpoint(v)
+            assert np.array_equal(sc.cpu().numpy(), np.repeat(rs, M, 0))
+            got = codes.cpu().numpy().astype(int)
+            # a fp32 reciprocal: 127 steps at 3 * 2^-24, so a neighbour at a tie only
+            assert np.all(np.abs(got - rq) <= 1) and not got[:, v[0] == 0].any()
+            assert np.mean(got != rq) <= 0.02
