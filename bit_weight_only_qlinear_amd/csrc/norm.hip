@@ -10,7 +10,9 @@
 //   ds = rstd (dy w - xh c) + ds_in;  dw[k] = sum over rows of dy xh.
 // s w of two 16-bit values is exact in fp32 (at most 22 significant bits), so
 // the int8 row needs only one reduction: sum s^2 and max |s w| together, and
-// max |y| = rstd max |s w|.  The sum and the int8 quotient are held in fp64:
+// max |y| = rstd max |s w|.  (bf16 has fp32's range: a row whose largest |s w|
+// is infinite in fp32, or so small that it may have lost bits, is read again and
+// takes its products in fp64.)  The sum and the int8 quotient are held in fp64:
 // a code then differs from the exact value's only within 1e-14 of a tie, and
 // squares of large bf16 do not overflow.  All of it is memory bound (6 to 8
 // bytes per value at two or three fp64 operations), so each row is read once,
@@ -129,6 +131,24 @@ __device__ __forceinline__ void row_reduce(double& sum, float& mx, double* red_s
   }
 }
 
+// Whether a row's products s w need more than fp32's range, from the largest
+// as fp32 numbers (codes other than 0 come from products of mx / 254 and more).
+// Alike in all threads of a row.
+template <bool BF>
+__device__ __forceinline__ bool wide_row(double sum, float mx) {
+  if constexpr (!BF) return false;
+  const bool wide = sum > 0. && !(mx >= 0x1p-100f && mx < __builtin_inff());
+  return __builtin_amdgcn_readfirstlane(wide);
+}
+// s w rstd of such a row.
+template <bool BF>
+__device__ __forceinline__ double wide_y(uint32_t s, uint32_t w, double rstd) {
+  return (double)val16<BF>(s) * (double)val16<BF>(w) * rstd;
+}
+__device__ __forceinline__ int wide_code(double y, float ys) {
+  return ys > 0.f ? (int)fmin(fmax(rint(y / (double)ys), -127.), 127.) : 0;
+}
+
 // The int8 row's scale from max |s w| and rstd, and what s w is multiplied
 // with to give the code before rounding (0 for a row of zeros).
 __device__ __forceinline__ void q8_scale(float mx, double rstd, float& ys, double& mul) {
@@ -152,6 +172,40 @@ struct NormArgs {
   int64_t M, K;
   float eps;
 };
+
+// The rest of a wide row, its elements one by one: per thread V columns of
+// every V * TPR, the ones whose stream it has stored itself (which may be in
+// place of x or r).
+template <bool BF, int TPR, int V>
+__device__ __forceinline__ void wide_rest(const NormArgs& a, int64_t row, int t, double rstd,
+                                          double* red_s, float* red_m) {
+  const int64_t base = row * a.K;
+  asm volatile("" ::: "memory");   // the stream's stores, of another type, come first
+  auto each = [&](auto use) __attribute__((always_inline)) {
+#pragma unroll 1
+    for (int64_t c = (int64_t)t * V; c < a.K; c += TPR * V)
+#pragma unroll 1
+      for (int64_t k = c; k < c + V; ++k) {
+        uint32_t b;
+        if (a.r && a.s) b = a.s[base + k];
+        else if (a.r) b = rnd16<BF>(val16<BF>(a.x[base + k]) + val16<BF>(a.r[base + k]));
+        else b = a.x[base + k];
+        use(k, wide_y<BF>(b, a.w ? a.w[k] : BF ? 0x3F80u : 0x3C00u, rstd));
+      }
+  };
+  if (!a.yq) {
+    each([&](int64_t k, double y) { a.y[base + k] = (uint16_t)rnd16<BF>((float)y); });
+    return;
+  }
+  float mx = 0.f;
+  double none = 0.;
+  each([&](int64_t, double y) { mx = max_nan(mx, (float)(fabs(y) / 127.)); });
+  none = mx - mx;   // NaN where the row is not finite: the maximum alone would lose it
+  row_reduce<TPR>(none, mx, red_s, red_m);
+  mx += (float)none;
+  if (t == 0) a.ys[row] = mx;
+  each([&](int64_t k, double y) { a.yq[base + k] = (int8_t)wide_code(y, mx); });
+}
 
 // One row per TPR threads, NU chunks of 8 columns per thread (K % 8 == 0,
 // K <= 8 TPR NU).
@@ -220,6 +274,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm(NormArgs a) {
   row_reduce<TPR>(sum, mx, red_s, red_m);
   const double rstd = 1. / sqrt(sum / (double)a.K + (double)a.eps);
   if (a.rstd && t == 0) a.rstd[row] = (float)rstd;
+  if (wide_row<BF>(sum, mx)) {
+    wide_rest<BF, TPR, 8>(a, row, t, rstd, red_s, red_m);
+    return;
+  }
   if (a.yq) {
     float ys;
     double mul;
@@ -279,6 +337,12 @@ __global__ void __launch_bounds__(kAny) k_norm_any(NormArgs a) {
   row_reduce<kAny>(sum, mx, red_s, red_m);
   const double rstd = 1. / sqrt(sum / (double)a.K + (double)a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = (float)rstd;
+  if (wide_row<BF>(sum, mx)) {
+    if (a.r && a.s)
+      for (int64_t k = threadIdx.x; k < a.K; k += kAny) a.s[base + k] = (uint16_t)stream(k);
+    wide_rest<BF, kAny, 1>(a, row, threadIdx.x, rstd, red_s, red_m);
+    return;
+  }
   float ys;
   double mul;
   q8_scale(mx, rstd, ys, mul);

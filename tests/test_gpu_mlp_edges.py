@@ -7,7 +7,7 @@ import pytest
 
 import oracle
 from oracle import mlp
-from test_gpu_mlp import DT, dev, f64, packed, q  # noqa: F401  (q: the fixture)
+from test_gpu_mlp import DT, TINY, U, dev, f64, packed, q, within  # noqa: F401  (q: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +127,45 @@ def test_gated_checkpoints_of_tiny_groups(q, N, K):
             # a fp32 reciprocal: 127 steps at 3 * 2^-24, so a neighbour at a tie only
             assert np.all(np.abs(got - rq) <= 1) and not got[:, v[0] == 0].any()
             assert np.mean(got != rq) <= 0.02
+
+
+# ---------------------------------------------------------------- the norm's range
+@pytest.mark.parametrize("K", [256, 250, 4096, 40000])
+def test_norm_products_past_fp32(q, K):
+    """s * weight past fp32's range, or below its normal numbers, where the
+    normed values are ordinary ones."""
+    rng = np.random.default_rng(K)
+    for sx, sw, eps in ((2e38, 1.0, 1e-5), (1e30, 1e20, 1e-5), (1e-25, 1e-15, 2.0 ** -126), (1e-28, 1e-12, 2.0 ** -126),
+                        (1e30, 1e-30, 1e-5)):
+        print("norm range", K, sx, sw, flush=True)
+        x, x64 = dev(rng.uniform(-1, 1, size=(5, K)) * sx, "bf16")
+        r, r64 = dev(rng.uniform(-0.2, 0.2, size=(5, K)) * sx, "bf16")
+        w, w64 = dev(sw * (1 + rng.uniform(0, 3, size=K)), "bf16")
+        for res in (None, r):
+            s64 = x64 if res is None else f64(torch.from_numpy(x64 + r64).bfloat16())
+            ref = mlp.norm(s64, w64, eps)
+            into = {} if res is None else dict(residual=res, s_out=x.clone())
+            o = q.qnorm_forward(into.get("s_out", x), w, eps=eps, **into)
+            assert np.array_equal(f64(o.s), s64)
+            within(o.y, ref, (U["bf16"] + 2.0 ** -21) * np.abs(ref) + TINY["bf16"], "y")
+            p = q.qnorm_forward(x, w, residual=res, eps=eps, quantize=True)
+            _, ys = mlp.row_codes(ref)
+            within(p.ys, ys.astype(np.float64), 2.0 ** -23 * ys, "ys")
+            step = f64(p.ys)[:, None]
+            assert np.all(np.abs(ref - f64(p.yq) * step) <= (0.5 + 1e-9) * step)
+
+
+@pytest.mark.parametrize("K", [256, 250, 4096])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_norm_keeps_what_is_not_finite(q, K, dt):
+    """A row with a NaN or an infinity: NaN in its 16-bit row, NaN as the int8
+    row's scale, and the other rows as they are."""
+    rng = np.random.default_rng(K)
+    x = torch.from_numpy(rng.normal(size=(7, K))).to(DT[dt])
+    ref, refq = q.qnorm_forward(x.cuda()).y, q.qnorm_forward(x.cuda(), quantize=True)
+    for m, v in ((1, float("nan")), (3, float("inf")), (5, float("-inf"))):
+        x[m, K // 3] = v
+    o, p = q.qnorm_forward(x.cuda()).y, q.qnorm_forward(x.cuda(), quantize=True)
+    assert torch.isnan(o[[1, 3, 5], K // 3]).all() and torch.isnan(p.ys[[1, 3, 5]]).all()
+    for a, b in ((o, ref), (p.yq, refq.yq), (p.ys, refq.ys)):
+        assert torch.equal(a[::2], b[::2])
