@@ -1,4 +1,5 @@
-"""GPU tests of the MLP-block operators at the ends of their ranges.
+"""GPU tests of the MLP-block operators at the ends of their ranges, and over
+long contractions under bounds that one lost step of 64 columns breaks.
 
 Tolerances as in test_gpu_mlp.py, whose helpers are used here.
 """
@@ -7,7 +8,7 @@ import pytest
 
 import oracle
 from oracle import mlp
-from test_gpu_mlp import DT, TINY, U, dev, f64, packed, q, within  # noqa: F401  (q: the fixture)
+from test_gpu_mlp import DT, TINY, U, dev, f64, packed, q, rel_limit, within  # noqa: F401  (q: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +170,92 @@ def test_norm_keeps_what_is_not_finite(q, K, dt):
     assert torch.isnan(o[[1, 3, 5], K // 3]).all() and torch.isnan(p.ys[[1, 3, 5]]).all()
     for a, b in ((o, ref), (p.yq, refq.yq), (p.ys, refq.ys)):
         assert torch.equal(a[::2], b[::2])
+
+
+# ---------------------------------------------------------------- long contractions
+def spread(D, w):
+    """What a product's error stays under when its terms' roundings do not all
+    point the same way.  Each term D w carries e with |e| <= 2^-11 |D w| from
+    the weight and as much from D, 2^-11 / sqrt(3) each in the rms at worst;
+    their signs go with D's, which are random here, so the sum's deviation is
+    at most 2^-11 sqrt(2/3 sum D^2 w^2), of which ten are allowed: 8.2 of
+    2^-11 sqrt(...), taken as 10.  Weights under fp16's normal range: 2^-25
+    each.  fp32 sums: 2^-24 of a partial sum, sqrt(n) of them, under 2^-16 of
+    the same root for n <= 65536."""
+    return 10 * (2.0 ** -11 + 2.0 ** -16) * np.sqrt((D * D) @ (w * w)) + \
+        10 * 2.0 ** -24 * np.sqrt(np.sum(D * D, axis=1, keepdims=True)) + 1e-30
+
+
+def two_or_three(q, N, K):
+    D = q.QDesc
+    out = [D.affine(N, K, 4, 64, "bf16"), D.affine(N, K, 8, 32, "f16"), D.sym4(N, K)]
+    return out + ([D.q4k(N, K), D.q6k(N, K)] if K % 256 == 0 else [])
+
+
+@pytest.mark.parametrize("M,N,K,save", [
+    (1, 20, 65536, False), (4, 20, 65536, True), (1, 37, 16384, True), (1, 37, 16384, False), (6, 35, 4096, True),
+    (2, 37, 5120, True), (17, 33, 8192, False), (130, 40, 8192, True), (300, 24, 16384, False), (5, 70, 8224, True)])
+def test_gated_forward_long(q, M, N, K, save):
+    rng = np.random.default_rng(M + K)
+    formats = two_or_three(q, N, K) if K % 64 == 0 else [q.QDesc.affine(N, K, 4, 32, "bf16")]
+    for i, d in enumerate(formats):
+        dt = ("bf16", "f16")[i % 2]
+        print("gated long", M, N, K, d.fmt, d.bits, dt, save, flush=True)
+        (bg, wg), (bu, wu) = packed(q, d, rng, 0.02), packed(q, d, rng, 0.02)
+        x, x64 = dev(rng.normal(size=(M, K)), dt)
+        o = q.qlinear_gated_forward(d, x, bg, bu, h_dtype="f32", save=save)
+        g, u, h = mlp.gated(x64, wg, wu, 0.0, 0.0, "silu")
+        dg, du = spread(x64, wg.T), spread(x64, wu.T)
+        tol = 1.13 * dg * (np.abs(u) + du) + np.abs(mlp.act(g, "silu")[0]) * du + 2.0 ** -17 * np.abs(h) + 1e-30
+        within(o.h, h, tol, "h")
+        # the bound is one: without any step of 64 columns the result breaks it
+        for t in (0, K // 128, (K - 1) // 64):
+            keep = np.ones(K)
+            keep[64 * t:64 * t + 64] = 0
+            lost = mlp.gated(x64 * keep, wg, wu, 0.0, 0.0, "silu")[2]
+            assert np.any(np.abs(lost - h) > 2 * tol)
+        if save:
+            for (codes, sc), v, e in ((o.gate, g, dg), (o.up, u, du)):
+                step = np.repeat(f64(sc), 64, axis=1)[:, :N]
+                got = mlp.restore(codes.cpu().numpy(), sc.cpu().numpy())
+                assert np.all(np.abs(got - v) <= (0.5 + 1e-4) * step + e)
+
+
+# rows of 1 to 8 chunks per thread in the staging kernel, and past its longest
+BACK = [(5, 1800, 256), (33, 4000, 320), (9, 6000, 512), (130, 14336, 256), (7, 20000, 256), (6, 33000, 256),
+        (3, 3001, 320)]
+
+
+@pytest.mark.parametrize("M,N,K", BACK)
+@pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
+def test_backward_long(q, M, N, K, kind):
+    rng = np.random.default_rng(M + N)
+    for i, d in enumerate(two_or_three(q, N, K)[(0 if kind == "silu" else 1)::2]):
+        dt = ("bf16", "f16")[i % 2]
+        print("backward long", M, N, K, d.fmt, d.bits, dt, kind, flush=True)
+        (bg, wg), (bu, wu) = packed(q, d, rng), packed(q, d, rng)
+        dh, dh64 = dev(rng.normal(size=(M, N)) * 1e-2, dt)
+        ck = []
+        for _ in range(2):
+            c, s = mlp.checkpoint(rng.normal(size=(M, N)) * 2)
+            ck.append((c, s, torch.from_numpy(c).cuda(), torch.from_numpy(s).cuda()))
+        g, u = (mlp.restore(c[0], c[1]) for c in ck)
+        o = q.qlinear_gated_backward(d, dh, bg, bu, ck[0][2:], ck[1][2:], act=kind, dx_dtype="f32")
+        dx, rg, ru = mlp.gated_backward(dh64, g, u, wg, wu, kind)
+        e = 2.0 ** -17       # fp32 chains of fewer than 16 operations around one exponential
+        tg, tu = e * np.abs(dh64 * u) * (1 + np.abs(g)), e * np.abs(dh64) * (1 + np.abs(g))
+        within(o.dgate, rg, U[dt] * np.abs(rg) + tg + TINY[dt], "dgate")
+        within(o.dup, ru, U[dt] * np.abs(ru) + tu + TINY[dt], "dup")
+        # their part of dx: 2^-17 of terms with dh's random signs, ten deviations
+        chains = 10 * np.sqrt((tg * tg) @ (wg * wg) + (tu * tu) @ (wu * wu))
+        both, w2 = np.concatenate([rg, ru], axis=1), np.concatenate([wg, wu])
+        within(o.dx, dx, spread(both, w2) + chains + 2.0 ** -24 * np.abs(dx), "dx")
+        assert oracle.rel_l2(f64(o.dx), dx) <= 2e-3
+        one = q.qlinear_backward(d, dh, bg, dx_dtype="f32")
+        ref = dh64 @ wg
+        within(one, ref, spread(dh64, wg) + 2.0 ** -24 * np.abs(ref), "dx of one layer")
+        assert oracle.rel_l2(f64(one), ref) <= rel_limit(ref, "f32", 2e-3)
+        # the bound is one: without any step of 64 rows of W the result breaks it
+        for t in (0, N // 128, (N - 1) // 64):
+            lost = dh64[:, 64 * t:64 * t + 64] @ wg[64 * t:64 * t + 64]
+            assert np.any(np.abs(lost) > 2 * spread(dh64, wg))
