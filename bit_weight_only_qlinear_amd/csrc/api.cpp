@@ -649,6 +649,42 @@ qp_status check_ptrs(std::initializer_list<PtrArg> args) {
   return QP_OK;
 }
 
+// The bytes of one buffer of a call; out: written.  Outputs and workspaces
+// must not reach into any other buffer (NULL and empty ones aside).
+struct Span {
+  const void* p;
+  size_t n;
+  const char* name;
+  bool out;
+};
+qp_status check_apart(const Span* a, int count) {
+  for (int i = 0; i < count; ++i) {
+    if (!a[i].out || !a[i].p || !a[i].n) continue;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(a[i].p), hi = lo + a[i].n;
+    for (int j = 0; j < count; ++j) {
+      if (j == i || !a[j].p || !a[j].n) continue;
+      const uintptr_t b = reinterpret_cast<uintptr_t>(a[j].p);
+      if (b < hi && lo < b + a[j].n)
+        return fail(QP_EINVAL, "%s overlaps %s: they must be buffers of their own", a[i].name, a[j].name);
+    }
+  }
+  return QP_OK;
+}
+template <int N>
+qp_status check_apart(const Span (&a)[N]) {
+  return check_apart(a, N);
+}
+// The five buffers of a layer, as spans.
+void weight_spans(const qp::Desc& d, const qp_weights* w, Span* out) {
+  const void* p[5] = {w->qweight, w->qweight_hi, w->scales, w->zeros, w->steps};
+  size_t n[5];
+  sizes_of(d, n);
+  for (int i = 0; i < 5; ++i) out[i] = {p[i], n[i], kBufName[i], false};
+}
+size_t scale_bytes(int64_t M, int64_t n) {
+  return (size_t)M * (size_t)((n + qp::kCkptGroup - 1) / qp::kCkptGroup) * 4u;
+}
+
 qp_status check_act_dtype(int32_t dt, const char* name) {
   if (dt != QP_F16 && dt != QP_BF16)
     return fail(QP_EINVAL, "%s must be QP_F16 or QP_BF16 (got %d)", name, dt);
@@ -736,6 +772,13 @@ qp_status qnorm_forward(const void* x, const void* residual, int32_t x_dtype, in
   const void* out = y ? y : yq;
   if (out == x || out == residual || out == s || out == weight)
     return fail(QP_EINVAL, "the output must be a buffer of its own");
+  const size_t rows = (size_t)M * (size_t)K * 2u;   // s may be x or residual itself
+  st = check_apart({{x == s ? nullptr : x, rows, "x", false},
+                    {residual == s ? nullptr : residual, rows, "residual", false},
+                    {weight, (size_t)K * 2u, "weight", false}, {s, rows, "s", true},
+                    {y, rows, "y", true}, {yq, rows / 2u, "yq", true}, {ys, (size_t)M * 4u, "ys", true},
+                    {rstd, (size_t)M * 4u, "rstd", true}});
+  if (st != QP_OK) return st;
   (void)hipGetLastError();
   return hip_status(qp::launch_norm(x, residual, x_dtype, M, K, weight, eps, s, y, yq, ys, rstd,
                                     (hipStream_t)stream),
@@ -770,6 +813,16 @@ qp_status qnorm_backward(const void* dy, const void* s, const void* s_codes, con
     st = check_workspace(workspace, workspace_bytes, (size_t)qp::norm_bwd_parts(M) * (size_t)K * 4u);
     if (st != QP_OK) return st;
   }
+  const size_t rows = (size_t)M * (size_t)K * 2u;   // ds may be dy or ds_in itself
+  st = check_apart({{dy == ds ? nullptr : dy, rows, "dy", false}, {s, rows, "s", false},
+                    {s_codes, rows / 2u, "s_codes", false},
+                    {s_scales, scale_bytes(M, K), "s_scales", false},
+                    {weight, (size_t)K * 2u, "weight", false}, {rstd, (size_t)M * 4u, "rstd", false},
+                    {ds_in == ds ? nullptr : ds_in, rows, "ds_in", false}, {ds, rows, "ds", true},
+                    {dweight, (size_t)K * 4u, "dweight", true},
+                    {dweight ? workspace : nullptr, (size_t)qp::norm_bwd_parts(M) * (size_t)K * 4u,
+                     "workspace", true}});
+  if (st != QP_OK) return st;
   (void)hipGetLastError();
   return hip_status(qp::launch_norm_bwd(dy, s, s_codes, s_scales, x_dtype, M, K, weight, rstd,
                                         ds_in, ds, dweight, static_cast<float*>(workspace),
@@ -783,6 +836,10 @@ qp_status qpack_checkpoint(const void* x, int32_t x_dtype, int64_t M, int64_t K,
   if (st != QP_OK || (st = check_rows(M, K)) != QP_OK) return st;
   st = check_ptrs({{x, "x", true}, {codes, "codes", true}, {scales, "scales", true}});
   if (st != QP_OK) return st;
+  st = check_apart({{x, (size_t)M * (size_t)K * 2u, "x", false},
+                    {codes, (size_t)M * (size_t)K, "codes", true},
+                    {scales, scale_bytes(M, K), "scales", true}});
+  if (st != QP_OK) return st;
   (void)hipGetLastError();
   return hip_status(qp::launch_checkpoint(x, x_dtype, M, K, codes, scales, (hipStream_t)stream),
                     "qpack_checkpoint launch");
@@ -793,6 +850,10 @@ qp_status qpack_checkpoint_restore(const void* codes, const float* scales, int64
   qp_status st = check_out_dtype(x_dtype, "x_dtype");
   if (st != QP_OK || (st = check_rows(M, K)) != QP_OK) return st;
   st = check_ptrs({{codes, "codes", true}, {scales, "scales", true}, {x, "x", true}});
+  if (st != QP_OK) return st;
+  st = check_apart({{codes, (size_t)M * (size_t)K, "codes", false},
+                    {scales, scale_bytes(M, K), "scales", false},
+                    {x, (size_t)M * (size_t)K * (x_dtype == QP_F32 ? 4u : 2u), "x", true}});
   if (st != QP_OK) return st;
   (void)hipGetLastError();
   return hip_status(qp::launch_checkpoint_restore(codes, scales, M, K, x, x_dtype,
@@ -834,10 +895,21 @@ qp_status qlinear_gated_forward(const qp_desc* d, const void* x, int32_t x_dtype
   if (h == x || (save && (gate_codes == up_codes || gate_scales == up_scales)))
     return fail(QP_EINVAL, "h and the checkpoints must be buffers of their own");
   const GatedForm form = gated_form(dd, M, save);
-  if (form == GATED_STAGED) {
-    st = check_workspace(workspace, workspace_bytes, qp::gated_workspace_bytes(dd, M));
-    if (st != QP_OK) return st;
-  }
+  const size_t need = form == GATED_STAGED ? qp::gated_workspace_bytes(dd, M) : 0;
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != QP_OK) return st;
+  const size_t outs = (size_t)M * (size_t)dd.N;
+  Span spans[19] = {{x, (size_t)M * (size_t)dd.K * 2u, "x", false},
+                    {bias_gate, (size_t)dd.N * 2u, "bias_gate", false},
+                    {bias_up, (size_t)dd.N * 2u, "bias_up", false},
+                    {h, outs * (h_dtype == QP_F32 ? 4u : 2u), "h", true},
+                    {gate_codes, outs, "gate_codes", true},
+                    {gate_scales, scale_bytes(M, dd.N), "gate_scales", true},
+                    {up_codes, outs, "up_codes", true},
+                    {up_scales, scale_bytes(M, dd.N), "up_scales", true},
+                    {workspace, need, "workspace", true}};
+  weight_spans(dd, gate, spans + 9);
+  weight_spans(dd, up, spans + 14);
+  if ((st = check_apart(spans)) != QP_OK) return st;
   qp::GatedArgs a{x, x_dtype, h_dtype, act, M, bufs_of(gate), bufs_of(up), bias_gate, bias_up, h,
                   static_cast<int8_t*>(gate_codes), gate_scales, static_cast<int8_t*>(up_codes),
                   up_scales};
@@ -874,6 +946,11 @@ qp_status qlinear_backward(const qp_desc* d, const void* dy, int32_t dy_dtype, i
       (st = check_workspace(workspace, workspace_bytes, qp::dx_workspace_bytes(dd, M, false))) != QP_OK)
     return st;
   if (dx == dy) return fail(QP_EINVAL, "dx must be a buffer of its own");
+  Span spans[8] = {{dy, (size_t)M * (size_t)dd.N * 2u, "dy", false},
+                   {dx, (size_t)M * (size_t)dd.K * (dx_dtype == QP_F32 ? 4u : 2u), "dx", true},
+                   {workspace, qp::dx_workspace_bytes(dd, M, false), "workspace", true}};
+  weight_spans(dd, w, spans + 3);
+  if ((st = check_apart(spans)) != QP_OK) return st;
   qp::DxArgs a{};
   a.dy = dy;
   a.dydt = dy_dtype;
@@ -910,6 +987,19 @@ qp_status qlinear_gated_backward(const qp_desc* d, const void* dh, int32_t dh_dt
     return st;
   if (dx == dh || dgate == dh || dup == dh || (dgate && dgate == dup) || dgate == dx || dup == dx)
     return fail(QP_EINVAL, "dx, dgate and dup must be buffers of their own");
+  const size_t ins = (size_t)M * (size_t)dd.N;
+  Span spans[19] = {{dh, ins * 2u, "dh", false},
+                    {gate_codes, ins, "gate_codes", false},
+                    {gate_scales, scale_bytes(M, dd.N), "gate_scales", false},
+                    {up_codes, ins, "up_codes", false},
+                    {up_scales, scale_bytes(M, dd.N), "up_scales", false},
+                    {dgate, ins * 2u, "dgate", true},
+                    {dup, ins * 2u, "dup", true},
+                    {dx, (size_t)M * (size_t)dd.K * (dx_dtype == QP_F32 ? 4u : 2u), "dx", true},
+                    {workspace, qp::dx_workspace_bytes(dd, M, true), "workspace", true}};
+  weight_spans(dd, gate, spans + 9);
+  weight_spans(dd, up, spans + 14);
+  if ((st = check_apart(spans)) != QP_OK) return st;
   qp::DxArgs a{};
   a.dy = dh;
   a.dydt = dh_dtype;

@@ -364,7 +364,9 @@ qp_status qlinear_forward_a8w4(const qp_desc* d, const void* xq, const float* xs
  * caller-owned; x_dtype (and dy_dtype) QP_F16 or QP_BF16 unless said
  * otherwise; asynchronous on `stream`; nothing is allocated, so every call
  * can be captured into a graph; results do not depend on timing (no atomics).
- * Calls that share a workspace must not overlap.  Limits: M <= 2^20 rows,
+ * Outputs and the workspace reach into no other buffer of the call, the
+ * packed weights included (QP_EINVAL), but where in place is said.  Calls that
+ * share a workspace must not overlap.  Limits: M <= 2^20 rows,
  * N <= 2^26, M * N <= 2^36. */
 
 /* Activation of a gated pair. */
