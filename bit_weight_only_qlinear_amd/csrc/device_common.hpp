@@ -129,6 +129,9 @@ __device__ __forceinline__ float wave_max_all(float v) {
 // group with a value that is not finite gets such a scale and codes of 0, and
 // so restores as NaN.
 __device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+// A scale's NaN without the payload that it may have from an activation: the
+// largest ones would round to a bf16 zero.
+__device__ __forceinline__ float plain_nan(float v) { return v == v ? v : __builtin_nanf(""); }
 __device__ __forceinline__ float wave_max_nan(float v) {
   for (int off = 32; off > 0; off >>= 1) v = max_nan(v, __shfl_xor(v, off, 64));
   return v;

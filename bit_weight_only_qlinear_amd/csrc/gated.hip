@@ -340,8 +340,8 @@ __device__ __forceinline__ void finish(const GatedK& a, float16_t (&acc)[4][J], 
     });
     CodeOf cg{}, cu{};
     if (a.gq) {   // group scales: 32 values here, 32 in the other half wave
-      mg = div_rn(max_nan(mg, __shfl_xor(mg, 32, 64)), 127.f);
-      mu = div_rn(max_nan(mu, __shfl_xor(mu, 32, 64)), 127.f);
+      mg = plain_nan(div_rn(max_nan(mg, __shfl_xor(mg, 32, 64)), 127.f));
+      mu = plain_nan(div_rn(max_nan(mu, __shfl_xor(mu, 32, 64)), 127.f));
       cg = code_of(mg);
       cu = code_of(mu);
       if (mok && el < 32) {
@@ -478,8 +478,8 @@ __global__ void __launch_bounds__(256) k_gated_join(GatedK a) {
         (uint16_t)(a.hdt == BF16 ? f32_to_bf16_rne(h) : f32_to_f16_rne(h));
   }
   if (a.gq) {
-    const float mg = div_rn(wave_max_nan(ok ? fabsf(g) : 0.f), 127.f);
-    const float mu = div_rn(wave_max_nan(ok ? fabsf(u) : 0.f), 127.f);
+    const float mg = plain_nan(div_rn(wave_max_nan(ok ? fabsf(g) : 0.f), 127.f));
+    const float mu = plain_nan(div_rn(wave_max_nan(ok ? fabsf(u) : 0.f), 127.f));
     if (ok) {
       a.gq[at] = (int8_t)code8(g, code_of(mg));
       a.uq[at] = (int8_t)code8(u, code_of(mu));

@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(1024) k_col_sum(const float* __restrict__ part
 // fl32(m / 127): the product with the reciprocal and one correction step,
 // correctly rounded away from the subnormals and the infinity.
 __device__ __forceinline__ float scale127(float m) {
-  if (!(m >= 1e-30f && m < __builtin_inff())) return m / 127.f;
+  if (!(m >= 1e-30f && m < __builtin_inff())) return plain_nan(m / 127.f);
   constexpr float r = 1.f / 127.f;
   const float q = m * r;
   return fmaf(fmaf(-q, 127.f, m), r, q);

@@ -68,6 +68,18 @@ def test_checkpoint_keeps_what_is_not_finite(q, K, dt):
     assert not ck[0].cpu().numpy()[bad].any()
 
 
+@pytest.mark.parametrize("K", [128, 100])
+def test_every_nan_of_fp16_is_kept(q, K):
+    """All 2046 NaN patterns, restored into each type."""
+    bits = np.array([p for p in range(0x10000) if (p & 0x7C00) == 0x7C00 and p & 0x3FF], dtype=np.uint16)
+    x = np.zeros((bits.size, K), dtype=np.uint16)
+    x[np.arange(bits.size), np.arange(bits.size) % 64] = bits
+    ck = q.qpack_checkpoint(torch.from_numpy(x.view(np.int16)).cuda().view(torch.float16))
+    for od in ("f32", "bf16", "f16"):
+        y = q.qpack_checkpoint_restore(ck, od)
+        assert torch.isnan(y[:, :64]).all() and not y[:, 64:].any(), od
+
+
 # stored as lines, as 4-column pieces and value by value; shares along K joined
 @pytest.mark.parametrize("M,N,K", [(300, 208, 256), (300, 196, 256), (300, 201, 256), (20, 200, 2048)])
 def test_gated_checkpoints_keep_what_is_not_finite(q, M, N, K):
