@@ -733,7 +733,8 @@ qp_status check_workspace(const void* ws, size_t have, size_t need) {
 // Which form of the gated pair a call takes.  With checkpoints, or above 16
 // rows (one MFMA tile), or with a buffer of 2 GiB, the staged product; one row
 // (two in some formats) streams the codes (int4 affine, 4096 -> 2 x 14336:
-// 14.9 us, 21.9 as an MFMA tile), up to 16 rows the MFMA tile on exact codes.
+// 13.8 us in a graph, the MFMA tile with two rows 20.7), up to 16 rows the MFMA
+// tile on exact codes.
 enum GatedForm { GATED_GEMV, GATED_SKINNY, GATED_STAGED };
 GatedForm gated_form(const qp::Desc& d, int64_t M, bool save) {
   size_t b[5];

@@ -447,7 +447,9 @@ qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int64_t M, int32_t sav
  * Otherwise (but for some longer single rows) fp16 MFMA as QP_KERNEL_GEMM, at
  * any K: x staged as fp16 in the workspace (16-byte aligned, busy until the
  * call's kernels finish), each weight rounded once to fp16 (per-channel SYM4:
- * exact codes), a relative L2 error of about 3e-4 in g and u. */
+ * exact codes), a relative L2 error of about 3e-4 in g and u; so h of 16 rows
+ * and fewer differs by as much with checkpoints and without.  What is said of
+ * small weights and scales under qlinear_backward holds here too. */
 qp_status qlinear_gated_forward(const qp_desc* d, const void* x, int32_t x_dtype, int64_t M,
                                 const qp_weights* gate, const qp_weights* up, const void* bias_gate,
                                 const void* bias_up, int32_t act, void* h, int32_t h_dtype,
@@ -477,7 +479,9 @@ qp_status qlinear_backward(const qp_desc* d, const void* dy, int32_t dy_dtype, i
  *   dg = dh * u * act'(g),  du = dh * act(g),  dx = dg Wg + du Wu.
  * dh [M, N] of dh_dtype; dgate and dup: [M, N] of dh_dtype (the gradients of
  * the projections' outputs, for adapters and biases), or NULL; dx [M, K] of
- * dx_dtype, from the unrounded dg and du.  Workspace as qlinear_backward. */
+ * dx_dtype, from dg and du in fp32, which the product takes as fp16 after a
+ * power of two per row (2^-11 of each value at most, next to dh_dtype's own
+ * rounding of dgate and dup).  Weights and workspace as qlinear_backward. */
 qp_status qlinear_gated_backward(const qp_desc* d, const void* dh, int32_t dh_dtype, int64_t M,
                                  const qp_weights* gate, const qp_weights* up, int32_t act,
                                  const void* gate_codes, const float* gate_scales,
