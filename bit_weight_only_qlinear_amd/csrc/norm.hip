@@ -137,11 +137,13 @@ __device__ __forceinline__ void row_reduce(double& sum, float& mx, double* red_s
 
 // Whether a row's products s w need more than fp32's range, from the largest
 // as fp32 numbers (codes other than 0 come from products of mx / 254 and more).
+// A maximum of 0 is one under 2^-150, which rstd <= 2^16 leaves under bf16's
+// smallest number: a row of zeros, as zero weights make it, stays ordinary.
 // Alike in all threads of a row.
 template <bool BF>
-__device__ __forceinline__ bool wide_row(double sum, float mx) {
+__device__ __forceinline__ bool wide_row(float mx, double rstd) {
   if constexpr (!BF) return false;
-  const bool wide = sum > 0. && !(mx >= 0x1p-100f && mx < __builtin_inff());
+  const bool wide = !(mx >= 0x1p-100f && mx < __builtin_inff()) && (mx != 0.f || rstd > 0x1p16);
   return __builtin_amdgcn_readfirstlane(wide);
 }
 // s w rstd of such a row.
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm(NormArgs a) {
   row_reduce<TPR>(sum, mx, red_s, red_m);
   const double rstd = 1. / sqrt(sum / (double)a.K + (double)a.eps);
   if (a.rstd && t == 0) a.rstd[row] = (float)rstd;
-  if (wide_row<BF>(sum, mx)) {
+  if (wide_row<BF>(mx, rstd)) {
     wide_rest<BF, TPR, 8>(a, row, t, rstd, red_s, red_m);
     return;
   }
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kAny) k_norm_any(NormArgs a) {
   row_reduce<kAny>(sum, mx, red_s, red_m);
   const double rstd = 1. / sqrt(sum / (double)a.K + (double)a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = (float)rstd;
-  if (wide_row<BF>(sum, mx)) {
+  if (wide_row<BF>(mx, rstd)) {
     if (a.r && a.s)
       for (int64_t k = threadIdx.x; k < a.K; k += kAny) a.s[base + k] = (uint16_t)stream(k);
     wide_rest<BF, kAny, 1>(a, row, threadIdx.x, rstd, red_s, red_m);

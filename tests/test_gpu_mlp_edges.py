@@ -169,6 +169,19 @@ def test_norm_products_past_fp32(q, K):
 
 
 @pytest.mark.parametrize("K", [256, 250, 4096])
+@pytest.mark.parametrize("eps", [1e-5, 1e-20])
+def test_norm_of_zeros(q, K, eps):
+    """Rows of zeros, and rows under weights of zero."""
+    x = torch.randn((6, K), device="cuda").bfloat16()
+    x[2:4] = 0
+    w = torch.ones(K, device="cuda").bfloat16()
+    for wt, rows in ((w, slice(2, 4)), (0 * w, slice(0, 6))):
+        o, p = q.qnorm_forward(x, wt, eps=eps), q.qnorm_forward(x, wt, eps=eps, quantize=True)
+        assert not o.y[rows].any() and not p.yq[rows].any() and not p.ys[rows].any()
+        assert torch.isfinite(o.y.float()).all()
+
+
+@pytest.mark.parametrize("K", [256, 250, 4096])
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_norm_keeps_what_is_not_finite(q, K, dt):
     """A row with a NaN or an infinity: NaN in its 16-bit row, NaN as the int8
