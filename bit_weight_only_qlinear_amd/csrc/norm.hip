@@ -15,12 +15,11 @@
 // takes its products in fp64.)  The sum and the int8 quotient are held in fp64:
 // a code then differs from the exact value's only within 1e-14 of a tie, and
 // squares of large bf16 do not overflow.  Rows of whole 16-byte chunks are read
-// once, kept in registers raw, and written once.  16-bit rows are then bound by
-// memory (2048 x 8192 with a residual 21 to 24 us, 5.5 to 6.4 TB/s, some of it
-// from the Infinity Cache), int8 rows by their fp64 products, roundings and
-// conversions (61 us, 1.9 TB/s; 26 VALU instructions per value, and of the
-// waves' cycles 58% wait to issue one, 28% for data), and the general forms by
-// 2-byte loads, read twice (2048 x 8191: 69 us, int8 107).
+// once, kept in registers raw, and written once, bound by memory (2048 x 8192
+// with a residual 21 to 24 us, 5.5 to 6.4 TB/s, some of it from the Infinity
+// Cache; int8 rows 21 us, 5.5 TB/s, for all their 26 VALU instructions per
+// value).  The general forms are bound by 2-byte loads, read twice (2048 x
+// 8191: 67 us, int8 65).
 //
 // A checkpoint is one int8 code per value and an fp32 scale per 64 columns
 // of a row: scale = fl32(max |x| / 127), code = rint(x / scale).

@@ -582,7 +582,7 @@ def qlinear_gated_forward(desc: QDesc, x, gate, up, act: str = "silu", bias_gate
     """h [M, N] = act(x Wg^T + bias_gate) * (x Wu^T + bias_up) for two packed
     layers of one descriptor; with `save` also the 8-bit checkpoints of both
     pre-activations for qlinear_gated_backward.  (16 rows and fewer then leave
-    the exact-code kernels for the fp16 product: 50 us in place of 15 for one
+    the exact-code kernels for the fp16 product: 46 us in place of 13 for one
     row of an int4 4096 -> 14336 pair.)"""
     import torch
     M, K, xd = _rows(x, "x")
