@@ -36,6 +36,8 @@ SOURCES = {
     "gated.hip": [],
     "backward.hip": [],
     "stage.hip": [],
+    "few.hip": [],
+    "mx.hip": [],
 }
 
 

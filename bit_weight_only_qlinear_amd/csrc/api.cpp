@@ -97,6 +97,13 @@ qp_status check_desc(const qp_desc* d, qp::Desc* out) {
       if (K % gs)
         return fail(QP_ESHAPE, "K=%lld is not a multiple of group_size=%d", (long long)K, gs);
       break;
+    case QP_FMT_MXFP4:
+      if (d->bits != 4 || gs != 32 || d->super_block != 0)
+        return fail(QP_EUNSUPPORTED, "MXFP4 needs bits=4, group_size=32, super_block=0 (got %d, %d, %d)",
+                    d->bits, gs, d->super_block);
+      if (K % 32)
+        return fail(QP_ESHAPE, "MXFP4 needs K %% 32 == 0 (K=%lld)", (long long)K);
+      break;
     default:
       return fail(QP_EINVAL, "unknown format %d", d->fmt);
   }
@@ -130,6 +137,10 @@ void sizes_of(const qp::Desc& d, size_t b[5]) {
       b[1] = N * K / 4;
       b[2] = N * K / 16;
       b[4] = N * (K / 256) * 2;
+      break;
+    case QP_FMT_MXFP4:
+      b[0] = N * K / 2;
+      b[2] = N * K / 32;
       break;
     default:
       b[0] = N * K / 2;
@@ -169,10 +180,11 @@ qp_status hip_status(hipError_t e, const char* what) {
 // to K = 8192 (the largest K of the workloads it is verified on), and longer
 // rows take the exact-code MFMA kernel instead.
 // fp16-rounded weights hold the output bound up to K = 8192; per-channel
-// SYM4 runs on exact codes (K up to 2^20: 32-bit tile offsets)
+// SYM4 runs on exact codes and MXFP4 weights are fp16 numbers (K up to 2^20:
+// 32-bit tile offsets)
 constexpr int64_t kGemmMaxK = 8192;
 bool gemm_ok(const qp::Desc& d) {
-  const bool exact = d.fmt == qp::SYM4 && d.gs == d.K;
+  const bool exact = (d.fmt == qp::SYM4 && d.gs == d.K) || d.fmt == qp::MXFP4;
   return d.K % 64 == 0 && d.K <= (exact ? (int64_t(1) << 20) : kGemmMaxK);
 }
 
@@ -347,7 +359,10 @@ qp_status qpack_dequantize(const qp_desc* d, const qp_weights* w, void* W_out, i
 
 namespace {
 
-enum Use { USE_GEMV, USE_SKINNY, USE_GEMM };
+enum Use { USE_GEMV, USE_SKINNY, USE_GEMM, USE_FEW };
+
+// Rows up to which MXFP4 products take the few-row kernel.
+constexpr int64_t kFewRows = 16;
 
 // Checks the forward arguments that do not involve a workspace and picks the
 // kernel family.
@@ -365,10 +380,19 @@ qp_status plan_forward(const qp_desc* d, qp::Desc* dd, int32_t x_dtype, int64_t 
   if (kernel == QP_KERNEL_GEMM && !gemm_ok(*dd))
     return fail(QP_EUNSUPPORTED,
                 "the qGEMM kernel (fp16-rounded weights) needs K %% 64 == 0 and K <= %lld, "
-                "where it meets the output bound (K=%lld; per-channel SYM4: exact codes, "
+                "where it meets the output bound (K=%lld; per-channel SYM4 and MXFP4: exact, "
                 "K <= 2^20); QP_KERNEL_AUTO and QP_KERNEL_GEMV_MFMA use exact codes at any K",
                 (long long)kGemmMaxK, (long long)dd->K);
   sizes_of(*dd, nbytes);
+  if (dd->fmt == qp::MXFP4) {
+    // One kernel for few rows behind both qGEMV selectors, in tiles of 16
+    // rows where K % 64 != 0 keeps more of them from the qGEMM.
+    *use = kernel == QP_KERNEL_GEMM || (kernel == QP_KERNEL_AUTO && M > kFewRows && gemm_ok(*dd))
+               ? USE_GEMM : USE_FEW;
+    if (*use == USE_FEW && M * ((dd->N + 15) / 16) > (int64_t(1) << 30))
+      return fail(QP_EUNSUPPORTED, "MXFP4 in tiles of 16 rows: M * N must be <= 2^34");
+    return QP_OK;
+  }
   bool small_bufs = (size_t)M * (size_t)dd->K * 2 < (size_t(1) << 31);
   for (int i = 0; i < 5; ++i) small_bufs = small_bufs && nbytes[i] < (size_t(1) << 31);
   const bool gemv_fits = qp::gemv_supported(*dd) && small_bufs;
@@ -502,6 +526,9 @@ qp_status qlinear_forward_ws(const qp_desc* d, const void* x, int32_t x_dtype, i
     e = qp::launch_skinny(dd, x, x_dtype, M, bufs_of(w), bias, y, y_dtype, nbytes,
                           (hipStream_t)stream);
     what = "MFMA qGEMV launch";
+  } else if (use == USE_FEW) {
+    e = qp::launch_few(dd, x, x_dtype, M, bufs_of(w), bias, y, y_dtype, (hipStream_t)stream);
+    what = "few-row MXFP4 launch";
   } else {
     e = qp::launch_gemv(dd, x, x_dtype, M, bufs_of(w), bias, y, y_dtype, nbytes,
                         (hipStream_t)stream);
@@ -735,8 +762,9 @@ qp_status check_workspace(const void* ws, size_t have, size_t need) {
 // (two in some formats) streams the codes (int4 affine, 4096 -> 2 x 14336:
 // 13.8 us in a graph, the MFMA tile with two rows 20.7), up to 16 rows the MFMA
 // tile on exact codes.
-enum GatedForm { GATED_GEMV, GATED_SKINNY, GATED_STAGED };
+enum GatedForm { GATED_GEMV, GATED_SKINNY, GATED_STAGED, GATED_FEW };
 GatedForm gated_form(const qp::Desc& d, int64_t M, bool save) {
+  if (d.fmt == qp::MXFP4) return save || M > kFewRows ? GATED_STAGED : GATED_FEW;
   size_t b[5];
   sizes_of(d, b);
   bool small_bufs = (size_t)M * (size_t)d.K * 2 < (size_t(1) << 31);
@@ -919,6 +947,7 @@ qp_status qlinear_gated_forward(const qp_desc* d, const void* x, int32_t x_dtype
   size_t nbytes[5];
   sizes_of(dd, nbytes);
   const hipError_t e = form == GATED_STAGED ? qp::launch_gated(dd, a, workspace, s)
+                     : form == GATED_FEW    ? qp::launch_few_gated(dd, a, s)
                      : form == GATED_GEMV   ? qp::launch_gated_gemv(dd, a, nbytes, s)
                                             : qp::launch_gated_skinny(dd, a, nbytes, s);
   return hip_status(e, "qlinear_gated_forward launch");
@@ -1020,6 +1049,145 @@ qp_status qlinear_gated_backward(const qp_desc* d, const void* dh, int32_t dh_dt
   a.ws = workspace;
   (void)hipGetLastError();
   return hip_status(qp::launch_dx(dd, a, (hipStream_t)stream), "qlinear_gated_backward launch");
+}
+
+}  // extern "C"
+
+// ---- MXFP4 activations and mixture-of-experts layers
+
+extern "C" {
+
+qp_status qpack_quantize_activations_mx(const void* x, int32_t x_dtype, int64_t M, int64_t K, void* xq,
+                                        void* xs, void* stream) {
+  qp_status st = check_out_dtype(x_dtype, "x_dtype");
+  if (st != QP_OK) return st;
+  if (M <= 0 || K <= 0)
+    return fail(QP_ESHAPE, "M and K must be positive (M=%lld, K=%lld)", (long long)M, (long long)K);
+  if (K % 32) return fail(QP_ESHAPE, "MXFP4 needs K %% 32 == 0 (K=%lld)", (long long)K);
+  if (M > (int64_t(1) << 31) - 1 || K > (int64_t(1) << 24))
+    return fail(QP_EUNSUPPORTED, "M must be < 2^31 and K <= 2^24 (M=%lld, K=%lld)", (long long)M,
+                (long long)K);
+  if ((st = check_ptrs({{x, "x", true}, {xq, "xq", true}, {xs, "xs", true}})) != QP_OK) return st;
+  const size_t n = (size_t)M * (size_t)K;
+  st = check_apart({{x, n * (x_dtype == QP_F32 ? 4u : 2u), "x", false}, {xq, n / 2, "xq", true},
+                    {xs, n / 32, "xs", true}});
+  if (st != QP_OK) return st;
+  (void)hipGetLastError();
+  return hip_status(qp::launch_mx_quant(x, x_dtype, M, K, xq, xs, (hipStream_t)stream),
+                    "qpack_quantize_activations_mx launch");
+}
+
+qp_status qlinear_forward_mx(const qp_desc* d, const void* xq, const void* xs, int64_t M,
+                             const qp_weights* w, const float* bias, void* y, int32_t y_dtype,
+                             void* stream) {
+  qp::Desc dd;
+  qp_status st = check_desc(d, &dd);
+  if (st != QP_OK) return st;
+  if (dd.fmt != qp::MXFP4)
+    return fail(QP_EUNSUPPORTED, "qlinear_forward_mx takes MXFP4 weights (got format %d)", dd.fmt);
+  if ((st = check_block(dd, M)) != QP_OK || (st = check_weights(dd, w, false)) != QP_OK ||
+      (st = check_out_dtype(y_dtype, "y_dtype")) != QP_OK ||
+      (st = check_ptrs({{xq, "xq", true}, {xs, "xs", true}, {bias, "bias", false}, {y, "y", true}})) != QP_OK)
+    return st;
+  const size_t n = (size_t)M * (size_t)dd.K;
+  Span spans[9] = {{xq, n / 2, "xq", false}, {xs, n / 32, "xs", false},
+                   {bias, (size_t)dd.N * 4u, "bias", false},
+                   {y, (size_t)M * (size_t)dd.N * (y_dtype == QP_F32 ? 4u : 2u), "y", true}};
+  weight_spans(dd, w, spans + 4);
+  if ((st = check_apart(spans)) != QP_OK) return st;
+  (void)hipGetLastError();
+  // whole dwords of scale bytes per row, and 32-bit offsets inside a tile
+  const bool tiles = M > kFewRows && dd.K % 128 == 0 && dd.K <= (int64_t(1) << 20);
+  const hipStream_t s = (hipStream_t)stream;
+  return hip_status(tiles ? qp::launch_mx_mx(dd, xq, xs, M, bufs_of(w), bias, y, y_dtype, s)
+                          : qp::launch_few_mx(dd, xq, xs, M, bufs_of(w), bias, y, y_dtype, s),
+                    "qlinear_forward_mx launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+// The two descriptors of a layer of experts and its sizes.
+qp_status check_moe(const qp_desc* d_up, const qp_desc* d_down, int64_t M, int32_t experts, int32_t topk,
+                    qp::Desc* up, qp::Desc* down) {
+  qp_status st = check_desc(d_up, up);
+  if (st != QP_OK || (st = check_desc(d_down, down)) != QP_OK) return st;
+  if (M <= 0) return fail(QP_ESHAPE, "M must be positive (got %lld)", (long long)M);
+  if (M > qp::moe_max_tokens())
+    return fail(QP_EUNSUPPORTED, "qmoe takes at most %d tokens (M=%lld)", qp::moe_max_tokens(), (long long)M);
+  if (experts <= 0 || experts > qp::moe_max_experts())
+    return fail(QP_EUNSUPPORTED, "experts must lie in [1, %d] (got %d)", qp::moe_max_experts(), experts);
+  if (topk <= 0 || topk > experts || topk > qp::moe_max_topk())
+    return fail(QP_EUNSUPPORTED, "topk must lie in [1, min(experts, %d)] (got %d)", qp::moe_max_topk(), topk);
+  if (!qp::moe_format(*up) || !qp::moe_format(*down))
+    return fail(QP_EUNSUPPORTED, "qmoe takes MXFP4, Q4K, SYM4 and 4-bit AFFINE weights");
+  if (up->N % experts || down->N % experts)
+    return fail(QP_ESHAPE, "the stacked N must be multiples of experts=%d (up N=%lld, down N=%lld)", experts,
+                (long long)up->N, (long long)down->N);
+  if (down->K != up->N / experts || up->K != down->N / experts)
+    return fail(QP_ESHAPE,
+                "an expert of %lld x %lld (up) needs a down projection of %lld x %lld, got %lld x %lld",
+                (long long)(up->N / experts), (long long)up->K, (long long)up->K,
+                (long long)(up->N / experts), (long long)(down->N / experts), (long long)down->K);
+  if (M * topk * (up->K > down->K ? up->K : down->K) >= int64_t(1) << 29)
+    return fail(QP_EUNSUPPORTED, "M * topk * max(K, inner) must be < 2^29 (M=%lld, topk=%d, K=%lld, inner=%lld)",
+                (long long)M, topk, (long long)up->K, (long long)down->K);
+  return QP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qp_status qmoe_workspace_bytes(const qp_desc* d_up, const qp_desc* d_down, int64_t M, int32_t experts,
+                               int32_t topk, size_t* bytes) {
+  if (!bytes) return fail(QP_EINVAL, "bytes is NULL");
+  *bytes = 0;
+  qp::Desc up, down;
+  const qp_status st = check_moe(d_up, d_down, M, experts, topk, &up, &down);
+  if (st != QP_OK) return st;
+  *bytes = qp::moe_workspace_bytes(M, topk, experts, up.K, down.K);
+  return ok();
+}
+
+qp_status qmoe_forward(const qp_desc* d_up, const qp_desc* d_down, int32_t experts, int32_t topk,
+                       const void* x, int32_t x_dtype, int64_t M, const void* router, int32_t score,
+                       int32_t norm, int32_t* ids, float* weights, const qp_weights* gate,
+                       const qp_weights* up, const qp_weights* down, int32_t act, void* y,
+                       int32_t y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  qp::Desc du, dd;
+  qp_status st = check_moe(d_up, d_down, M, experts, topk, &du, &dd);
+  if (st != QP_OK || (st = check_act_dtype(x_dtype, "x_dtype")) != QP_OK ||
+      (st = check_out_dtype(y_dtype, "y_dtype")) != QP_OK ||
+      (st = check_weights(du, gate, false)) != QP_OK || (st = check_weights(du, up, false)) != QP_OK ||
+      (st = check_weights(dd, down, false)) != QP_OK)
+    return st;
+  if (score != QP_SCORE_SOFTMAX && score != QP_SCORE_SIGMOID)
+    return fail(QP_EINVAL, "unknown score %d", score);
+  if (norm != 0 && norm != 1) return fail(QP_EINVAL, "norm must be 0 or 1 (got %d)", norm);
+  if (act != QP_ACT_SILU && act != QP_ACT_GELU_TANH)
+    return fail(QP_EINVAL, "unknown activation %d", act);
+  st = check_ptrs({{x, "x", true}, {router, "router", false}, {ids, "ids", true},
+                   {weights, "weights", true}, {y, "y", true}});
+  if (st != QP_OK) return st;
+  const size_t need = qp::moe_workspace_bytes(M, topk, experts, du.K, dd.K);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != QP_OK) return st;
+  const size_t rows = (size_t)M * (size_t)du.K, slots = (size_t)M * (size_t)topk * 4u;
+  Span spans[21] = {{x, rows * 2u, "x", false},
+                    {router, (size_t)experts * (size_t)du.K * 2u, "router", false},
+                    {ids, slots, "ids", router != nullptr},
+                    {weights, slots, "weights", router != nullptr},
+                    {y, rows * (y_dtype == QP_F32 ? 4u : 2u), "y", true},
+                    {workspace, need, "workspace", true}};
+  weight_spans(du, gate, spans + 6);
+  weight_spans(du, up, spans + 11);
+  weight_spans(dd, down, spans + 16);
+  if ((st = check_apart(spans)) != QP_OK) return st;
+  const qp::MoeArgs m{x, x_dtype, y_dtype, act, score, norm, experts, topk, M, router, bufs_of(gate),
+                      bufs_of(up), bufs_of(down), ids, weights, y, workspace};
+  (void)hipGetLastError();
+  return hip_status(qp::launch_moe(du, dd, m, (hipStream_t)stream), "qmoe_forward launch");
 }
 
 }  // extern "C"

@@ -121,6 +121,8 @@ __device__ __forceinline__ void dload(const DxK& a, const DOff& o, int t, DStage
     st.h[0] = v.x; st.h[1] = v.y;
     st.s0 = __builtin_amdgcn_raw_buffer_load_b16(res(b.scales, K / 16), o.s, 0, 0);
     st.s2 = __builtin_amdgcn_raw_buffer_load_b16(res(b.steps, (K / 256) * 2), o.p, 0, 0);
+  } else if constexpr (KIND == G_MX4) {
+    st.s0 = __builtin_amdgcn_raw_buffer_load_b8(res(b.scales, K / 32), o.s, 0, 0);
   } else {
     st.s0 = __builtin_amdgcn_raw_buffer_load_b32(res(b.scales, (K / a.gs) * 4), o.s, 0, 0);
   }
@@ -142,7 +144,8 @@ struct DTurned {
   uint32_t w[KIND == G_AFF8 ? 8 : 4];   // rows 0..3 (AFF8: columns 0-3, then 4-7)
   uint32_t h[KIND == G_Q6K ? 2 : 1];    // high bits of row pairs
   half2_t S[2], T[2];                   // hi parts (Q6K, SYM4: T is the lo part of S)
-  float Sf[KIND == G_AFF8 ? 4 : 1], Tf[KIND == G_AFF8 ? 4 : 1];   // AFF8, instead
+  // AFF8, instead; MX4: Sf alone
+  float Sf[KIND == G_AFF8 || KIND == G_MX4 ? 4 : 1], Tf[KIND == G_AFF8 ? 4 : 1];
   half2_t s[KIND == G_Q4K ? 2 : 1], t[KIND == G_Q4K ? 2 : 1];   // Q4K: lo parts
 };
 
@@ -180,7 +183,13 @@ __device__ __forceinline__ void dturn(const DStage<KIND>& st, DTurned<KIND>& d) 
     d.h[1] = __builtin_amdgcn_perm(p[3], p[2], 0x05040100u);
   }
   uint32_t m[4];
-  if constexpr (KIND == G_Q6K) {   // two groups of 16 in the chunk's 32 columns
+  if constexpr (KIND == G_MX4) {
+    m[0] = m[1] = m[2] = m[3] = __float_as_uint(e8m0_f32(st.s0 & 0xFFu));
+    turn4(m);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d.Sf[i] = __uint_as_float(m[i]);
+    return;
+  } else if constexpr (KIND == G_Q6K) {   // two groups of 16 in the chunk's 32 columns
     const float step = f16_to_f32(st.s2 & 0xFFFFu);
 #pragma unroll
     for (int g = 0; g < 2; ++g)
@@ -236,6 +245,20 @@ __device__ __forceinline__ void dcols(const DTurned<KIND>& d, uint32_t magic, ui
       for (int i = 0; i < 4; ++i)
         w[i] = fmaf((float)((d.w[o + i] >> (8 * (c + e))) & 255u), d.Sf[i], d.Tf[i]);
       out[e] = make_uint2(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]));
+    }
+    return;
+  }
+  if constexpr (KIND == G_MX4) {
+    // one conversion per row: the pair (column 2 b, column 2 b + 1) of byte b;
+    // then the rows of each column side by side
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d.w[i], d.Sf[i], b));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t sel = e ? 0x07060302u : 0x05040100u;
+      out[e] = make_uint2(__builtin_amdgcn_perm(v[1], v[0], sel), __builtin_amdgcn_perm(v[3], v[2], sel));
     }
     return;
   }
@@ -321,6 +344,8 @@ k_dx(DxK a) {
       o.p = ok ? row * (Ku / 256u) * 2u + (kcu / 256u) * 2u : kOff;
     } else if constexpr (KIND == G_SYM4) {
       o.s = row * (Ku / gs) * 4u + (kcu / gs) * 4u;
+    } else if constexpr (KIND == G_MX4) {
+      o.s = row * (Ku / 32u) + kcu / 32u;
     } else {
       o.s = row * (Ku / gs) * 2u + (kcu / gs) * 2u;
     }
@@ -617,6 +642,7 @@ hipError_t launch_dx(const Desc& d, const DxArgs& a, hipStream_t s) {
   DxFn fn = d.fmt == Q4K ? dx_pick<G_Q4K, false>(p.J)
           : d.fmt == Q6K ? dx_pick<G_Q6K, false>(p.J)
           : d.fmt == SYM4 ? dx_pick<G_SYM4, false>(p.J)
+          : d.fmt == MXFP4 ? dx_pick<G_MX4, false>(p.J)
           : d.bits == 2 ? (mb ? dx_pick<G_AFF2, true>(p.J) : dx_pick<G_AFF2, false>(p.J))
           : d.bits == 4 ? (mb ? dx_pick<G_AFF4, true>(p.J) : dx_pick<G_AFF4, false>(p.J))
                         : (mb ? dx_pick<G_AFF8, true>(p.J) : dx_pick<G_AFF8, false>(p.J));

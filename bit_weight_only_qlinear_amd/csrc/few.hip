@@ -1,0 +1,869 @@
+// Packed products for few activation rows: the MXFP4 qGEMV and gated pair of
+// up to 16 rows, and the two products of a mixture-of-experts layer, whose
+// experts' rows lie one after the other in the packed buffers.
+//
+// All of them are bound by the codes' way from HBM, so the arithmetic has to
+// stay out of the way of 16-byte loads.  v_mfma_f32_4x4x4_16b does that: it
+// multiplies 16 independent 4 x 4 x 4 blocks, lane l holding column l % 4 of
+// block l / 4 in B and in the result alike.  With the codes as B, a lane owns
+// one weight row (of four) and one 32-column chunk (of sixteen), i.e. one
+// 16-byte load; its accumulators are four activation rows of exactly that
+// chunk, so a format's scale and offset are two numbers of the same lane:
+//     y += S sum (MAG + u) x + T sum x,
+// with u the code, MAG + u held exactly (128 + u in bf16, 1024 + u in fp16;
+// MXFP4: the E2M1 value itself, MAG = T = 0, by one hardware conversion per
+// two codes) and sum x from the same instruction against ones.  One wave
+// load covers four rows x 256 contiguous bytes.  Four activation rows cost
+// the same as one; each further four cost 8 matrix instructions (64 cycles)
+// per 1 KiB of codes, still twice what HBM delivers at 16 rows.
+//
+// Four waves per block.  KW of them split a row's 512-column steps, the
+// others take other rows; the sums over lanes run as a transposed reduction
+// (permlane swaps, then DPP), those over waves through LDS.  The block's
+// metadata is staged in LDS by direct loads, in front of the first codes.
+//
+// Experts: a block's unit is (a-th expert that some token chose, 16 rows or
+// features of it); every block finds its expert and the expert's tokens from
+// the ids by itself, in LDS.  Grids cover as many experts as the tokens could
+// reach; blocks past the ones that are end at once.
+#include "device_common.hpp"
+#include "mlp_common.hpp"
+#include "qp_internal.hpp"
+
+namespace qp {
+namespace {
+
+enum FKind : int { F_MX4 = 0, F_AFF4 = 1, F_AFF4H = 2, F_Q4K = 3, F_SYM4 = 4 };
+enum FMode : int { FM_LINEAR = 0, FM_GATED = 1, FM_UP = 2, FM_DOWN = 3 };
+constexpr bool is_pair(int mode) { return mode == FM_GATED || mode == FM_UP; }
+
+constexpr int kFeat = 16;          // rows (features of a pair) per team
+constexpr uint32_t kOff = 0x80000000u;   // at or past every resource: reads 0
+
+struct FewArgs {
+  Bufs w[2];
+  int64_t K, N;            // columns; rows per expert (of the layer)
+  int C;                   // 32-column chunks per row
+  int gsh;                 // chunk -> group: >> gsh
+  int KW, RW;              // waves per row, row teams (KW * RW == 4)
+  int tiles;               // blocks per expert (or layer)
+  uint32_t mrow[3];        // metadata bytes per row: scales, zeros, steps
+  uint32_t mlds[2][3];     // LDS offset of each slice
+  int meta_lds;            // 1: metadata staged in LDS
+  const void* x;           // [rows, K] of 16 bits, or MXFP4 codes
+  const void* xsc;         //   and their scales
+  int64_t M;
+  void* y;                 // LINEAR, GATED: [M, N] of ydt; UP: h [M topk, N] of
+  int ydt;                 //   ydt; DOWN: partial sums [M topk, N] fp32
+  const void* bias[2];
+  int bdt;                 // type of the biases
+  int act;
+  const int* ids;          // experts: [M, topk]
+  int E, topk;
+};
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef short short4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t few_rsrc(const void* p, uint64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)(uint32_t)bytes,
+                                           0x00020000);
+}
+
+template <bool XB>
+__device__ __forceinline__ f32x4_t mfma4(uint2 a, uint2 b, f32x4_t c) {
+  if constexpr (XB)
+    return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(short4_t, a),
+                                                  __builtin_bit_cast(short4_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, a),
+                                              __builtin_bit_cast(half4_t, b), c, 0, 0, 0);
+}
+
+// E2M1 codes of byte SEL of w, times a power of two, as a pair (exact).
+template <bool XB, int SEL>
+__device__ __forceinline__ uint32_t e2m1_pair(uint32_t w, float scale = 1.f) {
+  if constexpr (XB)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, SEL));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, SEL));
+}
+
+// The 8 codes of one word as two operands of four; MXFP4 in their order,
+// nibbles as (0, 4, 1, 5) and (2, 6, 3, 7).
+template <int KIND, bool XB>
+__device__ __forceinline__ void code_ops(uint32_t w, uint2& lo, uint2& hi) {
+  if constexpr (KIND == F_MX4) {
+    lo = make_uint2(e2m1_pair<XB, 0>(w), e2m1_pair<XB, 1>(w));
+    hi = make_uint2(e2m1_pair<XB, 2>(w), e2m1_pair<XB, 3>(w));
+  } else {
+    const uint32_t mag = XB ? 0x43004300u : 0x64006400u;   // 128, 1024
+    lo = make_uint2((w & 0x000F000Fu) | mag, ((w >> 4) & 0x000F000Fu) | mag);
+    hi = make_uint2(((w >> 8) & 0x000F000Fu) | mag, ((w >> 12) & 0x000F000Fu) | mag);
+  }
+}
+
+// 8 activations (raw bits) in the order of the code operands.
+template <int KIND>
+__device__ __forceinline__ void x_ops(uint4 u, uint2& lo, uint2& hi) {
+  if constexpr (KIND == F_MX4) {
+    lo = make_uint2(u.x, u.y);
+    hi = make_uint2(u.z, u.w);
+  } else {
+    lo = make_uint2(__builtin_amdgcn_perm(u.z, u.x, 0x05040100u),
+                    __builtin_amdgcn_perm(u.z, u.x, 0x07060302u));
+    hi = make_uint2(__builtin_amdgcn_perm(u.w, u.y, 0x05040100u),
+                    __builtin_amdgcn_perm(u.w, u.y, 0x07060302u));
+  }
+}
+
+// E8M0 byte -> fp32: 2^(s - 127), NaN at 255.
+__device__ __forceinline__ float e8m0(uint32_t s) {
+  const uint32_t b = s == 0 ? 0x00400000u : s << 23;
+  return __uint_as_float(s == 255u ? 0x7FC00000u : b);
+}
+
+// Raw metadata of one chunk, and what it stands for.
+struct Meta {
+  uint32_t s, z, p;
+};
+template <int KIND, typename LD>
+__device__ __forceinline__ Meta load_meta(const FewArgs& a, uint32_t c, LD ld) {
+  Meta m{0, 0, 0};
+  const uint32_t g = c >> a.gsh;
+  if constexpr (KIND == F_MX4) {
+    m.s = ld(0, c, (uint8_t)0);
+  } else if constexpr (KIND == F_Q4K) {
+    m.s = ld(0, c, (uint8_t)0);
+    m.z = ld(1, c, (uint8_t)0);
+    m.p = ld(2, 4u * (c >> 3), 0u);
+  } else if constexpr (KIND == F_SYM4) {
+    m.s = ld(0, 4u * g, 0u);
+  } else {
+    m.s = ld(0, 2u * g, (uint16_t)0);
+    m.z = ld(1, 2u * g, (uint16_t)0);
+  }
+  return m;
+}
+template <int KIND, bool XB>
+__device__ __forceinline__ void scale_of(const Meta& m, float& S, float& T) {
+  constexpr float MAG = XB ? 128.f : 1024.f;
+  if constexpr (KIND == F_MX4) {
+    S = e8m0(m.s);
+    T = 0.f;
+  } else if constexpr (KIND == F_Q4K) {
+    S = (float)m.s * f16_to_f32(m.p & 0xFFFFu);
+    T = -S * (MAG + (float)m.z * f16_to_f32(m.p >> 16));
+  } else if constexpr (KIND == F_SYM4) {
+    S = __uint_as_float(m.s);
+    T = -S * (MAG + 8.f);
+  } else {
+    S = KIND == F_AFF4 ? bf16_to_f32(m.s) : f16_to_f32(m.s);
+    T = fmaf(-MAG, S, KIND == F_AFF4 ? bf16_to_f32(m.z) : f16_to_f32(m.z));
+  }
+}
+
+// What a block works on.
+struct Unit {
+  int64_t row0;            // first row of its expert in the packed buffers
+  int brow0, brows;        // rows (features) of the block inside the expert
+  int T;                   // tokens
+};
+
+// v[16] summed over the 16 lanes of equal l % 4: afterwards register k of a
+// lane of 16-lane row R holds value 4 k + (((R & 1) << 1) | (R >> 1)).
+__device__ __forceinline__ void sum16(float (&v)[16], float (&o)[4]) {
+  float b[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[2 * k]),
+                                                    __float_as_uint(v[2 * k + 1]), false, false);
+    b[k] = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(b[2 * k]),
+                                                    __float_as_uint(b[2 * k + 1]), false, false);
+    o[k] = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    o[k] += dpp_f<QP_DPP_ROW_ROR8>(0.f, o[k]);
+    o[k] += dpp_f<QP_DPP_ROW_ROR4>(0.f, o[k]);
+  }
+}
+
+// Rows 4 g + l % 4 of the pass (a pair: the first G / 2 groups of layer 0,
+// the others of layer 1) times 4 Q tokens, over this wave's steps; the sums
+// go to red [4 G][4 Q].
+// f0: the pass's first row in the block; xoff: byte offset of the lane's
+// token rows in x (kOff: none).
+template <int KIND, bool XB, bool XM, int Q, int G, bool PAIR>
+__device__ __forceinline__ void few_pass(const FewArgs& a, const Unit& u,
+                                         const unsigned char* smem, const uint32_t (&mbase)[2][3],
+                                         const __amdgpu_buffer_rsrc_t (&rw)[2],
+                                         const __amdgpu_buffer_rsrc_t (&rm)[2][3],
+                                         const __amdgpu_buffer_rsrc_t (&rx)[2],
+                                         const uint32_t (&xoff)[Q], int f0, int kw, float* red,
+                                         bool first) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t j = lane & 3, b = lane >> 2;
+  const uint32_t C = (uint32_t)a.C, rowb = (uint32_t)(a.K / 2);
+  const int S = (a.C + 15) / 16;
+  auto layer = [](int g) { return PAIR && g >= G / 2 ? 1 : 0; };
+  auto lrow = [&](int g) { return (uint32_t)f0 + 4u * (PAIR ? g % (G / 2) : g) + j; };
+
+  uint32_t wo[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) wo[g] = lrow(g) * rowb + 16u * b;
+
+  // the activations travel a step ahead with the codes where registers allow
+  constexpr bool AHEAD = Q == 1;
+  // one quad's activations of a step: the bits, or MXFP4 codes and scale
+  struct X {
+    uint4 v[XM ? 1 : 4];
+    uint32_t s;
+  };
+  struct Step {
+    uint4 w[G];
+    X x[AHEAD ? Q : 1];
+  };
+  auto load_x = [&](int s, int q) {
+    X r;
+    const bool ok = (uint32_t)s * 16u + b < C && xoff[q] != kOff;
+    const uint32_t at = xoff[q] + ((uint32_t)s * 16u + b) * (XM ? 16u : 64u);
+#pragma unroll
+    for (int v = 0; v < (XM ? 1 : 4); ++v)
+      r.v[v] = __builtin_bit_cast(
+          uint4, __builtin_amdgcn_raw_buffer_load_b128(rx[0], ok ? at + 16u * v : kOff, 0, 0));
+    r.s = 0;
+    if constexpr (XM) r.s = __builtin_amdgcn_raw_buffer_load_b8(rx[1], ok ? at / 16u : kOff, 0, 0);
+    return r;
+  };
+  auto load = [&](int s, Step& st) {
+    const bool ok = (uint32_t)s * 16u + b < C;
+    const uint32_t so = (uint32_t)s * 256u;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+      st.w[g] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                                              rw[layer(g)], ok ? wo[g] + so : kOff, 0, 2));
+    if constexpr (AHEAD) st.x[0] = load_x(s, 0);
+  };
+
+  f32x4_t acc[G][Q];
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int q = 0; q < Q; ++q) acc[g][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](int s, const Step& st) {
+    const uint32_t c = (uint32_t)s * 16u + b, cc = c < C ? c : C - 1u;
+    uint2 xo[Q][8];
+    f32x4_t xs[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const X x = AHEAD ? st.x[0] : load_x(s, q);
+      if constexpr (XM) {   // exact in bf16
+        const float sc = e8m0(x.s);
+        const uint32_t w[4] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          xo[q][2 * v] = make_uint2(e2m1_pair<true, 0>(w[v], sc), e2m1_pair<true, 1>(w[v], sc));
+          xo[q][2 * v + 1] = make_uint2(e2m1_pair<true, 2>(w[v], sc), e2m1_pair<true, 3>(w[v], sc));
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x_ops<KIND>(x.v[v], xo[q][2 * v], xo[q][2 * v + 1]);
+      }
+      xs[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if constexpr (KIND != F_MX4) {
+        const uint32_t one = XB ? 0x3F803F80u : 0x3C003C00u;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) xs[q] = mfma4<XB>(xo[q][v], make_uint2(one, one), xs[q]);
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint32_t lr = lrow(g) < (uint32_t)u.brows ? lrow(g) : (uint32_t)u.brows - 1u;
+      Meta m;
+      if (a.meta_lds)
+        m = load_meta<KIND>(a, cc, [&](int i, uint32_t o, auto t) {
+          return (uint32_t)*reinterpret_cast<const decltype(t)*>(smem + mbase[layer(g)][i] +
+                                                                 lr * a.mrow[i] + o);
+        });
+      else
+        m = load_meta<KIND>(a, cc, [&](int i, uint32_t o, auto t) {
+          const uint32_t at = lr * a.mrow[i] + o;
+          if constexpr (sizeof(t) == 1) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rm[layer(g)][i], at, 0, 0);
+          else if constexpr (sizeof(t) == 2) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rm[layer(g)][i], at, 0, 0);
+          else return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm[layer(g)][i], at, 0, 0);
+        });
+      float Sv, Tv;
+      scale_of<KIND, XB>(m, Sv, Tv);
+      f32x4_t d[Q];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) d[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      const uint32_t wv[4] = {st.w[g].x, st.w[g].y, st.w[g].z, st.w[g].w};
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        uint2 lo, hi;
+        code_ops<KIND, XB>(wv[v], lo, hi);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          d[q] = mfma4<XB>(xo[q][2 * v], lo, d[q]);
+          d[q] = mfma4<XB>(xo[q][2 * v + 1], hi, d[q]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[g][q][i] = fmaf(Sv, d[q][i], acc[g][q][i]);
+          if constexpr (KIND != F_MX4) acc[g][q][i] = fmaf(Tv, xs[q][i], acc[g][q][i]);
+        }
+    }
+  };
+
+  Step s0, s1;
+  load(kw, s0);   // steps past the end read zeros
+  if (first) {
+    // the metadata copies were issued before these loads
+    constexpr int n = G + (AHEAD ? (XM ? 2 : 4) : 0);
+    __builtin_amdgcn_s_waitcnt((n & 0xF) | (0x7 << 4) | (0xF << 8) | ((n >> 4) << 14));
+    __syncthreads();
+  }
+  for (int s = kw; s < S; s += 2 * a.KW) {
+    if (s + a.KW < S) load(s + a.KW, s1);
+    compute(s, s0);
+    if (s + a.KW >= S) break;
+    if (s + 2 * a.KW < S) load(s + 2 * a.KW, s0);
+    compute(s + a.KW, s1);
+  }
+
+  const int R = lane >> 4, p = ((R & 1) << 1) | (R >> 1);
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int h = 0; h < G / 4; ++h) {
+      float v[16], o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * k + i] = acc[4 * h + k][q][i];
+      sum16(v, o);
+      if ((lane & 12) == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) red[(16 * h + 4 * k + (int)j) * (4 * Q) + 4 * q + p] = o[k];
+      }
+    }
+}
+
+__device__ __forceinline__ void few_store(void* y, int64_t i, float v, int dt) {
+  if (dt == F32) static_cast<float*>(y)[i] = v;
+  else if (dt == BF16) static_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_bf16_rne(v);
+  else static_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_f16_rne(v);
+}
+
+// All tokens t0 .. t0 + 4 Q - 1 of the unit.  xrow, orow: rows of x and of
+// the output, per token.
+template <int KIND, bool XB, bool XM, int Q, int MODE>
+__device__ __forceinline__ void few_tokens(const FewArgs& a, const Unit& u,
+                                           const unsigned char* smem, const uint32_t (&mbase)[2][3],
+                                           const __amdgpu_buffer_rsrc_t (&rw)[2],
+                                           const __amdgpu_buffer_rsrc_t (&rm)[2][3],
+                                           const __amdgpu_buffer_rsrc_t (&rx)[2], const int* xrow,
+                                           const int* orow, int t0, float* red, bool first) {
+  constexpr bool PAIR = is_pair(MODE);
+  constexpr int G = PAIR ? (Q == 4 ? 4 : 8) : 4;     // groups of four rows per pass
+  constexpr int F = PAIR ? 2 * G : 4 * G;            // features per pass
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = wave % a.KW, team = wave / a.KW;
+  uint32_t xoff[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int t = t0 + 4 * q + (lane & 3);
+    xoff[q] = t < u.T ? (uint32_t)xrow[t] * (uint32_t)(XM ? a.K / 2 : a.K * 2) : kOff;
+  }
+  constexpr int kRed = 4 * G * 4 * Q;
+#pragma unroll 1
+  for (int f = 0; f < kFeat; f += F) {
+    const int f0 = team * kFeat + f;
+    few_pass<KIND, XB, XM, Q, G, PAIR>(a, u, smem, mbase, rw, rm, rx, xoff, f0, kw, red + wave * kRed,
+                                   first && f == 0);
+    __syncthreads();
+    // the team's threads: (feature, token) with the feature fastest
+    for (int i = threadIdx.x - team * a.KW * 64; i < F * 4 * Q; i += a.KW * 64) {
+      const int fe = i % F, t = i / F;
+      const float* r = red + team * a.KW * kRed;
+      float g = 0.f, v = 0.f;
+      for (int w = 0; w < a.KW; ++w) {
+        g += r[w * kRed + fe * 4 * Q + t];
+        if constexpr (PAIR) v += r[w * kRed + (F + fe) * 4 * Q + t];
+      }
+      if (f0 + fe < u.brows && t0 + t < u.T) {
+        const int64_t n = u.brow0 + f0 + fe;
+        if constexpr (MODE == FM_LINEAR || MODE == FM_GATED) {
+          auto bias = [&](const void* p) {
+            if (a.bdt == F32) return static_cast<const float*>(p)[n];
+            return meta_to_f32(static_cast<const uint16_t*>(p)[n], a.bdt == BF16);
+          };
+          if (a.bias[0]) g += bias(a.bias[0]);
+          if (PAIR && a.bias[1]) v += bias(a.bias[1]);
+        }
+        if constexpr (PAIR) g = (a.act == ACT_SILU ? act_f<ACT_SILU>(g) : act_f<ACT_GELU_TANH>(g)) * v;
+        if constexpr (MODE == FM_DOWN)
+          static_cast<float*>(a.y)[(int64_t)orow[t0 + t] * a.N + n] = g;
+        else
+          few_store(a.y, (int64_t)orow[t0 + t] * a.N + n, g, a.ydt);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+constexpr int kTok = 64;          // tokens of a call
+constexpr int kExperts = 512;
+constexpr int kSlots = 16;        // experts per token
+
+// The a-th expert that some token chose, its tokens (rising) and each one's
+// first slot with it; -1 where fewer are chosen.  Every wave ends up with the
+// answer; xrow and orow are complete after the last barrier.
+template <int MODE>
+__device__ __forceinline__ int find_unit(const FewArgs& a, int want, int* mask, int* xrow,
+                                         int* orow, int& T) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int e = tid; e < 2 * a.E; e += 256) mask[e] = 0;
+  __syncthreads();
+  const int n = (int)a.M * a.topk;
+  for (int i = tid; i < n; i += 256) {
+    const int e = a.ids[i], m = i / a.topk;
+    if (e >= 0 && e < a.E) atomicOr(&mask[2 * e + (m >> 5)], (int)(1u << (m & 31)));
+  }
+  __syncthreads();
+  int found = -1;
+  for (int e0 = 0, seen = 0; e0 < a.E; e0 += 64) {
+    const int e = e0 + lane;
+    const bool on = e < a.E && (mask[2 * e] | mask[2 * e + 1]) != 0;
+    uint64_t bits = __ballot(on);
+    const int cnt = __popcll(bits);
+    if (want < seen + cnt) {
+      for (int k = seen; k < want; ++k) bits &= bits - 1;
+      found = e0 + __ffsll((unsigned long long)bits) - 1;
+      break;
+    }
+    seen += cnt;
+  }
+  found = __builtin_amdgcn_readfirstlane(found);
+  if (found < 0) return -1;
+  const uint64_t tok = (uint64_t)(uint32_t)mask[2 * found] | ((uint64_t)(uint32_t)mask[2 * found + 1] << 32);
+  T = __popcll(tok);
+  if (tid < 64 && ((tok >> lane) & 1)) {
+    const int at = __popcll(tok & ((uint64_t(1) << lane) - 1));
+    int s = 0;
+    while (a.ids[lane * a.topk + s] != found) ++s;   // ends: the token is in the mask
+    const int slot = lane * a.topk + s;
+    xrow[at] = MODE == FM_UP ? lane : slot;
+    orow[at] = slot;
+  }
+  __syncthreads();
+  return found;
+}
+
+template <int KIND, bool XB, bool XM, int Q, int MODE>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+k_few(FewArgs a) {
+  constexpr bool EXPERTS = MODE == FM_UP || MODE == FM_DOWN;
+  constexpr bool PAIR = is_pair(MODE);
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  __shared__ float red[4 * 16 * 4 * 4];
+  __shared__ int xrow[kTok], orow[kTok];
+  __shared__ int mask[EXPERTS ? 2 * kExperts : 1];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  Unit u;
+  int expert = 0;
+  const int tile = (int)(blockIdx.x % (unsigned)a.tiles);   // and the expert or the tile of x's rows
+  int64_t xbase = 0;
+  if constexpr (EXPERTS) {
+    expert = find_unit<MODE>(a, (int)(blockIdx.x / (unsigned)a.tiles), mask, xrow, orow, u.T);
+    if (expert < 0) return;
+  } else {
+    xbase = (int64_t)(blockIdx.x / (unsigned)a.tiles) * (4 * Q);
+    u.T = (int)(a.M - xbase < 4 * Q ? a.M - xbase : 4 * Q);
+    if (tid < 4 * Q) {
+      xrow[tid] = tid;
+      orow[tid] = tid;
+    }
+  }
+  u.brow0 = tile * a.RW * kFeat;
+  u.brows = (int)(a.N - u.brow0 < a.RW * kFeat ? a.N - u.brow0 : a.RW * kFeat);
+  u.row0 = (int64_t)expert * a.N + u.brow0;
+
+  // resources of the block's rows; its metadata into LDS (1 KiB per wave and
+  // instruction, whole 16-byte units; bytes past the slice read 0)
+  __amdgpu_buffer_rsrc_t rw[2], rm[2][3];
+  uint32_t mbase[2][3];
+#pragma unroll
+  for (int l = 0; l < (PAIR ? 2 : 1); ++l) {
+    rw[l] = few_rsrc(static_cast<const unsigned char*>(a.w[l].qweight) + u.row0 * (a.K / 2),
+                     (uint64_t)u.brows * (uint64_t)(a.K / 2));
+    const void* arr[3] = {a.w[l].scales, a.w[l].zeros, a.w[l].steps};
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const uint64_t at = (uint64_t)u.row0 * a.mrow[i], lo = at & ~uint64_t(15);
+      const uint32_t head = (uint32_t)(at - lo), bytes = head + (uint32_t)u.brows * a.mrow[i];
+      rm[l][i] = few_rsrc(static_cast<const unsigned char*>(arr[i]) + (a.meta_lds ? lo : at),
+                          a.mrow[i] ? (a.meta_lds ? (bytes + 15u) & ~15u : bytes - head) : 0u);
+      mbase[l][i] = a.mlds[l][i] + head;
+      if (a.meta_lds && a.mrow[i])
+        for (uint32_t ch = (uint32_t)wave; ch * 1024u < bytes; ch += 4)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              rm[l][i], (__attribute__((address_space(3))) void*)(smem + a.mlds[l][i] + ch * 1024u), 16,
+              ch * 1024u + 16u * (uint32_t)lane, 0, 0, 0);
+    }
+  }
+  if constexpr (!PAIR) rw[1] = rw[0];
+  const int64_t xrows = MODE == FM_DOWN ? a.M * a.topk : a.M - xbase;
+  const int64_t xr = EXPERTS || xrows < 4 * Q ? xrows : 4 * Q, xrowb = XM ? a.K / 2 : a.K * 2;
+  const __amdgpu_buffer_rsrc_t rx[2] = {
+      few_rsrc(static_cast<const unsigned char*>(a.x) + xbase * xrowb, (uint64_t)(xr * xrowb)),
+      few_rsrc(static_cast<const unsigned char*>(a.xsc) + xbase * (a.K / 32), XM ? (uint64_t)(xr * (a.K / 32)) : 0u)};
+  if constexpr (!EXPERTS) {
+    FewArgs b = a;
+    if (xbase) b.y = static_cast<unsigned char*>(a.y) + xbase * a.N * (a.ydt == F32 ? 4 : 2);
+    __syncthreads();
+    few_tokens<KIND, XB, XM, Q, MODE>(b, u, smem, mbase, rw, rm, rx, xrow, orow, 0, red, true);
+  } else {
+    if (u.T <= 4) {
+      few_tokens<KIND, XB, XM, 1, MODE>(a, u, smem, mbase, rw, rm, rx, xrow, orow, 0, red, true);
+    } else if (u.T <= 8) {
+      few_tokens<KIND, XB, XM, 2, MODE>(a, u, smem, mbase, rw, rm, rx, xrow, orow, 0, red, true);
+    } else {
+      for (int t0 = 0; t0 < u.T; t0 += 16)
+        few_tokens<KIND, XB, XM, 4, MODE>(a, u, smem, mbase, rw, rm, rx, xrow, orow, t0, red, t0 == 0);
+    }
+  }
+}
+
+// y [M, N] = sum over slots of weight x partial sum (fixed order).  A slot
+// whose expert the token named before adds its weight to that one's sum; one
+// outside the layer adds nothing.
+__global__ void __launch_bounds__(256) k_combine(const float* __restrict__ part,
+                                                 const int* __restrict__ ids,
+                                                 const float* __restrict__ weights, int E, int topk,
+                                                 int64_t N, void* y, int ydt) {
+  const int64_t m = blockIdx.y;
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (n >= N) return;
+  float v = 0.f;
+  for (int s = 0; s < topk; ++s) {
+    const int e = ids[m * topk + s];
+    if (e < 0 || e >= E) continue;
+    int f = 0;
+    while (ids[m * topk + f] != e) ++f;
+    v = fmaf(weights[m * topk + s], part[(m * topk + f) * N + n], v);
+  }
+  few_store(y, m * N + n, v, ydt);
+}
+
+// ---- routing: logits in fp64 (products of two 16-bit values are exact in
+// fp32), so that the choice between two experts next to each other does not
+// depend on the order of additions.
+template <bool XB>
+__device__ __forceinline__ double logit_part(const uint16_t* x, const uint16_t* r, int64_t K, int lane) {
+  double s = 0.0;
+  for (int64_t c = lane; c < K / 8; c += 64) {   // K % 32 == 0
+    const uint4 u = reinterpret_cast<const uint4*>(x)[c], v = reinterpret_cast<const uint4*>(r)[c];
+    const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float p = XB ? __uint_as_float(a[i] << 16) * __uint_as_float(b[i] << 16)
+                         : f16_to_f32(a[i] & 0xFFFFu) * f16_to_f32(b[i] & 0xFFFFu);
+      const float q = XB ? __uint_as_float(a[i] & 0xFFFF0000u) * __uint_as_float(b[i] & 0xFFFF0000u)
+                         : f16_to_f32(a[i] >> 16) * f16_to_f32(b[i] >> 16);
+      s += (double)p;
+      s += (double)q;
+    }
+  }
+  return s;
+}
+__device__ __forceinline__ double wave_sum_f64(double v) {
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+struct RouteArgs {
+  const uint16_t* x;       // [M, K]
+  const uint16_t* r;       // [E, K]
+  int64_t M, K;
+  int E, topk, score, norm;
+  double* logits;          // [M, E]
+  int* ids;
+  float* weights;
+};
+
+// Token m's choice from its logits l [E]: one wave; each round takes the
+// largest left (ties: the lowest expert).  NaN logits are never chosen before
+// a number; a row with too few numbers ends with experts -1 and weights 0.
+__device__ __forceinline__ void choose(const RouteArgs& a, int64_t m, const double* l, int lane) {
+  constexpr int PL = kExperts / 64;
+  double v[PL];
+#pragma unroll
+  for (int i = 0; i < PL; ++i) {
+    const int e = lane + 64 * i;
+    v[i] = e < a.E ? l[e] : -__builtin_inf();
+    if (!(v[i] == v[i])) v[i] = -__builtin_inf();
+  }
+  // the largest first: the softmax's shift
+  auto best = [&](int& at) {
+    double t = v[0];
+#pragma unroll
+    for (int i = 1; i < PL; ++i) t = v[i] > t ? v[i] : t;
+    for (int off = 32; off > 0; off >>= 1) {
+      const double o = __shfl_xor(t, off, 64);
+      t = o > t ? o : t;
+    }
+    at = -1;
+    if (t > -__builtin_inf()) {
+#pragma unroll
+      for (int i = PL - 1; i >= 0; --i) {
+        const uint64_t b = __ballot(v[i] == t);
+        if (b) at = 64 * i + __ffsll((unsigned long long)b) - 1;
+      }
+    }
+    return t;
+  };
+  double sum = 0.0, top = 0.0, total = 0.0, mine = 0.0;
+  int my = -1;
+  for (int s = 0; s < a.topk; ++s) {
+    int at;
+    const double t = best(at);
+    if (s == 0) {
+      top = t;
+      if (a.score == 0) {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) sum += lane + 64 * i < a.E ? exp(v[i] - top) : 0.0;
+        sum = wave_sum_f64(sum);
+      }
+    }
+    if (at < 0) break;
+    const double p = a.score == 0 ? exp(t - top) / sum : 1.0 / (1.0 + exp(-t));
+    total += p;
+    if (lane == s) {
+      mine = p;
+      my = at;
+    }
+#pragma unroll
+    for (int i = 0; i < PL; ++i)
+      if (lane + 64 * i == at) v[i] = -__builtin_inf();
+  }
+  if (lane < a.topk) {
+    a.ids[m * a.topk + lane] = my;
+    a.weights[m * a.topk + lane] = (float)(a.norm ? (total > 0.0 ? mine / total : 0.0) : mine);
+  }
+}
+
+// One block per token: its logits (a wave per expert), then the choice.
+template <bool XB>
+__global__ void __launch_bounds__(1024) k_route(RouteArgs a) {
+  __shared__ double l[kExperts];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t m = blockIdx.x;
+  for (int e = wave; e < a.E; e += 16) {
+    const double s = wave_sum_f64(logit_part<XB>(a.x + m * a.K, a.r + e * a.K, a.K, lane));
+    if (lane == 0) l[e] = s;
+  }
+  __syncthreads();
+  if (wave == 0) choose(a, m, l, lane);
+}
+// A wave per logit, then a wave per token.
+template <bool XB>
+__global__ void __launch_bounds__(256) k_logits(RouteArgs a) {
+  const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t m = blockIdx.y;
+  if (e >= a.E) return;
+  const double s = wave_sum_f64(logit_part<XB>(a.x + m * a.K, a.r + (int64_t)e * a.K, a.K, lane));
+  if (lane == 0) a.logits[m * a.E + e] = s;
+}
+__global__ void __launch_bounds__(64) k_choose(RouteArgs a) {
+  choose(a, blockIdx.x, a.logits + (int64_t)blockIdx.x * a.E, threadIdx.x);
+}
+
+int few_kind(const Desc& d) {
+  if (d.fmt == MXFP4) return F_MX4;
+  if (d.fmt == AFFINE && d.bits == 4) return d.meta == BF16 ? F_AFF4 : F_AFF4H;
+  if (d.fmt == Q4K) return F_Q4K;
+  if (d.fmt == SYM4) return F_SYM4;
+  return -1;
+}
+
+// Sizes, LDS layout and launch shape that the modes share.
+size_t fill(const Desc& d, int64_t rows, bool pair, FewArgs& a) {
+  a.K = d.K;
+  a.N = rows;
+  a.C = (int)(d.K / 32);
+  a.gsh = 0;
+  const int kind = few_kind(d);
+  if (d.gs == d.K && kind == F_SYM4) a.gsh = 31;
+  else while ((32 << a.gsh) < d.gs) ++a.gsh;
+  const int S = (a.C + 15) / 16;
+  a.KW = S >= 4 ? 4 : S >= 2 ? 2 : 1;
+  a.RW = 4 / a.KW;
+  a.tiles = (int)((rows + a.RW * kFeat - 1) / (a.RW * kFeat));
+  for (int i = 0; i < 3; ++i) a.mrow[i] = 0;
+  if (kind == F_MX4) a.mrow[0] = (uint32_t)(d.K / 32);
+  else if (kind == F_Q4K) { a.mrow[0] = a.mrow[1] = (uint32_t)(d.K / 32); a.mrow[2] = (uint32_t)(d.K / 256 * 4); }
+  else if (kind == F_SYM4) a.mrow[0] = (uint32_t)(d.K / d.gs * 4);
+  else a.mrow[0] = a.mrow[1] = (uint32_t)(d.K / d.gs * 2);
+  size_t lds = 0;
+  for (int l = 0; l < (pair ? 2 : 1); ++l)
+    for (int i = 0; i < 3; ++i) {
+      a.mlds[l][i] = (uint32_t)lds;
+      if (a.mrow[i]) lds += ((size_t)a.RW * kFeat * a.mrow[i] + 15 + 1023) / 1024 * 1024;
+    }
+  // 48 KiB: two blocks per CU and more; longer rows read their metadata
+  // where it lies
+  a.meta_lds = lds <= 48 * 1024;
+  return a.meta_lds ? lds : 0;
+}
+
+using FewFn = void (*)(FewArgs);
+template <int KIND, int MODE>
+FewFn expert_fn(bool xb) {
+  return xb ? k_few<KIND, true, false, 4, MODE> : k_few<KIND, false, false, 4, MODE>;
+}
+template <int MODE>
+FewFn expert_fn(int kind, bool xb) {
+  switch (kind) {
+    case F_MX4: return expert_fn<F_MX4, MODE>(xb);
+    case F_AFF4: return expert_fn<F_AFF4, MODE>(xb);
+    case F_AFF4H: return expert_fn<F_AFF4H, MODE>(xb);
+    case F_Q4K: return expert_fn<F_Q4K, MODE>(xb);
+    default: return expert_fn<F_SYM4, MODE>(xb);
+  }
+}
+template <int MODE, bool XB, bool XM>
+FewFn mx_fn(int64_t M) {
+  return M <= 4 ? k_few<F_MX4, XB, XM, 1, MODE> : M <= 8 ? k_few<F_MX4, XB, XM, 2, MODE> : k_few<F_MX4, XB, XM, 4, MODE>;
+}
+template <int MODE>
+FewFn mx_fn(bool xb, int64_t M) {
+  return xb ? mx_fn<MODE, true, false>(M) : mx_fn<MODE, false, false>(M);
+}
+
+}  // namespace
+
+hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bufs& b,
+                      const void* bias, void* y, int ydt, hipStream_t s) {
+  FewArgs a{};
+  const size_t lds = fill(d, d.N, false, a);
+  a.w[0] = a.w[1] = b;
+  a.x = x;
+  a.M = M;
+  a.y = y;
+  a.ydt = ydt;
+  a.bias[0] = bias;
+  a.bdt = xdt;
+  const int64_t per = M <= 4 ? 4 : M <= 8 ? 8 : 16;
+  hipLaunchKernelGGL(mx_fn<FM_LINEAR>(xdt == BF16, M), dim3((unsigned)(a.tiles * ((M + per - 1) / per))),
+                     dim3(256), lds, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_few_mx(const Desc& d, const void* xq, const void* xs, int64_t M, const Bufs& b,
+                         const float* bias, void* y, int ydt, hipStream_t s) {
+  FewArgs a{};
+  const size_t lds = fill(d, d.N, false, a);
+  a.w[0] = a.w[1] = b;
+  a.x = xq;
+  a.xsc = xs;
+  a.M = M;
+  a.y = y;
+  a.ydt = ydt;
+  a.bias[0] = bias;
+  a.bdt = F32;
+  const int64_t per = M <= 4 ? 4 : M <= 8 ? 8 : 16;
+  hipLaunchKernelGGL((mx_fn<FM_LINEAR, true, true>(M)), dim3((unsigned)(a.tiles * ((M + per - 1) / per))),
+                     dim3(256), lds, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_few_gated(const Desc& d, const GatedArgs& g, hipStream_t s) {
+  FewArgs a{};
+  const size_t lds = fill(d, d.N, true, a);
+  a.w[0] = g.gate;
+  a.w[1] = g.up;
+  a.x = g.x;
+  a.M = g.M;
+  a.y = g.h;
+  a.ydt = g.hdt;
+  a.bias[0] = g.bias_g;
+  a.bias[1] = g.bias_u;
+  a.bdt = g.xdt;
+  a.act = g.act;
+  const int64_t per = g.M <= 4 ? 4 : g.M <= 8 ? 8 : 16;
+  hipLaunchKernelGGL(mx_fn<FM_GATED>(g.xdt == BF16, g.M),
+                     dim3((unsigned)(a.tiles * ((g.M + per - 1) / per))), dim3(256), lds, s, a);
+  return hipGetLastError();
+}
+
+bool moe_format(const Desc& d) { return few_kind(d) >= 0; }
+int moe_max_tokens() { return kTok; }
+int moe_max_experts() { return kExperts; }
+int moe_max_topk() { return kSlots; }
+
+namespace {
+size_t round16(size_t n) { return (n + 15) / 16 * 16; }
+}  // namespace
+
+// h (16 bits) and the partial sums, [M topk] rows each, then the logits.
+size_t moe_workspace_bytes(int64_t M, int topk, int E, int64_t K, int64_t inner) {
+  return round16((size_t)M * topk * (size_t)inner * 2) + round16((size_t)M * topk * (size_t)K * 4) +
+         round16((size_t)M * E * 8);
+}
+
+hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStream_t s) {
+  const int64_t inner = down.K, K = up.K;
+  unsigned char* ws = static_cast<unsigned char*>(m.ws);
+  void* h = ws;
+  float* part = reinterpret_cast<float*>(ws + round16((size_t)m.M * m.topk * (size_t)inner * 2));
+  double* logits = reinterpret_cast<double*>(reinterpret_cast<unsigned char*>(part) +
+                                             round16((size_t)m.M * m.topk * (size_t)K * 4));
+  const bool xb = m.xdt == BF16;
+  if (m.router) {
+    RouteArgs r{static_cast<const uint16_t*>(m.x), static_cast<const uint16_t*>(m.router), m.M, K, m.E,
+                m.topk, m.score, m.norm, logits, m.ids, m.weights};
+    if ((int64_t)m.E * K <= (int64_t(1) << 17)) {
+      hipLaunchKernelGGL((xb ? k_route<true> : k_route<false>), dim3((unsigned)m.M), dim3(1024), 0, s, r);
+    } else {
+      hipLaunchKernelGGL((xb ? k_logits<true> : k_logits<false>), dim3((unsigned)((m.E + 3) / 4), (unsigned)m.M),
+                         dim3(256), 0, s, r);
+      hipLaunchKernelGGL(k_choose, dim3((unsigned)m.M), dim3(64), 0, s, r);
+    }
+  }
+  const int64_t most = m.M * m.topk < m.E ? m.M * m.topk : m.E;
+  FewArgs a{};
+  size_t lds = fill(up, inner, true, a);
+  a.w[0] = m.gate;
+  a.w[1] = m.up;
+  a.x = m.x;
+  a.M = m.M;
+  a.y = h;
+  a.ydt = m.xdt;
+  a.act = m.act;
+  a.ids = m.ids;
+  a.E = m.E;
+  a.topk = m.topk;
+  hipLaunchKernelGGL(expert_fn<FM_UP>(few_kind(up), xb), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
+  lds = fill(down, K, false, a);
+  a.w[0] = a.w[1] = m.down;
+  a.x = h;
+  a.y = part;
+  hipLaunchKernelGGL(expert_fn<FM_DOWN>(few_kind(down), xb), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
+  hipLaunchKernelGGL(k_combine, dim3((unsigned)((K + 255) / 256), (unsigned)m.M), dim3(256), 0, s, part, m.ids,
+                     m.weights, m.E, m.topk, K, m.y, m.ydt);
+  return hipGetLastError();
+}
+
+}  // namespace qp

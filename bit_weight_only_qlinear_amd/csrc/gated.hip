@@ -70,6 +70,7 @@ struct GRes {
   __amdgpu_buffer_rsrc_t w, h, s, z, p;
   uint32_t wo, ho, so, zo, po;   // the thread's half row; starts of its metadata rows
   uint32_t half;
+  uint32_t ng;                   // groups per row
 };
 
 __device__ __forceinline__ uint32_t sel4(const uint4& v, int i) {   // uniform i
@@ -80,13 +81,13 @@ __device__ __forceinline__ uint32_t sel4(const uint4& v, int i) {   // uniform i
 // Steps per chunk.
 template <int KIND>
 __device__ __forceinline__ int chunk_steps(int lg) {
-  return KIND == G_Q4K ? 8 : KIND == G_Q6K ? 4 : KIND == G_SYM4 ? 2 << lg : 4 << lg;
+  return KIND == G_Q4K || KIND == G_MX4 ? 8 : KIND == G_Q6K ? 4 : KIND == G_SYM4 ? 2 << lg : 4 << lg;
 }
 
 template <int KIND>
 __device__ __forceinline__ void load_chunk(const GRes& r, int c, GChunk& m) {
   m.s = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r.s, r.so + 16u * (uint32_t)c, 0, 0));
-  if constexpr (KIND != G_Q6K && KIND != G_SYM4)
+  if constexpr (KIND != G_Q6K && KIND != G_SYM4 && KIND != G_MX4)
     m.z = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r.z, r.zo + 16u * (uint32_t)c, 0, 0));
   if constexpr (KIND == G_Q4K)
     m.p = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r.p, r.po + 8u * (uint32_t)c, 0, 0));
@@ -104,6 +105,8 @@ __device__ __forceinline__ void chunk_meta(const GChunk& m, int t, int lg, uint3
     st.s0 = sel4(m.s, r >> 1) >> sh;
     st.s1 = sel4(m.z, r >> 1) >> sh;
     st.s2 = r & 4 ? m.p.y : m.p.x;
+  } else if constexpr (KIND == G_MX4) {
+    st.s0 = sel4(m.s, r >> 1) >> (16u * (uint32_t)(r & 1) + 8u * half);
   } else if constexpr (KIND == G_Q6K) {
     st.s0 = sel4(m.s, r) >> (16u * half);
     st.s2 = m.p.x;
@@ -146,6 +149,10 @@ __device__ __forceinline__ void load_codes(const GRes& r, int t, int lg, GStage<
       st.s0 = __builtin_amdgcn_raw_buffer_load_b8(r.s, r.so + g2, 0, 0);
       st.s1 = __builtin_amdgcn_raw_buffer_load_b8(r.z, r.zo + g2, 0, 0);
       st.s2 = __builtin_amdgcn_raw_buffer_load_b32(r.p, r.po + (uint32_t)(t / 4) * 4u, 0, 0);
+    } else if constexpr (KIND == G_MX4) {
+      // past the row's end the scale 2^-127, whose weights are 0 in fp16: the
+      // next row's may be NaN
+      st.s0 = __builtin_amdgcn_raw_buffer_load_b8(r.s, g2 < r.ng ? r.so + g2 : kOff, 0, 0);
     } else if constexpr (KIND == G_SYM4) {
       st.s0 = __builtin_amdgcn_raw_buffer_load_b32(r.s, r.so + (g2 >> lg) * 4u, 0, 0);
     } else if constexpr (KIND == G_AFF2 || KIND == G_AFF4 || KIND == G_AFF8) {
@@ -160,7 +167,7 @@ template <int KIND>
 struct GScale {
   half2_t S[2], T[2];   // broadcast; Q6K, SYM4: hi and lo parts of the scale (Q6K: per group)
   half2_t s, t;         // Q4K: lo parts
-  float Sf, Tf;         // AFF8
+  float Sf, Tf;         // AFF8; Sf alone: MX4
 };
 
 __device__ __forceinline__ void split2(float v, half2_t& hi, half2_t& lo) {
@@ -180,6 +187,8 @@ __device__ __forceinline__ void scales_of(const GStage<KIND>& st, int mb, GScale
       split2((float)(int8_t)((st.s0 >> (8 * g)) & 0xFFu) * f16_to_f32(st.s2 & 0xFFFFu), c.S[g], c.T[g]);
   } else if constexpr (KIND == G_SYM4) {
     split2(__uint_as_float(st.s0), c.S[0], c.T[0]);
+  } else if constexpr (KIND == G_MX4) {
+    c.Sf = e8m0_f32(st.s0 & 0xFFu);
   } else if constexpr (KIND != G_SYM4C) {
     c.Sf = meta_to_f32(st.s0 & 0xFFFFu, mb);
     c.Tf = meta_to_f32(st.s1 & 0xFFFFu, mb);
@@ -198,6 +207,7 @@ __device__ __forceinline__ void scales_of(const GStage<KIND>& st, int mb, GScale
 template <int KIND>
 __device__ __forceinline__ uint4 gchunk(const GStage<KIND>& st, int j, const GScale<KIND>& c,
                                         uint32_t magic, uint32_t magic64) {
+  if constexpr (KIND == G_MX4) return mx4_chunk(st.w[j], c.Sf);
   uint32_t p[4];
   if constexpr (KIND == G_AFF8) {
     auto f = [&](int e) { return (float)((st.w[2 * j + (e >> 2)] >> (8 * (e & 3))) & 255u); };
@@ -522,6 +532,7 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
     r.h = r.s = r.z = r.p = r.w;
     r.ho = r.so = r.zo = r.po = 0;
     const int64_t ng = (K / 32) >> a.lg;
+    r.ng = (uint32_t)ng;
     if constexpr (KIND == G_Q4K) {
       r.s = res(b.scales, K / 32);
       r.z = res(b.zeros, K / 32);
@@ -538,6 +549,9 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
     } else if constexpr (KIND == G_SYM4) {
       r.s = res(b.scales, ng * 4);
       r.so = f * (uint32_t)(ng * 4);
+    } else if constexpr (KIND == G_MX4) {
+      r.s = res(b.scales, ng);
+      r.so = f * (uint32_t)ng;
     } else if constexpr (KIND != G_SYM4C) {
       r.s = res(b.scales, ng * 2);
       r.z = res(b.zeros, ng * 2);
@@ -804,9 +818,10 @@ hipError_t launch_gated(const Desc& d, const GatedArgs& g, void* ws, hipStream_t
   if (e != hipSuccess) return e;
   // whole 16-byte metadata chunks per row
   const bool ch = d.fmt == Q4K ? d.K % 512 == 0 : d.fmt == SYM4 ? d.K % (4 * d.gs) == 0
-                : d.fmt == AFFINE ? d.K % (8 * d.gs) == 0 : true;
+                : d.fmt == AFFINE ? d.K % (8 * d.gs) == 0 : d.fmt == MXFP4 ? d.K % 512 == 0 : true;
   void (*fn)(GatedK) = d.fmt == Q4K ? pick<G_Q4K>(ch)
                      : d.fmt == Q6K ? k_gated<G_Q6K, true>
+                     : d.fmt == MXFP4 ? pick<G_MX4>(ch)
                      : d.fmt == SYM4 ? (d.gs == d.K ? k_gated<G_SYM4C, true> : pick<G_SYM4>(ch))
                      : d.bits == 2 ? pick<G_AFF2>(ch)
                      : d.bits == 4 ? pick<G_AFF4>(ch) : pick<G_AFF8>(ch);

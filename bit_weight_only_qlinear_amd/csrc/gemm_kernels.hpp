@@ -117,7 +117,7 @@ constexpr uint32_t kXBase = 2u * kTileBytes;
 // codes q = u - 8 (fp16-exact); the channel scale multiplies the fp32 sum in
 // the epilogue, so no weight is rounded.
 enum GKind : int { G_AFF2 = 0, G_AFF4 = 1, G_AFF8 = 2, G_Q4K = 3, G_Q6K = 4, G_SYM4 = 5,
-                   G_SYM4C = 6 };
+                   G_SYM4C = 6, G_MX4 = 7 };
 
 // Packed code words per weight row per 64-column step (W), and Q6K high
 // plane words (H).  Two threads share a weight row, each taking half.
@@ -224,6 +224,8 @@ __device__ __forceinline__ void load_stage(const GemmArgs& a, const Rsrc& r, int
     // two int8 scale codes (groups of 16), the super-block fp16 step
     st.s0 = __builtin_amdgcn_raw_buffer_load_b16(r.s, r.so + 2u * g2, 0, 0);
     st.s2 = __builtin_amdgcn_raw_buffer_load_b16(r.p, r.po + (uint32_t)(kt / 4) * 2u, 0, 0);
+  } else if constexpr (KIND == G_MX4) {   // E8M0 scale byte
+    st.s0 = __builtin_amdgcn_raw_buffer_load_b8(r.s, r.so + g2, 0, 0);
   } else if constexpr (KIND == G_SYM4) {  // fp32 scale
     const uint32_t g = GS32 ? g2 : (uint32_t)kt * BK / (uint32_t)a.gs;
     st.s0 = __builtin_amdgcn_raw_buffer_load_b32(r.s, r.so + g * 4u, 0, 0);
@@ -283,9 +285,35 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, h);
 }
 
+// E8M0 scale byte -> fp32: 2^(s - 127), NaN at 255.
+__device__ __forceinline__ float e8m0_f32(uint32_t s) {
+  const uint32_t b = s == 0u ? 0x00400000u : s << 23;
+  return __uint_as_float(s == 255u ? 0x7FC00000u : b);
+}
+
+// E2M1 codes 0 .. 7 of a word times `scale`, as fp16 pairs (0,1), (2,3), (4,5),
+// (6,7): one hardware conversion per pair, exact while a weight is a multiple
+// of 2^-24 below 2^16.
+__device__ __forceinline__ void mx4_pairs(uint32_t w, float scale, uint32_t (&p)[4]) {
+  p[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 0));
+  p[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 1));
+  p[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 2));
+  p[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 3));
+}
+// The same in the order (0,4,1,5,2,6,3,7).
+__device__ __forceinline__ uint4 mx4_chunk(uint32_t w, float scale) {
+  uint32_t p[4];
+  mx4_pairs(w, scale, p);
+  return make_uint4(__builtin_amdgcn_perm(p[2], p[0], 0x05040100u),
+                    __builtin_amdgcn_perm(p[2], p[0], 0x07060302u),
+                    __builtin_amdgcn_perm(p[3], p[1], 0x05040100u),
+                    __builtin_amdgcn_perm(p[3], p[1], 0x07060302u));
+}
+
 // Weight chunk j of the thread's row as 8 fp16 in the order (0,4,1,5,2,6,3,7).
 template <int KIND, bool MBF16>
 __device__ __forceinline__ uint4 weight_chunk(const Stage<KIND>& st, int j, uint32_t magic) {
+  if constexpr (KIND == G_MX4) return mx4_chunk(st.w[j], e8m0_f32(st.s0 & 0xFFu));
   const int grp = KIND == G_Q6K ? (j >> 1) : 0;   // Q6K groups hold 16 columns
   float S, T;
   group_st<KIND, MBF16>(st, grp, S, T);
@@ -375,6 +403,7 @@ __device__ __forceinline__ void weight_rsrc(const GemmArgs& a, int64_t n0, int64
   int64_t srow = 0, zrow = 0, prow = 0;   // bytes per weight row
   if constexpr (KIND == G_Q4K) { srow = K / 32; zrow = K / 32; prow = (K / 256) * 4; }
   else if constexpr (KIND == G_Q6K) { srow = K / 16; prow = (K / 256) * 2; }
+  else if constexpr (KIND == G_MX4) { srow = K / 32; }
   else if constexpr (KIND == G_SYM4 || KIND == G_SYM4C) { srow = (K / a.gs) * 4; }
   else { srow = (K / a.gs) * 2; zrow = srow; }
   r.s = rsrc(static_cast<const unsigned char*>(a.scales) + n0 * srow, (uint32_t)(nrows * srow));
@@ -714,7 +743,7 @@ k_gemm224(GemmArgs a) {
   auto ld_chunk = [&](int c, uint4 (&dst)[2]) {
     dst[0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
                                            r.s, r.so + 16u * (uint32_t)c, 0, 0));
-    if constexpr (KIND != G_Q6K && KIND != G_SYM4)   // one array only
+    if constexpr (KIND != G_Q6K && KIND != G_SYM4 && KIND != G_MX4)   // one array only
       dst[1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
                                              r.z, r.zo + 16u * (uint32_t)c, 0, 0));
   };
@@ -734,8 +763,8 @@ k_gemm224(GemmArgs a) {
   // 64) or 2t + half (group size 32, Q4K) of the thread's row
   // steps per chunk (group-wise SYM4: 4 fp32 scales per chunk)
   constexpr int MP = KIND == G_SYM4 ? (MCH >= 16 ? MCH / 16 : 1)
-                     : ((MCH == 32 && KIND != G_Q4K) || KIND == G_Q6K) ? 4 : 8;
-  const uint32_t msh = (KIND == G_Q4K ? 8u : 16u) * (uint32_t)(tid & 1);
+                     : ((MCH == 32 && KIND != G_Q4K && KIND != G_MX4) || KIND == G_Q6K) ? 4 : 8;
+  const uint32_t msh = (KIND == G_Q4K || KIND == G_MX4 ? 8u : 16u) * (uint32_t)(tid & 1);
   // group size 128: one chunk per 16 steps, i.e. per unrolled iteration;
   // mc[0] holds the current chunk, mc[1] the next (NEXT: step 16 it + 16,
   // converted in the iteration's last step)
@@ -760,6 +789,9 @@ k_gemm224(GemmArgs a) {
       st.s0 = (mc[slot][0][w] >> (msh + sh)) & 0xFFu;
       st.s1 = (mc[slot][1][w] >> (msh + sh)) & 0xFFu;
       st.s2 = ms[(tu >> 2) & 1];
+    } else if constexpr (KIND == G_MX4) {   // chunks of 16 scale bytes (8 steps)
+      constexpr int w = (tu & 7) >> 1, sh = 16 * (tu & 1);
+      st.s0 = (mc[slot][0][w] >> (msh + sh)) & 0xFFu;
     } else if constexpr (MCH == 32) {
       constexpr int w = tu & 3;
       st.s0 = (mc[slot][0][w] >> msh) & 0xFFFFu;

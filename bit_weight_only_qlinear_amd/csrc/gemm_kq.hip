@@ -1,4 +1,4 @@
-// qGEMM instantiations for the Q4K, Q6K and SYM4 formats (kernels in
+// qGEMM instantiations for the Q4K, Q6K, MXFP4 and SYM4 formats (kernels in
 // gemm_kernels.hpp).
 #include "gemm_kernels.hpp"
 
@@ -19,6 +19,10 @@ hipError_t gemm_launch_kq(int fmt, const GemmArgs& a, const GemmPick& p, unsigne
     if (n224)   // K % 256 == 0 always holds for Q6K
       fn = xb ? k_gemm224<G_Q6K, true, false, false, 16> : k_gemm224<G_Q6K, false, false, false, 16>;
     else { QP_GEMM_FLAGS(G_Q6K, false, false) }
+  } else if (fmt == MXFP4) {
+    if (n224 && a.K % 512 == 0)
+      fn = xb ? k_gemm224<G_MX4, true, false, true, 32> : k_gemm224<G_MX4, false, false, true, 32>;
+    else { QP_GEMM_FLAGS(G_MX4, false, true) }
   } else {
     if (a.gs == a.K) {   // per-channel scale: exact codes
       QP_GEMM_FLAGS(G_SYM4C, false, false)

@@ -7,7 +7,7 @@
 
 namespace qp {
 
-enum Fmt : int { AFFINE = 0, Q4K = 1, Q6K = 2, SYM4 = 3 };
+enum Fmt : int { AFFINE = 0, Q4K = 1, Q6K = 2, SYM4 = 3, MXFP4 = 4 };
 enum DType : int { F16 = 0, BF16 = 1, F32 = 2 };
 enum Act : int { ACT_SILU = 0, ACT_GELU_TANH = 1 };
 constexpr int kCkptGroup = 64;   // columns per scale of an 8-bit checkpoint
@@ -155,6 +155,43 @@ struct DxArgs {
 };
 size_t dx_workspace_bytes(const Desc& d, int64_t M, bool gated);
 hipError_t launch_dx(const Desc& d, const DxArgs& a, hipStream_t s);
+
+// Few activation rows (few.hip): MXFP4 layers and gated pairs without
+// checkpoints, rows in tiles of up to 16 (any M, any K % 32 == 0).
+hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bufs& b,
+                      const void* bias, void* y, int ydt, hipStream_t s);
+hipError_t launch_few_gated(const Desc& d, const GatedArgs& a, hipStream_t s);
+// The same for MXFP4 activations (codes xq, scales xs).
+hipError_t launch_few_mx(const Desc& d, const void* xq, const void* xs, int64_t M, const Bufs& b,
+                         const float* bias, void* y, int ydt, hipStream_t s);
+
+// A mixture-of-experts layer for few tokens (few.hip): experts stacked along
+// the rows of `up` (E * inner rows, gate alike) and `down` (E * K rows).
+struct MoeArgs {
+  const void* x;
+  int xdt, ydt, act, score, norm, E, topk;
+  int64_t M;
+  const void* router;      // [E, K] of xdt, or null: ids and weights are given
+  Bufs gate, up, down;
+  int* ids;                // [M, topk]
+  float* weights;
+  void* y;
+  void* ws;
+};
+bool moe_format(const Desc& d);
+int moe_max_tokens();
+int moe_max_experts();
+int moe_max_topk();
+size_t moe_workspace_bytes(int64_t M, int topk, int E, int64_t K, int64_t inner);
+hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStream_t s);
+
+// MXFP4 rows from fp16, bf16 or fp32 ones, and back; products of two MXFP4
+// operands on the scaled matrix cores, K % 128 == 0 (mx.hip).
+hipError_t launch_mx_dequant(const Desc& d, const Bufs& b, void* out, int odt, hipStream_t st);
+hipError_t launch_mx_quant(const void* x, int xdt, int64_t M, int64_t K, void* q, void* s,
+                           hipStream_t st);
+hipError_t launch_mx_mx(const Desc& d, const void* xq, const void* xs, int64_t M, const Bufs& b,
+                        const float* bias, void* y, int ydt, hipStream_t s);
 
 // Static device scratch of the allocation-free forward (noalloc.hip): its
 // size, and its address on the current device (looked up once per device).

@@ -611,6 +611,8 @@ hipError_t launch_quantize(const Desc& d, const float* W, void* qweight,
     hipLaunchKernelGGL(k_quant_q6k, dim3(blocks_for(N * (K / 256))), dim3(kThreads), 0, s, W,
                        static_cast<uint32_t*>(qweight), static_cast<uint32_t*>(qweight_hi),
                        static_cast<int8_t*>(scales), static_cast<uint16_t*>(steps), N, K);
+  } else if (d.fmt == MXFP4) {
+    return launch_mx_quant(W, F32, N, K, qweight, scales, s);
   } else {
     const int64_t ng = N * (K / d.gs);
     hipLaunchKernelGGL(k_sym4_scales, dim3(blocks_for(ng * 64)), dim3(kThreads), 0, s, W,
@@ -664,6 +666,7 @@ hipError_t launch_pack(const Desc& d, const void* codes, void* qweight, void* qw
 }
 
 hipError_t launch_dequant(const Desc& d, const Bufs& b, void* out, int out_dt, hipStream_t s) {
+  if (d.fmt == MXFP4) return launch_mx_dequant(d, b, out, out_dt, s);
   hipLaunchKernelGGL(k_dequant, dim3(blocks_for(d.N * d.K / 8)), dim3(kThreads), 0, s,
                      static_cast<const uint32_t*>(b.qweight),
                      static_cast<const uint32_t*>(b.qweight_hi), b.scales, b.zeros, b.steps,

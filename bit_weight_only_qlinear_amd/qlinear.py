@@ -15,16 +15,18 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqlinear.so")
 
 QP_OK, QP_EINVAL, QP_ESHAPE, QP_EUNSUPPORTED, QP_EALIGN, QP_EHIP = range(6)
-QP_FMT_AFFINE, QP_FMT_Q4K, QP_FMT_Q6K, QP_FMT_SYM4 = range(4)
+QP_FMT_AFFINE, QP_FMT_Q4K, QP_FMT_Q6K, QP_FMT_SYM4, QP_FMT_MXFP4 = range(5)
 QP_F16, QP_BF16, QP_F32 = range(3)
 QP_ACT_SILU, QP_ACT_GELU_TANH = range(2)
+QP_SCORE_SOFTMAX, QP_SCORE_SIGMOID = range(2)
 QP_CHECKPOINT_GROUP = 64
 QP_KERNEL_AUTO, QP_KERNEL_GEMV, QP_KERNEL_GEMM, QP_KERNEL_GEMV_MFMA = range(4)
 
 FMT_IDS = {"affine": QP_FMT_AFFINE, "q4k": QP_FMT_Q4K, "q6k": QP_FMT_Q6K,
-           "sym4": QP_FMT_SYM4}
+           "sym4": QP_FMT_SYM4, "mxfp4": QP_FMT_MXFP4}
 DTYPE_IDS = {"f16": QP_F16, "bf16": QP_BF16, "f32": QP_F32}
 ACT_IDS = {"silu": QP_ACT_SILU, "gelu_tanh": QP_ACT_GELU_TANH}
+SCORE_IDS = {"softmax": QP_SCORE_SOFTMAX, "sigmoid": QP_SCORE_SIGMOID}
 BUFFERS = ("qweight", "qweight_hi", "scales", "zeros", "steps")
 
 
@@ -84,6 +86,11 @@ def _load():
         "qlinear_backward": (I32, [D, P, I32, I64, W, P, I32, P, ctypes.c_size_t, P]),
         "qlinear_gated_backward": (I32, [D, P, I32, I64, W, W, I32, P, P, P, P, P, P, P, I32, P,
                                          ctypes.c_size_t, P]),
+        "qpack_quantize_activations_mx": (I32, [P, I32, I64, I64, P, P, P]),
+        "qlinear_forward_mx": (I32, [D, P, P, I64, W, P, P, I32, P]),
+        "qmoe_workspace_bytes": (I32, [D, D, I64, I32, I32, ctypes.POINTER(ctypes.c_size_t)]),
+        "qmoe_forward": (I32, [D, D, I32, I32, P, I32, I64, P, I32, I32, P, P, W, W, W, I32, P, I32, P,
+                               ctypes.c_size_t, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -104,7 +111,9 @@ EXPORTED = ("qpack_abi_version", "qpack_last_error", "qpack_sizes", "qpack_quant
             "qnorm_forward", "qnorm_backward_workspace_bytes", "qnorm_backward",
             "qpack_checkpoint", "qpack_checkpoint_restore",
             "qlinear_gated_workspace_bytes", "qlinear_gated_forward",
-            "qlinear_backward_workspace_bytes", "qlinear_backward", "qlinear_gated_backward")
+            "qlinear_backward_workspace_bytes", "qlinear_backward", "qlinear_gated_backward",
+            "qpack_quantize_activations_mx", "qlinear_forward_mx", "qmoe_workspace_bytes",
+            "qmoe_forward")
 
 
 @dataclass(frozen=True)
@@ -133,6 +142,10 @@ class QDesc:
     @staticmethod
     def sym4(N, K, group_size=None):
         return QDesc("sym4", 4, K if group_size is None else group_size, N, K, "f32", 0)
+
+    @staticmethod
+    def mxfp4(N, K):
+        return QDesc("mxfp4", 4, 32, N, K, "f16", 0)
 
     @functools.cached_property
     def _cref(self):
@@ -184,6 +197,8 @@ def _buf_dtypes(desc):
     if desc.fmt == "q6k":
         return dict(qweight=torch.int32, qweight_hi=torch.int32, scales=torch.int8,
                     steps=torch.float16)
+    if desc.fmt == "mxfp4":
+        return dict(qweight=torch.int32, scales=torch.uint8)
     return dict(qweight=torch.int32, scales=torch.float32)
 
 
@@ -650,3 +665,87 @@ def qlinear_gated_backward(desc: QDesc, dh, gate, up, gate_saved, up_saved, act:
          *[None if t is None else t.data_ptr() for t in (dg, du)], dx.data_ptr(), DTYPE_IDS[xd],
          ws.data_ptr(), n)
     return QGatedGrads(dx, dg, du)
+
+
+# ---- MXFP4 activations, and mixture-of-experts layers for few tokens
+
+class QMoE(NamedTuple):
+    """qmoe_forward's outputs: y [M, K], and the experts (int32 [M, topk])
+    and their weights (fp32 [M, topk]) of each token."""
+    y: Any
+    ids: Any
+    weights: Any
+
+
+def quantize_activations_mx(x):
+    """MXFP4 rows of x [M, K] (fp16, bf16 or fp32, K % 32 == 0): (codes int32
+    [M, K / 8], scales uint8 [M, K / 32])."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"x must be a matrix [M, K], got {x.dim()} dimensions")
+    if not x.is_cuda:
+        raise ValueError(f"x must be a GPU tensor, got {x.device}")
+    xd = "f32" if x.dtype == torch.float32 else _xdtype(x)
+    M, K = x.shape
+    px = _arg(x, "x", (M, K), x.dtype, x.device)
+    xq = torch.empty((M, K // 8), dtype=torch.int32, device=x.device)
+    xs = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+    _run(x.device, lib.qpack_quantize_activations_mx, px, DTYPE_IDS[xd], M, K, xq.data_ptr(), xs.data_ptr())
+    return xq, xs
+
+
+def qlinear_forward_mx(desc: QDesc, xq, xs, w, bias=None, y_dtype: str = "bf16", out=None):
+    """y [M, N] = X W^T (+ bias fp32 [N]) for MXFP4 activations (codes and
+    scales of quantize_activations_mx) and MXFP4 weights."""
+    import torch
+    if xq.dim() != 2:
+        raise ValueError(f"xq must be a matrix [M, K / 8], got {xq.dim()} dimensions")
+    if not xq.is_cuda:
+        raise ValueError(f"xq must be a GPU tensor, got {xq.device}")
+    M, dev = xq.shape[0], xq.device
+    pq = _arg(xq, "xq", (M, desc.K // 8), torch.int32, dev)
+    ps = _arg(xs, "xs", (M, desc.K // 32), torch.uint8, dev)
+    ww = _weights_arg(desc, w, "w", dev)
+    pb = _opt(bias, "bias", (desc.N,), torch.float32, dev)
+    tdt = _torch_dt(y_dtype)
+    if out is None:
+        out = torch.empty((M, desc.N), dtype=tdt, device=dev)
+    po = _arg(out, "out", (M, desc.N), tdt, dev)
+    _run(dev, lib.qlinear_forward_mx, desc._cref, pq, ps, M, ww, pb, po, DTYPE_IDS[y_dtype])
+    return out
+
+
+def qmoe_forward(desc_up: QDesc, desc_down: QDesc, x, gate, up, down, experts: int, topk: int, router=None,
+                 ids=None, weights=None, score: str = "softmax", norm: bool = True, act: str = "silu",
+                 y_dtype: Optional[str] = None) -> QMoE:
+    """A mixture-of-experts layer for up to 64 tokens x [M, K]: the experts'
+    packed layers stacked along N (gate and up of desc_up, down of desc_down).
+    Pass the router's weights [experts, K], or each token's ids (int32
+    [M, topk]) and weights (fp32 [M, topk])."""
+    import torch
+    M, K, xd = _rows(x, "x")
+    dev = x.device
+    if (router is None) != (ids is not None and weights is not None) or (ids is None) != (weights is None):
+        raise ValueError("pass router, or ids and weights")
+    if score not in SCORE_IDS:
+        raise ValueError(f"score must be one of {tuple(SCORE_IDS)}, got {score!r}")
+    px = _arg(x, "x", (M, desc_up.K), x.dtype, dev)
+    pr = _opt(router, "router", (experts, desc_up.K), x.dtype, dev)
+    if router is None:
+        pi = _arg(ids, "ids", (M, topk), torch.int32, dev)
+        pw = _arg(weights, "weights", (M, topk), torch.float32, dev)
+    wg, wu = _weights_arg(desc_up, gate, "gate", dev), _weights_arg(desc_up, up, "up", dev)
+    wd = _weights_arg(desc_down, down, "down", dev)
+    a, yd = _act_id(act), y_dtype or xd
+    size = ctypes.c_size_t(0)
+    _check(lib.qmoe_workspace_bytes(desc_up._cref, desc_down._cref, M, experts, topk, ctypes.byref(size)))
+    if router is not None:
+        ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
+        weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
+        pi, pw = ids.data_ptr(), weights.data_ptr()
+    y = torch.empty((M, K), dtype=_torch_dt(yd), device=dev)
+    ws = _scratch(size.value, dev)
+    _run(dev, lib.qmoe_forward, desc_up._cref, desc_down._cref, experts, topk, px, DTYPE_IDS[xd], M, pr,
+         SCORE_IDS[score], int(norm), pi, pw, wg, wu, wd, a, y.data_ptr(), DTYPE_IDS[yd], ws.data_ptr(),
+         size.value)
+    return QMoE(y, ids, weights)

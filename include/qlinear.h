@@ -5,7 +5,7 @@
  * What the library computes
  * -------------------------
  *   y[m, n] = sum_k x[m, k] * w[n, k]  (+ bias[n])        (y = x W^T)
- * where W [N, K] is stored quantized in one of four formats and w is its
+ * where W [N, K] is stored quantized in one of five formats and w is its
  * dequantized value.  The formats and their dequantization rules:
  *
  *   QP_FMT_AFFINE  MLX-style group affine codes (HF Transformers "Metal"
@@ -27,6 +27,13 @@
  *                  (ExecuTorch PR #16577, description), fp32 scale per output
  *                  channel (group_size = K) or per group:
  *                      w = q * scale.
+ *   QP_FMT_MXFP4   microscaled 4-bit floating point (the OCP microscaling
+ *                  formats' MXFP4): a sign, two exponent bits and a mantissa
+ *                  bit per weight (E2M1), one power of two per 32 columns
+ *                  (E8M0); 4.25 bits per weight:
+ *                      w = v(q) * 2^(s - 127),  v = 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *                  for q = 0 .. 7 and their negatives for 8 .. 15; s = 255
+ *                  stands for NaN.
  *
  * Quantization rules (qpack_quantize) -- per group along K of each row, every
  * step one IEEE fp32 operation, codes rounded half-to-even and clamped:
@@ -44,17 +51,21 @@
  *           0, 127).
  *   SYM4:   s = fl32(max|w| / 7) (fp32, stored); q = clamp(rint(fl32(w/s)),
  *           -7, 7).
+ *   MXFP4:  s = max(floor(log2 max|w|) - 2 + 127, 0); q = the nearest v to
+ *           w / 2^(s - 127), ties to the even code, 6 at most, with w's sign.
+ *           A NaN or an infinity gives its group s = 255 and codes of 0.
  *   fp16 conversions keep subnormals (the nested steps usually are).
  *
  * Storage (all buffers row-major, N leading, caller-owned device memory):
  *   qweight     uint32 [N, K*b/32]: code k of a row at word k/(32/b), bits
  *               [b*(k % (32/b)), +b) -- least-significant first along K.
- *               SYM4 stores u = q + 8.  Q6K: low nibble of u = q + 32,
+ *               SYM4 stores u = q + 8, MXFP4 q itself.  Q6K: low nibble of u = q + 32,
  *               [N, K/8].
  *   qweight_hi  Q6K only: high 2 bits of u = q + 32, uint32 [N, K/16], same
  *               bit order.  NULL otherwise.
  *   scales      AFFINE: fp16|bf16 [N, K/gs];  Q4K: uint8 [N, K/32];
- *               Q6K: int8 [N, K/16];  SYM4: fp32 [N, K/gs].
+ *               Q6K: int8 [N, K/16];  SYM4: fp32 [N, K/gs];  MXFP4: uint8
+ *               [N, K/32].
  *   zeros       AFFINE: biases fp16|bf16 [N, K/gs];  Q4K: uint8 zero codes
  *               [N, K/32];  NULL otherwise.
  *   steps       Q4K: uint32 [N, K/256], low 16 bits = fp16 scale step, high
@@ -78,7 +89,8 @@
  *     nested formats), supported (fmt, bits, group_size, dtype) combinations,
  *     alignment, N, K, M > 0.
  *   * Inputs must be finite; non-finite weights or activations give
- *     unspecified results (8-bit checkpoints keep them, see there).
+ *     unspecified results (8-bit checkpoints and MXFP4 rows keep them, see
+ *     there).
  */
 #ifndef QLINEAR_H
 #define QLINEAR_H
@@ -105,7 +117,8 @@ typedef enum {
   QP_FMT_AFFINE = 0,
   QP_FMT_Q4K = 1,
   QP_FMT_Q6K = 2,
-  QP_FMT_SYM4 = 3
+  QP_FMT_SYM4 = 3,
+  QP_FMT_MXFP4 = 4
 } qp_format;
 
 typedef enum { QP_F16 = 0, QP_BF16 = 1, QP_F32 = 2 } qp_dtype;
@@ -126,14 +139,17 @@ typedef enum {
   QP_KERNEL_GEMV_MFMA = 3  /* MFMA qGEMV on exact codes, any M (tiles of 16
                               activation rows), K % 128 == 0, every buffer
                               < 2 GiB                                         */
+  /* MXFP4: both qGEMV selectors mean its few-row kernel, any M (tiles of 16
+     rows, M * N <= 2^34) and any K; AUTO takes it up to 16 rows and where
+     K % 64 != 0, the qGEMM (K <= 2^20) otherwise.                            */
 } qp_kernel;
 
 typedef struct {
   int32_t fmt;          /* qp_format                                         */
-  int32_t bits;         /* AFFINE: 2, 4 or 8; Q4K: 4; Q6K: 6; SYM4: 4         */
-  int32_t group_size;   /* AFFINE: 32, 64, 128; Q4K: 32; Q6K: 16;
+  int32_t bits;         /* AFFINE: 2, 4 or 8; Q6K: 6; others: 4               */
+  int32_t group_size;   /* AFFINE: 32, 64, 128; Q4K, MXFP4: 32; Q6K: 16;
                            SYM4: K (per output channel) or 32, 64, 128       */
-  int32_t super_block;  /* Q4K, Q6K: 256; AFFINE, SYM4: 0                     */
+  int32_t super_block;  /* Q4K, Q6K: 256; others: 0                           */
   int32_t meta_dtype;   /* AFFINE: QP_F16 or QP_BF16; others: ignored         */
   int32_t reserved;     /* must be 0                                         */
   int64_t N;            /* output features (rows of W)                       */
@@ -192,7 +208,7 @@ qp_status qpack_quantize_hqq(const qp_desc* d, const float* W, const qp_weights*
                              void* stream);
 
 /* Expand the packed codes of `w` into `codes` (device [N, K] bytes): uint8
- * q for AFFINE and Q4K, int8 q for Q6K and SYM4 (SYM4 gives the int8 carrier
+ * q for AFFINE, Q4K and MXFP4, int8 q for Q6K and SYM4 (SYM4 gives the int8 carrier
  * form of the a8w4 page, values in [-7, 7]). */
 qp_status qpack_unpack_codes(const qp_desc* d, const qp_weights* w, void* codes,
                              void* stream);
@@ -240,8 +256,8 @@ qp_status qpack_encode_nested(const qp_desc* d, const float* s, const float* z,
                               const qp_weights* out, int32_t* bad, void* stream);
 
 /* Dequantize into W_out (device [N, K] of out_dtype).  QP_F32 gives the fp32
- * evaluation of the format's rule in the order written above (exact for Q6K;
- * the exact value rounded once for AFFINE and SYM4; for Q4K the difference
+ * evaluation of the format's rule in the order written above (exact for Q6K
+ * and MXFP4; the exact value rounded once for AFFINE and SYM4; for Q4K the difference
  * q - zero is rounded once before the product).  QP_F16 / QP_BF16 round that
  * fp32 value to nearest-even. */
 qp_status qpack_dequantize(const qp_desc* d, const qp_weights* w, void* W_out,
@@ -257,7 +273,8 @@ qp_status qpack_dequantize(const qp_desc* d, const qp_weights* w, void* W_out,
  * rounded once to fp16 inside the kernel (scales, zero points and weights
  * are assumed to lie in the fp16 normal range) -- except per-channel SYM4,
  * whose codes q are fp16-exact and whose channel scale multiplies the fp32
- * sum -- and each activation row is
+ * sum, and MXFP4, whose weights are fp16 numbers where they are multiples of
+ * 2^-24 below 2^16 (scales of 2^-23 .. 2^13) -- and each activation row is
  * scaled by a power of two that brings its largest magnitude into fp16
  * range before it is converted (undone in fp32 after the sums), so every
  * finite bf16 activation is taken.  To hold the per-row exponents without a
@@ -488,6 +505,68 @@ qp_status qlinear_gated_backward(const qp_desc* d, const void* dh, int32_t dh_dt
                                  const void* up_codes, const float* up_scales, void* dgate,
                                  void* dup, void* dx, int32_t dx_dtype, void* workspace,
                                  size_t workspace_bytes, void* stream);
+
+/* ---- MXFP4 activations ---------------------------------------------------
+ *
+ * qpack_quantize_activations_mx: x [M, K] (QP_F16, QP_BF16 or QP_F32) into
+ * MXFP4 rows by the format's quantization rule above (bit-exact): xq uint32
+ * [M, K/8] and xs uint8 [M, K/32], laid out like a weight matrix's qweight
+ * and scales, so that qpack_dequantize and qpack_unpack_codes read them with a
+ * descriptor of N = M.  K % 32 == 0. */
+qp_status qpack_quantize_activations_mx(const void* x, int32_t x_dtype, int64_t M, int64_t K,
+                                        void* xq, void* xs, void* stream);
+
+/* y [M, N] (QP_F16, QP_BF16 or QP_F32) = X W^T (+ bias [N], fp32, or NULL)
+ * for MXFP4 activations (xq, xs) and MXFP4 weights; fp32 sums of exact
+ * products, rounded once.  Up to 16 rows, and at any M where K % 128 != 0 or
+ * K > 2^20: the few-row kernel (scales of X between 2^-126 and 2^125, which
+ * finite rows' are); otherwise the scaled matrix cores.  A row with a scale
+ * of 255 gives NaN in its outputs alone.  Limits as the MLP block's products;
+ * outputs reach into no other buffer (QP_EINVAL). */
+qp_status qlinear_forward_mx(const qp_desc* d, const void* xq, const void* xs, int64_t M,
+                             const qp_weights* w, const float* bias, void* y, int32_t y_dtype,
+                             void* stream);
+
+/* ---- Mixture-of-experts layer for few tokens ------------------------------ */
+
+/* What a router's logits become. */
+typedef enum {
+  QP_SCORE_SOFTMAX = 0,  /* e^l / sum over all experts of e^l                 */
+  QP_SCORE_SIGMOID = 1   /* 1 / (1 + e^-l)                                    */
+} qp_score;
+
+/* Host only.  Workspace bytes of qmoe_forward. */
+qp_status qmoe_workspace_bytes(const qp_desc* d_up, const qp_desc* d_down, int64_t M, int32_t experts,
+                               int32_t topk, size_t* bytes);
+
+/* y [M, K] = sum over a token's topk experts e of
+ *     weight * (act(x Wg_e^T) * (x Wu_e^T)) Wd_e^T.
+ * The experts lie one after the other along N (qpack_concat_n): gate and up
+ * are layers of d_up, N = experts * inner and K columns, down is one of
+ * d_down, N = experts * K and inner columns.  MXFP4, Q4K, SYM4 or AFFINE of 4
+ * bits, each of the two its own; 16-bit x [M, K]; y of y_dtype.
+ * router [experts, K] of x_dtype: logits l = x router^T, held in fp64; each
+ *     token takes the topk experts of the largest logits, falling, the lower
+ *     index first among equals (a NaN logit is never taken; where numbers run
+ *     out, ids are -1 and weights 0), with the weights that `score` makes of
+ *     their logits, divided by their sum where norm is 1.  ids (int32
+ *     [M, topk]) and weights (fp32 [M, topk]) are written.
+ * router NULL: ids and weights are read, in any order.  An id outside
+ *     [0, experts) names no expert (one that another GPU holds, say) and adds
+ *     nothing; a token may name an expert twice; score and norm are unused.
+ *     A token without experts gives zeros.
+ * Every weight matrix of an expert that some token takes is read once per 16
+ * of its tokens.  Exact codes, fp32 sums; the inner activations are rounded
+ * to x_dtype, everything else once at the end; results do not depend on
+ * timing, nor a token's on the other tokens.  Limits: M <= 64, experts <= 512,
+ * topk <= 16, M * topk * max(K, inner) < 2^29.  The workspace
+ * (qmoe_workspace_bytes, 16-byte aligned) is busy until the call's kernels
+ * finish; buffers and errors as the MLP block's entry points. */
+qp_status qmoe_forward(const qp_desc* d_up, const qp_desc* d_down, int32_t experts, int32_t topk,
+                       const void* x, int32_t x_dtype, int64_t M, const void* router, int32_t score,
+                       int32_t norm, int32_t* ids, float* weights, const qp_weights* gate,
+                       const qp_weights* up, const qp_weights* down, int32_t act, void* y,
+                       int32_t y_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
