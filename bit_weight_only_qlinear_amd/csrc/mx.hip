@@ -110,14 +110,17 @@ unsigned mx_blocks(int64_t n8) {
 // lane / 32 chooses the half), i.e. the 16 bytes as they lie in memory, so
 // codes go from HBM to LDS by direct loads and from there to the matrix
 // cores untouched; fp32 sums.
-//  * Block: 256 weight rows x 64 MW activation rows, 256 columns (128 bytes
-//    of codes) a step, 8 waves of 32 MW x 64 outputs.
-//  * LDS: two stages of each operand's codes.  A row is 128 bytes, its
-//    16-byte chunk c at c ^ (row & 7): the 16 lanes of a read phase, 16 rows
-//    of one column chunk, then touch every bank once (two rows span all 64).
-//  * Scales: 8 bytes per row and step, in LDS too; a lane's scale
-//    operand is its row's dword, shifted so that its half's byte is where the
-//    instruction's byte select expects it.
+//  * Block: 256 weight rows x 64 MW activation rows, 128 columns (64 bytes of
+//    codes, a dword of scales) a step, 8 waves of 32 MW x 64 outputs.
+//  * LDS: four stages, three of them in flight: a step of matrix instructions
+//    is shorter than the way from L2 (two stages of 256 columns: 130 us on
+//    2048 x 4096 x 14336, waiting most of the time).  Loads return in order, so
+//    waiting until ten are left is waiting for the oldest step's five; one
+//    barrier a step, after which the stage of the step before is free.
+//  * A row's 16-byte chunk c lies at c ^ (row / 4 % 4) of its 64 bytes: the 16
+//    lanes of a read phase, 16 rows of one chunk, then touch every bank once.
+//  * Scales: a lane's operand is its row's dword, shifted so that its half's
+//    bytes are where the instruction's byte select expects them.
 struct MxArgs {
   const unsigned char* xq;
   const unsigned char* xs;
@@ -135,46 +138,21 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_rsrc(const void* p, uint32_
 }
 
 constexpr int kMxN = 256;        // weight rows per block
-constexpr int kMxK = 256;        // columns per step
+constexpr int kMxK = 128;        // columns per step
 
 template <int MW>
 struct MxStage {
-  unsigned char w[kMxN * 128];
-  unsigned char x[64 * MW * 128];
-  unsigned char sw[kMxN * 8];    // scale bytes: per 64 rows two planes of dwords
-  unsigned char sx[64 * MW * 8];
+  unsigned char w[kMxN * 64];
+  unsigned char x[64 * MW * 64];
+  unsigned char sw[kMxN * 4];
+  unsigned char sx[256 * 4];     // 64 MW rows used
 };
 
 typedef int int4v_t __attribute__((ext_vector_type(4)));
 
-// 64 I rows x 128 bytes at column byte kb of a row-major array into LDS, chunk
-// c of a row at c ^ (row & 7); at: the lane's offset in the first 64 rows.
-// Columns from `rowb` on read 0 (last: the step that reaches it).
-template <int I>
-__device__ __forceinline__ void mx_copy(unsigned char* dst, __amdgpu_buffer_rsrc_t r, uint32_t at,
-                                        uint32_t rowb, uint32_t kb, uint32_t col, int wave) {
-  const bool in = kb + col < rowb;
-#pragma unroll
-  for (int i = 0; i < I; ++i)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        r, (__attribute__((address_space(3))) void*)(dst + 1024 * (wave + 8 * i)), 16,
-        in ? at + kb + 64u * (uint32_t)i * rowb : kOff, 0, 0, 0);
-}
-// 8 scale bytes from byte sb on of 64 rows, one row per lane, as two planes of
-// dwords (rows start at multiples of 4 bytes: K % 128 == 0).
-__device__ __forceinline__ void mx_copy_scales(unsigned char* dst, __amdgpu_buffer_rsrc_t r,
-                                               uint32_t rowb, uint32_t sb, int grp, int lane) {
-  const uint32_t at = (uint32_t)(64 * grp + lane) * rowb + sb;
-#pragma unroll
-  for (int d = 0; d < 2; ++d)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        r, (__attribute__((address_space(3))) void*)(dst + 512 * grp + 256 * d), 4,
-        sb + 4u * d < rowb ? at + 4u * d : kOff, 0, 0, 0);
-}
-
 template <int MW>
 __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) k_mxmx(MxArgs a) {
-  __shared__ __attribute__((aligned(16))) MxStage<MW> st0, st1;
+  __shared__ __attribute__((aligned(16))) MxStage<MW> st0, st1, st2, st3;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % MW, wn = wave / MW;   // 64-row block of X; 32 MW rows of W
@@ -187,8 +165,9 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
   const uint32_t mr = (uint32_t)(a.M - m0 < 64 * MW ? a.M - m0 : 64 * MW);
   const __amdgpu_buffer_rsrc_t rw = mx_rsrc(a.wq + n0 * rowb, nr * rowb);
   const __amdgpu_buffer_rsrc_t rx = mx_rsrc(a.xq + m0 * rowb, mr * rowb);
-  const __amdgpu_buffer_rsrc_t rsw = mx_rsrc(a.ws + n0 * srow, nr * srow);
-  const __amdgpu_buffer_rsrc_t rsx = mx_rsrc(a.xs + m0 * srow, mr * srow);
+  // waves 0-3 copy the scales of the weight rows, 4-7 those of X, 64 rows each
+  const __amdgpu_buffer_rsrc_t rs = wave < 4 ? mx_rsrc(a.ws + n0 * srow, nr * srow)
+                                             : mx_rsrc(a.xs + m0 * srow, mr * srow);
 
   float16v_t acc[MW][2];
 #pragma unroll
@@ -198,89 +177,106 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-  // copies: lane's row 8 wave + lane / 8 of each 64, its chunk (row & 7 == lane / 8)
-  const uint32_t ccol = 16u * (((uint32_t)lane & 7u) ^ ((uint32_t)lane >> 3));
-  const uint32_t cat = (uint32_t)(8 * wave + (lane >> 3)) * rowb + ccol;
+  // copies of 16 rows: lane's row lane / 4, its chunk (row / 4 % 4 == lane / 16)
+  const uint32_t cat = (uint32_t)(16 * wave + (lane >> 2)) * rowb +
+                       16u * (((uint32_t)lane & 3u) ^ ((uint32_t)lane >> 4));
+  const uint32_t sat = (uint32_t)(64 * (wave & 3) + lane) * srow;
+  const int S = (int)(a.K / kMxK);
+  using lds_t = __attribute__((address_space(3))) void*;
+  // five loads per wave (waves of tiles with fewer than 128 rows of X load
+  // zeros); steps at or past the end too
   auto load = [&](MxStage<MW>& st, int t) __attribute__((always_inline)) {
-    mx_copy<kMxN / 64>(st.w, rw, cat, rowb, (uint32_t)t * 128u, ccol, wave);
-    mx_copy<MW>(st.x, rx, cat, rowb, (uint32_t)t * 128u, ccol, wave);
-    if (wave < 4) mx_copy_scales(st.sw, rsw, srow, (uint32_t)t * 8u, wave, lane);
-    else if (wave - 4 < MW) mx_copy_scales(st.sx, rsx, srow, (uint32_t)t * 8u, wave - 4, lane);
+    const uint32_t at = t < S ? cat + 64u * (uint32_t)t : kOff;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_t)(st.w + 1024 * (wave + 8 * i)), 16,
+                                               t < S ? at + 128u * (uint32_t)i * rowb : kOff, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < (MW + 1) / 2; ++i)
+      if (MW > 1 || wave < 4)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_t)(st.x + 1024 * (wave + 8 * i)), 16,
+                                                 t < S ? at + 128u * (uint32_t)i * rowb : kOff, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rs, (lds_t)((wave < 4 ? st.sw : st.sx) + 256 * (wave & 3)), 4,
+        t < S ? sat + 4u * (uint32_t)t : kOff, 0, 0, 0);
   };
+  constexpr int kLoads = MW == 4 ? 5 : 4;   // MW == 1: 4 in waves 0-3, 3 in the others
   // fragment reads: row (lane & 31) + a multiple of 32, chunk 2 s + lane / 32
   const uint32_t frow = (uint32_t)lane & 31u, half = (uint32_t)lane >> 5;
-  uint32_t fo[4];
-#pragma unroll
-  for (int s = 0; s < 4; ++s) fo[s] = 128u * frow + 16u * ((2u * s + half) ^ (frow & 7u));
   const uint32_t wbase = (uint32_t)wn * 32u * MW, xbase = (uint32_t)wm * 64u;
-  auto rd = [&](const unsigned char* p, uint32_t o) __attribute__((always_inline)) {
-    return *reinterpret_cast<const int4v_t*>(p + o);
-  };
-  // dword d (of 2) of a row's scale bytes, this lane's half in bytes 0 and 2
-  auto rd_sc = [&](const unsigned char* p, uint32_t row, int d) __attribute__((always_inline)) {
-    return *reinterpret_cast<const uint32_t*>(p + 512u * (row >> 6) + 256u * d + 4u * (row & 63u)) >>
-           (8u * half);
-  };
+  uint32_t fo[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) fo[s] = 64u * frow + 16u * ((2u * s + half) ^ ((frow >> 2) & 3u));
   auto wide = [](int4v_t v) __attribute__((always_inline)) {
     return int8v_t{v[0], v[1], v[2], v[3], 0, 0, 0, 0};   // 4-bit operands: the first four registers
   };
   auto compute = [&](const MxStage<MW>& st) __attribute__((always_inline)) {
-    const unsigned char* pw = st.w + 128u * wbase;
-    const unsigned char* px = st.x + 128u * xbase;
-    uint32_t sw[MW], sx[2];
     int4v_t A[2][MW], B[2][2];
-    auto fetch = [&](int s, int4v_t (&fa)[MW], int4v_t (&fb)[2]) __attribute__((always_inline)) {
+    uint32_t sw[MW], sx[2];
 #pragma unroll
-      for (int i = 0; i < MW; ++i) fa[i] = rd(pw, fo[s] + 4096u * i);
+    for (int s = 0; s < 2; ++s) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) fb[j] = rd(px, fo[s] + 4096u * j);
-    };
-    fetch(0, A[0], B[0]);
+      for (int i = 0; i < MW; ++i)
+        A[s][i] = *reinterpret_cast<const int4v_t*>(st.w + 64u * wbase + fo[s] + 2048u * i);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (s % 2 == 0) {
+      for (int j = 0; j < 2; ++j)
+        B[s][j] = *reinterpret_cast<const int4v_t*>(st.x + 64u * xbase + fo[s] + 2048u * j);
+      if (s == 0) {
 #pragma unroll
-        for (int i = 0; i < MW; ++i) sw[i] = rd_sc(st.sw, wbase + 32u * i + frow, s / 2);
+        for (int i = 0; i < MW; ++i)
+          sw[i] = *reinterpret_cast<const uint32_t*>(st.sw + 4u * wbase + 4u * frow + 128u * i) >> (8u * half);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) sx[j] = rd_sc(st.sx, xbase + 32u * j + frow, s / 2);
+        for (int j = 0; j < 2; ++j)
+          sx[j] = *reinterpret_cast<const uint32_t*>(st.sx + 4u * xbase + 4u * frow + 128u * j) >> (8u * half);
       }
-      if (s < 3) fetch(s + 1, A[(s + 1) & 1], B[(s + 1) & 1]);   // a substep ahead
-      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int i = 0; i < MW; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          if (s & 1)
+          if (s)
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                wide(A[s & 1][i]), wide(B[s & 1][j]), acc[i][j], 4, 4, 2, (int)sw[i], 2, (int)sx[j]);
+                wide(A[s][i]), wide(B[s][j]), acc[i][j], 4, 4, 2, (int)sw[i], 2, (int)sx[j]);
           else
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                wide(A[s & 1][i]), wide(B[s & 1][j]), acc[i][j], 4, 4, 0, (int)sw[i], 0, (int)sx[j]);
+                wide(A[s][i]), wide(B[s][j]), acc[i][j], 4, 4, 0, (int)sw[i], 0, (int)sx[j]);
         }
-      __builtin_amdgcn_sched_barrier(0);
-    }
   };
+  // this wave's loads of the oldest step have landed; then everyone's have,
+  // and everyone is done with the step before
   auto turn = []() __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
+    constexpr int n = 2 * (MW == 1 ? 3 : kLoads);
+    __builtin_amdgcn_s_waitcnt((n & 0xF) | (0x7 << 4) | ((n >> 4) << 14));   // and its LDS reads
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
   };
 
-  const int S = (int)((a.K + kMxK - 1) / kMxK);
   load(st0, 0);
-  turn();
+  load(st1, 1);
+  load(st2, 2);
 #pragma unroll 1
-  for (int t = 0; t < S; t += 2) {   // columns past K are zeros: a step past S adds nothing
-    load(st1, t + 1);
+  for (int t = 0; t < S; t += 4) {   // a step past the end multiplies zeros
+    turn();
+    load(st3, t + 3);
     compute(st0);
     turn();
-    load(st0, t + 2);
-    compute(st1);
+    load(st0, t + 4);
+    if (t + 1 < S) compute(st1);
     turn();
+    load(st1, t + 5);
+    if (t + 2 < S) compute(st2);
+    turn();
+    load(st2, t + 6);
+    if (t + 3 < S) compute(st3);
   }
+  __builtin_amdgcn_s_waitcnt(0);   // the loads past the end write the stages too
+  __syncthreads();
 
   // Result: lane = activation row l % 32, weight rows 8 g + 4 (l / 32) + 0..3
   // in registers 4 g .. 4 g + 3.  16-bit outputs turn through the wave's own
-  // part of the first stage, so that every store is a run of 64 MW bytes of a row.
+  // part of the stages, so that every store is a run of 64 MW bytes of a row.
   const int64_t nw = n0 + wbase;
   auto bias4 = [&](int64_t n, float (&v)[4]) {
     if (!a.bias) return;
@@ -290,8 +286,10 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
         v[e] += a.bias[n + e];
   };
   constexpr uint32_t RB = 64u * MW;   // bytes of a row in LDS, chunk c at c ^ (row & (4 MW - 1))
-  static_assert(32u * RB * 8u <= sizeof(MxStage<MW>), "room for eight waves");
-  unsigned char* own = reinterpret_cast<unsigned char*>(&st0) + (uint32_t)wave * 32u * RB;
+  // two waves' parts per stage
+  static_assert(32u * RB * 2u <= sizeof(MxStage<MW>), "room for two waves");
+  MxStage<MW>& mine = wave < 2 ? st0 : wave < 4 ? st1 : wave < 6 ? st2 : st3;
+  unsigned char* own = reinterpret_cast<unsigned char*>(&mine) + (uint32_t)(wave & 1) * 32u * RB;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int64_t mj = m0 + xbase + 32 * j;
