@@ -1,6 +1,8 @@
 // MXFP4 (the microscaling format of E2M1 codes with one E8M0 scale byte per 32
 // columns): quantization, dequantization, and the product of two MXFP4
 // operands on the scaled matrix cores.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "qp_internal.hpp"
 
@@ -111,15 +113,16 @@ unsigned mx_blocks(int64_t n8) {
 // codes go from HBM to LDS by direct loads and from there to the matrix
 // cores untouched; fp32 sums.
 //  * Block: 256 weight rows x 64 MW activation rows, 128 columns (64 bytes of
-//    codes, a dword of scales) a step, 8 waves of 32 MW x 64 outputs.
+//    codes) a step, 8 waves of 32 MW x 64 outputs.
 //  * LDS: four stages, three of them in flight: a step of matrix instructions
 //    is shorter than the way from L2 (two stages of 256 columns: 130 us on
 //    2048 x 4096 x 14336, waiting most of the time).  Loads return in order, so
-//    waiting until ten are left is waiting for the oldest step's five; one
-//    barrier a step, after which the stage of the step before is free.
+//    waiting until two steps' are left is waiting for the oldest step's;
+//    one barrier a step, after which the stage of the step before is free.
 //  * A row's 16-byte chunk c lies at c ^ (row / 4 % 4) of its 64 bytes: the 16
 //    lanes of a read phase, 16 rows of one chunk, then touch every bank once.
-//  * Scales: a lane's operand is its row's dword, shifted so that its half's
+//  * Scales: 16 bytes per row for four steps (a dword per step and row touches
+//    a line for each four bytes).  A lane's operand is its row's dword, shifted so that its half's
 //    bytes are where the instruction's byte select expects them.
 struct MxArgs {
   const unsigned char* xq;
@@ -144,8 +147,10 @@ template <int MW>
 struct MxStage {
   unsigned char w[kMxN * 64];
   unsigned char x[64 * MW * 64];
-  unsigned char sw[kMxN * 4];
-  unsigned char sx[256 * 4];     // 64 MW rows used
+};
+struct MxScales {                // of four steps, 16 bytes per row
+  unsigned char w[kMxN * 16];
+  unsigned char x[256 * 16];     // 64 MW rows used
 };
 
 typedef int int4v_t __attribute__((ext_vector_type(4)));
@@ -153,6 +158,7 @@ typedef int int4v_t __attribute__((ext_vector_type(4)));
 template <int MW>
 __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) k_mxmx(MxArgs a) {
   __shared__ __attribute__((aligned(16))) MxStage<MW> st0, st1, st2, st3;
+  __shared__ __attribute__((aligned(16))) MxScales sc0, sc1;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % MW, wn = wave / MW;   // 64-row block of X; 32 MW rows of W
@@ -183,8 +189,7 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
   const uint32_t sat = (uint32_t)(64 * (wave & 3) + lane) * srow;
   const int S = (int)(a.K / kMxK);
   using lds_t = __attribute__((address_space(3))) void*;
-  // five loads per wave (waves of tiles with fewer than 128 rows of X load
-  // zeros); steps at or past the end too
+  // steps at or past the end load zeros, so that every step has as many loads
   auto load = [&](MxStage<MW>& st, int t) __attribute__((always_inline)) {
     const uint32_t at = t < S ? cat + 64u * (uint32_t)t : kOff;
 #pragma unroll
@@ -196,11 +201,14 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
       if (MW > 1 || wave < 4)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_t)(st.x + 1024 * (wave + 8 * i)), 16,
                                                  t < S ? at + 128u * (uint32_t)i * rowb : kOff, 0, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rs, (lds_t)((wave < 4 ? st.sw : st.sx) + 256 * (wave & 3)), 4,
-        t < S ? sat + 4u * (uint32_t)t : kOff, 0, 0, 0);
   };
-  constexpr int kLoads = MW == 4 ? 5 : 4;   // MW == 1: 4 in waves 0-3, 3 in the others
+  // the scales of steps t .. t + 3 (the row's last ones may reach into the
+  // next row's: bytes of steps that are not taken)
+  auto load_sc = [&](MxScales& sc, int t) __attribute__((always_inline)) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_t)((wave < 4 ? sc.w : sc.x) + 1024 * (wave & 3)), 16,
+                                             t < S ? sat + 4u * (uint32_t)t : kOff, 0, 0, 0);
+  };
+  constexpr int kLoads = MW == 4 ? 4 : MW == 2 ? 3 : 2;   // per step; MW == 1: 3 in waves 0-3
   // fragment reads: row (lane & 31) + a multiple of 32, chunk 2 s + lane / 32
   const uint32_t frow = (uint32_t)lane & 31u, half = (uint32_t)lane >> 5;
   const uint32_t wbase = (uint32_t)wn * 32u * MW, xbase = (uint32_t)wm * 64u;
@@ -210,7 +218,8 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
   auto wide = [](int4v_t v) __attribute__((always_inline)) {
     return int8v_t{v[0], v[1], v[2], v[3], 0, 0, 0, 0};   // 4-bit operands: the first four registers
   };
-  auto compute = [&](const MxStage<MW>& st) __attribute__((always_inline)) {
+  auto compute = [&](const MxStage<MW>& st, const MxScales& sc, auto U) __attribute__((always_inline)) {
+    constexpr uint32_t u = decltype(U)::value;
     int4v_t A[2][MW], B[2][2];
     uint32_t sw[MW], sx[2];
 #pragma unroll
@@ -224,10 +233,10 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
       if (s == 0) {
 #pragma unroll
         for (int i = 0; i < MW; ++i)
-          sw[i] = *reinterpret_cast<const uint32_t*>(st.sw + 4u * wbase + 4u * frow + 128u * i) >> (8u * half);
+          sw[i] = *reinterpret_cast<const uint32_t*>(sc.w + 16u * wbase + 16u * frow + 512u * i + 4u * u) >> (8u * half);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          sx[j] = *reinterpret_cast<const uint32_t*>(st.sx + 4u * xbase + 4u * frow + 128u * j) >> (8u * half);
+          sx[j] = *reinterpret_cast<const uint32_t*>(sc.x + 16u * xbase + 16u * frow + 512u * j + 4u * u) >> (8u * half);
       }
     }
 #pragma unroll
@@ -244,32 +253,43 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
                 wide(A[s][i]), wide(B[s][j]), acc[i][j], 4, 4, 0, (int)sw[i], 0, (int)sx[j]);
         }
   };
-  // this wave's loads of the oldest step have landed; then everyone's have,
-  // and everyone is done with the step before
-  auto turn = []() __attribute__((always_inline)) {
-    constexpr int n = 2 * (MW == 1 ? 3 : kLoads);
+  // This wave's loads of the oldest step have landed; then everyone's have,
+  // and everyone is done with the step before.  Younger: two steps' codes, and
+  // the next four steps' scales, which go out after a first step's codes.
+  auto turn = [](auto U) __attribute__((always_inline)) {
+    constexpr int n = 2 * kLoads + (decltype(U)::value ? 1 : 0);
     __builtin_amdgcn_s_waitcnt((n & 0xF) | (0x7 << 4) | ((n >> 4) << 14));   // and its LDS reads
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
+  using C0 = std::integral_constant<int, 0>;
+  using C1 = std::integral_constant<int, 1>;
+  using C2 = std::integral_constant<int, 2>;
+  using C3 = std::integral_constant<int, 3>;
 
+  load_sc(sc0, 0);
   load(st0, 0);
   load(st1, 1);
   load(st2, 2);
-#pragma unroll 1
-  for (int t = 0; t < S; t += 4) {   // a step past the end multiplies zeros
-    turn();
+  auto four = [&](int t, const MxScales& sc, MxScales& next) __attribute__((always_inline)) {
+    turn(C0{});
     load(st3, t + 3);
-    compute(st0);
-    turn();
+    load_sc(next, t + 4);
+    compute(st0, sc, C0{});
+    turn(C1{});
     load(st0, t + 4);
-    if (t + 1 < S) compute(st1);
-    turn();
+    if (t + 1 < S) compute(st1, sc, C1{});
+    turn(C2{});
     load(st1, t + 5);
-    if (t + 2 < S) compute(st2);
-    turn();
+    if (t + 2 < S) compute(st2, sc, C2{});
+    turn(C3{});
     load(st2, t + 6);
-    if (t + 3 < S) compute(st3);
+    if (t + 3 < S) compute(st3, sc, C3{});
+  };
+#pragma unroll 1
+  for (int t = 0; t < S; t += 8) {
+    four(t, sc0, sc1);
+    if (t + 4 < S) four(t + 4, sc1, sc0);
   }
   __builtin_amdgcn_s_waitcnt(0);   // the loads past the end write the stages too
   __syncthreads();
