@@ -218,40 +218,67 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
   auto wide = [](int4v_t v) __attribute__((always_inline)) {
     return int8v_t{v[0], v[1], v[2], v[3], 0, 0, 0, 0};   // 4-bit operands: the first four registers
   };
-  auto compute = [&](const MxStage<MW>& st, const MxScales& sc, auto U) __attribute__((always_inline)) {
-    constexpr uint32_t u = decltype(U)::value;
-    int4v_t A[2][MW], B[2][2];
-    uint32_t sw[MW], sx[2];
+  // Operands of a step's two halves (64 columns each), the second of which is
+  // multiplied after the next barrier, while that step's first fragments come
+  // from LDS.
+  int4v_t A[2][MW], B[2][2];
+  uint32_t sw[MW], sx[2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+  for (int i = 0; i < MW; ++i) {
+    A[1][i] = int4v_t{0, 0, 0, 0};
+    sw[i] = 0;
+  }
 #pragma unroll
-      for (int i = 0; i < MW; ++i)
-        A[s][i] = *reinterpret_cast<const int4v_t*>(st.w + 64u * wbase + fo[s] + 2048u * i);
+  for (int j = 0; j < 2; ++j) {
+    B[1][j] = int4v_t{0, 0, 0, 0};
+    sx[j] = 0;
+  }
+  auto fetch = [&](const MxStage<MW>& st, auto H) __attribute__((always_inline)) {
+    constexpr int h = decltype(H)::value;
+#pragma unroll
+    for (int i = 0; i < MW; ++i)
+      A[h][i] = *reinterpret_cast<const int4v_t*>(st.w + 64u * wbase + fo[h] + 2048u * i);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      B[h][j] = *reinterpret_cast<const int4v_t*>(st.x + 64u * xbase + fo[h] + 2048u * j);
+  };
+  auto multiply = [&](auto H) __attribute__((always_inline)) {
+    constexpr int h = decltype(H)::value;
+#pragma unroll
+    for (int i = 0; i < MW; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        B[s][j] = *reinterpret_cast<const int4v_t*>(st.x + 64u * xbase + fo[s] + 2048u * j);
-      if (s == 0) {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            wide(A[h][i]), wide(B[h][j]), acc[i][j], 4, 4, 2 * h, (int)sw[i], 2 * h, (int)sx[j]);
+  };
+  using C0 = std::integral_constant<int, 0>;
+  using C1 = std::integral_constant<int, 1>;
+  using C2 = std::integral_constant<int, 2>;
+  using C3 = std::integral_constant<int, 3>;
+  auto compute = [&](const MxStage<MW>& st, const MxScales& sc, int t, auto U) __attribute__((always_inline)) {
+    constexpr uint32_t u = decltype(U)::value;
+    // a step past the end multiplies codes of 0, whose scales (the next row's)
+    // must not be NaN
+    const uint32_t on = t + (int)u < S ? ~0u : 0u;
+    uint32_t nw[MW], nx[2];
+    fetch(st, C0{});
 #pragma unroll
-        for (int i = 0; i < MW; ++i)
-          sw[i] = *reinterpret_cast<const uint32_t*>(sc.w + 16u * wbase + 16u * frow + 512u * i + 4u * u) >> (8u * half);
+    for (int i = 0; i < MW; ++i)
+      nw[i] = *reinterpret_cast<const uint32_t*>(sc.w + 16u * wbase + 16u * frow + 512u * i + 4u * u);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          sx[j] = *reinterpret_cast<const uint32_t*>(sc.x + 16u * xbase + 16u * frow + 512u * j + 4u * u) >> (8u * half);
-      }
-    }
+    for (int j = 0; j < 2; ++j)
+      nx[j] = *reinterpret_cast<const uint32_t*>(sc.x + 16u * xbase + 16u * frow + 512u * j + 4u * u);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(C1{});
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(st, C1{});
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int i = 0; i < MW; ++i) sw[i] = (nw[i] & on) >> (8u * half);
 #pragma unroll
-      for (int i = 0; i < MW; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (s)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                wide(A[s][i]), wide(B[s][j]), acc[i][j], 4, 4, 2, (int)sw[i], 2, (int)sx[j]);
-          else
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                wide(A[s][i]), wide(B[s][j]), acc[i][j], 4, 4, 0, (int)sw[i], 0, (int)sx[j]);
-        }
+    for (int j = 0; j < 2; ++j) sx[j] = (nx[j] & on) >> (8u * half);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(C0{});
+    __builtin_amdgcn_sched_barrier(0);
   };
   // This wave's loads of the oldest step have landed; then everyone's have,
   // and everyone is done with the step before.  Younger: two steps' codes, and
@@ -262,10 +289,6 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  using C0 = std::integral_constant<int, 0>;
-  using C1 = std::integral_constant<int, 1>;
-  using C2 = std::integral_constant<int, 2>;
-  using C3 = std::integral_constant<int, 3>;
 
   load_sc(sc0, 0);
   load(st0, 0);
@@ -275,22 +298,23 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
     turn(C0{});
     load(st3, t + 3);
     load_sc(next, t + 4);
-    compute(st0, sc, C0{});
+    compute(st0, sc, t, C0{});
     turn(C1{});
     load(st0, t + 4);
-    if (t + 1 < S) compute(st1, sc, C1{});
+    compute(st1, sc, t, C1{});
     turn(C2{});
     load(st1, t + 5);
-    if (t + 2 < S) compute(st2, sc, C2{});
+    compute(st2, sc, t, C2{});
     turn(C3{});
     load(st2, t + 6);
-    if (t + 3 < S) compute(st3, sc, C3{});
+    compute(st3, sc, t, C3{});
   };
 #pragma unroll 1
   for (int t = 0; t < S; t += 8) {
     four(t, sc0, sc1);
     if (t + 4 < S) four(t + 4, sc1, sc0);
   }
+  multiply(C1{});
   __builtin_amdgcn_s_waitcnt(0);   // the loads past the end write the stages too
   __syncthreads();
 
