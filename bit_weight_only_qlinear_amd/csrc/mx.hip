@@ -154,6 +154,15 @@ struct MxScales {                // of four steps, 16 bytes per row
 };
 
 typedef int int4v_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+
+// Two values rounded to nearest even, as a pair of dt (bf16: one instruction).
+__device__ __forceinline__ uint32_t pack16(float a, float b, int dt) {
+  const f32x2_t v = {a, b};
+  return dt == BF16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t))
+                    : __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2_t));
+}
 
 template <int MW>
 __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) k_mxmx(MxArgs a) {
@@ -233,23 +242,19 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
     B[1][j] = int4v_t{0, 0, 0, 0};
     sx[j] = 0;
   }
-  auto fetch = [&](const MxStage<MW>& st, auto H) __attribute__((always_inline)) {
+  // Products of half H, one read of the other half's operands (then of the
+  // scales) after each: the reads of eight waves back up in the LDS queue, and
+  // what a wave issues behind them would wait.
+  auto product = [&](auto H, int k) __attribute__((always_inline)) {
     constexpr int h = decltype(H)::value;
-#pragma unroll
-    for (int i = 0; i < MW; ++i)
-      A[h][i] = *reinterpret_cast<const int4v_t*>(st.w + 64u * wbase + fo[h] + 2048u * i);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      B[h][j] = *reinterpret_cast<const int4v_t*>(st.x + 64u * xbase + fo[h] + 2048u * j);
+    const int i = k / 2, j = k % 2;
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+        wide(A[h][i]), wide(B[h][j]), acc[i][j], 4, 4, 2 * h, (int)sw[i], 2 * h, (int)sx[j]);
   };
-  auto multiply = [&](auto H) __attribute__((always_inline)) {
+  auto read = [&](const MxStage<MW>& st, auto H, int k) __attribute__((always_inline)) {
     constexpr int h = decltype(H)::value;
-#pragma unroll
-    for (int i = 0; i < MW; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-            wide(A[h][i]), wide(B[h][j]), acc[i][j], 4, 4, 2 * h, (int)sw[i], 2 * h, (int)sx[j]);
+    if (k < 2) B[h][k] = *reinterpret_cast<const int4v_t*>(st.x + 64u * xbase + fo[h] + 2048u * k);
+    else A[h][k - 2] = *reinterpret_cast<const int4v_t*>(st.w + 64u * wbase + fo[h] + 2048u * (k - 2));
   };
   using C0 = std::integral_constant<int, 0>;
   using C1 = std::integral_constant<int, 1>;
@@ -261,24 +266,27 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
     // must not be NaN
     const uint32_t on = t + (int)u < S ? ~0u : 0u;
     uint32_t nw[MW], nx[2];
-    fetch(st, C0{});
+    constexpr int P = 2 * MW, R = MW + 2;   // products and operands of a half
 #pragma unroll
-    for (int i = 0; i < MW; ++i)
-      nw[i] = *reinterpret_cast<const uint32_t*>(sc.w + 16u * wbase + 16u * frow + 512u * i + 4u * u);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      nx[j] = *reinterpret_cast<const uint32_t*>(sc.x + 16u * xbase + 16u * frow + 512u * j + 4u * u);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(C1{});
-    __builtin_amdgcn_sched_barrier(0);
-    fetch(st, C1{});
+    for (int k = 0; k < (P > R ? P : R); ++k) {
+      if (k < P) product(C1{}, k);
+      __builtin_amdgcn_sched_barrier(0);
+      if (k < R) read(st, C0{}, k);
+      if (k < 2) nx[k] = *reinterpret_cast<const uint32_t*>(sc.x + 16u * xbase + 16u * frow + 512u * k + 4u * u);
+      else if (k < R) nw[k - 2] = *reinterpret_cast<const uint32_t*>(sc.w + 16u * wbase + 16u * frow + 512u * (k - 2) + 4u * u);
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int i = 0; i < MW; ++i) sw[i] = (nw[i] & on) >> (8u * half);
 #pragma unroll
     for (int j = 0; j < 2; ++j) sx[j] = (nx[j] & on) >> (8u * half);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(C0{});
-    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < (P > R ? P : R); ++k) {
+      if (k < P) product(C0{}, k);
+      __builtin_amdgcn_sched_barrier(0);
+      if (k < R) read(st, C1{}, k);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   // This wave's loads of the oldest step have landed; then everyone's have,
   // and everyone is done with the step before.  Younger: two steps' codes, and
@@ -314,7 +322,8 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
     four(t, sc0, sc1);
     if (t + 4 < S) four(t + 4, sc1, sc0);
   }
-  multiply(C1{});
+#pragma unroll
+  for (int k = 0; k < 2 * MW; ++k) product(C1{}, k);
   __builtin_amdgcn_s_waitcnt(0);   // the loads past the end write the stages too
   __syncthreads();
 
@@ -360,11 +369,8 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
             }
           }
         } else {
-          uint32_t h[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = a.ydt == BF16 ? f32_to_bf16_rne(v[e]) : f32_to_f16_rne(v[e]);
-          *reinterpret_cast<uint2*>(own + frow * RB + 16u * ((4u * i + g) ^ (frow & (4u * MW - 1u))) + 8u * half) =
-              make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+          const uint2 h = make_uint2(pack16(v[0], v[1], a.ydt), pack16(v[2], v[3], a.ydt));
+          *reinterpret_cast<uint2*>(own + frow * RB + 16u * ((4u * i + g) ^ (frow & (4u * MW - 1u))) + 8u * half) = h;
         }
       }
     if (a.ydt == F32) continue;
