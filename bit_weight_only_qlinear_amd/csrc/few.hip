@@ -50,6 +50,7 @@ struct FewArgs {
   uint32_t mrow[3];        // metadata bytes per row: scales, zeros, steps
   uint32_t mlds[2][3];     // LDS offset of each slice
   int meta_lds;            // 1: metadata staged in LDS
+  uint32_t x_lds;          // LDS offset of the activations, 4 Q KiB per wave
   const void* x;           // [rows, K] of 16 bits, or MXFP4 codes
   const void* xsc;         //   and their scales
   int64_t M;
@@ -71,6 +72,11 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t few_rsrc(const void* p, uint64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)(uint32_t)bytes,
                                            0x00020000);
+}
+
+// 16 bytes per lane from `off` into 1 KiB of LDS.
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, unsigned char* lds, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
 }
 
 template <bool XB>
@@ -193,19 +199,31 @@ __device__ __forceinline__ void sum16(float (&v)[16], float (&o)[4]) {
   }
 }
 
+// The tokens of a pass: their rows of x (uniform byte offsets) and how many
+// there are.
+template <int Q>
+struct Tok {
+  uint32_t off[4 * Q];
+  int n;
+};
+
 // Rows 4 g + l % 4 of the pass (a pair: the first G / 2 groups of layer 0,
 // the others of layer 1) times 4 Q tokens, over this wave's steps; the sums
-// go to red [4 G][4 Q].
-// f0: the pass's first row in the block; xoff: byte offset of the lane's
-// token rows in x (kOff: none).
+// go to red [4 G][4 Q].  f0: the pass's first row in the block.
+//
+// 16-bit activations come through the wave's own part of LDS (xl): a load
+// instruction takes 1 KiB of one token's row, where the operands' own layout
+// would touch 64 pieces of 64 bytes (16 tokens: 2.4 TB/s of codes at most).
+// Token t's 16-byte piece j lies at j ^ (t % 4), so that the 16 lanes of a read
+// phase (four tokens, four chunks) touch every bank once.  Tokens that are not
+// there stay what was in LDS: they are rows of results of their own.
 template <int KIND, bool XB, bool XM, int Q, int G, bool PAIR>
 __device__ __forceinline__ void few_pass(const FewArgs& a, const Unit& u,
                                          const unsigned char* smem, const uint32_t (&mbase)[2][3],
                                          const __amdgpu_buffer_rsrc_t (&rw)[2],
                                          const __amdgpu_buffer_rsrc_t (&rm)[2][3],
-                                         const __amdgpu_buffer_rsrc_t (&rx)[2],
-                                         const uint32_t (&xoff)[Q], int f0, int kw, float* red,
-                                         bool first) {
+                                         const __amdgpu_buffer_rsrc_t (&rx)[2], const Tok<Q>& tok,
+                                         unsigned char* xl, int f0, int kw, float* red, bool first) {
   const int lane = threadIdx.x & 63;
   const uint32_t j = lane & 3, b = lane >> 2;
   const uint32_t C = (uint32_t)a.C, rowb = (uint32_t)(a.K / 2);
@@ -213,42 +231,50 @@ __device__ __forceinline__ void few_pass(const FewArgs& a, const Unit& u,
   auto layer = [](int g) { return PAIR && g >= G / 2 ? 1 : 0; };
   auto lrow = [&](int g) { return (uint32_t)f0 + 4u * (PAIR ? g % (G / 2) : g) + j; };
 
-  uint32_t wo[G];
-#pragma unroll
-  for (int g = 0; g < G; ++g) wo[g] = lrow(g) * rowb + 16u * b;
-
-  // the activations travel a step ahead with the codes where registers allow
-  constexpr bool AHEAD = Q == 1;
-  // one quad's activations of a step: the bits, or MXFP4 codes and scale
-  struct X {
-    uint4 v[XM ? 1 : 4];
-    uint32_t s;
-  };
+  const uint32_t wo = lrow(0) * rowb + 16u * b;
   struct Step {
     uint4 w[G];
-    X x[AHEAD ? Q : 1];
   };
-  auto load_x = [&](int s, int q) {
-    X r;
-    const bool ok = (uint32_t)s * 16u + b < C && xoff[q] != kOff;
-    const uint32_t at = xoff[q] + ((uint32_t)s * 16u + b) * (XM ? 16u : 64u);
+  // MXFP4 activations, straight into registers: the next step's codes and
+  // scales, and the lane's row of them
+  uint4 xc[XM ? Q : 1];
+  uint32_t xsc[XM ? Q : 1], xm[XM ? Q : 1];
+  if constexpr (XM) {
 #pragma unroll
-    for (int v = 0; v < (XM ? 1 : 4); ++v)
-      r.v[v] = __builtin_bit_cast(
-          uint4, __builtin_amdgcn_raw_buffer_load_b128(rx[0], ok ? at + 16u * v : kOff, 0, 0));
-    r.s = 0;
-    if constexpr (XM) r.s = __builtin_amdgcn_raw_buffer_load_b8(rx[1], ok ? at / 16u : kOff, 0, 0);
-    return r;
-  };
-  auto load = [&](int s, Step& st) {
-    const bool ok = (uint32_t)s * 16u + b < C;
-    const uint32_t so = (uint32_t)s * 256u;
+    for (int q = 0; q < Q; ++q) {
+      const uint32_t r01 = j & 1 ? tok.off[4 * q + 1] : tok.off[4 * q], r23 = j & 1 ? tok.off[4 * q + 3] : tok.off[4 * q + 2];
+      xm[q] = 4 * q + (int)j < tok.n ? (j & 2 ? r23 : r01) : kOff;
+    }
+  }
+  auto load = [&](int s, Step& st) __attribute__((always_inline)) {
+    const uint32_t c = (uint32_t)s * 16u + b;
+    const bool ok = c < C;
+    const uint32_t at = ok ? wo + (uint32_t)s * 256u : kOff;
 #pragma unroll
     for (int g = 0; g < G; ++g)
       st.w[g] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
-                                              rw[layer(g)], ok ? wo[g] + so : kOff, 0, 2));
-    if constexpr (AHEAD) st.x[0] = load_x(s, 0);
+                                              rw[layer(g)], at + 4u * (PAIR ? g % (G / 2) : g) * rowb, 0, 2));
   };
+  auto load_x = [&](int s) __attribute__((always_inline)) {
+    if constexpr (XM) {
+      const uint32_t c = (uint32_t)s * 16u + b;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const bool in = c < C && xm[q] != kOff;
+        xc[q] = __builtin_bit_cast(
+            uint4, __builtin_amdgcn_raw_buffer_load_b128(rx[0], in ? xm[q] + 16u * c : kOff, 0, 0));
+        xsc[q] = __builtin_amdgcn_raw_buffer_load_b8(rx[1], in ? xm[q] / 16u + c : kOff, 0, 0);
+      }
+    } else {
+      const bool ok = (uint32_t)s * 16u + b < C;
+#pragma unroll
+      for (int t = 0; t < 4 * Q; ++t)
+        if (t < tok.n)
+          to_lds(rx[0], xl + 1024 * t,
+                 ok ? tok.off[t] + (uint32_t)s * 1024u + 16u * ((uint32_t)lane ^ (t & 3u)) : kOff);
+    }
+  };
+  const uint32_t xr = j * 1024u + 64u * b + 16u * j;   // piece 0 of the lane's token and chunk
 
   f32x4_t acc[G][Q];
 #pragma unroll
@@ -256,16 +282,17 @@ __device__ __forceinline__ void few_pass(const FewArgs& a, const Unit& u,
 #pragma unroll
     for (int q = 0; q < Q; ++q) acc[g][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](int s, const Step& st) {
+  // step s from st, whose registers then take step s + 2 KW; the activations of
+  // step s + KW into LDS once this step's are read
+  auto compute = [&](int s, Step& st) __attribute__((always_inline)) {
     const uint32_t c = (uint32_t)s * 16u + b, cc = c < C ? c : C - 1u;
     uint2 xo[Q][8];
     f32x4_t xs[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const X x = AHEAD ? st.x[0] : load_x(s, q);
       if constexpr (XM) {   // exact in bf16
-        const float sc = e8m0(x.s);
-        const uint32_t w[4] = {x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w};
+        const float sc = e8m0(xsc[q]);
+        const uint32_t w[4] = {xc[q].x, xc[q].y, xc[q].z, xc[q].w};
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           xo[q][2 * v] = make_uint2(e2m1_pair<true, 0>(w[v], sc), e2m1_pair<true, 1>(w[v], sc));
@@ -273,8 +300,19 @@ __device__ __forceinline__ void few_pass(const FewArgs& a, const Unit& u,
         }
       } else {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) x_ops<KIND>(x.v[v], xo[q][2 * v], xo[q][2 * v + 1]);
+        for (int v = 0; v < 4; ++v)
+          x_ops<KIND>(*reinterpret_cast<const uint4*>(xl + 4096u * q + (xr ^ (16u * v))), xo[q][2 * v], xo[q][2 * v + 1]);
       }
+    }
+    if (s + a.KW < S) {
+      if constexpr (!XM) {
+        __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0): LDS is read
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      load_x(s + a.KW);
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
       xs[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       if constexpr (KIND != F_MX4) {
         const uint32_t one = XB ? 0x3F803F80u : 0x3C003C00u;
@@ -322,22 +360,24 @@ __device__ __forceinline__ void few_pass(const FewArgs& a, const Unit& u,
           if constexpr (KIND != F_MX4) acc[g][q][i] = fmaf(Tv, xs[q][i], acc[g][q][i]);
         }
     }
+    if (s + 2 * a.KW < S) load(s + 2 * a.KW, st);
   };
 
+  // codes two steps ahead, activations one
   Step s0, s1;
-  load(kw, s0);   // steps past the end read zeros
+  load_x(kw);
+  load(kw, s0);          // steps past the end read zeros
+  load(kw + a.KW, s1);
   if (first) {
     // the metadata copies were issued before these loads
-    constexpr int n = G + (AHEAD ? (XM ? 2 : 4) : 0);
+    constexpr int n = 2 * G;
+    static_assert(n < 64, "a wait counts to 63");
     __builtin_amdgcn_s_waitcnt((n & 0xF) | (0x7 << 4) | (0xF << 8) | ((n >> 4) << 14));
     __syncthreads();
   }
   for (int s = kw; s < S; s += 2 * a.KW) {
-    if (s + a.KW < S) load(s + a.KW, s1);
     compute(s, s0);
-    if (s + a.KW >= S) break;
-    if (s + 2 * a.KW < S) load(s + 2 * a.KW, s0);
-    compute(s + a.KW, s1);
+    if (s + a.KW < S) compute(s + a.KW, s1);
   }
 
   const int R = lane >> 4, p = ((R & 1) << 1) | (R >> 1);
@@ -371,24 +411,24 @@ __device__ __forceinline__ void few_tokens(const FewArgs& a, const Unit& u,
                                            const unsigned char* smem, const uint32_t (&mbase)[2][3],
                                            const __amdgpu_buffer_rsrc_t (&rw)[2],
                                            const __amdgpu_buffer_rsrc_t (&rm)[2][3],
-                                           const __amdgpu_buffer_rsrc_t (&rx)[2], const int* xrow,
-                                           const int* orow, int t0, float* red, bool first) {
+                                           const __amdgpu_buffer_rsrc_t (&rx)[2], unsigned char* xl,
+                                           const int* xrow, const int* orow, int t0, float* red,
+                                           bool first) {
   constexpr bool PAIR = is_pair(MODE);
-  constexpr int G = PAIR ? (Q == 4 ? 4 : 8) : 4;     // groups of four rows per pass
+  constexpr int G = PAIR && Q == 1 ? 8 : 4;          // groups of four rows per pass
   constexpr int F = PAIR ? 2 * G : 4 * G;            // features per pass
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = wave % a.KW, team = wave / a.KW;
-  uint32_t xoff[Q];
+  Tok<Q> tok;
+  tok.n = u.T - t0 < 4 * Q ? u.T - t0 : 4 * Q;
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    const int t = t0 + 4 * q + (lane & 3);
-    xoff[q] = t < u.T ? (uint32_t)xrow[t] * (uint32_t)(XM ? a.K / 2 : a.K * 2) : kOff;
-  }
+  for (int t = 0; t < 4 * Q; ++t)
+    tok.off[t] = t < tok.n ? (uint32_t)__builtin_amdgcn_readfirstlane(xrow[t0 + t]) * (uint32_t)(XM ? a.K / 2 : a.K * 2) : 0u;
   constexpr int kRed = 4 * G * 4 * Q;
 #pragma unroll 1
   for (int f = 0; f < kFeat; f += F) {
     const int f0 = team * kFeat + f;
-    few_pass<KIND, XB, XM, Q, G, PAIR>(a, u, smem, mbase, rw, rm, rx, xoff, f0, kw, red + wave * kRed,
+    few_pass<KIND, XB, XM, Q, G, PAIR>(a, u, smem, mbase, rw, rm, rx, tok, xl + wave * 4096 * Q, f0, kw, red + wave * kRed,
                                    first && f == 0);
     __syncthreads();
     // the team's threads: (feature, token) with the feature fastest
@@ -429,15 +469,23 @@ constexpr int kSlots = 16;        // experts per token
 // first slot with it; -1 where fewer are chosen.  Every wave ends up with the
 // answer; xrow and orow are complete after the last barrier.
 template <int MODE>
-__device__ __forceinline__ int find_unit(const FewArgs& a, int want, int* mask, int* xrow,
+__device__ __forceinline__ int find_unit(const FewArgs& a, int want, int* mask, int* ids, int* xrow,
                                          int* orow, int& T) {
   const int tid = threadIdx.x, lane = tid & 63;
+  const int n = (int)a.M * a.topk;
+  int got[kTok * kSlots / 256];
+#pragma unroll
+  for (int k = 0; k < kTok * kSlots / 256; ++k) got[k] = tid + 256 * k < n ? a.ids[tid + 256 * k] : -1;
   for (int e = tid; e < 2 * a.E; e += 256) mask[e] = 0;
   __syncthreads();
-  const int n = (int)a.M * a.topk;
-  for (int i = tid; i < n; i += 256) {
-    const int e = a.ids[i], m = i / a.topk;
-    if (e >= 0 && e < a.E) atomicOr(&mask[2 * e + (m >> 5)], (int)(1u << (m & 31)));
+#pragma unroll
+  for (int k = 0; k < kTok * kSlots / 256; ++k) {
+    const int i = tid + 256 * k, e = got[k];
+    if (i < n) ids[i] = e;
+    if (e >= 0 && e < a.E) {
+      const int m = i / a.topk;
+      atomicOr(&mask[2 * e + (m >> 5)], (int)(1u << (m & 31)));
+    }
   }
   __syncthreads();
   int found = -1;
@@ -460,7 +508,7 @@ __device__ __forceinline__ int find_unit(const FewArgs& a, int want, int* mask, 
   if (tid < 64 && ((tok >> lane) & 1)) {
     const int at = __popcll(tok & ((uint64_t(1) << lane) - 1));
     int s = 0;
-    while (a.ids[lane * a.topk + s] != found) ++s;   // ends: the token is in the mask
+    while (ids[lane * a.topk + s] != found) ++s;   // ends: the token is in the mask
     const int slot = lane * a.topk + s;
     xrow[at] = MODE == FM_UP ? lane : slot;
     orow[at] = slot;
@@ -477,7 +525,7 @@ k_few(FewArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   __shared__ float red[4 * 16 * 4 * 4];
   __shared__ int xrow[kTok], orow[kTok];
-  __shared__ int mask[EXPERTS ? 2 * kExperts : 1];
+  __shared__ int mask[EXPERTS ? 2 * kExperts : 1], ids[EXPERTS ? kTok * kSlots : 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -486,7 +534,7 @@ k_few(FewArgs a) {
   const int tile = (int)(blockIdx.x % (unsigned)a.tiles);   // and the expert or the tile of x's rows
   int64_t xbase = 0;
   if constexpr (EXPERTS) {
-    expert = find_unit<MODE>(a, (int)(blockIdx.x / (unsigned)a.tiles), mask, xrow, orow, u.T);
+    expert = find_unit<MODE>(a, (int)(blockIdx.x / (unsigned)a.tiles), mask, ids, xrow, orow, u.T);
     if (expert < 0) return;
   } else {
     xbase = (int64_t)(blockIdx.x / (unsigned)a.tiles) * (4 * Q);
@@ -518,9 +566,7 @@ k_few(FewArgs a) {
       mbase[l][i] = a.mlds[l][i] + head;
       if (a.meta_lds && a.mrow[i])
         for (uint32_t ch = (uint32_t)wave; ch * 1024u < bytes; ch += 4)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(
-              rm[l][i], (__attribute__((address_space(3))) void*)(smem + a.mlds[l][i] + ch * 1024u), 16,
-              ch * 1024u + 16u * (uint32_t)lane, 0, 0, 0);
+          to_lds(rm[l][i], smem + a.mlds[l][i] + ch * 1024u, ch * 1024u + 16u * (uint32_t)lane);
     }
   }
   if constexpr (!PAIR) rw[1] = rw[0];
@@ -533,15 +579,13 @@ k_few(FewArgs a) {
     FewArgs b = a;
     if (xbase) b.y = static_cast<unsigned char*>(a.y) + xbase * a.N * (a.ydt == F32 ? 4 : 2);
     __syncthreads();
-    few_tokens<KIND, XB, XM, Q, MODE>(b, u, smem, mbase, rw, rm, rx, xrow, orow, 0, red, true);
+    few_tokens<KIND, XB, XM, Q, MODE>(b, u, smem, mbase, rw, rm, rx, smem + a.x_lds, xrow, orow, 0, red, true);
   } else {
-    if (u.T <= 4) {
-      few_tokens<KIND, XB, XM, 1, MODE>(a, u, smem, mbase, rw, rm, rx, xrow, orow, 0, red, true);
-    } else if (u.T <= 8) {
-      few_tokens<KIND, XB, XM, 2, MODE>(a, u, smem, mbase, rw, rm, rx, xrow, orow, 0, red, true);
-    } else {
-      for (int t0 = 0; t0 < u.T; t0 += 16)
-        few_tokens<KIND, XB, XM, 4, MODE>(a, u, smem, mbase, rw, rm, rx, xrow, orow, t0, red, t0 == 0);
+    for (int t0 = 0; t0 < u.T; t0 += 4 * Q) {
+      if (Q == 1 || u.T - t0 <= 4)
+        few_tokens<KIND, XB, XM, 1, MODE>(a, u, smem, mbase, rw, rm, rx, smem + a.x_lds, xrow, orow, t0, red, t0 == 0);
+      else
+        few_tokens<KIND, XB, XM, Q, MODE>(a, u, smem, mbase, rw, rm, rx, smem + a.x_lds, xrow, orow, t0, red, t0 == 0);
     }
   }
 }
@@ -554,37 +598,83 @@ __global__ void __launch_bounds__(256) k_combine(const float* __restrict__ part,
                                                  const float* __restrict__ weights, int E, int topk,
                                                  int64_t N, void* y, int ydt) {
   const int64_t m = blockIdx.y;
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;   // N % 32 == 0
   if (n >= N) return;
-  float v = 0.f;
-  for (int s = 0; s < topk; ++s) {
-    const int e = ids[m * topk + s];
-    if (e < 0 || e >= E) continue;
-    int f = 0;
-    while (ids[m * topk + f] != e) ++f;
-    v = fmaf(weights[m * topk + s], part[(m * topk + f) * N + n], v);
+  int e[kSlots];
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    e[s] = s < topk ? ids[m * topk + s] : -1;
+    if (e[s] >= E) e[s] = -1;
   }
-  few_store(y, m * N + n, v, ydt);
+  // all loads first: a slot's sum lies with the first slot of its expert
+  float4 p[kSlots];
+  float w[kSlots];
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    int f = s;
+#pragma unroll
+    for (int k = kSlots - 1; k >= 0; --k)
+      if (k < s && e[k] == e[s]) f = k;
+    const bool on = e[s] >= 0;   // slots past topk hold -1
+    w[s] = on ? weights[m * topk + s] : 0.f;
+    p[s] = on ? *reinterpret_cast<const float4*>(part + (m * topk + f) * N + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    v[0] = fmaf(w[s], p[s].x, v[0]);
+    v[1] = fmaf(w[s], p[s].y, v[1]);
+    v[2] = fmaf(w[s], p[s].z, v[2]);
+    v[3] = fmaf(w[s], p[s].w, v[3]);
+  }
+  if (ydt == F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(y) + m * N + n) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = ydt == BF16 ? f32_to_bf16_rne(v[i]) : f32_to_f16_rne(v[i]);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + m * N + n) =
+        make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  }
 }
 
 // ---- routing: logits in fp64 (products of two 16-bit values are exact in
 // fp32), so that the choice between two experts next to each other does not
 // depend on the order of additions.
 template <bool XB>
-__device__ __forceinline__ double logit_part(const uint16_t* x, const uint16_t* r, int64_t K, int lane) {
+__device__ __forceinline__ double dot8(const uint4 u, const uint4 v) {
+  const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
   double s = 0.0;
-  for (int64_t c = lane; c < K / 8; c += 64) {   // K % 32 == 0
-    const uint4 u = reinterpret_cast<const uint4*>(x)[c], v = reinterpret_cast<const uint4*>(r)[c];
-    const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float p = XB ? __uint_as_float(a[i] << 16) * __uint_as_float(b[i] << 16)
-                         : f16_to_f32(a[i] & 0xFFFFu) * f16_to_f32(b[i] & 0xFFFFu);
-      const float q = XB ? __uint_as_float(a[i] & 0xFFFF0000u) * __uint_as_float(b[i] & 0xFFFF0000u)
-                         : f16_to_f32(a[i] >> 16) * f16_to_f32(b[i] >> 16);
-      s += (double)p;
-      s += (double)q;
+  for (int i = 0; i < 4; ++i) {
+    const float p = XB ? __uint_as_float(a[i] << 16) * __uint_as_float(b[i] << 16)
+                       : f16_to_f32(a[i] & 0xFFFFu) * f16_to_f32(b[i] & 0xFFFFu);
+    const float q = XB ? __uint_as_float(a[i] & 0xFFFF0000u) * __uint_as_float(b[i] & 0xFFFF0000u)
+                       : f16_to_f32(a[i] >> 16) * f16_to_f32(b[i] >> 16);
+    s += (double)p;
+    s += (double)q;
+  }
+  return s;
+}
+// A lane's part of a logit: columns 8 (lane + 64 (part + parts k)) ..., eight
+// loads of each row in flight.
+template <bool XB>
+__device__ __forceinline__ double logit_part(const uint16_t* x, const uint16_t* r, int64_t K, int lane,
+                                             int part, int parts) {
+  const uint4* xv = reinterpret_cast<const uint4*>(x);
+  const uint4* rv = reinterpret_cast<const uint4*>(r);
+  const int n = (int)(K / 8), step = 64 * parts;   // K % 32 == 0
+  double s = 0.0;
+  for (int c0 = lane + 64 * part; c0 < n; c0 += 8 * step) {
+    uint4 u[8], v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = c0 + k * step;
+      u[k] = c < n ? xv[c] : make_uint4(0, 0, 0, 0);
+      v[k] = c < n ? rv[c] : make_uint4(0, 0, 0, 0);
     }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += dot8<XB>(u[k], v[k]);
   }
   return s;
 }
@@ -603,91 +693,117 @@ struct RouteArgs {
   float* weights;
 };
 
-// Token m's choice from its logits l [E]: one wave; each round takes the
-// largest left (ties: the lowest expert).  NaN logits are never chosen before
-// a number; a row with too few numbers ends with experts -1 and weights 0.
-__device__ __forceinline__ void choose(const RouteArgs& a, int64_t m, const double* l, int lane) {
-  constexpr int PL = kExperts / 64;
-  double v[PL];
-#pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int e = lane + 64 * i;
-    v[i] = e < a.E ? l[e] : -__builtin_inf();
-    if (!(v[i] == v[i])) v[i] = -__builtin_inf();
+// Token m's choice from its logits l [E] in LDS, by a block of `threads`.
+// An expert's place is the number of those in front of it (a larger logit, or
+// the same and a lower index), counted by several threads each; the first topk
+// places are the choice.  NaN logits come after all numbers and are never
+// chosen: places that no number takes get expert -1 and weight 0.
+struct Choice {
+  double l[kExperts];
+  double part[16];
+  int place[kExperts];
+  double top[kSlots], w[kSlots];
+  int id[kSlots];
+};
+__device__ __forceinline__ void choose(const RouteArgs& a, int64_t m, Choice& c, int threads) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int E = a.E;
+  for (int e = tid; e < E; e += threads) c.place[e] = 0;
+  if (tid < kSlots) {
+    c.id[tid] = -1;
+    c.top[tid] = -__builtin_inf();
   }
-  // the largest first: the softmax's shift
-  auto best = [&](int& at) {
-    double t = v[0];
-#pragma unroll
-    for (int i = 1; i < PL; ++i) t = v[i] > t ? v[i] : t;
-    for (int off = 32; off > 0; off >>= 1) {
-      const double o = __shfl_xor(t, off, 64);
-      t = o > t ? o : t;
+  __syncthreads();
+  // threads per expert: a power of two
+  int per = 1;
+  while (2 * per * E <= threads) per *= 2;
+  for (int i = tid; i < E * per; i += threads) {
+    const int e = i / per, s = i % per;
+    const double v = c.l[e];
+    int n = 0;
+    for (int k = s; k < E; k += per) {
+      const double o = c.l[k];
+      n += o > v || (o == v && k < e) ? 1 : 0;
     }
-    at = -1;
-    if (t > -__builtin_inf()) {
-#pragma unroll
-      for (int i = PL - 1; i >= 0; --i) {
-        const uint64_t b = __ballot(v[i] == t);
-        if (b) at = 64 * i + __ffsll((unsigned long long)b) - 1;
-      }
-    }
-    return t;
-  };
-  double sum = 0.0, top = 0.0, total = 0.0, mine = 0.0;
-  int my = -1;
-  for (int s = 0; s < a.topk; ++s) {
-    int at;
-    const double t = best(at);
-    if (s == 0) {
-      top = t;
-      if (a.score == 0) {
-#pragma unroll
-        for (int i = 0; i < PL; ++i) sum += lane + 64 * i < a.E ? exp(v[i] - top) : 0.0;
-        sum = wave_sum_f64(sum);
-      }
-    }
-    if (at < 0) break;
-    const double p = a.score == 0 ? exp(t - top) / sum : 1.0 / (1.0 + exp(-t));
-    total += p;
-    if (lane == s) {
-      mine = p;
-      my = at;
-    }
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (lane + 64 * i == at) v[i] = -__builtin_inf();
+    if (!(v > -__builtin_inf())) n = kExperts;
+    if (n) atomicAdd(&c.place[e], n);
   }
-  if (lane < a.topk) {
-    a.ids[m * a.topk + lane] = my;
-    a.weights[m * a.topk + lane] = (float)(a.norm ? (total > 0.0 ? mine / total : 0.0) : mine);
+  __syncthreads();
+  for (int e = tid; e < E; e += threads)
+    if (c.place[e] < a.topk) {
+      c.id[c.place[e]] = e;
+      c.top[c.place[e]] = c.l[e];
+    }
+  __syncthreads();
+  const double hi = c.top[0];
+  double sum = 0.0;
+  if (a.score == 0) {
+    for (int e = tid; e < E; e += threads) sum += c.l[e] > -__builtin_inf() ? exp(c.l[e] - hi) : 0.0;
+    sum = wave_sum_f64(sum);
+    if (lane == 0) c.part[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+    for (int w = 0; w < threads / 64; ++w) sum += c.part[w];
+  }
+  if (tid < a.topk)
+    c.w[tid] = c.id[tid] < 0 ? 0.0 : a.score == 0 ? exp(c.top[tid] - hi) / sum : 1.0 / (1.0 + exp(-c.top[tid]));
+  __syncthreads();
+  if (tid < a.topk) {
+    double total = 0.0;
+    for (int s = 0; s < a.topk; ++s) total += c.w[s];
+    const double w = a.norm ? (total > 0.0 ? c.w[tid] / total : 0.0) : c.w[tid];
+    a.ids[m * a.topk + tid] = c.id[tid];
+    a.weights[m * a.topk + tid] = (float)w;
   }
 }
 
-// One block per token: its logits (a wave per expert), then the choice.
+// One block per token: its logits, `parts` waves to each (a power of two, in
+// one round of the 16 waves where E <= 8), then the choice.
 template <bool XB>
 __global__ void __launch_bounds__(1024) k_route(RouteArgs a) {
-  __shared__ double l[kExperts];
+  __shared__ Choice c;
+  __shared__ double s[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t m = blockIdx.x;
-  for (int e = wave; e < a.E; e += 16) {
-    const double s = wave_sum_f64(logit_part<XB>(a.x + m * a.K, a.r + e * a.K, a.K, lane));
-    if (lane == 0) l[e] = s;
+  int parts = 1;
+  while (2 * parts * a.E <= 16) parts *= 2;
+  if (parts == 1) {
+    for (int e = wave; e < a.E; e += 16) {
+      const double v = wave_sum_f64(logit_part<XB>(a.x + m * a.K, a.r + (int64_t)e * a.K, a.K, lane, 0, 1));
+      if (lane == 0) c.l[e] = v;
+    }
+  } else {
+    const int e = wave / parts;
+    if (e < a.E) {
+      const double v = wave_sum_f64(
+          logit_part<XB>(a.x + m * a.K, a.r + (int64_t)e * a.K, a.K, lane, wave % parts, parts));
+      if (lane == 0) s[wave] = v;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < a.E) {
+      double v = 0.0;
+      for (int p = 0; p < parts; ++p) v += s[threadIdx.x * parts + p];
+      c.l[threadIdx.x] = v;
+    }
   }
   __syncthreads();
-  if (wave == 0) choose(a, m, l, lane);
+  choose(a, m, c, 1024);
 }
-// A wave per logit, then a wave per token.
+// A wave per logit, then a block per token.
 template <bool XB>
 __global__ void __launch_bounds__(256) k_logits(RouteArgs a) {
   const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6);
   const int64_t m = blockIdx.y;
   if (e >= a.E) return;
-  const double s = wave_sum_f64(logit_part<XB>(a.x + m * a.K, a.r + (int64_t)e * a.K, a.K, lane));
+  const double s = wave_sum_f64(logit_part<XB>(a.x + m * a.K, a.r + (int64_t)e * a.K, a.K, lane, 0, 1));
   if (lane == 0) a.logits[m * a.E + e] = s;
 }
-__global__ void __launch_bounds__(64) k_choose(RouteArgs a) {
-  choose(a, blockIdx.x, a.logits + (int64_t)blockIdx.x * a.E, threadIdx.x);
+__global__ void __launch_bounds__(256) k_choose(RouteArgs a) {
+  __shared__ Choice c;
+  const int64_t m = blockIdx.x;
+  for (int e = threadIdx.x; e < a.E; e += 256) c.l[e] = a.logits[m * a.E + e];
+  __syncthreads();
+  choose(a, m, c, 256);
 }
 
 int few_kind(const Desc& d) {
@@ -698,8 +814,9 @@ int few_kind(const Desc& d) {
   return -1;
 }
 
-// Sizes, LDS layout and launch shape that the modes share.
-size_t fill(const Desc& d, int64_t rows, bool pair, FewArgs& a) {
+// Sizes, LDS layout and launch shape that the modes share; xq: quads of tokens
+// per pass whose activations go through LDS.
+size_t fill(const Desc& d, int64_t rows, bool pair, int xq, FewArgs& a) {
   a.K = d.K;
   a.N = rows;
   a.C = (int)(d.K / 32);
@@ -722,30 +839,35 @@ size_t fill(const Desc& d, int64_t rows, bool pair, FewArgs& a) {
       a.mlds[l][i] = (uint32_t)lds;
       if (a.mrow[i]) lds += ((size_t)a.RW * kFeat * a.mrow[i] + 15 + 1023) / 1024 * 1024;
     }
-  // 48 KiB: two blocks per CU and more; longer rows read their metadata
-  // where it lies
+  // longer rows read their metadata where it lies
   a.meta_lds = lds <= 48 * 1024;
-  return a.meta_lds ? lds : 0;
+  a.x_lds = a.meta_lds ? (uint32_t)lds : 0u;
+  return a.x_lds + (size_t)xq * 4 * 4096;
 }
 
 using FewFn = void (*)(FewArgs);
 template <int KIND, int MODE>
-FewFn expert_fn(bool xb) {
-  return xb ? k_few<KIND, true, false, 4, MODE> : k_few<KIND, false, false, 4, MODE>;
+FewFn expert_fn(bool xb, int q) {
+  if (q == 1) return xb ? k_few<KIND, true, false, 1, MODE> : k_few<KIND, false, false, 1, MODE>;
+  return xb ? k_few<KIND, true, false, 2, MODE> : k_few<KIND, false, false, 2, MODE>;
 }
 template <int MODE>
-FewFn expert_fn(int kind, bool xb) {
+FewFn expert_fn(int kind, bool xb, int q) {
   switch (kind) {
-    case F_MX4: return expert_fn<F_MX4, MODE>(xb);
-    case F_AFF4: return expert_fn<F_AFF4, MODE>(xb);
-    case F_AFF4H: return expert_fn<F_AFF4H, MODE>(xb);
-    case F_Q4K: return expert_fn<F_Q4K, MODE>(xb);
-    default: return expert_fn<F_SYM4, MODE>(xb);
+    case F_MX4: return expert_fn<F_MX4, MODE>(xb, q);
+    case F_AFF4: return expert_fn<F_AFF4, MODE>(xb, q);
+    case F_AFF4H: return expert_fn<F_AFF4H, MODE>(xb, q);
+    case F_Q4K: return expert_fn<F_Q4K, MODE>(xb, q);
+    default: return expert_fn<F_SYM4, MODE>(xb, q);
   }
 }
+// Quads of tokens per pass.
+int quads(int64_t M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
+
 template <int MODE, bool XB, bool XM>
 FewFn mx_fn(int64_t M) {
-  return M <= 4 ? k_few<F_MX4, XB, XM, 1, MODE> : M <= 8 ? k_few<F_MX4, XB, XM, 2, MODE> : k_few<F_MX4, XB, XM, 4, MODE>;
+  const int q = quads(M);
+  return q == 1 ? k_few<F_MX4, XB, XM, 1, MODE> : q == 2 ? k_few<F_MX4, XB, XM, 2, MODE> : k_few<F_MX4, XB, XM, 4, MODE>;
 }
 template <int MODE>
 FewFn mx_fn(bool xb, int64_t M) {
@@ -757,7 +879,7 @@ FewFn mx_fn(bool xb, int64_t M) {
 hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bufs& b,
                       const void* bias, void* y, int ydt, hipStream_t s) {
   FewArgs a{};
-  const size_t lds = fill(d, d.N, false, a);
+  const size_t lds = fill(d, d.N, false, quads(M), a);
   a.w[0] = a.w[1] = b;
   a.x = x;
   a.M = M;
@@ -765,7 +887,7 @@ hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bu
   a.ydt = ydt;
   a.bias[0] = bias;
   a.bdt = xdt;
-  const int64_t per = M <= 4 ? 4 : M <= 8 ? 8 : 16;
+  const int64_t per = 4 * quads(M);
   hipLaunchKernelGGL(mx_fn<FM_LINEAR>(xdt == BF16, M), dim3((unsigned)(a.tiles * ((M + per - 1) / per))),
                      dim3(256), lds, s, a);
   return hipGetLastError();
@@ -774,7 +896,7 @@ hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bu
 hipError_t launch_few_mx(const Desc& d, const void* xq, const void* xs, int64_t M, const Bufs& b,
                          const float* bias, void* y, int ydt, hipStream_t s) {
   FewArgs a{};
-  const size_t lds = fill(d, d.N, false, a);
+  const size_t lds = fill(d, d.N, false, 0, a);
   a.w[0] = a.w[1] = b;
   a.x = xq;
   a.xsc = xs;
@@ -783,7 +905,7 @@ hipError_t launch_few_mx(const Desc& d, const void* xq, const void* xs, int64_t 
   a.ydt = ydt;
   a.bias[0] = bias;
   a.bdt = F32;
-  const int64_t per = M <= 4 ? 4 : M <= 8 ? 8 : 16;
+  const int64_t per = 4 * quads(M);
   hipLaunchKernelGGL((mx_fn<FM_LINEAR, true, true>(M)), dim3((unsigned)(a.tiles * ((M + per - 1) / per))),
                      dim3(256), lds, s, a);
   return hipGetLastError();
@@ -791,7 +913,7 @@ hipError_t launch_few_mx(const Desc& d, const void* xq, const void* xs, int64_t 
 
 hipError_t launch_few_gated(const Desc& d, const GatedArgs& g, hipStream_t s) {
   FewArgs a{};
-  const size_t lds = fill(d, d.N, true, a);
+  const size_t lds = fill(d, d.N, true, quads(g.M), a);
   a.w[0] = g.gate;
   a.w[1] = g.up;
   a.x = g.x;
@@ -802,7 +924,7 @@ hipError_t launch_few_gated(const Desc& d, const GatedArgs& g, hipStream_t s) {
   a.bias[1] = g.bias_u;
   a.bdt = g.xdt;
   a.act = g.act;
-  const int64_t per = g.M <= 4 ? 4 : g.M <= 8 ? 8 : 16;
+  const int64_t per = 4 * quads(g.M);
   hipLaunchKernelGGL(mx_fn<FM_GATED>(g.xdt == BF16, g.M),
                      dim3((unsigned)(a.tiles * ((g.M + per - 1) / per))), dim3(256), lds, s, a);
   return hipGetLastError();
@@ -839,12 +961,14 @@ hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStr
     } else {
       hipLaunchKernelGGL((xb ? k_logits<true> : k_logits<false>), dim3((unsigned)((m.E + 3) / 4), (unsigned)m.M),
                          dim3(256), 0, s, r);
-      hipLaunchKernelGGL(k_choose, dim3((unsigned)m.M), dim3(64), 0, s, r);
+      hipLaunchKernelGGL(k_choose, dim3((unsigned)m.M), dim3(256), 0, s, r);
     }
   }
   const int64_t most = m.M * m.topk < m.E ? m.M * m.topk : m.E;
+  // up to four tokens: the form that holds one quad, in fewer registers
+  const int q = m.M <= 4 ? 1 : 2;
   FewArgs a{};
-  size_t lds = fill(up, inner, true, a);
+  size_t lds = fill(up, inner, true, q, a);
   a.w[0] = m.gate;
   a.w[1] = m.up;
   a.x = m.x;
@@ -855,13 +979,13 @@ hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStr
   a.ids = m.ids;
   a.E = m.E;
   a.topk = m.topk;
-  hipLaunchKernelGGL(expert_fn<FM_UP>(few_kind(up), xb), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
-  lds = fill(down, K, false, a);
+  hipLaunchKernelGGL(expert_fn<FM_UP>(few_kind(up), xb, q), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
+  lds = fill(down, K, false, q, a);
   a.w[0] = a.w[1] = m.down;
   a.x = h;
   a.y = part;
-  hipLaunchKernelGGL(expert_fn<FM_DOWN>(few_kind(down), xb), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
-  hipLaunchKernelGGL(k_combine, dim3((unsigned)((K + 255) / 256), (unsigned)m.M), dim3(256), 0, s, part, m.ids,
+  hipLaunchKernelGGL(expert_fn<FM_DOWN>(few_kind(down), xb, q), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
+  hipLaunchKernelGGL(k_combine, dim3((unsigned)((K + 1023) / 1024), (unsigned)m.M), dim3(256), 0, s, part, m.ids,
                      m.weights, m.E, m.topk, K, m.y, m.ydt);
   return hipGetLastError();
 }
