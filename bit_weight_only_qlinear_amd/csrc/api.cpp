@@ -387,8 +387,11 @@ qp_status plan_forward(const qp_desc* d, qp::Desc* dd, int32_t x_dtype, int64_t 
   if (dd->fmt == qp::MXFP4) {
     // One kernel for few rows behind both qGEMV selectors, in tiles of 16
     // rows where K % 64 != 0 keeps more of them from the qGEMM.
-    *use = kernel == QP_KERNEL_GEMM || (kernel == QP_KERNEL_AUTO && M > kFewRows && gemm_ok(*dd))
+    const bool fits = qp::few_fits(*dd, false);
+    *use = kernel == QP_KERNEL_GEMM || (kernel == QP_KERNEL_AUTO && (M > kFewRows || !fits) && gemm_ok(*dd))
                ? USE_GEMM : USE_FEW;
+    if (*use == USE_FEW && !fits)
+      return fail(QP_EUNSUPPORTED, "MXFP4 rows of K=%lld are too long for the few-row kernel", (long long)dd->K);
     if (*use == USE_FEW && M * ((dd->N + 15) / 16) > (int64_t(1) << 30))
       return fail(QP_EUNSUPPORTED, "MXFP4 in tiles of 16 rows: M * N must be <= 2^34");
     return QP_OK;
@@ -764,7 +767,8 @@ qp_status check_workspace(const void* ws, size_t have, size_t need) {
 // tile on exact codes.
 enum GatedForm { GATED_GEMV, GATED_SKINNY, GATED_STAGED, GATED_FEW };
 GatedForm gated_form(const qp::Desc& d, int64_t M, bool save) {
-  if (d.fmt == qp::MXFP4) return save || M > kFewRows ? GATED_STAGED : GATED_FEW;
+  if (d.fmt == qp::MXFP4)
+    return save || M > kFewRows || !qp::few_fits(d, true) ? GATED_STAGED : GATED_FEW;
   size_t b[5];
   sizes_of(d, b);
   bool small_bufs = (size_t)M * (size_t)d.K * 2 < (size_t(1) << 31);
@@ -1097,7 +1101,10 @@ qp_status qlinear_forward_mx(const qp_desc* d, const void* xq, const void* xs, i
   if ((st = check_apart(spans)) != QP_OK) return st;
   (void)hipGetLastError();
   // whole dwords of scale bytes per row, and 32-bit offsets inside a tile
-  const bool tiles = M > kFewRows && dd.K % 128 == 0 && dd.K <= (int64_t(1) << 20);
+  const bool fits = qp::few_fits(dd, false);
+  const bool tiles = (M > kFewRows || !fits) && dd.K % 128 == 0 && dd.K <= (int64_t(1) << 20);
+  if (!tiles && !fits)
+    return fail(QP_EUNSUPPORTED, "qlinear_forward_mx: K=%lld needs K %% 128 == 0 and K <= 2^20", (long long)dd.K);
   const hipStream_t s = (hipStream_t)stream;
   return hip_status(tiles ? qp::launch_mx_mx(dd, xq, xs, M, bufs_of(w), bias, y, y_dtype, s)
                           : qp::launch_few_mx(dd, xq, xs, M, bufs_of(w), bias, y, y_dtype, s),
@@ -1130,6 +1137,9 @@ qp_status check_moe(const qp_desc* d_up, const qp_desc* d_down, int64_t M, int32
                 "an expert of %lld x %lld (up) needs a down projection of %lld x %lld, got %lld x %lld",
                 (long long)(up->N / experts), (long long)up->K, (long long)up->K,
                 (long long)(up->N / experts), (long long)(down->N / experts), (long long)down->K);
+  if (!qp::few_fits(*up, true) || !qp::few_fits(*down, false))
+    return fail(QP_EUNSUPPORTED, "qmoe: rows of K=%lld or inner=%lld are too long (the metadata of 16 rows must "
+                "fit LDS)", (long long)up->K, (long long)down->K);
   if (M * topk * (up->K > down->K ? up->K : down->K) >= int64_t(1) << 29)
     return fail(QP_EUNSUPPORTED, "M * topk * max(K, inner) must be < 2^29 (M=%lld, topk=%d, K=%lld, inner=%lld)",
                 (long long)M, topk, (long long)up->K, (long long)down->K);

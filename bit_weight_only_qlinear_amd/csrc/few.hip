@@ -18,9 +18,12 @@
 // per 1 KiB of codes, still twice what HBM delivers at 16 rows.
 //
 // Four waves per block.  KW of them split a row's 512-column steps, the
-// others take other rows; the sums over lanes run as a transposed reduction
-// (permlane swaps, then DPP), those over waves through LDS.  The block's
-// metadata is staged in LDS by direct loads, in front of the first codes.
+// others take other rows.  A team of KW waves runs over its rows in passes of
+// 4 G, as one stream: the codes of the next two steps are always on their way,
+// those of the next pass while a pass's sums are taken.  The sums over lanes
+// are a transposed reduction (permlane swaps, then DPP), those over waves meet
+// in LDS.  The metadata of the block's rows is staged in LDS by direct loads,
+// in front of the first codes.
 //
 // Experts: a block's unit is (a-th expert that some token chose, 16 rows or
 // features of it); every block finds its expert and the expert's tokens from
@@ -37,7 +40,6 @@ enum FKind : int { F_MX4 = 0, F_AFF4 = 1, F_AFF4H = 2, F_Q4K = 3, F_SYM4 = 4 };
 enum FMode : int { FM_LINEAR = 0, FM_GATED = 1, FM_UP = 2, FM_DOWN = 3 };
 constexpr bool is_pair(int mode) { return mode == FM_GATED || mode == FM_UP; }
 
-constexpr int kFeat = 16;          // rows (features of a pair) per team
 constexpr uint32_t kOff = 0x80000000u;   // at or past every resource: reads 0
 
 struct FewArgs {
@@ -46,11 +48,10 @@ struct FewArgs {
   int C;                   // 32-column chunks per row
   int gsh;                 // chunk -> group: >> gsh
   int KW, RW;              // waves per row, row teams (KW * RW == 4)
+  int feats;               // rows (features of a pair) per team, a multiple of 16
   int tiles;               // blocks per expert (or layer)
   uint32_t mrow[3];        // metadata bytes per row: scales, zeros, steps
   uint32_t mlds[2][3];     // LDS offset of each slice
-  int meta_lds;            // 1: metadata staged in LDS
-  uint32_t x_lds;          // LDS offset of the activations, 4 Q KiB per wave
   const void* x;           // [rows, K] of 16 bits, or MXFP4 codes
   const void* xsc;         //   and their scales
   int64_t M;
@@ -207,9 +208,16 @@ struct Tok {
   int n;
 };
 
-// Rows 4 g + l % 4 of the pass (a pair: the first G / 2 groups of layer 0,
-// the others of layer 1) times 4 Q tokens, over this wave's steps; the sums
-// go to red [4 G][4 Q].  f0: the pass's first row in the block.
+__device__ __forceinline__ void few_store(void* y, int64_t i, float v, int dt) {
+  if (dt == F32) static_cast<float*>(y)[i] = v;
+  else if (dt == BF16) static_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_bf16_rne(v);
+  else static_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_f16_rne(v);
+}
+
+// All tokens t0 .. t0 + 4 Q - 1 of the unit, all rows of the block.  A pass of
+// a team takes rows 4 g + l % 4 for g < G from its row f0 on (a pair: g < G / 2
+// of layer 0, the others of layer 1).  xrow, orow: rows of x and of the output,
+// per token; red: two buffers of the passes' partial sums.
 //
 // 16-bit activations come through the wave's own part of LDS (xl): a load
 // instruction takes 1 KiB of one token's row, where the operands' own layout
@@ -217,21 +225,32 @@ struct Tok {
 // Token t's 16-byte piece j lies at j ^ (t % 4), so that the 16 lanes of a read
 // phase (four tokens, four chunks) touch every bank once.  Tokens that are not
 // there stay what was in LDS: they are rows of results of their own.
-template <int KIND, bool XB, bool XM, int Q, int G, bool PAIR>
-__device__ __forceinline__ void few_pass(const FewArgs& a, const Unit& u,
-                                         const unsigned char* smem, const uint32_t (&mbase)[2][3],
-                                         const __amdgpu_buffer_rsrc_t (&rw)[2],
-                                         const __amdgpu_buffer_rsrc_t (&rm)[2][3],
-                                         const __amdgpu_buffer_rsrc_t (&rx)[2], const Tok<Q>& tok,
-                                         unsigned char* xl, int f0, int kw, float* red, bool first) {
-  const int lane = threadIdx.x & 63;
+template <int KIND, bool XB, bool XM, int Q, int MODE>
+__device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const unsigned char* smem,
+                                        const uint32_t (&mbase)[2][3],
+                                        const __amdgpu_buffer_rsrc_t (&rw)[2],
+                                        const __amdgpu_buffer_rsrc_t (&rx)[2], unsigned char* xl,
+                                        const int* xrow, const int* orow, int t0, float* red,
+                                        bool first) {
+  constexpr bool PAIR = is_pair(MODE);
+  constexpr int G = PAIR && Q == 1 ? 8 : 4;          // groups of four rows per pass
+  constexpr int F = PAIR ? 2 * G : 4 * G;            // features per pass
+  constexpr int kRed = 4 * G * 4 * Q;                // sums of a wave and pass
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = wave % a.KW, team = wave / a.KW;
   const uint32_t j = lane & 3, b = lane >> 2;
   const uint32_t C = (uint32_t)a.C, rowb = (uint32_t)(a.K / 2);
   const int S = (a.C + 15) / 16;
+  const int base = team * a.feats;                   // the team's first row
+  xl += wave * 4096 * Q;
+  Tok<Q> tok;
+  tok.n = u.T - t0 < 4 * Q ? u.T - t0 : 4 * Q;
+#pragma unroll
+  for (int t = 0; t < 4 * Q; ++t)
+    tok.off[t] = t < tok.n ? (uint32_t)__builtin_amdgcn_readfirstlane(xrow[t0 + t]) * (uint32_t)(XM ? a.K / 2 : a.K * 2) : 0u;
   auto layer = [](int g) { return PAIR && g >= G / 2 ? 1 : 0; };
-  auto lrow = [&](int g) { return (uint32_t)f0 + 4u * (PAIR ? g % (G / 2) : g) + j; };
+  auto lrow = [&](int f0, int g) { return (uint32_t)f0 + 4u * (PAIR ? g % (G / 2) : g) + j; };
 
-  const uint32_t wo = lrow(0) * rowb + 16u * b;
   struct Step {
     uint4 w[G];
   };
@@ -246,10 +265,8 @@ __device__ __forceinline__ void few_pass(const FewArgs& a, const Unit& u,
       xm[q] = 4 * q + (int)j < tok.n ? (j & 2 ? r23 : r01) : kOff;
     }
   }
-  auto load = [&](int s, Step& st) __attribute__((always_inline)) {
-    const uint32_t c = (uint32_t)s * 16u + b;
-    const bool ok = c < C;
-    const uint32_t at = ok ? wo + (uint32_t)s * 256u : kOff;
+  auto load = [&](int f0, int s, Step& st) __attribute__((always_inline)) {
+    const uint32_t at = (uint32_t)s * 16u + b < C ? lrow(f0, 0) * rowb + 16u * b + (uint32_t)s * 256u : kOff;
 #pragma unroll
     for (int g = 0; g < G; ++g)
       st.w[g] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
@@ -282,9 +299,8 @@ __device__ __forceinline__ void few_pass(const FewArgs& a, const Unit& u,
 #pragma unroll
     for (int q = 0; q < Q; ++q) acc[g][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // step s from st, whose registers then take step s + 2 KW; the activations of
-  // step s + KW into LDS once this step's are read
-  auto compute = [&](int s, Step& st) __attribute__((always_inline)) {
+  // Step s of the pass at f0 from st; `more`: another step follows, at sx.
+  auto compute = [&](int f0, int s, const Step& st, bool more, int sx) __attribute__((always_inline)) {
     const uint32_t c = (uint32_t)s * 16u + b, cc = c < C ? c : C - 1u;
     uint2 xo[Q][8];
     f32x4_t xs[Q];
@@ -304,12 +320,12 @@ __device__ __forceinline__ void few_pass(const FewArgs& a, const Unit& u,
           x_ops<KIND>(*reinterpret_cast<const uint4*>(xl + 4096u * q + (xr ^ (16u * v))), xo[q][2 * v], xo[q][2 * v + 1]);
       }
     }
-    if (s + a.KW < S) {
+    if (more) {   // its activations, now that this step's are read
       if constexpr (!XM) {
-        __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0): LDS is read
+        __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
         __builtin_amdgcn_sched_barrier(0);
       }
-      load_x(s + a.KW);
+      load_x(sx);
     }
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -322,20 +338,10 @@ __device__ __forceinline__ void few_pass(const FewArgs& a, const Unit& u,
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const uint32_t lr = lrow(g) < (uint32_t)u.brows ? lrow(g) : (uint32_t)u.brows - 1u;
-      Meta m;
-      if (a.meta_lds)
-        m = load_meta<KIND>(a, cc, [&](int i, uint32_t o, auto t) {
-          return (uint32_t)*reinterpret_cast<const decltype(t)*>(smem + mbase[layer(g)][i] +
-                                                                 lr * a.mrow[i] + o);
-        });
-      else
-        m = load_meta<KIND>(a, cc, [&](int i, uint32_t o, auto t) {
-          const uint32_t at = lr * a.mrow[i] + o;
-          if constexpr (sizeof(t) == 1) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rm[layer(g)][i], at, 0, 0);
-          else if constexpr (sizeof(t) == 2) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rm[layer(g)][i], at, 0, 0);
-          else return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm[layer(g)][i], at, 0, 0);
-        });
+      const uint32_t lr = lrow(f0, g) < (uint32_t)u.brows ? lrow(f0, g) : (uint32_t)u.brows - 1u;
+      const Meta m = load_meta<KIND>(a, cc, [&](int i, uint32_t o, auto t) {
+        return (uint32_t)*reinterpret_cast<const decltype(t)*>(smem + mbase[layer(g)][i] + lr * a.mrow[i] + o);
+      });
       float Sv, Tv;
       scale_of<KIND, XB>(m, Sv, Tv);
       f32x4_t d[Q];
@@ -360,81 +366,37 @@ __device__ __forceinline__ void few_pass(const FewArgs& a, const Unit& u,
           if constexpr (KIND != F_MX4) acc[g][q][i] = fmaf(Tv, xs[q][i], acc[g][q][i]);
         }
     }
-    if (s + 2 * a.KW < S) load(s + 2 * a.KW, st);
   };
-
-  // codes two steps ahead, activations one
-  Step s0, s1;
-  load_x(kw);
-  load(kw, s0);          // steps past the end read zeros
-  load(kw + a.KW, s1);
-  if (first) {
-    // the metadata copies were issued before these loads
-    constexpr int n = 2 * G;
-    static_assert(n < 64, "a wait counts to 63");
-    __builtin_amdgcn_s_waitcnt((n & 0xF) | (0x7 << 4) | (0xF << 8) | ((n >> 4) << 14));
-    __syncthreads();
-  }
-  for (int s = kw; s < S; s += 2 * a.KW) {
-    compute(s, s0);
-    if (s + a.KW < S) compute(s + a.KW, s1);
-  }
-
-  const int R = lane >> 4, p = ((R & 1) << 1) | (R >> 1);
+  // A pass's sums: over lanes, then over the team's waves.  Two buffers by
+  // turns, so that one barrier per pass is enough.
+  const int R = lane >> 4, p4 = ((R & 1) << 1) | (R >> 1);
+  auto finish = [&](int f0, int pass) __attribute__((always_inline)) {
+    float* rb = red + (pass & 1) * 4 * kRed;
+    float* mine = rb + wave * kRed;
 #pragma unroll
-  for (int q = 0; q < Q; ++q)
+    for (int q = 0; q < Q; ++q)
 #pragma unroll
-    for (int h = 0; h < G / 4; ++h) {
-      float v[16], o[4];
+      for (int h = 0; h < G / 4; ++h) {
+        float v[16], o[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[4 * k + i] = acc[4 * h + k][q][i];
-      sum16(v, o);
-      if ((lane & 12) == 0) {
+          for (int i = 0; i < 4; ++i) {
+            v[4 * k + i] = acc[4 * h + k][q][i];
+            acc[4 * h + k][q][i] = 0.f;
+          }
+        sum16(v, o);
+        if ((lane & 12) == 0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) red[(16 * h + 4 * k + (int)j) * (4 * Q) + 4 * q + p] = o[k];
+          for (int k = 0; k < 4; ++k) mine[(16 * h + 4 * k + (int)j) * (4 * Q) + 4 * q + p4] = o[k];
+        }
       }
-    }
-}
-
-__device__ __forceinline__ void few_store(void* y, int64_t i, float v, int dt) {
-  if (dt == F32) static_cast<float*>(y)[i] = v;
-  else if (dt == BF16) static_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_bf16_rne(v);
-  else static_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_f16_rne(v);
-}
-
-// All tokens t0 .. t0 + 4 Q - 1 of the unit.  xrow, orow: rows of x and of
-// the output, per token.
-template <int KIND, bool XB, bool XM, int Q, int MODE>
-__device__ __forceinline__ void few_tokens(const FewArgs& a, const Unit& u,
-                                           const unsigned char* smem, const uint32_t (&mbase)[2][3],
-                                           const __amdgpu_buffer_rsrc_t (&rw)[2],
-                                           const __amdgpu_buffer_rsrc_t (&rm)[2][3],
-                                           const __amdgpu_buffer_rsrc_t (&rx)[2], unsigned char* xl,
-                                           const int* xrow, const int* orow, int t0, float* red,
-                                           bool first) {
-  constexpr bool PAIR = is_pair(MODE);
-  constexpr int G = PAIR && Q == 1 ? 8 : 4;          // groups of four rows per pass
-  constexpr int F = PAIR ? 2 * G : 4 * G;            // features per pass
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kw = wave % a.KW, team = wave / a.KW;
-  Tok<Q> tok;
-  tok.n = u.T - t0 < 4 * Q ? u.T - t0 : 4 * Q;
-#pragma unroll
-  for (int t = 0; t < 4 * Q; ++t)
-    tok.off[t] = t < tok.n ? (uint32_t)__builtin_amdgcn_readfirstlane(xrow[t0 + t]) * (uint32_t)(XM ? a.K / 2 : a.K * 2) : 0u;
-  constexpr int kRed = 4 * G * 4 * Q;
-#pragma unroll 1
-  for (int f = 0; f < kFeat; f += F) {
-    const int f0 = team * kFeat + f;
-    few_pass<KIND, XB, XM, Q, G, PAIR>(a, u, smem, mbase, rw, rm, rx, tok, xl + wave * 4096 * Q, f0, kw, red + wave * kRed,
-                                   first && f == 0);
-    __syncthreads();
+    __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0); loads stay in flight
+    __builtin_amdgcn_s_barrier();
     // the team's threads: (feature, token) with the feature fastest
     for (int i = threadIdx.x - team * a.KW * 64; i < F * 4 * Q; i += a.KW * 64) {
       const int fe = i % F, t = i / F;
-      const float* r = red + team * a.KW * kRed;
+      const float* r = rb + team * a.KW * kRed;
       float g = 0.f, v = 0.f;
       for (int w = 0; w < a.KW; ++w) {
         g += r[w * kRed + fe * 4 * Q + t];
@@ -457,8 +419,49 @@ __device__ __forceinline__ void few_tokens(const FewArgs& a, const Unit& u,
           few_store(a.y, (int64_t)orow[t0 + t] * a.N + n, g, a.ydt);
       }
     }
+  };
+
+  // the wave's steps: n per pass; passes whose rows lie past the block's end
+  // are left out, for all teams alike (the first team has the most)
+  const int n = (S - kw + a.KW - 1) / a.KW;
+  const int passes = ((u.brows < a.feats ? u.brows : a.feats) + F - 1) / F, total = passes * n;
+  int lf = base, lk = 0;   // next load: row and step of its pass
+  auto next = [&](Step& st) __attribute__((always_inline)) {
+    load(lf, kw + lk * a.KW, st);   // past the last pass: rows past the resource, or not used
+    if (++lk == n) {
+      lk = 0;
+      lf += F;
+    }
+  };
+  Step s0, s1;
+  load_x(kw);
+  next(s0);
+  next(s1);
+  if (first) {
+    // the metadata copies were issued before these loads
+    constexpr int w = 2 * G;
+    static_assert(w < 64, "a wait counts to 63");
+    __builtin_amdgcn_s_waitcnt((w & 0xF) | (0x7 << 4) | (0xF << 8) | ((w >> 4) << 14));
     __syncthreads();
   }
+  int f0 = base, k = 0, pass = 0;
+  auto step = [&](int i, Step& st) __attribute__((always_inline)) {
+    const bool last = k + 1 == n;
+    compute(f0, kw + k * a.KW, st, i + 1 < total, kw + (last ? 0 : (k + 1) * a.KW));
+    if (i + 2 < total) next(st);
+    ++k;
+    if (last) {
+      finish(f0, pass);
+      k = 0;
+      f0 += F;
+      ++pass;
+    }
+  };
+  for (int i = 0; i < total; i += 2) {
+    step(i, s0);
+    if (i + 1 < total) step(i + 1, s1);
+  }
+  __syncthreads();   // the next tokens' sums take the same buffers
 }
 
 constexpr int kTok = 64;          // tokens of a call
@@ -523,7 +526,10 @@ k_few(FewArgs a) {
   constexpr bool EXPERTS = MODE == FM_UP || MODE == FM_DOWN;
   constexpr bool PAIR = is_pair(MODE);
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  __shared__ float red[4 * 16 * 4 * 4];
+  // activations, 4 Q KiB per wave: an array of its own, or the compiler takes
+  // their loads for writes to the metadata and waits for them before reading it
+  __shared__ __attribute__((aligned(16))) unsigned char xbuf[XM ? 16 : 4 * 4096 * Q];
+  __shared__ float red[2 * 4 * 16 * 4 * Q * (PAIR && Q == 1 ? 2 : 1)];
   __shared__ int xrow[kTok], orow[kTok];
   __shared__ int mask[EXPERTS ? 2 * kExperts : 1], ids[EXPERTS ? kTok * kSlots : 1];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -544,13 +550,14 @@ k_few(FewArgs a) {
       orow[tid] = tid;
     }
   }
-  u.brow0 = tile * a.RW * kFeat;
-  u.brows = (int)(a.N - u.brow0 < a.RW * kFeat ? a.N - u.brow0 : a.RW * kFeat);
+  const int rows = a.RW * a.feats;
+  u.brow0 = tile * rows;
+  u.brows = (int)(a.N - u.brow0 < rows ? a.N - u.brow0 : rows);
   u.row0 = (int64_t)expert * a.N + u.brow0;
 
   // resources of the block's rows; its metadata into LDS (1 KiB per wave and
   // instruction, whole 16-byte units; bytes past the slice read 0)
-  __amdgpu_buffer_rsrc_t rw[2], rm[2][3];
+  __amdgpu_buffer_rsrc_t rw[2];
   uint32_t mbase[2][3];
 #pragma unroll
   for (int l = 0; l < (PAIR ? 2 : 1); ++l) {
@@ -561,12 +568,12 @@ k_few(FewArgs a) {
     for (int i = 0; i < 3; ++i) {
       const uint64_t at = (uint64_t)u.row0 * a.mrow[i], lo = at & ~uint64_t(15);
       const uint32_t head = (uint32_t)(at - lo), bytes = head + (uint32_t)u.brows * a.mrow[i];
-      rm[l][i] = few_rsrc(static_cast<const unsigned char*>(arr[i]) + (a.meta_lds ? lo : at),
-                          a.mrow[i] ? (a.meta_lds ? (bytes + 15u) & ~15u : bytes - head) : 0u);
       mbase[l][i] = a.mlds[l][i] + head;
-      if (a.meta_lds && a.mrow[i])
+      if (a.mrow[i]) {
+        const __amdgpu_buffer_rsrc_t rm = few_rsrc(static_cast<const unsigned char*>(arr[i]) + lo, (bytes + 15u) & ~15u);
         for (uint32_t ch = (uint32_t)wave; ch * 1024u < bytes; ch += 4)
-          to_lds(rm[l][i], smem + a.mlds[l][i] + ch * 1024u, ch * 1024u + 16u * (uint32_t)lane);
+          to_lds(rm, smem + a.mlds[l][i] + ch * 1024u, ch * 1024u + 16u * (uint32_t)lane);
+      }
     }
   }
   if constexpr (!PAIR) rw[1] = rw[0];
@@ -579,13 +586,13 @@ k_few(FewArgs a) {
     FewArgs b = a;
     if (xbase) b.y = static_cast<unsigned char*>(a.y) + xbase * a.N * (a.ydt == F32 ? 4 : 2);
     __syncthreads();
-    few_tokens<KIND, XB, XM, Q, MODE>(b, u, smem, mbase, rw, rm, rx, smem + a.x_lds, xrow, orow, 0, red, true);
+    few_run<KIND, XB, XM, Q, MODE>(b, u, smem, mbase, rw, rx, xbuf, xrow, orow, 0, red, true);
   } else {
     for (int t0 = 0; t0 < u.T; t0 += 4 * Q) {
       if (Q == 1 || u.T - t0 <= 4)
-        few_tokens<KIND, XB, XM, 1, MODE>(a, u, smem, mbase, rw, rm, rx, smem + a.x_lds, xrow, orow, t0, red, t0 == 0);
+        few_run<KIND, XB, XM, 1, MODE>(a, u, smem, mbase, rw, rx, xbuf, xrow, orow, t0, red, t0 == 0);
       else
-        few_tokens<KIND, XB, XM, Q, MODE>(a, u, smem, mbase, rw, rm, rx, smem + a.x_lds, xrow, orow, t0, red, t0 == 0);
+        few_run<KIND, XB, XM, Q, MODE>(a, u, smem, mbase, rw, rx, xbuf, xrow, orow, t0, red, t0 == 0);
     }
   }
 }
@@ -814,9 +821,14 @@ int few_kind(const Desc& d) {
   return -1;
 }
 
-// Sizes, LDS layout and launch shape that the modes share; xq: quads of tokens
-// per pass whose activations go through LDS.
-size_t fill(const Desc& d, int64_t rows, bool pair, int xq, FewArgs& a) {
+#ifndef QP_FEW_BLOCKS
+#define QP_FEW_BLOCKS 512
+#endif
+constexpr int64_t kFewBlocks = QP_FEW_BLOCKS;
+
+// Sizes, LDS layout and launch shape that the modes share; units: experts or row
+// tiles of x.
+size_t fill(const Desc& d, int64_t rows, int64_t units, bool pair, FewArgs& a) {
   a.K = d.K;
   a.N = rows;
   a.C = (int)(d.K / 32);
@@ -827,22 +839,30 @@ size_t fill(const Desc& d, int64_t rows, bool pair, int xq, FewArgs& a) {
   const int S = (a.C + 15) / 16;
   a.KW = S >= 4 ? 4 : S >= 2 ? 2 : 1;
   a.RW = 4 / a.KW;
-  a.tiles = (int)((rows + a.RW * kFeat - 1) / (a.RW * kFeat));
   for (int i = 0; i < 3; ++i) a.mrow[i] = 0;
   if (kind == F_MX4) a.mrow[0] = (uint32_t)(d.K / 32);
   else if (kind == F_Q4K) { a.mrow[0] = a.mrow[1] = (uint32_t)(d.K / 32); a.mrow[2] = (uint32_t)(d.K / 256 * 4); }
   else if (kind == F_SYM4) a.mrow[0] = (uint32_t)(d.K / d.gs * 4);
   else a.mrow[0] = a.mrow[1] = (uint32_t)(d.K / d.gs * 2);
-  size_t lds = 0;
-  for (int l = 0; l < (pair ? 2 : 1); ++l)
-    for (int i = 0; i < 3; ++i) {
-      a.mlds[l][i] = (uint32_t)lds;
-      if (a.mrow[i]) lds += ((size_t)a.RW * kFeat * a.mrow[i] + 15 + 1023) / 1024 * 1024;
-    }
-  // longer rows read their metadata where it lies
-  a.meta_lds = lds <= 48 * 1024;
-  a.x_lds = a.meta_lds ? (uint32_t)lds : 0u;
-  return a.x_lds + (size_t)xq * 4 * 4096;
+  auto meta = [&](int feats) {
+    size_t lds = 0;
+    for (int l = 0; l < (pair ? 2 : 1); ++l)
+      for (int i = 0; i < 3; ++i) {
+        a.mlds[l][i] = (uint32_t)lds;
+        if (a.mrow[i]) lds += ((size_t)a.RW * feats * a.mrow[i] + 15 + 1023) / 1024 * 1024;
+      }
+    return lds;
+  };
+  // Rows per team: so many that the blocks of all experts (or row tiles of x)
+  // come to about two per CU, all resident at once, while their metadata fits
+  // 40 KiB and their codes 1 GiB.
+  const int64_t most = units * ((rows + a.RW * 16 - 1) / (a.RW * 16));
+  int64_t k = most / kFewBlocks;
+  if (k < 1) k = 1;
+  while (k > 1 && (meta((int)k * 16) > 40 * 1024 || k * 16 * a.RW * (d.K / 2) > (int64_t(1) << 30))) --k;
+  a.feats = (int)k * 16;
+  a.tiles = (int)((rows + a.RW * a.feats - 1) / (a.RW * a.feats));
+  return meta(a.feats);
 }
 
 using FewFn = void (*)(FewArgs);
@@ -879,7 +899,7 @@ FewFn mx_fn(bool xb, int64_t M) {
 hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bufs& b,
                       const void* bias, void* y, int ydt, hipStream_t s) {
   FewArgs a{};
-  const size_t lds = fill(d, d.N, false, quads(M), a);
+  const size_t lds = fill(d, d.N, (M + 4 * quads(M) - 1) / (4 * quads(M)), false, a);
   a.w[0] = a.w[1] = b;
   a.x = x;
   a.M = M;
@@ -896,7 +916,7 @@ hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bu
 hipError_t launch_few_mx(const Desc& d, const void* xq, const void* xs, int64_t M, const Bufs& b,
                          const float* bias, void* y, int ydt, hipStream_t s) {
   FewArgs a{};
-  const size_t lds = fill(d, d.N, false, 0, a);
+  const size_t lds = fill(d, d.N, (M + 4 * quads(M) - 1) / (4 * quads(M)), false, a);
   a.w[0] = a.w[1] = b;
   a.x = xq;
   a.xsc = xs;
@@ -913,7 +933,7 @@ hipError_t launch_few_mx(const Desc& d, const void* xq, const void* xs, int64_t 
 
 hipError_t launch_few_gated(const Desc& d, const GatedArgs& g, hipStream_t s) {
   FewArgs a{};
-  const size_t lds = fill(d, d.N, true, quads(g.M), a);
+  const size_t lds = fill(d, d.N, (g.M + 4 * quads(g.M) - 1) / (4 * quads(g.M)), true, a);
   a.w[0] = g.gate;
   a.w[1] = g.up;
   a.x = g.x;
@@ -930,6 +950,12 @@ hipError_t launch_few_gated(const Desc& d, const GatedArgs& g, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The metadata of 16 rows (of both layers of a pair) has to fit LDS next to the
+// activations and sums of 8 rows of x.
+bool few_fits(const Desc& d, bool pair) {
+  FewArgs a{};
+  return fill(d, 16, 1, pair, a) <= 112 * 1024;
+}
 bool moe_format(const Desc& d) { return few_kind(d) >= 0; }
 int moe_max_tokens() { return kTok; }
 int moe_max_experts() { return kExperts; }
@@ -968,7 +994,7 @@ hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStr
   // up to four tokens: the form that holds one quad, in fewer registers
   const int q = m.M <= 4 ? 1 : 2;
   FewArgs a{};
-  size_t lds = fill(up, inner, true, q, a);
+  size_t lds = fill(up, inner, most, true, a);
   a.w[0] = m.gate;
   a.w[1] = m.up;
   a.x = m.x;
@@ -980,7 +1006,7 @@ hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStr
   a.E = m.E;
   a.topk = m.topk;
   hipLaunchKernelGGL(expert_fn<FM_UP>(few_kind(up), xb, q), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
-  lds = fill(down, K, false, q, a);
+  lds = fill(down, K, most, false, a);
   a.w[0] = a.w[1] = m.down;
   a.x = h;
   a.y = part;
