@@ -1137,12 +1137,12 @@ qp_status check_moe(const qp_desc* d_up, const qp_desc* d_down, int64_t M, int32
                 "an expert of %lld x %lld (up) needs a down projection of %lld x %lld, got %lld x %lld",
                 (long long)(up->N / experts), (long long)up->K, (long long)up->K,
                 (long long)(up->N / experts), (long long)(down->N / experts), (long long)down->K);
-  if (!qp::few_fits(*up, true) || !qp::few_fits(*down, false))
-    return fail(QP_EUNSUPPORTED, "qmoe: rows of K=%lld or inner=%lld are too long (the metadata of 16 rows must "
-                "fit LDS)", (long long)up->K, (long long)down->K);
   if (M * topk * (up->K > down->K ? up->K : down->K) >= int64_t(1) << 29)
     return fail(QP_EUNSUPPORTED, "M * topk * max(K, inner) must be < 2^29 (M=%lld, topk=%d, K=%lld, inner=%lld)",
                 (long long)M, topk, (long long)up->K, (long long)down->K);
+  if (!qp::few_fits(*up, true) || !qp::few_fits(*down, false))
+    return fail(QP_EUNSUPPORTED, "qmoe: rows of K=%lld or inner=%lld are too long (the metadata of 32 rows must "
+                "fit LDS)", (long long)up->K, (long long)down->K);
   return QP_OK;
 }
 

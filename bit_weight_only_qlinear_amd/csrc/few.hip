@@ -48,10 +48,11 @@ struct FewArgs {
   int C;                   // 32-column chunks per row
   int gsh;                 // chunk -> group: >> gsh
   int KW, RW;              // waves per row, row teams (KW * RW == 4)
-  int feats;               // rows (features of a pair) per team, a multiple of 16
+  int feats;               // rows (features of a pair) per team, whole passes
   int tiles;               // blocks per expert (or layer)
   uint32_t mrow[3];        // metadata bytes per row: scales, zeros, steps
   uint32_t mlds[2][3];     // LDS offset of each slice
+  uint32_t x_lds;          // and of the tokens' whole rows
   const void* x;           // [rows, K] of 16 bits, or MXFP4 codes
   const void* xsc;         //   and their scales
   int64_t M;
@@ -102,14 +103,13 @@ __device__ __forceinline__ uint32_t e2m1_pair(uint32_t w, float scale = 1.f) {
 // The 8 codes of one word as two operands of four; MXFP4 in their order,
 // nibbles as (0, 4, 1, 5) and (2, 6, 3, 7).
 template <int KIND, bool XB>
-__device__ __forceinline__ void code_ops(uint32_t w, uint2& lo, uint2& hi) {
+__device__ __forceinline__ void code_ops(uint32_t w, uint32_t mask, uint32_t mag, uint2& lo, uint2& hi) {
   if constexpr (KIND == F_MX4) {
     lo = make_uint2(e2m1_pair<XB, 0>(w), e2m1_pair<XB, 1>(w));
     hi = make_uint2(e2m1_pair<XB, 2>(w), e2m1_pair<XB, 3>(w));
   } else {
-    const uint32_t mag = XB ? 0x43004300u : 0x64006400u;   // 128, 1024
-    lo = make_uint2((w & 0x000F000Fu) | mag, ((w >> 4) & 0x000F000Fu) | mag);
-    hi = make_uint2(((w >> 8) & 0x000F000Fu) | mag, ((w >> 12) & 0x000F000Fu) | mag);
+    lo = make_uint2((w & mask) | mag, ((w >> 4) & mask) | mag);
+    hi = make_uint2(((w >> 8) & mask) | mag, ((w >> 12) & mask) | mag);
   }
 }
 
@@ -224,8 +224,10 @@ __device__ __forceinline__ void few_store(void* y, int64_t i, float v, int dt) {
 // would touch 64 pieces of 64 bytes (16 tokens: 2.4 TB/s of codes at most).
 // Token t's 16-byte piece j lies at j ^ (t % 4), so that the 16 lanes of a read
 // phase (four tokens, four chunks) touch every bank once.  Tokens that are not
-// there stay what was in LDS: they are rows of results of their own.
-template <int KIND, bool XB, bool XM, int Q, int MODE>
+// there read what else is in LDS: they are rows of results of their own.
+// WHOLE: the tokens' whole rows are loaded once per block, step by step, and
+// serve all of its waves and passes.
+template <int KIND, bool XB, bool XM, bool WHOLE, int Q, int MODE>
 __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const unsigned char* smem,
                                         const uint32_t (&mbase)[2][3],
                                         const __amdgpu_buffer_rsrc_t (&rw)[2],
@@ -233,7 +235,7 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
                                         const int* xrow, const int* orow, int t0, float* red,
                                         bool first) {
   constexpr bool PAIR = is_pair(MODE);
-  constexpr int G = PAIR && Q == 1 ? 8 : 4;          // groups of four rows per pass
+  constexpr int G = Q == 1 ? 8 : 4;                  // groups of four rows per pass
   constexpr int F = PAIR ? 2 * G : 4 * G;            // features per pass
   constexpr int kRed = 4 * G * 4 * Q;                // sums of a wave and pass
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -242,11 +244,11 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
   const uint32_t C = (uint32_t)a.C, rowb = (uint32_t)(a.K / 2);
   const int S = (a.C + 15) / 16;
   const int base = team * a.feats;                   // the team's first row
-  xl += wave * 4096 * Q;
+  if constexpr (!WHOLE) xl += wave * 4096 * Q;
   Tok<Q> tok;
   tok.n = u.T - t0 < 4 * Q ? u.T - t0 : 4 * Q;
 #pragma unroll
-  for (int t = 0; t < 4 * Q; ++t)
+  for (int t = 0; t < (WHOLE ? 0 : 4 * Q); ++t)
     tok.off[t] = t < tok.n ? (uint32_t)__builtin_amdgcn_readfirstlane(xrow[t0 + t]) * (uint32_t)(XM ? a.K / 2 : a.K * 2) : 0u;
   auto layer = [](int g) { return PAIR && g >= G / 2 ? 1 : 0; };
   auto lrow = [&](int f0, int g) { return (uint32_t)f0 + 4u * (PAIR ? g % (G / 2) : g) + j; };
@@ -265,15 +267,20 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
       xm[q] = 4 * q + (int)j < tok.n ? (j & 2 ? r23 : r01) : kOff;
     }
   }
-  auto load = [&](int f0, int s, Step& st) __attribute__((always_inline)) {
-    const uint32_t at = (uint32_t)s * 16u + b < C ? lrow(f0, 0) * rowb + 16u * b + (uint32_t)s * 256u : kOff;
+  auto load = [&](int f0, int s, bool on, Step& st) __attribute__((always_inline)) {
+    const uint32_t at = on && (uint32_t)s * 16u + b < C ? lrow(f0, 0) * rowb + 16u * b + (uint32_t)s * 256u : kOff;
+    // in this order, or the wait for one step's first codes is one for all
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+    for (int g = 0; g < G; ++g) {
       st.w[g] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
                                               rw[layer(g)], at + 4u * (PAIR ? g % (G / 2) : g) * rowb, 0, 2));
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   auto load_x = [&](int s) __attribute__((always_inline)) {
-    if constexpr (XM) {
+    if constexpr (WHOLE) {
+    } else if constexpr (XM) {
       const uint32_t c = (uint32_t)s * 16u + b;
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
@@ -291,6 +298,13 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
                  ok ? tok.off[t] + (uint32_t)s * 1024u + 16u * ((uint32_t)lane ^ (t & 3u)) : kOff);
     }
   };
+  // nibbles: 128 (bf16) or 1024 (fp16) and the code in its low bits, one
+  // v_and_or_b32 from registers (two literals would make it two instructions)
+  uint32_t mask = 0x000F000Fu, mag = XB ? 0x43004300u : 0x64006400u;
+  asm("" : "+v"(mask), "+s"(mag));
+  uint32_t jm[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) jm[i] = j * a.mrow[i];
   const uint32_t xr = j * 1024u + 64u * b + 16u * j;   // piece 0 of the lane's token and chunk
 
   f32x4_t acc[G][Q];
@@ -302,6 +316,13 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
   // Step s of the pass at f0 from st; `more`: another step follows, at sx.
   auto compute = [&](int f0, int s, const Step& st, bool more, int sx) __attribute__((always_inline)) {
     const uint32_t c = (uint32_t)s * 16u + b, cc = c < C ? c : C - 1u;
+    if constexpr (!WHOLE && !XM) {
+      // the compiler does not see these copies: what was issued after them are
+      // the next step's G loads (and stores)
+      __builtin_amdgcn_s_waitcnt((G & 0xF) | (0x7 << 4) | (0xF << 8));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const unsigned char* xs0 = WHOLE ? xl + (uint32_t)(s * tok.n) * 1024u : xl;
     uint2 xo[Q][8];
     f32x4_t xs[Q];
 #pragma unroll
@@ -317,10 +338,10 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
       } else {
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          x_ops<KIND>(*reinterpret_cast<const uint4*>(xl + 4096u * q + (xr ^ (16u * v))), xo[q][2 * v], xo[q][2 * v + 1]);
+          x_ops<KIND>(*reinterpret_cast<const uint4*>(xs0 + 4096u * q + (xr ^ (16u * v))), xo[q][2 * v], xo[q][2 * v + 1]);
       }
     }
-    if (more) {   // its activations, now that this step's are read
+    if (!WHOLE && more) {   // its activations, now that this step's are read
       if constexpr (!XM) {
         __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
         __builtin_amdgcn_sched_barrier(0);
@@ -338,9 +359,11 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const uint32_t lr = lrow(f0, g) < (uint32_t)u.brows ? lrow(f0, g) : (uint32_t)u.brows - 1u;
+      // LDS has room for whole passes; rows past the block's last are sums of
+      // their own that nothing stores
       const Meta m = load_meta<KIND>(a, cc, [&](int i, uint32_t o, auto t) {
-        return (uint32_t)*reinterpret_cast<const decltype(t)*>(smem + mbase[layer(g)][i] + lr * a.mrow[i] + o);
+        const uint32_t row = mbase[layer(g)][i] + ((uint32_t)f0 + 4u * (PAIR ? g % (G / 2) : g)) * a.mrow[i];
+        return (uint32_t)*reinterpret_cast<const decltype(t)*>(smem + row + (jm[i] + o));
       });
       float Sv, Tv;
       scale_of<KIND, XB>(m, Sv, Tv);
@@ -351,7 +374,7 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         uint2 lo, hi;
-        code_ops<KIND, XB>(wv[v], lo, hi);
+        code_ops<KIND, XB>(wv[v], mask, mag, lo, hi);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
           d[q] = mfma4<XB>(xo[q][2 * v], lo, d[q]);
@@ -369,15 +392,35 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
   };
   // A pass's sums: over lanes, then over the team's waves.  Two buffers by
   // turns, so that one barrier per pass is enough.
+  // A pass's sums over lanes; waves that share rows meet in LDS, in two buffers
+  // by turns, so that one barrier per pass is enough.
   const int R = lane >> 4, p4 = ((R & 1) << 1) | (R >> 1);
+  auto put = [&](int row, int t, float g, float v) __attribute__((always_inline)) {
+    if (row >= u.brows || t0 + t >= u.T) return;
+    const int64_t n = u.brow0 + row;
+    if constexpr (MODE == FM_LINEAR || MODE == FM_GATED) {
+      auto bias = [&](const void* p) {
+        if (a.bdt == F32) return static_cast<const float*>(p)[n];
+        return meta_to_f32(static_cast<const uint16_t*>(p)[n], a.bdt == BF16);
+      };
+      if (a.bias[0]) g += bias(a.bias[0]);
+      if (PAIR && a.bias[1]) v += bias(a.bias[1]);
+    }
+    if constexpr (PAIR) g = (a.act == ACT_SILU ? act_f<ACT_SILU>(g) : act_f<ACT_GELU_TANH>(g)) * v;
+    if constexpr (MODE == FM_DOWN)
+      static_cast<float*>(a.y)[(int64_t)orow[t0 + t] * a.N + n] = g;
+    else
+      few_store(a.y, (int64_t)orow[t0 + t] * a.N + n, g, a.ydt);
+  };
   auto finish = [&](int f0, int pass) __attribute__((always_inline)) {
     float* rb = red + (pass & 1) * 4 * kRed;
     float* mine = rb + wave * kRed;
 #pragma unroll
-    for (int q = 0; q < Q; ++q)
+    for (int q = 0; q < Q; ++q) {
+      float o[G / 4][4];   // rows 16 h + 4 k + l % 4 of the pass, token 4 q + p4
 #pragma unroll
       for (int h = 0; h < G / 4; ++h) {
-        float v[16], o[4];
+        float v[16];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -385,39 +428,32 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
             v[4 * k + i] = acc[4 * h + k][q][i];
             acc[4 * h + k][q][i] = 0.f;
           }
-        sum16(v, o);
-        if ((lane & 12) == 0) {
+        sum16(v, o[h]);
+      }
+      if ((lane & 12) == 0) {
+        if (a.KW == 1) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mine[(16 * h + 4 * k + (int)j) * (4 * Q) + 4 * q + p4] = o[k];
+          for (int k = 0; k < (PAIR ? G / 2 : G); ++k)
+            put(f0 + 4 * k + (int)j, 4 * q + p4, o[k / 4][k % 4], PAIR ? o[(k + G / 2) / 4][(k + G / 2) % 4] : 0.f);
+        } else {
+#pragma unroll
+          for (int k = 0; k < G; ++k) mine[(4 * k + (int)j) * (4 * Q) + 4 * q + p4] = o[k / 4][k % 4];
         }
       }
+    }
+    if (a.KW == 1) return;
     __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0); loads stay in flight
     __builtin_amdgcn_s_barrier();
     // the team's threads: (feature, token) with the feature fastest
     for (int i = threadIdx.x - team * a.KW * 64; i < F * 4 * Q; i += a.KW * 64) {
       const int fe = i % F, t = i / F;
-      const float* r = rb + team * a.KW * kRed;
+      const float* r = rb + team * a.KW * kRed + t;
       float g = 0.f, v = 0.f;
       for (int w = 0; w < a.KW; ++w) {
-        g += r[w * kRed + fe * 4 * Q + t];
-        if constexpr (PAIR) v += r[w * kRed + (F + fe) * 4 * Q + t];
+        g += r[w * kRed + fe * 4 * Q];
+        if constexpr (PAIR) v += r[w * kRed + (F + fe) * 4 * Q];
       }
-      if (f0 + fe < u.brows && t0 + t < u.T) {
-        const int64_t n = u.brow0 + f0 + fe;
-        if constexpr (MODE == FM_LINEAR || MODE == FM_GATED) {
-          auto bias = [&](const void* p) {
-            if (a.bdt == F32) return static_cast<const float*>(p)[n];
-            return meta_to_f32(static_cast<const uint16_t*>(p)[n], a.bdt == BF16);
-          };
-          if (a.bias[0]) g += bias(a.bias[0]);
-          if (PAIR && a.bias[1]) v += bias(a.bias[1]);
-        }
-        if constexpr (PAIR) g = (a.act == ACT_SILU ? act_f<ACT_SILU>(g) : act_f<ACT_GELU_TANH>(g)) * v;
-        if constexpr (MODE == FM_DOWN)
-          static_cast<float*>(a.y)[(int64_t)orow[t0 + t] * a.N + n] = g;
-        else
-          few_store(a.y, (int64_t)orow[t0 + t] * a.N + n, g, a.ydt);
-      }
+      put(f0 + fe, t, g, v);
     }
   };
 
@@ -425,20 +461,34 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
   // are left out, for all teams alike (the first team has the most)
   const int n = (S - kw + a.KW - 1) / a.KW;
   const int passes = ((u.brows < a.feats ? u.brows : a.feats) + F - 1) / F, total = passes * n;
+  const int end = base + passes * F;
   int lf = base, lk = 0;   // next load: row and step of its pass
   auto next = [&](Step& st) __attribute__((always_inline)) {
-    load(lf, kw + lk * a.KW, st);   // past the last pass: rows past the resource, or not used
+    // Past the last pass it reads nothing, but it is issued: after loads that
+    // may not have been, the wait for one step's codes is a wait for all.
+    load(lf, kw + lk * a.KW, lf < end, st);
     if (++lk == n) {
       lk = 0;
       lf += F;
     }
   };
   Step s0, s1;
+  if constexpr (WHOLE) {
+    // 1 KiB of one token and step per load, dealt out to the waves
+    if (!first) __syncthreads();   // the tokens before are done with it
+    for (int i = wave; i < S * tok.n; i += 4) {
+      const int s = i / tok.n, t = i - s * tok.n;
+      to_lds(rx[0], xl + 1024 * i,
+             (uint32_t)s * 16u + b < C ? (uint32_t)__builtin_amdgcn_readfirstlane(xrow[t0 + t]) * (uint32_t)(a.K * 2) +
+                                             (uint32_t)s * 1024u + 16u * ((uint32_t)lane ^ ((uint32_t)t & 3u))
+                                       : kOff);
+    }
+  }
   load_x(kw);
   next(s0);
   next(s1);
-  if (first) {
-    // the metadata copies were issued before these loads
+  if (first || WHOLE) {
+    // the metadata's and the rows' copies were issued before these loads
     constexpr int w = 2 * G;
     static_assert(w < 64, "a wait counts to 63");
     __builtin_amdgcn_s_waitcnt((w & 0xF) | (0x7 << 4) | (0xF << 8) | ((w >> 4) << 14));
@@ -448,18 +498,21 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
   auto step = [&](int i, Step& st) __attribute__((always_inline)) {
     const bool last = k + 1 == n;
     compute(f0, kw + k * a.KW, st, i + 1 < total, kw + (last ? 0 : (k + 1) * a.KW));
-    if (i + 2 < total) next(st);
+    next(st);
     ++k;
     if (last) {
-      finish(f0, pass);
+      if (i < total) finish(f0, pass);
       k = 0;
-      f0 += F;
+      f0 += i + 1 < total ? F : 0;
       ++pass;
     }
   };
+  // Two by two; an odd last step is followed by one that adds to sums nobody
+  // reads.  (Left out by a branch, the compiler's wait for s0's codes is also
+  // one for s1's.)
   for (int i = 0; i < total; i += 2) {
     step(i, s0);
-    if (i + 1 < total) step(i + 1, s1);
+    step(i + 1, s1);
   }
   __syncthreads();   // the next tokens' sums take the same buffers
 }
@@ -468,7 +521,7 @@ constexpr int kTok = 64;          // tokens of a call
 constexpr int kExperts = 512;
 constexpr int kSlots = 16;        // experts per token
 
-// The a-th expert that some token chose, its tokens (rising) and each one's
+// The want-th expert that some token chose, its tokens (rising) and each one's
 // first slot with it; -1 where fewer are chosen.  Every wave ends up with the
 // answer; xrow and orow are complete after the last barrier.
 template <int MODE>
@@ -491,18 +544,31 @@ __device__ __forceinline__ int find_unit(const FewArgs& a, int want, int* mask, 
     }
   }
   __syncthreads();
+  // by falling number of tokens, so that the longest blocks start first
+  int cnt[kExperts / 64], most = 0;
+#pragma unroll
+  for (int i = 0; i < kExperts / 64; ++i) {
+    const int e = 64 * i + lane;
+    cnt[i] = 64 * i < a.E && e < a.E ? __popc((unsigned)mask[2 * e]) + __popc((unsigned)mask[2 * e + 1]) : 0;
+    most = cnt[i] > most ? cnt[i] : most;
+  }
+  for (int off = 32; off > 0; off >>= 1) {
+    const int o = __shfl_xor(most, off, 64);
+    most = o > most ? o : most;
+  }
   int found = -1;
-  for (int e0 = 0, seen = 0; e0 < a.E; e0 += 64) {
-    const int e = e0 + lane;
-    const bool on = e < a.E && (mask[2 * e] | mask[2 * e + 1]) != 0;
-    uint64_t bits = __ballot(on);
-    const int cnt = __popcll(bits);
-    if (want < seen + cnt) {
-      for (int k = seen; k < want; ++k) bits &= bits - 1;
-      found = e0 + __ffsll((unsigned long long)bits) - 1;
-      break;
+  for (int t = most, left = want; t > 0 && found < 0; --t) {
+#pragma unroll
+    for (int i = 0; i < kExperts / 64; ++i) {
+      if (found >= 0 || 64 * i >= a.E) continue;
+      uint64_t bits = __ballot(cnt[i] == t);
+      const int n = __popcll(bits);
+      if (left < n) {
+        for (int k = 0; k < left; ++k) bits &= bits - 1;
+        found = 64 * i + __ffsll((unsigned long long)bits) - 1;
+      }
+      left -= n;
     }
-    seen += cnt;
   }
   found = __builtin_amdgcn_readfirstlane(found);
   if (found < 0) return -1;
@@ -520,16 +586,18 @@ __device__ __forceinline__ int find_unit(const FewArgs& a, int want, int* mask, 
   return found;
 }
 
-template <int KIND, bool XB, bool XM, int Q, int MODE>
+template <int KIND, bool XB, bool XM, bool WHOLE, int Q, int MODE>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 k_few(FewArgs a) {
   constexpr bool EXPERTS = MODE == FM_UP || MODE == FM_DOWN;
   constexpr bool PAIR = is_pair(MODE);
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  // activations, 4 Q KiB per wave: an array of its own, or the compiler takes
-  // their loads for writes to the metadata and waits for them before reading it
-  __shared__ __attribute__((aligned(16))) unsigned char xbuf[XM ? 16 : 4 * 4096 * Q];
-  __shared__ float red[2 * 4 * 16 * 4 * Q * (PAIR && Q == 1 ? 2 : 1)];
+  // activations by steps, 4 Q KiB per wave: an array of its own, or the compiler
+  // takes their loads for writes to the metadata and waits for them before
+  // reading it
+  __shared__ __attribute__((aligned(16))) unsigned char xstep[XM || WHOLE ? 16 : 4 * 4096 * Q];
+  unsigned char* xbuf = WHOLE ? smem + a.x_lds : xstep;
+  __shared__ float red[2 * 4 * 16 * 4 * (Q == 1 ? 2 : Q)];   // Q == 2 runs single quads too
   __shared__ int xrow[kTok], orow[kTok];
   __shared__ int mask[EXPERTS ? 2 * kExperts : 1], ids[EXPERTS ? kTok * kSlots : 1];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -586,13 +654,13 @@ k_few(FewArgs a) {
     FewArgs b = a;
     if (xbase) b.y = static_cast<unsigned char*>(a.y) + xbase * a.N * (a.ydt == F32 ? 4 : 2);
     __syncthreads();
-    few_run<KIND, XB, XM, Q, MODE>(b, u, smem, mbase, rw, rx, xbuf, xrow, orow, 0, red, true);
+    few_run<KIND, XB, XM, WHOLE, Q, MODE>(b, u, smem, mbase, rw, rx, xbuf, xrow, orow, 0, red, true);
   } else {
     for (int t0 = 0; t0 < u.T; t0 += 4 * Q) {
       if (Q == 1 || u.T - t0 <= 4)
-        few_run<KIND, XB, XM, 1, MODE>(a, u, smem, mbase, rw, rx, xbuf, xrow, orow, t0, red, t0 == 0);
+        few_run<KIND, XB, XM, WHOLE, 1, MODE>(a, u, smem, mbase, rw, rx, xbuf, xrow, orow, t0, red, t0 == 0);
       else
-        few_run<KIND, XB, XM, Q, MODE>(a, u, smem, mbase, rw, rx, xbuf, xrow, orow, t0, red, t0 == 0);
+        few_run<KIND, XB, XM, WHOLE, Q, MODE>(a, u, smem, mbase, rw, rx, xbuf, xrow, orow, t0, red, t0 == 0);
     }
   }
 }
@@ -822,13 +890,18 @@ int few_kind(const Desc& d) {
 }
 
 #ifndef QP_FEW_BLOCKS
-#define QP_FEW_BLOCKS 512
+#define QP_FEW_BLOCKS 1024
 #endif
+#ifndef QP_FEW_WAVES
+#define QP_FEW_WAVES 2048
+#endif
+constexpr int64_t kFewWaves = QP_FEW_WAVES;
 constexpr int64_t kFewBlocks = QP_FEW_BLOCKS;
 
 // Sizes, LDS layout and launch shape that the modes share; units: experts or row
-// tiles of x.
-size_t fill(const Desc& d, int64_t rows, int64_t units, bool pair, FewArgs& a) {
+// tiles of x; q: quads of tokens that the kernel is made for; tokens: the most a pass can have, or 0 where their rows do not go
+// through LDS.  a.x_lds: where the tokens' whole rows lie, or 0.
+size_t fill(const Desc& d, int64_t rows, int64_t units, bool pair, int q, int tokens, FewArgs& a) {
   a.K = d.K;
   a.N = rows;
   a.C = (int)(d.K / 32);
@@ -837,14 +910,18 @@ size_t fill(const Desc& d, int64_t rows, int64_t units, bool pair, FewArgs& a) {
   if (d.gs == d.K && kind == F_SYM4) a.gsh = 31;
   else while ((32 << a.gsh) < d.gs) ++a.gsh;
   const int S = (a.C + 15) / 16;
-  a.KW = S >= 4 ? 4 : S >= 2 ? 2 : 1;
-  a.RW = 4 / a.KW;
+  const int F = q == 4 || pair ? 16 : 32;   // rows of the longest pass
+  // Waves per row: as few as fill the chip (two per SIMD), since waves that
+  // share rows have to add their sums up.
+  a.KW = 1;
+  while (a.KW < 4 && 2 * a.KW <= S && units * ((rows + F - 1) / F) * a.KW < kFewWaves) a.KW *= 2;
   for (int i = 0; i < 3; ++i) a.mrow[i] = 0;
   if (kind == F_MX4) a.mrow[0] = (uint32_t)(d.K / 32);
   else if (kind == F_Q4K) { a.mrow[0] = a.mrow[1] = (uint32_t)(d.K / 32); a.mrow[2] = (uint32_t)(d.K / 256 * 4); }
   else if (kind == F_SYM4) a.mrow[0] = (uint32_t)(d.K / d.gs * 4);
   else a.mrow[0] = a.mrow[1] = (uint32_t)(d.K / d.gs * 2);
   auto meta = [&](int feats) {
+    a.RW = 4 / a.KW;
     size_t lds = 0;
     for (int l = 0; l < (pair ? 2 : 1); ++l)
       for (int i = 0; i < 3; ++i) {
@@ -853,45 +930,51 @@ size_t fill(const Desc& d, int64_t rows, int64_t units, bool pair, FewArgs& a) {
       }
     return lds;
   };
+  while (a.KW < 4 && 2 * a.KW <= S && meta(F) > 32 * 1024) a.KW *= 2;
+  a.RW = 4 / a.KW;
   // Rows per team: so many that the blocks of all experts (or row tiles of x)
-  // come to about two per CU, all resident at once, while their metadata fits
-  // 40 KiB and their codes 1 GiB.
-  const int64_t most = units * ((rows + a.RW * 16 - 1) / (a.RW * 16));
+  // come to a few per CU, while their metadata fits 12 KiB and their codes 1 GiB.
+  const int64_t most = units * ((rows + a.RW * F - 1) / (a.RW * F));
   int64_t k = most / kFewBlocks;
   if (k < 1) k = 1;
-  while (k > 1 && (meta((int)k * 16) > 40 * 1024 || k * 16 * a.RW * (d.K / 2) > (int64_t(1) << 30))) --k;
-  a.feats = (int)k * 16;
+  while (k > 1 && (meta((int)k * F) > 12 * 1024 || k * F * a.RW * (d.K / 2) > (int64_t(1) << 30))) --k;
+  a.feats = (int)k * F;
   a.tiles = (int)((rows + a.RW * a.feats - 1) / (a.RW * a.feats));
-  return meta(a.feats);
+  const size_t lds = meta(a.feats), x = (size_t)S * (size_t)tokens * 1024u;
+  a.x_lds = 0;
+  // three KiB more: tokens that are not there are read past the last row
+  if (x > 0 && x + lds <= 72 * 1024) a.x_lds = (uint32_t)lds;   // two blocks per CU
+  return a.x_lds ? lds + x + 3 * 1024u : lds;
 }
 
 using FewFn = void (*)(FewArgs);
-template <int KIND, int MODE>
+template <int KIND, bool W, int MODE>
 FewFn expert_fn(bool xb, int q) {
-  if (q == 1) return xb ? k_few<KIND, true, false, 1, MODE> : k_few<KIND, false, false, 1, MODE>;
-  return xb ? k_few<KIND, true, false, 2, MODE> : k_few<KIND, false, false, 2, MODE>;
+  if (q == 1) return xb ? k_few<KIND, true, false, W, 1, MODE> : k_few<KIND, false, false, W, 1, MODE>;
+  return xb ? k_few<KIND, true, false, W, 2, MODE> : k_few<KIND, false, false, W, 2, MODE>;
 }
 template <int MODE>
-FewFn expert_fn(int kind, bool xb, int q) {
+FewFn expert_fn(int kind, bool xb, bool whole, int q) {
   switch (kind) {
-    case F_MX4: return expert_fn<F_MX4, MODE>(xb, q);
-    case F_AFF4: return expert_fn<F_AFF4, MODE>(xb, q);
-    case F_AFF4H: return expert_fn<F_AFF4H, MODE>(xb, q);
-    case F_Q4K: return expert_fn<F_Q4K, MODE>(xb, q);
-    default: return expert_fn<F_SYM4, MODE>(xb, q);
+    case F_MX4: return whole ? expert_fn<F_MX4, true, MODE>(xb, q) : expert_fn<F_MX4, false, MODE>(xb, q);
+    case F_AFF4: return whole ? expert_fn<F_AFF4, true, MODE>(xb, q) : expert_fn<F_AFF4, false, MODE>(xb, q);
+    case F_AFF4H: return whole ? expert_fn<F_AFF4H, true, MODE>(xb, q) : expert_fn<F_AFF4H, false, MODE>(xb, q);
+    case F_Q4K: return whole ? expert_fn<F_Q4K, true, MODE>(xb, q) : expert_fn<F_Q4K, false, MODE>(xb, q);
+    default: return whole ? expert_fn<F_SYM4, true, MODE>(xb, q) : expert_fn<F_SYM4, false, MODE>(xb, q);
   }
 }
 // Quads of tokens per pass.
 int quads(int64_t M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
 
-template <int MODE, bool XB, bool XM>
+template <int MODE, bool XB, bool XM, bool W>
 FewFn mx_fn(int64_t M) {
   const int q = quads(M);
-  return q == 1 ? k_few<F_MX4, XB, XM, 1, MODE> : q == 2 ? k_few<F_MX4, XB, XM, 2, MODE> : k_few<F_MX4, XB, XM, 4, MODE>;
+  return q == 1 ? k_few<F_MX4, XB, XM, W, 1, MODE> : q == 2 ? k_few<F_MX4, XB, XM, W, 2, MODE> : k_few<F_MX4, XB, XM, W, 4, MODE>;
 }
 template <int MODE>
-FewFn mx_fn(bool xb, int64_t M) {
-  return xb ? mx_fn<MODE, true, false>(M) : mx_fn<MODE, false, false>(M);
+FewFn mx_fn(bool xb, bool whole, int64_t M) {
+  if (whole) return xb ? mx_fn<MODE, true, false, true>(M) : mx_fn<MODE, false, false, true>(M);
+  return xb ? mx_fn<MODE, true, false, false>(M) : mx_fn<MODE, false, false, false>(M);
 }
 
 }  // namespace
@@ -899,7 +982,7 @@ FewFn mx_fn(bool xb, int64_t M) {
 hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bufs& b,
                       const void* bias, void* y, int ydt, hipStream_t s) {
   FewArgs a{};
-  const size_t lds = fill(d, d.N, (M + 4 * quads(M) - 1) / (4 * quads(M)), false, a);
+  const size_t lds = fill(d, d.N, (M + 4 * quads(M) - 1) / (4 * quads(M)), false, quads(M), (int)(M < 16 ? M : 16), a);
   a.w[0] = a.w[1] = b;
   a.x = x;
   a.M = M;
@@ -908,7 +991,7 @@ hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bu
   a.bias[0] = bias;
   a.bdt = xdt;
   const int64_t per = 4 * quads(M);
-  hipLaunchKernelGGL(mx_fn<FM_LINEAR>(xdt == BF16, M), dim3((unsigned)(a.tiles * ((M + per - 1) / per))),
+  hipLaunchKernelGGL(mx_fn<FM_LINEAR>(xdt == BF16, a.x_lds > 0, M), dim3((unsigned)(a.tiles * ((M + per - 1) / per))),
                      dim3(256), lds, s, a);
   return hipGetLastError();
 }
@@ -916,7 +999,7 @@ hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bu
 hipError_t launch_few_mx(const Desc& d, const void* xq, const void* xs, int64_t M, const Bufs& b,
                          const float* bias, void* y, int ydt, hipStream_t s) {
   FewArgs a{};
-  const size_t lds = fill(d, d.N, (M + 4 * quads(M) - 1) / (4 * quads(M)), false, a);
+  const size_t lds = fill(d, d.N, (M + 4 * quads(M) - 1) / (4 * quads(M)), false, quads(M), 0, a);
   a.w[0] = a.w[1] = b;
   a.x = xq;
   a.xsc = xs;
@@ -926,14 +1009,14 @@ hipError_t launch_few_mx(const Desc& d, const void* xq, const void* xs, int64_t 
   a.bias[0] = bias;
   a.bdt = F32;
   const int64_t per = 4 * quads(M);
-  hipLaunchKernelGGL((mx_fn<FM_LINEAR, true, true>(M)), dim3((unsigned)(a.tiles * ((M + per - 1) / per))),
+  hipLaunchKernelGGL((mx_fn<FM_LINEAR, true, true, false>(M)), dim3((unsigned)(a.tiles * ((M + per - 1) / per))),
                      dim3(256), lds, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_few_gated(const Desc& d, const GatedArgs& g, hipStream_t s) {
   FewArgs a{};
-  const size_t lds = fill(d, d.N, (g.M + 4 * quads(g.M) - 1) / (4 * quads(g.M)), true, a);
+  const size_t lds = fill(d, d.N, (g.M + 4 * quads(g.M) - 1) / (4 * quads(g.M)), true, quads(g.M), (int)(g.M < 16 ? g.M : 16), a);
   a.w[0] = g.gate;
   a.w[1] = g.up;
   a.x = g.x;
@@ -945,16 +1028,16 @@ hipError_t launch_few_gated(const Desc& d, const GatedArgs& g, hipStream_t s) {
   a.bdt = g.xdt;
   a.act = g.act;
   const int64_t per = 4 * quads(g.M);
-  hipLaunchKernelGGL(mx_fn<FM_GATED>(g.xdt == BF16, g.M),
+  hipLaunchKernelGGL(mx_fn<FM_GATED>(g.xdt == BF16, a.x_lds > 0, g.M),
                      dim3((unsigned)(a.tiles * ((g.M + per - 1) / per))), dim3(256), lds, s, a);
   return hipGetLastError();
 }
 
-// The metadata of 16 rows (of both layers of a pair) has to fit LDS next to the
-// activations and sums of 8 rows of x.
+// The metadata of a pass's 32 rows has to fit LDS next to the activations of two
+// steps and the sums.
 bool few_fits(const Desc& d, bool pair) {
   FewArgs a{};
-  return fill(d, 16, 1, pair, a) <= 112 * 1024;
+  return fill(d, 16, 1, pair, 1, 0, a) <= 112 * 1024;
 }
 bool moe_format(const Desc& d) { return few_kind(d) >= 0; }
 int moe_max_tokens() { return kTok; }
@@ -992,9 +1075,9 @@ hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStr
   }
   const int64_t most = m.M * m.topk < m.E ? m.M * m.topk : m.E;
   // up to four tokens: the form that holds one quad, in fewer registers
-  const int q = m.M <= 4 ? 1 : 2;
+  const int q = m.M <= 4 ? 1 : 2, tokens = (int)(m.M < 4 * q ? m.M : 4 * q);
   FewArgs a{};
-  size_t lds = fill(up, inner, most, true, a);
+  size_t lds = fill(up, inner, most, true, q, tokens, a);
   a.w[0] = m.gate;
   a.w[1] = m.up;
   a.x = m.x;
@@ -1005,12 +1088,12 @@ hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStr
   a.ids = m.ids;
   a.E = m.E;
   a.topk = m.topk;
-  hipLaunchKernelGGL(expert_fn<FM_UP>(few_kind(up), xb, q), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
-  lds = fill(down, K, most, false, a);
+  hipLaunchKernelGGL(expert_fn<FM_UP>(few_kind(up), xb, a.x_lds > 0, q), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
+  lds = fill(down, K, most, false, q, tokens, a);
   a.w[0] = a.w[1] = m.down;
   a.x = h;
   a.y = part;
-  hipLaunchKernelGGL(expert_fn<FM_DOWN>(few_kind(down), xb, q), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
+  hipLaunchKernelGGL(expert_fn<FM_DOWN>(few_kind(down), xb, a.x_lds > 0, q), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
   hipLaunchKernelGGL(k_combine, dim3((unsigned)((K + 1023) / 1024), (unsigned)m.M), dim3(256), 0, s, part, m.ids,
                      m.weights, m.E, m.topk, K, m.y, m.ydt);
   return hipGetLastError();

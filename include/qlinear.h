@@ -140,7 +140,7 @@ typedef enum {
                               activation rows), K % 128 == 0, every buffer
                               < 2 GiB                                         */
   /* MXFP4: both qGEMV selectors mean its few-row kernel, any M (tiles of 16
-     rows, M * N <= 2^34), K <= 229376; AUTO takes it up to 16 rows and where
+     rows, M * N <= 2^34), K <= 114688; AUTO takes it up to 16 rows and where
      K % 64 != 0, the qGEMM (K <= 2^20) otherwise.                            */
 } qp_kernel;
 
@@ -519,7 +519,7 @@ qp_status qpack_quantize_activations_mx(const void* x, int32_t x_dtype, int64_t 
 /* y [M, N] (QP_F16, QP_BF16 or QP_F32) = X W^T (+ bias [N], fp32, or NULL)
  * for MXFP4 activations (xq, xs) and MXFP4 weights; fp32 sums of exact
  * products, rounded once.  Up to 16 rows, and at any M where K % 128 != 0: the
- * few-row kernel (K <= 229376; scales of X between 2^-126 and 2^125, which
+ * few-row kernel (K <= 114688; scales of X between 2^-126 and 2^125, which
  * finite rows' are); otherwise the scaled matrix cores (K <= 2^20).  A row with a scale
  * of 255 gives NaN in its outputs alone.  Limits as the MLP block's products;
  * outputs reach into no other buffer (QP_EINVAL). */
@@ -559,9 +559,9 @@ qp_status qmoe_workspace_bytes(const qp_desc* d_up, const qp_desc* d_down, int64
  * of its tokens.  Exact codes, fp32 sums; the inner activations are rounded
  * to x_dtype, everything else once at the end; results do not depend on
  * timing, nor a token's on the other tokens.  Limits: M <= 64, experts <= 512,
- * topk <= 16, M * topk * max(K, inner) < 2^29, and rows whose metadata, 16 of
- * gate and up or of down together, fits 112 KiB (K <= 28672 and inner <= 57344
- * for AFFINE of group size 32, more for the others).  The workspace
+ * topk <= 16, M * topk * max(K, inner) < 2^29, and rows 32 of whose metadata fit
+ * 112 KiB (K and inner <= 28672 for AFFINE of group size 32 and SYM4 of 32,
+ * 57344 for groups of 64 and Q4K, 114688 for MXFP4).  The workspace
  * (qmoe_workspace_bytes, 16-byte aligned) is busy until the call's kernels
  * finish; buffers and errors as the MLP block's entry points. */
 qp_status qmoe_forward(const qp_desc* d_up, const qp_desc* d_down, int32_t experts, int32_t topk,
