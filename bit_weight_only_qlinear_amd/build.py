@@ -37,7 +37,9 @@ SOURCES = {
     "backward.hip": [],
     "stage.hip": [],
     "few.hip": [],
+    "moe.hip": [],
     "mx.hip": [],
+    "mx_few.hip": [],
 }
 
 

@@ -1,980 +1,21 @@
-// Packed products for few activation rows: the MXFP4 qGEMV and gated pair of
-// up to 16 rows, and the two products of a mixture-of-experts layer, whose
-// experts' rows lie one after the other in the packed buffers.
-//
-// All of them are bound by the codes' way from HBM, so the arithmetic has to
-// stay out of the way of 16-byte loads.  v_mfma_f32_4x4x4_16b does that: it
-// multiplies 16 independent 4 x 4 x 4 blocks, lane l holding column l % 4 of
-// block l / 4 in B and in the result alike.  With the codes as B, a lane owns
-// one weight row (of four) and one 32-column chunk (of sixteen), i.e. one
-// 16-byte load; its accumulators are four activation rows of exactly that
-// chunk, so a format's scale and offset are two numbers of the same lane:
-//     y += S sum (MAG + u) x + T sum x,
-// with u the code, MAG + u held exactly (128 + u in bf16, 1024 + u in fp16;
-// MXFP4: the E2M1 value itself, MAG = T = 0, by one hardware conversion per
-// two codes) and sum x from the same instruction against ones.  One wave
-// load covers four rows x 256 contiguous bytes.  Four activation rows cost
-// the same as one; each further four cost 8 matrix instructions (64 cycles)
-// per 1 KiB of codes, still twice what HBM delivers at 16 rows.
-//
-// Four waves per block.  KW of them split a row's 512-column steps, the
-// others take other rows.  A team of KW waves runs over its rows in passes of
-// 4 G, as one stream: the codes of the next two steps are always on their way,
-// those of the next pass while a pass's sums are taken.  The sums over lanes
-// are a transposed reduction (permlane swaps, then DPP), those over waves meet
-// in LDS.  The metadata of the block's rows is staged in LDS by direct loads,
-// in front of the first codes.
-//
-// Experts: a block's unit is (a-th expert that some token chose, 16 rows or
-// features of it); every block finds its expert and the expert's tokens from
-// the ids by itself, in LDS.  Grids cover as many experts as the tokens could
-// reach; blocks past the ones that are end at once.
-#include "device_common.hpp"
-#include "mlp_common.hpp"
-#include "qp_internal.hpp"
+// MXFP4 products and gated pairs for few activation rows.
+#include "few_kernels.hpp"
 
 namespace qp {
 namespace {
 
-enum FKind : int { F_MX4 = 0, F_AFF4 = 1, F_AFF4H = 2, F_Q4K = 3, F_SYM4 = 4 };
-enum FMode : int { FM_LINEAR = 0, FM_GATED = 1, FM_UP = 2, FM_DOWN = 3 };
-constexpr bool is_pair(int mode) { return mode == FM_GATED || mode == FM_UP; }
-
-constexpr uint32_t kOff = 0x80000000u;   // at or past every resource: reads 0
-
-struct FewArgs {
-  Bufs w[2];
-  int64_t K, N;            // columns; rows per expert (of the layer)
-  int C;                   // 32-column chunks per row
-  int gsh;                 // chunk -> group: >> gsh
-  int KW, RW;              // waves per row, row teams (KW * RW == 4)
-  int feats;               // rows (features of a pair) per team, whole passes
-  int tiles;               // blocks per expert (or layer)
-  uint32_t mrow[3];        // metadata bytes per row: scales, zeros, steps
-  uint32_t mlds[2][3];     // LDS offset of each slice
-  uint32_t x_lds;          // and of the tokens' whole rows
-  const void* x;           // [rows, K] of 16 bits, or MXFP4 codes
-  const void* xsc;         //   and their scales
-  int64_t M;
-  void* y;                 // LINEAR, GATED: [M, N] of ydt; UP: h [M topk, N] of
-  int ydt;                 //   ydt; DOWN: partial sums [M topk, N] fp32
-  const void* bias[2];
-  int bdt;                 // type of the biases
-  int act;
-  const int* ids;          // experts: [M, topk]
-  int E, topk;
-};
-
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
-typedef short short4_t __attribute__((ext_vector_type(4)));
-typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t few_rsrc(const void* p, uint64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)(uint32_t)bytes,
-                                           0x00020000);
-}
-
-// 16 bytes per lane from `off` into 1 KiB of LDS.
-__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, unsigned char* lds, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
-}
-
-template <bool XB>
-__device__ __forceinline__ f32x4_t mfma4(uint2 a, uint2 b, f32x4_t c) {
-  if constexpr (XB)
-    return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(short4_t, a),
-                                                  __builtin_bit_cast(short4_t, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, a),
-                                              __builtin_bit_cast(half4_t, b), c, 0, 0, 0);
-}
-
-// E2M1 codes of byte SEL of w, times a power of two, as a pair (exact).
-template <bool XB, int SEL>
-__device__ __forceinline__ uint32_t e2m1_pair(uint32_t w, float scale = 1.f) {
-  if constexpr (XB)
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, SEL));
-  else
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, SEL));
-}
-
-// The 8 codes of one word as two operands of four; MXFP4 in their order,
-// nibbles as (0, 4, 1, 5) and (2, 6, 3, 7).
-template <int KIND, bool XB>
-__device__ __forceinline__ void code_ops(uint32_t w, uint32_t mask, uint32_t mag, uint2& lo, uint2& hi) {
-  if constexpr (KIND == F_MX4) {
-    lo = make_uint2(e2m1_pair<XB, 0>(w), e2m1_pair<XB, 1>(w));
-    hi = make_uint2(e2m1_pair<XB, 2>(w), e2m1_pair<XB, 3>(w));
-  } else {
-    lo = make_uint2((w & mask) | mag, ((w >> 4) & mask) | mag);
-    hi = make_uint2(((w >> 8) & mask) | mag, ((w >> 12) & mask) | mag);
-  }
-}
-
-// 8 activations (raw bits) in the order of the code operands.
-template <int KIND>
-__device__ __forceinline__ void x_ops(uint4 u, uint2& lo, uint2& hi) {
-  if constexpr (KIND == F_MX4) {
-    lo = make_uint2(u.x, u.y);
-    hi = make_uint2(u.z, u.w);
-  } else {
-    lo = make_uint2(__builtin_amdgcn_perm(u.z, u.x, 0x05040100u),
-                    __builtin_amdgcn_perm(u.z, u.x, 0x07060302u));
-    hi = make_uint2(__builtin_amdgcn_perm(u.w, u.y, 0x05040100u),
-                    __builtin_amdgcn_perm(u.w, u.y, 0x07060302u));
-  }
-}
-
-// E8M0 byte -> fp32: 2^(s - 127), NaN at 255.
-__device__ __forceinline__ float e8m0(uint32_t s) {
-  const uint32_t b = s == 0 ? 0x00400000u : s << 23;
-  return __uint_as_float(s == 255u ? 0x7FC00000u : b);
-}
-
-// Raw metadata of one chunk, and what it stands for.
-struct Meta {
-  uint32_t s, z, p;
-};
-template <int KIND, typename LD>
-__device__ __forceinline__ Meta load_meta(const FewArgs& a, uint32_t c, LD ld) {
-  Meta m{0, 0, 0};
-  const uint32_t g = c >> a.gsh;
-  if constexpr (KIND == F_MX4) {
-    m.s = ld(0, c, (uint8_t)0);
-  } else if constexpr (KIND == F_Q4K) {
-    m.s = ld(0, c, (uint8_t)0);
-    m.z = ld(1, c, (uint8_t)0);
-    m.p = ld(2, 4u * (c >> 3), 0u);
-  } else if constexpr (KIND == F_SYM4) {
-    m.s = ld(0, 4u * g, 0u);
-  } else {
-    m.s = ld(0, 2u * g, (uint16_t)0);
-    m.z = ld(1, 2u * g, (uint16_t)0);
-  }
-  return m;
-}
-template <int KIND, bool XB>
-__device__ __forceinline__ void scale_of(const Meta& m, float& S, float& T) {
-  constexpr float MAG = XB ? 128.f : 1024.f;
-  if constexpr (KIND == F_MX4) {
-    S = e8m0(m.s);
-    T = 0.f;
-  } else if constexpr (KIND == F_Q4K) {
-    S = (float)m.s * f16_to_f32(m.p & 0xFFFFu);
-    T = -S * (MAG + (float)m.z * f16_to_f32(m.p >> 16));
-  } else if constexpr (KIND == F_SYM4) {
-    S = __uint_as_float(m.s);
-    T = -S * (MAG + 8.f);
-  } else {
-    S = KIND == F_AFF4 ? bf16_to_f32(m.s) : f16_to_f32(m.s);
-    T = fmaf(-MAG, S, KIND == F_AFF4 ? bf16_to_f32(m.z) : f16_to_f32(m.z));
-  }
-}
-
-// What a block works on.
-struct Unit {
-  int64_t row0;            // first row of its expert in the packed buffers
-  int brow0, brows;        // rows (features) of the block inside the expert
-  int T;                   // tokens
-};
-
-// v[16] summed over the 16 lanes of equal l % 4: afterwards register k of a
-// lane of 16-lane row R holds value 4 k + (((R & 1) << 1) | (R >> 1)).
-__device__ __forceinline__ void sum16(float (&v)[16], float (&o)[4]) {
-  float b[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[2 * k]),
-                                                    __float_as_uint(v[2 * k + 1]), false, false);
-    b[k] = __uint_as_float(p[0]) + __uint_as_float(p[1]);
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(b[2 * k]),
-                                                    __float_as_uint(b[2 * k + 1]), false, false);
-    o[k] = __uint_as_float(p[0]) + __uint_as_float(p[1]);
-    o[k] += dpp_f<QP_DPP_ROW_ROR8>(0.f, o[k]);
-    o[k] += dpp_f<QP_DPP_ROW_ROR4>(0.f, o[k]);
-  }
-}
-
-// The tokens of a pass: their rows of x (uniform byte offsets) and how many
-// there are.
-template <int Q>
-struct Tok {
-  uint32_t off[4 * Q];
-  int n;
-};
-
-__device__ __forceinline__ void few_store(void* y, int64_t i, float v, int dt) {
-  if (dt == F32) static_cast<float*>(y)[i] = v;
-  else if (dt == BF16) static_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_bf16_rne(v);
-  else static_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_f16_rne(v);
-}
-
-// All tokens t0 .. t0 + 4 Q - 1 of the unit, all rows of the block.  A pass of
-// a team takes rows 4 g + l % 4 for g < G from its row f0 on (a pair: g < G / 2
-// of layer 0, the others of layer 1).  xrow, orow: rows of x and of the output,
-// per token; red: two buffers of the passes' partial sums.
-//
-// 16-bit activations come through the wave's own part of LDS (xl): a load
-// instruction takes 1 KiB of one token's row, where the operands' own layout
-// would touch 64 pieces of 64 bytes (16 tokens: 2.4 TB/s of codes at most).
-// Token t's 16-byte piece j lies at j ^ (t % 4), so that the 16 lanes of a read
-// phase (four tokens, four chunks) touch every bank once.  Tokens that are not
-// there read what else is in LDS: they are rows of results of their own.
-// WHOLE: the tokens' whole rows are loaded once per block, step by step, and
-// serve all of its waves and passes.
-template <int KIND, bool XB, bool XM, bool WHOLE, int Q, int MODE>
-__device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const unsigned char* smem,
-                                        const uint32_t (&mbase)[2][3],
-                                        const __amdgpu_buffer_rsrc_t (&rw)[2],
-                                        const __amdgpu_buffer_rsrc_t (&rx)[2], unsigned char* xl,
-                                        const int* xrow, const int* orow, int t0, float* red,
-                                        bool first) {
-  constexpr bool PAIR = is_pair(MODE);
-  constexpr int G = Q == 1 ? 8 : 4;                  // groups of four rows per pass
-  constexpr int F = PAIR ? 2 * G : 4 * G;            // features per pass
-  constexpr int kRed = 4 * G * 4 * Q;                // sums of a wave and pass
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kw = wave % a.KW, team = wave / a.KW;
-  const uint32_t j = lane & 3, b = lane >> 2;
-  const uint32_t C = (uint32_t)a.C, rowb = (uint32_t)(a.K / 2);
-  const int S = (a.C + 15) / 16;
-  const int base = team * a.feats;                   // the team's first row
-  if constexpr (!WHOLE) xl += wave * 4096 * Q;
-  Tok<Q> tok;
-  tok.n = u.T - t0 < 4 * Q ? u.T - t0 : 4 * Q;
-#pragma unroll
-  for (int t = 0; t < (WHOLE ? 0 : 4 * Q); ++t)
-    tok.off[t] = t < tok.n ? (uint32_t)__builtin_amdgcn_readfirstlane(xrow[t0 + t]) * (uint32_t)(XM ? a.K / 2 : a.K * 2) : 0u;
-  auto layer = [](int g) { return PAIR && g >= G / 2 ? 1 : 0; };
-  auto lrow = [&](int f0, int g) { return (uint32_t)f0 + 4u * (PAIR ? g % (G / 2) : g) + j; };
-
-  struct Step {
-    uint4 w[G];
-  };
-  // MXFP4 activations, straight into registers: the next step's codes and
-  // scales, and the lane's row of them
-  uint4 xc[XM ? Q : 1];
-  uint32_t xsc[XM ? Q : 1], xm[XM ? Q : 1];
-  if constexpr (XM) {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const uint32_t r01 = j & 1 ? tok.off[4 * q + 1] : tok.off[4 * q], r23 = j & 1 ? tok.off[4 * q + 3] : tok.off[4 * q + 2];
-      xm[q] = 4 * q + (int)j < tok.n ? (j & 2 ? r23 : r01) : kOff;
-    }
-  }
-  auto load = [&](int f0, int s, bool on, Step& st) __attribute__((always_inline)) {
-    const uint32_t at = on && (uint32_t)s * 16u + b < C ? lrow(f0, 0) * rowb + 16u * b + (uint32_t)s * 256u : kOff;
-    // in this order, or the wait for one step's first codes is one for all
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      st.w[g] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
-                                              rw[layer(g)], at + 4u * (PAIR ? g % (G / 2) : g) * rowb, 0, 2));
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  auto load_x = [&](int s) __attribute__((always_inline)) {
-    if constexpr (WHOLE) {
-    } else if constexpr (XM) {
-      const uint32_t c = (uint32_t)s * 16u + b;
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        const bool in = c < C && xm[q] != kOff;
-        xc[q] = __builtin_bit_cast(
-            uint4, __builtin_amdgcn_raw_buffer_load_b128(rx[0], in ? xm[q] + 16u * c : kOff, 0, 0));
-        xsc[q] = __builtin_amdgcn_raw_buffer_load_b8(rx[1], in ? xm[q] / 16u + c : kOff, 0, 0);
-      }
-    } else {
-      const bool ok = (uint32_t)s * 16u + b < C;
-#pragma unroll
-      for (int t = 0; t < 4 * Q; ++t)
-        if (t < tok.n)
-          to_lds(rx[0], xl + 1024 * t,
-                 ok ? tok.off[t] + (uint32_t)s * 1024u + 16u * ((uint32_t)lane ^ (t & 3u)) : kOff);
-    }
-  };
-  // nibbles: 128 (bf16) or 1024 (fp16) and the code in its low bits, one
-  // v_and_or_b32 from registers (two literals would make it two instructions)
-  uint32_t mask = 0x000F000Fu, mag = XB ? 0x43004300u : 0x64006400u;
-  asm("" : "+v"(mask), "+s"(mag));
-  uint32_t jm[3];
-#pragma unroll
-  for (int i = 0; i < 3; ++i) jm[i] = j * a.mrow[i];
-  const uint32_t xr = j * 1024u + 64u * b + 16u * j;   // piece 0 of the lane's token and chunk
-
-  f32x4_t acc[G][Q];
-#pragma unroll
-  for (int g = 0; g < G; ++g)
-#pragma unroll
-    for (int q = 0; q < Q; ++q) acc[g][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  // Step s of the pass at f0 from st; `more`: another step follows, at sx.
-  auto compute = [&](int f0, int s, const Step& st, bool more, int sx) __attribute__((always_inline)) {
-    const uint32_t c = (uint32_t)s * 16u + b, cc = c < C ? c : C - 1u;
-    if constexpr (!WHOLE && !XM) {
-      // the compiler does not see these copies: what was issued after them are
-      // the next step's G loads (and stores)
-      __builtin_amdgcn_s_waitcnt((G & 0xF) | (0x7 << 4) | (0xF << 8));
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    const unsigned char* xs0 = WHOLE ? xl + (uint32_t)(s * tok.n) * 1024u : xl;
-    uint2 xo[Q][8];
-    f32x4_t xs[Q];
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      if constexpr (XM) {   // exact in bf16
-        const float sc = e8m0(xsc[q]);
-        const uint32_t w[4] = {xc[q].x, xc[q].y, xc[q].z, xc[q].w};
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          xo[q][2 * v] = make_uint2(e2m1_pair<true, 0>(w[v], sc), e2m1_pair<true, 1>(w[v], sc));
-          xo[q][2 * v + 1] = make_uint2(e2m1_pair<true, 2>(w[v], sc), e2m1_pair<true, 3>(w[v], sc));
-        }
-      } else {
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          x_ops<KIND>(*reinterpret_cast<const uint4*>(xs0 + 4096u * q + (xr ^ (16u * v))), xo[q][2 * v], xo[q][2 * v + 1]);
-      }
-    }
-    if (!WHOLE && more) {   // its activations, now that this step's are read
-      if constexpr (!XM) {
-        __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      load_x(sx);
-    }
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      xs[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      if constexpr (KIND != F_MX4) {
-        const uint32_t one = XB ? 0x3F803F80u : 0x3C003C00u;
-#pragma unroll
-        for (int v = 0; v < 8; ++v) xs[q] = mfma4<XB>(xo[q][v], make_uint2(one, one), xs[q]);
-      }
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      // LDS has room for whole passes; rows past the block's last are sums of
-      // their own that nothing stores
-      const Meta m = load_meta<KIND>(a, cc, [&](int i, uint32_t o, auto t) {
-        const uint32_t row = mbase[layer(g)][i] + ((uint32_t)f0 + 4u * (PAIR ? g % (G / 2) : g)) * a.mrow[i];
-        return (uint32_t)*reinterpret_cast<const decltype(t)*>(smem + row + (jm[i] + o));
-      });
-      float Sv, Tv;
-      scale_of<KIND, XB>(m, Sv, Tv);
-      f32x4_t d[Q];
-#pragma unroll
-      for (int q = 0; q < Q; ++q) d[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      const uint32_t wv[4] = {st.w[g].x, st.w[g].y, st.w[g].z, st.w[g].w};
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        uint2 lo, hi;
-        code_ops<KIND, XB>(wv[v], mask, mag, lo, hi);
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-          d[q] = mfma4<XB>(xo[q][2 * v], lo, d[q]);
-          d[q] = mfma4<XB>(xo[q][2 * v + 1], hi, d[q]);
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < Q; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[g][q][i] = fmaf(Sv, d[q][i], acc[g][q][i]);
-          if constexpr (KIND != F_MX4) acc[g][q][i] = fmaf(Tv, xs[q][i], acc[g][q][i]);
-        }
-    }
-  };
-  // A pass's sums: over lanes, then over the team's waves.  Two buffers by
-  // turns, so that one barrier per pass is enough.
-  // A pass's sums over lanes; waves that share rows meet in LDS, in two buffers
-  // by turns, so that one barrier per pass is enough.
-  const int R = lane >> 4, p4 = ((R & 1) << 1) | (R >> 1);
-  auto put = [&](int row, int t, float g, float v) __attribute__((always_inline)) {
-    if (row >= u.brows || t0 + t >= u.T) return;
-    const int64_t n = u.brow0 + row;
-    if constexpr (MODE == FM_LINEAR || MODE == FM_GATED) {
-      auto bias = [&](const void* p) {
-        if (a.bdt == F32) return static_cast<const float*>(p)[n];
-        return meta_to_f32(static_cast<const uint16_t*>(p)[n], a.bdt == BF16);
-      };
-      if (a.bias[0]) g += bias(a.bias[0]);
-      if (PAIR && a.bias[1]) v += bias(a.bias[1]);
-    }
-    if constexpr (PAIR) g = (a.act == ACT_SILU ? act_f<ACT_SILU>(g) : act_f<ACT_GELU_TANH>(g)) * v;
-    if constexpr (MODE == FM_DOWN)
-      static_cast<float*>(a.y)[(int64_t)orow[t0 + t] * a.N + n] = g;
-    else
-      few_store(a.y, (int64_t)orow[t0 + t] * a.N + n, g, a.ydt);
-  };
-  auto finish = [&](int f0, int pass) __attribute__((always_inline)) {
-    float* rb = red + (pass & 1) * 4 * kRed;
-    float* mine = rb + wave * kRed;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      float o[G / 4][4];   // rows 16 h + 4 k + l % 4 of the pass, token 4 q + p4
-#pragma unroll
-      for (int h = 0; h < G / 4; ++h) {
-        float v[16];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[4 * k + i] = acc[4 * h + k][q][i];
-            acc[4 * h + k][q][i] = 0.f;
-          }
-        sum16(v, o[h]);
-      }
-      if ((lane & 12) == 0) {
-        if (a.KW == 1) {
-#pragma unroll
-          for (int k = 0; k < (PAIR ? G / 2 : G); ++k)
-            put(f0 + 4 * k + (int)j, 4 * q + p4, o[k / 4][k % 4], PAIR ? o[(k + G / 2) / 4][(k + G / 2) % 4] : 0.f);
-        } else {
-#pragma unroll
-          for (int k = 0; k < G; ++k) mine[(4 * k + (int)j) * (4 * Q) + 4 * q + p4] = o[k / 4][k % 4];
-        }
-      }
-    }
-    if (a.KW == 1) return;
-    __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0); loads stay in flight
-    __builtin_amdgcn_s_barrier();
-    // the team's threads: (feature, token) with the feature fastest
-    for (int i = threadIdx.x - team * a.KW * 64; i < F * 4 * Q; i += a.KW * 64) {
-      const int fe = i % F, t = i / F;
-      const float* r = rb + team * a.KW * kRed + t;
-      float g = 0.f, v = 0.f;
-      for (int w = 0; w < a.KW; ++w) {
-        g += r[w * kRed + fe * 4 * Q];
-        if constexpr (PAIR) v += r[w * kRed + (F + fe) * 4 * Q];
-      }
-      put(f0 + fe, t, g, v);
-    }
-  };
-
-  // the wave's steps: n per pass; passes whose rows lie past the block's end
-  // are left out, for all teams alike (the first team has the most)
-  const int n = (S - kw + a.KW - 1) / a.KW;
-  const int passes = ((u.brows < a.feats ? u.brows : a.feats) + F - 1) / F, total = passes * n;
-  const int end = base + passes * F;
-  int lf = base, lk = 0;   // next load: row and step of its pass
-  auto next = [&](Step& st) __attribute__((always_inline)) {
-    // Past the last pass it reads nothing, but it is issued: after loads that
-    // may not have been, the wait for one step's codes is a wait for all.
-    load(lf, kw + lk * a.KW, lf < end, st);
-    if (++lk == n) {
-      lk = 0;
-      lf += F;
-    }
-  };
-  Step s0, s1;
-  if constexpr (WHOLE) {
-    // 1 KiB of one token and step per load, dealt out to the waves
-    if (!first) __syncthreads();   // the tokens before are done with it
-    for (int i = wave; i < S * tok.n; i += 4) {
-      const int s = i / tok.n, t = i - s * tok.n;
-      to_lds(rx[0], xl + 1024 * i,
-             (uint32_t)s * 16u + b < C ? (uint32_t)__builtin_amdgcn_readfirstlane(xrow[t0 + t]) * (uint32_t)(a.K * 2) +
-                                             (uint32_t)s * 1024u + 16u * ((uint32_t)lane ^ ((uint32_t)t & 3u))
-                                       : kOff);
-    }
-  }
-  load_x(kw);
-  next(s0);
-  next(s1);
-  if (first || WHOLE) {
-    // the metadata's and the rows' copies were issued before these loads
-    constexpr int w = 2 * G;
-    static_assert(w < 64, "a wait counts to 63");
-    __builtin_amdgcn_s_waitcnt((w & 0xF) | (0x7 << 4) | (0xF << 8) | ((w >> 4) << 14));
-    __syncthreads();
-  }
-  int f0 = base, k = 0, pass = 0;
-  auto step = [&](int i, Step& st) __attribute__((always_inline)) {
-    const bool last = k + 1 == n;
-    compute(f0, kw + k * a.KW, st, i + 1 < total, kw + (last ? 0 : (k + 1) * a.KW));
-    next(st);
-    ++k;
-    if (last) {
-      if (i < total) finish(f0, pass);
-      k = 0;
-      f0 += i + 1 < total ? F : 0;
-      ++pass;
-    }
-  };
-  // Two by two; an odd last step is followed by one that adds to sums nobody
-  // reads.  (Left out by a branch, the compiler's wait for s0's codes is also
-  // one for s1's.)
-  for (int i = 0; i < total; i += 2) {
-    step(i, s0);
-    step(i + 1, s1);
-  }
-  __syncthreads();   // the next tokens' sums take the same buffers
-}
-
-constexpr int kTok = 64;          // tokens of a call
-constexpr int kExperts = 512;
-constexpr int kSlots = 16;        // experts per token
-
-// The want-th expert that some token chose, its tokens (rising) and each one's
-// first slot with it; -1 where fewer are chosen.  Every wave ends up with the
-// answer; xrow and orow are complete after the last barrier.
-template <int MODE>
-__device__ __forceinline__ int find_unit(const FewArgs& a, int want, int* mask, int* ids, int* xrow,
-                                         int* orow, int& T) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int n = (int)a.M * a.topk;
-  int got[kTok * kSlots / 256];
-#pragma unroll
-  for (int k = 0; k < kTok * kSlots / 256; ++k) got[k] = tid + 256 * k < n ? a.ids[tid + 256 * k] : -1;
-  for (int e = tid; e < 2 * a.E; e += 256) mask[e] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kTok * kSlots / 256; ++k) {
-    const int i = tid + 256 * k, e = got[k];
-    if (i < n) ids[i] = e;
-    if (e >= 0 && e < a.E) {
-      const int m = i / a.topk;
-      atomicOr(&mask[2 * e + (m >> 5)], (int)(1u << (m & 31)));
-    }
-  }
-  __syncthreads();
-  // by falling number of tokens, so that the longest blocks start first
-  int cnt[kExperts / 64], most = 0;
-#pragma unroll
-  for (int i = 0; i < kExperts / 64; ++i) {
-    const int e = 64 * i + lane;
-    cnt[i] = 64 * i < a.E && e < a.E ? __popc((unsigned)mask[2 * e]) + __popc((unsigned)mask[2 * e + 1]) : 0;
-    most = cnt[i] > most ? cnt[i] : most;
-  }
-  for (int off = 32; off > 0; off >>= 1) {
-    const int o = __shfl_xor(most, off, 64);
-    most = o > most ? o : most;
-  }
-  int found = -1;
-  for (int t = most, left = want; t > 0 && found < 0; --t) {
-#pragma unroll
-    for (int i = 0; i < kExperts / 64; ++i) {
-      if (found >= 0 || 64 * i >= a.E) continue;
-      uint64_t bits = __ballot(cnt[i] == t);
-      const int n = __popcll(bits);
-      if (left < n) {
-        for (int k = 0; k < left; ++k) bits &= bits - 1;
-        found = 64 * i + __ffsll((unsigned long long)bits) - 1;
-      }
-      left -= n;
-    }
-  }
-  found = __builtin_amdgcn_readfirstlane(found);
-  if (found < 0) return -1;
-  const uint64_t tok = (uint64_t)(uint32_t)mask[2 * found] | ((uint64_t)(uint32_t)mask[2 * found + 1] << 32);
-  T = __popcll(tok);
-  if (tid < 64 && ((tok >> lane) & 1)) {
-    const int at = __popcll(tok & ((uint64_t(1) << lane) - 1));
-    int s = 0;
-    while (ids[lane * a.topk + s] != found) ++s;   // ends: the token is in the mask
-    const int slot = lane * a.topk + s;
-    xrow[at] = MODE == FM_UP ? lane : slot;
-    orow[at] = slot;
-  }
-  __syncthreads();
-  return found;
-}
-
-template <int KIND, bool XB, bool XM, bool WHOLE, int Q, int MODE>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
-k_few(FewArgs a) {
-  constexpr bool EXPERTS = MODE == FM_UP || MODE == FM_DOWN;
-  constexpr bool PAIR = is_pair(MODE);
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  // activations by steps, 4 Q KiB per wave: an array of its own, or the compiler
-  // takes their loads for writes to the metadata and waits for them before
-  // reading it
-  __shared__ __attribute__((aligned(16))) unsigned char xstep[XM || WHOLE ? 16 : 4 * 4096 * Q];
-  unsigned char* xbuf = WHOLE ? smem + a.x_lds : xstep;
-  __shared__ float red[2 * 4 * 16 * 4 * (Q == 1 ? 2 : Q)];   // Q == 2 runs single quads too
-  __shared__ int xrow[kTok], orow[kTok];
-  __shared__ int mask[EXPERTS ? 2 * kExperts : 1], ids[EXPERTS ? kTok * kSlots : 1];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-
-  Unit u;
-  int expert = 0;
-  const int tile = (int)(blockIdx.x % (unsigned)a.tiles);   // and the expert or the tile of x's rows
-  int64_t xbase = 0;
-  if constexpr (EXPERTS) {
-    expert = find_unit<MODE>(a, (int)(blockIdx.x / (unsigned)a.tiles), mask, ids, xrow, orow, u.T);
-    if (expert < 0) return;
-  } else {
-    xbase = (int64_t)(blockIdx.x / (unsigned)a.tiles) * (4 * Q);
-    u.T = (int)(a.M - xbase < 4 * Q ? a.M - xbase : 4 * Q);
-    if (tid < 4 * Q) {
-      xrow[tid] = tid;
-      orow[tid] = tid;
-    }
-  }
-  const int rows = a.RW * a.feats;
-  u.brow0 = tile * rows;
-  u.brows = (int)(a.N - u.brow0 < rows ? a.N - u.brow0 : rows);
-  u.row0 = (int64_t)expert * a.N + u.brow0;
-
-  // resources of the block's rows; its metadata into LDS (1 KiB per wave and
-  // instruction, whole 16-byte units; bytes past the slice read 0)
-  __amdgpu_buffer_rsrc_t rw[2];
-  uint32_t mbase[2][3];
-#pragma unroll
-  for (int l = 0; l < (PAIR ? 2 : 1); ++l) {
-    rw[l] = few_rsrc(static_cast<const unsigned char*>(a.w[l].qweight) + u.row0 * (a.K / 2),
-                     (uint64_t)u.brows * (uint64_t)(a.K / 2));
-    const void* arr[3] = {a.w[l].scales, a.w[l].zeros, a.w[l].steps};
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const uint64_t at = (uint64_t)u.row0 * a.mrow[i], lo = at & ~uint64_t(15);
-      const uint32_t head = (uint32_t)(at - lo), bytes = head + (uint32_t)u.brows * a.mrow[i];
-      mbase[l][i] = a.mlds[l][i] + head;
-      if (a.mrow[i]) {
-        const __amdgpu_buffer_rsrc_t rm = few_rsrc(static_cast<const unsigned char*>(arr[i]) + lo, (bytes + 15u) & ~15u);
-        for (uint32_t ch = (uint32_t)wave; ch * 1024u < bytes; ch += 4)
-          to_lds(rm, smem + a.mlds[l][i] + ch * 1024u, ch * 1024u + 16u * (uint32_t)lane);
-      }
-    }
-  }
-  if constexpr (!PAIR) rw[1] = rw[0];
-  const int64_t xrows = MODE == FM_DOWN ? a.M * a.topk : a.M - xbase;
-  const int64_t xr = EXPERTS || xrows < 4 * Q ? xrows : 4 * Q, xrowb = XM ? a.K / 2 : a.K * 2;
-  const __amdgpu_buffer_rsrc_t rx[2] = {
-      few_rsrc(static_cast<const unsigned char*>(a.x) + xbase * xrowb, (uint64_t)(xr * xrowb)),
-      few_rsrc(static_cast<const unsigned char*>(a.xsc) + xbase * (a.K / 32), XM ? (uint64_t)(xr * (a.K / 32)) : 0u)};
-  if constexpr (!EXPERTS) {
-    FewArgs b = a;
-    if (xbase) b.y = static_cast<unsigned char*>(a.y) + xbase * a.N * (a.ydt == F32 ? 4 : 2);
-    __syncthreads();
-    few_run<KIND, XB, XM, WHOLE, Q, MODE>(b, u, smem, mbase, rw, rx, xbuf, xrow, orow, 0, red, true);
-  } else {
-    for (int t0 = 0; t0 < u.T; t0 += 4 * Q) {
-      if (Q == 1 || u.T - t0 <= 4)
-        few_run<KIND, XB, XM, WHOLE, 1, MODE>(a, u, smem, mbase, rw, rx, xbuf, xrow, orow, t0, red, t0 == 0);
-      else
-        few_run<KIND, XB, XM, WHOLE, Q, MODE>(a, u, smem, mbase, rw, rx, xbuf, xrow, orow, t0, red, t0 == 0);
-    }
-  }
-}
-
-// y [M, N] = sum over slots of weight x partial sum (fixed order).  A slot
-// whose expert the token named before adds its weight to that one's sum; one
-// outside the layer adds nothing.
-__global__ void __launch_bounds__(256) k_combine(const float* __restrict__ part,
-                                                 const int* __restrict__ ids,
-                                                 const float* __restrict__ weights, int E, int topk,
-                                                 int64_t N, void* y, int ydt) {
-  const int64_t m = blockIdx.y;
-  const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;   // N % 32 == 0
-  if (n >= N) return;
-  int e[kSlots];
-#pragma unroll
-  for (int s = 0; s < kSlots; ++s) {
-    e[s] = s < topk ? ids[m * topk + s] : -1;
-    if (e[s] >= E) e[s] = -1;
-  }
-  // all loads first: a slot's sum lies with the first slot of its expert
-  float4 p[kSlots];
-  float w[kSlots];
-#pragma unroll
-  for (int s = 0; s < kSlots; ++s) {
-    int f = s;
-#pragma unroll
-    for (int k = kSlots - 1; k >= 0; --k)
-      if (k < s && e[k] == e[s]) f = k;
-    const bool on = e[s] >= 0;   // slots past topk hold -1
-    w[s] = on ? weights[m * topk + s] : 0.f;
-    p[s] = on ? *reinterpret_cast<const float4*>(part + (m * topk + f) * N + n) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int s = 0; s < kSlots; ++s) {
-    v[0] = fmaf(w[s], p[s].x, v[0]);
-    v[1] = fmaf(w[s], p[s].y, v[1]);
-    v[2] = fmaf(w[s], p[s].z, v[2]);
-    v[3] = fmaf(w[s], p[s].w, v[3]);
-  }
-  if (ydt == F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(y) + m * N + n) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = ydt == BF16 ? f32_to_bf16_rne(v[i]) : f32_to_f16_rne(v[i]);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + m * N + n) =
-        make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-  }
-}
-
-// ---- routing: logits in fp64 (products of two 16-bit values are exact in
-// fp32), so that the choice between two experts next to each other does not
-// depend on the order of additions.
-template <bool XB>
-__device__ __forceinline__ double dot8(const uint4 u, const uint4 v) {
-  const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
-  double s = 0.0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float p = XB ? __uint_as_float(a[i] << 16) * __uint_as_float(b[i] << 16)
-                       : f16_to_f32(a[i] & 0xFFFFu) * f16_to_f32(b[i] & 0xFFFFu);
-    const float q = XB ? __uint_as_float(a[i] & 0xFFFF0000u) * __uint_as_float(b[i] & 0xFFFF0000u)
-                       : f16_to_f32(a[i] >> 16) * f16_to_f32(b[i] >> 16);
-    s += (double)p;
-    s += (double)q;
-  }
-  return s;
-}
-// A lane's part of a logit: columns 8 (lane + 64 (part + parts k)) ..., eight
-// loads of each row in flight.
-template <bool XB>
-__device__ __forceinline__ double logit_part(const uint16_t* x, const uint16_t* r, int64_t K, int lane,
-                                             int part, int parts) {
-  const uint4* xv = reinterpret_cast<const uint4*>(x);
-  const uint4* rv = reinterpret_cast<const uint4*>(r);
-  const int n = (int)(K / 8), step = 64 * parts;   // K % 32 == 0
-  double s = 0.0;
-  for (int c0 = lane + 64 * part; c0 < n; c0 += 8 * step) {
-    uint4 u[8], v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = c0 + k * step;
-      u[k] = c < n ? xv[c] : make_uint4(0, 0, 0, 0);
-      v[k] = c < n ? rv[c] : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s += dot8<XB>(u[k], v[k]);
-  }
-  return s;
-}
-__device__ __forceinline__ double wave_sum_f64(double v) {
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
-}
-
-struct RouteArgs {
-  const uint16_t* x;       // [M, K]
-  const uint16_t* r;       // [E, K]
-  int64_t M, K;
-  int E, topk, score, norm;
-  double* logits;          // [M, E]
-  int* ids;
-  float* weights;
-};
-
-// Token m's choice from its logits l [E] in LDS, by a block of `threads`.
-// An expert's place is the number of those in front of it (a larger logit, or
-// the same and a lower index), counted by several threads each; the first topk
-// places are the choice.  NaN logits come after all numbers and are never
-// chosen: places that no number takes get expert -1 and weight 0.
-struct Choice {
-  double l[kExperts];
-  double part[16];
-  int place[kExperts];
-  double top[kSlots], w[kSlots];
-  int id[kSlots];
-};
-__device__ __forceinline__ void choose(const RouteArgs& a, int64_t m, Choice& c, int threads) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int E = a.E;
-  for (int e = tid; e < E; e += threads) c.place[e] = 0;
-  if (tid < kSlots) {
-    c.id[tid] = -1;
-    c.top[tid] = -__builtin_inf();
-  }
-  __syncthreads();
-  // threads per expert: a power of two
-  int per = 1;
-  while (2 * per * E <= threads) per *= 2;
-  for (int i = tid; i < E * per; i += threads) {
-    const int e = i / per, s = i % per;
-    const double v = c.l[e];
-    int n = 0;
-    for (int k = s; k < E; k += per) {
-      const double o = c.l[k];
-      n += o > v || (o == v && k < e) ? 1 : 0;
-    }
-    if (!(v > -__builtin_inf())) n = kExperts;
-    if (n) atomicAdd(&c.place[e], n);
-  }
-  __syncthreads();
-  for (int e = tid; e < E; e += threads)
-    if (c.place[e] < a.topk) {
-      c.id[c.place[e]] = e;
-      c.top[c.place[e]] = c.l[e];
-    }
-  __syncthreads();
-  const double hi = c.top[0];
-  double sum = 0.0;
-  if (a.score == 0) {
-    for (int e = tid; e < E; e += threads) sum += c.l[e] > -__builtin_inf() ? exp(c.l[e] - hi) : 0.0;
-    sum = wave_sum_f64(sum);
-    if (lane == 0) c.part[wave] = sum;
-    __syncthreads();
-    sum = 0.0;
-    for (int w = 0; w < threads / 64; ++w) sum += c.part[w];
-  }
-  if (tid < a.topk)
-    c.w[tid] = c.id[tid] < 0 ? 0.0 : a.score == 0 ? exp(c.top[tid] - hi) / sum : 1.0 / (1.0 + exp(-c.top[tid]));
-  __syncthreads();
-  if (tid < a.topk) {
-    double total = 0.0;
-    for (int s = 0; s < a.topk; ++s) total += c.w[s];
-    const double w = a.norm ? (total > 0.0 ? c.w[tid] / total : 0.0) : c.w[tid];
-    a.ids[m * a.topk + tid] = c.id[tid];
-    a.weights[m * a.topk + tid] = (float)w;
-  }
-}
-
-// One block per token: its logits, `parts` waves to each (a power of two, in
-// one round of the 16 waves where E <= 8), then the choice.
-template <bool XB>
-__global__ void __launch_bounds__(1024) k_route(RouteArgs a) {
-  __shared__ Choice c;
-  __shared__ double s[16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m = blockIdx.x;
-  int parts = 1;
-  while (2 * parts * a.E <= 16) parts *= 2;
-  if (parts == 1) {
-    for (int e = wave; e < a.E; e += 16) {
-      const double v = wave_sum_f64(logit_part<XB>(a.x + m * a.K, a.r + (int64_t)e * a.K, a.K, lane, 0, 1));
-      if (lane == 0) c.l[e] = v;
-    }
-  } else {
-    const int e = wave / parts;
-    if (e < a.E) {
-      const double v = wave_sum_f64(
-          logit_part<XB>(a.x + m * a.K, a.r + (int64_t)e * a.K, a.K, lane, wave % parts, parts));
-      if (lane == 0) s[wave] = v;
-    }
-    __syncthreads();
-    if ((int)threadIdx.x < a.E) {
-      double v = 0.0;
-      for (int p = 0; p < parts; ++p) v += s[threadIdx.x * parts + p];
-      c.l[threadIdx.x] = v;
-    }
-  }
-  __syncthreads();
-  choose(a, m, c, 1024);
-}
-// A wave per logit, then a block per token.
-template <bool XB>
-__global__ void __launch_bounds__(256) k_logits(RouteArgs a) {
-  const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t m = blockIdx.y;
-  if (e >= a.E) return;
-  const double s = wave_sum_f64(logit_part<XB>(a.x + m * a.K, a.r + (int64_t)e * a.K, a.K, lane, 0, 1));
-  if (lane == 0) a.logits[m * a.E + e] = s;
-}
-__global__ void __launch_bounds__(256) k_choose(RouteArgs a) {
-  __shared__ Choice c;
-  const int64_t m = blockIdx.x;
-  for (int e = threadIdx.x; e < a.E; e += 256) c.l[e] = a.logits[m * a.E + e];
-  __syncthreads();
-  choose(a, m, c, 256);
-}
-
-int few_kind(const Desc& d) {
-  if (d.fmt == MXFP4) return F_MX4;
-  if (d.fmt == AFFINE && d.bits == 4) return d.meta == BF16 ? F_AFF4 : F_AFF4H;
-  if (d.fmt == Q4K) return F_Q4K;
-  if (d.fmt == SYM4) return F_SYM4;
-  return -1;
-}
-
-#ifndef QP_FEW_BLOCKS
-#define QP_FEW_BLOCKS 1024
-#endif
-#ifndef QP_FEW_WAVES
-#define QP_FEW_WAVES 2048
-#endif
-constexpr int64_t kFewWaves = QP_FEW_WAVES;
-constexpr int64_t kFewBlocks = QP_FEW_BLOCKS;
-
-// Sizes, LDS layout and launch shape that the modes share; units: experts or row
-// tiles of x; q: quads of tokens that the kernel is made for; tokens: the most a pass can have, or 0 where their rows do not go
-// through LDS.  a.x_lds: where the tokens' whole rows lie, or 0.
-size_t fill(const Desc& d, int64_t rows, int64_t units, bool pair, int q, int tokens, FewArgs& a) {
-  a.K = d.K;
-  a.N = rows;
-  a.C = (int)(d.K / 32);
-  a.gsh = 0;
-  const int kind = few_kind(d);
-  if (d.gs == d.K && kind == F_SYM4) a.gsh = 31;
-  else while ((32 << a.gsh) < d.gs) ++a.gsh;
-  const int S = (a.C + 15) / 16;
-  const int F = q == 4 || pair ? 16 : 32;   // rows of the longest pass
-  // Waves per row: as few as fill the chip (two per SIMD), since waves that
-  // share rows have to add their sums up.
-  a.KW = 1;
-  while (a.KW < 4 && 2 * a.KW <= S && units * ((rows + F - 1) / F) * a.KW < kFewWaves) a.KW *= 2;
-  for (int i = 0; i < 3; ++i) a.mrow[i] = 0;
-  if (kind == F_MX4) a.mrow[0] = (uint32_t)(d.K / 32);
-  else if (kind == F_Q4K) { a.mrow[0] = a.mrow[1] = (uint32_t)(d.K / 32); a.mrow[2] = (uint32_t)(d.K / 256 * 4); }
-  else if (kind == F_SYM4) a.mrow[0] = (uint32_t)(d.K / d.gs * 4);
-  else a.mrow[0] = a.mrow[1] = (uint32_t)(d.K / d.gs * 2);
-  auto meta = [&](int feats) {
-    a.RW = 4 / a.KW;
-    size_t lds = 0;
-    for (int l = 0; l < (pair ? 2 : 1); ++l)
-      for (int i = 0; i < 3; ++i) {
-        a.mlds[l][i] = (uint32_t)lds;
-        if (a.mrow[i]) lds += ((size_t)a.RW * feats * a.mrow[i] + 15 + 1023) / 1024 * 1024;
-      }
-    return lds;
-  };
-  while (a.KW < 4 && 2 * a.KW <= S && meta(F) > 32 * 1024) a.KW *= 2;
-  a.RW = 4 / a.KW;
-  // Rows per team: so many that the blocks of all experts (or row tiles of x)
-  // come to a few per CU, while their metadata fits 12 KiB and their codes 1 GiB.
-  const int64_t most = units * ((rows + a.RW * F - 1) / (a.RW * F));
-  int64_t k = most / kFewBlocks;
-  if (k < 1) k = 1;
-  while (k > 1 && (meta((int)k * F) > 12 * 1024 || k * F * a.RW * (d.K / 2) > (int64_t(1) << 30))) --k;
-  a.feats = (int)k * F;
-  a.tiles = (int)((rows + a.RW * a.feats - 1) / (a.RW * a.feats));
-  const size_t lds = meta(a.feats), x = (size_t)S * (size_t)tokens * 1024u;
-  a.x_lds = 0;
-  // three KiB more: tokens that are not there are read past the last row
-  if (x > 0 && x + lds <= 72 * 1024) a.x_lds = (uint32_t)lds;   // two blocks per CU
-  return a.x_lds ? lds + x + 3 * 1024u : lds;
-}
-
-using FewFn = void (*)(FewArgs);
-template <int KIND, bool W, int MODE>
-FewFn expert_fn(bool xb, int q) {
-  if (q == 1) return xb ? k_few<KIND, true, false, W, 1, MODE> : k_few<KIND, false, false, W, 1, MODE>;
-  return xb ? k_few<KIND, true, false, W, 2, MODE> : k_few<KIND, false, false, W, 2, MODE>;
-}
-template <int MODE>
-FewFn expert_fn(int kind, bool xb, bool whole, int q) {
-  switch (kind) {
-    case F_MX4: return whole ? expert_fn<F_MX4, true, MODE>(xb, q) : expert_fn<F_MX4, false, MODE>(xb, q);
-    case F_AFF4: return whole ? expert_fn<F_AFF4, true, MODE>(xb, q) : expert_fn<F_AFF4, false, MODE>(xb, q);
-    case F_AFF4H: return whole ? expert_fn<F_AFF4H, true, MODE>(xb, q) : expert_fn<F_AFF4H, false, MODE>(xb, q);
-    case F_Q4K: return whole ? expert_fn<F_Q4K, true, MODE>(xb, q) : expert_fn<F_Q4K, false, MODE>(xb, q);
-    default: return whole ? expert_fn<F_SYM4, true, MODE>(xb, q) : expert_fn<F_SYM4, false, MODE>(xb, q);
-  }
-}
 // Quads of tokens per pass.
 int quads(int64_t M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
 
-template <int MODE, bool XB, bool XM, bool W>
+template <int MODE, bool XB, bool W>
 FewFn mx_fn(int64_t M) {
   const int q = quads(M);
-  return q == 1 ? k_few<F_MX4, XB, XM, W, 1, MODE> : q == 2 ? k_few<F_MX4, XB, XM, W, 2, MODE> : k_few<F_MX4, XB, XM, W, 4, MODE>;
+  return q == 1 ? k_few<F_MX4, XB, W, 1, MODE> : q == 2 ? k_few<F_MX4, XB, W, 2, MODE> : k_few<F_MX4, XB, W, 4, MODE>;
 }
 template <int MODE>
 FewFn mx_fn(bool xb, bool whole, int64_t M) {
-  if (whole) return xb ? mx_fn<MODE, true, false, true>(M) : mx_fn<MODE, false, false, true>(M);
-  return xb ? mx_fn<MODE, true, false, false>(M) : mx_fn<MODE, false, false, false>(M);
+  if (whole) return xb ? mx_fn<MODE, true, true>(M) : mx_fn<MODE, false, true>(M);
+  return xb ? mx_fn<MODE, true, false>(M) : mx_fn<MODE, false, false>(M);
 }
 
 }  // namespace
@@ -992,24 +33,6 @@ hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bu
   a.bdt = xdt;
   const int64_t per = 4 * quads(M);
   hipLaunchKernelGGL(mx_fn<FM_LINEAR>(xdt == BF16, a.x_lds > 0, M), dim3((unsigned)(a.tiles * ((M + per - 1) / per))),
-                     dim3(256), lds, s, a);
-  return hipGetLastError();
-}
-
-hipError_t launch_few_mx(const Desc& d, const void* xq, const void* xs, int64_t M, const Bufs& b,
-                         const float* bias, void* y, int ydt, hipStream_t s) {
-  FewArgs a{};
-  const size_t lds = fill(d, d.N, (M + 4 * quads(M) - 1) / (4 * quads(M)), false, quads(M), 0, a);
-  a.w[0] = a.w[1] = b;
-  a.x = xq;
-  a.xsc = xs;
-  a.M = M;
-  a.y = y;
-  a.ydt = ydt;
-  a.bias[0] = bias;
-  a.bdt = F32;
-  const int64_t per = 4 * quads(M);
-  hipLaunchKernelGGL((mx_fn<FM_LINEAR, true, true, false>(M)), dim3((unsigned)(a.tiles * ((M + per - 1) / per))),
                      dim3(256), lds, s, a);
   return hipGetLastError();
 }
@@ -1038,65 +61,6 @@ hipError_t launch_few_gated(const Desc& d, const GatedArgs& g, hipStream_t s) {
 bool few_fits(const Desc& d, bool pair) {
   FewArgs a{};
   return fill(d, 16, 1, pair, 1, 0, a) <= 112 * 1024;
-}
-bool moe_format(const Desc& d) { return few_kind(d) >= 0; }
-int moe_max_tokens() { return kTok; }
-int moe_max_experts() { return kExperts; }
-int moe_max_topk() { return kSlots; }
-
-namespace {
-size_t round16(size_t n) { return (n + 15) / 16 * 16; }
-}  // namespace
-
-// h (16 bits) and the partial sums, [M topk] rows each, then the logits.
-size_t moe_workspace_bytes(int64_t M, int topk, int E, int64_t K, int64_t inner) {
-  return round16((size_t)M * topk * (size_t)inner * 2) + round16((size_t)M * topk * (size_t)K * 4) +
-         round16((size_t)M * E * 8);
-}
-
-hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStream_t s) {
-  const int64_t inner = down.K, K = up.K;
-  unsigned char* ws = static_cast<unsigned char*>(m.ws);
-  void* h = ws;
-  float* part = reinterpret_cast<float*>(ws + round16((size_t)m.M * m.topk * (size_t)inner * 2));
-  double* logits = reinterpret_cast<double*>(reinterpret_cast<unsigned char*>(part) +
-                                             round16((size_t)m.M * m.topk * (size_t)K * 4));
-  const bool xb = m.xdt == BF16;
-  if (m.router) {
-    RouteArgs r{static_cast<const uint16_t*>(m.x), static_cast<const uint16_t*>(m.router), m.M, K, m.E,
-                m.topk, m.score, m.norm, logits, m.ids, m.weights};
-    if ((int64_t)m.E * K <= (int64_t(1) << 17)) {
-      hipLaunchKernelGGL((xb ? k_route<true> : k_route<false>), dim3((unsigned)m.M), dim3(1024), 0, s, r);
-    } else {
-      hipLaunchKernelGGL((xb ? k_logits<true> : k_logits<false>), dim3((unsigned)((m.E + 3) / 4), (unsigned)m.M),
-                         dim3(256), 0, s, r);
-      hipLaunchKernelGGL(k_choose, dim3((unsigned)m.M), dim3(256), 0, s, r);
-    }
-  }
-  const int64_t most = m.M * m.topk < m.E ? m.M * m.topk : m.E;
-  // up to four tokens: the form that holds one quad, in fewer registers
-  const int q = m.M <= 4 ? 1 : 2, tokens = (int)(m.M < 4 * q ? m.M : 4 * q);
-  FewArgs a{};
-  size_t lds = fill(up, inner, most, true, q, tokens, a);
-  a.w[0] = m.gate;
-  a.w[1] = m.up;
-  a.x = m.x;
-  a.M = m.M;
-  a.y = h;
-  a.ydt = m.xdt;
-  a.act = m.act;
-  a.ids = m.ids;
-  a.E = m.E;
-  a.topk = m.topk;
-  hipLaunchKernelGGL(expert_fn<FM_UP>(few_kind(up), xb, a.x_lds > 0, q), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
-  lds = fill(down, K, most, false, q, tokens, a);
-  a.w[0] = a.w[1] = m.down;
-  a.x = h;
-  a.y = part;
-  hipLaunchKernelGGL(expert_fn<FM_DOWN>(few_kind(down), xb, a.x_lds > 0, q), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
-  hipLaunchKernelGGL(k_combine, dim3((unsigned)((K + 1023) / 1024), (unsigned)m.M), dim3(256), 0, s, part, m.ids,
-                     m.weights, m.E, m.topk, K, m.y, m.ydt);
-  return hipGetLastError();
 }
 
 }  // namespace qp

@@ -419,12 +419,21 @@ hipError_t launch_mx_dequant(const Desc& d, const Bufs& b, void* out, int odt, h
   return hipGetLastError();
 }
 
+namespace {
+int mx_width(int64_t M) { return M <= 64 ? 1 : M <= 128 ? 2 : 4; }   // MW
+}  // namespace
+
+int64_t mx_tiles(const Desc& d, int64_t M) {
+  const int rows = 64 * mx_width(M);
+  return (M + rows - 1) / rows * ((d.N + kMxN - 1) / kMxN);
+}
+
 hipError_t launch_mx_mx(const Desc& d, const void* xq, const void* xs, int64_t M, const Bufs& b,
                         const float* bias, void* y, int ydt, hipStream_t s) {
   MxArgs a{static_cast<const unsigned char*>(xq), static_cast<const unsigned char*>(xs),
            static_cast<const unsigned char*>(b.qweight), static_cast<const unsigned char*>(b.scales),
            bias, y, M, d.N, d.K, ydt, 0, 0};
-  const int mw = M <= 64 ? 1 : M <= 128 ? 2 : 4;
+  const int mw = mx_width(M);
   a.tilesM = (int)((M + 64 * mw - 1) / (64 * mw));
   a.tilesN = (int)((d.N + kMxN - 1) / kMxN);
   auto fn = mw == 1 ? k_mxmx<1> : mw == 2 ? k_mxmx<2> : k_mxmx<4>;

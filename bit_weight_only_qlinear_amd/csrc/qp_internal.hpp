@@ -161,9 +161,6 @@ hipError_t launch_dx(const Desc& d, const DxArgs& a, hipStream_t s);
 hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bufs& b,
                       const void* bias, void* y, int ydt, hipStream_t s);
 hipError_t launch_few_gated(const Desc& d, const GatedArgs& a, hipStream_t s);
-// The same for MXFP4 activations (codes xq, scales xs).
-hipError_t launch_few_mx(const Desc& d, const void* xq, const void* xs, int64_t M, const Bufs& b,
-                         const float* bias, void* y, int ydt, hipStream_t s);
 
 // A mixture-of-experts layer for few tokens (few.hip): experts stacked along
 // the rows of `up` (E * inner rows, gate alike) and `down` (E * K rows).
@@ -187,10 +184,15 @@ size_t moe_workspace_bytes(int64_t M, int topk, int E, int64_t K, int64_t inner)
 hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStream_t s);
 
 // MXFP4 rows from fp16, bf16 or fp32 ones, and back; products of two MXFP4
-// operands on the scaled matrix cores, K % 128 == 0 (mx.hip).
+// operands on the scaled matrix cores, for few rows of X and any K (mx_few.hip) or
+// in tiles and K % 128 == 0 (mx.hip).
 hipError_t launch_mx_dequant(const Desc& d, const Bufs& b, void* out, int odt, hipStream_t st);
 hipError_t launch_mx_quant(const void* x, int xdt, int64_t M, int64_t K, void* q, void* s,
                            hipStream_t st);
+bool mx_few_fits(const Desc& d, int64_t M);   // rows short enough for launch_mx_few
+hipError_t launch_mx_few(const Desc& d, const void* xq, const void* xs, int64_t M, const Bufs& b,
+                         const float* bias, void* y, int ydt, hipStream_t s);
+int64_t mx_tiles(const Desc& d, int64_t M);      // blocks of launch_mx_mx
 hipError_t launch_mx_mx(const Desc& d, const void* xq, const void* xs, int64_t M, const Bufs& b,
                         const float* bias, void* y, int ydt, hipStream_t s);
 

@@ -518,10 +518,10 @@ qp_status qpack_quantize_activations_mx(const void* x, int32_t x_dtype, int64_t 
 
 /* y [M, N] (QP_F16, QP_BF16 or QP_F32) = X W^T (+ bias [N], fp32, or NULL)
  * for MXFP4 activations (xq, xs) and MXFP4 weights; fp32 sums of exact
- * products, rounded once.  Up to 16 rows, and at any M where K % 128 != 0: the
- * few-row kernel (K <= 114688; scales of X between 2^-126 and 2^125, which
- * finite rows' are); otherwise the scaled matrix cores (K <= 2^20).  A row with a scale
- * of 255 gives NaN in its outputs alone.  Limits as the MLP block's products;
+ * products on the scaled matrix cores, rounded once.  Rows whose scales fit LDS
+ * (K <= 94208 up to 16 rows of X, 62464 up to 32, 30720 beyond) may have any K
+ * and M; longer ones need K % 128 == 0 and K <= 2^20.  A row with a scale of 255
+ * gives NaN in its outputs alone.  Limits as the MLP block's products;
  * outputs reach into no other buffer (QP_EINVAL). */
 qp_status qlinear_forward_mx(const qp_desc* d, const void* xq, const void* xs, int64_t M,
                              const qp_weights* w, const float* bias, void* y, int32_t y_dtype,

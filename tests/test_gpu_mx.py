@@ -254,6 +254,55 @@ def test_mx_times_mx_is_exact_on_small_numbers(q):
         assert np.array_equal(f64(y), mx.dequantize(x, xs) @ mx.dequantize(w, ws).T)
 
 
+# Beyond 64 rows and 32 tiles of 64, 128 or 256 x 256 outputs, or where the scales of
+# a tile of rows do not fit LDS: the tiled kernel.  K % 128 != 0 never is.
+TILED = [(40, 300, 65536), (100, 8450, 256), (128, 8449, 128), (130, 8500, 384), (600, 4500, 640), (257, 8200, 512)]
+UNTILED = [(130, 70, 96), (200, 33, 32), (70, 8500, 160), (5, 30, 94208), (20, 18, 62464), (40, 17, 30720),
+           (5, 30, 94336), (20, 18, 62592), (40, 17, 30848)]
+
+
+@pytest.mark.parametrize("M,N,K", TILED + UNTILED)
+def test_mx_times_mx_by_size(q, M, N, K):
+    rng = np.random.default_rng(M + 5 * N + K)
+    d, w, w64 = layer(q, rng, N, K, spread=4)
+    xc, xs, x64 = mx_rows(rng, M, K, scale=1.0, spread=4)
+    x = on_gpu(xc, xs)
+    b = rng.normal(size=N).astype(np.float32)
+    tol, product = mxmx_tol(x64, w64), x64 @ w64.T
+    for yd, bias in (("f32", torch.from_numpy(b).cuda()), ("bf16", None)):
+        print("mxmx", M, N, K, yd, flush=True)
+        y = q.qlinear_forward_mx(d, x["qweight"], x["scales"], w, bias=bias, y_dtype=yd)
+        ref = product + (0 if bias is None else b)
+        within(y, ref, tol * (1 + U[yd]) + (U[yd] + 2.0 ** -23) * np.abs(ref) + TINY[yd], yd)
+
+
+def test_mx_times_mx_is_exact_at_every_size(q):
+    """Small numbers as above, where every output tells its place."""
+    rng = np.random.default_rng(18)
+    for M, N, K in ((1, 70, 544), (33, 90, 96), (64, 8300, 512), (65, 100, 160), (100, 8450, 256), (130, 8500, 128),
+                    (600, 4500, 640), (48, 33, 2080)):
+        print("exact", M, N, K, flush=True)
+        w, x = (rng.integers(0, 16, size=(r, K)).astype(np.uint8) for r in (N, M))
+        ws, xs = (rng.integers(125, 130, size=(r, K // 32)).astype(np.uint8) for r in (N, M))
+        t, p = on_gpu(w, ws), on_gpu(x, xs)
+        y = q.qlinear_forward_mx(q.QDesc.mxfp4(N, K), p["qweight"], p["scales"], t, y_dtype="f32")
+        assert np.array_equal(f64(y), mx.dequantize(x, xs) @ mx.dequantize(w, ws).T)
+
+
+def test_nan_blocks_of_tiles_stay_in_their_rows(q):
+    rng = np.random.default_rng(19)
+    for M, N, K in ((130, 8500, 256), (1, 70, 96), (64, 33, 1056)):
+        print("nan", M, N, K, flush=True)
+        c, s, _ = mx_rows(rng, N, K)
+        s[7, K // 32 - 1] = 255
+        xc, xs, _ = mx_rows(rng, M, K)
+        xs[M - 1, 0] = 255
+        x = on_gpu(xc, xs)
+        y = q.qlinear_forward_mx(q.QDesc.mxfp4(N, K), x["qweight"], x["scales"], on_gpu(c, s))
+        bad = torch.isnan(y).cpu().numpy()
+        assert bad[:, 7].all() and bad[M - 1].all() and bad.sum() == M + N - 1
+
+
 # ---------------------------------------------------------------- gated pair and gradients
 @pytest.mark.parametrize("M,N,K,save", [(1, 48, 512, False), (3, 100, 96, False), (8, 33, 4096, False),
                                         (16, 257, 544, False), (5, 70, 96, True), (17, 130, 512, False),

@@ -136,3 +136,11 @@ def test_binding_refuses(q):
                  lambda: q.qmoe_forward(up, down, x, {}, {}, {}, 4, 2, router=x)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_forward_mx_long_rows(q):
+    """Rows whose scales do not fit LDS need whole 128-column steps."""
+    w = q._Weights(FAKE, None, FAKE, None, None)
+    for M, K in ((5, 94240), (20, 62496), (40, 30752), (3000, 30752), (1, (1 << 20) + 128)):
+        assert q.lib.qlinear_forward_mx(ctypes.byref(q.QDesc.mxfp4(8, K).c()), OTHER, WS, M, ctypes.byref(w), None, OUT,
+                                        1, None) == q.QP_EUNSUPPORTED and "K % 128" in _err(q), (M, K, _err(q))
