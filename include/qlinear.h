@@ -519,7 +519,7 @@ qp_status qpack_quantize_activations_mx(const void* x, int32_t x_dtype, int64_t 
 /* y [M, N] (QP_F16, QP_BF16 or QP_F32) = X W^T (+ bias [N], fp32, or NULL)
  * for MXFP4 activations (xq, xs) and MXFP4 weights; fp32 sums of exact
  * products on the scaled matrix cores, rounded once.  Rows whose scales fit LDS
- * (K <= 94208 up to 16 rows of X, 62464 up to 32, 30720 beyond) may have any K
+ * (K <= 95200 up to 16 rows of X, 63456 up to 32, 31200 beyond) may have any K
  * and M; longer ones need K % 128 == 0 and K <= 2^20.  A row with a scale of 255
  * gives NaN in its outputs alone.  Limits as the MLP block's products;
  * outputs reach into no other buffer (QP_EINVAL). */

@@ -257,8 +257,8 @@ def test_mx_times_mx_is_exact_on_small_numbers(q):
 # Beyond 64 rows and 32 tiles of 64, 128 or 256 x 256 outputs, or where the scales of
 # a tile of rows do not fit LDS: the tiled kernel.  K % 128 != 0 never is.
 TILED = [(40, 300, 65536), (100, 8450, 256), (128, 8449, 128), (130, 8500, 384), (600, 4500, 640), (257, 8200, 512)]
-UNTILED = [(130, 70, 96), (200, 33, 32), (70, 8500, 160), (5, 30, 94208), (20, 18, 62464), (40, 17, 30720),
-           (5, 30, 94336), (20, 18, 62592), (40, 17, 30848)]
+UNTILED = [(130, 70, 96), (200, 33, 32), (70, 8500, 160), (5, 30, 95200), (20, 18, 63456), (40, 17, 31200),
+           (5, 30, 95232), (20, 18, 63488), (40, 17, 31232)]
 
 
 @pytest.mark.parametrize("M,N,K", TILED + UNTILED)

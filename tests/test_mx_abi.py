@@ -141,6 +141,6 @@ def test_binding_refuses(q):
 def test_forward_mx_long_rows(q):
     """Rows whose scales do not fit LDS need whole 128-column steps."""
     w = q._Weights(FAKE, None, FAKE, None, None)
-    for M, K in ((5, 94240), (20, 62496), (40, 30752), (3000, 30752), (1, (1 << 20) + 128)):
+    for M, K in ((5, 95264), (20, 63520), (40, 31264), (3000, 31264), (1, (1 << 20) + 128)):
         assert q.lib.qlinear_forward_mx(ctypes.byref(q.QDesc.mxfp4(8, K).c()), OTHER, WS, M, ctypes.byref(w), None, OUT,
                                         1, None) == q.QP_EUNSUPPORTED and "K % 128" in _err(q), (M, K, _err(q))
