@@ -361,8 +361,12 @@ namespace {
 
 enum Use { USE_GEMV, USE_SKINNY, USE_GEMM, USE_FEW };
 
-// Rows up to which MXFP4 products take the few-row kernel.
-constexpr int64_t kFewRows = 16;
+// Rows up to which MXFP4 products take the few-row kernel, and outputs up to
+// which they do at more rows: its time is proportional to M N K, the qGEMM's, 18 us
+// per 1000 columns, starts to depend on M N where its tiles fill the chip.  Few-row
+// and qGEMM: 64 x 4096 x 4096 19 and 77 us, 256 x 4096 x 4096 79 and 80, 128 x 8192 x
+// 8192 133 and 145, 64 x 4096 x 14336 76 and 78, 48 x 5120 x 25600 112 and 95.
+constexpr int64_t kFewRows = 16, kFewOutputs = int64_t(1) << 20;
 constexpr int64_t kMxFewRows = 64, kMxFewTiles = 32;   // both operands MXFP4
 
 // Checks the forward arguments that do not involve a workspace and picks the
@@ -389,7 +393,8 @@ qp_status plan_forward(const qp_desc* d, qp::Desc* dd, int32_t x_dtype, int64_t 
     // One kernel for few rows behind both qGEMV selectors, in tiles of 16
     // rows where K % 64 != 0 keeps more of them from the qGEMM.
     const bool fits = qp::few_fits(*dd, false);
-    *use = kernel == QP_KERNEL_GEMM || (kernel == QP_KERNEL_AUTO && (M > kFewRows || !fits) && gemm_ok(*dd))
+    const bool many = M > kFewRows && M * dd->N > kFewOutputs;
+    *use = kernel == QP_KERNEL_GEMM || (kernel == QP_KERNEL_AUTO && (many || !fits) && gemm_ok(*dd))
                ? USE_GEMM : USE_FEW;
     if (*use == USE_FEW && !fits)
       return fail(QP_EUNSUPPORTED, "MXFP4 rows of K=%lld are too long for the few-row kernel", (long long)dd->K);

@@ -265,7 +265,7 @@ hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStr
   if (m.router) {
     RouteArgs r{static_cast<const uint16_t*>(m.x), static_cast<const uint16_t*>(m.router), m.M, K, m.E,
                 m.topk, m.score, m.norm, logits, m.ids, m.weights};
-    if ((int64_t)m.E * K <= (int64_t(1) << 17)) {
+    if (m.E <= 16) {
       hipLaunchKernelGGL((xb ? k_route<true> : k_route<false>), dim3((unsigned)m.M), dim3(1024), 0, s, r);
     } else {
       hipLaunchKernelGGL((xb ? k_logits<true> : k_logits<false>), dim3((unsigned)((m.E + 3) / 4), (unsigned)m.M),

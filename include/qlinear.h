@@ -140,8 +140,8 @@ typedef enum {
                               activation rows), K % 128 == 0, every buffer
                               < 2 GiB                                         */
   /* MXFP4: both qGEMV selectors mean its few-row kernel, any M (tiles of 16
-     rows, M * N <= 2^34), K <= 114688; AUTO takes it up to 16 rows and where
-     K % 64 != 0, the qGEMM (K <= 2^20) otherwise.                            */
+     rows, M * N <= 2^34), K <= 114688; AUTO takes it up to 16 rows or M * N =
+     2^20 and where K % 64 != 0, the qGEMM (K <= 2^20) otherwise.             */
 } qp_kernel;
 
 typedef struct {

@@ -179,6 +179,37 @@ def test_gemm(q, M, N, K, dt):
         within(y, ref, tol * (1 + U[yd]) + (U[yd] + 2.0 ** -23) * np.abs(ref) + TINY[yd], yd)
 
 
+@pytest.mark.parametrize("M,N,K", [(17, 64, 64), (33, 200, 320), (130, 257, 512), (300, 14, 1024), (64, 70, 16384),
+                                   (260, 300, 4096)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_gemm_by_name(q, M, N, K, dt):
+    rng = np.random.default_rng(M * N + 1)
+    d, w, w64 = layer(q, rng, N, K, spread=2)
+    v = rng.normal(size=(M, K))
+    v[3] = 0
+    if dt == "bf16":
+        v[5] *= 1e20
+    x, x64 = dev(v, dt)
+    tol = product_tolerance(x64, w64.T)
+    ref = x64 @ w64.T
+    for yd in ("f32", dt):
+        y = q.qlinear_forward(d, x, w, y_dtype=yd, kernel=q.QP_KERNEL_GEMM)
+        within(y, ref, tol * (1 + U[yd]) + (U[yd] + 2.0 ** -23) * np.abs(ref) + TINY[yd], yd)
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 300, 512), (70, 1000, 1088), (500, 33, 64), (257, 4080, 128)])
+def test_few_rows_take_many(q, M, N, K):
+    """AUTO up to M N = 2^20: the few-row kernel, in tiles of 16 rows."""
+    rng = np.random.default_rng(M + N)
+    d, w, w64 = layer(q, rng, N, K, spread=3)
+    x, x64 = dev(rng.normal(size=(M, K)), "bf16")
+    assert q.workspace_bytes(d, M) == 0
+    y = q.qlinear_forward(d, x, w, y_dtype="f32")
+    ref = x64 @ w64.T
+    within(y, ref, few_tol(x64, w64) + 2.0 ** -23 * np.abs(ref) + TINY["f32"], "f32")
+    assert torch.equal(y, q.qlinear_forward(d, x, w, y_dtype="f32", kernel=q.QP_KERNEL_GEMV))
+
+
 def test_scales_over_the_range(q):
     """Blocks at both ends of the scale byte, in the exact kernels."""
     N, K = 16, 64

@@ -144,3 +144,11 @@ def test_forward_mx_long_rows(q):
     for M, K in ((5, 95264), (20, 63520), (40, 31264), (3000, 31264), (1, (1 << 20) + 128)):
         assert q.lib.qlinear_forward_mx(ctypes.byref(q.QDesc.mxfp4(8, K).c()), OTHER, WS, M, ctypes.byref(w), None, OUT,
                                         1, None) == q.QP_EUNSUPPORTED and "K % 128" in _err(q), (M, K, _err(q))
+
+
+def test_selector_by_outputs(q):
+    """More rows: the few-row kernel while M N <= 2^20, the qGEMM (a workspace for bf16 rows) beyond."""
+    n = ctypes.c_size_t(7)
+    for M, N, few in ((16, 1 << 20, True), (17, 4096, True), (256, 4096, True), (257, 4096, False), (64, 16385, False)):
+        assert q.lib.qlinear_workspace_bytes(ctypes.byref(q.QDesc.mxfp4(N, 4096).c()), 1, M, q.QP_KERNEL_AUTO,
+                                             ctypes.byref(n)) == 0 and (n.value == 0) == few, (M, N)
