@@ -40,6 +40,7 @@ SOURCES = {
     "moe.hip": [],
     "mx.hip": [],
     "mx_few.hip": [],
+    "mx_rows.hip": [],
 }
 
 

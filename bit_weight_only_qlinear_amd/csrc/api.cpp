@@ -361,12 +361,13 @@ namespace {
 
 enum Use { USE_GEMV, USE_SKINNY, USE_GEMM, USE_FEW };
 
-// Rows up to which MXFP4 products take the few-row kernel, and outputs up to
-// which they do at more rows: its time is proportional to M N K, the qGEMM's, 18 us
-// per 1000 columns, starts to depend on M N where its tiles fill the chip.  Few-row
-// and qGEMM: 64 x 4096 x 4096 19 and 77 us, 256 x 4096 x 4096 79 and 80, 128 x 8192 x
-// 8192 133 and 145, 64 x 4096 x 14336 76 and 78, 48 x 5120 x 25600 112 and 95.
-constexpr int64_t kFewRows = 16, kFewOutputs = int64_t(1) << 20;
+// MXFP4 products: up to 8 rows the few-row kernel, whose codes lie four rows to a
+// load (8 rows of 4096 x 14336 12.8 us, on 16-row matrix instructions 15.6; 16
+// rows 21 and 15, 16 x 8192 x 8192 20 and 16); then those in tiles of 16 to 64
+// rows; the qGEMM, 18 us per 1000 columns where its tiles do not fill the chip,
+// for more than 16 rows and M N = 2^22 (256 x 4096 x 4096 25 and 80 us, 256 x 8192 x 8192 76 and 144, 256
+// x 4096 x 14336 69 and 80, 128 x 5120 x 25600 80 and 97).  Gated pairs: few rows up to 16.
+constexpr int64_t kQuadRows = 8, kFewRows = 16, kFewOutputs = int64_t(1) << 22;
 constexpr int64_t kMxFewRows = 64, kMxFewTiles = 32;   // both operands MXFP4
 
 // Checks the forward arguments that do not involve a workspace and picks the
@@ -536,7 +537,8 @@ qp_status qlinear_forward_ws(const qp_desc* d, const void* x, int32_t x_dtype, i
                           (hipStream_t)stream);
     what = "MFMA qGEMV launch";
   } else if (use == USE_FEW) {
-    e = qp::launch_few(dd, x, x_dtype, M, bufs_of(w), bias, y, y_dtype, (hipStream_t)stream);
+    e = (M > kQuadRows && qp::mx_rows_fits(dd) ? qp::launch_mx_rows : qp::launch_few)(
+        dd, x, x_dtype, M, bufs_of(w), bias, y, y_dtype, (hipStream_t)stream);
     what = "few-row MXFP4 launch";
   } else {
     e = qp::launch_gemv(dd, x, x_dtype, M, bufs_of(w), bias, y, y_dtype, nbytes,

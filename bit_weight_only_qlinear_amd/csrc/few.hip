@@ -4,18 +4,31 @@
 namespace qp {
 namespace {
 
-// Quads of tokens per pass.
-int quads(int64_t M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
+// Quads of tokens per pass.  Products of more than eight rows come here only
+// where their scales are too long for the 16-row kernel's LDS.
+template <int MODE>
+int quads(int64_t M) { return M <= 4 ? 1 : M <= 8 || MODE == FM_LINEAR ? 2 : 4; }
 
 template <int MODE, bool XB, bool W>
-FewFn mx_fn(int64_t M) {
-  const int q = quads(M);
-  return q == 1 ? k_few<F_MX4, XB, W, 1, MODE> : q == 2 ? k_few<F_MX4, XB, W, 2, MODE> : k_few<F_MX4, XB, W, 4, MODE>;
+FewFn mx_fn(int q) {
+  if constexpr (MODE != FM_LINEAR)
+    if (q == 4) return k_few<F_MX4, XB, W, 4, MODE>;
+  return q == 1 ? k_few<F_MX4, XB, W, 1, MODE> : k_few<F_MX4, XB, W, 2, MODE>;
 }
 template <int MODE>
-FewFn mx_fn(bool xb, bool whole, int64_t M) {
-  if (whole) return xb ? mx_fn<MODE, true, true>(M) : mx_fn<MODE, false, true>(M);
-  return xb ? mx_fn<MODE, true, false>(M) : mx_fn<MODE, false, false>(M);
+FewFn mx_fn(bool xb, bool whole, int q) {
+  if (whole) return xb ? mx_fn<MODE, true, true>(q) : mx_fn<MODE, false, true>(q);
+  return xb ? mx_fn<MODE, true, false>(q) : mx_fn<MODE, false, false>(q);
+}
+
+// Sizes and launch of M rows in tiles of 4 q.
+template <int MODE>
+hipError_t launch(const Desc& d, int xdt, FewArgs& a, hipStream_t s) {
+  const int q = quads<MODE>(a.M);
+  const int64_t mt = (a.M + 4 * q - 1) / (4 * q);
+  const size_t lds = fill(d, d.N, mt, is_pair(MODE), q, (int)(a.M < 4 * q ? a.M : 4 * q), a);
+  hipLaunchKernelGGL(mx_fn<MODE>(xdt == BF16, a.x_lds > 0, q), dim3((unsigned)(a.tiles * mt)), dim3(256), lds, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -23,7 +36,6 @@ FewFn mx_fn(bool xb, bool whole, int64_t M) {
 hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bufs& b,
                       const void* bias, void* y, int ydt, hipStream_t s) {
   FewArgs a{};
-  const size_t lds = fill(d, d.N, (M + 4 * quads(M) - 1) / (4 * quads(M)), false, quads(M), (int)(M < 16 ? M : 16), a);
   a.w[0] = a.w[1] = b;
   a.x = x;
   a.M = M;
@@ -31,15 +43,11 @@ hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bu
   a.ydt = ydt;
   a.bias[0] = bias;
   a.bdt = xdt;
-  const int64_t per = 4 * quads(M);
-  hipLaunchKernelGGL(mx_fn<FM_LINEAR>(xdt == BF16, a.x_lds > 0, M), dim3((unsigned)(a.tiles * ((M + per - 1) / per))),
-                     dim3(256), lds, s, a);
-  return hipGetLastError();
+  return launch<FM_LINEAR>(d, xdt, a, s);
 }
 
 hipError_t launch_few_gated(const Desc& d, const GatedArgs& g, hipStream_t s) {
   FewArgs a{};
-  const size_t lds = fill(d, d.N, (g.M + 4 * quads(g.M) - 1) / (4 * quads(g.M)), true, quads(g.M), (int)(g.M < 16 ? g.M : 16), a);
   a.w[0] = g.gate;
   a.w[1] = g.up;
   a.x = g.x;
@@ -50,10 +58,7 @@ hipError_t launch_few_gated(const Desc& d, const GatedArgs& g, hipStream_t s) {
   a.bias[1] = g.bias_u;
   a.bdt = g.xdt;
   a.act = g.act;
-  const int64_t per = 4 * quads(g.M);
-  hipLaunchKernelGGL(mx_fn<FM_GATED>(g.xdt == BF16, a.x_lds > 0, g.M),
-                     dim3((unsigned)(a.tiles * ((g.M + per - 1) / per))), dim3(256), lds, s, a);
-  return hipGetLastError();
+  return launch<FM_GATED>(d, g.xdt, a, s);
 }
 
 // The metadata of a pass's 32 rows has to fit LDS next to the activations of two

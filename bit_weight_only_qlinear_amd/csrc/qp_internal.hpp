@@ -162,7 +162,12 @@ hipError_t launch_few(const Desc& d, const void* x, int xdt, int64_t M, const Bu
                       const void* bias, void* y, int ydt, hipStream_t s);
 hipError_t launch_few_gated(const Desc& d, const GatedArgs& a, hipStream_t s);
 
-// A mixture-of-experts layer for few tokens (few.hip): experts stacked along
+// MXFP4 layers and more than a few rows, on exact codes too (mx_rows.hip).
+bool mx_rows_fits(const Desc& d);
+hipError_t launch_mx_rows(const Desc& d, const void* x, int xdt, int64_t M, const Bufs& b,
+                          const void* bias, void* y, int ydt, hipStream_t s);
+
+// A mixture-of-experts layer for few tokens (moe.hip): experts stacked along
 // the rows of `up` (E * inner rows, gate alike) and `down` (E * K rows).
 struct MoeArgs {
   const void* x;

@@ -139,9 +139,9 @@ typedef enum {
   QP_KERNEL_GEMV_MFMA = 3  /* MFMA qGEMV on exact codes, any M (tiles of 16
                               activation rows), K % 128 == 0, every buffer
                               < 2 GiB                                         */
-  /* MXFP4: both qGEMV selectors mean its few-row kernel, any M (tiles of 16
-     rows, M * N <= 2^34), K <= 114688; AUTO takes it up to 16 rows or M * N =
-     2^20 and where K % 64 != 0, the qGEMM (K <= 2^20) otherwise.             */
+  /* MXFP4: both qGEMV selectors mean its kernels on exact codes, any M (M * N
+     <= 2^34), K <= 114688; AUTO takes them up to 16 rows or M * N = 2^22 and
+     where K % 64 != 0, the qGEMM (K <= 2^20) otherwise.                      */
 } qp_kernel;
 
 typedef struct {

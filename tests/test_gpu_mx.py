@@ -152,9 +152,9 @@ def test_few_rows(q, M, N, K, dt):
         within(y, ref, tol * (1 + U[yd]) + (U[yd] + 2.0 ** -23) * np.abs(ref) + TINY[yd], yd)
         if M <= 16 or K % 64:
             assert torch.equal(y, q.qlinear_forward(d, x, w, bias=bias, y_dtype=yd))
-    # rows do not depend on how many there are
-    one = q.qlinear_forward(d, x[M - 1:].contiguous(), w, y_dtype="f32", kernel=q.QP_KERNEL_GEMV_MFMA)
-    assert torch.equal(one[0], q.qlinear_forward(d, x, w, y_dtype="f32", kernel=q.QP_KERNEL_GEMV)[-1])
+    # both selectors
+    assert torch.equal(q.qlinear_forward(d, x, w, y_dtype="f32", kernel=q.QP_KERNEL_GEMV_MFMA),
+                       q.qlinear_forward(d, x, w, y_dtype="f32", kernel=q.QP_KERNEL_GEMV))
 
 
 @pytest.mark.parametrize("M,N,K", [(17, 64, 64), (33, 200, 320), (130, 257, 512), (300, 14, 1024), (64, 70, 16384),
@@ -197,12 +197,15 @@ def test_gemm_by_name(q, M, N, K, dt):
         within(y, ref, tol * (1 + U[yd]) + (U[yd] + 2.0 ** -23) * np.abs(ref) + TINY[yd], yd)
 
 
-@pytest.mark.parametrize("M,N,K", [(17, 300, 512), (70, 1000, 1088), (500, 33, 64), (257, 4080, 128)])
-def test_few_rows_take_many(q, M, N, K):
-    """AUTO up to M N = 2^20: the few-row kernel, in tiles of 16 rows."""
+@pytest.mark.parametrize("M,N,K", [(17, 300, 512), (70, 1000, 1088), (500, 33, 64), (257, 8200, 128), (9, 8300, 192),
+                                   (33, 8250, 320), (16, 20, 94144), (13, 20, 98304), (40, 24, 30784), (64, 70, 14336),
+                                   (9, 1, 64), (64, 16, 4096), (1000, 4096, 256), (100, 9000, 608)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_few_rows_take_many(q, M, N, K, dt):
+    """AUTO up to M N = 2^22: exact codes, in tiles of 16 to 64 rows."""
     rng = np.random.default_rng(M + N)
     d, w, w64 = layer(q, rng, N, K, spread=3)
-    x, x64 = dev(rng.normal(size=(M, K)), "bf16")
+    x, x64 = dev(rng.normal(size=(M, K)), dt)
     assert q.workspace_bytes(d, M) == 0
     y = q.qlinear_forward(d, x, w, y_dtype="f32")
     ref = x64 @ w64.T

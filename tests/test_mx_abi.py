@@ -147,8 +147,8 @@ def test_forward_mx_long_rows(q):
 
 
 def test_selector_by_outputs(q):
-    """More rows: the few-row kernel while M N <= 2^20, the qGEMM (a workspace for bf16 rows) beyond."""
+    """More rows: the kernels on exact codes while M N <= 2^22, the qGEMM (a workspace for bf16 rows) beyond."""
     n = ctypes.c_size_t(7)
-    for M, N, few in ((16, 1 << 20, True), (17, 4096, True), (256, 4096, True), (257, 4096, False), (64, 16385, False)):
+    for M, N, few in ((16, 1 << 20, True), (17, 4096, True), (1024, 4096, True), (1025, 4096, False), (64, 65537, False)):
         assert q.lib.qlinear_workspace_bytes(ctypes.byref(q.QDesc.mxfp4(N, 4096).c()), 1, M, q.QP_KERNEL_AUTO,
                                              ctypes.byref(n)) == 0 and (n.value == 0) == few, (M, N)
