@@ -24,9 +24,14 @@ FewFn mx_fn(bool xb, bool whole, int q) {
 // Sizes and launch of M rows in tiles of 4 q.
 template <int MODE>
 hipError_t launch(const Desc& d, int xdt, FewArgs& a, hipStream_t s) {
-  const int q = quads<MODE>(a.M);
-  const int64_t mt = (a.M + 4 * q - 1) / (4 * q);
-  const size_t lds = fill(d, d.N, mt, is_pair(MODE), q, (int)(a.M < 4 * q ? a.M : 4 * q), a);
+  int q = quads<MODE>(a.M);
+  int64_t mt;
+  size_t lds;
+  for (;; q = 2) {   // a step of 16 rows takes 64 KiB of LDS: long rows in tiles of eight
+    mt = (a.M + 4 * q - 1) / (4 * q);
+    lds = fill(d, d.N, mt, is_pair(MODE), q, (int)(a.M < 4 * q ? a.M : 4 * q), a);
+    if (q < 4 || a.x_lds || lds <= 80 * 1024) break;
+  }
   hipLaunchKernelGGL(mx_fn<MODE>(xdt == BF16, a.x_lds > 0, q), dim3((unsigned)(a.tiles * mt)), dim3(256), lds, s, a);
   return hipGetLastError();
 }
@@ -61,8 +66,8 @@ hipError_t launch_few_gated(const Desc& d, const GatedArgs& g, hipStream_t s) {
   return launch<FM_GATED>(d, g.xdt, a, s);
 }
 
-// The metadata of a pass's 32 rows has to fit LDS next to the activations of two
-// steps and the sums.
+// The metadata of a pass's 32 rows has to fit LDS next to a step of eight rows of
+// x (32 KiB), the sums and an expert's lists.
 bool few_fits(const Desc& d, bool pair) {
   FewArgs a{};
   return fill(d, 16, 1, pair, 1, 0, a) <= 112 * 1024;

@@ -1,5 +1,5 @@
-// Packed products for few activation rows: the MXFP4 qGEMV and gated pair of
-// up to 16 rows, and the two products of a mixture-of-experts layer, whose
+// Packed products for few activation rows: the MXFP4 qGEMV of up to 8 rows, its
+// gated pair of up to 16, and the two products of a mixture-of-experts layer, whose
 // experts' rows lie one after the other in the packed buffers.
 //
 // All of them are bound by the codes' way from HBM, so the arithmetic has to
@@ -29,6 +29,11 @@
 // features of it); every block finds its expert and the expert's tokens from
 // the ids by itself, in LDS.  Grids cover as many experts as the tokens could
 // reach; blocks past the ones that are end at once.
+//
+// 1 x 4096 x 14336: 10.2 us, 3.1 TB/s of which 4 us are the launch, the metadata
+// and the first codes.  Experts: 2 of 8 of 4096 x 14336 int4 32 + 17 us (4.1 TB/s),
+// 64 of 2048 x 1024 MXFP4 with 2 tokens each 33 + 23 (3.8), 32 of 4096 x 1536 with
+// 6 each 61 + 37 (3.3; the tokens beyond eight read their expert again).
 #pragma once
 #include "device_common.hpp"
 #include "mlp_common.hpp"

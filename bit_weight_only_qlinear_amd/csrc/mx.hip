@@ -29,6 +29,7 @@ __device__ __forceinline__ float e8m0(uint32_t s) {
 // which divides by the scale, rounds to the nearest code (ties to even) and
 // stops at 6; blocks whose scale is below 2^-64 are taken times 2^64 first
 // (exact), so that neither the values nor the scale are subnormal.
+// 2048 x 14336 bf16: 14.2 us, 5.2 TB/s (a copy's rate); back: 12.9.
 template <int DT>
 __global__ void __launch_bounds__(256) k_mx_quant(const void* __restrict__ x, uint32_t* __restrict__ q,
                                                   uint8_t* __restrict__ s, int64_t n8) {
@@ -122,8 +123,11 @@ unsigned mx_blocks(int64_t n8) {
 //  * A row's 16-byte chunk c lies at c ^ (row / 4 % 4) of its 64 bytes: the 16
 //    lanes of a read phase, 16 rows of one chunk, then touch every bank once.
 //  * Scales: 16 bytes per row for four steps (a dword per step and row touches
-//    a line for each four bytes).  A lane's operand is its row's dword, shifted so that its half's
-//    bytes are where the instruction's byte select expects them.
+//    a line for each four bytes).  A lane's operand is its row's dword, shifted
+//    so that its half's bytes are where the instruction's byte select expects
+//    them.
+// 2048 x 4096 x 14336: 72.6 us, 3.3 PFLOP/s; of the 72, 32 are the matrix
+// instructions alone (18 ns per instruction and SIMD), 11 the stores of 59 MB.
 struct MxArgs {
   const unsigned char* xq;
   const unsigned char* xs;

@@ -73,6 +73,8 @@ __device__ __forceinline__ float e8m0(uint32_t s) {
 //    per column against 8 G of codes); G = 1 where that leaves too few waves.
 //  * KW waves share rows and add up through LDS at the end.  Scale bytes of the
 //    block's rows are copied to LDS first.
+// 13 x 8192 x 8192: 16.2 us, 2.2 TB/s of codes: 256 blocks of four waves with four
+// steps each way from L2 in front; 64 x 4096 x 14336 23 us, 326 TFLOP/s.
 template <bool XB, int G, int T, int NS>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) k_mx_rows(RowsArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];

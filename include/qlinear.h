@@ -555,8 +555,8 @@ qp_status qmoe_workspace_bytes(const qp_desc* d_up, const qp_desc* d_down, int64
  *     [0, experts) names no expert (one that another GPU holds, say) and adds
  *     nothing; a token may name an expert twice; score and norm are unused.
  *     A token without experts gives zeros.
- * Every weight matrix of an expert that some token takes is read once per 16
- * of its tokens.  Exact codes, fp32 sums; the inner activations are rounded
+ * Every weight matrix of an expert that some token takes is read once per 8
+ * of its tokens (4 where M <= 4).  Exact codes, fp32 sums; the inner activations are rounded
  * to x_dtype, everything else once at the end; results do not depend on
  * timing, nor a token's on the other tokens.  Limits: M <= 64, experts <= 512,
  * topk <= 16, M * topk * max(K, inner) < 2^29, and rows 32 of whose metadata fit

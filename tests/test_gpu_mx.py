@@ -365,6 +365,21 @@ def test_gated(q, M, N, K, save, kind):
                 assert np.all(np.abs(got - v) <= (0.5 + 1e-4) * step + t)
 
 
+@pytest.mark.parametrize("M,N,K", [(13, 20, 98304), (9, 18, 114688), (16, 20, 65568), (5, 17, 114688)])
+def test_gated_long_rows(q, M, N, K):
+    """Scales that leave no room for a step of 16 rows in LDS: tiles of eight."""
+    rng = np.random.default_rng(M + N)
+    (d, bg, wg), (_, bu, wu) = layer(q, rng, N, K), layer(q, rng, N, K)
+    x, x64 = dev(rng.normal(size=(M, K)) * 0.05, "bf16")
+    print("gated", M, N, K, flush=True)
+    o = q.qlinear_gated_forward(d, x, bg, bu, act="silu", h_dtype="f32")
+    none = np.zeros(N)
+    g, u, h = mlp.gated(x64, wg, wu, none, none, "silu")
+    dg, du = few_tol(x64, wg) + 2.0 ** -22 * np.abs(g), few_tol(x64, wu) + 2.0 ** -22 * np.abs(u)
+    tol = 1.13 * dg * (np.abs(u) + du) + np.abs(mlp.act(g, "silu")[0]) * du + (U["f32"] + 2.0 ** -17) * np.abs(h) + TINY["f32"]
+    within(o.h, h, tol, "h")
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 48, 256), (3, 100, 512), (17, 1, 96), (64, 63, 320), (130, 257, 512),
                                    (300, 192, 96), (5, 1000, 160), (260, 640, 320)])
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
