@@ -140,7 +140,7 @@ typedef enum {
                               activation rows), K % 128 == 0, every buffer
                               < 2 GiB                                         */
   /* MXFP4: both qGEMV selectors mean its kernels on exact codes, any M (M * N
-     <= 2^34), K <= 114688; AUTO takes them up to 16 rows or M * N = 2^22 and
+     <= 2^34), K <= 114656; AUTO takes them up to 16 rows or M * N = 2^22 and
      where K % 64 != 0, the qGEMM (K <= 2^20) otherwise.                      */
 } qp_kernel;
 
@@ -560,8 +560,8 @@ qp_status qmoe_workspace_bytes(const qp_desc* d_up, const qp_desc* d_down, int64
  * to x_dtype, everything else once at the end; results do not depend on
  * timing, nor a token's on the other tokens.  Limits: M <= 64, experts <= 512,
  * topk <= 16, M * topk * max(K, inner) < 2^29, and rows 32 of whose metadata fit
- * 112 KiB (K and inner <= 28672 for AFFINE of group size 32 and SYM4 of 32,
- * 57344 for groups of 64 and Q4K, 114688 for MXFP4).  The workspace
+ * 112 KiB (K and inner <= 28640 for groups of 32 of AFFINE and SYM4, 57280 of
+ * 64, 114560 of 128, 44800 for Q4K, 114656 for MXFP4).  The workspace
  * (qmoe_workspace_bytes, 16-byte aligned) is busy until the call's kernels
  * finish; buffers and errors as the MLP block's entry points. */
 qp_status qmoe_forward(const qp_desc* d_up, const qp_desc* d_down, int32_t experts, int32_t topk,

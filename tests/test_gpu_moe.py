@@ -106,6 +106,11 @@ CASES = [  # M, E, topk, K, inner, up format, down format, dt, y, act, score, no
     (6, 300, 5, 128, 64, "affine64.bf16", "sym4", "f16", "f32", "gelu_tanh", "sigmoid", True),
     (1, 2, 2, 256, 24576, "affine32.bf16", "affine32.bf16", "bf16", "f32", "silu", "softmax", True),
     (1, 2, 2, 20480, 64, "affine32.bf16", "mxfp4", "bf16", "f32", "silu", "softmax", True),
+    (5, 1, 1, 114656, 32, "mxfp4", "mxfp4", "bf16", "f32", "silu", "softmax", True),
+    (5, 1, 1, 32, 114656, "mxfp4", "mxfp4", "f16", "f32", "silu", "softmax", True),
+    (6, 1, 1, 44800, 64, "q4k", "mxfp4", "bf16", "f32", "silu", "softmax", True),
+    (6, 1, 1, 64, 28640, "mxfp4", "affine32.bf16", "bf16", "f32", "silu", "softmax", True),
+    (5, 1, 1, 28640, 32, "affine32.f16", "mxfp4", "f16", "f32", "silu", "softmax", True),
 ]
 
 

@@ -199,7 +199,7 @@ def test_gemm_by_name(q, M, N, K, dt):
 
 @pytest.mark.parametrize("M,N,K", [(17, 300, 512), (70, 1000, 1088), (500, 33, 64), (257, 8200, 128), (9, 8300, 192),
                                    (33, 8250, 320), (16, 20, 94144), (13, 20, 98304), (40, 24, 30784), (64, 70, 14336),
-                                   (9, 1, 64), (64, 16, 4096), (1000, 4096, 256), (100, 9000, 608)])
+                                   (9, 1, 64), (64, 16, 4096), (13, 40, 114656), (3, 40, 114656), (1000, 4096, 256), (100, 9000, 608)])
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_few_rows_take_many(q, M, N, K, dt):
     """AUTO up to M N = 2^22: exact codes, in tiles of 16 to 64 rows."""
@@ -365,7 +365,8 @@ def test_gated(q, M, N, K, save, kind):
                 assert np.all(np.abs(got - v) <= (0.5 + 1e-4) * step + t)
 
 
-@pytest.mark.parametrize("M,N,K", [(13, 20, 98304), (9, 18, 114688), (16, 20, 65568), (5, 17, 114688)])
+@pytest.mark.parametrize("M,N,K", [(13, 20, 98304), (9, 18, 114656), (16, 20, 65568), (5, 17, 114656),
+                                   (1, 17, 114656), (9, 18, 114688)])
 def test_gated_long_rows(q, M, N, K):
     """Scales that leave no room for a step of 16 rows in LDS: tiles of eight."""
     rng = np.random.default_rng(M + N)
@@ -530,6 +531,43 @@ def test_offsets_past_32_bits(q):
     y = q.qlinear_forward_mx(s, *a, few)                      # 2.8e9 outputs
     z = q.qlinear_forward_mx(s, *b, few)
     assert torch.equal(y[-300:], z)
+
+
+@pytest.mark.parametrize("M,N", [(9, 21), (13, 70), (33, 35), (64, 18), (40, 130), (100, 8451)])
+def test_outputs_stay_inside_by_size(q, M, N):
+    rng = np.random.default_rng(M)
+    K = 160 if N < 1000 else 128
+    d, w, _ = layer(q, rng, N, K)
+    x, _ = dev(rng.normal(size=(M, K)), "f16")
+    xq, xs = q.quantize_activations_mx(x)
+    for dt, yd in ((torch.float16, "f16"), (torch.float32, "f32")):
+        t = torch.full((M * N + 4096,), 77, dtype=dt, device="cuda")
+        for f in (lambda o: q.qlinear_forward_mx(d, xq, xs, w, y_dtype=yd, out=o),
+                  lambda o: q.qlinear_forward(d, x, w, y_dtype=yd, kernel=q.QP_KERNEL_GEMV, out=o)):
+            t.fill_(77)
+            f(t[:M * N].view(M, N))
+            assert torch.all(t[M * N:] == 77) and not torch.any(t[:M * N] == 77)
+
+
+def test_weights_past_32_bits(q):
+    """Codes of more than 2^32 bytes: the last rows against the same rows alone (small
+    numbers, whose sums are exact in any order)."""
+    N, K, n = 560000, 16384, 50
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    codes = torch.randint(-2 ** 31, 2 ** 31, (N, K // 8), dtype=torch.int32, device="cuda", generator=g)
+    scales = torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda")
+    w, last = dict(qweight=codes, scales=scales), dict(qweight=codes[-n:], scales=scales[-n:])
+    d, e = q.QDesc.mxfp4(N, K), q.QDesc.mxfp4(n, K)
+    for M in (1, 6, 9, 33, 70):
+        print("weights", M, flush=True)
+        x = torch.randint(-2, 3, (M, K), device="cuda", generator=g).bfloat16()
+        y = q.qlinear_forward(d, x, w, y_dtype="f32", kernel=q.QP_KERNEL_GEMV)
+        assert torch.equal(y[:, -n:], q.qlinear_forward(e, x, last, y_dtype="f32", kernel=q.QP_KERNEL_GEMV))
+        a = torch.randint(-2 ** 31, 2 ** 31, (M, K // 8), dtype=torch.int32, device="cuda", generator=g)
+        b = torch.full((M, K // 32), 127, dtype=torch.uint8, device="cuda")
+        y = q.qlinear_forward_mx(d, a, b, w, y_dtype="f32")
+        assert torch.equal(y[:, -n:], q.qlinear_forward_mx(e, a, b, last, y_dtype="f32"))
 
 
 def test_binding_refuses_wrong_tensors(q):

@@ -152,3 +152,22 @@ def test_selector_by_outputs(q):
     for M, N, few in ((16, 1 << 20, True), (17, 4096, True), (1024, 4096, True), (1025, 4096, False), (64, 65537, False)):
         assert q.lib.qlinear_workspace_bytes(ctypes.byref(q.QDesc.mxfp4(N, 4096).c()), 1, M, q.QP_KERNEL_AUTO,
                                              ctypes.byref(n)) == 0 and (n.value == 0) == few, (M, N)
+
+
+def test_longest_rows(q):
+    """The longest rows of each format whose metadata fits LDS, and the next."""
+    n = ctypes.c_size_t()
+
+    def moe(up, down):
+        return q.lib.qmoe_workspace_bytes(ctypes.byref(up.c()), ctypes.byref(down.c()), 64, 1, 1, ctypes.byref(n))
+    for make, K, step in ((q.QDesc.mxfp4, 114656, 32), (lambda N, K: q.QDesc.affine(N, K, 4, 32), 28640, 32),
+                          (lambda N, K: q.QDesc.affine(N, K, 4, 64), 57280, 64),
+                          (lambda N, K: q.QDesc.affine(N, K, 4, 128), 114560, 128), (q.QDesc.q4k, 44800, 256),
+                          (lambda N, K: q.QDesc.sym4(N, K, 32), 28640, 32)):
+        for k, ok in ((K, True), (K + step, False)):
+            assert (moe(make(64, k), q.QDesc.mxfp4(k, 64)) == 0) == ok, (make(64, k), _err(q))
+            assert (moe(q.QDesc.mxfp4(k, 64), make(64, k)) == 0) == ok, (make(64, k), _err(q))
+    w = q._Weights(FAKE, None, FAKE, None, None)
+    for M in (1, 9, 40):
+        assert q.lib.qlinear_forward_kernel(ctypes.byref(q.QDesc.mxfp4(8, 114688).c()), FAKE, 1, M, ctypes.byref(w), None,
+                                            OUT, 1, q.QP_KERNEL_GEMV, None) == q.QP_EUNSUPPORTED and "long" in _err(q)
