@@ -25,10 +25,11 @@
 // in LDS.  The metadata of the block's rows is staged in LDS by direct loads,
 // in front of the first codes.
 //
-// Experts: a block's unit is (a-th expert that some token chose, 16 rows or
-// features of it); every block finds its expert and the expert's tokens from
-// the ids by itself, in LDS.  Grids cover as many experts as the tokens could
-// reach; blocks past the ones that are end at once.
+// Experts: a block's unit is (an expert that some token chose, 4 Q of its tokens,
+// some of its rows or features); every block finds its own from the ids, in LDS.
+// Grids cover as many as the tokens could need; blocks past the ones that are end
+// at once.  (An expert's tokens one after the other in one block: 22 tokens of
+// 2 experts of 736 x 1568 42 us instead of 27, 50 x 4096 x 1536 105 and 100.)
 //
 // 1 x 4096 x 14336: 10.2 us, 3.1 TB/s of which 4 us are the launch, the metadata
 // and the first codes.  Experts: 2 of 8 of 4096 x 14336 int4 32 + 17 us (4.1 TB/s),
@@ -219,7 +220,7 @@ __device__ __forceinline__ void few_store(void* y, int64_t i, float v, int dt) {
   else static_cast<uint16_t*>(y)[i] = (uint16_t)f32_to_f16_rne(v);
 }
 
-// All tokens t0 .. t0 + 4 Q - 1 of the unit, all rows of the block.  A pass of
+// Tokens t0 .. t0 + 4 Q - 1 of the unit, all rows of the block.  A pass of
 // a team takes rows 4 g + l % 4 for g < G from its row f0 on (a pair: g < G / 2
 // of layer 0, the others of layer 1).  xrow, orow: rows of x and of the output,
 // per token; red: two buffers of the passes' partial sums.
@@ -237,8 +238,7 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
                                         const uint32_t (&mbase)[2][3],
                                         const __amdgpu_buffer_rsrc_t (&rw)[2],
                                         const __amdgpu_buffer_rsrc_t rx, unsigned char* xl,
-                                        const int* xrow, const int* orow, int t0, float* red,
-                                        bool first) {
+                                        const int* xrow, const int* orow, int t0, float* red) {
   constexpr bool PAIR = is_pair(MODE);
   constexpr int G = Q == 1 ? 8 : 4;                  // groups of four rows per pass
   constexpr int F = PAIR ? 2 * G : 4 * G;            // features per pass
@@ -448,7 +448,6 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
   Step s0, s1;
   if constexpr (WHOLE) {
     // 1 KiB of one token and step per load, dealt out to the waves
-    if (!first) __syncthreads();   // the tokens before are done with it
     for (int i = wave; i < S * tok.n; i += 4) {
       const int s = i / tok.n, t = i - s * tok.n;
       to_lds(rx, xl + 1024 * i,
@@ -460,7 +459,7 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
   load_x(kw);
   next(s0);
   next(s1);
-  if (first || WHOLE) {
+  {
     // the metadata's and the rows' copies were issued before these loads
     constexpr int w = 2 * G;
     static_assert(w < 64, "a wait counts to 63");
@@ -487,19 +486,19 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
     step(i, s0);
     step(i + 1, s1);
   }
-  __syncthreads();   // the next tokens' sums take the same buffers
 }
 
 constexpr int kTok = 64;          // tokens of a call
 constexpr int kExperts = 512;
 constexpr int kSlots = 16;        // experts per token
 
-// The want-th expert that some token chose, its tokens (rising) and each one's
-// first slot with it; -1 where fewer are chosen.  Every wave ends up with the
-// answer; xrow and orow are complete after the last barrier.
-template <int MODE>
+// The want-th (expert that some token chose, TQ of its tokens): the expert, its
+// tokens (rising) and each one's first slot with it, and the first of the TQ; -1
+// where there are fewer.  Every wave ends up with the answer; xrow and orow are
+// complete after the last barrier.
+template <int MODE, int TQ>
 __device__ __forceinline__ int find_unit(const FewArgs& a, int want, int* mask, int* ids, int* xrow,
-                                         int* orow, int& T) {
+                                         int* orow, int& T, int& t0) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int n = (int)a.M * a.topk;
   int got[kTok * kSlots / 256];
@@ -535,10 +534,11 @@ __device__ __forceinline__ int find_unit(const FewArgs& a, int want, int* mask, 
     for (int i = 0; i < kExperts / 64; ++i) {
       if (found >= 0 || 64 * i >= a.E) continue;
       uint64_t bits = __ballot(cnt[i] == t);
-      const int n = __popcll(bits);
+      const int p = (t + TQ - 1) / TQ, n = __popcll(bits) * p;
       if (left < n) {
-        for (int k = 0; k < left; ++k) bits &= bits - 1;
+        for (int k = left / p; k > 0; --k) bits &= bits - 1;
         found = 64 * i + __ffsll((unsigned long long)bits) - 1;
+        t0 = left % p * TQ;
       }
       left -= n;
     }
@@ -577,11 +577,11 @@ k_few(FewArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   Unit u;
-  int expert = 0;
+  int expert = 0, t0 = 0;
   const int tile = (int)(blockIdx.x % (unsigned)a.tiles);   // and the expert or the tile of x's rows
   int64_t xbase = 0;
   if constexpr (EXPERTS) {
-    expert = find_unit<MODE>(a, (int)(blockIdx.x / (unsigned)a.tiles), mask, ids, xrow, orow, u.T);
+    expert = find_unit<MODE, 4 * Q>(a, (int)(blockIdx.x / (unsigned)a.tiles), mask, ids, xrow, orow, u.T, t0);
     if (expert < 0) return;
   } else {
     xbase = (int64_t)(blockIdx.x / (unsigned)a.tiles) * (4 * Q);
@@ -626,14 +626,12 @@ k_few(FewArgs a) {
     FewArgs b = a;
     if (xbase) b.y = static_cast<unsigned char*>(a.y) + xbase * a.N * (a.ydt == F32 ? 4 : 2);
     __syncthreads();
-    few_run<KIND, XB, WHOLE, Q, MODE>(b, u, smem, mbase, rw, rx, xbuf, xrow, orow, 0, red, true);
+    few_run<KIND, XB, WHOLE, Q, MODE>(b, u, smem, mbase, rw, rx, xbuf, xrow, orow, 0, red);
   } else {
-    for (int t0 = 0; t0 < u.T; t0 += 4 * Q) {
-      if (Q == 1 || u.T - t0 <= 4)
-        few_run<KIND, XB, WHOLE, 1, MODE>(a, u, smem, mbase, rw, rx, xbuf, xrow, orow, t0, red, t0 == 0);
-      else
-        few_run<KIND, XB, WHOLE, Q, MODE>(a, u, smem, mbase, rw, rx, xbuf, xrow, orow, t0, red, t0 == 0);
-    }
+    if (Q == 1 || u.T - t0 <= 4)
+      few_run<KIND, XB, WHOLE, 1, MODE>(a, u, smem, mbase, rw, rx, xbuf, xrow, orow, t0, red);
+    else
+      few_run<KIND, XB, WHOLE, Q, MODE>(a, u, smem, mbase, rw, rx, xbuf, xrow, orow, t0, red);
   }
 }
 

@@ -276,6 +276,8 @@ hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStr
   const int64_t most = m.M * m.topk < m.E ? m.M * m.topk : m.E;
   // up to four tokens: the form that holds one quad, in fewer registers
   const int q = m.M <= 4 ? 1 : 2, tokens = (int)(m.M < 4 * q ? m.M : 4 * q);
+  // at most so many tiles of 4 q tokens
+  const int64_t tiles = (m.M * m.topk + most * (4 * q - 1)) / (4 * q), units = tiles < m.M * m.topk ? tiles : m.M * m.topk;
   FewArgs a{};
   size_t lds = fill(up, inner, most, true, q, tokens, a);
   a.w[0] = m.gate;
@@ -288,12 +290,12 @@ hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStr
   a.ids = m.ids;
   a.E = m.E;
   a.topk = m.topk;
-  hipLaunchKernelGGL(expert_fn<FM_UP>(few_kind(up), xb, a.x_lds > 0, q), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
+  hipLaunchKernelGGL(expert_fn<FM_UP>(few_kind(up), xb, a.x_lds > 0, q), dim3((unsigned)(a.tiles * units)), dim3(256), lds, s, a);
   lds = fill(down, K, most, false, q, tokens, a);
   a.w[0] = a.w[1] = m.down;
   a.x = h;
   a.y = part;
-  hipLaunchKernelGGL(expert_fn<FM_DOWN>(few_kind(down), xb, a.x_lds > 0, q), dim3((unsigned)(a.tiles * most)), dim3(256), lds, s, a);
+  hipLaunchKernelGGL(expert_fn<FM_DOWN>(few_kind(down), xb, a.x_lds > 0, q), dim3((unsigned)(a.tiles * units)), dim3(256), lds, s, a);
   hipLaunchKernelGGL(k_combine, dim3((unsigned)((K + 1023) / 1024), (unsigned)m.M), dim3(256), 0, s, part, m.ids,
                      m.weights, m.E, m.topk, K, m.y, m.ydt);
   return hipGetLastError();
