@@ -10,7 +10,6 @@ typedef int int8v_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kOff = 0x80000000u;   // at or past every resource: reads 0
-constexpr int kG = 2;                    // groups of 16 weight rows per wave
 
 struct MxFewArgs {
   const unsigned char *xq, *xs, *wq, *ws;
@@ -34,14 +33,14 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, unsigned char* 
 // is the format's own block: codes go from memory into the operands without a
 // shuffle, a conversion or LDS.  A step is 512 columns: load i of a row takes
 // chunks 4 i + l / 16, 64 bytes of each of 16 rows, and the four loads together
-// whole lines.  16 x 5120 x 25600: 17.7 us, 3.9 TB/s.  A wave works on 2 x 16 rows of W, loaded two steps ahead, and
-// 16 T rows of X.  Those come from L2 through the wave's own part of LDS, 256
+// whole lines.  A wave works on 16 kG rows of W, loaded two steps ahead, and 16 T
+// rows of X.  Those come from L2 through the wave's own part of LDS, 256
 // bytes of four rows per instruction (as operands, 64 bytes of 16 rows, they
 // took as long as the weights): piece p of row t lies at p ^ (t % 16), so that
 // 16 lanes of one piece touch every bank once.  KW waves share rows and add up
 // through LDS at the end.  The scale bytes of the block's rows, of W and of X,
-// are copied to LDS first.
-template <int T>
+// are copied to LDS first.  16 x 5120 x 25600: 17.7 us, 3.9 TB/s.
+template <int kG, int T>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) k_mx_few(MxFewArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   __shared__ __attribute__((aligned(16))) unsigned char xstep[4 * 4096 * T];   // an object of its own: see load_x
@@ -214,8 +213,16 @@ int quads_of(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }   // T
 bool mx_few_fits(const Desc& d, int64_t M) {
   const int64_t C = d.K / 32;
   const int T = quads_of(M);
-  return scale_lds(16 * kG, C) + scale_lds(16 * T, C) + (size_t)T * 16 * 1024 <= 156 * 1024;
+  return scale_lds(32, C) + scale_lds(16 * T, C) + (size_t)T * 16 * 1024 <= 156 * 1024;
 }
+
+namespace {
+using MxFewFn = void (*)(MxFewArgs);
+template <int G>
+MxFewFn mx_few_fn(int T) {
+  return T == 1 ? k_mx_few<G, 1> : T == 2 ? k_mx_few<G, 2> : k_mx_few<G, 4>;
+}
+}  // namespace
 
 hipError_t launch_mx_few(const Desc& d, const void* xq, const void* xs, int64_t M, const Bufs& b,
                          const float* bias, void* y, int ydt, hipStream_t s) {
@@ -226,17 +233,20 @@ hipError_t launch_mx_few(const Desc& d, const void* xq, const void* xs, int64_t 
   // many as the scales' LDS asks for.  25600 x 5120, four and two of them: 19.0 and
   // 19.5 us for 16 rows, 36.0 and 29.1 for 64.
   const int64_t fill = T == 4 ? 1024 : 2048;
+  // Two groups of weight rows per wave, which halve the traffic of X; one where
+  // four waves per row would still be fewer than 1024: 16 x 14336 x 4096 11.6 and 9.0 us,
+  // 64 x 8192 x 1024 13.7 and 10.0.
+  const int G = mt * ((d.N + 31) / 32) * 4 < 1024 ? 1 : 2;
   int KW = 1;
-  while (KW < 4 && 2 * KW <= S && (mt * ((d.N + 16 * kG - 1) / (16 * kG)) * KW < fill ||
-                                   scale_lds(4 / KW * 16 * kG, C) > 32 * 1024))
+  while (KW < 4 && 2 * KW <= S && (mt * ((d.N + 16 * G - 1) / (16 * G)) * KW < fill ||
+                                   scale_lds(4 / KW * 16 * G, C) > 32 * 1024))
     KW *= 2;
-  const int rows = 4 / KW * 16 * kG;
-  const size_t wl = scale_lds(rows, C), xl = scale_lds(16 * T, C), red = KW > 1 ? (size_t)4 * kG * T * 1024 : 0;
+  const int rows = 4 / KW * 16 * G;
+  const size_t wl = scale_lds(rows, C), xl = scale_lds(16 * T, C), red = KW > 1 ? (size_t)4 * G * T * 1024 : 0;
   MxFewArgs a{static_cast<const unsigned char*>(xq), static_cast<const unsigned char*>(xs),
               static_cast<const unsigned char*>(b.qweight), static_cast<const unsigned char*>(b.scales),
               bias, y, M, d.N, d.K, ydt, KW, (int)((d.N + rows - 1) / rows), (uint32_t)wl};
-  auto fn = T == 1 ? k_mx_few<1> : T == 2 ? k_mx_few<2> : k_mx_few<4>;
-  hipLaunchKernelGGL(fn, dim3((unsigned)(a.tiles * mt)), dim3(256), wl + xl > red ? wl + xl : red, s, a);
+  hipLaunchKernelGGL(G == 1 ? mx_few_fn<1>(T) : mx_few_fn<2>(T), dim3((unsigned)(a.tiles * mt)), dim3(256), wl + xl > red ? wl + xl : red, s, a);
   return hipGetLastError();
 }
 
