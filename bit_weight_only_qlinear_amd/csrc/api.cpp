@@ -362,7 +362,7 @@ namespace {
 enum Use { USE_GEMV, USE_SKINNY, USE_GEMM, USE_FEW };
 
 // MXFP4 products: up to 8 rows the few-row kernel, whose codes lie four rows to a
-// load (8 rows of 4096 x 14336 12.8 us, on 16-row matrix instructions 15.6; 16
+// load (8 rows of 4096 x 14336 11.6 us, on 16-row matrix instructions 15.3; 16
 // rows 21 and 15, 16 x 8192 x 8192 20 and 16); then those in tiles of 16 to 64
 // rows; the qGEMM, 18 us per 1000 columns where its tiles do not fill the chip,
 // for more than 16 rows and M N = 2^22 (256 x 4096 x 4096 25 and 80 us, 256 x 8192 x 8192 76 and 144, 256
@@ -393,7 +393,7 @@ qp_status plan_forward(const qp_desc* d, qp::Desc* dd, int32_t x_dtype, int64_t 
   if (dd->fmt == qp::MXFP4) {
     // One kernel for few rows behind both qGEMV selectors, in tiles of 16
     // rows where K % 64 != 0 keeps more of them from the qGEMM.
-    const bool fits = qp::few_fits(*dd, false);
+    const bool fits = qp::few_fits(*dd);
     const bool many = M > kFewRows && M * dd->N > kFewOutputs;
     *use = kernel == QP_KERNEL_GEMM || (kernel == QP_KERNEL_AUTO && (many || !fits) && gemm_ok(*dd))
                ? USE_GEMM : USE_FEW;
@@ -776,7 +776,7 @@ qp_status check_workspace(const void* ws, size_t have, size_t need) {
 enum GatedForm { GATED_GEMV, GATED_SKINNY, GATED_STAGED, GATED_FEW };
 GatedForm gated_form(const qp::Desc& d, int64_t M, bool save) {
   if (d.fmt == qp::MXFP4)
-    return save || M > kFewRows || !qp::few_fits(d, true) ? GATED_STAGED : GATED_FEW;
+    return save || M > kFewRows || !qp::few_fits(d) ? GATED_STAGED : GATED_FEW;
   size_t b[5];
   sizes_of(d, b);
   bool small_bufs = (size_t)M * (size_t)d.K * 2 < (size_t(1) << 31);
@@ -1152,7 +1152,7 @@ qp_status check_moe(const qp_desc* d_up, const qp_desc* d_down, int64_t M, int32
   if (M * topk * (up->K > down->K ? up->K : down->K) >= int64_t(1) << 29)
     return fail(QP_EUNSUPPORTED, "M * topk * max(K, inner) must be < 2^29 (M=%lld, topk=%d, K=%lld, inner=%lld)",
                 (long long)M, topk, (long long)up->K, (long long)down->K);
-  if (!qp::few_fits(*up, true) || !qp::few_fits(*down, false))
+  if (!qp::few_fits(*up) || !qp::few_fits(*down))
     return fail(QP_EUNSUPPORTED, "qmoe: rows of K=%lld or inner=%lld are too long (the metadata of 32 rows must "
                 "fit LDS)", (long long)up->K, (long long)down->K);
   return QP_OK;

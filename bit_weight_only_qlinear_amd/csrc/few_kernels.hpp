@@ -31,10 +31,10 @@
 // at once.  (An expert's tokens one after the other in one block: 22 tokens of
 // 2 experts of 736 x 1568 42 us instead of 27, 50 x 4096 x 1536 105 and 100.)
 //
-// 1 x 4096 x 14336: 10.2 us, 3.1 TB/s of which 4 us are the launch, the metadata
-// and the first codes.  Experts: 2 of 8 of 4096 x 14336 int4 32 + 17 us (4.1 TB/s),
-// 64 of 2048 x 1024 MXFP4 with 2 tokens each 33 + 23 (3.8), 32 of 4096 x 1536 with
-// 6 each 61 + 37 (3.3; the tokens beyond eight read their expert again).
+// 1 x 4096 x 14336: 8.8 us, 3.5 TB/s, of which 4 us are the launch, the metadata
+// and the first codes.  Experts: 2 of 8 of 4096 x 14336 int4 31 + 16 us (4.2 TB/s),
+// 64 of 2048 x 1024 MXFP4 with 2 tokens each 32 + 21 (4.0), 32 of 4096 x 1536 with
+// 6 each 60 + 33 (3.4; the tokens beyond eight read their expert again).
 #pragma once
 #include "device_common.hpp"
 #include "mlp_common.hpp"
@@ -240,7 +240,7 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
                                         const __amdgpu_buffer_rsrc_t rx, unsigned char* xl,
                                         const int* xrow, const int* orow, int t0, float* red) {
   constexpr bool PAIR = is_pair(MODE);
-  constexpr int G = Q == 1 ? 8 : 4;                  // groups of four rows per pass
+  constexpr int G = 4;                               // groups of four rows per pass
   constexpr int F = PAIR ? 2 * G : 4 * G;            // features per pass
   constexpr int kRed = 4 * G * 4 * Q;                // sums of a wave and pass
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -570,7 +570,7 @@ k_few(FewArgs a) {
   // reading it
   __shared__ __attribute__((aligned(16))) unsigned char xstep[WHOLE ? 16 : 4 * 4096 * Q];
   unsigned char* xbuf = WHOLE ? smem + a.x_lds : xstep;
-  __shared__ float red[2 * 4 * 16 * 4 * (Q == 1 ? 2 : Q)];   // Q == 2 runs single quads too
+  __shared__ float red[2 * 4 * 64 * Q];
   __shared__ int xrow[kTok], orow[kTok];
   __shared__ int mask[EXPERTS ? 2 * kExperts : 1], ids[EXPERTS ? kTok * kSlots : 1];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -643,19 +643,12 @@ inline int few_kind(const Desc& d) {
   return -1;
 }
 
-#ifndef QP_FEW_BLOCKS
-#define QP_FEW_BLOCKS 1024
-#endif
-#ifndef QP_FEW_WAVES
-#define QP_FEW_WAVES 2048
-#endif
-constexpr int64_t kFewWaves = QP_FEW_WAVES;
-constexpr int64_t kFewBlocks = QP_FEW_BLOCKS;
+constexpr int64_t kFewWaves = 1536, kFewBlocks = 1024;
 
 // Sizes, LDS layout and launch shape that the modes share; units: experts or row
-// tiles of x; q: quads of tokens that the kernel is made for; tokens: the most a pass can have, or 0 where their rows do not go
-// through LDS.  a.x_lds: where the tokens' whole rows lie, or 0.
-inline size_t fill(const Desc& d, int64_t rows, int64_t units, bool pair, int q, int tokens, FewArgs& a) {
+// tiles of x; tokens: the most a pass can have.  a.x_lds: where the tokens' whole
+// rows lie, or 0.
+inline size_t fill(const Desc& d, int64_t rows, int64_t units, bool pair, int tokens, FewArgs& a) {
   a.K = d.K;
   a.N = rows;
   a.C = (int)(d.K / 32);
@@ -664,9 +657,12 @@ inline size_t fill(const Desc& d, int64_t rows, int64_t units, bool pair, int q,
   if (d.gs == d.K && kind == F_SYM4) a.gsh = 31;
   else while ((32 << a.gsh) < d.gs) ++a.gsh;
   const int S = (a.C + 15) / 16;
-  const int F = q == 4 || pair ? 16 : 32;   // rows of the longest pass
-  // Waves per row: as few as fill the chip (two per SIMD), since waves that
-  // share rows have to add their sums up.
+  const int F = 16;   // at most so many rows or features in a pass
+  // Waves per row: as few as fill the chip, since waves that share rows have to
+  // add their sums up and take the activations again: 8 rows of 4096 x 14336 on two
+  // and four 11.6 and 15.5 us, 4 of 5120 x 25600 on one and two 16.8 and 20.3.
+  // (Passes of 32 rows for up to four tokens: 1 x 14336 x 4096 12.8 instead of 9.3
+  // us, 1 x 5120 x 25600 19.8 instead of 15.6.)
   a.KW = 1;
   while (a.KW < 4 && 2 * a.KW <= S && units * ((rows + F - 1) / F) * a.KW < kFewWaves) a.KW *= 2;
   for (int i = 0; i < 3; ++i) a.mrow[i] = 0;

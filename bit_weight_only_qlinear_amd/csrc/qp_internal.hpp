@@ -180,7 +180,7 @@ struct MoeArgs {
   void* y;
   void* ws;
 };
-bool few_fits(const Desc& d, bool pair);   // rows short enough for the few-row kernels
+bool few_fits(const Desc& d);   // rows short enough for the few-row kernels
 bool moe_format(const Desc& d);
 int moe_max_tokens();
 int moe_max_experts();
