@@ -558,7 +558,9 @@ qp_status qmoe_workspace_bytes(const qp_desc* d_up, const qp_desc* d_down, int64
  * Every weight matrix of an expert that some token takes is read once per 8
  * of its tokens (4 where M <= 4).  Exact codes, fp32 sums; the inner activations are rounded
  * to x_dtype, everything else once at the end; results do not depend on
- * timing, nor a token's on the other tokens.  Limits: M <= 64, experts <= 512,
+ * timing, nor a token's on the other tokens' values (their number may change
+ * the order of sums).  Infinite rows of AFFINE, Q4K and SYM4 experts may give NaN
+ * where the exact result is an infinity.  Limits: M <= 64, experts <= 512,
  * topk <= 16, M * topk * max(K, inner) < 2^29, and rows 32 of whose metadata fit
  * 112 KiB (K and inner <= 28640 for groups of 32 of AFFINE and SYM4, 57280 of
  * 64, 114560 of 128, 44800 for Q4K, 114656 for MXFP4).  The workspace
