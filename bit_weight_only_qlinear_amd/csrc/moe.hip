@@ -53,21 +53,23 @@ __global__ void __launch_bounds__(256) k_combine(const float* __restrict__ part,
   }
 }
 
-// ---- routing: logits in fp64 (products of two 16-bit values are exact in
-// fp32), so that the choice between two experts next to each other does not
-// depend on the order of additions.
+// ---- routing: logits in fp64, so that the choice between two experts next to
+// each other does not depend on the order of additions.  A product of two fp16
+// values is exact in fp32 (22 bits, 2^-48 .. 2^32); bf16's range is fp32's own, so
+// that theirs would overflow or vanish there, and is multiplied in fp64.
 template <bool XB>
 __device__ __forceinline__ double dot8(const uint4 u, const uint4 v) {
   const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
   double s = 0.0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float p = XB ? __uint_as_float(a[i] << 16) * __uint_as_float(b[i] << 16)
-                       : f16_to_f32(a[i] & 0xFFFFu) * f16_to_f32(b[i] & 0xFFFFu);
-    const float q = XB ? __uint_as_float(a[i] & 0xFFFF0000u) * __uint_as_float(b[i] & 0xFFFF0000u)
-                       : f16_to_f32(a[i] >> 16) * f16_to_f32(b[i] >> 16);
-    s += (double)p;
-    s += (double)q;
+    if constexpr (XB) {
+      s = fma((double)__uint_as_float(a[i] << 16), (double)__uint_as_float(b[i] << 16), s);
+      s = fma((double)__uint_as_float(a[i] & 0xFFFF0000u), (double)__uint_as_float(b[i] & 0xFFFF0000u), s);
+    } else {
+      s += (double)(f16_to_f32(a[i] & 0xFFFFu) * f16_to_f32(b[i] & 0xFFFFu));
+      s += (double)(f16_to_f32(a[i] >> 16) * f16_to_f32(b[i] >> 16));
+    }
   }
   return s;
 }

@@ -1,6 +1,6 @@
 """GPU parity of mixture-of-experts layers with their fp64 statement.
 
-Tolerances.  The router's products are exact in fp32 and summed in fp64: the
+Tolerances.  The router's logits are held in fp64: the
 choice is the statement's.  An expert's product: 36 roundings of 2^-24 (32
 additions, the chunk's two fused steps, their sum) of a chunk's magnitude
 sum (MAG + u) |x| S + |T| |x|, whose codes carry MAG = 128 (bf16), 1024 (fp16)
@@ -290,3 +290,27 @@ def test_binding_refuses_wrong_tensors(q):
                     (q.QLinearError, dict(E=4, router=r[:4].contiguous()))):
         with pytest.raises(err):
             call(**kw)
+
+
+def routed(q, x, r, topk, score="softmax", norm=True):
+    """(ids, weights) of a layer of small experts."""
+    _, g, u, n, _, _ = small(q, 2, M=x.shape[0], E=r.shape[0], K=x.shape[1])
+    o = q.qmoe_forward(g[0], n[0], x, g[1], u[1], n[1], experts=r.shape[0], topk=topk, router=r, score=score, norm=norm)
+    return o.ids.cpu().numpy(), o.weights
+
+
+@pytest.mark.parametrize("E", [5, 20])       # the router in one kernel, and in two
+@pytest.mark.parametrize("up", [70, 100, -70, -90, 0])
+def test_router_products_past_fp32(q, E, up):
+    """bf16 rows and routers whose products lie outside fp32's range: logits are held
+    in fp64, so the choice is the statement's."""
+    rng = np.random.default_rng(100 + E + up)
+    x, x64 = dev(rng.normal(size=(6, 128)) * 2.0 ** up, "bf16")
+    r, r64 = dev(rng.normal(size=(E, 128)) * 2.0 ** up, "bf16")
+    for score in ("softmax", "sigmoid"):
+        print("router", E, up, score, flush=True)
+        with np.errstate(over="ignore"):
+            ids, w = moe.route(x64, r64, 4, score, False)
+        got, gw = routed(q, x, r, 4, score, False)
+        assert np.array_equal(got, ids)
+        within(gw, w, 2.0 ** -23 * w + 1e-45, "weights")
