@@ -29,7 +29,7 @@ hipError_t launch(const Desc& d, int xdt, FewArgs& a, hipStream_t s) {
   size_t lds;
   for (;; q = 2) {   // a step of 16 rows takes 64 KiB of LDS: long rows in tiles of eight
     mt = (a.M + 4 * q - 1) / (4 * q);
-    lds = fill(d, d.N, mt, is_pair(MODE), (int)(a.M < 4 * q ? a.M : 4 * q), a);
+    lds = fill(d, d.N, mt, is_pair(MODE), (int)(a.M < 4 * q ? a.M : 4 * q), 4 * q, a);
     if (q < 4 || a.x_lds || lds <= 80 * 1024) break;
   }
   hipLaunchKernelGGL(mx_fn<MODE>(xdt == BF16, a.x_lds > 0, q), dim3((unsigned)(a.tiles * mt)), dim3(256), lds, s, a);
@@ -70,7 +70,7 @@ hipError_t launch_few_gated(const Desc& d, const GatedArgs& g, hipStream_t s) {
 // x (32 KiB), the sums and an expert's lists.
 bool few_fits(const Desc& d) {
   FewArgs a{};
-  return fill(d, 16, 1, true, 0, a) <= 112 * 1024;
+  return fill(d, 16, 1, true, 0, 0, a) <= 112 * 1024;
 }
 
 }  // namespace qp

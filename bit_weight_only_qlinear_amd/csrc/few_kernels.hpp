@@ -646,9 +646,9 @@ inline int few_kind(const Desc& d) {
 constexpr int64_t kFewWaves = 1536, kFewBlocks = 1024;
 
 // Sizes, LDS layout and launch shape that the modes share; units: experts or row
-// tiles of x; tokens: the most a pass can have.  a.x_lds: where the tokens' whole
-// rows lie, or 0.
-inline size_t fill(const Desc& d, int64_t rows, int64_t units, bool pair, int tokens, FewArgs& a) {
+// tiles of x; tokens: the most a pass can have, of `slots` (4 Q).  a.x_lds: where
+// the tokens' whole rows lie, or 0.
+inline size_t fill(const Desc& d, int64_t rows, int64_t units, bool pair, int tokens, int slots, FewArgs& a) {
   a.K = d.K;
   a.N = rows;
   a.C = (int)(d.K / 32);
@@ -692,9 +692,13 @@ inline size_t fill(const Desc& d, int64_t rows, int64_t units, bool pair, int to
   a.tiles = (int)((rows + a.RW * a.feats - 1) / (a.RW * a.feats));
   const size_t lds = meta(a.feats), x = (size_t)S * (size_t)tokens * 1024u;
   a.x_lds = 0;
-  // three KiB more: tokens that are not there are read past the last row
   if (x > 0 && x + lds <= 72 * 1024) a.x_lds = (uint32_t)lds;   // two blocks per CU
-  return a.x_lds ? lds + x + 3 * 1024u : lds;
+  // Slots without a token are read past the last row, a step of n tokens in S n KiB
+  // up to KiB (S - 1) n + its slots: 4 with n from 1 (an expert's few), the others with
+  // n from slots - 3 or, in one tile of 16, from 9; later tiles with n < slots end
+  // inside S slots.
+  const int past = slots - tokens > 3 ? slots - tokens : 3;
+  return a.x_lds ? lds + x + (size_t)past * 1024u : lds;
 }
 
 using FewFn = void (*)(FewArgs);

@@ -281,7 +281,7 @@ hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStr
   // at most so many tiles of 4 q tokens
   const int64_t tiles = (m.M * m.topk + most * (4 * q - 1)) / (4 * q), units = tiles < m.M * m.topk ? tiles : m.M * m.topk;
   FewArgs a{};
-  size_t lds = fill(up, inner, most, true, tokens, a);
+  size_t lds = fill(up, inner, most, true, tokens, 4 * q, a);
   a.w[0] = m.gate;
   a.w[1] = m.up;
   a.x = m.x;
@@ -293,7 +293,7 @@ hipError_t launch_moe(const Desc& up, const Desc& down, const MoeArgs& m, hipStr
   a.E = m.E;
   a.topk = m.topk;
   hipLaunchKernelGGL(expert_fn<FM_UP>(few_kind(up), xb, a.x_lds > 0, q), dim3((unsigned)(a.tiles * units)), dim3(256), lds, s, a);
-  lds = fill(down, K, most, false, tokens, a);
+  lds = fill(down, K, most, false, tokens, 4 * q, a);
   a.w[0] = a.w[1] = m.down;
   a.x = h;
   a.y = part;

@@ -589,3 +589,18 @@ def test_binding_refuses_wrong_tensors(q):
             (ValueError, lambda: q.qlinear_forward_mx(d, xq, xs, w, y_dtype="f64"))):
         with pytest.raises(err):
             call()
+
+
+@pytest.mark.parametrize("M", [9, 10, 11, 12, 13, 15])
+@pytest.mark.parametrize("N,K", [(70, 512), (33, 32), (130, 544), (40, 2048)])
+def test_gated_of_nine_rows_and_more(q, M, N, K):
+    """One tile of 16 rows that are not all there, whole rows of x in LDS."""
+    rng = np.random.default_rng(M + N)
+    (d, bg, wg), (_, bu, wu) = layer(q, rng, N, K), layer(q, rng, N, K)
+    x, x64 = dev(rng.normal(size=(M, K)), "bf16")
+    print("gated", M, N, K, flush=True)
+    o = q.qlinear_gated_forward(d, x, bg, bu, act="silu", h_dtype="f32")
+    g, u, h = mlp.gated(x64, wg, wu, np.zeros(N), np.zeros(N), "silu")
+    dg, du = few_tol(x64, wg) + 2.0 ** -22 * np.abs(g), few_tol(x64, wu) + 2.0 ** -22 * np.abs(u)
+    tol = 1.13 * dg * (np.abs(u) + du) + np.abs(mlp.act(g, "silu")[0]) * du + 2.0 ** -16 * np.abs(h) + TINY["f32"]
+    within(o.h, h, tol, "h")
