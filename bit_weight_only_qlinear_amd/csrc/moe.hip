@@ -113,8 +113,9 @@ struct RouteArgs {
 // Token m's choice from its logits l [E] in LDS, by a block of `threads`.
 // An expert's place is the number of those in front of it (a larger logit, or
 // the same and a lower index), counted by several threads each; the first topk
-// places are the choice.  NaN logits come after all numbers and are never
-// chosen: places that no number takes get expert -1 and weight 0.
+// places are the choice.  NaN logits come after all numbers, infinities among
+// them, and are never chosen: places that no number takes get expert -1 and weight
+// 0.  Where the largest logit is infinite, a softmax's weights are NaN.
 struct Choice {
   double l[kExperts];
   double part[16];
@@ -142,7 +143,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t m, Choice& c,
       const double o = c.l[k];
       n += o > v || (o == v && k < e) ? 1 : 0;
     }
-    if (!(v > -__builtin_inf())) n = kExperts;
+    if (v != v) n = kExperts;
     if (n) atomicAdd(&c.place[e], n);
   }
   __syncthreads();
@@ -155,7 +156,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t m, Choice& c,
   const double hi = c.top[0];
   double sum = 0.0;
   if (a.score == 0) {
-    for (int e = tid; e < E; e += threads) sum += c.l[e] > -__builtin_inf() ? exp(c.l[e] - hi) : 0.0;
+    for (int e = tid; e < E; e += threads) sum += c.l[e] == c.l[e] ? exp(c.l[e] - hi) : 0.0;
     sum = wave_sum_f64(sum);
     if (lane == 0) c.part[wave] = sum;
     __syncthreads();
@@ -168,7 +169,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t m, Choice& c,
   if (tid < a.topk) {
     double total = 0.0;
     for (int s = 0; s < a.topk; ++s) total += c.w[s];
-    const double w = a.norm ? (total > 0.0 ? c.w[tid] / total : 0.0) : c.w[tid];
+    const double w = a.norm && c.id[tid] >= 0 && total != 0.0 ? c.w[tid] / total : c.w[tid];
     a.ids[m * a.topk + tid] = c.id[tid];
     a.weights[m * a.topk + tid] = (float)w;
   }

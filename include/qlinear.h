@@ -548,8 +548,9 @@ qp_status qmoe_workspace_bytes(const qp_desc* d_up, const qp_desc* d_down, int64
  * router [experts, K] of x_dtype: logits l = x router^T, held in fp64; each
  *     token takes the topk experts of the largest logits, falling, the lower
  *     index first among equals (a NaN logit is never taken; where numbers run
- *     out, ids are -1 and weights 0), with the weights that `score` makes of
- *     their logits, divided by their sum where norm is 1.  ids (int32
+ *     out, ids are -1 and weights 0; infinities are numbers, the largest of which
+ *     makes a softmax NaN), with the weights that `score` makes of their logits,
+ *     divided by their sum where norm is 1 and the sum is not 0.  ids (int32
  *     [M, topk]) and weights (fp32 [M, topk]) are written.
  * router NULL: ids and weights are read, in any order.  An id outside
  *     [0, experts) names no expert (one that another GPU holds, say) and adds

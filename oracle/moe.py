@@ -8,12 +8,17 @@ from .mlp import act
 def route(x, router, topk, score="softmax", norm=True):
     """(ids [M, topk], weights [M, topk]): the experts of the largest logits,
     falling, the lower index among equals; a NaN logit is never taken (ids of -1
-    and weights of 0 where numbers run out)."""
-    logits = x @ router.T
+    and weights of 0 where numbers run out), an infinite one is a number like others
+    (a softmax whose largest logit is infinite is NaN)."""
+    with np.errstate(invalid="ignore"):
+        return _route(x @ router.T, topk, score, norm)
+
+
+def _route(logits, topk, score, norm):
     M, E = logits.shape
     ids, w = np.full((M, topk), -1), np.zeros((M, topk))
     for m in range(M):
-        ok = [e for e in range(E) if logits[m, e] == logits[m, e] and logits[m, e] > -np.inf]
+        ok = [e for e in range(E) if logits[m, e] == logits[m, e]]
         order = sorted(ok, key=lambda e: (-logits[m, e], e))[:topk]
         if not order:
             continue
@@ -24,7 +29,7 @@ def route(x, router, topk, score="softmax", norm=True):
             w[m, i] = np.exp(logits[m, e] - top) / total if score == "softmax" else 1 / (1 + np.exp(-logits[m, e]))
     if norm:
         total = w.sum(axis=1, keepdims=True)
-        w = np.divide(w, total, out=np.zeros_like(w), where=total > 0)
+        w = np.divide(w, total, out=np.zeros_like(w), where=(ids >= 0) & (total != 0))
     return ids, w
 
 

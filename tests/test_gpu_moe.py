@@ -314,3 +314,48 @@ def test_router_products_past_fp32(q, E, up):
         got, gw = routed(q, x, r, 4, score, False)
         assert np.array_equal(got, ids)
         within(gw, w, 2.0 ** -23 * w + 1e-45, "weights")
+
+
+@pytest.mark.parametrize("E", [5, 20])
+def test_infinite_logits(q, E):
+    """A logit of -infinity is a number: taken last, with weight 0.  One of +infinity
+    is taken first; a softmax whose largest logit is infinite is NaN, normed or not."""
+    rng = np.random.default_rng(E)
+    x, _ = dev(np.abs(rng.normal(size=(6, 128))) + 0.1, "bf16")
+    r, r64 = dev(rng.normal(size=(E, 128)) / 16, "bf16")
+    order = np.argsort(-(f64(x) @ r64.T), axis=1, kind="stable")
+    s = r.clone()
+    s[2, 0] = -float("inf")
+    s[3, 0] = float("nan")
+    want = np.array([[e for e in row if e not in (2, 3)] + [2, -1] for row in order])
+    if E == 5:
+        for score in ("softmax", "sigmoid"):
+            for norm in (False, True):
+                ids, w = routed(q, x, s, 5, score, norm)
+                assert np.array_equal(ids, want)
+                w = f64(w)
+                assert not w[:, 3:].any() and np.all(w[:, :3] > 0)
+                if norm:
+                    assert np.allclose(w.sum(1), 1, atol=1e-6)
+    s = r.clone()
+    s[1, 0] = float("inf")
+    for norm in (False, True):
+        ids, w = routed(q, x, s, 3, "softmax", norm)
+        assert np.all(ids[:, 0] == 1) and np.isnan(f64(w)).all()
+        ids, w = routed(q, x, s, 3, "sigmoid", norm)
+        w = f64(w)
+        assert np.all(ids[:, 0] == 1) and np.isfinite(w).all() and (norm or np.all(w[:, 0] == 1))
+    s[:, 0] = -float("inf")
+    ids, w = routed(q, x, s, 3, "softmax", True)
+    assert np.all(ids == [0, 1, 2]) and np.isnan(f64(w)).all()
+    ids, w = routed(q, x, s, 3, "sigmoid", True)
+    assert np.all(ids == [0, 1, 2]) and not f64(w).any()
+    # NaN weights reach y; the other tokens keep their results
+    _, g, u, n, _, _ = small(q, 2, E=5)
+    y = x.clone()
+    y[4] = float("inf")
+    t = r[:5].abs() + 0.01
+    a = q.qmoe_forward(g[0], n[0], x, g[1], u[1], n[1], experts=5, topk=2, router=t)
+    b = q.qmoe_forward(g[0], n[0], y, g[1], u[1], n[1], experts=5, topk=2, router=t)
+    keep = [0, 1, 2, 3, 5]
+    assert torch.equal(a.y[keep], b.y[keep]) and torch.isnan(b.weights[4]).all() and torch.isnan(b.y[4]).all()

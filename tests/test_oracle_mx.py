@@ -72,3 +72,15 @@ def test_layer_is_the_weighted_sum():
     assert np.allclose(y[0], 0.5 * (d[2] @ h))
     h = (g[0] @ x[1]) / (1 + np.exp(-(g[0] @ x[1]))) * (u[0] @ x[1])
     assert np.allclose(y[1], 0.75 * (d[0] @ h))
+
+
+def test_route_with_infinite_logits():
+    x, r = np.array([[1.0]]), np.array([[2.0], [-np.inf], [1.0], [np.nan]])
+    for norm in (False, True):
+        ids, w = moe.route(x, r, 4, norm=norm)
+        assert ids.tolist() == [[0, 2, 1, -1]] and np.allclose(w[0, :2], [1 / (1 + np.exp(-1)), 1 / (1 + np.e)])
+        assert w[0, 2:].tolist() == [0, 0]
+    ids, w = moe.route(x, np.array([[np.inf], [1.0], [np.nan]]), 3)
+    assert ids.tolist() == [[0, 1, -1]] and np.isnan(w[0, :2]).all() and w[0, 2] == 0
+    ids, w = moe.route(x, np.array([[-np.inf], [-np.inf]]), 2, score="sigmoid")
+    assert ids.tolist() == [[0, 1]] and w.tolist() == [[0, 0]]
