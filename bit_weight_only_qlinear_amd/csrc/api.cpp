@@ -180,8 +180,8 @@ qp_status hip_status(hipError_t e, const char* what) {
 // to K = 8192 (the largest K of the workloads it is verified on), and longer
 // rows take the exact-code MFMA kernel instead.
 // fp16-rounded weights hold the output bound up to K = 8192; per-channel
-// SYM4 runs on exact codes and MXFP4 weights are fp16 numbers (K up to 2^20:
-// 32-bit tile offsets)
+// SYM4 runs on exact codes and MXFP4 weights are fp16 numbers after a power of
+// two per row (K up to 2^20: 32-bit tile offsets)
 constexpr int64_t kGemmMaxK = 8192;
 bool gemm_ok(const qp::Desc& d) {
   const bool exact = (d.fmt == qp::SYM4 && d.gs == d.K) || d.fmt == qp::MXFP4;
@@ -386,8 +386,8 @@ qp_status plan_forward(const qp_desc* d, qp::Desc* dd, int32_t x_dtype, int64_t 
   if (kernel == QP_KERNEL_GEMM && !gemm_ok(*dd))
     return fail(QP_EUNSUPPORTED,
                 "the qGEMM kernel (fp16-rounded weights) needs K %% 64 == 0 and K <= %lld, "
-                "where it meets the output bound (K=%lld; per-channel SYM4 and MXFP4: exact, "
-                "K <= 2^20); QP_KERNEL_AUTO and QP_KERNEL_GEMV_MFMA use exact codes at any K",
+                "where it meets the output bound (K=%lld; per-channel SYM4 and MXFP4, whose weights "
+                "it does not round: K <= 2^20); QP_KERNEL_AUTO and QP_KERNEL_GEMV_MFMA use exact codes at any K",
                 (long long)kGemmMaxK, (long long)dd->K);
   sizes_of(*dd, nbytes);
   if (dd->fmt == qp::MXFP4) {

@@ -42,7 +42,10 @@
 //      Q6K: S = sc*step, T = -32*S;  SYM4: S = scale, T = -8*S.
 //    SYM4 with one scale per output channel keeps the codes themselves
 //    (S = 1, T = -8, exact in fp16) and scales the fp32 result per channel
-//    in the epilogue: no weight rounding, so no limit on K.
+//    in the epilogue: no weight rounding, so no limit on K.  MXFP4 weights are
+//    fp16 numbers after a power of two per row, which the epilogue undoes (MxRow):
+//    a scan of the tile's scale bytes ahead of the first step, about 1 us a tile
+//    (2048 x 4096 x 14336: 190 us, without it 188).
 //  * Tiles are handed out so that each XCD works on a contiguous run of
 //    tiles (shared L2).
 //
@@ -291,9 +294,70 @@ __device__ __forceinline__ float e8m0_f32(uint32_t s) {
   return __uint_as_float(s == 255u ? 0x7FC00000u : b);
 }
 
+// MXFP4 weights as fp16 numbers.  A scale byte covers 2^-127 .. 2^127 and fp16's
+// numbers 2^-24 .. 2^16, so a row (a block of columns, where the sum runs over rows)
+// is taken times 2^shift, which brings its largest scale to 2^13 (weights of up to
+// 6 2^13), and the fp32 sum times 2^-shift.  Weights are then multiples of 2^-37 of
+// the largest scale: exact in blocks down to 2^-36 of it.
+constexpr int kMxTop = 127 + 13;
+// Byte s (255: NaN) and the shift -> the scale.  (Exponents past 254 come only of
+// bytes outside the row, which no sum takes.)
+__device__ __forceinline__ float mx4_scale(uint32_t s, int shift) {
+  const int e = (int)s + shift;
+  return __uint_as_float(s == 255u ? 0x7FC00000u : (uint32_t)(e > 1 ? e : 1) << 23);
+}
+// Shift of the row whose scale bytes lie at so .. so + n - 1, which two neighbouring
+// threads (half 0 and 1) share, each in every second 16 bytes.  load takes the first
+// 128 bytes, to be issued ahead of a tile's first codes; shift those and the rest.
+// As 16-bit numbers, bytes plus 1 in the upper halves compare like the bytes, and
+// 255 becomes 0.
+struct MxRow {
+  uint4 v[4];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t end) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)   // offsets past the resource read 0
+      v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                                           r, at + 32u * i < end ? at + 32u * i : 0x80000000u, 0, 0));
+  }
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t so, uint32_t n, uint32_t half) {
+    load(r, (so & ~15u) + 16u * half, so + n);
+  }
+  __device__ __forceinline__ int shift(__amdgpu_buffer_rsrc_t r, uint32_t so, uint32_t n, uint32_t half) {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    const uint32_t end = so + n;
+    const u16x2_t one = {0x0100, 0x0100};
+    u16x2_t m = {0, 0};
+    for (uint32_t at = (so & ~15u) + 16u * half;;) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t p = at + 32u * i;
+        if (p >= end) break;
+        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        if (p < so || p + 16u > end) {   // bytes of the rows before and after: 0
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k) {
+            const uint32_t b = p + 4u * k;
+            if (b < so) w[k] = so - b < 4u ? w[k] & (0xFFFFFFFFu << (8u * (so - b))) : 0u;
+            if (b + 4u > end) w[k] = b < end ? w[k] & (0xFFFFFFFFu >> (8u * (b + 4u - end))) : 0u;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const u16x2_t b = __builtin_bit_cast(u16x2_t, w[k]);
+          m = __builtin_elementwise_max(m, __builtin_elementwise_max((u16x2_t)(b + one), (u16x2_t)((b << 8) + one)));
+        }
+      }
+      at += 128u;
+      if (at >= end) break;
+      load(r, at, end);
+    }
+    const int t = (m.x > m.y ? m.x : m.y) >> 8, o = __shfl_xor(t, 1, 64), top = (t > o ? t : o) - 1;
+    return kMxTop - (top > 0 ? top : 0);
+  }
+};
+
 // E2M1 codes 0 .. 7 of a word times `scale`, as fp16 pairs (0,1), (2,3), (4,5),
-// (6,7): one hardware conversion per pair, exact while a weight is a multiple
-// of 2^-24 below 2^16.
+// (6,7): one hardware conversion per pair.
 __device__ __forceinline__ void mx4_pairs(uint32_t w, float scale, uint32_t (&p)[4]) {
   p[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 0));
   p[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 1));
@@ -311,9 +375,10 @@ __device__ __forceinline__ uint4 mx4_chunk(uint32_t w, float scale) {
 }
 
 // Weight chunk j of the thread's row as 8 fp16 in the order (0,4,1,5,2,6,3,7).
+// MXFP4: times 2^shift.
 template <int KIND, bool MBF16>
-__device__ __forceinline__ uint4 weight_chunk(const Stage<KIND>& st, int j, uint32_t magic) {
-  if constexpr (KIND == G_MX4) return mx4_chunk(st.w[j], e8m0_f32(st.s0 & 0xFFu));
+__device__ __forceinline__ uint4 weight_chunk(const Stage<KIND>& st, int j, uint32_t magic, int shift) {
+  if constexpr (KIND == G_MX4) return mx4_chunk(st.w[j], mx4_scale(st.s0 & 0xFFu, shift));
   const int grp = KIND == G_Q6K ? (j >> 1) : 0;   // Q6K groups hold 16 columns
   float S, T;
   group_st<KIND, MBF16>(st, grp, S, T);
@@ -372,7 +437,8 @@ __device__ __forceinline__ int wrow_of(int t) {
 // half row.
 template <int KIND, bool XBF16, bool MBF16>
 __device__ __forceinline__ void convert_part(const Stage<KIND>& st, int p, unsigned char* smem,
-                                             uint32_t buf, int tid, uint32_t magic, const int* xe) {
+                                             uint32_t buf, int tid, uint32_t magic, int shift,
+                                             const int* xe) {
   // activation row (tid >> 3) + 64 p: (row >> 1) & 7 == (tid >> 4) & 7
   const uint32_t xb = kXBase + (uint32_t)(tid >> 3) * 128u +
                       (uint32_t)((tid & 7) ^ ((tid >> 4) & 7)) * 16u;
@@ -380,7 +446,7 @@ __device__ __forceinline__ void convert_part(const Stage<KIND>& st, int p, unsig
       act_chunk<XBF16>(st.x[p], XBF16 ? xe[(tid >> 3) + 64 * p] : 0);
   const int n = wrow_of(tid), j = 4 * (tid & 1) + p;
   const uint32_t wb = (uint32_t)n * 128u + (uint32_t)((j ^ ((n >> 1) & 7)) * 16);
-  *reinterpret_cast<uint4*>(smem + wb + buf * kTileBytes) = weight_chunk<KIND, MBF16>(st, p, magic);
+  *reinterpret_cast<uint4*>(smem + wb + buf * kTileBytes) = weight_chunk<KIND, MBF16>(st, p, magic, shift);
 }
 
 // Weight-side buffer resources and offsets of a block's rows n0 .. n0 +
@@ -406,7 +472,9 @@ __device__ __forceinline__ void weight_rsrc(const GemmArgs& a, int64_t n0, int64
   else if constexpr (KIND == G_MX4) { srow = K / 32; }
   else if constexpr (KIND == G_SYM4 || KIND == G_SYM4C) { srow = (K / a.gs) * 4; }
   else { srow = (K / a.gs) * 2; zrow = srow; }
-  r.s = rsrc(static_cast<const unsigned char*>(a.scales) + n0 * srow, (uint32_t)(nrows * srow));
+  // (MXFP4: whole 16-byte units of memory, of which MxRow takes dwords)
+  r.s = rsrc(static_cast<const unsigned char*>(a.scales) + n0 * srow,
+             KIND == G_MX4 ? ((uint32_t)(nrows * srow) + 15u) & ~15u : (uint32_t)(nrows * srow));
   r.so = (uint32_t)(n * srow);
   r.z = r.s; r.zo = r.so;
   if (zrow) {
@@ -425,6 +493,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
 k_gemm(GemmArgs a) {
   __shared__ __attribute__((aligned(16))) unsigned char smem[4 * kTileBytes];
   __shared__ int s_xe[BM];   // prescale exponents of the block's activation rows
+  __shared__ int s_we[KIND == G_MX4 ? BN : 1];   // shifts of its weight rows
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -473,6 +542,7 @@ k_gemm(GemmArgs a) {
 
   const int KT = (int)(K / BK);
   const uint32_t magic = 0x64006400u;   // fp16 pair (1024, 1024), kept in a VGPR
+  int shift = 0;   // MXFP4: of the thread's weight row
 
   auto rd_a = [&](uint32_t buf, int s, int i) {
     return *reinterpret_cast<const half8_t*>(smem + fa[s] + (buf * kTileBytes + 4096u * i));
@@ -520,7 +590,7 @@ k_gemm(GemmArgs a) {
         B[0] = Bn[0];
         B[1] = Bn[1];
       }
-      convert_part<KIND, XBF16, MBF16>(nxt, s, smem, cur ^ 1u, tid, magic, s_xe);
+      convert_part<KIND, XBF16, MBF16>(nxt, s, smem, cur ^ 1u, tid, magic, shift, s_xe);
 #if QP_GEMM_SGB
       // instruction order of the slice: B prefetch, then per A fragment two
       // MFMAs, its re-read and a share of the conversion
@@ -553,21 +623,24 @@ k_gemm(GemmArgs a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[i], bf[j], acc[i][j], 0, 0, 0);
-      convert_part<KIND, XBF16, MBF16>(nxt, s, smem, cur ^ 1u, tid, magic, s_xe);
+      convert_part<KIND, XBF16, MBF16>(nxt, s, smem, cur ^ 1u, tid, magic, shift, s_xe);
     }
 #endif
     __syncthreads();
   };
 
+  MxRow row;
+  if constexpr (KIND == G_MX4) row.load(r.s, r.so, (uint32_t)(K / 32), r.half);
   Stage<KIND> st0, st1;
   load_stage<KIND, GS32>(a, r, 0, st0);
   load_stage<KIND, GS32>(a, r, 1, st1);
+  if constexpr (KIND == G_MX4) s_we[wrow_of(tid)] = shift = row.shift(r.s, r.so, (uint32_t)(K / 32), r.half);
   if constexpr (XBF16) {
     if (tid < BM) s_xe[tid] = m0 + tid < a.M ? read_exp(a, m0 + tid, n0) : 0;
     __syncthreads();
   }
 #pragma unroll
-  for (int p = 0; p < 4; ++p) convert_part<KIND, XBF16, MBF16>(st0, p, smem, 0u, tid, magic, s_xe);
+  for (int p = 0; p < 4; ++p) convert_part<KIND, XBF16, MBF16>(st0, p, smem, 0u, tid, magic, shift, s_xe);
   __syncthreads();
   for (int kt = 0; kt < KT; kt += 2) {
     kstep(kt, st0, st1);
@@ -605,6 +678,11 @@ k_gemm(GemmArgs a) {
         for (int q = 0; q < 4; ++q)
           sv[q] = static_cast<const float*>(a.scales)[n + q < a.N ? n + q : a.N - 1];
       }
+      int we[4] = {0, 0, 0, 0};
+      if constexpr (KIND == G_MX4) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) we[q] = s_we[wi * 128 + i * 32 + 8 * g + 4 * (el >> 5) + q];
+      }
       static_for<2>([&](auto J) {
         constexpr int j = decltype(J)::value;
         const int64_t m = m0 + wj * 64 + j * 32 + (el & 31);
@@ -614,7 +692,7 @@ k_gemm(GemmArgs a) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           v[q] = KIND == G_SYM4C ? fmaf(ldexpf(acc[i][j][4 * g + q], -xe), sv[q], bv[q])
-                                 : ldexpf(acc[i][j][4 * g + q], -xe) + bv[q];
+                                 : ldexpf(acc[i][j][4 * g + q], -xe - we[q]) + bv[q];
         const bool mok = m < a.M;
         if (mok && vec4 && n < a.N) {
           if (ydt == F32) {
@@ -673,6 +751,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
 k_gemm224(GemmArgs a) {
   __shared__ __attribute__((aligned(16))) unsigned char smem[2 * kTileBytes];
   __shared__ int s_xe[BM];   // prescale exponents of the block's activation rows
+  __shared__ int s_we[KIND == G_MX4 ? BN : 1];   // shifts of its weight rows
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -729,6 +808,7 @@ k_gemm224(GemmArgs a) {
 
   const int KT = (int)(K / BK);
   const uint32_t magic = 0x64006400u;
+  int shift = 0;   // MXFP4: of the thread's weight row
   half8_t Bf[2][4];
 
   // One k-step (two MFMA k-substeps of 32): MFMAs on LDS buffer kt & 1 and
@@ -859,8 +939,8 @@ k_gemm224(GemmArgs a) {
         for (int i = 0; i < 7; ++i) An[i] = rd_a(cur, 1, i);
       }
       __builtin_amdgcn_sched_barrier(0);
-      uint4 w0 = weight_chunk<KIND, MBF16>(nxt, 2 * sub, magic);
-      uint4 w1 = weight_chunk<KIND, MBF16>(nxt, 2 * sub + 1, magic);
+      uint4 w0 = weight_chunk<KIND, MBF16>(nxt, 2 * sub, magic, shift);
+      uint4 w1 = weight_chunk<KIND, MBF16>(nxt, 2 * sub + 1, magic, shift);
       static_for<(sub == 1 ? 7 - ND : 7)>([&](auto I) {
         constexpr int i = decltype(I)::value;
         static_for<4>([&](auto J) {
@@ -892,6 +972,11 @@ k_gemm224(GemmArgs a) {
     __syncthreads();
   };
 
+  MxRow row;
+  if constexpr (KIND == G_MX4) {
+    row.load(r.s, r.so, (uint32_t)(K / 32), r.half);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   Stage<KIND> st0, st1;
   load_stage<KIND, GS32, false, !MCH>(a, r, 0, st0);
   load_stage<KIND, GS32, false, !MCH>(a, r, 1, st1);
@@ -912,8 +997,9 @@ k_gemm224(GemmArgs a) {
   for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
     for (int j = 0; j < 4; ++j) Bf[sub][j] = ld_b(0, sub, j);
+  if constexpr (KIND == G_MX4) s_we[wn] = shift = row.shift(r.s, r.so, (uint32_t)(K / 32), r.half);
 #pragma unroll
-  for (int p = 0; p < 4; ++p) st_w(0u, p, weight_chunk<KIND, MBF16>(st0, p, magic));
+  for (int p = 0; p < 4; ++p) st_w(0u, p, weight_chunk<KIND, MBF16>(st0, p, magic, shift));
   if constexpr (XBF16) {
     if (tid < BM) s_xe[tid] = m0 + tid < a.M ? a.xe[m0 + tid] : 0;
   }
@@ -965,6 +1051,11 @@ k_gemm224(GemmArgs a) {
       for (int v = 0; v < 4; ++v)
         sv[v] = static_cast<const float*>(a.scales)[n + v < a.N ? n + v : a.N - 1];
     }
+    int we[4] = {0, 0, 0, 0};
+    if constexpr (KIND == G_MX4) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) we[v] = s_we[wi * 112 + i * 16 + 4 * (el >> 4) + v];
+    }
     static_for<4>([&](auto J) {
       constexpr int j = decltype(J)::value;
       const int64_t m = m0 + wj * 64 + j * 16 + (el & 15);
@@ -974,7 +1065,7 @@ k_gemm224(GemmArgs a) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         v[q] = KIND == G_SYM4C ? fmaf(ldexpf(acc[i][j][q], -xe), sv[q], bv[q])
-                               : ldexpf(acc[i][j][q], -xe) + bv[q];
+                               : ldexpf(acc[i][j][q], -xe - we[q]) + bv[q];
       const bool mok = m < a.M;
       if (mok && vec4 && n < a.N) {
         if (ydt == F32) {

@@ -273,11 +273,12 @@ qp_status qpack_dequantize(const qp_desc* d, const qp_weights* w, void* W_out,
  * rounded once to fp16 inside the kernel (scales, zero points and weights
  * are assumed to lie in the fp16 normal range) -- except per-channel SYM4,
  * whose codes q are fp16-exact and whose channel scale multiplies the fp32
- * sum, and MXFP4, whose weights are fp16 numbers where they are multiples of
- * 2^-24 below 2^16 (scales of 2^-23 .. 2^13) -- and each activation row is
- * scaled by a power of two that brings its largest magnitude into fp16
- * range before it is converted (undone in fp32 after the sums), so every
- * finite bf16 activation is taken.  To hold the per-row exponents without a
+ * sum, and MXFP4, whose rows are taken times the power of two that brings
+ * their largest scale to 2^13 (undone in fp32): weights of any scale, exact but
+ * for rounding to multiples of 2^-37 of their row's largest scale -- and each
+ * activation row is scaled by a power of two that brings its largest magnitude
+ * into fp16 range before it is converted (undone in fp32 after the sums), so
+ * every finite bf16 activation is taken.  To hold the per-row exponents without a
  * workspace the qGEMM writes them into y before it computes; y's contents
  * are undefined until the call completes.  QP_KERNEL_AUTO picks by M and K as
  * listed under qp_kernel.

@@ -604,3 +604,121 @@ def test_gated_of_nine_rows_and_more(q, M, N, K):
     dg, du = few_tol(x64, wg) + 2.0 ** -22 * np.abs(g), few_tol(x64, wu) + 2.0 ** -22 * np.abs(u)
     tol = 1.13 * dg * (np.abs(u) + du) + np.abs(mlp.act(g, "silu")[0]) * du + 2.0 ** -16 * np.abs(h) + TINY["f32"]
     within(o.h, h, tol, "h")
+
+
+# ---------------------------------------------------------------- the qGEMM, by name and where AUTO takes it
+def mx_tolerance(D, w, top):
+    """Largest error of D [M, n] (rounded once to fp16: 2^-11 of each value, 2^-39 of
+    its row's maximum for the smallest) times w [n, K], whose columns' fp16 numbers
+    are multiples of 2^-37 of 2^top, a column's largest scale (fp16's last bit, 2^-24,
+    where that scale becomes 2^13): half of that; the sums n + 32 additions of 2^-23 in
+    instructions that truncate."""
+    a, v = np.abs(D), np.abs(w)
+    n = w.shape[0]
+    return (2.0 ** -11 + (n + 32) * 2.0 ** -23) * (a @ v) + 2.0 ** -38 * a.sum(axis=1, keepdims=True) * np.exp2(top) + \
+        2.0 ** -39 * a.max(axis=1, keepdims=True) * v.sum(axis=0)
+
+
+def scales_from(rng, N, C, low, high, wide):
+    """Scale bytes [N, C] of rows whose largest lie in low .. high, and up to `wide` below."""
+    top = rng.integers(low, high + 1, size=(N, 1))
+    s = top - rng.integers(0, wide + 1, size=(N, C))
+    s[:, rng.integers(0, C)] = top[:, 0]
+    return np.clip(s, 0, 254).astype(np.uint8)
+
+
+QGEMM = [(17, 64, 64), (300, 257, 512), (33, 130, 1088), (257, 301, 1024), (16, 20, 192), (520, 250, 128), (40, 33, 64),
+         (290, 225, 192)]
+
+
+@pytest.mark.parametrize("M,N,K", QGEMM)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_qgemm_in_both_tilings(q, M, N, K, dt):
+    """With a workspace where the call has a use for one, and without; a block of
+    scale 255 keeps to its output column."""
+    rng = np.random.default_rng(M + N + K)
+    c = rng.integers(0, 16, size=(N, K)).astype(np.uint8)
+    s = scales_from(rng, N, K // 32, 112, 124, 6)
+    w64 = mx.dequantize(c, s)
+    d, w = q.QDesc.mxfp4(N, K), on_gpu(c, s)
+    x, x64 = dev(rng.normal(size=(M, K)), dt)
+    b, b64 = dev(rng.normal(size=N), dt)
+    ref = x64 @ w64.T + b64
+    tol = mx_tolerance(x64, w64.T, s.max(axis=1) - 127.0)
+    for ws in (None, "auto"):
+        for yd in ("f32", dt):
+            print("qgemm", M, N, K, dt, ws, yd, q.workspace_bytes(d, M, kernel=q.QP_KERNEL_GEMM), flush=True)
+            y = q.qlinear_forward(d, x, w, bias=b, y_dtype=yd, kernel=q.QP_KERNEL_GEMM, workspace=ws)
+            within(y, ref, tol * (1 + U[yd]) + (U[yd] + 2.0 ** -23) * np.abs(ref) + TINY[yd], yd)
+        s2 = s.copy()
+        s2[N - 1, 0] = s2[3, K // 32 - 1] = 255
+        y2 = q.qlinear_forward(d, x, on_gpu(c, s2), bias=b, y_dtype="f32", kernel=q.QP_KERNEL_GEMM, workspace=ws)
+        bad = torch.isnan(y2).cpu().numpy()
+        assert bad[:, [3, N - 1]].all() and bad.sum() == 2 * M
+        keep = [n for n in range(N) if n not in (3, N - 1)]
+        within(y2[:, keep], ref[:, keep], (tol + 2.0 ** -22 * np.abs(ref))[:, keep] + TINY["f32"], "others")
+
+
+@pytest.mark.parametrize("M,N,K,staged", [(257, 32763, 128, False), (300, 14336, 512, True), (290, 14500, 320, True)])
+def test_auto_takes_the_qgemm(q, M, N, K, staged):
+    """M N past 2^22: AUTO is the qGEMM, with a workspace or not."""
+    rng = np.random.default_rng(M + N)
+    c = rng.integers(0, 16, size=(N, K)).astype(np.uint8)
+    s = scales_from(rng, N, K // 32, 112, 124, 6)
+    w64 = mx.dequantize(c, s)
+    d, w = q.QDesc.mxfp4(N, K), on_gpu(c, s)
+    x, x64 = dev(rng.normal(size=(M, K)), "bf16")
+    need = q.workspace_bytes(d, M)
+    print("auto", M, N, K, need, flush=True)
+    assert need == q.workspace_bytes(d, M, kernel=q.QP_KERNEL_GEMM) and staged == (need > 0)
+    ref = x64 @ w64.T
+    tol = mx_tolerance(x64, w64.T, s.max(axis=1) - 127.0) + 2.0 ** -23 * np.abs(ref) + TINY["f32"]
+    for ws in (None, "auto"):
+        y = q.qlinear_forward(d, x, w, y_dtype="f32", workspace=ws)
+        within(y, ref, tol, "y")
+        assert torch.equal(y, q.qlinear_forward(d, x, w, y_dtype="f32", kernel=q.QP_KERNEL_GEMM, workspace=ws))
+
+
+# scale bytes of a row's (a column's) largest block: fp16 alone holds weights of 104 .. 140
+RANGES = [(0, 8), (40, 60), (100, 107), (138, 143), (200, 236), (0, 236)]
+
+
+@pytest.mark.parametrize("low,high", RANGES)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_qgemm_takes_every_scale(q, low, high, dt):
+    for M, N, K in ((40, 70, 512), (300, 300, 576)):
+        rng = np.random.default_rng(M + low)
+        c = rng.integers(0, 16, size=(N, K)).astype(np.uint8)
+        s = scales_from(rng, N, K // 32, low, high, 12)
+        c[5], s[6] = 0, 0          # a row of zeros, and one of the smallest scale
+        w64 = mx.dequantize(c, s)
+        d, w = q.QDesc.mxfp4(N, K), on_gpu(c, s)
+        x, x64 = dev(rng.normal(size=(M, K)) / 16, dt)
+        b, b64 = dev(rng.normal(size=N), dt)
+        ref = x64 @ w64.T
+        tol = mx_tolerance(x64, w64.T, s.max(axis=1) - 127.0) + 2.0 ** -22 * np.abs(ref) + TINY["f32"]
+        for ws in (None, "auto"):
+            print("scales", M, N, K, low, high, dt, ws, flush=True)
+            y = q.qlinear_forward(d, x, w, y_dtype="f32", kernel=q.QP_KERNEL_GEMM, workspace=ws)
+            within(y, ref, tol, "y")
+            y = q.qlinear_forward(d, x, w, bias=b, y_dtype="f32", kernel=q.QP_KERNEL_GEMM, workspace=ws)
+            within(y, ref + b64, tol + 2.0 ** -23 * np.abs(ref + b64), "with bias")
+        # the kernels on exact codes
+        within(q.qlinear_forward(d, x, w, y_dtype="f32", kernel=q.QP_KERNEL_GEMV), ref,
+               few_tol(x64, w64) + 2.0 ** -22 * np.abs(ref) + TINY["f32"], "exact codes")
+
+
+def test_qgemm_takes_the_largest_rows_and_weights(q):
+    """bf16 rows of 1e30 against weights of 1e-25, and the other way round: finite results."""
+    rng = np.random.default_rng(21)
+    N, K = 70, 512
+    c = rng.integers(0, 16, size=(N, K)).astype(np.uint8)
+    for M, up, byte in ((40, 1e30, 40), (40, 1e-28, 210), (300, 1e30, 40)):
+        s = scales_from(rng, N, K // 32, byte - 2, byte + 2, 3)
+        w64 = mx.dequantize(c, s)
+        x, x64 = dev(rng.normal(size=(M, K)) * up, "bf16")
+        ref = x64 @ w64.T
+        for ws in (None, "auto"):
+            y = q.qlinear_forward(q.QDesc.mxfp4(N, K), x, on_gpu(c, s), y_dtype="f32", kernel=q.QP_KERNEL_GEMM,
+                                  workspace=ws)
+            within(y, ref, mx_tolerance(x64, w64.T, s.max(axis=1) - 127.0) + 2.0 ** -22 * np.abs(ref), "y")
