@@ -12,6 +12,7 @@
 //  * Weights go through LDS dequantized to fp16 as in the qGEMM (same tile
 //    layout and column order); activations are staged once per call (stage.hip)
 //    and their fragments loaded from L2 straight into registers a step ahead.
+//  * MXFP4 rows are taken times a power of two each, as in the qGEMM (MxRow).
 //  * Scales and biases come in 16-byte chunks (8 groups, 16 codes or 4 fp32
 //    scales) a chunk ahead where the rows are whole chunks, else per step: a
 //    wave's 32 rows make two loads of 32 cache lines each per step otherwise.
@@ -150,7 +151,7 @@ __device__ __forceinline__ void load_codes(const GRes& r, int t, int lg, GStage<
       st.s1 = __builtin_amdgcn_raw_buffer_load_b8(r.z, r.zo + g2, 0, 0);
       st.s2 = __builtin_amdgcn_raw_buffer_load_b32(r.p, r.po + (uint32_t)(t / 4) * 4u, 0, 0);
     } else if constexpr (KIND == G_MX4) {
-      // past the row's end the scale 2^-127, whose weights are 0 in fp16: the
+      // past the row's end byte 0, whose weights are finite (x is 0 there): the
       // next row's may be NaN
       st.s0 = __builtin_amdgcn_raw_buffer_load_b8(r.s, g2 < r.ng ? r.so + g2 : kOff, 0, 0);
     } else if constexpr (KIND == G_SYM4) {
@@ -176,7 +177,7 @@ __device__ __forceinline__ void split2(float v, half2_t& hi, half2_t& lo) {
 }
 
 template <int KIND>
-__device__ __forceinline__ void scales_of(const GStage<KIND>& st, int mb, GScale<KIND>& c) {
+__device__ __forceinline__ void scales_of(const GStage<KIND>& st, int mb, int shift, GScale<KIND>& c) {
   if constexpr (KIND == G_Q4K) {
     const float S = (float)(st.s0 & 0xFFu) * f16_to_f32(st.s2 & 0xFFFFu);
     split2(S, c.S[0], c.s);
@@ -188,7 +189,7 @@ __device__ __forceinline__ void scales_of(const GStage<KIND>& st, int mb, GScale
   } else if constexpr (KIND == G_SYM4) {
     split2(__uint_as_float(st.s0), c.S[0], c.T[0]);
   } else if constexpr (KIND == G_MX4) {
-    c.Sf = e8m0_f32(st.s0 & 0xFFu);
+    c.Sf = mx4_scale(st.s0 & 0xFFu, shift);
   } else if constexpr (KIND != G_SYM4C) {
     c.Sf = meta_to_f32(st.s0 & 0xFFFFu, mb);
     c.Tf = meta_to_f32(st.s1 & 0xFFFFu, mb);
@@ -270,14 +271,17 @@ __device__ __forceinline__ uint32_t code8(float v, const CodeOf& c) {
   return (uint32_t)(int)rintf(fminf(fmaxf(v * c.up * c.inv, -127.f), 127.f)) & c.keep;
 }
 
-// g and u of the lane's four consecutive features f .. f + 3 in block (i, j).
+// g and u of the lane's four consecutive features f .. f + 3 in block (i, j); we: the
+// shifts of the wave's weight rows from the lane's first on (MXFP4).
 template <int KIND, int J, bool BIAS = true>
 __device__ __forceinline__ void pre_act4(const GatedK& a, const float16_t (&acc)[4][J], int i, int j,
-                                         int g4, int f, int xe, float (&g)[4], float (&u)[4]) {
+                                         int g4, int f, int xe, const int* we, float (&g)[4],
+                                         float (&u)[4]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    g[q] = ldexpf(acc[i][j][4 * g4 + q], -xe);
-    u[q] = ldexpf(acc[i + 2][j][4 * g4 + q], -xe);
+    const int at = 32 * i + 8 * g4 + q;
+    g[q] = ldexpf(acc[i][j][4 * g4 + q], KIND == G_MX4 ? -xe - we[at] : -xe);
+    u[q] = ldexpf(acc[i + 2][j][4 * g4 + q], KIND == G_MX4 ? -xe - we[64 + at] : -xe);
   }
   const int last = (int)a.N - 1;
   asm volatile("" : "+v"(f));   // keeps the loads below from gathering ahead of all their uses
@@ -325,7 +329,7 @@ __device__ __forceinline__ uint32_t q_at(int r, int chunk) {
 // request rate.
 template <int KIND, int J, int ACT>
 __device__ __forceinline__ void finish(const GatedK& a, float16_t (&acc)[4][J], int el, int mbw,
-                                       int f0, unsigned char* lds) {
+                                       int f0, const int* we, unsigned char* lds) {
   const int N = (int)a.N;
   const bool lines = N % 16 == 0 && a.hdt != F32, vec = N % 4 == 0;
   const int hh = el >> 5;
@@ -339,7 +343,7 @@ __device__ __forceinline__ void finish(const GatedK& a, float16_t (&acc)[4][J], 
       constexpr int i = decltype(G)::value / 4, g4 = decltype(G)::value % 4;
       const int f = f0 + 32 * i + 8 * g4 + 4 * hh;
       float g[4], u[4];
-      pre_act4<KIND, J>(a, acc, i, j, g4, f, xe, g, u);
+      pre_act4<KIND, J>(a, acc, i, j, g4, f, xe, we, g, u);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         acc[i][j][4 * g4 + q] = g[q];
@@ -441,7 +445,7 @@ __device__ __forceinline__ void finish(const GatedK& a, float16_t (&acc)[4][J], 
 // The same for one of several blocks along K: its share of g and u.
 template <int KIND, int J>
 __device__ __forceinline__ void finish_part(const GatedK& a, float16_t (&acc)[4][J], int el, int mbw,
-                                            int f0, int sp) {
+                                            int f0, int sp, const int* we) {
   static_for<J>([&](auto JJ) {
     constexpr int j = decltype(JJ)::value;
     const int64_t m = (int64_t)(mbw + j) * 32 + (el & 31);
@@ -452,7 +456,7 @@ __device__ __forceinline__ void finish_part(const GatedK& a, float16_t (&acc)[4]
         constexpr int i = decltype(G)::value / 4, g4 = decltype(G)::value % 4;
         const int f = f0 + 32 * i + 8 * g4 + 4 * (el >> 5);
         float g[4], u[4];
-        pre_act4<KIND, J, false>(a, acc, i, j, g4, f, xe, g, u);
+        pre_act4<KIND, J, false>(a, acc, i, j, g4, f, xe, we, g, u);
         if (f < a.Np) {
           *reinterpret_cast<float4*>(row + f) = make_float4(g[0], g[1], g[2], g[3]);
           *reinterpret_cast<float4*>(row + a.Np + f) = make_float4(u[0], u[1], u[2], u[3]);
@@ -504,8 +508,8 @@ __global__ void __launch_bounds__(256) k_gated_join(GatedK a) {
 // One tile: features n0 .. n0 + 127, 32-row blocks mb0 .. of x (J per wave),
 // share sp of the steps along K.
 template <int KIND, bool CH, int J>
-__device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem, int64_t n0, int mb0,
-                                           int sp) {
+__device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem, int* s_we, int64_t n0,
+                                           int mb0, int sp) {
   const int t0 = (int)((int64_t)a.T * sp / a.split), t1 = (int)((int64_t)a.T * (sp + 1) / a.split);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -550,7 +554,7 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
       r.s = res(b.scales, ng * 4);
       r.so = f * (uint32_t)(ng * 4);
     } else if constexpr (KIND == G_MX4) {
-      r.s = res(b.scales, ng);
+      r.s = rsrc(static_cast<const unsigned char*>(b.scales) + n0 * ng, ((uint32_t)(nrows * ng) + 15u) & ~15u);   // whole units
       r.so = f * (uint32_t)ng;
     } else if constexpr (KIND != G_SYM4C) {
       r.s = res(b.scales, ng * 2);
@@ -598,6 +602,7 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
 
   half8_t Bf[4][J];
   GChunk cur, nxt;
+  int shift = 0;   // MXFP4: of the thread's weight row
   const int MP = chunk_steps<KIND>(a.lg);
   constexpr bool RING = CH && KIND != G_SYM4C;
 
@@ -629,7 +634,7 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
       chunk_meta<KIND>(cur, t + 1, a.lg, r.half, nx);
     }
     GScale<KIND> sc;
-    scales_of<KIND>(nx, a.mb, sc);
+    scales_of<KIND>(nx, a.mb, shift, sc);
     // the matrix cores start on the last step's deferred products while this
     // step's first fragments come from LDS
     A[0] = rd_a(buf, 0, 0);
@@ -658,6 +663,11 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
     __syncthreads();
   };
 
+  MxRow row;
+  if constexpr (KIND == G_MX4) {
+    row.load(r.s, r.so, r.ng, r.half);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   GStage<KIND> st0, st1;
   load_codes<KIND, CH>(r, t0, a.lg, st0);
   load_codes<KIND, CH>(r, t0 + 1, a.lg, st1);
@@ -670,9 +680,10 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
   for (int s = 0; s < 3; ++s)
 #pragma unroll
     for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t0, s, j);
+  if constexpr (KIND == G_MX4) s_we[wn] = shift = row.shift(r.s, r.so, r.ng, r.half);
   {
     GScale<KIND> sc;
-    scales_of<KIND>(st0, a.mb, sc);
+    scales_of<KIND>(st0, a.mb, shift, sc);
 #pragma unroll
     for (int p = 0; p < 4; ++p) put(0u, p, st0, sc);
   }
@@ -687,33 +698,35 @@ __device__ __forceinline__ void gated_tile(const GatedK& a, unsigned char* smem,
   asm volatile("" : "+v"(el));   // keeps the epilogue's addresses after the loop
   const int f0 = (int)n0 + 64 * wi;
   if (f0 >= a.N) return;
+  const int* we = s_we + 128 * wi + 4 * (el >> 5);
   if (a.part) {
-    finish_part<KIND, J>(a, acc, el, mbw, f0, sp);
+    finish_part<KIND, J>(a, acc, el, mbw, f0, sp, we);
     return;
   }
   unsigned char* lds = smem + 8192 * wave;
-  if (a.act == ACT_SILU) finish<KIND, J, ACT_SILU>(a, acc, el, mbw, f0, lds);
-  else finish<KIND, J, ACT_GELU_TANH>(a, acc, el, mbw, f0, lds);
+  if (a.act == ACT_SILU) finish<KIND, J, ACT_SILU>(a, acc, el, mbw, f0, we, lds);
+  else finish<KIND, J, ACT_GELU_TANH>(a, acc, el, mbw, f0, we, lds);
 }
 
 template <int KIND, bool CH>
 __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 k_gated(GatedK a) {
   __shared__ __attribute__((aligned(16))) unsigned char smem[2 * kTileBytes];
+  __shared__ __attribute__((aligned(16))) int s_we[KIND == G_MX4 ? 256 : 1];   // shifts of the tile's weight rows
   // contiguous runs of tiles per XCD, m fastest
   const int bid = blockIdx.x;
   auto run = [](int i, int n) { return n % 8 == 0 ? (i % 8) * (n / 8) + i / 8 : i; };
   if (bid < a.full) {
     const int t = run(bid, a.full), sp = t / (a.full / a.split), u = t - sp * (a.full / a.split);
-    gated_tile<KIND, CH, 2>(a, smem, (int64_t)(u / a.tilesM) * kGF, (u % a.tilesM) * 8, sp);
+    gated_tile<KIND, CH, 2>(a, smem, s_we, (int64_t)(u / a.tilesM) * kGF, (u % a.tilesM) * 8, sp);
   } else {
     const int nh = (int)gridDim.x - a.full, t = run(bid - a.full, nh);
     if (a.small) {
       const int sp = t / (nh / a.split), u = t - sp * (nh / a.split);
-      gated_tile<KIND, CH, 1>(a, smem, (int64_t)(u / a.tilesM1) * kGF, (u % a.tilesM1) * 4, sp);
+      gated_tile<KIND, CH, 1>(a, smem, s_we, (int64_t)(u / a.tilesM1) * kGF, (u % a.tilesM1) * 4, sp);
     } else {   // halves of the last round's tiles
       const int u = a.full + t / 2;
-      gated_tile<KIND, CH, 1>(a, smem, (int64_t)(u / a.tilesM) * kGF, (u % a.tilesM) * 8 + 4 * (t & 1), 0);
+      gated_tile<KIND, CH, 1>(a, smem, s_we, (int64_t)(u / a.tilesM) * kGF, (u % a.tilesM) * 8 + 4 * (t & 1), 0);
     }
   }
 }

@@ -465,9 +465,10 @@ qp_status qlinear_gated_workspace_bytes(const qp_desc* d, int64_t M, int32_t sav
  * Otherwise (but for some longer single rows) fp16 MFMA as QP_KERNEL_GEMM, at
  * any K: x staged as fp16 in the workspace (16-byte aligned, busy until the
  * call's kernels finish), each weight rounded once to fp16 (per-channel SYM4:
- * exact codes), a relative L2 error of about 3e-4 in g and u; so h of 16 rows
+ * exact codes; MXFP4: any scale, as there), a relative L2 error of about 3e-4 in g and u; so h of 16 rows
  * and fewer differs by as much with checkpoints and without.  What is said of
- * small weights and scales under qlinear_backward holds here too. */
+ * small weights and scales of the other formats under qlinear_backward holds here
+ * too. */
 qp_status qlinear_gated_forward(const qp_desc* d, const void* x, int32_t x_dtype, int64_t M,
                                 const qp_weights* gate, const qp_weights* up, const void* bias_gate,
                                 const void* bias_up, int32_t act, void* h, int32_t h_dtype,

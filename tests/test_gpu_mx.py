@@ -722,3 +722,39 @@ def test_qgemm_takes_the_largest_rows_and_weights(q):
             y = q.qlinear_forward(q.QDesc.mxfp4(N, K), x, on_gpu(c, s), y_dtype="f32", kernel=q.QP_KERNEL_GEMM,
                                   workspace=ws)
             within(y, ref, mx_tolerance(x64, w64.T, s.max(axis=1) - 127.0) + 2.0 ** -22 * np.abs(ref), "y")
+
+
+GATED_RANGES = [(20, 40), (100, 107), (110, 150)]
+
+
+@pytest.mark.parametrize("low,high", GATED_RANGES)
+@pytest.mark.parametrize("M,N,K,save", [(40, 70, 512, True), (20, 33, 96, False), (300, 200, 608, False),
+                                        (3, 130, 1024, True), (700, 5000, 64, False)])
+def test_gated_takes_every_scale(q, M, N, K, save, low, high):
+    """The gate's scales over the range, the up projection's the other way (products of
+    the two stay finite)."""
+    rng = np.random.default_rng(M + low)
+    c1, c2 = (rng.integers(0, 16, size=(N, K)).astype(np.uint8) for _ in range(2))
+    s1 = scales_from(rng, N, K // 32, low, high, 12)
+    s2 = scales_from(rng, N, K // 32, 254 - high - 12, 254 - low - 12, 12)
+    w1, w2 = mx.dequantize(c1, s1), mx.dequantize(c2, s2)
+    d = q.QDesc.mxfp4(N, K)
+    x, x64 = dev(rng.normal(size=(M, K)) / 16, "bf16")
+    print("gated scales", M, N, K, save, low, high, flush=True)
+    o = q.qlinear_gated_forward(d, x, on_gpu(c1, s1), on_gpu(c2, s2), act="silu", h_dtype="f32", save=save)
+    none = np.zeros(N)
+    with np.errstate(over="ignore"):
+        g, u, h = mlp.gated(x64, w1, w2, none, none, "silu")
+    dg = mx_tolerance(x64, w1.T, s1.max(axis=1) - 127.0) + 2.0 ** -22 * np.abs(g)
+    du = mx_tolerance(x64, w2.T, s2.max(axis=1) - 127.0) + 2.0 ** -22 * np.abs(u)
+    with np.errstate(over="ignore"):
+        a = np.abs(mlp.act(g, "silu")[0])
+    # the logistic's argument and exponential: 2^-17 where it is not next to 0; below -80 it is under 2^-115
+    tol = 1.13 * dg * (np.abs(u) + du) + a * du + 2.0 ** -16 * np.abs(h) + TINY["f32"] + \
+        np.where(g < -80, 2.0 ** -100 * np.abs(u), 0)
+    within(o.h, h, tol, "h")
+    if save:
+        for (codes, sc), v, t in ((o.gate, g, dg), (o.up, u, du)):
+            got = mlp.restore(codes.cpu().numpy(), sc.cpu().numpy())
+            step = np.repeat(f64(sc), 64, axis=1)[:, :N]
+            assert np.all(np.abs(got - v) <= (0.5 + 1e-4) * step + t)
