@@ -288,12 +288,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, h);
 }
 
-// E8M0 scale byte -> fp32: 2^(s - 127), NaN at 255.
-__device__ __forceinline__ float e8m0_f32(uint32_t s) {
-  const uint32_t b = s == 0u ? 0x00400000u : s << 23;
-  return __uint_as_float(s == 255u ? 0x7FC00000u : b);
-}
-
 // MXFP4 weights as fp16 numbers.  A scale byte covers 2^-127 .. 2^127 and fp16's
 // numbers 2^-24 .. 2^16, so a row (a block of columns, where the sum runs over rows)
 // is taken times 2^shift, which brings its largest scale to 2^13 (weights of up to

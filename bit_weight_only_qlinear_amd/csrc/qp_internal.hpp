@@ -133,6 +133,13 @@ struct StageArgs {
   void* xf;
   int* xe;
   int64_t M, N;
+  // MXFP4 weights [N, 32 tops_cols] whose rows the product sums over: the largest
+  // scale byte below 255 of each 32 columns in `tops_parts` runs of rows, into tops
+  // [tops_parts, tops_cols]; both layers together for the gated pair.  Or parts 0.
+  const uint8_t* scales[2];
+  uint8_t* tops;
+  int tops_parts;
+  int64_t tops_cols;
 };
 hipError_t launch_stage(const StageArgs& r, int dt, bool gated, int act, bool perm, hipStream_t s);
 

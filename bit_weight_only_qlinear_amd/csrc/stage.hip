@@ -20,7 +20,8 @@
 // dg and du computed, once.  A row's chunks of a fragment are 32 bytes of its
 // 1 KiB, so the 32 rows of a block go to blocks of one XCD, whose L2 completes
 // the lines.  k_stage_exp and k_stage, any N: row maxima, then one wave per
-// 32 x 64 values.  Gated, 2048 x 14336
+// 32 x 64 values.  In front of MXFP4 weights the first blocks take the largest scales
+// of their columns (mx_tops).  Gated, 2048 x 14336
 // (351 MB moved): 82 us, against 34 + 127 us in two passes.
 #include "mlp_common.hpp"
 
@@ -47,7 +48,44 @@ struct StageK {
   int* xe;
   int64_t M, N;
   int MB, T1;
+  int lead;                  // first blocks: mx_tops (a multiple of 8, as XCDs go)
+  const uint8_t* scales[2];
+  uint8_t* tops;
+  int parts;
+  int64_t cols;
 };
+
+// Block `part` of a.parts: the largest scale byte below 255 of each 32 columns in
+// its run of weight rows, of one layer or two.  A thread takes a column (several
+// where there are more than threads) and, where there are fewer, some of the rows.
+// The blocks run beside those that stage rows, so the pass over the scales (1/17 of
+// the weights) costs no launch.
+__device__ __forceinline__ void mx_tops(const StageK& a, int part) {
+  if (part >= a.parts) return;
+  __shared__ uint32_t top[1024];
+  const uint32_t nt = blockDim.x, tid = threadIdx.x;
+  const int64_t n0 = a.N * part / a.parts, n1 = a.N * (part + 1) / a.parts;
+  const uint32_t width = a.cols < (int64_t)nt ? (uint32_t)a.cols : nt, groups = nt / width;
+  const uint32_t g = tid / width, c = tid - g * width;
+  for (int64_t c0 = 0; c0 < a.cols; c0 += width) {
+    top[tid] = 0;
+    __syncthreads();
+    if (g < groups && c0 + c < a.cols) {
+      uint32_t m = 0;   // bytes plus 1, of which a NaN's is 0
+      for (int l = 0; l < 2; ++l) {
+        if (!a.scales[l]) break;
+        const uint8_t* p = a.scales[l] + c0 + c;
+#pragma unroll 8
+        for (int64_t n = n0 + g; n < n1; n += groups) m = max(m, (p[n * a.cols] + 1u) & 0xFFu);
+      }
+      atomicMax(&top[c], m);
+    }
+    __syncthreads();
+    if (tid < width && c0 + tid < a.cols)
+      a.tops[(int64_t)part * a.cols + c0 + tid] = (uint8_t)(top[tid] > 0 ? top[tid] - 1u : 0u);
+    __syncthreads();
+  }
+}
 
 template <bool BF>
 __device__ __forceinline__ float dval(uint32_t b) {
@@ -110,7 +148,11 @@ __device__ __forceinline__ void load8(const StageK& a, int64_t at, int64_t n, bo
 template <bool BF, bool GATED, bool V8, int ACT>
 __global__ void __launch_bounds__(256) k_stage_exp(StageK a) {
   __shared__ float red[4];
-  const int64_t row = blockIdx.x;
+  if ((int)blockIdx.x < a.lead) {
+    mx_tops(a, (int)blockIdx.x);
+    return;
+  }
+  const int64_t row = (int)blockIdx.x - a.lead;
   float b = 0.f;
   if (row < a.M) {
     const int64_t ng = (a.N + kCkptGroup - 1) / kCkptGroup;
@@ -191,9 +233,14 @@ __global__ void __launch_bounds__(256) k_stage(StageK a) {
 template <bool BF, bool GATED, int ACT, bool PERM, int NT, int NC>
 __global__ void __launch_bounds__(NT) k_stage_row(StageK a) {
   __shared__ float red[NT / 64];
+  if ((int)blockIdx.x < a.lead) {
+    mx_tops(a, (int)blockIdx.x);
+    return;
+  }
+  const int bid = (int)blockIdx.x - a.lead;
   // 32 consecutive blocks of an XCD (every 8th block id) share a row block
-  const int i0 = (int)blockIdx.x >> 3;
-  const int mb = (i0 >> 5) * 8 + ((int)blockIdx.x & 7), r = i0 & 31;
+  const int i0 = bid >> 3;
+  const int mb = (i0 >> 5) * 8 + (bid & 7), r = i0 & 31;
   if (mb >= a.MB) return;   // whole blocks
   const int64_t row = (int64_t)mb * 32 + r;
   const bool rok = row < a.M;
@@ -308,14 +355,15 @@ void stage_pick(bool gated, int act, bool perm, StageFn* ex, StageFn* st) {
 
 hipError_t launch_stage(const StageArgs& r, int dt, bool gated, int act, bool perm, hipStream_t s) {
   StageK a{r.d, r.gq, r.gs, r.uq, r.us, r.dg, r.du, static_cast<uint4*>(r.xf), r.xe, r.M, r.N,
-           (int)((r.M + 31) / 32), (int)((r.N + 63) / 64)};
+           (int)((r.M + 31) / 32), (int)((r.N + 63) / 64), (r.tops_parts + 7) / 8 * 8, {r.scales[0], r.scales[1]}, r.tops,
+           r.tops_parts, r.tops_cols};
   const bool bf = dt == BF16;
   if (r.N % 8 == 0 && r.N <= 32768) {
     int nt = 0;
     const uint32_t chunks = (uint32_t)a.T1 * 8u;
     StageFn fn = bf ? row_pick<true>(gated, act, perm, chunks, &nt)
                     : row_pick<false>(gated, act, perm, chunks, &nt);
-    hipLaunchKernelGGL(fn, dim3((unsigned)((a.MB + 7) / 8) * 256u), dim3(nt), 0, s, a);
+    hipLaunchKernelGGL(fn, dim3((unsigned)(a.lead + (a.MB + 7) / 8 * 256)), dim3(nt), 0, s, a);
     return hipGetLastError();
   }
   StageFn ex, sf;
@@ -323,7 +371,7 @@ hipError_t launch_stage(const StageArgs& r, int dt, bool gated, int act, bool pe
                        : stage_pick<false, true>(gated, act, perm, &ex, &sf);
   else bf ? stage_pick<true, false>(gated, act, perm, &ex, &sf)
           : stage_pick<false, false>(gated, act, perm, &ex, &sf);
-  hipLaunchKernelGGL(ex, dim3((unsigned)a.MB * 32u), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(ex, dim3((unsigned)(a.lead + a.MB * 32)), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(sf, dim3((unsigned)(((int64_t)a.MB * a.T1 + 3) / 4)), dim3(256), 0, s, a);

@@ -489,7 +489,9 @@ qp_status qlinear_backward_workspace_bytes(const qp_desc* d, int64_t M, int32_t 
  * fp16 (a relative L2 of 2e-4; 5e-4 where their standard deviation is 1e-4,
  * since below 2^-14 fp16 has steps of 2^-24); scales and biases are held to
  * multiples of 2^-24 but for AFFINE of 8 bits, where they stay as they are
- * (bf16 ones of 2^-17 and more are such multiples). */
+ * (bf16 ones of 2^-17 and more are such multiples).  MXFP4 weights of any scale
+ * are exact but for rounding to multiples of 2^-37 of the largest scale of
+ * their 32 columns (over all N; for the gated pair over both layers). */
 qp_status qlinear_backward(const qp_desc* d, const void* dy, int32_t dy_dtype, int64_t M,
                            const qp_weights* w, void* dx, int32_t dx_dtype, void* workspace,
                            size_t workspace_bytes, void* stream);

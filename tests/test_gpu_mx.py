@@ -758,3 +758,55 @@ def test_gated_takes_every_scale(q, M, N, K, save, low, high):
             got = mlp.restore(codes.cpu().numpy(), sc.cpu().numpy())
             step = np.repeat(f64(sc), 64, axis=1)[:, :N]
             assert np.all(np.abs(got - v) <= (0.5 + 1e-4) * step + t)
+
+
+@pytest.mark.parametrize("low,high", RANGES)
+@pytest.mark.parametrize("M,N,K", [(3, 70, 96), (40, 300, 512), (300, 130, 800), (5, 2100, 256), (130, 64, 32), (4, 2101, 96),
+                                   (3, 33, 40960), (2, 1, 64)])
+def test_backward_takes_every_scale(q, M, N, K, low, high):
+    """Columns (32 of them share a scale byte) of every size, and rows of every size."""
+    rng = np.random.default_rng(N + low)
+    c = rng.integers(0, 16, size=(N, K)).astype(np.uint8)
+    dy, dy64 = dev(rng.normal(size=(M, N)) / 16, "bf16")
+    d = q.QDesc.mxfp4(N, K)
+    for s in (np.ascontiguousarray(scales_from(rng, K // 32, N, low, high, 12).T), scales_from(rng, N, K // 32, low, high, 12)):
+        w64 = mx.dequantize(c, s)
+        print("gradient scales", M, N, K, low, high, flush=True)
+        ref = dy64 @ w64
+        tol = mx_tolerance(dy64, w64, np.repeat(s.max(axis=0) - 127.0, 32))
+        for xd in ("f32", "bf16"):
+            got = q.qlinear_backward(d, dy, on_gpu(c, s), dx_dtype=xd)
+            within(got, ref, tol * (1 + U[xd]) + (U[xd] + 2.0 ** -22) * np.abs(ref) + TINY[xd], "dx")
+
+
+@pytest.mark.parametrize("low,high", [(20, 40), (110, 150)])
+@pytest.mark.parametrize("M,N,K", [(3, 70, 96), (300, 130, 544)])
+def test_gated_backward_takes_every_scale(q, M, N, K, low, high):
+    rng = np.random.default_rng(N + low)
+    cs = [rng.integers(0, 16, size=(N, K)).astype(np.uint8) for _ in range(2)]
+    s1 = np.ascontiguousarray(scales_from(rng, K // 32, N, low, high, 12).T)
+    s2 = np.clip(s1.astype(int) + rng.integers(-6, 7, size=s1.shape), 0, 254).astype(np.uint8)
+    wg, wu = mx.dequantize(cs[0], s1), mx.dequantize(cs[1], s2)
+    dh, dh64 = dev(rng.normal(size=(M, N)) * 1e-2, "bf16")
+    ck = [mlp.checkpoint(rng.normal(size=(M, N)) * 2) for _ in range(2)]
+    g, u = (mlp.restore(*k) for k in ck)
+    print("gated gradient scales", M, N, K, low, high, flush=True)
+    o = q.qlinear_gated_backward(q.QDesc.mxfp4(N, K), dh, on_gpu(cs[0], s1), on_gpu(cs[1], s2),
+                                 *[tuple(torch.from_numpy(a).cuda() for a in k) for k in ck], act="silu", dx_dtype="f32")
+    dx, rg, ru = mlp.gated_backward(dh64, g, u, wg, wu, "silu")
+    own = 2.0 ** -17 * (np.abs(dh64 * u) * (1 + np.abs(g)) @ np.abs(wg) + np.abs(dh64) * (1 + np.abs(g)) @ np.abs(wu))
+    top = np.repeat(np.maximum(s1, s2).max(axis=0) - 127.0, 32)
+    tol = mx_tolerance(np.concatenate([rg, ru], 1), np.concatenate([wg, wu]), top) + own
+    within(o.dx, dx, tol + 2.0 ** -22 * np.abs(dx) + TINY["f32"], "gated dx")
+
+
+def test_nan_blocks_in_gradients(q):
+    """A weight block of scale 255 makes its 32 columns of every gradient NaN, and no others."""
+    rng = np.random.default_rng(23)
+    for M, N, K in ((5, 200, 96), (300, 130, 800)):
+        c = rng.integers(0, 16, size=(N, K)).astype(np.uint8)
+        s = scales_from(rng, N, K // 32, 112, 124, 6)
+        s[N - 1, 1] = 255
+        dy, _ = dev(rng.normal(size=(M, N)), "bf16")
+        bad = torch.isnan(q.qlinear_backward(q.QDesc.mxfp4(N, K), dy, on_gpu(c, s))).cpu().numpy()
+        assert bad[:, 32:64].all() and bad.sum() == 32 * M
