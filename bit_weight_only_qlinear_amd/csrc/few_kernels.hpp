@@ -97,6 +97,16 @@ __device__ __forceinline__ f32x4_t mfma4(uint2 a, uint2 b, f32x4_t c) {
                                               __builtin_bit_cast(half4_t, b), c, 0, 0, 0);
 }
 
+// A barrier for what the block's waves exchange through LDS, which leaves loads in
+// flight.  The wait and the barrier do the work; the fences, which are no
+// instructions, keep the compiler from moving LDS accesses over them.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // E2M1 codes of byte SEL of w, times a power of two, as a pair (exact).
 template <bool XB, int SEL>
 __device__ __forceinline__ uint32_t e2m1_pair(uint32_t w, float scale = 1.f) {
@@ -363,8 +373,6 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
         }
     }
   };
-  // A pass's sums: over lanes, then over the team's waves.  Two buffers by
-  // turns, so that one barrier per pass is enough.
   // A pass's sums over lanes; waves that share rows meet in LDS, in two buffers
   // by turns, so that one barrier per pass is enough.
   const int R = lane >> 4, p4 = ((R & 1) << 1) | (R >> 1);
@@ -415,8 +423,7 @@ __device__ __forceinline__ void few_run(const FewArgs& a, const Unit& u, const u
       }
     }
     if (a.KW == 1) return;
-    __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));   // lgkmcnt(0); loads stay in flight
-    __builtin_amdgcn_s_barrier();
+    lds_barrier();
     // the team's threads: (feature, token) with the feature fastest
     for (int i = threadIdx.x - team * a.KW * 64; i < F * 4 * Q; i += a.KW * 64) {
       const int fe = i % F, t = i / F;

@@ -297,8 +297,10 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))
   // the next four steps' scales, which go out after a first step's codes.
   auto turn = [](auto U) __attribute__((always_inline)) {
     constexpr int n = 2 * kLoads + (decltype(U)::value ? 1 : 0);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");   // for the compiler alone: no instructions
     __builtin_amdgcn_s_waitcnt((n & 0xF) | (0x7 << 4) | ((n >> 4) << 14));   // and its LDS reads
     __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     __builtin_amdgcn_sched_barrier(0);
   };
 
