@@ -359,3 +359,103 @@ def test_infinite_logits(q, E):
     b = q.qmoe_forward(g[0], n[0], y, g[1], u[1], n[1], experts=5, topk=2, router=t)
     keep = [0, 1, 2, 3, 5]
     assert torch.equal(a.y[keep], b.y[keep]) and torch.isnan(b.weights[4]).all() and torch.isnan(b.y[4]).all()
+
+
+# ---------------------------------------------------------------- layers with many units of work
+MAG = {"bf16": 128.0, "f16": 1024.0}
+
+
+def big_stack(q, fmt, g, E, rows, K, dt):
+    """A stacked layer of random codes: descriptor, buffers, and e -> the expert's weights
+    and the magnitudes that its chunks' sums pass through (both fp64, on the GPU)."""
+    d = desc(q, fmt, E * rows, K)
+    N, cuda = E * rows, dict(device="cuda", generator=g)
+    words = torch.randint(-2 ** 31, 2 ** 31, (N, K // 8), dtype=torch.int32, **cuda)
+    buf = dict(qweight=words, qweight_hi=None, scales=None, zeros=None, steps=None)
+    if fmt == "mxfp4":
+        buf["scales"] = torch.randint(118, 123, (N, K // 32), dtype=torch.uint8, **cuda)
+    elif fmt == "q4k":
+        buf["scales"] = torch.randint(1, 64, (N, K // 32), dtype=torch.uint8, **cuda)
+        buf["zeros"] = torch.randint(0, 64, (N, K // 32), dtype=torch.uint8, **cuda)
+        steps = torch.rand((N, K // 256, 2), **cuda) * torch.tensor([4e-4, 0.2], device="cuda") + 1e-4
+        buf["steps"] = steps.half().view(torch.int32).view(N, K // 256)
+    elif fmt.startswith("sym4"):
+        words |= 0x11111111
+        buf["scales"] = torch.rand((N, K // d.group_size), **cuda) * 0.01 + 0.005
+    else:
+        s = torch.rand((N, K // d.group_size), **cuda) * 0.01 + 0.005
+        buf["scales"], buf["zeros"] = s.to(DT[fmt[-4:].strip(".")]), (s * -7).to(DT[fmt[-4:].strip(".")])
+
+    def expert(e):
+        b = {k: None if v is None else v[e * rows:(e + 1) * rows] for k, v in buf.items()}
+        c = torch.stack([(b["qweight"] >> (4 * i)) & 15 for i in range(8)], -1).view(rows, K).double()
+        rep = lambda t, n: t.double().repeat_interleave(n, 1)
+        if fmt == "mxfp4":
+            m = torch.tensor(list(mx.VALUES) + list(-mx.VALUES), dtype=torch.float64, device="cuda")
+            w = m[c.long()] * torch.exp2(rep(b["scales"], 32) - 127)
+            return w, w.abs()
+        if fmt == "q4k":
+            st = b["steps"].contiguous().view(torch.float16).view(rows, K // 256, 2)
+            S = rep(b["scales"], 32) * rep(st[..., 0], 256)
+            z = S * rep(b["zeros"], 32) * rep(st[..., 1], 256)
+            return c * S - z, (2 * MAG[dt] + 32) * S + z.abs()
+        S = rep(b["scales"], d.group_size)
+        z = 8 * S if fmt.startswith("sym4") else -rep(b["zeros"], d.group_size)
+        return c * S - z, (2 * MAG[dt] + 32) * S + z.abs()
+    return d, buf, expert
+
+
+# Sizes at which an expert's rows take several passes, a row all of a wave's steps, and the last
+# tile is part of one: M, E, topk, K, inner, formats, dt, act
+BIG = [
+    (12, 64, 8, 1056, 480, "mxfp4", "mxfp4", "bf16", "silu"),       # a wave per row, 3 steps
+    (4, 64, 16, 1056, 480, "mxfp4", "mxfp4", "f16", "gelu_tanh"),   # the same, up to four tokens
+    (9, 64, 8, 5152, 416, "mxfp4", "mxfp4", "bf16", "silu"),        # 11 steps, x step by step; five passes down
+    (20, 128, 8, 1056, 1056, "mxfp4", "mxfp4", "bf16", "silu"),     # two passes of three steps both ways
+    (64, 512, 16, 288, 544, "mxfp4", "mxfp4", "f16", "silu"),       # the limits; four passes up, two of two steps down
+    (3, 64, 16, 2848, 544, "mxfp4", "mxfp4", "bf16", "gelu_tanh"),  # two passes down, up to four tokens
+    (40, 16, 4, 2080, 4640, "mxfp4", "mxfp4", "bf16", "silu"),      # 10 steps down, step by step
+    (60, 12, 4, 1056, 2080, "mxfp4", "mxfp4", "f16", "silu"),       # many tokens each
+    (16, 64, 8, 1088, 1088, "affine64.bf16", "affine64.bf16", "bf16", "silu"),
+    (4, 64, 16, 1088, 544, "affine32.f16", "affine32.bf16", "f16", "silu"),
+    (20, 64, 8, 1280, 2560, "q4k", "q4k", "bf16", "gelu_tanh"),
+    (10, 64, 8, 1056, 2112, "sym4", "sym4.32", "f16", "silu"),
+]
+
+
+@pytest.mark.parametrize("c", BIG, ids=[f"{c[0]}x{c[3]}x{c[4]}-{c[2]}of{c[1]}-{c[5]}-{c[7]}" for c in BIG])
+def test_layers_of_many_units(q, c):
+    M, E, topk, K, inner, fu, fd, dt, kind = c
+    print("moe", *c, flush=True)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(M * K + inner)
+    G, Um, Dn = (big_stack(q, f, gen, E, a, b, dt) for f, a, b in ((fu, inner, K), (fu, inner, K), (fd, K, inner)))
+    x = (torch.randn((M, K), device="cuda", generator=gen) * 0.25).to(DT[dt])
+    ids = torch.stack([torch.randperm(E, device="cuda", generator=gen)[:topk] for _ in range(M)]).int()
+    wts = torch.rand((M, topk), device="cuda", generator=gen)
+    o = q.qmoe_forward(G[0], Dn[0], x, G[1], Um[1], Dn[1], experts=E, topk=topk, ids=ids, weights=wts, act=kind,
+                       y_dtype="f32")
+    again = q.qmoe_forward(G[0], Dn[0], x, G[1], Um[1], Dn[1], experts=E, topk=topk, ids=ids, weights=wts, act=kind,
+                           y_dtype="f32")
+    assert torch.equal(o.y, again.y)
+
+    def tol(v, w, mag):
+        n = w.shape[1]
+        return 72 * 2.0 ** -24 * (v @ mag.t()) + 2 * (n // 32 + 24) * 2.0 ** -24 * (v @ w.abs().t())
+    x64, ref, lim = x.double(), torch.zeros((M, K), device="cuda").double(), torch.zeros((M, K), device="cuda").double()
+    for e in range(E):
+        m, slot = (ids == e).nonzero(as_tuple=True)
+        if not len(m):
+            continue
+        (gw, gm), (uw, um), (dw, dm) = G[2](e), Um[2](e), Dn[2](e)
+        v = x64[m]
+        g, u = v @ gw.t(), v @ uw.t()
+        dg, du = tol(v.abs(), gw, gm), tol(v.abs(), uw, um)
+        a = torch.from_numpy(mlp.act(g.cpu().numpy(), kind)[0]).cuda()
+        h = a * u
+        dh = 1.13 * dg * (u.abs() + du) + a.abs() * du + (U[dt] + 2.0 ** -17) * h.abs() + TINY[dt]
+        w = wts[m, slot].double()[:, None]
+        ref.index_add_(0, m, w * (h @ dw.t()))
+        lim.index_add_(0, m, w * (dh @ dw.abs().t() + tol(h.abs() + dh, dw, dm) + 2.0 ** -22 * (h.abs() @ dw.abs().t())))
+    err, lim = (o.y.double() - ref).abs(), lim * (1 + 2.0 ** -23) + 2.0 ** -20 * ref.abs() + TINY["f32"]
+    assert bool(torch.isfinite(o.y).all()) and bool((err <= lim).all()), float((err / lim).max())
