@@ -69,7 +69,7 @@ struct DxK {
   int T1, T;               // steps per part, in all
   int MB;                  // 32-row blocks of D
   int tilesK, tilesM, split;
-  const uint8_t* tops;     // MXFP4: largest scale bytes [parts, K / 32]
+  const uint8_t* tops;     // MXFP4: the runs' largest scale bytes (StageArgs)
   int parts;
   int* we;                 // and the shifts [K / 32] for k_dx_sum
 };
@@ -471,6 +471,16 @@ k_dx(DxK a) {
     __syncthreads();
   };
 
+  uint32_t runs[kRuns / 64];
+  if constexpr (KIND == G_MX4) {   // past the columns and the runs: bytes that change nothing
+    const int64_t c = k0 / 32 + (tid & 7);
+#pragma unroll
+    for (int u = 0; u < kRuns / 64; ++u) {
+      const int i = (tid >> 3) + 64 * u;
+      runs[u] = a.tops[tops_at(c < K / 32 ? c : k0 / 32, i < a.parts ? i : 0, a.parts)];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
   DStage<KIND> st0, st1;
   dload<KIND>(a, o, t0, st0);
   dload<KIND>(a, o, t0 + 1, st1);
@@ -480,13 +490,7 @@ k_dx(DxK a) {
     for (int j = 0; j < J; ++j) Bf[s][j] = ld_b(t0, s, j);
   if constexpr (KIND == G_MX4) {   // the runs' largest scales, then what brings them to 2^13
     const int64_t C = K / 32, c = k0 / 32 + (tid & 7);
-    uint32_t runs[kRuns / 64], top = 0;   // all loads first
-#pragma unroll
-    for (int u = 0; u < kRuns / 64; ++u) {
-      const int i = (tid >> 3) + 64 * u;
-      runs[u] = a.tops[i < a.parts && c < C ? (int64_t)i * C + c : (int64_t)0];
-      runs[u] = i < a.parts && c < C ? runs[u] : 0u;
-    }
+    uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < kRuns / 64; ++u) top = max(top, runs[u]);
 #pragma unroll
@@ -643,7 +647,7 @@ DxPlan dx_plan(const Desc& d, int64_t M, bool gated) {
   if (d.fmt == MXFP4) {   // a run per CU, of at least a row, and 1 MiB of bytes in all
     const int64_t C = d.K / 32, most = (int64_t(1) << 20) / C, n = d.N < kRuns ? d.N : (int64_t)kRuns;
     p.parts = (int)(most < 1 ? 1 : most < n ? most : n);
-    p.tops = (size_t)cdiv((int64_t)p.parts * C, 16) * 16u;
+    p.tops = (size_t)cdiv(cdiv(C, 8) * 8 * p.parts, 16) * 16u;
     p.we = p.split > 1 ? (size_t)cdiv(C, 4) * 16u : 0;
   }
   return p;

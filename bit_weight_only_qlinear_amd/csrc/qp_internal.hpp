@@ -135,12 +135,16 @@ struct StageArgs {
   int64_t M, N;
   // MXFP4 weights [N, 32 tops_cols] whose rows the product sums over: the largest
   // scale byte below 255 of each 32 columns in `tops_parts` runs of rows, into tops
-  // [tops_parts, tops_cols]; both layers together for the gated pair.  Or parts 0.
+  // (at tops_at); both layers together for the gated pair.  Or parts 0.
   const uint8_t* scales[2];
   uint8_t* tops;
   int tops_parts;
   int64_t tops_cols;
 };
+// Eight neighbouring columns' bytes of all runs lie together: a product tile's.
+__host__ __device__ inline int64_t tops_at(int64_t col, int part, int parts) {
+  return ((col >> 3) * parts + part) * 8 + (col & 7);
+}
 hipError_t launch_stage(const StageArgs& r, int dt, bool gated, int act, bool perm, hipStream_t s);
 
 // Input gradients.  dx [M, K] = dy [M, N] W, or with `gated` the sum of two

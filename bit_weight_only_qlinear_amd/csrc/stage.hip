@@ -82,7 +82,7 @@ __device__ __forceinline__ void mx_tops(const StageK& a, int part) {
     }
     __syncthreads();
     if (tid < width && c0 + tid < a.cols)
-      a.tops[(int64_t)part * a.cols + c0 + tid] = (uint8_t)(top[tid] > 0 ? top[tid] - 1u : 0u);
+      a.tops[tops_at(c0 + tid, part, a.parts)] = (uint8_t)(top[tid] > 0 ? top[tid] - 1u : 0u);
     __syncthreads();
   }
 }
