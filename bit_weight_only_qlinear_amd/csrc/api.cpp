@@ -1108,12 +1108,12 @@ qp_status qlinear_forward_mx(const qp_desc* d, const void* xq, const void* xs, i
   weight_spans(dd, w, spans + 4);
   if ((st = check_apart(spans)) != QP_OK) return st;
   (void)hipGetLastError();
-  // whole dwords of scale bytes per row, and 32-bit offsets inside a tile
   const bool fits = qp::mx_few_fits(dd, M);
   // The tiles' time does not depend on how few of them there are, the few-row
   // kernel's is proportional to M N: 128 x 14336 x 4096 (16 tiles) 52 and 20 us, 256
   // x 8192 x 8192 (32) 44 and 43, 384 x 8192 x 8192 (64) 43 and 62, 128 x 4096 x
-  // 14336 (56) 19 and 27; up to 64 rows 64 x 5120 x 25600 (100) 33 and 29.
+  // 14336 (56) 19 and 27; up to 64 rows 64 x 5120 x 25600 (100) 33 and 29.  The tiles
+  // need whole dwords of scale bytes per row, and 32-bit offsets inside a tile.
   const bool tiles = ((M > kMxFewRows && qp::mx_tiles(dd, M) > kMxFewTiles) || !fits) && dd.K % 128 == 0 && dd.K <= (int64_t(1) << 20);
   if (!tiles && !fits)
     return fail(QP_EUNSUPPORTED, "qlinear_forward_mx: K=%lld needs K %% 128 == 0 and K <= 2^20", (long long)dd.K);

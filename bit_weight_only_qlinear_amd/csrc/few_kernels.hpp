@@ -31,9 +31,9 @@
 // at once.  (An expert's tokens one after the other in one block: 22 tokens of
 // 2 experts of 736 x 1568 42 us instead of 27, 50 x 4096 x 1536 105 and 100.)
 //
-// 1 x 4096 x 14336: 8.8 us, 3.5 TB/s, of which 4 us are the launch, the metadata
+// 1 x 4096 x 14336: 9.0 us, 3.5 TB/s, of which 4 us are the launch, the metadata
 // and the first codes.  Experts: 2 of 8 of 4096 x 14336 int4 31 + 16 us (4.2 TB/s),
-// 64 of 2048 x 1024 MXFP4 with 2 tokens each 32 + 21 (4.0), 32 of 4096 x 1536 with
+// 64 of 2048 x 1024 MXFP4 with 2 tokens each 33 + 21 (3.9), 32 of 4096 x 1536 with
 // 6 each 60 + 33 (3.4; the tokens beyond eight read their expert again).
 #pragma once
 #include "device_common.hpp"

@@ -126,7 +126,7 @@ unsigned mx_blocks(int64_t n8) {
 //    a line for each four bytes).  A lane's operand is its row's dword, shifted
 //    so that its half's bytes are where the instruction's byte select expects
 //    them.
-// 2048 x 4096 x 14336: 72.6 us, 3.3 PFLOP/s; of the 72, 32 are the matrix
+// 2048 x 4096 x 14336: 72 us, 3.3 PFLOP/s; of the 72, 32 are the matrix
 // instructions alone (18 ns per instruction and SIMD), 11 the stores of 59 MB.
 struct MxArgs {
   const unsigned char* xq;

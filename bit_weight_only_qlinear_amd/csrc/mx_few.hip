@@ -39,7 +39,7 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, unsigned char* 
 // took as long as the weights): piece p of row t lies at p ^ (t % 16), so that
 // 16 lanes of one piece touch every bank once.  KW waves share rows and add up
 // through LDS at the end.  The scale bytes of the block's rows, of W and of X,
-// are copied to LDS first.  16 x 5120 x 25600: 17.7 us, 3.9 TB/s.
+// are copied to LDS first.  16 x 5120 x 25600: 19 us, 3.7 TB/s.
 template <int kG, int T>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) k_mx_few(MxFewArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];

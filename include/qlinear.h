@@ -268,7 +268,8 @@ qp_status qpack_dequantize(const qp_desc* d, const qp_weights* w, void* W_out,
  * QP_F16, QP_BF16 or QP_F32.  Accumulation is fp32.
  * The qGEMV (QP_KERNEL_GEMV) and the MFMA qGEMV (QP_KERNEL_GEMV_MFMA) use
  * the codes exactly, in products with the activations in their own type,
- * and apply each group's scale and offset in fp32.  The qGEMM
+ * and apply each group's scale and offset in fp32 (sums that scales have yet to
+ * bring down may overflow for bf16 activations past 2^100).  The qGEMM
  * (QP_KERNEL_GEMM) runs on fp16 MFMA: each weight is dequantized and
  * rounded once to fp16 inside the kernel (scales, zero points and weights
  * are assumed to lie in the fp16 normal range) -- except per-channel SYM4,
@@ -561,8 +562,10 @@ qp_status qmoe_workspace_bytes(const qp_desc* d_up, const qp_desc* d_down, int64
  *     nothing; a token may name an expert twice; score and norm are unused.
  *     A token without experts gives zeros.
  * Every weight matrix of an expert that some token takes is read once per 8
- * of its tokens (4 where M <= 4).  Exact codes, fp32 sums; the inner activations are rounded
- * to x_dtype, everything else once at the end; results do not depend on
+ * of its tokens (4 where M <= 4).  Exact codes, fp32 sums; the inner activations
+ * are rounded to x_dtype, as the gated pair's h of that type (infinite past 65504 in
+ * fp16; of y's error in a 16-bit type they make half, in squares), everything else
+ * once at the end; results do not depend on
  * timing, nor a token's on the other tokens' values (their number may change
  * the order of sums).  Infinite rows of AFFINE, Q4K and SYM4 experts may give NaN
  * where the exact result is an infinity.  Limits: M <= 64, experts <= 512,
